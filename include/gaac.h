@@ -462,6 +462,136 @@ GAAC_API int gaac_nested_decode_tiles(const uint8_t* slots, const uint16_t* esc_
                                       const uint8_t* base2, const uint8_t* base3, const uint8_t* base4,
                                       uint16_t* tiles, int32_t* d_status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions and an 8-bit paged cache.  The GAAC page relates its coding
+ * to a cache already in FP8 (Appendix B) and studies rotary keys (Appendix C);
+ * the entry points below serve such a cache: keys and queries are rotated, new
+ * tokens are quantised into pages as their blocks fill, decode attention reads
+ * the pages, and whole sequences are forked, released and compacted.
+ * ---------------------------------------------------------------------- */
+
+/* Types of model tensors. */
+enum { GAAC_BF16 = 0, GAAC_F16 = 1, GAAC_F32 = 2 };
+
+/* One tensor to rotate: elements (seq, tok, head, channel) at x + seq*x_seq +
+ * tok*x_tok + head*x_head + channel and likewise at out (strides in elements,
+ * not negative).  A zero stride of x repeats it; out's elements are distinct.
+ * out may be x itself with the same strides (in place), else the two must not
+ * overlap. */
+typedef struct {
+  const void* x;
+  void* out;
+  int32_t n_heads;
+  int64_t x_seq, x_tok, x_head;
+  int64_t out_seq, out_tok, out_head;
+} gaac_rope_tensor;
+
+#define GAAC_ROPE_INTERLEAVED 1u /* pair j is channels 2j, 2j+1 (else j, j + rot_dim/2) */
+#define GAAC_ROPE_INVERSE 2u     /* turn backwards: the gradient of the same call without the flag */
+
+/*
+ * Rotates the first rot_dim channels of every head of one or two tensors (q and
+ * k; they share no elements) by their token's position and copies the others:
+ *   a' = mscale (a cos - b sin), b' = mscale (b cos + a sin), angle = pos * w_j.
+ * turns[j] = w_j / (2 pi) * 2^64 (mod 2^64), j < rot_dim/2: the product with the
+ * position is exact modulo one turn, however far the position.  positions:
+ * pos_bits-wide (32 or 64) signed integers at seq*pos_seq_stride +
+ * tok*pos_tok_stride; any value.  dtype: GAAC_BF16, GAAC_F16 or GAAC_F32,
+ * computed in fp32 and rounded once.  2 <= rot_dim <= head_dim <= 4096, even.
+ */
+GAAC_API int gaac_rope(const gaac_rope_tensor* tensors, int n_tensors, int dtype, int64_t n_seq, int64_t n_tok,
+                       int head_dim, int rot_dim, const void* positions, int pos_bits, int64_t pos_seq_stride,
+                       int64_t pos_tok_stride, const uint64_t* turns, float mscale, unsigned flags, void* stream);
+
+/* One layer's 8-bit paged cache, in caller-owned device memory.
+ *  pages     [n_pages][n_kv_heads][2 (K, V)][64][128] FP8 numbers (fmt: GAAC_FP8_E4M3 or
+ *            GAAC_FP8_E5M2), 16-byte aligned; a value is its FP8 number times its scale
+ *  scales    fp32 [n_pages][n_kv_heads][2]: one for each block of tokens, kv-head and K|V;
+ *            finite and positive, 8-byte aligned
+ *  tail      [batch][n_kv_heads][2][64][128] of dtype (GAAC_BF16 or GAAC_F16), 16-byte
+ *            aligned: row t of sequence b is token 64*(len/64) + t of its open block
+ *  table     int32 [batch][max_blocks]: the page of each block, -1 without one
+ *  refs      int32 [n_pages]: sequences that hold a page; 0 = free.  16-byte aligned
+ *  seq_lens  int32 [batch]
+ *  work      gaac_kv8_workspace(batch, n_pages) bytes, 16-byte aligned, zero before the first
+ *            call; calls on one cache are ordered on the GPU (one stream, or events)
+ * batch <= 65535, n_kv_heads <= 1024, 128 * n_kv_heads * n_pages < 2^31 and the same for batch.
+ * Only full blocks have pages, and a full block never changes; lengths, tables and counts change
+ * through the calls below only.  A new cache has seq_lens and refs 0 and table -1. */
+typedef struct {
+  uint8_t* pages;
+  float* scales;
+  void* tail;
+  int32_t* table;
+  int32_t* refs;
+  int32_t* seq_lens;
+  int32_t* work;
+  int64_t n_pages;
+  int32_t batch, n_kv_heads, max_blocks, fmt, dtype;
+} gaac_kv8;
+
+GAAC_API size_t gaac_kv8_workspace(int batch, int64_t n_pages);
+
+/*
+ * Appends tokens: rows [cu_tokens[b], cu_tokens[b+1]) of k and v (dtype, element
+ * (row, h, c) at row*tok_stride + h*128 + c; 16-byte aligned, strides multiples of 8)
+ * go to sequence b, cu_tokens being int32 [batch+1] on the device, not decreasing,
+ * within [0, n_tokens].  cu_tokens NULL: one token for each sequence (n_tokens = batch).
+ * Every block that fills is quantised into its page, K and V of each kv-head with a scale
+ * of their own: the smallest power of two 2^e, e >= -126, that brings the block's largest
+ * finite magnitude to the format's largest value or below (1 for a block of zeros); the
+ * division is exact and the rounding to FP8 is to nearest, ties to even.  NaN stays NaN;
+ * infinities stay in E5M2 and become NaN in E4M3.  The tokens of the block that stays
+ * open are copied to the tail; the tail's rows behind it are left as they were.
+ * The pages of blocks that fill must be in the table (gaac_kv8_reserve): a sequence with
+ * one missing reports GAAC_EPOOL, one that would pass max_blocks GAAC_EINVAL, and either
+ * is left as it was.  Bad cu_tokens: GAAC_EINVAL, nothing appended.
+ */
+GAAC_API int gaac_kv8_append(const gaac_kv8* cache, const void* k, const void* v, int64_t n_tokens,
+                             int64_t k_tok_stride, int64_t v_tok_stride, const int32_t* cu_tokens, int32_t* d_status,
+                             void* stream);
+
+/*
+ * Decode attention over the cache, one query token per sequence:
+ *   out[b][hq][c] = sum_{t < seq_lens[b]} softmax_t(scale * q[b][hq] . k[b][t][hk]) v[b][t][hk][c],
+ * hk = hq / (n_q_heads / n_kv_heads), which is an integer <= GAAC_MAX_GQA; 0 for an empty
+ * sequence.  q: the cache's dtype, [batch] rows q_seq_stride elements apart (a multiple of
+ * 8), each [n_q_heads][128], 16-byte aligned; out: contiguous [batch][n_q_heads][128] of the
+ * cache's dtype or GAAC_F32, 16-byte aligned.  workspace: gaac_kv8_attention_workspace()
+ * bytes, 16-byte aligned, zero before the first call and left so; not shared by calls that
+ * may overlap on the GPU.  A page index outside the pool reports GAAC_EFORMAT and its
+ * block contributes nothing; a length outside the table reports GAAC_EINVAL and counts as 0.
+ */
+GAAC_API size_t gaac_kv8_attention_workspace(void);
+GAAC_API int gaac_kv8_decode_attention(const gaac_kv8* cache, const void* q, int n_q_heads, int64_t q_seq_stride,
+                                       float scale, void* out, int out_dtype, void* workspace,
+                                       size_t workspace_bytes, int32_t* d_status, void* stream);
+
+/*
+ * Pages for the blocks that the given appends (cu_tokens as gaac_kv8_append; NULL: one token
+ * each) will fill: table entries without a page, in order of sequence and block, get the
+ * lowest free pages in order.  When they run out the rest stays -1 and GAAC_EPOOL is
+ * reported; a sequence that would pass max_blocks gets none and reports GAAC_EINVAL.
+ */
+GAAC_API int gaac_kv8_reserve(const gaac_kv8* cache, const int32_t* cu_tokens, int32_t* d_status, void* stream);
+
+/* Empties the listed sequences (int32 seqs[n] on the device): their pages lose a holder, their
+ * rows become -1 and their lengths 0.  An index out of range reports GAAC_EINVAL and is
+ * skipped; listing a sequence twice is listing it once. */
+GAAC_API int gaac_kv8_release(const gaac_kv8* cache, const int32_t* seqs, int n, int32_t* d_status, void* stream);
+
+/* dst[i] becomes a copy of src[i] (int32 on the device, n <= batch): full blocks are shared, the
+ * open block's rows copied.  dst[i] must be empty, without reserved pages.  A pair with an
+ * index out of range, a dst in use or listed before, or a src that is some pair's dst reports
+ * GAAC_EINVAL and is skipped; a src whose own row or length is not valid, GAAC_EFORMAT. */
+GAAC_API int gaac_kv8_fork(const gaac_kv8* cache, const int32_t* src, const int32_t* dst, int n, int32_t* d_status,
+                           void* stream);
+
+/* Moves the held pages to the front of the pool: with n held, the lowest free page below n takes
+ * the contents of the highest held one at n or above, and so on.  The table follows.
+ * moved_to: int32 [n_pages] on the device, each page's new place, -1 for a free one. */
+GAAC_API int gaac_kv8_compact(const gaac_kv8* cache, int32_t* moved_to, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

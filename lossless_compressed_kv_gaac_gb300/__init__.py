@@ -12,6 +12,7 @@ Personal Devices" (sections 3.1-3.3).  Tile format v3 is described in gaac.h.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -117,6 +118,25 @@ def lib() -> ctypes.CDLL:
             L.gaac_fp8_encode_tiles.restype = i32
             L.gaac_fp8_decompress_tiles.argtypes = [P, P, i64, i32, P, P, i32, P, P, P, P, P]
             L.gaac_fp8_decompress_tiles.restype = i32
+            L.gaac_rope.argtypes = [P, i32, i32, i64, i64, i32, i32, P, i32, i64, i64, P, ctypes.c_float,
+                                    ctypes.c_uint, P]
+            L.gaac_rope.restype = i32
+            L.gaac_kv8_workspace.argtypes = [i32, i64]
+            L.gaac_kv8_workspace.restype = sz
+            L.gaac_kv8_append.argtypes = [P, P, P, i64, i64, i64, P, P, P]
+            L.gaac_kv8_append.restype = i32
+            L.gaac_kv8_attention_workspace.argtypes = []
+            L.gaac_kv8_attention_workspace.restype = sz
+            L.gaac_kv8_decode_attention.argtypes = [P, P, i32, i64, ctypes.c_float, P, i32, P, sz, P, P]
+            L.gaac_kv8_decode_attention.restype = i32
+            L.gaac_kv8_reserve.argtypes = [P, P, P, P]
+            L.gaac_kv8_reserve.restype = i32
+            L.gaac_kv8_release.argtypes = [P, P, i32, P, P]
+            L.gaac_kv8_release.restype = i32
+            L.gaac_kv8_fork.argtypes = [P, P, P, i32, P, P]
+            L.gaac_kv8_fork.restype = i32
+            L.gaac_kv8_compact.argtypes = [P, P, P]
+            L.gaac_kv8_compact.restype = i32
             _lib = L
     return _lib
 
@@ -424,3 +444,285 @@ def decode_attention_hd256(q, seq_lens, table, pools: Pools, base3, base4, scale
         q.data_ptr(), B, Hq, n_kv, table.shape[1], seq_lens.data_ptr(), table.data_ptr(), ctypes.byref(pc),
         base3.data_ptr(), base4.data_ptr(), float(scale), n_splits, out.data_ptr(), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream)))
+
+
+# ---------------------------------------------------------------- rotary positions
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # GAAC_BF16, GAAC_F16, GAAC_F32
+ROPE_INTERLEAVED, ROPE_INVERSE = 1, 2
+
+
+class gaac_rope_tensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n_heads", ctypes.c_int32),
+                ("x_seq", ctypes.c_int64), ("x_tok", ctypes.c_int64), ("x_head", ctypes.c_int64),
+                ("out_seq", ctypes.c_int64), ("out_tok", ctypes.c_int64), ("out_head", ctypes.c_int64)]
+
+
+def rope_frequencies(rot_dim: int, theta: float = 1e4, scaling: str | None = None, factor: float = 1.0,
+                     original_len: int | None = None, fast: float = 32.0, slow: float = 1.0):
+    """(w, mscale): the angular frequencies w_j = theta^(-2j/rot_dim) as a float64 tensor [rot_dim/2], scaled for
+    a context `factor` times the trained one, and the multiplier of the rotated channels that goes with them.
+
+    scaling None: as they are.  "linear": w / factor (positions interpolated).  "base": theta stretched to
+    theta * factor^(rot_dim/(rot_dim-2)), which leaves the fastest pair alone and slows the slowest by factor.
+    "bands": by how often a pair turns within original_len tokens: `fast` turns and more keep w, `slow` and fewer
+    get w / factor, linear in the pair's index between; mscale = 0.1 ln(factor) + 1."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and positive")
+    if not theta > 0 or not factor > 0:
+        raise ValueError("theta and factor must be positive")
+    j = torch.arange(rot_dim // 2, dtype=torch.float64)
+    if scaling == "base":
+        if rot_dim < 4:
+            raise ValueError("base scaling needs rot_dim >= 4")
+        theta = theta * factor ** (rot_dim / (rot_dim - 2))
+    w = theta ** (-2.0 * j / rot_dim)
+    if scaling in (None, "base"):
+        return w, 1.0
+    if scaling == "linear":
+        return w / factor, 1.0
+    if scaling != "bands":
+        raise ValueError("scaling must be None, 'linear', 'base' or 'bands'")
+    if not original_len or original_len <= 0 or not fast > slow > 0:
+        raise ValueError("band scaling needs original_len > 0 and fast > slow > 0")
+
+    def pair_of(turns):  # the (real) index of the pair that turns so often within original_len
+        return rot_dim * math.log(original_len / (2 * math.pi * turns)) / (2 * math.log(theta))
+
+    lo = max(0.0, math.floor(pair_of(fast)))
+    hi = min(rot_dim / 2 - 1.0, math.ceil(pair_of(slow)))
+    keep = 1.0 - ((j - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+    return w * keep + w / factor * (1.0 - keep), (0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0)
+
+
+def rope_turns(w: torch.Tensor, device=None) -> torch.Tensor:
+    """The angular frequencies w (radians per position) as fractions of a turn in 64-bit fixed point, the form
+    rope() takes: int64 tensor of round(w / (2 pi) * 2^64) modulo 2^64, on `device` (default: w's)."""
+    if w.dim() != 1:
+        raise ValueError("w must be one-dimensional")
+    values = w.double().tolist()
+    if not all(math.isfinite(x) for x in values):
+        raise ValueError("frequencies must be finite")
+    fixed = [round(x / (2 * math.pi) * 2.0 ** 64) & (2 ** 64 - 1) for x in values]
+    return torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in fixed], dtype=torch.int64,
+                        device=w.device if device is None else device)
+
+
+def _same_device(first, *tensors):
+    """The CUDA device that all of them are on."""
+    if not first.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    for t in tensors:
+        if t is not None and t.device != first.device:
+            raise ValueError("tensors must be on one device")
+    return first.device
+
+
+def _call(fn: str, device, stream, *args):
+    """Calls the library with `device` current and the stream (default: the device's current one) last."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(fn, device, stream, *args)
+    if stream is None:
+        s = torch.cuda.current_stream(device).cuda_stream
+    else:
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    status = getattr(_lib or lib(), fn)(*args, s)
+    if status != OK:
+        raise GaacError(fn, status)
+
+
+def _rope_view(t, name):
+    """(n_seq, n_tok, heads, dim, seq, tok and head strides) of [tokens, heads, dim] or [batch, tokens, heads, dim]."""
+    if t.dim() == 3:
+        n_seq, seq = 1, 0
+    elif t.dim() == 4:
+        n_seq, seq = t.shape[0], t.stride(0)
+    else:
+        raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
+    n_tok, heads, dim = t.shape[-3:]
+    if dim > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: channels must be contiguous")
+    return n_seq, n_tok, heads, dim, seq, t.stride(-3), t.stride(-2)
+
+
+def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, turns: torch.Tensor, q_out=None, k_out=None,
+         interleaved: bool = False, mscale: float = 1.0, inverse: bool = False, stream=None) -> None:
+    """Rotary positions of q and, if given, k in one launch.  q, k: [tokens, heads, dim] or [batch, tokens, heads,
+    dim], BF16, FP16 or FP32, channels contiguous, other strides free; positions: int32 or int64, [tokens] or
+    [batch, tokens]; turns: rope_turns(...), one for each pair of the rotated channels (the first
+    2 * turns.numel() of a head; the others are copied).  Pairs are (j, j + half) or, interleaved, (2j, 2j + 1).
+    q_out, k_out: default in place.  inverse turns the other way: the gradient of the call without it."""
+    qo = q if q_out is None else q_out
+    pairs = [(q, qo)]
+    if k is not None:
+        pairs.append((k, k if k_out is None else k_out))
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    device = _same_device(q, qo, *pairs[-1], positions, turns)
+    if q.dtype not in _DTYPES or any(t.dtype != q.dtype for p in pairs for t in p):
+        raise ValueError("q, k and the outputs must be of one type: BF16, FP16 or FP32")
+    if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+        raise ValueError("turns must be a contiguous int64 tensor [pairs]")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise ValueError("positions must be int32 or int64")
+    desc = (gaac_rope_tensor * len(pairs))()
+    shape = None
+    for d, (x, out) in zip(desc, pairs):
+        n_seq, n_tok, heads, dim, *xs = _rope_view(x, "input")
+        o_seq, o_tok, o_heads, o_dim, *outs = _rope_view(out, "output")
+        if out.shape != x.shape:
+            raise ValueError("an output must have its input's shape")
+        if shape is None:
+            shape, n_dim = (n_seq, n_tok, dim), x.dim()
+        elif (n_seq, n_tok, dim) != shape or x.dim() != n_dim:
+            raise ValueError("q and k must have the same tokens and width")
+        d.x, d.out, d.n_heads = x.data_ptr(), out.data_ptr(), heads
+        d.x_seq, d.x_tok, d.x_head = xs
+        d.out_seq, d.out_tok, d.out_head = outs
+    n_seq, n_tok, dim = shape
+    if positions.dim() == 1 and positions.shape[0] == n_tok:
+        ps, pt = 0, positions.stride(0)
+    elif positions.dim() == 2 and n_dim == 4 and tuple(positions.shape) == (n_seq, n_tok):
+        ps, pt = positions.stride()
+    else:
+        raise ValueError("positions must be [tokens] or [batch, tokens]")
+    _call("gaac_rope", device, stream, desc, len(pairs), _DTYPES[q.dtype], n_seq, n_tok, dim, 2 * turns.shape[0],
+          positions.data_ptr(), 8 * positions.element_size(), ps, pt, turns.data_ptr(), float(mscale),
+          (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0))
+
+
+# ---------------------------------------------------------------- 8-bit paged cache
+class gaac_kv8(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("tail", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("work", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("batch", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("fmt", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class Kv8:
+    """Storage of one layer's 8-bit paged cache around the caller's tensors, which stay the ones it was made with.
+
+    pages: uint8 [n_pages, kv_heads, 2, 64, 128]; scales: fp32 [n_pages, kv_heads, 2]; tail: BF16 or FP16
+    [batch, kv_heads, 2, 64, 128]; table: int32 [batch, max_blocks]; refs: int32 [n_pages]; seq_lens: int32
+    [batch].  fmt: FP8_E4M3 or FP8_E5M2."""
+
+    def __init__(self, pages, scales, tail, table, refs, seq_lens, fmt: int):
+        self.device = _same_device(pages, scales, tail, table, refs, seq_lens)
+        if pages.dim() != 5 or tuple(pages.shape[2:]) != (2, BLOCK, HEAD_DIM) or pages.dtype != torch.uint8:
+            raise ValueError(f"pages must be uint8 [n_pages, kv_heads, 2, {BLOCK}, {HEAD_DIM}]")
+        n_pages, heads = pages.shape[:2]
+        if tuple(scales.shape) != (n_pages, heads, 2) or scales.dtype != torch.float32:
+            raise ValueError("scales must be fp32 [n_pages, kv_heads, 2]")
+        if table.dim() != 2 or table.dtype != torch.int32:
+            raise ValueError("table must be int32 [batch, max_blocks]")
+        batch, max_blocks = table.shape
+        if tuple(tail.shape) != (batch, heads, 2, BLOCK, HEAD_DIM) or tail.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"tail must be BF16 or FP16 [batch, kv_heads, 2, {BLOCK}, {HEAD_DIM}]")
+        if tuple(refs.shape) != (n_pages,) or refs.dtype != torch.int32:
+            raise ValueError("refs must be int32 [n_pages]")
+        if tuple(seq_lens.shape) != (batch,) or seq_lens.dtype != torch.int32:
+            raise ValueError("seq_lens must be int32 [batch]")
+        if fmt not in (FP8_E4M3, FP8_E5M2):
+            raise ValueError("fmt must be FP8_E4M3 or FP8_E5M2")
+        for t, name in ((pages, "pages"), (scales, "scales"), (tail, "tail"), (table, "table"), (refs, "refs"),
+                        (seq_lens, "seq_lens")):
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        self.batch, self.max_blocks, self.n_pages, self.n_kv_heads, self.fmt = batch, max_blocks, n_pages, heads, fmt
+        self.dtype = tail.dtype
+        work = torch.zeros(max(4, lib().gaac_kv8_workspace(batch, n_pages) // 4), dtype=torch.int32, device=self.device)
+        self._tensors = (pages, scales, tail, table, refs, seq_lens, work)
+        self._c = gaac_kv8(*(t.data_ptr() for t in self._tensors), n_pages, batch, heads, max_blocks, fmt,
+                           _DTYPES[tail.dtype])
+        self._ref = ctypes.byref(self._c)
+
+    pages = property(lambda s: s._tensors[0])
+    scales = property(lambda s: s._tensors[1])
+    tail = property(lambda s: s._tensors[2])
+    table = property(lambda s: s._tensors[3])
+    refs = property(lambda s: s._tensors[4])
+    seq_lens = property(lambda s: s._tensors[5])
+
+
+def _index_list(t, name, device):
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 tensor on the cache's device")
+    return t.shape[0]
+
+
+def _kv8_cu(cache: Kv8, cu_tokens):
+    if cu_tokens is None:
+        return 0
+    if _index_list(cu_tokens, "cu_tokens", cache.device) != cache.batch + 1:
+        raise ValueError("cu_tokens must hold batch + 1 offsets")
+    return cu_tokens.data_ptr()
+
+
+def kv8_append(cache: Kv8, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor | None = None, status=None,
+               stream=None) -> None:
+    """Appends rows cu_tokens[b] .. cu_tokens[b + 1] of k and v ([n, kv_heads, 128] of the cache's type, heads and
+    channels contiguous) to sequence b; without cu_tokens (int32 [batch + 1]) one row for each sequence.  The pages
+    of blocks that fill must have been reserved."""
+    cu = _kv8_cu(cache, cu_tokens)
+    for t in (k, v):
+        if (t.dtype != cache.dtype or t.device != cache.device or t.dim() != 3 or t.shape[1] != cache.n_kv_heads or
+                t.shape[2] != HEAD_DIM or t.stride(2) != 1 or (t.stride(1) != HEAD_DIM and t.shape[1] > 1)):
+            raise ValueError("k and v must be [n, kv_heads, 128] of the cache's type and device, heads and channels "
+                             "contiguous")
+    n = k.shape[0]
+    if v.shape[0] != n or (cu == 0 and n != cache.batch):
+        raise ValueError("k and v must hold the same rows: one for each sequence without cu_tokens")
+    width = cache.n_kv_heads * HEAD_DIM
+    _call("gaac_kv8_append", cache.device, stream, cache._ref, k.data_ptr(), v.data_ptr(), n,
+          k.stride(0) if n > 1 else width, v.stride(0) if n > 1 else width, cu, _ptr(status))
+
+
+def kv8_attention_workspace() -> int:
+    """Bytes of decode attention's workspace on the current device; zero them before the first call."""
+    return lib().gaac_kv8_attention_workspace()
+
+
+def kv8_decode_attention(cache: Kv8, q: torch.Tensor, scale: float, out: torch.Tensor, workspace: torch.Tensor,
+                         status=None, stream=None) -> None:
+    """q: [batch, q_heads, 128] of the cache's type (rows may be strided); out: the same shape, contiguous, of the
+    cache's type or fp32; workspace: kv8_attention_workspace() bytes, zero before the first call."""
+    if (q.dtype != cache.dtype or q.device != cache.device or q.dim() != 3 or q.shape[0] != cache.batch or
+            q.shape[2] != HEAD_DIM or q.stride(2) != 1 or (q.stride(1) != HEAD_DIM and q.shape[1] > 1)):
+        raise ValueError("q must be [batch, q_heads, 128] of the cache's type and device, heads and channels contiguous")
+    if out.shape != q.shape or out.dtype not in (cache.dtype, torch.float32) or out.device != cache.device or \
+            not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's shape and device, in the cache's type or fp32")
+    if workspace.device != cache.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the cache's device")
+    hq = q.shape[1]
+    _call("gaac_kv8_decode_attention", cache.device, stream, cache._ref, q.data_ptr(), hq,
+          q.stride(0) if cache.batch > 1 else hq * HEAD_DIM, scale, out.data_ptr(), _DTYPES[out.dtype],
+          workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(status))
+
+
+def kv8_reserve(cache: Kv8, cu_tokens: torch.Tensor | None = None, status=None, stream=None) -> None:
+    """Pages for the blocks that appending these tokens fills: the lowest free ones, in order of sequence and block."""
+    _call("gaac_kv8_reserve", cache.device, stream, cache._ref, _kv8_cu(cache, cu_tokens), _ptr(status))
+
+
+def kv8_release(cache: Kv8, seqs: torch.Tensor, status=None, stream=None) -> None:
+    """Empties the listed sequences (int32); pages that no other sequence holds become free."""
+    n = _index_list(seqs, "seqs", cache.device)
+    _call("gaac_kv8_release", cache.device, stream, cache._ref, seqs.data_ptr(), n, _ptr(status))
+
+
+def kv8_fork(cache: Kv8, src: torch.Tensor, dst: torch.Tensor, status=None, stream=None) -> None:
+    """Empty sequences dst (int32) become copies of src, sharing their full blocks."""
+    n = _index_list(src, "src", cache.device)
+    if _index_list(dst, "dst", cache.device) != n:
+        raise ValueError("src and dst must have the same length")
+    _call("gaac_kv8_fork", cache.device, stream, cache._ref, src.data_ptr(), dst.data_ptr(), n, _ptr(status))
+
+
+def kv8_compact(cache: Kv8, moved_to: torch.Tensor, stream=None) -> None:
+    """Moves the held pages to the front of the pool; moved_to (int32 [n_pages]) gets each page's new place, -1 for
+    free ones."""
+    if _index_list(moved_to, "moved_to", cache.device) != cache.n_pages:
+        raise ValueError("moved_to must hold n_pages values")
+    _call("gaac_kv8_compact", cache.device, stream, cache._ref, moved_to.data_ptr())

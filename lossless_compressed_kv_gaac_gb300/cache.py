@@ -7,8 +7,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (BLOCK, HEAD_DIM, Pools, append, attention_workspace, calibrate, decode_attention,
-               decode_attention_bf16, decompress, encode_blocks, entry_fields, new_stats, new_table)
+from . import (BLOCK, FP8_E4M3, HEAD_DIM, Kv8, Pools, append, attention_workspace, calibrate, decode_attention,
+               decode_attention_bf16, decompress, encode_blocks, entry_fields, kv8_append, kv8_attention_workspace,
+               kv8_compact, kv8_decode_attention, kv8_fork, kv8_release, kv8_reserve, new_stats, new_table)
 
 
 class LayerCache:
@@ -112,3 +113,74 @@ class LayerCache:
         n_raw = int((mode == 1).sum().item())
         return {"slot_tiles": n_slot, "raw_tiles": n_raw, "slot_bytes": n_slot * 12032, "raw_bytes": n_raw * 16384,
                 "table_bytes": self.table.numel() * 8}
+
+
+def _used_on(t: torch.Tensor, stream):
+    """A tensor made here for a call on another stream than the current one: its memory is not given out again
+    before that stream is past the call."""
+    if isinstance(stream, torch.cuda.Stream):
+        t.record_stream(stream)
+
+
+class Kv8Cache(Kv8):
+    """One layer's 8-bit paged KV cache: FP8 pages of 64 tokens with a scale for each (page, kv-head, K|V), the open
+    block of every sequence in the model's type, and counted pages that sequences share.
+
+    dtype: BF16 or FP16, the type of k, v, q and the open block.  Faults that only the device sees (no page left, a
+    length past the table) are recorded in `status`, as by the calls of the lossless cache; such a call leaves the
+    sequence as it was.
+    """
+
+    def __init__(self, n_pages: int, batch: int, n_kv_heads: int, max_blocks: int, fmt: int = FP8_E4M3,
+                 dtype: torch.dtype = torch.bfloat16, device="cuda"):
+        self._over(torch.zeros((n_pages, n_kv_heads, 2, BLOCK, HEAD_DIM), dtype=torch.uint8, device=device),
+                   torch.ones((n_pages, n_kv_heads, 2), dtype=torch.float32, device=device),
+                   torch.zeros((batch, n_kv_heads, 2, BLOCK, HEAD_DIM), dtype=dtype, device=device),
+                   torch.full((batch, max_blocks), -1, dtype=torch.int32, device=device),
+                   torch.zeros(n_pages, dtype=torch.int32, device=device),
+                   torch.zeros(batch, dtype=torch.int32, device=device), fmt)
+
+    @classmethod
+    def over(cls, pages, scales, tail, table, refs, seq_lens, fmt: int = FP8_E4M3) -> "Kv8Cache":
+        """A cache around existing tensors (the shapes are Kv8's)."""
+        self = cls.__new__(cls)
+        self._over(pages, scales, tail, table, refs, seq_lens, fmt)
+        return self
+
+    def _over(self, *args):
+        Kv8.__init__(self, *args)
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        with torch.cuda.device(self.device):
+            self._ws = torch.zeros(kv8_attention_workspace(), dtype=torch.uint8, device=self.device)
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor | None = None, reserve: bool = True,
+               stream=None):
+        """Tokens behind the sequences: rows cu_tokens[b] .. cu_tokens[b + 1] of k, v [n, kv_heads, 128] for sequence
+        b, or one row for each.  reserve=False: the pages of blocks that fill have been reserved before."""
+        if reserve:
+            kv8_reserve(self, cu_tokens, self.status, stream)
+        kv8_append(self, k, v, cu_tokens, self.status, stream)
+
+    def attention(self, q: torch.Tensor, scale: float, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """q: [batch, q_heads, 128] -> the same shape and type (or `out`'s: fp32 is allowed)."""
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            _used_on(out, stream)
+        kv8_decode_attention(self, q, scale, out, self._ws, self.status, stream)
+        return out
+
+    def reserve(self, cu_tokens: torch.Tensor | None = None, stream=None):
+        kv8_reserve(self, cu_tokens, self.status, stream)
+
+    def release(self, seqs: torch.Tensor, stream=None):
+        kv8_release(self, seqs, self.status, stream)
+
+    def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None):
+        kv8_fork(self, src, dst, self.status, stream)
+
+    def compact(self, stream=None) -> torch.Tensor:
+        """int32 [n_pages]: where each page has gone, -1 for free ones."""
+        moved_to = torch.empty(self.n_pages, dtype=torch.int32, device=self.device)
+        _used_on(moved_to, stream)
+        kv8_compact(self, moved_to, stream)
+        return moved_to

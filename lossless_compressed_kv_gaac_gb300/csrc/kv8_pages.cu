@@ -1,0 +1,387 @@
+// Pages of the 8-bit cache: reserve, release, fork, compact.
+//
+// refs[p] counts the sequences that hold page p; a page with none is free.  There is no free list to keep: the
+// lowest free pages are found by counting refs, so every result is a function of the tables alone (no order of
+// atomics shows).  Full blocks never change, so a fork shares them by counting and copies only the open block's
+// rows; nothing ever has to be copied on a write.
+//
+// All of it is bound by latency but the moves of a compaction, which are bound by memory.
+#include "kv8.cuh"
+
+namespace gaac {
+
+constexpr int kPgThreads = 1024;
+constexpr int kPgPer = kKv8Chunk / kPgThreads;  // pages per thread of a chunk
+
+// Exclusive prefix of x over the CTA's 1024 threads and the total.
+__device__ __forceinline__ int block_exclusive(int x, int* total) {
+  __shared__ int warp_sum[33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += v;
+  }
+  __syncthreads();  // the previous call's readers are done
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const int s = warp_sum[lane];
+    int t = s;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, t, d);
+      if (lane >= d) t += v;
+    }
+    warp_sum[lane] = t - s;
+    if (lane == 31) warp_sum[32] = t;
+  }
+  __syncthreads();
+  *total = warp_sum[32];
+  return warp_sum[warp] + incl - x;
+}
+
+// Bit i of the result: page p0 + i (of this thread's kPgPer) is held by a sequence; bits of pages that do not
+// exist are clear in both masks.
+__device__ __forceinline__ uint32_t held_mask(const int32_t* refs, int64_t p0, int64_t n_pages, uint32_t* exists) {
+  uint32_t held = 0, ex = 0;
+  if (p0 + kPgPer <= n_pages) {
+    int32_t r[kPgPer];
+#pragma unroll
+    for (int i = 0; i < kPgPer / 4; ++i) {
+      const int4 v = reinterpret_cast<const int4*>(refs + p0)[i];
+      r[4 * i] = v.x, r[4 * i + 1] = v.y, r[4 * i + 2] = v.z, r[4 * i + 3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < kPgPer; ++i) held |= (r[i] > 0 ? 1u : 0u) << i;
+    ex = (1u << kPgPer) - 1u;
+  } else {
+    for (int i = 0; i < kPgPer; ++i)
+      if (p0 + i < n_pages) {
+        ex |= 1u << i;
+        held |= (refs[p0 + i] > 0 ? 1u : 0u) << i;
+      }
+  }
+  *exists = ex;
+  return held;
+}
+
+// This CTA's chunk: counts its free (or held) pages, and says whether it is the last CTA to do so.
+__device__ __forceinline__ bool count_chunk(const Kv8Dev& c, const Kv8Work& w, bool free_ones, int32_t* ticket) {
+  __shared__ int last;
+  uint32_t ex;
+  const uint32_t held = held_mask(c.refs, static_cast<int64_t>(blockIdx.x) * kKv8Chunk + threadIdx.x * kPgPer, c.n_pages, &ex);
+  int total;
+  block_exclusive(__popc(free_ones ? ex & ~held : held), &total);
+  if (threadIdx.x == 0) {
+    c.work[w.chunks + blockIdx.x] = total;
+    last = kv8_atomic_add_acq_rel(ticket, 1u) == gridDim.x - 1;
+    if (last) *ticket = 0;
+  }
+  __syncthreads();
+  return last;
+}
+
+// Blocks of sequence b that the next tokens fill: [lo, hi).  false: the lengths are not valid.
+__device__ __forceinline__ bool fill_range(const Kv8Dev& c, const int32_t* cu, int b, int* lo, int* hi) {
+  const int len = c.lens[b];
+  const int64_t n = cu == nullptr ? 1 : static_cast<int64_t>(cu[b + 1]) - cu[b];
+  const int64_t now = len + n;
+  *lo = *hi = 0;
+  if (len < 0 || n < 0 || now > static_cast<int64_t>(c.max_blocks) * kBlock) return false;
+  *lo = len / kBlock;
+  *hi = static_cast<int>(now / kBlock);
+  return true;
+}
+
+// Entries without a page among the blocks that fill, in order of sequence and block, get the lowest free pages
+// in order.  Every CTA counts the free pages of its chunk; the last one to finish does the rest.
+__global__ void __launch_bounds__(kPgThreads) kv8_reserve_kernel(Kv8Dev c, const int32_t* cu, int32_t* status) {
+  __shared__ int sh_free;
+  dependent_wait();
+  dependent_launch();
+  const Kv8Work w = kv8_work(c.batch, c.n_pages);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (!count_chunk(c, w, true, c.work + w.tickets)) return;
+  // ---- how many pages each sequence lacks
+  int32_t* need = c.work + w.need;
+  for (int b = warp; b < c.batch; b += kPgThreads / 32) {
+    int lo, hi, miss = 0;
+    if (!fill_range(c, cu, b, &lo, &hi) && lane == 0) report(status, GAAC_EINVAL);
+    const int32_t* row = c.table + static_cast<int64_t>(b) * c.max_blocks;
+    for (int i0 = lo; i0 < hi; i0 += 32) miss += __popc(__ballot_sync(0xFFFFFFFFu, i0 + lane < hi && row[i0 + lane] < 0));
+    if (lane == 0) need[b] = miss;
+  }
+  __syncthreads();
+  // ---- the rank of each sequence's first one
+  int total = 0;
+  for (int b0 = 0; b0 < c.batch; b0 += kPgThreads) {
+    const int x = b0 + tid < c.batch ? need[b0 + tid] : 0;
+    int sum;
+    const int at = total + block_exclusive(x, &sum);
+    if (b0 + tid < c.batch) need[b0 + tid] = at;
+    total += sum;
+  }
+  if (tid == 0) need[c.batch] = total;
+  if (total == 0) return;
+  // ---- the lowest free pages, as many as are lacking
+  int32_t* list = c.work + w.list_a;
+  int found = 0;
+  for (unsigned ch = 0; ch < gridDim.x && found < total; ++ch) {
+    if (tid == 0) sh_free = __ldcg(c.work + w.chunks + ch);
+    __syncthreads();
+    const int n_free = sh_free;
+    __syncthreads();
+    if (n_free == 0) continue;
+    const int64_t p0 = static_cast<int64_t>(ch) * kKv8Chunk + tid * kPgPer;
+    uint32_t ex;
+    const uint32_t held = held_mask(c.refs, p0, c.n_pages, &ex);
+    uint32_t m = ex & ~held;
+    int sum, r = found + block_exclusive(__popc(m), &sum);
+    while (m != 0u && r < total) {
+      list[r++] = static_cast<int32_t>(p0 + __ffs(m) - 1);
+      m &= m - 1u;
+    }
+    found += sum;
+  }
+  if (found < total && tid == 0) report(status, GAAC_EPOOL);
+  __syncthreads();
+  // ---- into the table
+  for (int b = warp; b < c.batch; b += kPgThreads / 32) {
+    int r = need[b];
+    if (need[b + 1] == r) continue;
+    int lo, hi;
+    fill_range(c, cu, b, &lo, &hi);
+    int32_t* row = c.table + static_cast<int64_t>(b) * c.max_blocks;
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+      const bool miss = i0 + lane < hi && row[i0 + lane] < 0;
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, miss);
+      const int at = r + __popc(m & ((1u << lane) - 1u));
+      if (miss && at < found) {
+        const int32_t p = list[at];
+        row[i0 + lane] = p;
+        c.refs[p] = 1;
+      }
+      r += __popc(m);
+    }
+  }
+}
+
+constexpr int kRelThreads = 256;
+
+// One CTA per listed sequence.  A sequence listed twice is released once: whoever takes an entry out of the
+// table gives its page back.
+__global__ void __launch_bounds__(kRelThreads) kv8_release_kernel(Kv8Dev c, const int32_t* seqs, int32_t* status) {
+  dependent_wait();
+  dependent_launch();
+  const int b = seqs[blockIdx.x];
+  if (b < 0 || b >= c.batch) {
+    if (threadIdx.x == 0) report(status, GAAC_EINVAL);
+    return;
+  }
+  int32_t* row = c.table + static_cast<int64_t>(b) * c.max_blocks;
+  for (int i = threadIdx.x; i < c.max_blocks; i += kRelThreads) {
+    if (row[i] == -1) continue;
+    const int32_t p = atomicExch(row + i, -1);
+    if (p == -1) continue;
+    if (p < 0 || p >= c.n_pages) {
+      report(status, GAAC_EFORMAT);
+    } else if (atomicSub(c.refs + p, 1) <= 0) {
+      atomicAdd(c.refs + p, 1);
+      report(status, GAAC_EFORMAT);
+    }
+  }
+  if (threadIdx.x == 0) c.lens[b] = 0;
+}
+
+// One CTA per pair (src, dst).  A pair is refused as a whole (and reported) when an index is out of range, dst is
+// not empty, dst is listed before, src is the dst of some pair, or src's own row is not valid.
+__global__ void __launch_bounds__(kPgThreads) kv8_fork_kernel(Kv8Dev c, const int32_t* src, const int32_t* dst, int n,
+                                                              int32_t* status) {
+  dependent_wait();
+  dependent_launch();
+  const int tid = threadIdx.x, i = blockIdx.x;
+  const int s = src[i], d = dst[i];
+  int bad = 0;
+  if (s < 0 || s >= c.batch || d < 0 || d >= c.batch) {
+    bad = GAAC_EINVAL;
+  } else {
+    for (int j = tid; j < n; j += kPgThreads)
+      if (dst[j] == s || (j < i && dst[j] == d)) bad = GAAC_EINVAL;
+  }
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) report(status, GAAC_EINVAL);
+    return;
+  }
+  const int32_t* from = c.table + static_cast<int64_t>(s) * c.max_blocks;
+  int32_t* to = c.table + static_cast<int64_t>(d) * c.max_blocks;
+  const int len = c.lens[s], full = len / kBlock, open = len % kBlock;
+  int odd = 0;
+  if (len < 0 || len > static_cast<int64_t>(c.max_blocks) * kBlock) {
+    odd = 1;
+  } else {
+    for (int k = tid; k < c.max_blocks; k += kPgThreads) {
+      if (to[k] != -1) bad = 1;
+      if (k < full && (from[k] < 0 || from[k] >= c.n_pages)) odd = 1;
+    }
+    if (c.lens[d] != 0) bad = 1;
+  }
+  bad = __syncthreads_or(bad);
+  odd = __syncthreads_or(odd);
+  if (bad || odd) {
+    if (tid == 0) report(status, odd ? GAAC_EFORMAT : GAAC_EINVAL);
+    return;
+  }
+  for (int k = tid; k < full; k += kPgThreads) {
+    const int32_t p = from[k];
+    to[k] = p;
+    atomicAdd(c.refs + p, 1);
+  }
+  // open rows of every (kv-head, K|V): 16 vectors of 16 bytes each
+  const int64_t tile = kBlock * kD;
+  const uint4* ts = reinterpret_cast<const uint4*>(c.tail + static_cast<int64_t>(s) * c.heads * 2 * tile);
+  uint4* td = reinterpret_cast<uint4*>(c.tail + static_cast<int64_t>(d) * c.heads * 2 * tile);
+  const int per = open * (kD / 8), all = per * 2 * c.heads;
+  for (int k = tid; k < all; k += kPgThreads) {
+    const int64_t at = static_cast<int64_t>(k / per) * (tile / 8) + k % per;
+    td[at] = ts[at];
+  }
+  if (tid == 0) c.lens[d] = len;
+}
+
+// ------------------------------------------------------------------ compact
+// With n held pages, the held pages at n and above move into the holes below n: the lowest hole takes the highest
+// page, and so on.  Source and target never overlap.
+//   1. every CTA counts the held pages of its chunk; the last one makes the counts prefixes
+//   2. holes and movers into two lists by rank; moved_to of the pages that stay
+//   3. contents, counts and the table
+
+__global__ void __launch_bounds__(kPgThreads) kv8_compact_count_kernel(Kv8Dev c) {
+  dependent_wait();
+  dependent_launch();
+  const Kv8Work w = kv8_work(c.batch, c.n_pages);
+  if (!count_chunk(c, w, false, c.work + w.tickets + 1)) return;
+  int run = 0;
+  for (unsigned c0 = 0; c0 < gridDim.x; c0 += kPgThreads) {
+    const unsigned ch = c0 + threadIdx.x;
+    const int x = ch < gridDim.x ? __ldcg(c.work + w.chunks + ch) : 0;
+    int sum;
+    const int at = run + block_exclusive(x, &sum);
+    if (ch < gridDim.x) c.work[w.chunks + ch] = at;
+    run += sum;
+  }
+  if (threadIdx.x == 0) {
+    c.work[w.chunks + gridDim.x] = run;  // held pages
+    if (run == c.n_pages) c.work[w.tickets + 2] = 0;  // nothing moves; otherwise step 2 says how many do
+  }
+}
+
+__global__ void __launch_bounds__(kPgThreads) kv8_compact_list_kernel(Kv8Dev c, int32_t* moved_to) {
+  dependent_wait();
+  dependent_launch();
+  const Kv8Work w = kv8_work(c.batch, c.n_pages);
+  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kKv8Chunk + threadIdx.x * kPgPer;
+  const int64_t held_all = c.work[w.chunks + gridDim.x];
+  uint32_t ex;
+  const uint32_t held = held_mask(c.refs, p0, c.n_pages, &ex);
+  int sum;
+  int before = c.work[w.chunks + blockIdx.x] + block_exclusive(__popc(held), &sum);
+  int32_t* holes = c.work + w.list_a;
+  int32_t* movers = c.work + w.list_b;
+#pragma unroll
+  for (int i = 0; i < kPgPer; ++i) {
+    if (!((ex >> i) & 1u)) continue;
+    const int64_t p = p0 + i;
+    const bool h = (held >> i) & 1u;
+    if (p == held_all) c.work[w.tickets + 2] = static_cast<int32_t>(held_all) - before;  // pages that move
+    int32_t to = h ? static_cast<int32_t>(p) : -1;
+    if (h && p >= held_all) {
+      const int rank = static_cast<int>(held_all) - 1 - before;
+      movers[rank] = static_cast<int32_t>(p);
+      to = -2 - rank;  // the hole of that rank, known when every list is written
+    } else if (!h && p < held_all) {
+      holes[p - before] = static_cast<int32_t>(p);
+    }
+    moved_to[p] = to;
+    before += h;
+  }
+}
+
+constexpr int kMvThreads = 256;
+
+__global__ void __launch_bounds__(kMvThreads) kv8_compact_move_kernel(Kv8Dev c, int32_t* moved_to) {
+  dependent_wait();
+  dependent_launch();
+  const Kv8Work w = kv8_work(c.batch, c.n_pages);
+  const int32_t* holes = c.work + w.list_a;
+  const int32_t* movers = c.work + w.list_b;
+  const int64_t items = static_cast<int64_t>(c.work[w.tickets + 2]) * c.heads;
+  const int tid = threadIdx.x;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int64_t m = it / c.heads;
+    const int h = static_cast<int>(it % c.heads);
+    const int64_t from = movers[m], to = holes[m];
+    const uint4* s = reinterpret_cast<const uint4*>(c.pages + (from * c.heads + h) * kKv8Pair);
+    uint4* d = reinterpret_cast<uint4*>(c.pages + (to * c.heads + h) * kKv8Pair);
+    uint4 x[kKv8Pair / 16 / kMvThreads];
+#pragma unroll
+    for (int i = 0; i < kKv8Pair / 16 / kMvThreads; ++i) x[i] = s[tid + kMvThreads * i];
+#pragma unroll
+    for (int i = 0; i < kKv8Pair / 16 / kMvThreads; ++i) d[tid + kMvThreads * i] = x[i];
+    if (tid == 0) {
+      reinterpret_cast<float2*>(c.scales)[to * c.heads + h] = reinterpret_cast<const float2*>(c.scales)[from * c.heads + h];
+      if (h == 0) {
+        c.refs[to] = c.refs[from];
+        c.refs[from] = 0;
+        moved_to[from] = static_cast<int32_t>(to);
+      }
+    }
+  }
+  // The table.  moved_to of a page that moves may or may not have been replaced above yet: both forms say the same.
+  const int64_t entries = static_cast<int64_t>(c.batch) * c.max_blocks;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kMvThreads + tid; i < entries; i += static_cast<int64_t>(gridDim.x) * kMvThreads) {
+    const int32_t p = c.table[i];
+    if (p < 0 || p >= c.n_pages) continue;
+    int32_t to = *reinterpret_cast<volatile int32_t*>(moved_to + p);
+    if (to <= -2) to = holes[-2 - to];
+    if (to != p) c.table[i] = to;
+  }
+}
+
+}  // namespace gaac
+
+using namespace gaac;
+
+static unsigned chunks_of(const gaac_kv8* c) { return static_cast<unsigned>((c->n_pages + kKv8Chunk - 1) / kKv8Chunk); }
+
+extern "C" int gaac_kv8_reserve(const gaac_kv8* cache, const int32_t* cu_tokens, int32_t* d_status, void* stream) {
+  if (!kv8_ok(cache) || (reinterpret_cast<uintptr_t>(cu_tokens) & 3u)) return GAAC_EINVAL;
+  return kv8_launch(kv8_reserve_kernel, dim3(chunks_of(cache)), kPgThreads, 0, stream, kv8_dev(cache), cu_tokens, d_status);
+}
+
+extern "C" int gaac_kv8_release(const gaac_kv8* cache, const int32_t* seqs, int n, int32_t* d_status, void* stream) {
+  if (!kv8_ok(cache) || n < 0) return GAAC_EINVAL;
+  if (n == 0) return GAAC_OK;
+  if (seqs == nullptr || (reinterpret_cast<uintptr_t>(seqs) & 3u)) return GAAC_EINVAL;
+  return kv8_launch(kv8_release_kernel, dim3(n), kRelThreads, 0, stream, kv8_dev(cache), seqs, d_status);
+}
+
+extern "C" int gaac_kv8_fork(const gaac_kv8* cache, const int32_t* src, const int32_t* dst, int n, int32_t* d_status,
+                             void* stream) {
+  if (!kv8_ok(cache) || n < 0 || n > cache->batch) return GAAC_EINVAL;
+  if (n == 0) return GAAC_OK;
+  if (src == nullptr || dst == nullptr || ((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) & 3u))
+    return GAAC_EINVAL;
+  return kv8_launch(kv8_fork_kernel, dim3(n), kPgThreads, 0, stream, kv8_dev(cache), src, dst, n, d_status);
+}
+
+extern "C" int gaac_kv8_compact(const gaac_kv8* cache, int32_t* moved_to, void* stream) {
+  if (!kv8_ok(cache) || moved_to == nullptr || (reinterpret_cast<uintptr_t>(moved_to) & 3u)) return GAAC_EINVAL;
+  const Kv8Dev c = kv8_dev(cache);
+  const unsigned chunks = chunks_of(cache);
+  int e = kv8_launch(kv8_compact_count_kernel, dim3(chunks), kPgThreads, 0, stream, c);
+  if (e == GAAC_OK) e = kv8_launch(kv8_compact_list_kernel, dim3(chunks), kPgThreads, 0, stream, c, moved_to);
+  if (e == GAAC_OK) e = kv8_launch(kv8_compact_move_kernel, dim3(152 * 8), kMvThreads, 0, stream, c, moved_to);
+  return e;
+}

@@ -1,0 +1,261 @@
+// Rotary positions.
+//
+// Channels (a, b) of pair j at position p turn by the angle p * w_j:
+//   a' = m (a cos - b sin),  b' = m (b cos + a sin).
+// The GAAC page's Appendix C studies rotary keys; this is the operator itself, applied before an append.
+//
+// Angles: w_j comes as a fraction of a turn in 64-bit fixed point, F_j = w_j / (2 pi) * 2^64.  The product
+// p * F_j modulo 2^64 is the exact fraction of the turn whatever the position (32-bit floats would be off by
+// 0.06 rad at a million), and its top 32 bits, as a signed number, are the angle in [-pi, pi): one float
+// conversion, then sincospi.  The angle is off by at most 2^-33 turns plus p * 2^-65.
+//
+// Memory bound: 2 bytes moved per byte of input.  A thread owns V pairs (16-byte vectors where alignment
+// allows) of one row and walks over heads with them, so the V sines and cosines are computed once for the
+// thread's heads; neighbouring threads take neighbouring vectors, then neighbouring heads.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "common.cuh"
+
+namespace gaac {
+
+struct RopeTensor {
+  const char* x;
+  char* out;
+  int64_t x_seq, x_tok, x_head, out_seq, out_tok, out_head;  // bytes
+  int copy;                                                  // out is other memory: the rest of the head is copied
+};
+
+struct RopeArgs {
+  RopeTensor t[2];
+  int heads0, heads;  // heads of the first tensor; of both
+  int n_tok, rot, dim;
+  const void* pos;
+  int pos64;
+  int64_t pos_seq, pos_tok;
+  const uint64_t* turns;
+  float mscale;
+  int inverse;
+  int units, rot_units;  // V-pair units of a head's rotated part; all units, the copied rest included
+  int walkers;           // threads that share the heads of a row
+  int64_t n;             // rows * walkers * units
+};
+
+template <typename T>
+struct RopeNum;
+template <>
+struct RopeNum<float> {
+  static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ float put(float v) { return v; }
+};
+template <>
+struct RopeNum<__nv_bfloat16> {
+  static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct RopeNum<__half> {
+  static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
+  static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
+};
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) RopeVec {
+  T v[V];
+};
+
+constexpr int kRopeThreads = 256;
+
+template <typename T, int V, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x;
+  if (id >= a.n) return;
+  const int u = static_cast<int>(id % a.units);
+  const int64_t rw = id / a.units;
+  const int walker = static_cast<int>(rw % a.walkers);
+  const int64_t row = rw / a.walkers;
+  const int64_t seq = row / a.n_tok, tok = row % a.n_tok;
+  using Vec = RopeVec<T, V>;
+  if (u >= a.rot_units) {  // channels behind the rotated part
+    const int64_t off = (a.rot + static_cast<int64_t>(u - a.rot_units) * V) * static_cast<int64_t>(sizeof(T));
+    for (int h = walker; h < a.heads; h += a.walkers) {
+      const RopeTensor& t = a.t[h >= a.heads0];
+      if (!t.copy) continue;
+      const int hh = h >= a.heads0 ? h - a.heads0 : h;
+      *reinterpret_cast<Vec*>(t.out + seq * t.out_seq + tok * t.out_tok + hh * t.out_head + off) =
+          *reinterpret_cast<const Vec*>(t.x + seq * t.x_seq + tok * t.x_tok + hh * t.x_head + off);
+    }
+    return;
+  }
+  const int64_t pi = seq * a.pos_seq + tok * a.pos_tok;
+  uint64_t p = a.pos64 ? static_cast<uint64_t>(static_cast<const int64_t*>(a.pos)[pi])
+                       : static_cast<uint64_t>(static_cast<int64_t>(static_cast<const int32_t*>(a.pos)[pi]));
+  if (a.inverse) p = 0 - p;
+  float c[V], s[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint64_t turn = p * a.turns[u * V + i] + (1ull << 31);
+    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s[i], &c[i]);
+    s[i] *= a.mscale;
+    c[i] *= a.mscale;
+  }
+  const int64_t o0 = static_cast<int64_t>(INTER ? 2 * u * V : u * V) * sizeof(T);
+  const int64_t o1 = INTER ? o0 + static_cast<int64_t>(V * sizeof(T)) : o0 + static_cast<int64_t>(a.rot / 2) * sizeof(T);
+  for (int h = walker; h < a.heads; h += a.walkers) {
+    const RopeTensor& t = a.t[h >= a.heads0];
+    const int hh = h >= a.heads0 ? h - a.heads0 : h;
+    const char* x = t.x + seq * t.x_seq + tok * t.x_tok + hh * t.x_head;
+    char* out = t.out + seq * t.out_seq + tok * t.out_tok + hh * t.out_head;
+    Vec v0 = *reinterpret_cast<const Vec*>(x + o0), v1 = *reinterpret_cast<const Vec*>(x + o1);
+    T e[2 * V], r[2 * V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      e[i] = v0.v[i];
+      e[V + i] = v1.v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : V + i;
+      const float x0 = RopeNum<T>::get(e[ia]), x1 = RopeNum<T>::get(e[ib]);
+      r[ia] = RopeNum<T>::put(x0 * c[i] - x1 * s[i]);
+      r[ib] = RopeNum<T>::put(x1 * c[i] + x0 * s[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      v0.v[i] = r[i];
+      v1.v[i] = r[V + i];
+    }
+    *reinterpret_cast<Vec*>(out + o0) = v0;
+    *reinterpret_cast<Vec*>(out + o1) = v1;
+  }
+}
+
+template <typename T, int V>
+static int rope_launch(const RopeArgs& a, bool inter, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.n + kRopeThreads - 1) / kRopeThreads));
+  cfg.blockDim = dim3(kRopeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = inter ? cudaLaunchKernelEx(&cfg, rope_kernel<T, V, true>, a)
+                              : cudaLaunchKernelEx(&cfg, rope_kernel<T, V, false>, a);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? GAAC_OK : GAAC_ECUDA;
+}
+
+template <typename T>
+static int rope_vec(RopeArgs& a, int v, bool inter, cudaStream_t st) {
+  switch (v) {
+    case 8:
+      if constexpr (sizeof(T) == 2) return rope_launch<T, 8>(a, inter, st);
+      return GAAC_EINVAL;
+    case 4: return rope_launch<T, 4>(a, inter, st);
+    case 2: return rope_launch<T, 2>(a, inter, st);
+    default: return rope_launch<T, 1>(a, inter, st);
+  }
+}
+
+// Elements (seq, tok, head) of the output are distinct: taken from the smallest stride up, each dimension
+// steps over everything below it.  Dimensions of size 1 do not count.
+static bool distinct(int64_t dim, int64_t n[3], int64_t s[3]) {
+  int64_t extent = dim;
+  bool used[3] = {n[0] <= 1, n[1] <= 1, n[2] <= 1};
+  for (int k = 0; k < 3; ++k) {
+    int at = -1;
+    for (int i = 0; i < 3; ++i)
+      if (!used[i] && (at < 0 || s[i] < s[at])) at = i;
+    if (at < 0) return true;
+    if (s[at] < extent) return false;
+    extent = s[at] * (n[at] - 1) + extent;
+    used[at] = true;
+  }
+  return true;
+}
+
+}  // namespace gaac
+
+using namespace gaac;
+
+extern "C" int gaac_rope(const gaac_rope_tensor* tensors, int n_tensors, int dtype, int64_t n_seq, int64_t n_tok,
+                         int head_dim, int rot_dim, const void* positions, int pos_bits, int64_t pos_seq_stride,
+                         int64_t pos_tok_stride, const uint64_t* turns, float mscale, unsigned flags, void* stream) {
+  if (tensors == nullptr || n_tensors < 1 || n_tensors > 2 || (dtype != GAAC_BF16 && dtype != GAAC_F16 && dtype != GAAC_F32) ||
+      (pos_bits != 32 && pos_bits != 64) || (flags & ~static_cast<unsigned>(GAAC_ROPE_INTERLEAVED | GAAC_ROPE_INVERSE)) ||
+      !std::isfinite(mscale))
+    return GAAC_EINVAL;
+  if (n_seq < 0 || n_tok < 0 || n_seq > 0x7FFFFFFF || n_tok > 0x7FFFFFFF || head_dim < 2 || head_dim > 4096 || rot_dim < 2 ||
+      rot_dim > head_dim || (rot_dim & 1))
+    return GAAC_EINVAL;
+  const int64_t rows = n_seq * n_tok;
+  if (rows > 0x7FFFFFFF) return GAAC_EINVAL;
+  const int size = dtype == GAAC_F32 ? 4 : 2;
+  int64_t heads = 0;
+  for (int i = 0; i < n_tensors; ++i) {
+    if (tensors[i].n_heads < 1 || tensors[i].n_heads > 65536) return GAAC_EINVAL;
+    heads += tensors[i].n_heads;
+  }
+  if (rows == 0) return GAAC_OK;
+  if (positions == nullptr || turns == nullptr || pos_seq_stride < 0 || pos_tok_stride < 0 ||
+      (reinterpret_cast<uintptr_t>(positions) & (pos_bits / 8 - 1)) || (reinterpret_cast<uintptr_t>(turns) & 7u))
+    return GAAC_EINVAL;
+  // Vector width: as many elements as one 16-byte access holds, halved until both halves of the rotated part,
+  // the rest of the head and every pointer and stride are multiples of it.
+  int v = 16 / size;
+  while (v > 1 && ((rot_dim / 2) % v || (head_dim - rot_dim) % v)) v /= 2;
+  RopeArgs a = {};
+  bool copies = false;
+  for (int i = 0; i < n_tensors; ++i) {
+    const gaac_rope_tensor& t = tensors[i];
+    if (t.x == nullptr || t.out == nullptr || t.x_seq < 0 || t.x_tok < 0 || t.x_head < 0) return GAAC_EINVAL;
+    const int64_t most = int64_t{1} << 56;
+    if (t.x_seq > most / n_seq || t.x_tok > most / n_tok || t.x_head > most / t.n_heads || t.out_seq > most / n_seq ||
+        t.out_tok > most / n_tok || t.out_head > most / t.n_heads)
+      return GAAC_EINVAL;
+    int64_t n[3] = {n_seq, n_tok, t.n_heads}, so[3] = {t.out_seq, t.out_tok, t.out_head};
+    if (t.out_seq < 0 || t.out_tok < 0 || t.out_head < 0 || !distinct(head_dim, n, so)) return GAAC_EINVAL;
+    const uintptr_t x0 = reinterpret_cast<uintptr_t>(t.x), o0 = reinterpret_cast<uintptr_t>(t.out);
+    if ((x0 | o0) & (size - 1)) return GAAC_EINVAL;
+    // In place means the same elements; any other overlap of input and output would read rotated values.
+    const bool same = x0 == o0 && (n_seq == 1 || t.x_seq == t.out_seq) && (n_tok == 1 || t.x_tok == t.out_tok) &&
+                      (t.n_heads == 1 || t.x_head == t.out_head);
+    const uintptr_t xe = x0 + ((n_seq - 1) * t.x_seq + (n_tok - 1) * t.x_tok + (t.n_heads - 1) * t.x_head + head_dim) * size;
+    const uintptr_t oe = o0 + ((n_seq - 1) * t.out_seq + (n_tok - 1) * t.out_tok + (t.n_heads - 1) * t.out_head + head_dim) * size;
+    if (!same && x0 < oe && o0 < xe) return GAAC_EINVAL;
+    const uintptr_t all = (n_seq > 1 ? (t.x_seq | t.out_seq) : 0) | (n_tok > 1 ? (t.x_tok | t.out_tok) : 0) |
+                          (t.n_heads > 1 ? (t.x_head | t.out_head) : 0);
+    while (v > 1 && ((all % v) || ((x0 | o0) & (static_cast<uintptr_t>(v) * size - 1)))) v /= 2;
+    a.t[i] = RopeTensor{static_cast<const char*>(t.x), static_cast<char*>(t.out), t.x_seq * size, t.x_tok * size,
+                        t.x_head * size, t.out_seq * size, t.out_tok * size, t.out_head * size, same ? 0 : 1};
+    copies = copies || !same;
+  }
+  a.heads0 = tensors[0].n_heads;
+  a.heads = static_cast<int>(heads);
+  a.n_tok = static_cast<int>(n_tok);
+  a.rot = rot_dim;
+  a.dim = head_dim;
+  a.pos = positions;
+  a.pos64 = pos_bits == 64;
+  a.pos_seq = pos_seq_stride;
+  a.pos_tok = pos_tok_stride;
+  a.turns = turns;
+  a.mscale = mscale;
+  a.inverse = (flags & GAAC_ROPE_INVERSE) != 0;
+  a.rot_units = rot_dim / 2 / v;
+  a.units = a.rot_units + (copies ? (head_dim - rot_dim) / v : 0);
+  a.walkers = a.heads;
+  a.n = rows * a.walkers * a.units;
+  if (a.n > (int64_t{1} << 38)) return GAAC_EINVAL;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool inter = (flags & GAAC_ROPE_INTERLEAVED) != 0;
+  if (dtype == GAAC_BF16) return rope_vec<__nv_bfloat16>(a, v, inter, st);
+  if (dtype == GAAC_F16) return rope_vec<__half>(a, v, inter, st);
+  return rope_vec<float>(a, v, inter, st);
+}

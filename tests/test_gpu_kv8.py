@@ -1,0 +1,560 @@
+"""The 8-bit paged cache on the GPU: append, decode attention and the page calls, alone and together."""
+import math
+import random
+
+import pytest
+import torch
+
+import lossless_compressed_kv_gaac_gb300 as G
+from lossless_compressed_kv_gaac_gb300.cache import Kv8Cache
+from tests import kv8_util as U
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+E4, E5 = G.FP8_E4M3, G.FP8_E5M2
+SCALE = 1 / math.sqrt(128)
+
+
+def rand(shape, dtype, seed=0, mul=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * mul).to(dtype)
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def cu_of(new):
+    return ints([0] + torch.cumsum(torch.tensor(new), 0).tolist())
+
+
+def ok(c):
+    torch.cuda.synchronize()
+    return int(c.status.item())
+
+
+def kv_of(n, heads, dtype, seed):
+    """Keys with uneven channels, values with others."""
+    s = torch.exp(0.5 * rand((2, heads, 128), F32, 77))
+    return ((rand((n, heads, 128), F32, seed) * s[0]).to(dtype), (rand((n, heads, 128), F32, seed + 1) * s[1]).to(dtype))
+
+
+def filled(lens, heads, fmt=E4, dtype=BF16, seed=0, spare=3, max_blocks=None, shuffle=True):
+    """A cache of sequences of these lengths, its pages scattered over the pool, and the tokens it was given."""
+    B = len(lens)
+    mb = max_blocks or max(1, max((n + 63) // 64 for n in lens))
+    need = sum(n // 64 for n in lens)
+    c = Kv8Cache(max(1, need + spare), B, heads, mb, fmt, dtype)
+    k, v = kv_of(sum(lens), heads, dtype, seed)
+    cu = cu_of(lens)
+    c.reserve(cu)
+    if shuffle and need:
+        perm = torch.randperm(c.n_pages, generator=torch.Generator().manual_seed(seed)).to(torch.int32).cuda()
+        c.table.copy_(torch.where(c.table >= 0, perm[c.table.clamp(min=0).long()], c.table))
+        held = torch.zeros_like(c.refs)
+        held[perm[:need].long()] = 1
+        c.refs.copy_(held)
+    c.append(k, v, cu, reserve=False)
+    assert ok(c) == 0
+    return c, k, v
+
+
+def check_blocks(c, streams):
+    """Every sequence's pages, scales and open block are those of its tokens ([2, n, heads, 128])."""
+    lens = c.seq_lens.tolist()
+    for b, x in streams.items():
+        assert lens[b] == x.shape[1]
+        full = lens[b] // 64
+        ids = c.table[b, :full].long()
+        blocks = x[:, :full * 64].reshape(2, full, 64, c.n_kv_heads, 128).permute(1, 3, 0, 2, 4)
+        f8, s = U.quantise(blocks, c.fmt)
+        assert U.f8_equal(c.pages[ids].view(U.FP8[c.fmt]), f8)
+        assert torch.equal(c.scales[ids], s)
+        assert torch.equal(c.tail[b, :, :, :lens[b] % 64], x[:, full * 64:].permute(2, 0, 1, 3))
+
+
+# ------------------------------------------------------------------ append
+
+@pytest.mark.parametrize("fmt", [E4, E5])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("heads,steps", [(1, [[1], [62], [1], [1], [63], [200]]), (3, [[5, 0, 64], [59, 0, 1], [0, 130, 0]]),
+                                         (8, [[63, 64, 65, 1], [1, 64, 63, 500], [128, 1, 1, 12]]),
+                                         (2, [[7] * 70, [57] * 70, [1] * 70])])
+def test_append_chunks(heads, steps, fmt, dtype):
+    B = len(steps[0])
+    total = [sum(s[b] for s in steps) for b in range(B)]
+    c = Kv8Cache(sum(n // 64 for n in total) + 2, B, heads, max(n // 64 for n in total) + 1, fmt, dtype)
+    got = {b: torch.zeros((2, 0, heads, 128), dtype=dtype, device="cuda") for b in range(B)}
+    for i, new in enumerate(steps):
+        k, v = kv_of(sum(new), heads, dtype, 10 * i)
+        c.append(k, v, cu_of(new))
+        at = 0
+        for b, n in enumerate(new):
+            got[b] = torch.cat([got[b], torch.stack([k[at:at + n], v[at:at + n]])], 1)
+            at += n
+        assert ok(c) == 0
+        check_blocks(c, got)
+    assert int((c.refs > 0).sum()) == sum(n // 64 for n in total)
+
+
+def test_append_one_by_one_equals_at_once():
+    lens = [64, 70, 130]
+    a, k, v = filled(lens, 4, E5, F16, shuffle=False)
+    b = Kv8Cache(a.n_pages, 3, 4, a.max_blocks, E5, F16)
+    cu = [0, 64, 134]
+    for t in range(130):
+        new = [int(t < n) for n in lens]
+        rows = [cu[i] + t for i in range(3) if new[i]]
+        b.append(k[rows], v[rows], cu_of(new))
+    assert ok(b) == 0
+    for i, n in enumerate(lens):
+        pa, pb = a.table[i, :n // 64].long(), b.table[i, :n // 64].long()
+        assert torch.equal(a.pages[pa], b.pages[pb]) and torch.equal(a.scales[pa], b.scales[pb])
+        assert torch.equal(a.tail[i, :, :, :n % 64], b.tail[i, :, :, :n % 64])
+
+
+def test_append_single_form_and_strides():
+    """Without cu_tokens; k and v slices of one projection's output with different token strides."""
+    c, k, v = filled([62, 0, 127, 5], 2, max_blocks=3)
+    tail, mine = c.tail.clone(), {b: U.tokens_of(c, b) for b in range(4)}
+    for step in range(3):
+        qkv = rand((4, 8, 128), BF16, step)
+        other = rand((4, 6, 128), BF16, step + 5)
+        c.append(qkv[:, 4:6], other[:, 2:4])
+        for b in range(4):
+            pos = int(c.seq_lens[b]) - 1
+            if (pos + 1) % 64:
+                assert torch.equal(c.tail[b, :, 0, pos % 64], qkv[b, 4:6]) and torch.equal(c.tail[b, :, 1, pos % 64], other[b, 2:4])
+    assert ok(c) == 0 and c.seq_lens.tolist() == [65, 3, 130, 8]
+    # rows that no new token took are as they were: sequence 0 filled its block (row 63 stays), then opened row 0
+    assert torch.equal(c.tail[0, :, :, 1:62], tail[0, :, :, 1:62]) and torch.equal(c.tail[0, :, :, 63], tail[0, :, :, 63])
+    assert torch.equal(c.tail[3, :, :, 8:], tail[3, :, :, 8:])
+    assert torch.equal(U.tokens_of(c, 3)[:, :5], mine[3])
+
+
+@pytest.mark.parametrize("fmt", [E4, E5])
+def test_append_special_blocks(fmt):
+    """Zeros, the type's extremes, subnormal magnitudes, NaN and infinities, each in a block of its own."""
+    k = rand((64 * 8, 1, 128), BF16, 3)
+    v = rand((64 * 8, 1, 128), BF16, 4)
+    big, tiny = torch.finfo(BF16).max, 2.0 ** -133
+    k[0:64] = 0
+    v[0:64] = -0.0
+    k[64:128] *= tiny
+    v[64:128] = tiny
+    k[130, 0, 7] = big
+    v[130, 0, 7] = -big
+    k[200, 0, 0], k[201, 0, 1], k[202, 0, 2] = math.nan, math.inf, -math.inf
+    v[256:320] = math.inf
+    k[256:320] = math.nan
+    k[320:384] = 1.75  # the format's largest number in every place
+    v[320:384] = -1.765625  # just above: the next scale
+    c = Kv8Cache(8, 1, 1, 8, fmt, BF16)
+    c.append(k, v, cu_of([512]))
+    assert ok(c) == 0
+    check_blocks(c, {0: torch.stack([k, v])})
+    assert c.scales[c.table[0, 0].long()].eq(1).all()
+
+
+def test_append_refused_on_the_device():
+    c, _, _ = filled([60, 60, 64, 192], 2, max_blocks=3, spare=1)
+    before = [t.clone() for t in c._tensors[:6]]
+    k, v = kv_of(40, 2, BF16, 9)
+    # sequence 0 lacks a page, 1 has one, 3 would pass the table
+    c.table[1, 0] = -1
+    c.table[0, 0] = -1
+    free = int((c.refs == 0).nonzero()[0])
+    c.table[1, 0] = free
+    c.append(k, v, cu_of([10, 10, 10, 10]), reserve=False)
+    assert ok(c) in (G.EPOOL, G.EINVAL)
+    assert c.seq_lens.tolist() == [60, 70, 74, 192]
+    assert torch.equal(c.tail[0], before[2][0]) and torch.equal(c.tail[3], before[2][3])
+    # the sequence works again once it has a page
+    c.status.zero_()
+    c.refs[free] = 1
+    c.release(ints([3]))
+    c.append(k[:10], v[:10], cu_of([10, 0, 0, 0]))
+    assert ok(c) == 0 and c.seq_lens.tolist() == [70, 70, 74, 0]
+    # offsets that are not valid: nothing happens
+    lens = c.seq_lens.tolist()
+    for cu in ([0, 5, 3, 10, 10], [0, 10, 20, 30, 41], [-1, 10, 20, 30, 40]):
+        c.status.zero_()
+        c.append(k, v, ints(cu), reserve=False)
+        assert ok(c) == G.EINVAL and c.seq_lens.tolist() == lens
+    c.status.zero_()
+    c.append(k, v, ints([20, 20, 20, 20, 30]), reserve=False)  # rows before the first offset belong to nobody
+    assert ok(c) == 0 and c.seq_lens.tolist() == lens[:3] + [10]
+    assert torch.equal(c.tail[3, :, 0, :10].transpose(0, 1), k[20:30])
+
+
+def test_append_empty_chunk():
+    c, _, _ = filled([3, 64], 1)
+    e = torch.empty((0, 1, 128), dtype=BF16, device="cuda")
+    c.append(e, e, ints([0, 0, 0]))
+    assert ok(c) == 0 and c.seq_lens.tolist() == [3, 64]
+
+
+# ------------------------------------------------------------------ attention
+
+@pytest.mark.parametrize("fmt,dtype", [(E4, BF16), (E5, F16), (E4, F16), (E5, BF16)])
+@pytest.mark.parametrize("lens,heads,group", [([1], 1, 1), ([64], 2, 4), ([65, 0, 63], 2, 8), ([777], 8, 2),
+                                              ([5, 128, 129, 191, 192, 1000], 4, 5), ([4096, 1, 300, 2049], 2, 7),
+                                              ([20000], 1, 8), ([63] * 40, 3, 3)])
+def test_attention(lens, heads, group, fmt, dtype):
+    c, _, _ = filled(lens, heads, fmt, dtype)
+    q = rand((len(lens), heads * group, 128), dtype, 5)
+    out = c.attention(q, SCALE)
+    assert ok(c) == 0 and out.dtype == dtype
+    U.check_attention(c, q, SCALE, out)
+    full = torch.full(q.shape, math.nan, dtype=F32, device="cuda")
+    assert c.attention(q, SCALE, out=full) is full
+    U.check_attention(c, q, SCALE, full)
+    for b, n in enumerate(lens):
+        if n == 0:
+            assert (out[b] == 0).all()
+
+
+def test_attention_many_short_sequences():
+    """More (sequence, head) pairs than the GPU holds at once, ragged, with empty rows among them."""
+    lens = [(37 * i) % 400 for i in range(300)]
+    c, _, _ = filled(lens, 4)
+    q = rand((300, 16, 128), BF16, 5)
+    U.check_attention(c, q, SCALE, c.attention(q, SCALE))
+    assert ok(c) == 0
+
+
+def test_attention_scales_far_apart():
+    """V scales 2^-40 .. 2^40 apart between blocks, K scales 2^-6 .. 2^6, and scores that favour either end."""
+    c, _, _ = filled([64 * 40 + 7] * 3, 2)
+    e = torch.randint(-40, 41, c.scales.shape[:2], generator=torch.Generator().manual_seed(1)).cuda()
+    c.scales[:, :, 1] = torch.exp2(e.float())
+    c.scales[:, :, 0] = torch.exp2((e % 13 - 6).float() - 6)
+    q = rand((3, 8, 128), BF16, 5)
+    for scale in (SCALE, -SCALE, 0.0, 3.0):
+        U.check_attention(c, q, scale, c.attention(q, scale, out=torch.empty(q.shape, device="cuda")))
+    # scales that are not powers of two
+    c.scales.mul_(torch.rand(c.scales.shape, device="cuda") + 0.5)
+    U.check_attention(c, q, SCALE, c.attention(q, SCALE))
+    assert ok(c) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_attention_query_range(dtype):
+    """Queries of 1e4 with a small scale and of 1e-4 with a large one; one row of zeros."""
+    c, _, _ = filled([300, 64, 40], 2, E4, dtype)
+    for mul in (1e4, 1e-4):
+        q = rand((3, 8, 128), F32, 5)
+        q = (q * mul).to(dtype)
+        q[0, 3] = 0
+        U.check_attention(c, q, SCALE / mul, c.attention(q, SCALE / mul))
+    if dtype == BF16:
+        q = (rand((3, 8, 128), F32, 5) * 1e30).to(dtype)
+        U.check_attention(c, q, 1e-31, c.attention(q, 1e-31))
+    assert ok(c) == 0
+
+
+def test_attention_ignores_what_is_not_its_own():
+    """Rows behind the open block's tokens, other pages and entries behind the length: NaN there changes nothing."""
+    lens = [130, 1, 64, 0, 127]
+    c, _, _ = filled(lens, 2, max_blocks=6)
+    q = rand((5, 8, 128), BF16, 5)
+    a = c.attention(q, SCALE)
+    for b, n in enumerate(lens):
+        c.tail[b, :, :, n % 64:] = math.nan if b % 2 else math.inf
+        c.table[b, n // 64:] = 2 ** 31 - 1 if b % 2 else -7
+    c.pages[c.refs == 0] = 0x7F
+    c.scales[c.refs == 0] = math.nan
+    assert torch.equal(c.attention(q, SCALE), a) and ok(c) == 0
+
+
+def test_attention_nan_and_infinite_tokens():
+    """A NaN in a head's key spoils that head's rows alone; an infinite logit makes its weight NaN as in a softmax."""
+    c, k, v = filled([200, 200], 2)
+    q = rand((2, 8, 128), BF16, 5)
+    a = c.attention(q, SCALE)
+    page = int(c.table[0, 1])
+    c.pages[page, 1, 0, 3, 5] = 0x7F
+    b = c.attention(q, SCALE)
+    assert torch.isnan(b[0, 4:]).all() and torch.equal(b[0, :4], a[0, :4]) and torch.equal(b[1], a[1])
+    c.pages[page, 1, 0, 3, 5] = 0
+    c.tail[1, 0, 1, 2, 9] = math.nan  # V, token 194 of sequence 1, channel 9
+    b = c.attention(q, SCALE)
+    bad = torch.isnan(b)
+    assert bad[1, :4, 9].all() and bad.sum() == 4
+
+
+def test_attention_bad_table_and_lengths():
+    c, _, _ = filled([300, 300, 300], 2)
+    q = rand((3, 8, 128), BF16, 5)
+    a = c.attention(q, SCALE)
+    good = c.table.clone()
+    for bad in (c.n_pages, -1, 2 ** 31 - 1, -2 ** 31):
+        c.table[1, 2] = bad
+        b = c.attention(q, SCALE)
+        assert ok(c) == G.EFORMAT
+        c.status.zero_()
+        assert torch.equal(b[0], a[0]) and torch.equal(b[2], a[2]) and torch.isfinite(b).all()
+    c.table.copy_(good)
+    for bad in (-1, 64 * c.max_blocks + 1, 2 ** 31 - 1, -2 ** 31):
+        c.seq_lens[1] = bad
+        b = c.attention(q, SCALE)
+        assert ok(c) == G.EINVAL
+        c.status.zero_()
+        assert torch.equal(b[0], a[0]) and torch.equal(b[2], a[2]) and (b[1] == 0).all()
+    c.seq_lens[1] = 300
+    assert torch.equal(c.attention(q, SCALE), a) and ok(c) == 0
+
+
+def test_attention_strided_queries_streams_and_graph():
+    c, _, _ = filled([700, 33, 1500], 4)
+    qkv = rand((3, 24, 128), BF16, 5)
+    q = qkv[:, :16]
+    a = c.attention(q.contiguous(), SCALE)
+    assert torch.equal(c.attention(q, SCALE), a)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    b = c.attention(q, SCALE, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(b, a)
+    out = torch.empty_like(a)
+    g = torch.cuda.CUDAGraph()
+    k1, v1 = kv_of(3, 4, BF16, 50)
+    with torch.cuda.graph(g):
+        c.append(k1, v1)
+        c.attention(q, SCALE, out=out)
+    h = torch.cuda.CUDAGraph()
+    out2 = torch.empty_like(a)
+    with torch.cuda.graph(h):  # a second graph over the same cache and workspace, replayed in turn
+        c.attention(q, SCALE, out=out2)
+    for step in range(3):
+        g.replay()
+        h.replay()
+        assert ok(c) == 0 and c.seq_lens.tolist() == [701 + step, 34 + step, 1501 + step]
+        U.check_attention(c, q, SCALE, out)
+        assert torch.equal(out, out2)
+
+
+def test_attention_offsets_past_32_bits():
+    """A pool of more than 4 GB: pages at its end."""
+    n = 36000
+    c = Kv8Cache(n, 2, 8, 40, E4, BF16)
+    k, v = kv_of(2 * 2000, 8, BF16, 1)
+    c.reserve(ints([0, 2000, 4000]))
+    c.refs.zero_()
+    c.table.copy_(torch.where(c.table >= 0, n - 1 - c.table, c.table))
+    c.refs[-62:] = 1
+    c.append(k, v, ints([0, 2000, 4000]), reserve=False)
+    q = rand((2, 16, 128), BF16, 5)
+    U.check_attention(c, q, SCALE, c.attention(q, SCALE))
+    moved = c.compact()
+    assert moved[-62:].sort().values.tolist() == list(range(62))
+    U.check_attention(c, q, SCALE, c.attention(q, SCALE))
+    check_blocks(c, {0: torch.stack([k[:2000], v[:2000]]), 1: torch.stack([k[2000:], v[2000:]])})
+    assert ok(c) == 0
+
+
+def test_attention_refusals():
+    c, _, _ = filled([10, 10], 2)
+    q = rand((2, 8, 128), BF16)
+    for bad in (lambda: c.attention(q.half(), SCALE), lambda: c.attention(q[:1], SCALE), lambda: c.attention(q.cpu(), SCALE),
+                lambda: c.attention(q[..., :64], SCALE), lambda: c.attention(q, SCALE, out=torch.empty_like(q)[:, :4]),
+                lambda: c.attention(q, SCALE, out=q.half()), lambda: c.attention(q.transpose(0, 1), SCALE)):
+        with pytest.raises(ValueError):
+            bad()
+    for n in (7, 36):
+        with pytest.raises(G.GaacError) as e:
+            c.attention(rand((2, n, 128), BF16), SCALE)
+        assert e.value.status == G.EINVAL
+    with pytest.raises(G.GaacError):
+        c.attention(q, math.nan)
+    with pytest.raises(ValueError):
+        c.append(q[:, :2], q[:, :3])
+    with pytest.raises(ValueError):
+        c.append(q[:1, :2], q[:1, :2])
+    with pytest.raises(ValueError):
+        c.append(q[:, :2], q[:, :2], ints([0, 1]))
+    with pytest.raises(ValueError):
+        c.release(torch.tensor([0], device="cuda"))
+    with pytest.raises(ValueError):
+        c.fork(ints([0]), ints([0, 1]))
+    with pytest.raises(ValueError):
+        G.kv8_compact(c, ints([0]))
+
+
+# ------------------------------------------------------------------ pages
+
+def both(c, m, what, *args):
+    """The call on the cache and on the plain model."""
+    if what in ("reserve", "append"):
+        new = args[0]
+        if what == "append":
+            k, v = kv_of(max(1, sum(new)), c.n_kv_heads, c.dtype, sum(new))
+            c.append(k, v, cu_of(new), reserve=False)
+        else:
+            c.reserve(cu_of(new))
+        getattr(m, what)(new)
+    elif what == "compact":
+        assert c.compact().tolist() == m.compact()
+    else:
+        getattr(c, what)(*(ints(a) for a in args))
+        getattr(m, what)(*args)
+    torch.cuda.synchronize()
+    m.check(c)
+
+
+@pytest.mark.parametrize("n_pages,batch,max_blocks", [(1, 1, 1), (7, 3, 4), (63, 5, 40), (8193, 40, 300), (20000, 70, 33)])
+def test_page_calls_follow_the_model(n_pages, batch, max_blocks):
+    rng = random.Random(n_pages)
+    c, m = Kv8Cache(n_pages, batch, 1, max_blocks), U.Model(n_pages, batch, max_blocks)
+    for step in range(24):
+        what = rng.choice(["grow", "grow", "reserve", "release", "fork", "compact"])
+        some = [rng.randrange(-1, batch + 1) for _ in range(rng.randrange(0, batch + 1))]
+        if what in ("grow", "reserve"):
+            most = rng.choice([1, 70, 64 * max_blocks // 3 + 1])
+            new = [rng.randrange(most + 1) for _ in range(batch)]
+            both(c, m, "reserve", new)
+            if what == "grow":
+                both(c, m, "append", new)
+        elif what == "fork":
+            both(c, m, "fork", some, [rng.randrange(-1, batch + 1) for _ in some])
+        elif what == "release":
+            both(c, m, "release", some)
+        else:
+            both(c, m, "compact")
+
+
+def test_fork_shares_and_release_gives_back():
+    c, k, v = filled([200, 0, 0, 0], 2, max_blocks=6, spare=10)
+    q = rand((1, 8, 128), BF16, 5).expand(4, 8, 128).contiguous()
+    c.fork(ints([0, 0, 0]), ints([1, 3, 2]))
+    a = c.attention(q, SCALE)
+    assert ok(c) == 0 and all(torch.equal(a[0], a[i]) for i in range(1, 4))
+    assert int((c.refs > 0).sum()) == 3 and c.refs.max() == 4
+    # the branches grow apart without touching one another
+    own = {}
+    for b in range(4):
+        n = 30 + 40 * b
+        kb, vb = kv_of(n, 2, BF16, 100 + b)
+        new = [0] * 4
+        new[b] = n
+        c.append(kb, vb, cu_of(new))
+        own[b] = torch.cat([torch.stack([k, v]), torch.stack([kb, vb])], 1)
+    assert ok(c) == 0
+    check_blocks(c, own)
+    U.check_attention(c, q, SCALE, c.attention(q, SCALE))
+    c.release(ints([0, 2, 0]))
+    check_blocks(c, {1: own[1], 3: own[3]})
+    c.compact()
+    check_blocks(c, {1: own[1], 3: own[3]})
+    c.release(ints([1, 3]))
+    assert ok(c) == 0 and (c.refs == 0).all() and (c.table == -1).all() and (c.seq_lens == 0).all()
+
+
+def test_fork_and_release_refusals():
+    c, _, _ = filled([100, 64, 0, 0, 0], 1, max_blocks=4, spare=4)
+    c.reserve(cu_of([0, 0, 64, 0, 0]))  # sequence 2: empty, but with a page reserved
+    m = U.Model(c.n_pages, 5, 4)
+    m.table, m.refs, m.lens = c.table.tolist(), c.refs.tolist(), c.seq_lens.tolist()
+    for src, dst in (([0], [1]), ([0], [2]), ([0], [5]), ([-1], [3]), ([0, 1], [3, 3]), ([0, 3], [4, 1]), ([0], [0])):
+        c.status.zero_()
+        both(c, m, "fork", src, dst)
+        assert ok(c) == G.EINVAL
+    c.status.zero_()
+    both(c, m, "release", [2, 2, -1])
+    assert ok(c) == G.EINVAL
+    c.status.zero_()
+    c.table[0, 0] = c.n_pages
+    c.fork(ints([0]), ints([2]))
+    assert ok(c) == G.EFORMAT and int(c.seq_lens[2]) == 0
+    c.status.zero_()
+    c.release(ints([0]))
+    assert ok(c) == G.EFORMAT and (c.table[0] == -1).all()
+
+
+def test_pool_runs_out_and_recovers():
+    c, m = Kv8Cache(5, 3, 1, 8), U.Model(5, 3, 8)
+    new = [128, 128, 128]
+    both(c, m, "reserve", new)
+    assert ok(c) == G.EPOOL
+    both(c, m, "append", new)  # the third sequence lacks a page and stays as it was
+    assert c.seq_lens.tolist() == [128, 128, 0]
+    c.status.zero_()
+    both(c, m, "release", [0])
+    both(c, m, "reserve", [0, 0, 128])
+    both(c, m, "append", [0, 0, 128])
+    assert ok(c) == 0 and c.seq_lens.tolist() == [0, 128, 128]
+    c.reserve(ints([0, 600, 600, 600]))  # past the table
+    assert ok(c) == G.EINVAL
+    m.check(c)
+
+
+def test_full_and_empty_pools_compact():
+    c, m = Kv8Cache(9, 2, 1, 9), U.Model(9, 2, 9)
+    both(c, m, "compact")
+    both(c, m, "reserve", [320, 256])
+    both(c, m, "append", [320, 256])
+    both(c, m, "compact")
+    assert ok(c) == 0
+
+
+# ------------------------------------------------------------------ together
+
+@pytest.mark.parametrize("fmt,dtype", [(E4, BF16), (E5, F16)])
+def test_serving_run(fmt, dtype):
+    """Prefill, forks, decode steps with rotary positions in a captured graph, release, compact: the attention at
+    every step against 64 bits over exactly the tokens that went in."""
+    heads, group, B = 2, 4, 6
+    w, ms = G.rope_frequencies(128, 1e6, "bands", 4.0, original_len=1024)
+    turns = G.rope_turns(w, "cuda")
+    c = Kv8Cache(64, B, heads, 12, fmt, dtype)
+    seen = {}
+
+    def take(k, v, new):
+        at = 0
+        for b, n in enumerate(new):
+            seen[b] = torch.cat([seen.get(b, torch.zeros((2, 0, heads, 128), dtype=dtype, device="cuda")),
+                                 torch.stack([k[at:at + n], v[at:at + n]])], 1)
+            at += n
+
+    new = [150, 64, 0, 3, 0, 0]
+    q, (k, v) = rand((sum(new), heads * group, 128), dtype, 1), kv_of(sum(new), heads, dtype, 2)
+    pos = torch.cat([torch.arange(n) for n in new]).cuda()
+    k0 = k.clone()
+    G.rope(q, k, pos, turns, mscale=ms)
+    assert ((k.double() - U.rope_ref(k0, pos, w, mscale=ms)).abs() <= torch.finfo(dtype).eps * 4 * (k0.double().abs().amax())).all()
+    c.append(k, v, cu_of(new))
+    take(k, v, new)
+    c.fork(ints([0, 0, 3]), ints([2, 4, 5]))
+    seen.update({2: seen[0], 4: seen[0], 5: seen[3]})
+    assert ok(c) == 0
+    check_blocks(c, seen)
+    # decode steps: one graph for rope, append and attention
+    qs, ks, vs = rand((B, heads * group, 128), dtype), rand((B, heads, 128), dtype), rand((B, heads, 128), dtype)
+    out = torch.empty_like(qs)
+
+    def step():
+        G.rope(qs, ks, c.seq_lens, turns, mscale=ms)
+        c.append(ks, vs)
+        c.attention(qs, SCALE, out=out)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(70):
+        if i == 40:
+            c.release(ints([1, 4]))
+            seen[1] = seen[4] = torch.zeros((2, 0, heads, 128), dtype=dtype, device="cuda")
+            c.compact()
+        qs.copy_(rand((B, heads * group, 128), dtype, 100 + i))
+        kn, vn = kv_of(B, heads, dtype, 300 + i)
+        ks.copy_(kn)
+        vs.copy_(vn)
+        g.replay()
+        take(ks, vs, [1] * B)
+        if i % 13 == 0 or i == 41:
+            U.check_attention(c, qs, SCALE, out)
+            check_blocks(c, seen)
+    assert ok(c) == 0
+    check_blocks(c, seen)
