@@ -101,15 +101,4 @@ __device__ __forceinline__ float2 kv8_pair(uint32_t w) {  // two 16-bit numbers 
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-// Two FP8 numbers (low byte first) as f16x2: exact, e5m2's infinities and both formats' NaN included.
-template <int FMT>
-__device__ __forceinline__ uint32_t fp8x2_to_f16x2(uint16_t b) {
-  uint32_t r;
-  if (FMT == GAAC_FP8_E4M3)
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(b));
-  else
-    asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(r) : "h"(b));
-  return r;
-}
-
 }  // namespace gaac

@@ -29,33 +29,30 @@
 
 namespace gaac {
 
-constexpr int kKaWarps = 4;                  // compute warps
-constexpr int kKaThreads = 32 * (kKaWarps + 1);
-constexpr int kKaStages = 5;
-constexpr int kKaCtasPerSm = 2;
+constexpr int kKaGroups = 5;                 // pairs of compute warps, units dealt out in turn
+constexpr int kKaWarps = 2 * kKaGroups;      // a warp takes 32 tokens of a page, 16 of half an open block
+constexpr int kKaCompute = 32 * kKaWarps;
+constexpr int kKaCopyWarps = 2;
+constexpr int kKaThreads = kKaCompute + 32 * kKaCopyWarps;
+constexpr int kKaStages = 10;                // unit i uses stage i % stages and belongs to group i % groups
+constexpr int kKaHalf = kBlock / 2;          // tokens of an open block's unit
 constexpr int kKaRows = 8;                   // query heads per kv-head in the MMA columns
-constexpr int kKaMinUnits = 2;               // fewer units than this are not worth a CTA
+constexpr int kKaMinUnits = 5;               // fewer units than this are not worth a CTA
 constexpr int kKaStride = kD + 4;            // floats per row of a warp's state in shared memory (bank spread)
 constexpr int kKaQStride = 2 * kD + 8;       // bytes per query row kept for the open block
 constexpr int kKaPart = 3 * kKaRows + kKaRows * kD;  // floats of a partial: m, l, M, O
 constexpr uint32_t kKaFull = 0xFFFFFFFFu;
+static_assert(kKaStages % kKaGroups == 0, "a stage belongs to one group, which waits for all of its phases in turn");
 
-enum { kUnitPage = 0, kUnitOpen = 1, kUnitNone = 2, kUnitEnd = 3 };
-
-struct KaMeta {
-  int kind, first, last;
-  int n_tok;               // open block: its tokens
-  int b, h;
-  int cta0, n_cta;         // the CTAs that share the pair
-};
+enum { kUnitPage, kUnitOpen, kUnitNone, kUnitEnd };
 
 struct KaSmem {
   alignas(1024) uint8_t stage[kKaStages][kKv8Pair];
   alignas(128) uint16_t q[kKaStages][kKaRows * kD];
   alignas(16) float state[kKaWarps][kKaRows][kKaStride];
   alignas(16) uint8_t qraw[kKaRows][kKaQStride];
+  alignas(16) int4 meta[kKaStages][2];  // {kind, first of the pair in its group, last, tokens}, {b, h, first CTA, CTAs}
   alignas(16) float2 scale[kKaStages];
-  KaMeta meta[kKaStages];
   float m[kKaWarps][kKaRows], l[kKaWarps][kKaRows], mv[kKaWarps][kKaRows];
   uint64_t full[kKaStages], empty[kKaStages], sync;
   int last;
@@ -96,6 +93,23 @@ __device__ __forceinline__ float ka_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float ka_log2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Four FP8 numbers as two f16x2: (0, 1), (2, 3), or with SPLIT (0, 2), (1, 3).
+template <int FMT, bool SPLIT>
+__device__ __forceinline__ void ka_widen(uint32_t w, uint32_t& x, uint32_t& y) {
+  if (FMT == GAAC_FP8_E5M2) {  // an e5m2 byte is the high byte of the f16
+    x = __byte_perm(w, 0u, SPLIT ? 0x2404 : 0x1404);
+    y = __byte_perm(w, 0u, SPLIT ? 0x3414 : 0x3424);
+  } else {
+    if (SPLIT) w = __byte_perm(w, 0u, 0x3120);
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n cvt.rn.f16x2.e4m3x2 %1, hi;\n}"
+        : "=r"(x), "=r"(y) : "r"(w));
+  }
+}
 __device__ __forceinline__ uint32_t ka_pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -120,7 +134,7 @@ __device__ __forceinline__ KaSeq ka_seq(const Kv8Dev& c, int len) {
   KaSeq s;
   s.full = len / kBlock;
   s.open = len % kBlock;
-  s.units = max(1, s.full + (s.open ? 2 : 0));
+  s.units = max(1, s.full + (s.open + kKaHalf - 1) / kKaHalf);
   return s;
 }
 
@@ -160,167 +174,162 @@ __device__ __forceinline__ void ka_next(KaRing& r) {
   }
 }
 
-__device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pages, const CUtensorMap* tail) {
+__device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pages, const CUtensorMap* tail, int copier) {
   const Kv8Dev& c = a.c;
   const int lane = threadIdx.x & 31;
   KaRing ring;
-  // ---- all units, then this CTA's and where they begin
+  // ---- the cut: pieces of at most `piece` units
   int64_t total = 0;
+  int len32 = 0;  // lengths of 32 sequences, one a lane
   for (int b0 = 0; b0 < c.batch; b0 += 32) {
     int u = 0;
     if (b0 + lane < c.batch) {
-      const int len = c.lens[b0 + lane];
+      const int len = len32 = c.lens[b0 + lane];
       if (blockIdx.x == 0 && (len < 0 || len > static_cast<int64_t>(c.max_blocks) * kBlock)) report(a.status, GAAC_EINVAL);
       u = ka_seq(c, len).units;
     }
     // 32 sequences of up to 2^24 + 2 units: 30 bits
     total += static_cast<int64_t>(__reduce_add_sync(kKaFull, u)) * c.heads;
   }
-  const int64_t G = min(static_cast<int64_t>(gridDim.x), (total + kKaMinUnits - 1) / kKaMinUnits);
-  const int64_t u_begin = static_cast<int64_t>(blockIdx.x) * total / G, u_end = (static_cast<int64_t>(blockIdx.x) + 1) * total / G;
-  bool ok = true;
-  if (blockIdx.x < G && u_begin < u_end) {
-    int b = 0;
-    int64_t base = 0;  // units before sequence b
-    int len32 = 0, b32 = -1;
+  const int64_t piece = max(static_cast<int64_t>(kKaMinUnits), (total + gridDim.x - 1) / gridDim.x);
+  // Pieces begin with their pair where that needs no more CTAs: then none has parts of two pairs to bring to an
+  // end.  Otherwise the row of all units is cut without regard to pairs.
+  bool aligned = false;
+  if (static_cast<int64_t>(c.batch) * c.heads <= gridDim.x) {
+    int64_t pieces = 0;
     for (int b0 = 0; b0 < c.batch; b0 += 32) {
-      const int len = b0 + lane < c.batch ? c.lens[b0 + lane] : 0;
-      const int64_t u = b0 + lane < c.batch ? static_cast<int64_t>(ka_seq(c, len).units) * c.heads : 0;
-      int64_t incl = u;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t v = __shfl_up_sync(kKaFull, incl, d);
-        if (lane >= d) incl += v;
-      }
-      const uint32_t past = __ballot_sync(kKaFull, base + incl > u_begin);
-      if (past) {
-        const int at = __ffs(past) - 1;
-        base += __shfl_sync(kKaFull, incl - u, at);
-        b = b0 + at;
-        len32 = len;
-        b32 = b0;
-        break;
-      }
-      base += __shfl_sync(kKaFull, incl, 31);
+      const int len = c.batch <= 32 ? len32 : b0 + lane < c.batch ? c.lens[b0 + lane] : 0;
+      const int k = b0 + lane < c.batch ? static_cast<int>((ka_seq(c, len).units + piece - 1) / piece) : 0;
+      pieces += static_cast<int64_t>(__reduce_add_sync(kKaFull, k)) * c.heads;
     }
-    KaSeq s = ka_seq(c, __shfl_sync(kKaFull, len32, b - b32));
-    int h = static_cast<int>((u_begin - base) / s.units);
-    int64_t seg = base + static_cast<int64_t>(h) * s.units;  // first unit of the pair
-    int64_t u = u_begin;
-    while (u < u_end && ok) {
-      const int l0 = static_cast<int>(u - seg);
-      int l1 = static_cast<int>(min(u_end, seg + s.units) - seg);
-      // An open block's two units go together to the CTA that has the first.
-      const bool skip = s.open && l0 == s.full + 1;
-      if (!skip) {
-        if (s.open && l1 > s.full) l1 = s.full + 2;
-        const int64_t tail_unit = seg + s.units - (s.open ? 2 : 1);
-        KaMeta meta;
-        meta.b = b;
-        meta.h = h;
-        meta.cta0 = static_cast<int>(((seg + 1) * G - 1) / total);
-        meta.n_cta = static_cast<int>(((tail_unit + 1) * G - 1) / total) - meta.cta0 + 1;
-        meta.n_tok = s.open;
-        const int blk_end = min(l1, s.full);
-        const bool with_open = s.open && l1 > s.full;
-        const uint32_t q_bytes = static_cast<uint32_t>(a.r) * kD * 2;
-        const uint16_t* q = a.q + b * a.q_seq + static_cast<int64_t>(h) * a.r * kD;
-        bool first = true;
-        const int32_t* row = c.table + static_cast<int64_t>(b) * c.max_blocks;
-        int32_t pg = l0 + lane < blk_end ? row[l0 + lane] : 0;
-        for (int blk0 = l0; blk0 < blk_end && ok; blk0 += 32) {
-          const int32_t pg_next = blk0 + 32 + lane < blk_end ? row[blk0 + 32 + lane] : 0;
-          const int n = min(32, blk_end - blk0);
-          for (int i = 0; i < n && ok; ++i) {
-            const int32_t page = __shfl_sync(kKaFull, pg, i);
-            ok = ka_acquire(sm, ring, a.status);
-            if (lane == 0 && ok) {
-              const bool valid = page >= 0 && page < c.n_pages;
-              if (!valid) report(a.status, GAAC_EFORMAT);
-              meta.kind = valid ? kUnitPage : kUnitNone;
-              meta.first = first;
-              meta.last = !with_open && blk0 + i + 1 == blk_end;
-              sm.meta[ring.stage] = meta;
-              uint64_t* full = &sm.full[ring.stage];
-              const int64_t tile = static_cast<int64_t>(valid ? page : 0) * c.heads + h;
-              if (valid) {
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(&sm.scale[ring.stage])),
-                             "l"(c.scales + 2 * tile) : "memory");
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(full)) : "memory");
-              } else {
-                ka_arrive(full);
-              }
-              mbar_arrive_expect_tx(full, (valid ? kKv8Pair : 0) + (first ? q_bytes : 0));
-              if (valid) ka_tma(sm.stage[ring.stage], pages, 0, static_cast<int>(tile * 2 * kBlock), full);
-              if (first) bulk_g2s(sm.q[ring.stage], q, q_bytes, full);
-            }
-            first = false;
-            ka_next(ring);
-          }
-          pg = pg_next;
-        }
-        if (with_open && ok) {
-#pragma unroll 1
-          for (int kind = 0; kind < 2 && ok; ++kind) {
-            ok = ka_acquire(sm, ring, a.status);
-            if (lane == 0 && ok) {
-              meta.kind = kUnitOpen;
-              meta.first = first;
-              meta.last = 1;
-              sm.meta[ring.stage] = meta;
-              uint64_t* full = &sm.full[ring.stage];
-              ka_arrive(full);
-              mbar_arrive_expect_tx(full, kKv8Pair + (first ? q_bytes : 0));
-              const int y = static_cast<int>(((static_cast<int64_t>(b) * c.heads + h) * 2 + kind) * kBlock);
-              ka_tma(sm.stage[ring.stage], tail, 0, y, full);
-              ka_tma(sm.stage[ring.stage] + kKv8Tile, tail, kD / 2, y, full);
-              if (first) bulk_g2s(sm.q[ring.stage], q, q_bytes, full);
-            }
-            first = false;
-            ka_next(ring);
-          }
-        } else if (s.units == 1 && s.full == 0 && ok) {  // an empty sequence
-          ok = ka_acquire(sm, ring, a.status);
-          if (lane == 0 && ok) {
-            meta.kind = kUnitNone;
-            meta.first = 1;
-            meta.last = 1;
-            sm.meta[ring.stage] = meta;
-            ka_arrive(&sm.full[ring.stage]);
-            mbar_arrive_expect_tx(&sm.full[ring.stage], q_bytes);
-            bulk_g2s(sm.q[ring.stage], q, q_bytes, &sm.full[ring.stage]);
-          }
-          ka_next(ring);
-        }
-      }
-      // ---- the next pair
-      seg += s.units;
-      u = seg;
-      if (++h == c.heads) {
-        h = 0;
-        if (++b >= c.batch) break;
-        if (b - b32 >= 32) {
-          b32 += 32;
-          len32 = b32 + lane < c.batch ? c.lens[b32 + lane] : 0;
-        }
-        s = ka_seq(c, __shfl_sync(kKaFull, len32, b - b32));
-      }
-    }
+    aligned = pieces <= gridDim.x;
   }
-  if (ok) ok = ka_acquire(sm, ring, a.status);
-  if (ok) {
-    if (lane == 0) {
-      sm.meta[ring.stage].kind = kUnitEnd;
-      ka_arrive(&sm.full[ring.stage]);
-      ka_arrive(&sm.full[ring.stage]);
+  // In places (units, or pieces when aligned): where this CTA begins and ends.
+  const int64_t begin = aligned ? blockIdx.x : blockIdx.x * piece;
+  int b = c.batch;
+  int64_t base = 0;  // places before sequence b
+  int b32 = -1;
+  for (int b0 = 0; b0 < c.batch; b0 += 32) {
+    const int len = c.batch <= 32 ? len32 : b0 + lane < c.batch ? c.lens[b0 + lane] : 0;
+    int64_t u = 0;
+    if (b0 + lane < c.batch) {
+      u = ka_seq(c, len).units;
+      u = (aligned ? (u + piece - 1) / piece : u) * c.heads;
+    }
+    int64_t incl = u;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t v = __shfl_up_sync(kKaFull, incl, d);
+      if (lane >= d) incl += v;
+    }
+    const uint32_t past = __ballot_sync(kKaFull, base + incl > begin);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      base += __shfl_sync(kKaFull, incl - u, at);
+      b = b0 + at;
+      len32 = len;
+      b32 = b0;
+      break;
+    }
+    base += __shfl_sync(kKaFull, incl, 31);
+  }
+  KaSeq s = {};
+  int h = 0;
+  int64_t own = 1;      // places of a pair of sequence b
+  int64_t skipped = 0;  // places of the first pair before this CTA's
+  int64_t seg = 0, u = 0, u_end = 0;  // in units: the pair's first, this CTA's next and last
+  if (b < c.batch) {
+    s = ka_seq(c, __shfl_sync(kKaFull, len32, b - b32));
+    own = aligned ? (s.units + piece - 1) / piece : s.units;
+    h = static_cast<int>((begin - base) / own);
+    skipped = begin - base - h * own;
+    seg = aligned ? 0 : begin - skipped;
+    u = aligned ? skipped * piece : begin;
+    u_end = min(u + piece, aligned ? static_cast<int64_t>(s.units) : total);
+  }
+  bool ok = true;
+  while (u < u_end && ok) {
+    const int l0 = static_cast<int>(u - seg);
+    const int n = static_cast<int>(min(u_end, seg + s.units) - u);
+    const int n_all = max(n, kKaGroups);  // every group takes part in every pair, with an empty unit if need be
+    const int cta0 = static_cast<int>(aligned ? blockIdx.x - skipped : seg / piece);
+    const int n_cta = static_cast<int>(aligned ? own : (seg + s.units - 1) / piece - cta0 + 1);
+    const uint32_t q_bytes = static_cast<uint32_t>(a.r) * kD * 2;
+    const uint16_t* q = a.q + b * a.q_seq + static_cast<int64_t>(h) * a.r * kD;
+    const int32_t* row = c.table + static_cast<int64_t>(b) * c.max_blocks;
+    const int n_pages = max(0, min(n, s.full - l0));
+    int32_t pg = 0, pg_next = lane < n_pages ? row[l0 + lane] : 0;
+#pragma unroll 1
+    for (int i = 0; i < n_all && ok; ++i) {
+      if ((i & 31) == 0) {
+        pg = pg_next;
+        pg_next = i + 32 + lane < n_pages ? row[l0 + i + 32 + lane] : 0;
+      }
+      const int32_t page = __shfl_sync(kKaFull, pg, i & 31);
+      const bool mine = kKaCopyWarps == 1 || ring.stage % kKaCopyWarps == copier;
+      if (mine) ok = ka_acquire(sm, ring, a.status);
+      if (mine && lane == 0 && ok) {
+        const bool first = i < kKaGroups;
+        const int st = ring.stage;
+        uint64_t* full = &sm.full[st];
+        int kind = kUnitNone, n_tok = kBlock;
+        if (i < n_pages) {
+          kind = page >= 0 && page < c.n_pages ? kUnitPage : kUnitNone;
+          if (kind == kUnitNone) report(a.status, GAAC_EFORMAT);
+        } else if (i < n && s.open) {
+          kind = kUnitOpen;
+          n_tok = min(kKaHalf, s.open - kKaHalf * (l0 + i - s.full));
+        }
+        sm.meta[st][0] = make_int4(kind, first, i >= n_all - kKaGroups, n_tok);
+        sm.meta[st][1] = make_int4(b, h, cta0, n_cta);
+        const int64_t tile = static_cast<int64_t>(page) * c.heads + h;
+        if (kind == kUnitPage) {
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(&sm.scale[st])),
+                       "l"(c.scales + 2 * tile) : "memory");
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(full)) : "memory");
+        } else {
+          ka_arrive(full);
+        }
+        mbar_arrive_expect_tx(full, (kind == kUnitNone ? 0 : kKv8Pair) + (first ? q_bytes : 0));
+        if (kind == kUnitPage) {
+          ka_tma(sm.stage[st], pages, 0, static_cast<int>(tile * 2 * kBlock), full);
+        } else if (kind == kUnitOpen) {  // K channels 0-63, 64-127, V the same
+          const int y = static_cast<int>((static_cast<int64_t>(b) * c.heads + h) * 2 * kBlock) + kKaHalf * (l0 + i - s.full);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ka_tma(sm.stage[st] + k * (kKv8Pair / 4), tail, (k & 1) * (kD / 2), y + (k >> 1) * kBlock, full);
+        }
+        if (first) bulk_g2s(sm.q[st], q, q_bytes, full);
+      }
+      ka_next(ring);
+    }
+    // ---- the next pair
+    seg += s.units;
+    u = seg;
+    if (++h == c.heads) {
+      h = 0;
+      if (++b >= c.batch) break;
+      if (b - b32 >= 32) {
+        b32 += 32;
+        len32 = b32 + lane < c.batch ? c.lens[b32 + lane] : 0;
+      }
+      s = ka_seq(c, __shfl_sync(kKaFull, len32, b - b32));
     }
   }
   // No copy may be in flight when the CTA ends, not even where a consumer's wait ran out: the last use of every stage
-  // is waited for (bounded).  The end unit has taken the stage of the oldest of them, which was consumed.
-  const int n = min(ring.issued, ok ? kKaStages - 1 : kKaStages);
-  for (int i = 0; i < n; ++i) {
+  // is waited for (bounded) before the end is passed on.
+  for (int i = 0; i < min(ring.issued, kKaStages); ++i) {
     const int j = ring.issued - 1 - i;
-    mbar_wait(&sm.full[j % kKaStages], (j / kKaStages) & 1, a.status);
+    if (kKaCopyWarps == 1 || j % kKaStages % kKaCopyWarps == copier) mbar_wait(&sm.full[j % kKaStages], (j / kKaStages) & 1, a.status);
+  }
+  for (int i = 0; i < kKaGroups && ok; ++i) {
+    const bool mine = kKaCopyWarps == 1 || ring.stage % kKaCopyWarps == copier;
+    if (mine) ok = ka_acquire(sm, ring, a.status);
+    if (mine && lane == 0 && ok) {
+      sm.meta[ring.stage][0] = make_int4(kUnitEnd, 0, 0, 0);
+      ka_arrive(&sm.full[ring.stage]);
+      ka_arrive(&sm.full[ring.stage]);
+    }
+    ka_next(ring);
   }
 }
 
@@ -359,11 +368,73 @@ __device__ __forceinline__ float4 ka_result(float4 o, float m, float l, float mv
   return make_float4(o.x * e / l * e, o.y * e / l * e, o.z * e / l * e, o.w * e / l * e);
 }
 
+// Folds a partial (m, l, mv, o) into the running one.
+__device__ __forceinline__ void ka_fold(float& m, float& l, float& mv, float4& o, float m1, float l1, float mv1, float4 o1) {
+  const float mn = fmaxf(m, m1), vn = fmaxf(mv, mv1), z = ka_finite(mn), zv = ka_finite(vn);
+  l = l * ka_exp2(m - z) + l1 * ka_exp2(m1 - z);
+  const float f0 = ka_exp2(mv - zv), f1 = ka_exp2(mv1 - zv);
+  o.x = o.x * f0 + o1.x * f1, o.y = o.y * f0 + o1.y * f1, o.z = o.z * f0 + o1.z * f1, o.w = o.w * f0 + o1.w * f1;
+  m = mn;
+  mv = vn;
+}
+
+// The last CTA of a pair joins the partials of the n CTAs that share it.  Thread (share, row, four channels) folds
+// partials share, share + shares, ... in order, twelve of them in flight; the shares (as many as the threads allow
+// for r rows) meet in shared memory.
+template <bool HALF>
+__device__ __forceinline__ bool ka_join(const KaArgs& a, KaSmem& sm, int b, int h, int cta0, int n, KaSync& meet) {
+  constexpr int kBatch = 12;
+  const int per = a.r * (kD / 4), shares = kKaCompute / per;
+  const int share = threadIdx.x / per, at = threadIdx.x % per, row = at / (kD / 4), ch = 4 * (at % (kD / 4));
+  float m = -INFINITY, l = 0.f, mv = -INFINITY;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (share < shares) {
+#pragma unroll 1
+    for (int i0 = share; i0 < n; i0 += kBatch * shares) {
+      float m1[kBatch], l1[kBatch], mv1[kBatch];
+      float4 o1[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * shares;
+        m1[k] = mv1[k] = -INFINITY;
+        l1[k] = 0.f;
+        o1[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n) {
+          const float* p = a.part + static_cast<int64_t>(2 * (cta0 + i) + (i == 0 ? 1 : 0)) * kKaPart + row;
+          m1[k] = __ldcg(p);
+          l1[k] = __ldcg(p + kKaRows);
+          mv1[k] = __ldcg(p + 2 * kKaRows);
+          o1[k] = __ldcg(reinterpret_cast<const float4*>(p + 3 * kKaRows + row * (kD - 1) + ch));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) ka_fold(m, l, mv, o, m1[k], l1[k], mv1[k], o1[k]);
+    }
+    if (share > 0) {
+      *reinterpret_cast<float4*>(&sm.state[share][row][ch]) = o;
+      if (ch == 0) {
+        sm.m[share][row] = m;
+        sm.l[share][row] = l;
+        sm.mv[share][row] = mv;
+      }
+    }
+  }
+  if (shares > 1 && !ka_meet(sm, meet, a.status)) return false;
+  if (share == 0) {
+#pragma unroll 1
+    for (int w = 1; w < shares; ++w)
+      ka_fold(m, l, mv, o, sm.m[w][row], sm.l[w][row], sm.mv[w][row], *reinterpret_cast<const float4*>(&sm.state[w][row][ch]));
+    ka_store<HALF>(a, b, h, row, ch, ka_result(o, m, l, mv));
+  }
+  return true;
+}
+
 template <bool HALF, int FMT>
 __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+  const int warp = tid >> 5, part = warp & 1;  // part: which half of a unit's tokens
   KaSync meet;
-  int stage = 0;
+  int stage = warp >> 1;
   uint32_t phase = 0;
   uint32_t qf[8][2];       // q^T operand: row g, channels 16 j + 4 tq .. + 3 of k-step j
   float qc[2];             // logit factor of rows 2 tq, 2 tq + 1 before sK: scale * log2(e) / (the row's power of two)
@@ -376,20 +447,17 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
   for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
   m[0] = m[1] = mv[0] = mv[1] = -INFINITY;
   l[0] = l[1] = 0.f;
-  // addresses of this lane's ldmatrix rows within a stage
-  const int i8 = lane >> 3, r8 = lane & 7;
-  const uint32_t k_row = static_cast<uint32_t>(16 * warp + 8 * (i8 & 1) + r8);   // K: matrices (tokens 0-7, 8-15) x (chunk, chunk + 1)
-  const uint32_t k_off = k_row * kD;
-  const uint32_t v_off = kKv8Tile + k_off;                                        // V: the same tokens, read transposed
-  const uint32_t half = static_cast<uint32_t>(i8 >> 1);
+  // This lane's ldmatrix row of the first 16 tokens (matrices: tokens 0-7, 8-15 of chunk 0, then of chunk 1), its
+  // 16-byte chunk swizzled by the row: chunk c of row t lies at c ^ (t & 7).
+  const uint32_t lm_row = static_cast<uint32_t>(32 * part + 8 * ((lane >> 3) & 1) + (lane & 7));
+  const uint32_t lm_off = lm_row * 128u + ((static_cast<uint32_t>(lane >> 4) ^ (lm_row & 7u)) << 4);
 
   while (true) {
     if (!ka_wait(&sm.full[stage], phase, a.status)) return;
-    const KaMeta& meta = sm.meta[stage];
-    const int kind = meta.kind;
+    const int4 meta = sm.meta[stage][0];
+    const int kind = meta.x, last = meta.z;
     if (kind == kUnitEnd) return;
-    const bool last = meta.last;
-    if (meta.first) {
+    if (meta.y) {
       // ---- the pair's queries
       const uint16_t* qs = sm.q[stage];
       uint32_t w[8][2];
@@ -399,7 +467,7 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
         uint2 x = make_uint2(0u, 0u);
         if (g < a.r) x = *reinterpret_cast<const uint2*>(qs + g * kD + 16 * j + 4 * tq);
         w[j][0] = x.x, w[j][1] = x.y;
-        *reinterpret_cast<uint2*>(sm.qraw[g] + 2 * (16 * j + 4 * tq)) = x;  // every warp writes the same
+        *reinterpret_cast<uint2*>(sm.qraw[g] + 2 * (16 * j + 4 * tq)) = x;  // every warp writes the same, and reads its own
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t mag = w[j][i] & 0x7FFF7FFFu;
@@ -409,13 +477,13 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
       big = max(big & 0xFFFFu, big >> 16);
       big = max(big, __shfl_xor_sync(kKaFull, big, 1));
       big = max(big, __shfl_xor_sync(kKaFull, big, 2));
-      // row's power of two: its largest magnitude to [2^14, 2^15); both factors of it are normal numbers
+      // The row's power of two takes its largest magnitude to [2^14, 2^15).  Its exponent is read after a scaling
+      // that makes any 16-bit number normal in fp32; it is applied in two halves, both normal.
       int e = 0;
       if (big != 0u) {
-        const float f = kv8_pair<HALF>(big).x * 0x1p100f;  // a 16-bit number below 2^28 keeps clear of overflow ...
-        const float f2 = kv8_pair<HALF>(big).x * 0x1p-100f;
-        e = isinf(f) ? static_cast<int>(__float_as_uint(f2) >> 23) - 127 + 100 : static_cast<int>(__float_as_uint(f) >> 23) - 127 - 100;
-        e = 14 - e;  // multiply by 2^e, in [-113, 147]
+        const float f = kv8_pair<HALF>(big).x;
+        const bool low = f < 0x1p-60f;
+        e = 14 - (static_cast<int>(__float_as_uint(low ? f * 0x1p80f : f) >> 23) - 127 - (low ? 80 : 0));
       }
       const float s1 = __uint_as_float(static_cast<uint32_t>(127 + e / 2) << 23);
       const float s2 = __uint_as_float(static_cast<uint32_t>(127 + e - e / 2) << 23);
@@ -439,60 +507,69 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
       l[0] = l[1] = 0.f;
     }
 
-    // ---- logits of this warp's 16 tokens: s[0], s[1] token g, rows 2tq, 2tq+1; s[2], s[3] token g + 8
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    float lv = 0.f;
-    const uint32_t base = smem_addr(sm.stage[stage]);
-    if (kind == kUnitPage) {
-      const float2 sc = sm.scale[stage];
-      float t[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        uint32_t r[4];
-        ka_ldmatrix(r, base + k_off + (((j + half) ^ (k_row & 7u)) << 4));
-        const uint32_t a0[4] = {fp8x2_to_f16x2<FMT>(r[0] & 0xFFFFu), fp8x2_to_f16x2<FMT>(r[1] & 0xFFFFu),
-                                fp8x2_to_f16x2<FMT>(r[0] >> 16), fp8x2_to_f16x2<FMT>(r[1] >> 16)};
-        const uint32_t a1[4] = {fp8x2_to_f16x2<FMT>(r[2] & 0xFFFFu), fp8x2_to_f16x2<FMT>(r[3] & 0xFFFFu),
-                                fp8x2_to_f16x2<FMT>(r[2] >> 16), fp8x2_to_f16x2<FMT>(r[3] >> 16)};
-        ka_mma_f16(s, a0, qf[j][0], qf[j][1]);
-        ka_mma_f16(t, a1, qf[j + 1][0], qf[j + 1][1]);
-      }
-      lv = log2f(sc.y);
-      const float c0 = qc[0] * sc.x, c1 = qc[1] * sc.x;
-      s[0] = (s[0] + t[0]) * c0, s[1] = (s[1] + t[1]) * c1, s[2] = (s[2] + t[2]) * c0, s[3] = (s[3] + t[3]) * c1;
-    } else if (kind == kUnitOpen) {
-      const int n_tok = meta.n_tok;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        // token g (and g + 8), channels 16 j + 4 tq .. + 3: eight bytes of one 16-byte chunk
-        const uint32_t chunk = static_cast<uint32_t>(2 * (j & 3) + (tq >> 1));
-        const uint32_t row = static_cast<uint32_t>(16 * warp + g);  // (row + 8) & 7 == row & 7
-        const uint32_t at = (j >> 2) * kKv8Tile + row * 128u + ((chunk ^ (row & 7u)) << 4) + 8u * (tq & 1);
-        const uint2 x0 = *reinterpret_cast<const uint2*>(sm.stage[stage] + at);
-        const uint2 x1 = *reinterpret_cast<const uint2*>(sm.stage[stage] + at + 8 * 128);
-        const uint2 qw = *reinterpret_cast<const uint2*>(sm.qraw[g] + 2 * (16 * j + 4 * tq));
-        const uint32_t aw[4] = {x0.x, x1.x, x0.y, x1.y};
-        if (HALF)
-          ka_mma_f16(s, aw, qw.x, qw.y);
-        else
-          mma_bf16(s, aw[0], aw[1], aw[2], aw[3], qw.x, qw.y);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = 16 * warp + g + 8 * (i >> 1) < n_tok ? s[i] * a.c_log2 : -INFINITY;
-    }
-
-    // ---- softmax state
-    uint32_t pb[4];  // P^T operand (tokens 0-7, 8-15): f16, or bf16 high parts and then low parts
     if (kind != kUnitNone) {
-      float x0 = fmaxf(s[0], s[2]), x1 = fmaxf(s[1], s[3]);
+      // ---- logits: s[t][0], s[t][1] token 16 t + g, rows 2tq, 2tq+1; s[t][2], s[t][3] token 16 t + g + 8
+      float s[2][4];
+      float lv = 0.f;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = kind == kUnitPage ? 0.f : -INFINITY;
+      const uint32_t base = smem_addr(sm.stage[stage]);
+      if (kind == kUnitPage) {
+        const float2 sc = sm.scale[stage];
+        float u[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            uint32_t r[4], a0[4], a1[4];
+            ka_ldmatrix(r, ((base + lm_off) ^ (j << 4)) + 16 * 128 * t);
+            ka_widen<FMT, false>(r[0], a0[0], a0[2]);
+            ka_widen<FMT, false>(r[1], a0[1], a0[3]);
+            ka_widen<FMT, false>(r[2], a1[0], a1[2]);
+            ka_widen<FMT, false>(r[3], a1[1], a1[3]);
+            ka_mma_f16(s[t], a0, qf[j][0], qf[j][1]);
+            ka_mma_f16(u[t], a1, qf[j + 1][0], qf[j + 1][1]);
+          }
+        lv = ka_log2(sc.y);
+        const float c0 = qc[0] * sc.x, c1 = qc[1] * sc.x;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          s[t][0] = (s[t][0] + u[t][0]) * c0, s[t][1] = (s[t][1] + u[t][1]) * c1;
+          s[t][2] = (s[t][2] + u[t][2]) * c0, s[t][3] = (s[t][3] + u[t][3]) * c1;
+        }
+      } else {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          // token g (and g + 8), channels 16 j + 4 tq .. + 3: eight bytes of one 16-byte chunk
+          const uint32_t chunk = static_cast<uint32_t>(2 * (j & 3) + (tq >> 1));
+          const uint32_t row = static_cast<uint32_t>(16 * part + g);  // (row + 8) & 7 == row & 7
+          const uint32_t at = (j >> 2) * (kKv8Pair / 4) + row * 128u + ((chunk ^ (row & 7u)) << 4) + 8u * (tq & 1);
+          const uint2 x0 = *reinterpret_cast<const uint2*>(sm.stage[stage] + at);
+          const uint2 x1 = *reinterpret_cast<const uint2*>(sm.stage[stage] + at + 8 * 128);
+          const uint2 qw = *reinterpret_cast<const uint2*>(sm.qraw[g] + 2 * (16 * j + 4 * tq));
+          const uint32_t aw[4] = {x0.x, x1.x, x0.y, x1.y};
+          if (HALF)
+            ka_mma_f16(d, aw, qw.x, qw.y);
+          else
+            mma_bf16(d, aw[0], aw[1], aw[2], aw[3], qw.x, qw.y);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (16 * part + g + 8 * (i >> 1) < meta.w) s[0][i] = d[i] * a.c_log2;
+      }
+
+      // ---- softmax state
+      float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
+      float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) {
         x0 = fmaxf(x0, __shfl_xor_sync(kKaFull, x0, d));
         x1 = fmaxf(x1, __shfl_xor_sync(kKaFull, x1, d));
       }
-      const float n0 = fmaxf(m[0], x0), n1 = fmaxf(m[1], x1);
-      const float w0 = fmaxf(mv[0], x0 + lv - 15.f), w1 = fmaxf(mv[1], x1 + lv - 15.f);
-      if (__any_sync(kKaFull, n0 > m[0] || n1 > m[1] || w0 > mv[0] || w1 > mv[1])) {
+      const float y0 = x0 + (lv - 15.f), y1 = x1 + (lv - 15.f);
+      if (__any_sync(kKaFull, x0 > m[0] || x1 > m[1] || y0 > mv[0] || y1 > mv[1])) {
+        const float n0 = fmaxf(m[0], x0), n1 = fmaxf(m[1], x1), w0 = fmaxf(mv[0], y0), w1 = fmaxf(mv[1], y1);
         l[0] *= ka_exp2(m[0] - ka_finite(n0));
         l[1] *= ka_exp2(m[1] - ka_finite(n1));
         const float f0 = ka_exp2(mv[0] - ka_finite(w0)), f1 = ka_exp2(mv[1] - ka_finite(w1));
@@ -506,77 +583,80 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
         m[0] = n0, m[1] = n1, mv[0] = w0, mv[1] = w1;
       }
       const float m0 = ka_finite(m[0]), m1 = ka_finite(m[1]), v0 = ka_finite(mv[0]) - lv, v1 = ka_finite(mv[1]) - lv;
-      l[0] += ka_exp2(s[0] - m0) + ka_exp2(s[2] - m0);
-      l[1] += ka_exp2(s[1] - m1) + ka_exp2(s[3] - m1);
-      const float p[4] = {ka_exp2(s[0] - v0), ka_exp2(s[1] - v1), ka_exp2(s[2] - v0), ka_exp2(s[3] - v1)};
-      if (HALF || kind == kUnitPage) {
-        pb[0] = ka_transpose(ka_pack_f16(p[0], p[1]));
-        pb[1] = ka_transpose(ka_pack_f16(p[2], p[3]));
-      } else {
-        const uint32_t h0 = ka_pack_bf16(p[0], p[1]), h1 = ka_pack_bf16(p[2], p[3]);
-        const float2 b0 = kv8_pair<false>(h0), b1 = kv8_pair<false>(h1);
-        pb[0] = ka_transpose(h0);
-        pb[1] = ka_transpose(h1);
-        pb[2] = ka_transpose(ka_pack_bf16(p[0] - b0.x, p[1] - b0.y));
-        pb[3] = ka_transpose(ka_pack_bf16(p[2] - b1.x, p[3] - b1.y));
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        l[0] += ka_exp2(s[t][0] - m0) + ka_exp2(s[t][2] - m0);
+        l[1] += ka_exp2(s[t][1] - m1) + ka_exp2(s[t][3] - m1);
+        s[t][0] = ka_exp2(s[t][0] - v0), s[t][1] = ka_exp2(s[t][1] - v1);
+        s[t][2] = ka_exp2(s[t][2] - v0), s[t][3] = ka_exp2(s[t][3] - v1);
       }
-    }
 
-    // ---- O^T += V^T P^T
-    if (kind == kUnitPage) {
+      // ---- O^T += V^T P^T
+      if (kind == kUnitPage) {
+        uint32_t pb[2][2];
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        // matrices (tokens 0-7, 8-15) of channels 16 i .. and of 16 (i + 1) ..; a lane gets channels 2g, 2g+1 of
-        // tokens 2tq (low half) and 2tq+1
-        uint32_t r[4];
-        ka_ldmatrix_t(r, base + v_off + (((i + half) ^ (k_row & 7u)) << 4));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) r[k] = __byte_perm(r[k], 0u, 0x3120);
-        const uint32_t a0[4] = {fp8x2_to_f16x2<FMT>(r[0] & 0xFFFFu), fp8x2_to_f16x2<FMT>(r[0] >> 16),
-                                fp8x2_to_f16x2<FMT>(r[1] & 0xFFFFu), fp8x2_to_f16x2<FMT>(r[1] >> 16)};
-        const uint32_t a1[4] = {fp8x2_to_f16x2<FMT>(r[2] & 0xFFFFu), fp8x2_to_f16x2<FMT>(r[2] >> 16),
-                                fp8x2_to_f16x2<FMT>(r[3] & 0xFFFFu), fp8x2_to_f16x2<FMT>(r[3] >> 16)};
-        ka_mma_f16(acc[i], a0, pb[0], pb[1]);
-        ka_mma_f16(acc[i + 1], a1, pb[0], pb[1]);
-      }
-    } else if (kind == kUnitOpen) {
-      // the next stage holds V
-      const int n_tok = meta.n_tok;
-      __syncwarp();
-      if (lane == 0) ka_arrive(&sm.empty[stage]);
-      if (++stage == kKaStages) {
-        stage = 0;
-        phase ^= 1u;
-      }
-      if (!ka_wait(&sm.full[stage], phase, a.status)) return;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t aw[4];
-#pragma unroll
-        for (int t8 = 0; t8 < 2; ++t8) {
-          uint32_t x[2];
-#pragma unroll
-          for (int o = 0; o < 2; ++o) {  // token 2tq + o (+ 8): channels 16 i + 2g, + 1
-            const uint32_t row = static_cast<uint32_t>(16 * warp + 8 * t8 + 2 * tq + o);
-            const uint32_t chunk = static_cast<uint32_t>(2 * (i & 3) + (g >> 2));
-            const uint32_t at = (i >> 2) * kKv8Tile + row * 128u + ((chunk ^ (row & 7u)) << 4) + 4u * (g & 3);
-            x[o] = static_cast<int>(row) < n_tok ? *reinterpret_cast<const uint32_t*>(sm.stage[stage] + at) : 0u;
-          }
-          aw[2 * t8] = __byte_perm(x[0], x[1], 0x5410);
-          aw[2 * t8 + 1] = __byte_perm(x[0], x[1], 0x7632);
+        for (int t = 0; t < 2; ++t) {
+          pb[t][0] = ka_transpose(ka_pack_f16(s[t][0], s[t][1]));
+          pb[t][1] = ka_transpose(ka_pack_f16(s[t][2], s[t][3]));
         }
+#pragma unroll
+        for (int i = 0; i < 8; i += 2)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            // matrices (tokens 0-7, 8-15) of channels 16 i .. and of 16 (i + 1) ..; a lane gets channels 2g, 2g+1 of
+            // token 2tq (low half of the word) and of 2tq+1
+            uint32_t r[4], a0[4], a1[4];
+            ka_ldmatrix_t(r, ((base + lm_off) ^ (i << 4)) + kKv8Tile + 16 * 128 * t);
+            ka_widen<FMT, true>(r[0], a0[0], a0[1]);
+            ka_widen<FMT, true>(r[1], a0[2], a0[3]);
+            ka_widen<FMT, true>(r[2], a1[0], a1[1]);
+            ka_widen<FMT, true>(r[3], a1[2], a1[3]);
+            ka_mma_f16(acc[i], a0, pb[t][0], pb[t][1]);
+            ka_mma_f16(acc[i + 1], a1, pb[t][0], pb[t][1]);
+          }
+      } else {
+        uint32_t pb[4];  // f16, or bf16 high parts and then what they leave
         if (HALF) {
-          ka_mma_f16(acc[i], aw, pb[0], pb[1]);
+          pb[0] = ka_transpose(ka_pack_f16(s[0][0], s[0][1]));
+          pb[1] = ka_transpose(ka_pack_f16(s[0][2], s[0][3]));
         } else {
-          mma_bf16(acc[i], aw[0], aw[1], aw[2], aw[3], pb[0], pb[1]);
-          mma_bf16(acc[i], aw[0], aw[1], aw[2], aw[3], pb[2], pb[3]);
+          const uint32_t h0 = ka_pack_bf16(s[0][0], s[0][1]), h1 = ka_pack_bf16(s[0][2], s[0][3]);
+          const float2 b0 = kv8_pair<false>(h0), b1 = kv8_pair<false>(h1);
+          pb[0] = ka_transpose(h0);
+          pb[1] = ka_transpose(h1);
+          pb[2] = ka_transpose(ka_pack_bf16(s[0][0] - b0.x, s[0][1] - b0.y));
+          pb[3] = ka_transpose(ka_pack_bf16(s[0][2] - b1.x, s[0][3] - b1.y));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t aw[4];
+#pragma unroll
+          for (int t8 = 0; t8 < 2; ++t8) {
+            uint32_t x[2];
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {  // token 2tq + o (+ 8): channels 16 i + 2g, + 1; rows behind the tokens are 0
+              const uint32_t row = static_cast<uint32_t>(16 * part + 8 * t8 + 2 * tq + o);
+              const uint32_t chunk = static_cast<uint32_t>(2 * (i & 3) + (g >> 2));
+              const uint32_t at = kKv8Tile + (i >> 2) * (kKv8Pair / 4) + row * 128u + ((chunk ^ (row & 7u)) << 4) + 4u * (g & 3);
+              x[o] = static_cast<int>(row) < meta.w ? *reinterpret_cast<const uint32_t*>(sm.stage[stage] + at) : 0u;
+            }
+            aw[2 * t8] = __byte_perm(x[0], x[1], 0x5410);
+            aw[2 * t8 + 1] = __byte_perm(x[0], x[1], 0x7632);
+          }
+          if (HALF) {
+            ka_mma_f16(acc[i], aw, pb[0], pb[1]);
+          } else {
+            mma_bf16(acc[i], aw[0], aw[1], aw[2], aw[3], pb[0], pb[1]);
+            mma_bf16(acc[i], aw[0], aw[1], aw[2], aw[3], pb[2], pb[3]);
+          }
         }
       }
     }
 
     // ---- the end of the pair in this CTA
     if (last) {
-      const int b = sm.meta[stage].b, h = sm.meta[stage].h, cta0 = sm.meta[stage].cta0, n_cta = sm.meta[stage].n_cta;
+      const int4 pair = sm.meta[stage][1];
+      const int b = pair.x, h = pair.y, cta0 = pair.z, n_cta = pair.w;
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) {
         l[0] += __shfl_xor_sync(kKaFull, l[0], d);
@@ -597,64 +677,45 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
       }
       if (!ka_meet(sm, meet, a.status)) return;
       const bool whole = n_cta == 1;
-      float* part = a.part + static_cast<int64_t>(2 * blockIdx.x + (static_cast<int>(blockIdx.x) == cta0 ? 1 : 0)) * kKaPart;
+      float* mine = a.part + static_cast<int64_t>(2 * blockIdx.x + (static_cast<int>(blockIdx.x) == cta0 ? 1 : 0)) * kKaPart;
+      {
+        static_assert(kKaRows * kD / 4 <= kKaCompute, "at most one float4 of the result for each thread");
+        const int row = tid / (kD / 4), ch = 4 * (tid % (kD / 4));
+        if (row < a.r) {
+          float mx = -INFINITY, vx = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < kKaRows * kD / 4 / (32 * kKaWarps); ++k) {
-        const int at = tid + 32 * kKaWarps * k, row = at / (kD / 4), ch = 4 * (at % (kD / 4));
-        float mx = -INFINITY, vx = -INFINITY;
+          for (int w = 0; w < kKaWarps; ++w) {
+            mx = fmaxf(mx, sm.m[w][row]);
+            vx = fmaxf(vx, sm.mv[w][row]);
+          }
+          float den = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kKaWarps; ++w) {
-          mx = fmaxf(mx, sm.m[w][row]);
-          vx = fmaxf(vx, sm.mv[w][row]);
-        }
-        float den = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kKaWarps; ++w) {
-          den += ka_exp2(sm.m[w][row] - ka_finite(mx)) * sm.l[w][row];
-          const float f = ka_exp2(sm.mv[w][row] - ka_finite(vx));
-          const float4 x = *reinterpret_cast<const float4*>(&sm.state[w][row][ch]);
-          o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
-        }
-        if (whole) {
-          if (row < a.r) ka_store<HALF>(a, b, h, row, ch, ka_result(o, mx, den, vx));
-        } else {
-          *reinterpret_cast<float4*>(part + 3 * kKaRows + row * kD + ch) = o;
-          if (ch == 0) {
-            part[row] = mx;
-            part[kKaRows + row] = den;
-            part[2 * kKaRows + row] = vx;
+          for (int w = 0; w < kKaWarps; ++w) {
+            den += ka_exp2(sm.m[w][row] - ka_finite(mx)) * sm.l[w][row];
+            const float f = ka_exp2(sm.mv[w][row] - ka_finite(vx));
+            const float4 x = *reinterpret_cast<const float4*>(&sm.state[w][row][ch]);
+            o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+          }
+          if (whole) {
+            ka_store<HALF>(a, b, h, row, ch, ka_result(o, mx, den, vx));
+          } else {
+            *reinterpret_cast<float4*>(mine + 3 * kKaRows + row * kD + ch) = o;
+            if (ch == 0) {
+              mine[row] = mx;
+              mine[kKaRows + row] = den;
+              mine[2 * kKaRows + row] = vx;
+            }
           }
         }
       }
       if (!whole) {
-        __threadfence();
+        // the barrier orders everybody's stores before thread 0's release, which passes them on
         if (!ka_meet(sm, meet, a.status)) return;
         if (tid == 0) sm.last = kv8_atomic_add_acq_rel(a.counters + cta0, 1u) == static_cast<unsigned int>(n_cta - 1);
         if (!ka_meet(sm, meet, a.status)) return;
         if (sm.last) {
-          // ---- the last CTA of the pair joins the partials, in order
-          auto slot = [&](int i) { return a.part + static_cast<int64_t>(2 * (cta0 + i) + (i == 0 ? 1 : 0)) * kKaPart; };
-#pragma unroll 1
-          for (int k = 0; k < kKaRows * kD / 4 / (32 * kKaWarps); ++k) {
-            const int at = tid + 32 * kKaWarps * k, row = at / (kD / 4), ch = 4 * (at % (kD / 4));
-            float mx = -INFINITY, vx = -INFINITY, den = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int i = 0; i < n_cta; ++i) {
-              mx = fmaxf(mx, __ldcg(slot(i) + row));
-              vx = fmaxf(vx, __ldcg(slot(i) + 2 * kKaRows + row));
-            }
-#pragma unroll 8
-            for (int i = 0; i < n_cta; ++i) {
-              const float* p = slot(i);
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(p + 3 * kKaRows + row * kD + ch));
-              den += ka_exp2(__ldcg(p + row) - ka_finite(mx)) * __ldcg(p + kKaRows + row);
-              const float f = ka_exp2(__ldcg(p + 2 * kKaRows + row) - ka_finite(vx));
-              o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
-            }
-            if (row < a.r) ka_store<HALF>(a, b, h, row, ch, ka_result(o, mx, den, vx));
-          }
+          if (!ka_join<HALF>(a, sm, b, h, cta0, n_cta, meet)) return;
           if (tid == 0) a.counters[cta0] = 0;
         }
       }
@@ -663,22 +724,23 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
     }
     __syncwarp();
     if (lane == 0) ka_arrive(&sm.empty[stage]);
-    if (++stage == kKaStages) {
-      stage = 0;
+    stage += kKaGroups;
+    if (stage >= kKaStages) {
+      stage -= kKaStages;
       phase ^= 1u;
     }
   }
 }
 
 template <bool HALF, int FMT>
-__global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm)
+__global__ void __launch_bounds__(kKaThreads, 1)
     kv8_attention_kernel(const KaArgs a, const __grid_constant__ CUtensorMap pages, const __grid_constant__ CUtensorMap tail) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   KaSmem& sm = *reinterpret_cast<KaSmem*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKaStages; ++i) {
       mbar_init(&sm.full[i], 2);
-      mbar_init(&sm.empty[i], kKaWarps);
+      mbar_init(&sm.empty[i], 2);
     }
     mbar_init(&sm.sync, kKaWarps);
     fence_mbar_init();
@@ -689,7 +751,7 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm)
   dependent_wait();
   dependent_launch();
   if (threadIdx.x >= 32 * kKaWarps)
-    ka_copy_warp(a, sm, &pages, &tail);
+    ka_copy_warp(a, sm, &pages, &tail, threadIdx.x / 32 - kKaWarps);
   else
     ka_compute<HALF, FMT>(a, sm);
 }
@@ -755,7 +817,7 @@ static int ka_launch(const KaArgs& a, const CUtensorMap& pages, const CUtensorMa
 using namespace gaac;
 
 extern "C" size_t gaac_kv8_attention_workspace(void) {
-  const int grid = kKaCtasPerSm * ka_sms();
+  const int grid = ka_sms();
   return ka_counter_bytes(grid) + static_cast<size_t>(2 * grid) * kKaPart * sizeof(float);
 }
 
@@ -773,7 +835,7 @@ extern "C" int gaac_kv8_decode_attention(const gaac_kv8* cache, const void* q, i
   const int sms = ka_sms();
   if (sms <= 0 || ka_encode() == nullptr) return GAAC_ECUDA;
   if (workspace_bytes < gaac_kv8_attention_workspace()) return GAAC_EINVAL;
-  const int grid = kKaCtasPerSm * sms;
+  const int grid = sms;
   KaArgs a;
   a.c = kv8_dev(cache);
   a.q = static_cast<const uint16_t*>(q);
@@ -788,7 +850,7 @@ extern "C" int gaac_kv8_decode_attention(const gaac_kv8* cache, const void* q, i
   CUtensorMap pages, tail;
   const int64_t rows = int64_t{2} * kBlock * cache->n_kv_heads;
   if (!ka_map(&pages, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, cache->pages, cache->n_pages * rows, kD, 2 * kBlock) ||
-      !ka_map(&tail, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, cache->tail, cache->batch * rows, kD / 2, kBlock))
+      !ka_map(&tail, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, cache->tail, cache->batch * rows, kD / 2, kKaHalf))
     return GAAC_ECUDA;
   if (cache->dtype == GAAC_BF16)
     return cache->fmt == GAAC_FP8_E4M3 ? ka_launch<false, GAAC_FP8_E4M3>(a, pages, tail, grid, stream)
