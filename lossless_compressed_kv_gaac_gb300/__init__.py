@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 
 import torch
@@ -457,6 +458,10 @@ class gaac_rope_tensor(ctypes.Structure):
                 ("out_seq", ctypes.c_int64), ("out_tok", ctypes.c_int64), ("out_head", ctypes.c_int64)]
 
 
+_ROPE_TENSOR = struct.Struct("@PPi6q")  # gaac_rope_tensor packed in one go
+assert _ROPE_TENSOR.size == ctypes.sizeof(gaac_rope_tensor)
+
+
 def rope_frequencies(rot_dim: int, theta: float = 1e4, scaling: str | None = None, factor: float = 1.0,
                      original_len: int | None = None, fast: float = 32.0, slow: float = 1.0):
     """(w, mscale): the angular frequencies w_j = theta^(-2j/rot_dim) as a float64 tensor [rot_dim/2], scaled for
@@ -507,23 +512,27 @@ def rope_turns(w: torch.Tensor, device=None) -> torch.Tensor:
                         device=w.device if device is None else device)
 
 
-def _same_device(first, *tensors):
-    """The CUDA device that all of them are on."""
-    if not first.is_cuda:
-        raise ValueError("tensors must be on a CUDA device")
+def _gpu(*tensors) -> int:
+    """The index of the CUDA device that all of them are on."""
+    index = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != first.device:
-            raise ValueError("tensors must be on one device")
-    return first.device
+        if t.get_device() != index or index < 0:
+            raise ValueError("tensors must be on one CUDA device")
+    return index
 
 
-def _call(fn: str, device, stream, *args):
-    """Calls the library with `device` current and the stream (default: the device's current one) last."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _call(fn, device, stream, *args)
+# The current stream's handle, without the stream object that torch.cuda.current_stream() makes (2 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(fn: str, index: int, stream, *args):
+    """Calls the library with device `index` current and the stream (default: the device's current one) last."""
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _call(fn, index, stream, *args)
     if stream is None:
-        s = torch.cuda.current_stream(device).cuda_stream
+        s = _raw_stream(index)
     else:
         s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     status = getattr(_lib or lib(), fn)(*args, s)
@@ -531,18 +540,12 @@ def _call(fn: str, device, stream, *args):
         raise GaacError(fn, status)
 
 
-def _rope_view(t, name):
-    """(n_seq, n_tok, heads, dim, seq, tok and head strides) of [tokens, heads, dim] or [batch, tokens, heads, dim]."""
-    if t.dim() == 3:
-        n_seq, seq = 1, 0
-    elif t.dim() == 4:
-        n_seq, seq = t.shape[0], t.stride(0)
-    else:
-        raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
-    n_tok, heads, dim = t.shape[-3:]
-    if dim > 1 and t.stride(-1) != 1:
+def _rope_strides(t, name):
+    """Batch (0 without one), token and head strides of [tokens, heads, dim] or [batch, tokens, heads, dim]."""
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: channels must be contiguous")
-    return n_seq, n_tok, heads, dim, seq, t.stride(-3), t.stride(-2)
+    return st[:3] if len(st) == 4 else (0, st[0], st[1])
 
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, turns: torch.Tensor, q_out=None, k_out=None,
@@ -552,43 +555,49 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, turns
     [batch, tokens]; turns: rope_turns(...), one for each pair of the rotated channels (the first
     2 * turns.numel() of a head; the others are copied).  Pairs are (j, j + half) or, interleaved, (2j, 2j + 1).
     q_out, k_out: default in place.  inverse turns the other way: the gradient of the call without it."""
-    qo = q if q_out is None else q_out
-    pairs = [(q, qo)]
+    dtype, shape = q.dtype, q.shape
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError("q must be BF16, FP16 or FP32")
+    if len(shape) == 3:
+        n_seq, (n_tok, heads, dim) = 1, shape
+    elif len(shape) == 4:
+        n_seq, n_tok, heads, dim = shape
+    else:
+        raise ValueError("q must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
+    index = _gpu(q, positions, turns)
+    if q_out is None:
+        q_out = q
+    elif q_out.dtype != dtype or q_out.shape != shape or q_out.get_device() != index:
+        raise ValueError("q_out must have q's type, shape and device")
+    desc = _ROPE_TENSOR.pack(q.data_ptr(), q_out.data_ptr(), heads, *_rope_strides(q, "q"), *_rope_strides(q_out, "q_out"))
+    count = 1
     if k is not None:
-        pairs.append((k, k if k_out is None else k_out))
+        k_shape = k.shape
+        if k.dtype != dtype or len(k_shape) != len(shape) or k_shape[:-2] != shape[:-2] or k_shape[-1] != dim or \
+                k.get_device() != index:
+            raise ValueError("k must have q's type, tokens, width and device")
+        if k_out is None:
+            k_out = k
+        elif k_out.dtype != dtype or k_out.shape != k_shape or k_out.get_device() != index:
+            raise ValueError("k_out must have k's type, shape and device")
+        desc += _ROPE_TENSOR.pack(k.data_ptr(), k_out.data_ptr(), k_shape[-2], *_rope_strides(k, "k"),
+                                  *_rope_strides(k_out, "k_out"))
+        count = 2
     elif k_out is not None:
         raise ValueError("k_out without k")
-    device = _same_device(q, qo, *pairs[-1], positions, turns)
-    if q.dtype not in _DTYPES or any(t.dtype != q.dtype for p in pairs for t in p):
-        raise ValueError("q, k and the outputs must be of one type: BF16, FP16 or FP32")
     if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
         raise ValueError("turns must be a contiguous int64 tensor [pairs]")
-    if positions.dtype not in (torch.int32, torch.int64):
+    bits = 32 if positions.dtype == torch.int32 else 64
+    if bits == 64 and positions.dtype != torch.int64:
         raise ValueError("positions must be int32 or int64")
-    desc = (gaac_rope_tensor * len(pairs))()
-    shape = None
-    for d, (x, out) in zip(desc, pairs):
-        n_seq, n_tok, heads, dim, *xs = _rope_view(x, "input")
-        o_seq, o_tok, o_heads, o_dim, *outs = _rope_view(out, "output")
-        if out.shape != x.shape:
-            raise ValueError("an output must have its input's shape")
-        if shape is None:
-            shape, n_dim = (n_seq, n_tok, dim), x.dim()
-        elif (n_seq, n_tok, dim) != shape or x.dim() != n_dim:
-            raise ValueError("q and k must have the same tokens and width")
-        d.x, d.out, d.n_heads = x.data_ptr(), out.data_ptr(), heads
-        d.x_seq, d.x_tok, d.x_head = xs
-        d.out_seq, d.out_tok, d.out_head = outs
-    n_seq, n_tok, dim = shape
-    if positions.dim() == 1 and positions.shape[0] == n_tok:
-        ps, pt = 0, positions.stride(0)
-    elif positions.dim() == 2 and n_dim == 4 and tuple(positions.shape) == (n_seq, n_tok):
-        ps, pt = positions.stride()
-    else:
+    pos_shape, ps = positions.shape, positions.stride()
+    if len(pos_shape) == 1 and pos_shape[0] == n_tok:
+        ps = (0, ps[0])
+    elif len(pos_shape) != 2 or len(shape) != 4 or pos_shape[0] != n_seq or pos_shape[1] != n_tok:
         raise ValueError("positions must be [tokens] or [batch, tokens]")
-    _call("gaac_rope", device, stream, desc, len(pairs), _DTYPES[q.dtype], n_seq, n_tok, dim, 2 * turns.shape[0],
-          positions.data_ptr(), 8 * positions.element_size(), ps, pt, turns.data_ptr(), float(mscale),
-          (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0))
+    _call("gaac_rope", index, stream, desc, count, code, n_seq, n_tok, dim, 2 * turns.shape[0], positions.data_ptr(), bits,
+          *ps, turns.data_ptr(), mscale, (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0))
 
 
 # ---------------------------------------------------------------- 8-bit paged cache
@@ -608,7 +617,8 @@ class Kv8:
     [batch].  fmt: FP8_E4M3 or FP8_E5M2."""
 
     def __init__(self, pages, scales, tail, table, refs, seq_lens, fmt: int):
-        self.device = _same_device(pages, scales, tail, table, refs, seq_lens)
+        self._index = _gpu(pages, scales, tail, table, refs, seq_lens)
+        self.device = pages.device
         if pages.dim() != 5 or tuple(pages.shape[2:]) != (2, BLOCK, HEAD_DIM) or pages.dtype != torch.uint8:
             raise ValueError(f"pages must be uint8 [n_pages, kv_heads, 2, {BLOCK}, {HEAD_DIM}]")
         n_pages, heads = pages.shape[:2]
@@ -645,8 +655,8 @@ class Kv8:
     seq_lens = property(lambda s: s._tensors[5])
 
 
-def _index_list(t, name, device):
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.device != device:
+def _index_list(t, name, cache):
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.get_device() != cache._index:
         raise ValueError(f"{name} must be a contiguous int32 tensor on the cache's device")
     return t.shape[0]
 
@@ -654,9 +664,19 @@ def _index_list(t, name, device):
 def _kv8_cu(cache: Kv8, cu_tokens):
     if cu_tokens is None:
         return 0
-    if _index_list(cu_tokens, "cu_tokens", cache.device) != cache.batch + 1:
+    if _index_list(cu_tokens, "cu_tokens", cache) != cache.batch + 1:
         raise ValueError("cu_tokens must hold batch + 1 offsets")
     return cu_tokens.data_ptr()
+
+
+def _kv8_rows(cache: Kv8, t, heads, name):
+    """Row stride of t [n, heads (any if None), 128] of the cache's type, heads and channels contiguous; n."""
+    shape, st = t.shape, t.stride()
+    if t.dtype != cache.dtype or t.get_device() != cache._index or len(shape) != 3 or shape[2] != HEAD_DIM or \
+            (heads is not None and shape[1] != heads) or st[2] != 1 or (st[1] != HEAD_DIM and shape[1] > 1):
+        raise ValueError(f"{name} must be [n, heads, {HEAD_DIM}] of the cache's type and device, heads and channels "
+                         "contiguous")
+    return shape[0], (st[0] if shape[0] > 1 else shape[1] * HEAD_DIM)
 
 
 def kv8_append(cache: Kv8, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor | None = None, status=None,
@@ -665,17 +685,11 @@ def kv8_append(cache: Kv8, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Te
     channels contiguous) to sequence b; without cu_tokens (int32 [batch + 1]) one row for each sequence.  The pages
     of blocks that fill must have been reserved."""
     cu = _kv8_cu(cache, cu_tokens)
-    for t in (k, v):
-        if (t.dtype != cache.dtype or t.device != cache.device or t.dim() != 3 or t.shape[1] != cache.n_kv_heads or
-                t.shape[2] != HEAD_DIM or t.stride(2) != 1 or (t.stride(1) != HEAD_DIM and t.shape[1] > 1)):
-            raise ValueError("k and v must be [n, kv_heads, 128] of the cache's type and device, heads and channels "
-                             "contiguous")
-    n = k.shape[0]
-    if v.shape[0] != n or (cu == 0 and n != cache.batch):
+    n, k_row = _kv8_rows(cache, k, cache.n_kv_heads, "k")
+    n_v, v_row = _kv8_rows(cache, v, cache.n_kv_heads, "v")
+    if n_v != n or (cu == 0 and n != cache.batch):
         raise ValueError("k and v must hold the same rows: one for each sequence without cu_tokens")
-    width = cache.n_kv_heads * HEAD_DIM
-    _call("gaac_kv8_append", cache.device, stream, cache._ref, k.data_ptr(), v.data_ptr(), n,
-          k.stride(0) if n > 1 else width, v.stride(0) if n > 1 else width, cu, _ptr(status))
+    _call("gaac_kv8_append", cache._index, stream, cache._ref, k.data_ptr(), v.data_ptr(), n, k_row, v_row, cu, _ptr(status))
 
 
 def kv8_attention_workspace() -> int:
@@ -687,42 +701,40 @@ def kv8_decode_attention(cache: Kv8, q: torch.Tensor, scale: float, out: torch.T
                          status=None, stream=None) -> None:
     """q: [batch, q_heads, 128] of the cache's type (rows may be strided); out: the same shape, contiguous, of the
     cache's type or fp32; workspace: kv8_attention_workspace() bytes, zero before the first call."""
-    if (q.dtype != cache.dtype or q.device != cache.device or q.dim() != 3 or q.shape[0] != cache.batch or
-            q.shape[2] != HEAD_DIM or q.stride(2) != 1 or (q.stride(1) != HEAD_DIM and q.shape[1] > 1)):
-        raise ValueError("q must be [batch, q_heads, 128] of the cache's type and device, heads and channels contiguous")
-    if out.shape != q.shape or out.dtype not in (cache.dtype, torch.float32) or out.device != cache.device or \
-            not out.is_contiguous():
-        raise ValueError("out must be contiguous, of q's shape and device, in the cache's type or fp32")
-    if workspace.device != cache.device or not workspace.is_contiguous():
+    n, row = _kv8_rows(cache, q, None, "q")
+    code = _DTYPES.get(out.dtype)
+    if n != cache.batch or out.shape != q.shape or (out.dtype != cache.dtype and code != 2) or \
+            out.get_device() != cache._index or not out.is_contiguous():
+        raise ValueError("q must have a row for each sequence, and out must be contiguous, of q's shape and device, in "
+                         "the cache's type or fp32")
+    if workspace.get_device() != cache._index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous on the cache's device")
-    hq = q.shape[1]
-    _call("gaac_kv8_decode_attention", cache.device, stream, cache._ref, q.data_ptr(), hq,
-          q.stride(0) if cache.batch > 1 else hq * HEAD_DIM, scale, out.data_ptr(), _DTYPES[out.dtype],
-          workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(status))
+    _call("gaac_kv8_decode_attention", cache._index, stream, cache._ref, q.data_ptr(), q.shape[1], row, scale,
+          out.data_ptr(), code, workspace.data_ptr(), workspace.nbytes, _ptr(status))
 
 
 def kv8_reserve(cache: Kv8, cu_tokens: torch.Tensor | None = None, status=None, stream=None) -> None:
     """Pages for the blocks that appending these tokens fills: the lowest free ones, in order of sequence and block."""
-    _call("gaac_kv8_reserve", cache.device, stream, cache._ref, _kv8_cu(cache, cu_tokens), _ptr(status))
+    _call("gaac_kv8_reserve", cache._index, stream, cache._ref, _kv8_cu(cache, cu_tokens), _ptr(status))
 
 
 def kv8_release(cache: Kv8, seqs: torch.Tensor, status=None, stream=None) -> None:
     """Empties the listed sequences (int32); pages that no other sequence holds become free."""
-    n = _index_list(seqs, "seqs", cache.device)
-    _call("gaac_kv8_release", cache.device, stream, cache._ref, seqs.data_ptr(), n, _ptr(status))
+    n = _index_list(seqs, "seqs", cache)
+    _call("gaac_kv8_release", cache._index, stream, cache._ref, seqs.data_ptr(), n, _ptr(status))
 
 
 def kv8_fork(cache: Kv8, src: torch.Tensor, dst: torch.Tensor, status=None, stream=None) -> None:
     """Empty sequences dst (int32) become copies of src, sharing their full blocks."""
-    n = _index_list(src, "src", cache.device)
-    if _index_list(dst, "dst", cache.device) != n:
+    n = _index_list(src, "src", cache)
+    if _index_list(dst, "dst", cache) != n:
         raise ValueError("src and dst must have the same length")
-    _call("gaac_kv8_fork", cache.device, stream, cache._ref, src.data_ptr(), dst.data_ptr(), n, _ptr(status))
+    _call("gaac_kv8_fork", cache._index, stream, cache._ref, src.data_ptr(), dst.data_ptr(), n, _ptr(status))
 
 
 def kv8_compact(cache: Kv8, moved_to: torch.Tensor, stream=None) -> None:
     """Moves the held pages to the front of the pool; moved_to (int32 [n_pages]) gets each page's new place, -1 for
     free ones."""
-    if _index_list(moved_to, "moved_to", cache.device) != cache.n_pages:
+    if _index_list(moved_to, "moved_to", cache) != cache.n_pages:
         raise ValueError("moved_to must hold n_pages values")
-    _call("gaac_kv8_compact", cache.device, stream, cache._ref, moved_to.data_ptr())
+    _call("gaac_kv8_compact", cache._index, stream, cache._ref, moved_to.data_ptr())

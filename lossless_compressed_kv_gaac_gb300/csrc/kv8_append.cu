@@ -9,9 +9,13 @@
 // the numbers themselves, however its tokens arrive.  NaN stays NaN; an infinity stays one in E5M2 and becomes
 // NaN in E4M3, which has none.
 //
-// One CTA for each (block touched, kv-head), K and V together: 256 threads hold the block's 32 KB in registers
-// (eight 16-byte loads in flight each), so every number is read once and written once.  The first block's CTA
-// also writes the new open block's rows, after it has read the old ones from the same tail.
+// Memory bound: 2 bytes read and 1 written per number.  A CTA takes a run of consecutive blocks of one kv-head, K and
+// V together: 512 threads hold a block's 32 KB in registers and have the next block's loads in flight while they
+// quantise it, so the reads never pause and what the run's sequence and pages are is looked up once.  Runs are one
+// block long where there are few (latency), longer where every SM has several.  The first block's CTA also
+// writes the new open block's rows, after it has read the old ones from the same tail.
+#include <algorithm>
+
 #include "kv8.cuh"
 
 namespace gaac {
@@ -23,10 +27,13 @@ struct Kv8AppendArgs {
   int64_t k_tok, v_tok;  // elements between tokens
   const int32_t* cu;     // first token of each sequence, batch + 1; nullptr: one token each
   int64_t total;
+  int run;               // blocks of a CTA
   int32_t* status;
 };
 
-constexpr int kApThreads = 256;
+constexpr int kApThreads = 512;
+constexpr int kApRows = kBlock * 16 / kApThreads;  // 16-byte vectors of a thread in each of K and V
+constexpr int kApCtasPerSm = 2;
 
 template <int FMT>
 __device__ __forceinline__ uint32_t to_fp8x2(float lo, float hi) {
@@ -59,148 +66,211 @@ __device__ __forceinline__ int scale_exponent(uint32_t bits) {
   return max(e - top + ((f & 0x7FFFFFu) > 0x600000u ? 1 : 0), -126);
 }
 
+// A thread's part of a block that fills: channels c8 .. c8 + 7 of kApRows rows, and the block's page.
+struct ApBlock {
+  uint4 w[2][kApRows];
+  int32_t page;
+};
+
+// A block of new tokens only: k, v at this thread's first row of it.
+__device__ __forceinline__ void ap_load(ApBlock& x, const uint16_t* k, const uint16_t* v, int64_t k_tok, int64_t v_tok) {
+#pragma unroll
+  for (int i = 0; i < kApRows; ++i) {
+    x.w[0][i] = *reinterpret_cast<const uint4*>(k + kApThreads / 16 * i * k_tok);
+    x.w[1][i] = *reinterpret_cast<const uint4*>(v + kApThreads / 16 * i * v_tok);
+  }
+}
+
+// A block that opened before this call: its first `old` tokens are in the tail.
+__device__ __forceinline__ void ap_load_open(ApBlock& x, const uint16_t* tail, int old, const uint16_t* k, const uint16_t* v,
+                                             int64_t k_tok, int64_t v_tok, int t0) {
+#pragma unroll
+  for (int i = 0; i < kApRows; ++i) {
+    const int t = t0 + kApThreads / 16 * i;
+    const bool in_tail = t < old;
+    x.w[0][i] = *reinterpret_cast<const uint4*>(in_tail ? tail + t * kD : k + (t - t0) * k_tok);
+    x.w[1][i] = *reinterpret_cast<const uint4*>(in_tail ? tail + kKv8Tile + t * kD : v + (t - t0) * v_tok);
+  }
+}
+
+// The block's largest magnitudes as 16-bit patterns, whose order is the numbers': K's in the low half of the result,
+// V's in the high one.  FINITE leaves out infinities and NaN, which are otherwise the largest.  One barrier.
+template <bool HALF, bool FINITE>
+__device__ __forceinline__ uint32_t ap_largest(const ApBlock& x, uint32_t* sh) {
+  const int tid = threadIdx.x;
+  uint32_t mx = 0;
+#pragma unroll
+  for (int kind = 0; kind < 2; ++kind) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kApRows; ++i) {
+      const uint32_t w[4] = {x.w[kind][i].x, x.w[kind][i].y, x.w[kind][i].z, x.w[kind][i].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t mag = w[q] & 0x7FFF7FFFu;
+        m = __vmaxu2(m, FINITE ? mag & ~__vcmpgeu2(mag, HALF ? 0x7C007C00u : 0x7F807F80u) : mag);
+      }
+    }
+    m = max(m & 0xFFFFu, m >> 16);
+    mx |= m << (16 * kind);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+  if ((tid & 31) == 0) sh[tid >> 5] = mx;
+  __syncthreads();
+  mx = sh[tid & (kApThreads / 32 - 1)];
+#pragma unroll
+  for (int d = kApThreads / 64; d > 0; d >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+  return mx;
+}
+
+// Four numbers of the model's type times `inv`, as FP8.
 template <bool HALF, int FMT>
-__global__ void __launch_bounds__(kApThreads) kv8_append_kernel(Kv8AppendArgs a) {
-  __shared__ uint32_t sh_max[kApThreads / 32];
+__device__ __forceinline__ uint32_t ap_four(uint32_t w0, uint32_t w1, float inv) {
+  const float2 a = kv8_pair<HALF>(w0), b = kv8_pair<HALF>(w1);
+  float r[4];
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(r[0]), "=f"(r[1]) : "f"(a.x), "f"(a.y), "f"(inv));
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(r[2]), "=f"(r[3]) : "f"(b.x), "f"(b.y), "f"(inv));
+  return to_fp8x2<FMT>(r[0], r[1]) | to_fp8x2<FMT>(r[2], r[3]) << 16;
+}
+
+// Quantises the block into its page.  sh: two sets of the warps' maxima; a barrier at least, behind which the old
+// rows of the tail have been read.
+template <bool HALF, int FMT>
+__device__ __forceinline__ void ap_seal(const ApBlock& x, const Kv8Dev& c, int h, int t0, int c8, uint32_t (*sh)[kApThreads / 32]) {
+  constexpr uint32_t kInf = HALF ? 0x7C00u : 0x7F80u;
+  const int tid = threadIdx.x;
+  uint32_t mx = ap_largest<HALF, false>(x, sh[0]);
+  const bool odd = (mx & 0xFFFFu) >= kInf || (mx >> 16) >= kInf;  // the same for the whole CTA
+  if (odd) mx = ap_largest<HALF, true>(x, sh[1]);
+  const int64_t tile = static_cast<int64_t>(x.page) * c.heads + h;
+  uint8_t* dst = c.pages + tile * kKv8Pair + t0 * kD + c8;
+#pragma unroll
+  for (int kind = 0; kind < 2; ++kind) {
+    const int e = scale_exponent<HALF, FMT>((mx >> (16 * kind)) & 0xFFFFu);
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < kApRows; ++i) {
+      const uint4 w = x.w[kind][i];
+      uint2 o;
+      if (!odd) {
+        o = make_uint2(ap_four<HALF, FMT>(w.x, w.y, inv), ap_four<HALF, FMT>(w.z, w.w, inv));
+      } else {
+        o = make_uint2(0u, 0u);
+#pragma unroll 1
+        for (int q = 0; q < 8; ++q) {
+          const float2 f = kv8_pair<HALF>(q < 2 ? w.x : q < 4 ? w.y : q < 6 ? w.z : w.w);
+          const uint32_t y = to_fp8_any<FMT>((q & 1 ? f.y : f.x) * inv) << (8 * (q & 3));
+          if (q < 4) o.x |= y; else o.y |= y;
+        }
+      }
+      *reinterpret_cast<uint2*>(dst + kind * kKv8Tile + kApThreads / 16 * i * kD) = o;
+    }
+    if (tid == 0) c.scales[tile * 2 + kind] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  }
+}
+
+template <bool HALF, int FMT>
+__global__ void __launch_bounds__(kApThreads, kApCtasPerSm) kv8_append_kernel(const Kv8AppendArgs a) {
+  __shared__ uint32_t sh_max[2][2][kApThreads / 32];  // of a block and the next
   dependent_wait();
   dependent_launch();
   const Kv8Dev& c = a.c;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int h = static_cast<int>(blockIdx.x % c.heads);
-  const int64_t tile = blockIdx.x / c.heads;
-  // ---- the sequence and the block of this CTA
-  // Sequence b owns tiles [cu[b]/64 + 2b, cu[b+1]/64 + 2b + 2): at least as many as its tokens can touch, wherever
-  // its open block ends.
-  int b, j, n, span;
-  int64_t first;
+  const int64_t place = blockIdx.x / c.heads;
+  // ---- the sequence and the run of this CTA
+  // With R blocks in a run, sequence b owns places [cu[b]/64R + 2b, cu[b+1]/64R + 2b + 2): at least as many as its
+  // tokens can touch, wherever its open block ends.  Every warp looks it up for itself.
+  int b, j, span;
+  int64_t n, first;  // new tokens, and the row of the first
   if (a.cu == nullptr) {
-    b = static_cast<int>(tile);
+    b = static_cast<int>(place);
     j = 0;
     n = 1;
     span = 1;
     first = b;
   } else {
+    const int64_t per = static_cast<int64_t>(kBlock) * a.run;
     int count = 0, bad = 0;
-    for (int i0 = 0; i0 < c.batch; i0 += kApThreads) {
-      const int i = i0 + tid;
-      int below = 0;
+#pragma unroll 4
+    for (int i0 = 0; i0 < c.batch; i0 += 32) {
+      const int i = i0 + lane;
+      bool below = false;
       if (i < c.batch) {
         const int64_t lo = a.cu[i], hi = a.cu[i + 1];
         if (lo < 0 || hi < lo || hi > a.total) bad = 1;
-        below = hi / kBlock + 2 * (static_cast<int64_t>(i) + 1) <= tile;
+        below = hi / per + 2 * (static_cast<int64_t>(i) + 1) <= place;
       }
-      count += __syncthreads_count(below);
+      count += __popc(__ballot_sync(0xFFFFFFFFu, below));
     }
-    if (__syncthreads_or(bad)) {
+    if (__any_sync(0xFFFFFFFFu, bad)) {
       if (blockIdx.x == 0 && tid == 0) report(a.status, GAAC_EINVAL);
       return;
     }
     b = count;
     if (b >= c.batch) return;
     first = a.cu[b];
-    const int64_t t0 = first / kBlock + 2 * static_cast<int64_t>(b), t1 = a.cu[b + 1] / kBlock + 2 * (static_cast<int64_t>(b) + 1);
-    if (tile < t0) return;
-    j = static_cast<int>(tile - t0);
-    span = static_cast<int>(t1 - t0);
-    n = static_cast<int>(a.cu[b + 1] - first);
+    const int64_t end = a.cu[b + 1];
+    const int64_t p0 = first / per + 2 * static_cast<int64_t>(b), p1 = end / per + 2 * (static_cast<int64_t>(b) + 1);
+    if (place < p0) return;
+    j = static_cast<int>(place - p0) * a.run;
+    span = static_cast<int>(p1 - p0);
+    n = end - first;
   }
   const int len = c.lens[b];
-  const int64_t now = static_cast<int64_t>(len) + n;
-  const int blk0 = len / kBlock, blk1 = static_cast<int>(now / kBlock);
+  const int64_t now = len + n;
+  const bool fits = len >= 0 && now <= static_cast<int64_t>(c.max_blocks) * kBlock;
+  const int blk0 = fits ? len / kBlock : 0, blk1 = fits ? static_cast<int>(now / kBlock) : 0;  // blocks [blk0, blk1) fill
   const int32_t* row = c.table + static_cast<int64_t>(b) * c.max_blocks;
-  int fault = 0;
-  if (len < 0 || now > static_cast<int64_t>(c.max_blocks) * kBlock) {
-    fault = GAAC_EINVAL;
-  } else {
-    int missing = 0;
-    for (int i = blk0 + tid; i < blk1; i += kApThreads) {
-      const int32_t p = row[i];
-      if (p < 0 || p >= c.n_pages) missing = 1;
-    }
-    if (__syncthreads_or(missing)) fault = GAAC_EPOOL;
+  const int t0 = tid >> 4, c8 = 8 * (tid & 15);
+  uint16_t* tail = c.tail + (static_cast<int64_t>(b) * c.heads + h) * kKv8Pair + c8;
+  const uint16_t* src[2] = {a.k + h * kD + c8, a.v + h * kD + c8};
+  const int64_t step[2] = {a.k_tok, a.v_tok};
+  const int blk_begin = blk0 + j, blk_end = min(blk_begin + a.run, blk1);
+  // this thread's first row of the run's next block that is loaded
+  const int64_t at0 = first + static_cast<int64_t>(blk_begin) * kBlock + t0 - len;
+  const uint16_t* k = src[0] + at0 * step[0];
+  const uint16_t* v = src[1] + at0 * step[1];
+  auto load = [&](ApBlock& x, int blk) {
+    if (blk * kBlock < len)
+      ap_load_open(x, tail, len - blk * kBlock, k, v, a.k_tok, a.v_tok, t0);
+    else
+      ap_load(x, k, v, a.k_tok, a.v_tok);
+    x.page = row[blk];
+    k += kBlock * a.k_tok;
+    v += kBlock * a.v_tok;
+  };
+  ApBlock x, y;
+  if (blk_begin < blk_end) load(x, blk_begin);  // under way while the pages are checked
+  int missing = 0;
+  for (int i = blk0 + tid; i < blk1; i += kApThreads) {
+    const int32_t p = row[i];
+    if (p < 0 || p >= c.n_pages) missing = 1;
   }
-  if (fault && tid == 0) report(a.status, fault);
-  const int touched = n == 0 || fault ? 0 : static_cast<int>((now + kBlock - 1) / kBlock) - blk0;
-  if (j < touched) {
-    const int blk = blk0 + j;
-    const bool seal = blk < blk1;
-    uint16_t* tail = c.tail + (static_cast<int64_t>(b) * c.heads + h) * 2 * kKv8Tile;
-    const int t0 = tid >> 4, c8 = 8 * (tid & 15);
-    const uint16_t* src[2] = {a.k + h * kD + c8, a.v + h * kD + c8};
-    const int64_t step[2] = {a.k_tok, a.v_tok};
-    if (seal) {
-      uint4 w[2][4];
-#pragma unroll
-      for (int kind = 0; kind < 2; ++kind)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = t0 + 16 * i;
-          const int64_t at = static_cast<int64_t>(blk) * kBlock + t - len;  // among the new tokens
-          w[kind][i] = *reinterpret_cast<const uint4*>(at < 0 ? tail + kind * kKv8Tile + t * kD + c8
-                                                              : src[kind] + (first + at) * step[kind]);
-        }
-      // largest finite magnitudes as 16-bit patterns (their order is the numbers'): K in the low half, V in the high
-      uint32_t mx = 0, odd = 0;
-#pragma unroll
-      for (int kind = 0; kind < 2; ++kind) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t* x = reinterpret_cast<const uint32_t*>(&w[kind][i]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t mag = x[q] & 0x7FFF7FFFu;
-            const uint32_t inf = __vcmpgeu2(mag, HALF ? 0x7C007C00u : 0x7F807F80u);
-            odd |= inf;
-            m = __vmaxu2(m, mag & ~inf);
-          }
-        }
-        m = max(m & 0xFFFFu, m >> 16);
-        mx |= m << (16 * kind);
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-      if ((tid & 31) == 0) sh_max[tid >> 5] = mx;
-      const bool any_odd = __syncthreads_or(odd != 0u);  // also: the old rows of the tail have been read
-#pragma unroll
-      for (int i = 0; i < kApThreads / 32; ++i) mx = __vmaxu2(mx, sh_max[i]);
-      const int64_t page = row[blk];
-      uint8_t* dst = c.pages + (page * c.heads + h) * kKv8Pair + t0 * kD + c8;
-#pragma unroll
-      for (int kind = 0; kind < 2; ++kind) {
-        const int e = scale_exponent<HALF, FMT>((mx >> (16 * kind)) & 0xFFFFu);
-        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t* x = reinterpret_cast<const uint32_t*>(&w[kind][i]);
-          uint32_t o[2] = {0u, 0u};
-          if (!any_odd) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float2 f = kv8_pair<HALF>(x[q]);
-              o[q >> 1] |= to_fp8x2<FMT>(f.x * inv, f.y * inv) << (16 * (q & 1));
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float2 f = kv8_pair<HALF>(x[q]);
-              o[q >> 1] |= (to_fp8_any<FMT>(f.x * inv) | to_fp8_any<FMT>(f.y * inv) << 8) << (16 * (q & 1));
-            }
-          }
-          *reinterpret_cast<uint2*>(dst + kind * kKv8Tile + 16 * i * kD) = make_uint2(o[0], o[1]);
-        }
-        if (tid == 0) c.scales[(page * c.heads + h) * 2 + kind] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  const int fault = !fits ? GAAC_EINVAL : __syncthreads_or(missing) ? GAAC_EPOOL : 0;
+  if (fault) {
+    if (tid == 0) report(a.status, fault);
+  } else if (n > 0) {
+    for (int blk = blk_begin; blk < blk_end; blk += 2) {
+      if (blk + 1 < blk_end) load(y, blk + 1);
+      ap_seal<HALF, FMT>(x, c, h, t0, c8, sh_max[0]);
+      if (blk + 1 < blk_end) {
+        if (blk + 2 < blk_end) load(x, blk + 2);
+        ap_seal<HALF, FMT>(y, c, h, t0, c8, sh_max[1]);
       }
     }
     // the rows of the new open block
-    if (j == 0 && blk1 < blk0 + touched) {
+    if (j == 0) {
       const int64_t open = static_cast<int64_t>(blk1) * kBlock;
 #pragma unroll
       for (int kind = 0; kind < 2; ++kind)
-        for (int t = t0; t < now - open; t += 16) {
+        for (int t = t0; t < now - open; t += kApThreads / 16) {
           const int64_t at = open + t - len;
           if (at >= 0)
-            *reinterpret_cast<uint4*>(tail + kind * kKv8Tile + t * kD + c8) =
+            *reinterpret_cast<uint4*>(tail + kind * kKv8Tile + t * kD) =
                 *reinterpret_cast<const uint4*>(src[kind] + (first + at) * step[kind]);
         }
     }
@@ -235,11 +305,14 @@ extern "C" int gaac_kv8_append(const gaac_kv8* cache, const void* k, const void*
       (reinterpret_cast<uintptr_t>(cu_tokens) & 3u) || k_tok_stride < width || v_tok_stride < width ||
       (k_tok_stride & 7) || (v_tok_stride & 7) || k_tok_stride > (int64_t{1} << 40) || v_tok_stride > (int64_t{1} << 40))
     return GAAC_EINVAL;
-  const int64_t tiles = cu_tokens == nullptr ? cache->batch : n_tokens / kBlock + 2 * static_cast<int64_t>(cache->batch);
-  if (tiles * cache->n_kv_heads > 0x7FFFFFFF) return GAAC_EINVAL;
+  // Blocks of a run: one while the blocks leave an SM with fewer than eight, at most sixteen.
+  const int64_t blocks = n_tokens / kBlock * cache->n_kv_heads;
+  const int run = cu_tokens == nullptr ? 1 : static_cast<int>(std::min<int64_t>(16, std::max<int64_t>(1, blocks / (152 * 8))));
+  const int64_t places = cu_tokens == nullptr ? cache->batch : n_tokens / (kBlock * run) + 2 * static_cast<int64_t>(cache->batch);
+  if (places * cache->n_kv_heads > 0x7FFFFFFF) return GAAC_EINVAL;
   const Kv8AppendArgs a{kv8_dev(cache), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_tok_stride,
-                        v_tok_stride, cu_tokens, n_tokens, d_status};
-  const dim3 grid(static_cast<unsigned>(tiles * cache->n_kv_heads));
+                        v_tok_stride, cu_tokens, n_tokens, run, d_status};
+  const dim3 grid(static_cast<unsigned>(places * cache->n_kv_heads));
   if (cache->dtype == GAAC_BF16)
     return cache->fmt == GAAC_FP8_E4M3 ? kv8_launch(kv8_append_kernel<false, GAAC_FP8_E4M3>, grid, kApThreads, 0, stream, a)
                                        : kv8_launch(kv8_append_kernel<false, GAAC_FP8_E5M2>, grid, kApThreads, 0, stream, a);

@@ -51,7 +51,7 @@ struct KaSmem {
   alignas(128) uint16_t q[kKaStages][kKaRows * kD];
   alignas(16) float state[kKaWarps][kKaRows][kKaStride];
   alignas(16) uint8_t qraw[kKaRows][kKaQStride];
-  alignas(16) int4 meta[kKaStages][2];  // {kind, first of the pair in its group, last, tokens}, {b, h, first CTA, CTAs}
+  alignas(16) int4 meta[kKaStages][2];  // {kind, first of the pair in its group (2: with queries), last, tokens}, {b, h, first CTA, CTAs}
   alignas(16) float2 scale[kKaStages];
   float m[kKaWarps][kKaRows], l[kKaWarps][kKaRows], mv[kKaWarps][kKaRows];
   uint64_t full[kKaStages], empty[kKaStages], sync;
@@ -247,6 +247,8 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
     u = aligned ? skipped * piece : begin;
     u_end = min(u + piece, aligned ? static_cast<int64_t>(s.units) : total);
   }
+  int32_t row32 = 0;  // entries 0-31 of the table row of sequence row_of
+  int row_of = -1;
   bool ok = true;
   while (u < u_end && ok) {
     const int l0 = static_cast<int>(u - seg);
@@ -258,7 +260,17 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
     const uint16_t* q = a.q + b * a.q_seq + static_cast<int64_t>(h) * a.r * kD;
     const int32_t* row = c.table + static_cast<int64_t>(b) * c.max_blocks;
     const int n_pages = max(0, min(n, s.full - l0));
-    int32_t pg = 0, pg_next = lane < n_pages ? row[l0 + lane] : 0;
+    // The row's first entries serve every head of the sequence, and those of the next sequence are fetched early.
+    const bool ahead = l0 == 0 && row_of == b;
+    int32_t pg = 0, pg_next = ahead ? row32 : lane < n_pages ? row[l0 + lane] : 0;
+    if (l0 == 0) {
+      row32 = pg_next;
+      row_of = b;
+    }
+    if (h == c.heads - 1 && b + 1 < c.batch && u_end > seg + s.units) {
+      row32 = lane < c.max_blocks ? row[c.max_blocks + lane] : 0;
+      row_of = b + 1;
+    }
 #pragma unroll 1
     for (int i = 0; i < n_all && ok; ++i) {
       if ((i & 31) == 0) {
@@ -269,7 +281,7 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
       const bool mine = kKaCopyWarps == 1 || ring.stage % kKaCopyWarps == copier;
       if (mine) ok = ka_acquire(sm, ring, a.status);
       if (mine && lane == 0 && ok) {
-        const bool first = i < kKaGroups;
+        const bool first = i < kKaGroups, with_q = i < min(n, kKaGroups);
         const int st = ring.stage;
         uint64_t* full = &sm.full[st];
         int kind = kUnitNone, n_tok = kBlock;
@@ -280,7 +292,7 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
           kind = kUnitOpen;
           n_tok = min(kKaHalf, s.open - kKaHalf * (l0 + i - s.full));
         }
-        sm.meta[st][0] = make_int4(kind, first, i >= n_all - kKaGroups, n_tok);
+        sm.meta[st][0] = make_int4(kind, first ? 1 + with_q : 0, i >= n_all - kKaGroups, n_tok);
         sm.meta[st][1] = make_int4(b, h, cta0, n_cta);
         const int64_t tile = static_cast<int64_t>(page) * c.heads + h;
         if (kind == kUnitPage) {
@@ -290,7 +302,7 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
         } else {
           ka_arrive(full);
         }
-        mbar_arrive_expect_tx(full, (kind == kUnitNone ? 0 : kKv8Pair) + (first ? q_bytes : 0));
+        mbar_arrive_expect_tx(full, (kind == kUnitNone ? 0 : kKv8Pair) + (with_q ? q_bytes : 0));
         if (kind == kUnitPage) {
           ka_tma(sm.stage[st], pages, 0, static_cast<int>(tile * 2 * kBlock), full);
         } else if (kind == kUnitOpen) {  // K channels 0-63, 64-127, V the same
@@ -298,7 +310,7 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
 #pragma unroll
           for (int k = 0; k < 4; ++k) ka_tma(sm.stage[st] + k * (kKv8Pair / 4), tail, (k & 1) * (kD / 2), y + (k >> 1) * kBlock, full);
         }
-        if (first) bulk_g2s(sm.q[st], q, q_bytes, full);
+        if (with_q) bulk_g2s(sm.q[st], q, q_bytes, full);
       }
       ka_next(ring);
     }
@@ -458,6 +470,12 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
     const int kind = meta.x, last = meta.z;
     if (kind == kUnitEnd) return;
     if (meta.y) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+      m[0] = m[1] = mv[0] = mv[1] = -INFINITY;
+      l[0] = l[1] = 0.f;
+    }
+    if (meta.y == 2) {
       // ---- the pair's queries
       const uint16_t* qs = sm.q[stage];
       uint32_t w[8][2];
@@ -501,10 +519,6 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
         qc[i] = a.c_log2 * __uint_as_float(static_cast<uint32_t>(127 + er / 2) << 23) *
                 __uint_as_float(static_cast<uint32_t>(127 + er - er / 2) << 23);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-      m[0] = m[1] = mv[0] = mv[1] = -INFINITY;
-      l[0] = l[1] = 0.f;
     }
 
     if (kind != kUnitNone) {

@@ -16,6 +16,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -32,34 +33,18 @@ struct RopeTensor {
 struct RopeArgs {
   RopeTensor t[2];
   int heads0, heads;  // heads of the first tensor; of both
-  int n_tok, rot, dim;
+  unsigned n_seq, n_tok;
+  int rot, dim;
   const void* pos;
   int pos64;
   int64_t pos_seq, pos_tok;
   const uint64_t* turns;
   float mscale;
   int inverse;
-  int units, rot_units;  // V-pair units of a head's rotated part; all units, the copied rest included
-  int walkers;           // threads that share the heads of a row
-  int64_t n;             // rows * walkers * units
-};
-
-template <typename T>
-struct RopeNum;
-template <>
-struct RopeNum<float> {
-  static __device__ __forceinline__ float get(float v) { return v; }
-  static __device__ __forceinline__ float put(float v) { return v; }
-};
-template <>
-struct RopeNum<__nv_bfloat16> {
-  static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
-  static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
-};
-template <>
-struct RopeNum<__half> {
-  static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
-  static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
+  unsigned units, rot_units;          // of a head: all units, the copied rest included; the rotated ones
+  int walkers;                        // threads that share the heads of a row
+  unsigned row_walkers;               // rows * walkers
+  unsigned unit_threads, per_block;   // threads for the units of a (row, walker); those of a block
 };
 
 template <typename T, int V>
@@ -67,78 +52,154 @@ struct alignas(sizeof(T) * V) RopeVec {
   T v[V];
 };
 
-constexpr int kRopeThreads = 256;
+__device__ __forceinline__ float2 rope_pair(__nv_bfloat162 w) { return __bfloat1622float2(w); }
+__device__ __forceinline__ float2 rope_pair(__half2 w) { return __half22float2(w); }
+template <typename T>
+struct RopePair;
+template <>
+struct RopePair<__nv_bfloat16> {
+  using type = __nv_bfloat162;
+  static __device__ __forceinline__ type pack(float a, float b) { return __floats2bfloat162_rn(a, b); }
+  static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct RopePair<__half> {
+  using type = __half2;
+  static __device__ __forceinline__ type pack(float a, float b) { return __floats2half2_rn(a, b); }
+  static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
+  static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
+};
 
+template <typename T, int V>
+__device__ __forceinline__ void rope_unpack(const RopeVec<T, V>& x, float* f) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = x.v[i];
+  } else if constexpr (V == 1) {
+    f[0] = RopePair<T>::get(x.v[0]);
+  } else {
+    const auto* w = reinterpret_cast<const typename RopePair<T>::type*>(x.v);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 p = rope_pair(w[i]);
+      f[2 * i] = p.x;
+      f[2 * i + 1] = p.y;
+    }
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void rope_pack(RopeVec<T, V>& x, const float* f) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x.v[i] = f[i];
+  } else if constexpr (V == 1) {
+    x.v[0] = RopePair<T>::put(f[0]);
+  } else {
+    auto* w = reinterpret_cast<typename RopePair<T>::type*>(x.v);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) w[i] = RopePair<T>::pack(f[2 * i], f[2 * i + 1]);
+  }
+}
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeBatch = 2;  // heads whose loads a thread has in flight
+constexpr int kRopeMost = 8;   // most heads of a thread
+
+// Thread (row, walker, unit): heads walker, walker + walkers, ... of one row, V pairs of each.
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x;
-  if (id >= a.n) return;
-  const int u = static_cast<int>(id % a.units);
-  const int64_t rw = id / a.units;
-  const int walker = static_cast<int>(rw % a.walkers);
-  const int64_t row = rw / a.walkers;
-  const int64_t seq = row / a.n_tok, tok = row % a.n_tok;
   using Vec = RopeVec<T, V>;
-  if (u >= a.rot_units) {  // channels behind the rotated part
-    const int64_t off = (a.rot + static_cast<int64_t>(u - a.rot_units) * V) * static_cast<int64_t>(sizeof(T));
-    for (int h = walker; h < a.heads; h += a.walkers) {
-      const RopeTensor& t = a.t[h >= a.heads0];
-      if (!t.copy) continue;
-      const int hh = h >= a.heads0 ? h - a.heads0 : h;
-      *reinterpret_cast<Vec*>(t.out + seq * t.out_seq + tok * t.out_tok + hh * t.out_head + off) =
-          *reinterpret_cast<const Vec*>(t.x + seq * t.x_seq + tok * t.x_tok + hh * t.x_head + off);
-    }
-    return;
+  const unsigned local = threadIdx.x / a.unit_threads;
+  const unsigned rw = blockIdx.x * a.per_block + local;
+  if (local >= a.per_block || rw >= a.row_walkers) return;
+  const unsigned row = rw / a.walkers;
+  const int walker = static_cast<int>(rw - row * a.walkers);
+  unsigned seq = 0, tok = row;
+  if (a.n_seq > 1) {
+    seq = row / a.n_tok;
+    tok = row - seq * a.n_tok;
   }
   const int64_t pi = seq * a.pos_seq + tok * a.pos_tok;
   uint64_t p = a.pos64 ? static_cast<uint64_t>(static_cast<const int64_t*>(a.pos)[pi])
                        : static_cast<uint64_t>(static_cast<int64_t>(static_cast<const int32_t*>(a.pos)[pi]));
   if (a.inverse) p = 0 - p;
-  float c[V], s[V];
+  const char* const xq = a.t[0].x + seq * a.t[0].x_seq + tok * a.t[0].x_tok;
+  const char* const xk = a.t[1].x + seq * a.t[1].x_seq + tok * a.t[1].x_tok;
+  char* const outq = a.t[0].out + seq * a.t[0].out_seq + tok * a.t[0].out_tok;
+  char* const outk = a.t[1].out + seq * a.t[1].out_seq + tok * a.t[1].out_tok;
+  for (unsigned u = threadIdx.x - local * a.unit_threads; u < a.units; u += a.unit_threads) {
+    // a unit is two vectors: of the rotated part, or of the channels behind it (the last may be one)
+    const bool turned = u < a.rot_units;
+    const int e0 = turned ? (INTER ? 2 * u * V : u * V) : a.rot + 2 * (u - a.rot_units) * V;
+    const int e1 = turned && !INTER ? e0 + a.rot / 2 : e0 + V;
+    const bool two = e1 < a.dim;
+    const int64_t o0 = e0 * static_cast<int64_t>(sizeof(T)), o1 = e1 * static_cast<int64_t>(sizeof(T));
+    float c[V], s[V];
+    if (turned) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const uint64_t turn = p * a.turns[u * V + i] + (1ull << 31);
-    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s[i], &c[i]);
-    s[i] *= a.mscale;
-    c[i] *= a.mscale;
-  }
-  const int64_t o0 = static_cast<int64_t>(INTER ? 2 * u * V : u * V) * sizeof(T);
-  const int64_t o1 = INTER ? o0 + static_cast<int64_t>(V * sizeof(T)) : o0 + static_cast<int64_t>(a.rot / 2) * sizeof(T);
-  for (int h = walker; h < a.heads; h += a.walkers) {
-    const RopeTensor& t = a.t[h >= a.heads0];
-    const int hh = h >= a.heads0 ? h - a.heads0 : h;
-    const char* x = t.x + seq * t.x_seq + tok * t.x_tok + hh * t.x_head;
-    char* out = t.out + seq * t.out_seq + tok * t.out_tok + hh * t.out_head;
-    Vec v0 = *reinterpret_cast<const Vec*>(x + o0), v1 = *reinterpret_cast<const Vec*>(x + o1);
-    T e[2 * V], r[2 * V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      e[i] = v0.v[i];
-      e[V + i] = v1.v[i];
+      for (int i = 0; i < V; ++i) {
+        const uint64_t turn = p * a.turns[u * V + i] + (1ull << 31);
+        const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
+        // A 16-bit result is rounded at 2^-12 or coarser, so the hardware's sine and cosine (2^-21.2 off at most in
+        // [-pi, pi]) serve it; they take a tenth of the instructions, which bound the kernel otherwise.
+        if constexpr (sizeof(T) == 2)
+          __sincosf(half_turns * 3.14159265358979f, &s[i], &c[i]);
+        else
+          sincospif(half_turns, &s[i], &c[i]);
+        s[i] *= a.mscale;
+        c[i] *= a.mscale;
+      }
     }
+    // the loads of kRopeBatch heads come before the first store
+    for (int h0 = walker; h0 < a.heads; h0 += kRopeBatch * a.walkers) {
+      Vec v[kRopeBatch][2];
+      char* out[kRopeBatch];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : V + i;
-      const float x0 = RopeNum<T>::get(e[ia]), x1 = RopeNum<T>::get(e[ib]);
-      r[ia] = RopeNum<T>::put(x0 * c[i] - x1 * s[i]);
-      r[ib] = RopeNum<T>::put(x1 * c[i] + x0 * s[i]);
-    }
+      for (int j = 0; j < kRopeBatch; ++j) {
+        const int h = h0 + j * a.walkers;
+        out[j] = nullptr;
+        if (h < a.heads) {
+          const bool second = h >= a.heads0;
+          if (turned || (second ? a.t[1].copy : a.t[0].copy)) {
+            const char* x = second ? xk + (h - a.heads0) * a.t[1].x_head : xq + h * a.t[0].x_head;
+            out[j] = second ? outk + (h - a.heads0) * a.t[1].out_head : outq + h * a.t[0].out_head;
+            v[j][0] = *reinterpret_cast<const Vec*>(x + o0);
+            if (two) v[j][1] = *reinterpret_cast<const Vec*>(x + o1);
+          }
+        }
+      }
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      v0.v[i] = r[i];
-      v1.v[i] = r[V + i];
+      for (int j = 0; j < kRopeBatch; ++j) {
+        if (out[j] != nullptr) {
+          if (turned) {
+            float e[2 * V];
+            rope_unpack<T, V>(v[j][0], e);
+            rope_unpack<T, V>(v[j][1], e + V);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : V + i;
+              const float x0 = e[ia], x1 = e[ib];
+              e[ia] = x0 * c[i] - x1 * s[i];
+              e[ib] = x1 * c[i] + x0 * s[i];
+            }
+            rope_pack<T, V>(v[j][0], e);
+            rope_pack<T, V>(v[j][1], e + V);
+          }
+          *reinterpret_cast<Vec*>(out[j] + o0) = v[j][0];
+          if (two) *reinterpret_cast<Vec*>(out[j] + o1) = v[j][1];
+        }
+      }
     }
-    *reinterpret_cast<Vec*>(out + o0) = v0;
-    *reinterpret_cast<Vec*>(out + o1) = v1;
   }
 }
 
 template <typename T, int V>
 static int rope_launch(const RopeArgs& a, bool inter, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.n + kRopeThreads - 1) / kRopeThreads));
+  cfg.gridDim = dim3((a.row_walkers + a.per_block - 1) / a.per_block);
   cfg.blockDim = dim3(kRopeThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -238,7 +299,8 @@ extern "C" int gaac_rope(const gaac_rope_tensor* tensors, int n_tensors, int dty
   }
   a.heads0 = tensors[0].n_heads;
   a.heads = static_cast<int>(heads);
-  a.n_tok = static_cast<int>(n_tok);
+  a.n_seq = static_cast<unsigned>(n_seq);
+  a.n_tok = static_cast<unsigned>(n_tok);
   a.rot = rot_dim;
   a.dim = head_dim;
   a.pos = positions;
@@ -249,10 +311,16 @@ extern "C" int gaac_rope(const gaac_rope_tensor* tensors, int n_tensors, int dty
   a.mscale = mscale;
   a.inverse = (flags & GAAC_ROPE_INVERSE) != 0;
   a.rot_units = rot_dim / 2 / v;
-  a.units = a.rot_units + (copies ? (head_dim - rot_dim) / v : 0);
-  a.walkers = a.heads;
-  a.n = rows * a.walkers * a.units;
-  if (a.n > (int64_t{1} << 38)) return GAAC_EINVAL;
+  a.units = a.rot_units + (copies ? ((head_dim - rot_dim) / v + 1) / 2 : 0);
+  // Heads per thread: as many as leave every SM its threads, so that sines are shared where there is work for all,
+  // and single heads where latency counts.
+  const int64_t want = int64_t{152} * 2048, per_row = rows * a.units;
+  const int64_t walkers = std::max<int64_t>((heads + kRopeMost - 1) / kRopeMost, (want + per_row - 1) / per_row);
+  a.walkers = static_cast<int>(std::min<int64_t>(heads, walkers));
+  if (rows * a.walkers > 0x7FFFFFFF) return GAAC_EINVAL;
+  a.row_walkers = static_cast<unsigned>(rows * a.walkers);
+  a.unit_threads = std::min<unsigned>(a.units, kRopeThreads);
+  a.per_block = kRopeThreads / a.unit_threads;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool inter = (flags & GAAC_ROPE_INTERLEAVED) != 0;
   if (dtype == GAAC_BF16) return rope_vec<__nv_bfloat16>(a, v, inter, st);
