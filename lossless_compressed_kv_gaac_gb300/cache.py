@@ -180,7 +180,7 @@ class Kv8Cache(Kv8):
 
     def compact(self, stream=None) -> torch.Tensor:
         """int32 [n_pages]: where each page has gone, -1 for free ones."""
-        moved_to = torch.empty(self.n_pages, dtype=torch.int32, device=self.device)
+        moved_to = torch.empty_like(self.refs)
         _used_on(moved_to, stream)
         kv8_compact(self, moved_to, stream)
         return moved_to

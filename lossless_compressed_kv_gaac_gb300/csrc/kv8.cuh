@@ -75,21 +75,29 @@ __device__ __forceinline__ unsigned int kv8_atomic_add_acq_rel(int32_t* p, unsig
 }
 
 // One launch that may be set up while its predecessor on the stream drains; the kernel waits for it
-// (griddepcontrol.wait) before it touches memory.
+// (griddepcontrol.wait) before it touches memory.  cluster: CTAs of a thread-block cluster.
 template <typename... P, typename... A>
-inline int kv8_launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, void* stream, A... args) {
+inline int kv8_launch_cluster(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, void* stream, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? GAAC_OK : GAAC_ECUDA;
+}
+template <typename... P, typename... A>
+inline int kv8_launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, void* stream, A... args) {
+  return kv8_launch_cluster(kernel, grid, threads, smem, 1, stream, args...);
 }
 
 __device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

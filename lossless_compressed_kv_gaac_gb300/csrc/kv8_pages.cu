@@ -12,6 +12,7 @@ namespace gaac {
 
 constexpr int kPgThreads = 1024;
 constexpr int kPgPer = kKv8Chunk / kPgThreads;  // pages per thread of a chunk
+constexpr unsigned kCompactAlone = 4;           // most chunks that every CTA counts for itself
 
 // Exclusive prefix of x over the CTA's 1024 threads and the total.
 __device__ __forceinline__ int block_exclusive(int x, int* total) {
@@ -67,7 +68,8 @@ __device__ __forceinline__ uint32_t held_mask(const int32_t* refs, int64_t p0, i
   return held;
 }
 
-// This CTA's chunk: counts its free (or held) pages, and says whether it is the last CTA to do so.
+// This CTA's chunk: counts its free (or held) pages, and says whether it is the last CTA to do so.  What the CTA's
+// threads have written before is visible to the last one.
 __device__ __forceinline__ bool count_chunk(const Kv8Dev& c, const Kv8Work& w, bool free_ones, int32_t* ticket) {
   __shared__ int last;
   uint32_t ex;
@@ -95,35 +97,65 @@ __device__ __forceinline__ bool fill_range(const Kv8Dev& c, const int32_t* cu, i
   return true;
 }
 
+// For sequences b, b + step, ... (at most 32, one a lane, with blocks [lo, hi) each): visit(k, i, miss) for every 32
+// blocks i .. of the k-th one, miss: this lane's block is there and has no page.  The first table entries of four
+// sequences are fetched at a time.
+template <typename F>
+__device__ __forceinline__ void for_missing(const Kv8Dev& c, int b, int step, int lo, int hi, F visit) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  const int lane = threadIdx.x & 31;
+  uint32_t todo = __ballot_sync(kAll, hi > lo);
+  while (todo != 0u) {
+    int k[4], l[4], h[4], entry[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      k[j] = todo ? __ffs(todo) - 1 : -1;
+      todo &= todo - 1u;
+      l[j] = __shfl_sync(kAll, lo, max(k[j], 0));
+      h[j] = k[j] < 0 ? l[j] : __shfl_sync(kAll, hi, k[j]);
+      entry[j] = l[j] + lane < h[j] ? c.table[static_cast<int64_t>(b + k[j] * step) * c.max_blocks + l[j] + lane] : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (k[j] < 0) continue;
+      visit(k[j], l[j], entry[j] < 0);
+      const int32_t* row = c.table + static_cast<int64_t>(b + k[j] * step) * c.max_blocks;
+      for (int i = l[j] + 32; i < h[j]; i += 32) visit(k[j], i, i + lane < h[j] && row[i + lane] < 0);
+    }
+  }
+}
+
 // Entries without a page among the blocks that fill, in order of sequence and block, get the lowest free pages
-// in order.  Every CTA counts the free pages of its chunk; the last one to finish does the rest.
+// in order.  Every CTA counts the free pages of its chunk and the missing entries of some sequences, a warp each; the
+// last one to finish ranks them, lists the pages and hands them out.
 __global__ void __launch_bounds__(kPgThreads) kv8_reserve_kernel(Kv8Dev c, const int32_t* cu, int32_t* status) {
   __shared__ int sh_free;
   dependent_wait();
   dependent_launch();
   const Kv8Work w = kv8_work(c.batch, c.n_pages);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (!count_chunk(c, w, true, c.work + w.tickets)) return;
-  // ---- how many pages each sequence lacks
   int32_t* need = c.work + w.need;
-  for (int b = warp; b < c.batch; b += kPgThreads / 32) {
-    int lo, hi, miss = 0;
-    if (!fill_range(c, cu, b, &lo, &hi) && lane == 0) report(status, GAAC_EINVAL);
-    const int32_t* row = c.table + static_cast<int64_t>(b) * c.max_blocks;
-    for (int i0 = lo; i0 < hi; i0 += 32) miss += __popc(__ballot_sync(0xFFFFFFFFu, i0 + lane < hi && row[i0 + lane] < 0));
-    if (lane == 0) need[b] = miss;
+  const int warps = gridDim.x * (kPgThreads / 32);
+  for (int b0 = blockIdx.x * (kPgThreads / 32) + warp; b0 < c.batch; b0 += 32 * warps) {
+    int lo = 0, hi = 0, mine = 0;
+    const int64_t b = b0 + static_cast<int64_t>(lane) * warps;
+    if (b < c.batch && !fill_range(c, cu, static_cast<int>(b), &lo, &hi)) report(status, GAAC_EINVAL);
+    for_missing(c, b0, warps, lo, hi, [&](int k, int, bool miss) {
+      const int n = __popc(__ballot_sync(0xFFFFFFFFu, miss));
+      if (lane == k) mine += n;
+    });
+    if (b < c.batch) need[b] = mine;
   }
-  __syncthreads();
+  if (!count_chunk(c, w, true, c.work + w.tickets)) return;
   // ---- the rank of each sequence's first one
   int total = 0;
   for (int b0 = 0; b0 < c.batch; b0 += kPgThreads) {
-    const int x = b0 + tid < c.batch ? need[b0 + tid] : 0;
+    const int x = b0 + tid < c.batch ? __ldcg(need + b0 + tid) : 0;
     int sum;
     const int at = total + block_exclusive(x, &sum);
     if (b0 + tid < c.batch) need[b0 + tid] = at;
     total += sum;
   }
-  if (tid == 0) need[c.batch] = total;
   if (total == 0) return;
   // ---- the lowest free pages, as many as are lacking
   int32_t* list = c.work + w.list_a;
@@ -148,23 +180,23 @@ __global__ void __launch_bounds__(kPgThreads) kv8_reserve_kernel(Kv8Dev c, const
   if (found < total && tid == 0) report(status, GAAC_EPOOL);
   __syncthreads();
   // ---- into the table
-  for (int b = warp; b < c.batch; b += kPgThreads / 32) {
-    int r = need[b];
-    if (need[b + 1] == r) continue;
-    int lo, hi;
-    fill_range(c, cu, b, &lo, &hi);
-    int32_t* row = c.table + static_cast<int64_t>(b) * c.max_blocks;
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-      const bool miss = i0 + lane < hi && row[i0 + lane] < 0;
+  for (int b0 = warp; b0 < c.batch; b0 += 32 * (kPgThreads / 32)) {
+    int lo = 0, hi = 0, rank = 0;
+    const int b = b0 + lane * (kPgThreads / 32);
+    if (b < c.batch) {
+      fill_range(c, cu, b, &lo, &hi);
+      rank = need[b];
+    }
+    for_missing(c, b0, kPgThreads / 32, lo, hi, [&](int k, int i, bool miss) {
       const uint32_t m = __ballot_sync(0xFFFFFFFFu, miss);
-      const int at = r + __popc(m & ((1u << lane) - 1u));
+      const int at = __shfl_sync(0xFFFFFFFFu, rank, k) + __popc(m & ((1u << lane) - 1u));
       if (miss && at < found) {
         const int32_t p = list[at];
-        row[i0 + lane] = p;
+        c.table[static_cast<int64_t>(b0 + k * (kPgThreads / 32)) * c.max_blocks + i + lane] = p;
         c.refs[p] = 1;
       }
-      r += __popc(m);
-    }
+      if (lane == k) rank += __popc(m);
+    });
   }
 }
 
@@ -195,65 +227,67 @@ __global__ void __launch_bounds__(kRelThreads) kv8_release_kernel(Kv8Dev c, cons
   if (threadIdx.x == 0) c.lens[b] = 0;
 }
 
-// One CTA per pair (src, dst).  A pair is refused as a whole (and reported) when an index is out of range, dst is
-// not empty, dst is listed before, src is the dst of some pair, or src's own row is not valid.
-__global__ void __launch_bounds__(kPgThreads) kv8_fork_kernel(Kv8Dev c, const int32_t* src, const int32_t* dst, int n,
+constexpr int kFkThreads = 512;
+constexpr int kFkCtas = 8;  // a cluster for each pair
+
+// One cluster per pair (src, dst).  A pair is refused as a whole (and reported) when an index is out of range, dst is
+// not empty, dst is listed before, src is the dst of some pair, or src's own row is not valid.  Every CTA of the
+// cluster checks; none writes before all have (the cluster's barrier), since what is written is what is checked.
+__global__ void __launch_bounds__(kFkThreads) kv8_fork_kernel(Kv8Dev c, const int32_t* src, const int32_t* dst, int n,
                                                               int32_t* status) {
   dependent_wait();
   dependent_launch();
-  const int tid = threadIdx.x, i = blockIdx.x;
+  const int tid = threadIdx.x, i = blockIdx.x / kFkCtas, part = blockIdx.x % kFkCtas;
   const int s = src[i], d = dst[i];
-  int bad = 0;
-  if (s < 0 || s >= c.batch || d < 0 || d >= c.batch) {
-    bad = GAAC_EINVAL;
-  } else {
-    for (int j = tid; j < n; j += kPgThreads)
-      if (dst[j] == s || (j < i && dst[j] == d)) bad = GAAC_EINVAL;
-  }
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) report(status, GAAC_EINVAL);
-    return;
-  }
-  const int32_t* from = c.table + static_cast<int64_t>(s) * c.max_blocks;
-  int32_t* to = c.table + static_cast<int64_t>(d) * c.max_blocks;
-  const int len = c.lens[s], full = len / kBlock, open = len % kBlock;
-  int odd = 0;
-  if (len < 0 || len > static_cast<int64_t>(c.max_blocks) * kBlock) {
-    odd = 1;
-  } else {
-    for (int k = tid; k < c.max_blocks; k += kPgThreads) {
-      if (to[k] != -1) bad = 1;
-      if (k < full && (from[k] < 0 || from[k] >= c.n_pages)) odd = 1;
-    }
+  const bool in = s >= 0 && s < c.batch && d >= 0 && d < c.batch;
+  int bad = !in, odd = 0, len = 0;
+  const int32_t* from = c.table + (in ? static_cast<int64_t>(s) * c.max_blocks : 0);
+  int32_t* to = c.table + (in ? static_cast<int64_t>(d) * c.max_blocks : 0);
+  if (in) {
+    len = c.lens[s];
     if (c.lens[d] != 0) bad = 1;
+    for (int j = tid; j < n; j += kFkThreads)
+      if (dst[j] == s || (j < i && dst[j] == d)) bad = 1;
+    for (int k = tid; k < c.max_blocks; k += kFkThreads)
+      if (to[k] != -1) bad = 1;
+    if (len < 0 || len > static_cast<int64_t>(c.max_blocks) * kBlock) {
+      odd = 1;
+    } else {
+      for (int k = tid; k < len / kBlock; k += kFkThreads)
+        if (from[k] < 0 || from[k] >= c.n_pages) odd = 1;
+    }
   }
   bad = __syncthreads_or(bad);
   odd = __syncthreads_or(odd);
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (bad || odd) {
-    if (tid == 0) report(status, odd ? GAAC_EFORMAT : GAAC_EINVAL);
+    if (tid == 0 && part == 0) report(status, bad ? GAAC_EINVAL : GAAC_EFORMAT);
     return;
   }
-  for (int k = tid; k < full; k += kPgThreads) {
+  const int full = len / kBlock, open = len % kBlock;
+  for (int k = part * kFkThreads + tid; k < full; k += kFkCtas * kFkThreads) {
     const int32_t p = from[k];
     to[k] = p;
     atomicAdd(c.refs + p, 1);
   }
   // open rows of every (kv-head, K|V): 16 vectors of 16 bytes each
-  const int64_t tile = kBlock * kD;
-  const uint4* ts = reinterpret_cast<const uint4*>(c.tail + static_cast<int64_t>(s) * c.heads * 2 * tile);
-  uint4* td = reinterpret_cast<uint4*>(c.tail + static_cast<int64_t>(d) * c.heads * 2 * tile);
-  const int per = open * (kD / 8), all = per * 2 * c.heads;
-  for (int k = tid; k < all; k += kPgThreads) {
-    const int64_t at = static_cast<int64_t>(k / per) * (tile / 8) + k % per;
+  constexpr int kRow = kD / 8;
+  const uint4* ts = reinterpret_cast<const uint4*>(c.tail) + static_cast<int64_t>(s) * c.heads * 2 * kBlock * kRow;
+  uint4* td = reinterpret_cast<uint4*>(c.tail) + static_cast<int64_t>(d) * c.heads * 2 * kBlock * kRow;
+  const int per = open * kRow, all = per * 2 * c.heads;
+#pragma unroll 4
+  for (int k = part * kFkThreads + tid; k < all; k += kFkCtas * kFkThreads) {
+    const int at = k / per * (kBlock * kRow) + k % per;
     td[at] = ts[at];
   }
-  if (tid == 0) c.lens[d] = len;
+  if (tid == 0 && part == 0) c.lens[d] = len;
 }
 
 // ------------------------------------------------------------------ compact
 // With n held pages, the held pages at n and above move into the holes below n: the lowest hole takes the highest
 // page, and so on.  Source and target never overlap.
-//   1. every CTA counts the held pages of its chunk; the last one makes the counts prefixes
+//   1. (pools of more than kCompactAlone chunks) every CTA counts the held pages of its chunk; the last one makes the
+//      counts prefixes
 //   2. holes and movers into two lists by rank; moved_to of the pages that stay
 //   3. contents, counts and the table
 
@@ -277,16 +311,42 @@ __global__ void __launch_bounds__(kPgThreads) kv8_compact_count_kernel(Kv8Dev c)
   }
 }
 
+// ALONE: no counts from step 1; every CTA counts the whole pool itself, which for a few chunks is quicker than a
+// launch more.
+template <bool ALONE>
 __global__ void __launch_bounds__(kPgThreads) kv8_compact_list_kernel(Kv8Dev c, int32_t* moved_to) {
   dependent_wait();
   dependent_launch();
   const Kv8Work w = kv8_work(c.batch, c.n_pages);
   const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kKv8Chunk + threadIdx.x * kPgPer;
-  const int64_t held_all = c.work[w.chunks + gridDim.x];
   uint32_t ex;
   const uint32_t held = held_mask(c.refs, p0, c.n_pages, &ex);
-  int sum;
-  int before = c.work[w.chunks + blockIdx.x] + block_exclusive(__popc(held), &sum);
+  int sum, in_chunk = block_exclusive(__popc(held), &sum);
+  int64_t held_all;
+  int before;
+  if (ALONE) {
+    int earlier = 0, all = 0, total;
+    for (unsigned ch = 0; ch < gridDim.x; ++ch) {
+      uint32_t e;
+      const int n = ch == blockIdx.x ? __popc(held)
+                                     : __popc(held_mask(c.refs, static_cast<int64_t>(ch) * kKv8Chunk + threadIdx.x * kPgPer, c.n_pages, &e));
+      all += n;
+      if (ch < blockIdx.x) earlier += n;
+    }
+    if (gridDim.x > 1) {
+      block_exclusive(earlier, &before);
+      block_exclusive(all, &total);
+    } else {
+      before = 0;
+      total = sum;
+    }
+    held_all = total;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && held_all == c.n_pages) c.work[w.tickets + 2] = 0;
+  } else {
+    held_all = c.work[w.chunks + gridDim.x];
+    before = c.work[w.chunks + blockIdx.x];
+  }
+  before += in_chunk;
   int32_t* holes = c.work + w.list_a;
   int32_t* movers = c.work + w.list_b;
 #pragma unroll
@@ -309,26 +369,37 @@ __global__ void __launch_bounds__(kPgThreads) kv8_compact_list_kernel(Kv8Dev c, 
 }
 
 constexpr int kMvThreads = 256;
+constexpr int kMvCtasPerSm = 8;
 
-__global__ void __launch_bounds__(kMvThreads) kv8_compact_move_kernel(Kv8Dev c, int32_t* moved_to) {
+// A CTA copies one (page, kv-head) at a time, 16 KB with four 16-byte loads a thread in flight; where the next one
+// lies is fetched meanwhile.
+__global__ void __launch_bounds__(kMvThreads, kMvCtasPerSm) kv8_compact_move_kernel(Kv8Dev c, int32_t* moved_to) {
   dependent_wait();
   dependent_launch();
   const Kv8Work w = kv8_work(c.batch, c.n_pages);
   const int32_t* holes = c.work + w.list_a;
   const int32_t* movers = c.work + w.list_b;
-  const int64_t items = static_cast<int64_t>(c.work[w.tickets + 2]) * c.heads;
   const int tid = threadIdx.x;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int64_t m = it / c.heads;
-    const int h = static_cast<int>(it % c.heads);
-    const int64_t from = movers[m], to = holes[m];
+  const unsigned heads = c.heads, items = static_cast<unsigned>(c.work[w.tickets + 2]) * heads;  // below 2^24
+  unsigned it = blockIdx.x;
+  int64_t from = 0, to = 0;
+  if (it < items) {
+    from = movers[it / heads];
+    to = holes[it / heads];
+  }
+  while (it < items) {
+    const unsigned h = it % heads;
     const uint4* s = reinterpret_cast<const uint4*>(c.pages + (from * c.heads + h) * kKv8Pair);
     uint4* d = reinterpret_cast<uint4*>(c.pages + (to * c.heads + h) * kKv8Pair);
     uint4 x[kKv8Pair / 16 / kMvThreads];
 #pragma unroll
     for (int i = 0; i < kKv8Pair / 16 / kMvThreads; ++i) x[i] = s[tid + kMvThreads * i];
-#pragma unroll
-    for (int i = 0; i < kKv8Pair / 16 / kMvThreads; ++i) d[tid + kMvThreads * i] = x[i];
+    const unsigned next = it + gridDim.x;
+    int64_t from2 = 0, to2 = 0;
+    if (next < items) {
+      from2 = movers[next / heads];
+      to2 = holes[next / heads];
+    }
     if (tid == 0) {
       reinterpret_cast<float2*>(c.scales)[to * c.heads + h] = reinterpret_cast<const float2*>(c.scales)[from * c.heads + h];
       if (h == 0) {
@@ -337,15 +408,20 @@ __global__ void __launch_bounds__(kMvThreads) kv8_compact_move_kernel(Kv8Dev c, 
         moved_to[from] = static_cast<int32_t>(to);
       }
     }
+#pragma unroll
+    for (int i = 0; i < kKv8Pair / 16 / kMvThreads; ++i) d[tid + kMvThreads * i] = x[i];
+    it = next;
+    from = from2;
+    to = to2;
   }
   // The table.  moved_to of a page that moves may or may not have been replaced above yet: both forms say the same.
   const int64_t entries = static_cast<int64_t>(c.batch) * c.max_blocks;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kMvThreads + tid; i < entries; i += static_cast<int64_t>(gridDim.x) * kMvThreads) {
     const int32_t p = c.table[i];
     if (p < 0 || p >= c.n_pages) continue;
-    int32_t to = *reinterpret_cast<volatile int32_t*>(moved_to + p);
-    if (to <= -2) to = holes[-2 - to];
-    if (to != p) c.table[i] = to;
+    int32_t q = *reinterpret_cast<volatile int32_t*>(moved_to + p);
+    if (q <= -2) q = holes[-2 - q];
+    if (q != p) c.table[i] = q;
   }
 }
 
@@ -373,15 +449,21 @@ extern "C" int gaac_kv8_fork(const gaac_kv8* cache, const int32_t* src, const in
   if (n == 0) return GAAC_OK;
   if (src == nullptr || dst == nullptr || ((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) & 3u))
     return GAAC_EINVAL;
-  return kv8_launch(kv8_fork_kernel, dim3(n), kPgThreads, 0, stream, kv8_dev(cache), src, dst, n, d_status);
+  return kv8_launch_cluster(kv8_fork_kernel, dim3(kFkCtas * n), kFkThreads, 0, kFkCtas, stream, kv8_dev(cache), src, dst, n,
+                            d_status);
 }
 
 extern "C" int gaac_kv8_compact(const gaac_kv8* cache, int32_t* moved_to, void* stream) {
   if (!kv8_ok(cache) || moved_to == nullptr || (reinterpret_cast<uintptr_t>(moved_to) & 3u)) return GAAC_EINVAL;
   const Kv8Dev c = kv8_dev(cache);
   const unsigned chunks = chunks_of(cache);
-  int e = kv8_launch(kv8_compact_count_kernel, dim3(chunks), kPgThreads, 0, stream, c);
-  if (e == GAAC_OK) e = kv8_launch(kv8_compact_list_kernel, dim3(chunks), kPgThreads, 0, stream, c, moved_to);
-  if (e == GAAC_OK) e = kv8_launch(kv8_compact_move_kernel, dim3(152 * 8), kMvThreads, 0, stream, c, moved_to);
+  int e;
+  if (chunks <= kCompactAlone) {
+    e = kv8_launch(kv8_compact_list_kernel<true>, dim3(chunks), kPgThreads, 0, stream, c, moved_to);
+  } else {
+    e = kv8_launch(kv8_compact_count_kernel, dim3(chunks), kPgThreads, 0, stream, c);
+    if (e == GAAC_OK) e = kv8_launch(kv8_compact_list_kernel<false>, dim3(chunks), kPgThreads, 0, stream, c, moved_to);
+  }
+  if (e == GAAC_OK) e = kv8_launch(kv8_compact_move_kernel, dim3(152 * kMvCtasPerSm), kMvThreads, 0, stream, c, moved_to);
   return e;
 }
