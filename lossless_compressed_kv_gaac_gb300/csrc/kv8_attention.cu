@@ -37,10 +37,11 @@ constexpr int kKaThreads = kKaCompute + 32 * kKaCopyWarps;
 constexpr int kKaStages = 10;                // unit i uses stage i % stages and belongs to group i % groups
 constexpr int kKaHalf = kBlock / 2;          // tokens of an open block's unit
 constexpr int kKaRows = 8;                   // query heads per kv-head in the MMA columns
-constexpr int kKaMinUnits = 5;               // fewer units than this are not worth a CTA
+constexpr int kKaMinUnits = 4;               // fewer units than this are not worth a CTA
 constexpr int kKaStride = kD + 4;            // floats per row of a warp's state in shared memory (bank spread)
 constexpr int kKaQStride = 2 * kD + 8;       // bytes per query row kept for the open block
 constexpr int kKaPart = 3 * kKaRows + kKaRows * kD;  // floats of a partial: m, l, M, O
+constexpr int kKaJoin = 8;                   // partials in flight when they are joined
 constexpr uint32_t kKaFull = 0xFFFFFFFFu;
 static_assert(kKaStages % kKaGroups == 0, "a stage belongs to one group, which waits for all of its phases in turn");
 
@@ -127,22 +128,29 @@ __device__ __forceinline__ void ka_arrive(uint64_t* bar) {
 // ------------------------------------------------------------------ units
 
 struct KaSeq {  // a sequence's units per kv-head
-  int full, open, units;
+  int full, open;
+  unsigned units;
 };
 __device__ __forceinline__ KaSeq ka_seq(const Kv8Dev& c, int len) {
   if (len < 0 || len > static_cast<int64_t>(c.max_blocks) * kBlock) len = 0;
   KaSeq s;
   s.full = len / kBlock;
   s.open = len % kBlock;
-  s.units = max(1, s.full + (s.open + kKaHalf - 1) / kKaHalf);
+  s.units = static_cast<unsigned>(max(1, s.full + (s.open + kKaHalf - 1) / kKaHalf));
   return s;
 }
 
-__device__ __forceinline__ void ka_tma(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+// The cache is read once a step: its lines leave L2 first (1 x 65536 tokens: 26.8 us, 28.3 without the hint).
+__device__ __forceinline__ uint64_t ka_evict_first() {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ void ka_tma(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          smem_addr(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], "
+      "[%4], %5;" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar)), "l"(policy)
       : "memory");
 }
 
@@ -178,48 +186,46 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
   const Kv8Dev& c = a.c;
   const int lane = threadIdx.x & 31;
   KaRing ring;
-  // ---- the cut: pieces of at most `piece` units
-  int64_t total = 0;
+  // ---- the cut: pieces of at most `piece` units (all counts below 2^31: the host has checked)
+  unsigned total = 0;
   int len32 = 0;  // lengths of 32 sequences, one a lane
   for (int b0 = 0; b0 < c.batch; b0 += 32) {
-    int u = 0;
+    unsigned u = 0;
     if (b0 + lane < c.batch) {
       const int len = len32 = c.lens[b0 + lane];
       if (blockIdx.x == 0 && (len < 0 || len > static_cast<int64_t>(c.max_blocks) * kBlock)) report(a.status, GAAC_EINVAL);
       u = ka_seq(c, len).units;
     }
-    // 32 sequences of up to 2^24 + 2 units: 30 bits
-    total += static_cast<int64_t>(__reduce_add_sync(kKaFull, u)) * c.heads;
+    total += __reduce_add_sync(kKaFull, u) * c.heads;
   }
-  const int64_t piece = max(static_cast<int64_t>(kKaMinUnits), (total + gridDim.x - 1) / gridDim.x);
+  const unsigned piece = max(static_cast<unsigned>(kKaMinUnits), (total + gridDim.x - 1) / gridDim.x);
   // Pieces begin with their pair where that needs no more CTAs: then none has parts of two pairs to bring to an
   // end.  Otherwise the row of all units is cut without regard to pairs.
   bool aligned = false;
-  if (static_cast<int64_t>(c.batch) * c.heads <= gridDim.x) {
-    int64_t pieces = 0;
+  if (static_cast<unsigned>(c.batch) * c.heads <= gridDim.x) {
+    unsigned pieces = 0;
     for (int b0 = 0; b0 < c.batch; b0 += 32) {
       const int len = c.batch <= 32 ? len32 : b0 + lane < c.batch ? c.lens[b0 + lane] : 0;
-      const int k = b0 + lane < c.batch ? static_cast<int>((ka_seq(c, len).units + piece - 1) / piece) : 0;
-      pieces += static_cast<int64_t>(__reduce_add_sync(kKaFull, k)) * c.heads;
+      pieces += __reduce_add_sync(kKaFull, b0 + lane < c.batch ? (ka_seq(c, len).units + piece - 1) / piece : 0u) * c.heads;
     }
     aligned = pieces <= gridDim.x;
   }
   // In places (units, or pieces when aligned): where this CTA begins and ends.
-  const int64_t begin = aligned ? blockIdx.x : blockIdx.x * piece;
+  const unsigned begin = aligned ? blockIdx.x : blockIdx.x * piece;
   int b = c.batch;
-  int64_t base = 0;  // places before sequence b
+  unsigned base = 0;  // places before sequence b
   int b32 = -1;
   for (int b0 = 0; b0 < c.batch; b0 += 32) {
     const int len = c.batch <= 32 ? len32 : b0 + lane < c.batch ? c.lens[b0 + lane] : 0;
-    int64_t u = 0;
+    unsigned u = 0;
     if (b0 + lane < c.batch) {
       u = ka_seq(c, len).units;
       u = (aligned ? (u + piece - 1) / piece : u) * c.heads;
     }
-    int64_t incl = u;
+    unsigned incl = u;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t v = __shfl_up_sync(kKaFull, incl, d);
+      const unsigned v = __shfl_up_sync(kKaFull, incl, d);
       if (lane >= d) incl += v;
     }
     const uint32_t past = __ballot_sync(kKaFull, base + incl > begin);
@@ -235,9 +241,9 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
   }
   KaSeq s = {};
   int h = 0;
-  int64_t own = 1;      // places of a pair of sequence b
-  int64_t skipped = 0;  // places of the first pair before this CTA's
-  int64_t seg = 0, u = 0, u_end = 0;  // in units: the pair's first, this CTA's next and last
+  unsigned own = 1;      // places of a pair of sequence b
+  unsigned skipped = 0;  // places of the first pair before this CTA's
+  unsigned seg = 0, u = 0, u_end = 0;  // in units: the pair's first, this CTA's next and last
   if (b < c.batch) {
     s = ka_seq(c, __shfl_sync(kKaFull, len32, b - b32));
     own = aligned ? (s.units + piece - 1) / piece : s.units;
@@ -245,8 +251,9 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
     skipped = begin - base - h * own;
     seg = aligned ? 0 : begin - skipped;
     u = aligned ? skipped * piece : begin;
-    u_end = min(u + piece, aligned ? static_cast<int64_t>(s.units) : total);
+    u_end = min(u + piece, aligned ? static_cast<unsigned>(s.units) : total);
   }
+  const uint64_t policy = ka_evict_first();
   int32_t row32 = 0;  // entries 0-31 of the table row of sequence row_of
   int row_of = -1;
   bool ok = true;
@@ -267,7 +274,7 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
       row32 = pg_next;
       row_of = b;
     }
-    if (h == c.heads - 1 && b + 1 < c.batch && u_end > seg + s.units) {
+    if (h == c.heads - 1 && b + 1 < c.batch && !aligned && u_end > seg + s.units) {
       row32 = lane < c.max_blocks ? row[c.max_blocks + lane] : 0;
       row_of = b + 1;
     }
@@ -304,11 +311,12 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
         }
         mbar_arrive_expect_tx(full, (kind == kUnitNone ? 0 : kKv8Pair) + (with_q ? q_bytes : 0));
         if (kind == kUnitPage) {
-          ka_tma(sm.stage[st], pages, 0, static_cast<int>(tile * 2 * kBlock), full);
+          ka_tma(sm.stage[st], pages, 0, static_cast<int>(tile * 2 * kBlock), full, policy);
         } else if (kind == kUnitOpen) {  // K channels 0-63, 64-127, V the same
           const int y = static_cast<int>((static_cast<int64_t>(b) * c.heads + h) * 2 * kBlock) + kKaHalf * (l0 + i - s.full);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) ka_tma(sm.stage[st] + k * (kKv8Pair / 4), tail, (k & 1) * (kD / 2), y + (k >> 1) * kBlock, full);
+          for (int k = 0; k < 4; ++k)
+            ka_tma(sm.stage[st] + k * (kKv8Pair / 4), tail, (k & 1) * (kD / 2), y + (k >> 1) * kBlock, full, policy);
         }
         if (with_q) bulk_g2s(sm.q[st], q, q_bytes, full);
       }
@@ -390,29 +398,30 @@ __device__ __forceinline__ void ka_fold(float& m, float& l, float& mv, float4& o
   mv = vn;
 }
 
-// The last CTA of a pair joins the partials of the n CTAs that share it.  Thread (share, row, four channels) folds
-// partials share, share + shares, ... in order, twelve of them in flight; the shares (as many as the threads allow
-// for r rows) meet in shared memory.
+// Folds n partials, the first at `head`, the others `step` floats apart from `rest` on.  Thread (share, row, four
+// channels) takes partials share, share + shares, ... in order, kKaJoin of them in flight; the shares (as many as the
+// threads allow for r rows) meet in shared memory.  Threads of share 0 get the result of their row and channels.
 template <bool HALF>
-__device__ __forceinline__ bool ka_join(const KaArgs& a, KaSmem& sm, int b, int h, int cta0, int n, KaSync& meet) {
-  constexpr int kBatch = 12;
+__device__ __forceinline__ bool ka_fold_all(const KaArgs& a, KaSmem& sm, const float* head, const float* rest, int64_t step,
+                                            int n, KaSync& meet, float& m, float& l, float& mv, float4& o) {
   const int per = a.r * (kD / 4), shares = kKaCompute / per;
   const int share = threadIdx.x / per, at = threadIdx.x % per, row = at / (kD / 4), ch = 4 * (at % (kD / 4));
-  float m = -INFINITY, l = 0.f, mv = -INFINITY;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  m = mv = -INFINITY;
+  l = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
   if (share < shares) {
 #pragma unroll 1
-    for (int i0 = share; i0 < n; i0 += kBatch * shares) {
-      float m1[kBatch], l1[kBatch], mv1[kBatch];
-      float4 o1[kBatch];
+    for (int i0 = share; i0 < n; i0 += kKaJoin * shares) {
+      float m1[kKaJoin], l1[kKaJoin], mv1[kKaJoin];
+      float4 o1[kKaJoin];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
+      for (int k = 0; k < kKaJoin; ++k) {
         const int i = i0 + k * shares;
         m1[k] = mv1[k] = -INFINITY;
         l1[k] = 0.f;
         o1[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i < n) {
-          const float* p = a.part + static_cast<int64_t>(2 * (cta0 + i) + (i == 0 ? 1 : 0)) * kKaPart + row;
+          const float* p = (i == 0 ? head : rest + (i - 1) * step) + row;
           m1[k] = __ldcg(p);
           l1[k] = __ldcg(p + kKaRows);
           mv1[k] = __ldcg(p + 2 * kKaRows);
@@ -420,7 +429,7 @@ __device__ __forceinline__ bool ka_join(const KaArgs& a, KaSmem& sm, int b, int 
         }
       }
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) ka_fold(m, l, mv, o, m1[k], l1[k], mv1[k], o1[k]);
+      for (int k = 0; k < kKaJoin; ++k) ka_fold(m, l, mv, o, m1[k], l1[k], mv1[k], o1[k]);
     }
     if (share > 0) {
       *reinterpret_cast<float4*>(&sm.state[share][row][ch]) = o;
@@ -431,12 +440,77 @@ __device__ __forceinline__ bool ka_join(const KaArgs& a, KaSmem& sm, int b, int 
       }
     }
   }
-  if (shares > 1 && !ka_meet(sm, meet, a.status)) return false;
-  if (share == 0) {
+  if (shares > 1) {
+    if (!ka_meet(sm, meet, a.status)) return false;
+    if (share == 0) {
 #pragma unroll 1
-    for (int w = 1; w < shares; ++w)
-      ka_fold(m, l, mv, o, sm.m[w][row], sm.l[w][row], sm.mv[w][row], *reinterpret_cast<const float4*>(&sm.state[w][row][ch]));
-    ka_store<HALF>(a, b, h, row, ch, ka_result(o, m, l, mv));
+      for (int w = 1; w < shares; ++w)
+        ka_fold(m, l, mv, o, sm.m[w][row], sm.l[w][row], sm.mv[w][row], *reinterpret_cast<const float4*>(&sm.state[w][row][ch]));
+    }
+  }
+  return true;
+}
+
+// One more CTA has written its partial where `count` of them meet.  last: it was the last one.  Everybody's stores
+// come before thread 0's release by the barrier, and what the others released comes before what follows.
+__device__ __forceinline__ bool ka_arrived(KaSmem& sm, int32_t* counter, int count, KaSync& meet, int32_t* status, bool& last) {
+  if (!ka_meet(sm, meet, status)) return false;
+  if (threadIdx.x == 0) {
+    sm.last = kv8_atomic_add_acq_rel(counter, 1u) == static_cast<unsigned int>(count - 1);
+    if (sm.last) *counter = 0;
+  }
+  if (!ka_meet(sm, meet, status)) return false;
+  last = sm.last;
+  return true;
+}
+
+// The partial of a (CTA, pair): slot 1 where the pair begins in the CTA, 0 where it does not.
+__device__ __forceinline__ int64_t ka_slot(int cta, int cta0) { return 2 * static_cast<int64_t>(cta) + (cta == cta0 ? 1 : 0); }
+
+__device__ __forceinline__ void ka_put(float* slot, int row, int ch, float m, float l, float mv, float4 o) {
+  *reinterpret_cast<float4*>(slot + 3 * kKaRows + row * kD + ch) = o;
+  if (ch == 0) {
+    slot[row] = m;
+    slot[kKaRows + row] = l;
+    slot[2 * kKaRows + row] = mv;
+  }
+}
+
+// This CTA's partial of a pair that n CTAs share is in its slot: the last to come joins them.  Up to kKaJoin partials
+// for each share of the threads are one round of loads; more than that are joined in teams of kKaJoin first, so that
+// two rounds and two counters take the place of up to a dozen rounds.
+template <bool HALF>
+__device__ __forceinline__ bool ka_join(const KaArgs& a, KaSmem& sm, int b, int h, int cta0, int n, KaSync& meet) {
+  const int per = a.r * (kD / 4), at = threadIdx.x % per, row = at / (kD / 4), ch = 4 * (at % (kD / 4));
+  const bool writer = threadIdx.x < per;
+  const int64_t grid = gridDim.x;
+  const float* rest = a.part + 2 * static_cast<int64_t>(cta0 + 1) * kKaPart;
+  float m, l, mv;
+  float4 o;
+  bool last;
+  if (n <= kKaJoin * (kKaCompute / per)) {
+    if (!ka_arrived(sm, a.counters + cta0, n, meet, a.status, last)) return false;
+    if (last) {
+      if (!ka_fold_all<HALF>(a, sm, a.part + ka_slot(cta0, cta0) * kKaPart, rest, 2 * kKaPart, n, meet, m, l, mv, o)) return false;
+      if (writer) ka_store<HALF>(a, b, h, row, ch, ka_result(o, m, l, mv));
+    }
+    return true;
+  }
+  const int team = (static_cast<int>(blockIdx.x) - cta0) / kKaJoin, teams = (n + kKaJoin - 1) / kKaJoin;
+  const int head = cta0 + team * kKaJoin, size = min(kKaJoin, n - team * kKaJoin);
+  if (!ka_arrived(sm, a.counters + grid + ka_slot(head, cta0), size, meet, a.status, last)) return false;
+  if (!last) return true;
+  if (!ka_fold_all<HALF>(a, sm, a.part + ka_slot(head, cta0) * kKaPart, rest + 2 * static_cast<int64_t>(head - cta0) * kKaPart,
+                         2 * kKaPart, size, meet, m, l, mv, o))
+    return false;
+  float* joined = a.part + 2 * grid * kKaPart;  // the teams' partials: slots like the CTAs', at a team's first CTA
+  if (writer) ka_put(joined + ka_slot(head, cta0) * kKaPart, row, ch, m, l, mv, o);
+  if (!ka_arrived(sm, a.counters + cta0, teams, meet, a.status, last)) return false;
+  if (last) {
+    if (!ka_fold_all<HALF>(a, sm, joined + ka_slot(cta0, cta0) * kKaPart, joined + 2 * static_cast<int64_t>(cta0 + kKaJoin) * kKaPart,
+                           2 * kKaJoin * kKaPart, teams, meet, m, l, mv, o))
+      return false;
+    if (writer) ka_store<HALF>(a, b, h, row, ch, ka_result(o, m, l, mv));
   }
   return true;
 }
@@ -691,7 +765,7 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
       }
       if (!ka_meet(sm, meet, a.status)) return;
       const bool whole = n_cta == 1;
-      float* mine = a.part + static_cast<int64_t>(2 * blockIdx.x + (static_cast<int>(blockIdx.x) == cta0 ? 1 : 0)) * kKaPart;
+      float* mine = a.part + ka_slot(blockIdx.x, cta0) * kKaPart;
       {
         static_assert(kKaRows * kD / 4 <= kKaCompute, "at most one float4 of the result for each thread");
         const int row = tid / (kD / 4), ch = 4 * (tid % (kD / 4));
@@ -711,28 +785,13 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
             const float4 x = *reinterpret_cast<const float4*>(&sm.state[w][row][ch]);
             o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
           }
-          if (whole) {
+          if (whole)
             ka_store<HALF>(a, b, h, row, ch, ka_result(o, mx, den, vx));
-          } else {
-            *reinterpret_cast<float4*>(mine + 3 * kKaRows + row * kD + ch) = o;
-            if (ch == 0) {
-              mine[row] = mx;
-              mine[kKaRows + row] = den;
-              mine[2 * kKaRows + row] = vx;
-            }
-          }
+          else
+            ka_put(mine, row, ch, mx, den, vx, o);
         }
       }
-      if (!whole) {
-        // the barrier orders everybody's stores before thread 0's release, which passes them on
-        if (!ka_meet(sm, meet, a.status)) return;
-        if (tid == 0) sm.last = kv8_atomic_add_acq_rel(a.counters + cta0, 1u) == static_cast<unsigned int>(n_cta - 1);
-        if (!ka_meet(sm, meet, a.status)) return;
-        if (sm.last) {
-          if (!ka_join<HALF>(a, sm, b, h, cta0, n_cta, meet)) return;
-          if (tid == 0) a.counters[cta0] = 0;
-        }
-      }
+      if (!whole && !ka_join<HALF>(a, sm, b, h, cta0, n_cta, meet)) return;
       // the next pair's state may be written once everybody has read this one's
       if (!ka_meet(sm, meet, a.status)) return;
     }
@@ -784,7 +843,8 @@ static int ka_sms() {
   return cached[dev];
 }
 
-static size_t ka_counter_bytes(int grid) { return (static_cast<size_t>(grid) * 4 + 15) & ~static_cast<size_t>(15); }
+// Counters: one for each pair (at its first CTA) and two for the teams that begin at a CTA.
+static size_t ka_counter_bytes(int grid) { return (static_cast<size_t>(3 * grid) * 4 + 15) & ~static_cast<size_t>(15); }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -832,7 +892,7 @@ using namespace gaac;
 
 extern "C" size_t gaac_kv8_attention_workspace(void) {
   const int grid = ka_sms();
-  return ka_counter_bytes(grid) + static_cast<size_t>(2 * grid) * kKaPart * sizeof(float);
+  return ka_counter_bytes(grid) + static_cast<size_t>(4 * grid) * kKaPart * sizeof(float);
 }
 
 extern "C" int gaac_kv8_decode_attention(const gaac_kv8* cache, const void* q, int n_q_heads, int64_t q_seq_stride,
@@ -845,6 +905,8 @@ extern "C" int gaac_kv8_decode_attention(const gaac_kv8* cache, const void* q, i
       q_seq_stride < static_cast<int64_t>(n_q_heads) * kD || (q_seq_stride & 7) || q_seq_stride > (int64_t{1} << 40) ||
       (reinterpret_cast<uintptr_t>(q) & 15u) || (reinterpret_cast<uintptr_t>(out) & 15u) ||
       (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < 16)
+    return GAAC_EINVAL;
+  if (static_cast<int64_t>(cache->batch) * cache->n_kv_heads > 0x7FFFFFFF / (static_cast<int64_t>(cache->max_blocks) + 1))
     return GAAC_EINVAL;
   const int sms = ka_sms();
   if (sms <= 0 || ka_encode() == nullptr) return GAAC_ECUDA;
