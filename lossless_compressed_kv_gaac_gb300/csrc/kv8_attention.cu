@@ -38,24 +38,24 @@ constexpr int kKaStages = 10;                // unit i uses stage i % stages and
 constexpr int kKaHalf = kBlock / 2;          // tokens of an open block's unit
 constexpr int kKaRows = 8;                   // query heads per kv-head in the MMA columns
 constexpr int kKaMinUnits = 4;               // fewer units than this are not worth a CTA
+constexpr unsigned kKaSolo = 16;             // most units of a pair that one group may take alone (at most 32)
 constexpr int kKaStride = kD + 4;            // floats per row of a warp's state in shared memory (bank spread)
-constexpr int kKaQStride = 2 * kD + 8;       // bytes per query row kept for the open block
 constexpr int kKaPart = 3 * kKaRows + kKaRows * kD;  // floats of a partial: m, l, M, O
 constexpr int kKaJoin = 8;                   // partials in flight when they are joined
 constexpr uint32_t kKaFull = 0xFFFFFFFFu;
 static_assert(kKaStages % kKaGroups == 0, "a stage belongs to one group, which waits for all of its phases in turn");
 
 enum { kUnitPage, kUnitOpen, kUnitNone, kUnitEnd };
+enum { kLastAll = 1, kLastSolo = 2 };        // the pair ends for all groups of the CTA; for its one group
 
 struct KaSmem {
   alignas(1024) uint8_t stage[kKaStages][kKv8Pair];
   alignas(128) uint16_t q[kKaStages][kKaRows * kD];
   alignas(16) float state[kKaWarps][kKaRows][kKaStride];
-  alignas(16) uint8_t qraw[kKaRows][kKaQStride];
   alignas(16) int4 meta[kKaStages][2];  // {kind, first of the pair in its group (2: with queries), last, tokens}, {b, h, first CTA, CTAs}
   alignas(16) float2 scale[kKaStages];
   float m[kKaWarps][kKaRows], l[kKaWarps][kKaRows], mv[kKaWarps][kKaRows];
-  uint64_t full[kKaStages], empty[kKaStages], sync;
+  uint64_t full[kKaStages], empty[kKaStages], sync, pair_sync[kKaGroups];
   int last;
 };
 
@@ -254,22 +254,110 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
     u_end = min(u + piece, aligned ? static_cast<unsigned>(s.units) : total);
   }
   const uint64_t policy = ka_evict_first();
+  const uint32_t q_bytes = static_cast<uint32_t>(a.r) * kD * 2;
+  bool ok = true;
+  // One unit of pair (pb, ph) into the ring's next stage; lane 0 starts its copies.  unit: its place in the pair.
+  auto issue = [&](const KaSeq& ps, int pb, int ph, int unit, int32_t page, bool empty, bool first, int last, int cta0, int n_cta) {
+    const bool mine = ring.stage % kKaCopyWarps == copier;
+    if (mine) ok = ka_acquire(sm, ring, a.status);
+    if (mine && lane == 0 && ok) {
+      const int st = ring.stage;
+      uint64_t* full = &sm.full[st];
+      int kind = kUnitNone, n_tok = kBlock;
+      if (empty) {
+      } else if (unit < ps.full) {
+        kind = page >= 0 && page < c.n_pages ? kUnitPage : kUnitNone;
+        if (kind == kUnitNone) report(a.status, GAAC_EFORMAT);
+      } else if (ps.open) {
+        kind = kUnitOpen;
+        n_tok = min(kKaHalf, ps.open - kKaHalf * (unit - ps.full));
+      }
+      const bool with_q = first && !empty;
+      sm.meta[st][0] = make_int4(kind, first ? 1 + with_q : 0, last, n_tok);
+      sm.meta[st][1] = make_int4(pb, ph, cta0, n_cta);
+      const int64_t tile = static_cast<int64_t>(page) * c.heads + ph;
+      if (kind == kUnitPage) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(&sm.scale[st])), "l"(c.scales + 2 * tile) : "memory");
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(full)) : "memory");
+      } else {
+        ka_arrive(full);
+      }
+      mbar_arrive_expect_tx(full, (kind == kUnitNone ? 0 : kKv8Pair) + (with_q ? q_bytes : 0));
+      if (kind == kUnitPage) {
+        ka_tma(sm.stage[st], pages, 0, static_cast<int>(tile * 2 * kBlock), full, policy);
+      } else if (kind == kUnitOpen) {  // K channels 0-63, 64-127, V the same
+        const int y = static_cast<int>((static_cast<int64_t>(pb) * c.heads + ph) * 2 * kBlock) + kKaHalf * (unit - ps.full);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          ka_tma(sm.stage[st] + k * (kKv8Pair / 4), tail, (k & 1) * (kD / 2), y + (k >> 1) * kBlock, full, policy);
+      }
+      if (with_q) bulk_g2s(sm.q[st], a.q + pb * a.q_seq + static_cast<int64_t>(ph) * a.r * kD, q_bytes, full);
+    }
+    ka_next(ring);
+  };
+  auto next_pair = [&]() {  // (b, h), s, seg and u move on
+    seg += s.units;
+    u = seg;
+    if (++h < c.heads) return;
+    h = 0;
+    if (++b >= c.batch) {
+      u_end = u;
+      return;
+    }
+    if (b - b32 >= 32) {
+      b32 += 32;
+      len32 = b32 + lane < c.batch ? c.lens[b32 + lane] : 0;
+    }
+    s = ka_seq(c, __shfl_sync(kKaFull, len32, b - b32));
+  };
   int32_t row32 = 0;  // entries 0-31 of the table row of sequence row_of
   int row_of = -1;
-  bool ok = true;
   while (u < u_end && ok) {
+    if (!aligned && u == seg && s.units <= kKaSolo && u + s.units <= u_end && (s.units <= 2 || u_end - u >= 3 * s.units)) {
+      // ---- short pairs: the next ones of about the same length, up to one for each group, side by side.  Lane k
+      // keeps the k-th; pg[k], lane i: its i-th page.
+      KaSeq ps = {};
+      int pb = 0, ph = 0;
+      int32_t pg[kKaGroups];
+      unsigned most = 0, least = kKaSolo;
+#pragma unroll
+      for (int k = 0; k < kKaGroups; ++k) {
+        pg[k] = 0;
+        if (u < u_end && u + s.units <= u_end && max(most, s.units) <= min(least, s.units) + kKaSolo / 4 && s.units <= kKaSolo) {
+          if (lane < s.full) pg[k] = c.table[static_cast<int64_t>(b) * c.max_blocks + lane];
+          if (lane == k) {
+            ps = s;
+            pb = b;
+            ph = h;
+          }
+          most = max(most, s.units);
+          least = min(least, s.units);
+          next_pair();
+        }
+      }
+#pragma unroll 1
+      for (unsigned i = 0; i < most && ok; ++i) {
+#pragma unroll 1
+        for (int k = 0; k < kKaGroups; ++k) {
+          int32_t page = pg[0];
+#pragma unroll
+          for (int j = 1; j < kKaGroups; ++j) page = k == j ? pg[j] : page;
+          const KaSeq of{__shfl_sync(kKaFull, ps.full, k), __shfl_sync(kKaFull, ps.open, k), __shfl_sync(kKaFull, ps.units, k)};
+          issue(of, __shfl_sync(kKaFull, pb, k), __shfl_sync(kKaFull, ph, k), i, __shfl_sync(kKaFull, page, i), i >= of.units,
+                i == 0, i + 1 == of.units ? kLastSolo : 0, 0, 1);
+        }
+      }
+      continue;
+    }
     const int l0 = static_cast<int>(u - seg);
     const int n = static_cast<int>(min(u_end, seg + s.units) - u);
     const int n_all = max(n, kKaGroups);  // every group takes part in every pair, with an empty unit if need be
     const int cta0 = static_cast<int>(aligned ? blockIdx.x - skipped : seg / piece);
     const int n_cta = static_cast<int>(aligned ? own : (seg + s.units - 1) / piece - cta0 + 1);
-    const uint32_t q_bytes = static_cast<uint32_t>(a.r) * kD * 2;
-    const uint16_t* q = a.q + b * a.q_seq + static_cast<int64_t>(h) * a.r * kD;
     const int32_t* row = c.table + static_cast<int64_t>(b) * c.max_blocks;
     const int n_pages = max(0, min(n, s.full - l0));
     // The row's first entries serve every head of the sequence, and those of the next sequence are fetched early.
-    const bool ahead = l0 == 0 && row_of == b;
-    int32_t pg = 0, pg_next = ahead ? row32 : lane < n_pages ? row[l0 + lane] : 0;
+    int32_t pg = 0, pg_next = l0 == 0 && row_of == b ? row32 : lane < n_pages ? row[l0 + lane] : 0;
     if (l0 == 0) {
       row32 = pg_next;
       row_of = b;
@@ -285,55 +373,9 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
         pg_next = i + 32 + lane < n_pages ? row[l0 + i + 32 + lane] : 0;
       }
       const int32_t page = __shfl_sync(kKaFull, pg, i & 31);
-      const bool mine = kKaCopyWarps == 1 || ring.stage % kKaCopyWarps == copier;
-      if (mine) ok = ka_acquire(sm, ring, a.status);
-      if (mine && lane == 0 && ok) {
-        const bool first = i < kKaGroups, with_q = i < min(n, kKaGroups);
-        const int st = ring.stage;
-        uint64_t* full = &sm.full[st];
-        int kind = kUnitNone, n_tok = kBlock;
-        if (i < n_pages) {
-          kind = page >= 0 && page < c.n_pages ? kUnitPage : kUnitNone;
-          if (kind == kUnitNone) report(a.status, GAAC_EFORMAT);
-        } else if (i < n && s.open) {
-          kind = kUnitOpen;
-          n_tok = min(kKaHalf, s.open - kKaHalf * (l0 + i - s.full));
-        }
-        sm.meta[st][0] = make_int4(kind, first ? 1 + with_q : 0, i >= n_all - kKaGroups, n_tok);
-        sm.meta[st][1] = make_int4(b, h, cta0, n_cta);
-        const int64_t tile = static_cast<int64_t>(page) * c.heads + h;
-        if (kind == kUnitPage) {
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(&sm.scale[st])),
-                       "l"(c.scales + 2 * tile) : "memory");
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(full)) : "memory");
-        } else {
-          ka_arrive(full);
-        }
-        mbar_arrive_expect_tx(full, (kind == kUnitNone ? 0 : kKv8Pair) + (with_q ? q_bytes : 0));
-        if (kind == kUnitPage) {
-          ka_tma(sm.stage[st], pages, 0, static_cast<int>(tile * 2 * kBlock), full, policy);
-        } else if (kind == kUnitOpen) {  // K channels 0-63, 64-127, V the same
-          const int y = static_cast<int>((static_cast<int64_t>(b) * c.heads + h) * 2 * kBlock) + kKaHalf * (l0 + i - s.full);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            ka_tma(sm.stage[st] + k * (kKv8Pair / 4), tail, (k & 1) * (kD / 2), y + (k >> 1) * kBlock, full, policy);
-        }
-        if (with_q) bulk_g2s(sm.q[st], q, q_bytes, full);
-      }
-      ka_next(ring);
+      issue(s, b, h, l0 + i, page, i >= n, i < kKaGroups, i >= n_all - kKaGroups ? kLastAll : 0, cta0, n_cta);
     }
-    // ---- the next pair
-    seg += s.units;
-    u = seg;
-    if (++h == c.heads) {
-      h = 0;
-      if (++b >= c.batch) break;
-      if (b - b32 >= 32) {
-        b32 += 32;
-        len32 = b32 + lane < c.batch ? c.lens[b32 + lane] : 0;
-      }
-      s = ka_seq(c, __shfl_sync(kKaFull, len32, b - b32));
-    }
+    next_pair();
   }
   // No copy may be in flight when the CTA ends, not even where a consumer's wait ran out: the last use of every stage
   // is waited for (bounded) before the end is passed on.
@@ -358,14 +400,15 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
 struct KaSync {
   uint32_t phase = 0;
 };
-// The four compute warps meet.  false: gave up.
-__device__ __forceinline__ bool ka_meet(KaSmem& sm, KaSync& s, int32_t* status) {
+// The compute warps (or the two of a group) meet.  false: gave up.
+__device__ __forceinline__ bool ka_meet_at(uint64_t* bar, KaSync& s, int32_t* status) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) ka_arrive(&sm.sync);
-  const bool ok = ka_wait(&sm.sync, s.phase, status);
+  if ((threadIdx.x & 31) == 0) ka_arrive(bar);
+  const bool ok = ka_wait(bar, s.phase, status);
   s.phase ^= 1u;
   return ok;
 }
+__device__ __forceinline__ bool ka_meet(KaSmem& sm, KaSync& s, int32_t* status) { return ka_meet_at(&sm.sync, s, status); }
 
 __device__ __forceinline__ float ka_finite(float m) { return m == -INFINITY ? 0.f : m; }
 
@@ -519,7 +562,7 @@ template <bool HALF, int FMT>
 __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, tq = lane & 3;
   const int warp = tid >> 5, part = warp & 1;  // part: which half of a unit's tokens
-  KaSync meet;
+  KaSync meet, meet_pair;
   int stage = warp >> 1;
   uint32_t phase = 0;
   uint32_t qf[8][2];       // q^T operand: row g, channels 16 j + 4 tq .. + 3 of k-step j
@@ -559,7 +602,6 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
         uint2 x = make_uint2(0u, 0u);
         if (g < a.r) x = *reinterpret_cast<const uint2*>(qs + g * kD + 16 * j + 4 * tq);
         w[j][0] = x.x, w[j][1] = x.y;
-        *reinterpret_cast<uint2*>(sm.qraw[g] + 2 * (16 * j + 4 * tq)) = x;  // every warp writes the same, and reads its own
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t mag = w[j][i] & 0x7FFF7FFFu;
@@ -635,16 +677,22 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
           const uint32_t at = (j >> 2) * (kKv8Pair / 4) + row * 128u + ((chunk ^ (row & 7u)) << 4) + 8u * (tq & 1);
           const uint2 x0 = *reinterpret_cast<const uint2*>(sm.stage[stage] + at);
           const uint2 x1 = *reinterpret_cast<const uint2*>(sm.stage[stage] + at + 8 * 128);
-          const uint2 qw = *reinterpret_cast<const uint2*>(sm.qraw[g] + 2 * (16 * j + 4 * tq));
           const uint32_t aw[4] = {x0.x, x1.x, x0.y, x1.y};
-          if (HALF)
-            ka_mma_f16(d, aw, qw.x, qw.y);
-          else
-            mma_bf16(d, aw[0], aw[1], aw[2], aw[3], qw.x, qw.y);
+          if (HALF) {
+            ka_mma_f16(d, aw, qf[j][0], qf[j][1]);
+          } else {  // the scaled query as bf16 again (exact), its largest magnitude in [1, 2)
+            uint32_t qb[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float2 f = kv8_pair<true>(qf[j][i]);
+              qb[i] = ka_pack_bf16(f.x * 0x1p-14f, f.y * 0x1p-14f);
+            }
+            mma_bf16(d, aw[0], aw[1], aw[2], aw[3], qb[0], qb[1]);
+          }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (16 * part + g + 8 * (i >> 1) < meta.w) s[0][i] = d[i] * a.c_log2;
+          if (16 * part + g + 8 * (i >> 1) < meta.w) s[0][i] = d[i] * (HALF ? qc[i & 1] : qc[i & 1] * 0x1p14f);
       }
 
       // ---- softmax state
@@ -743,6 +791,7 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
 
     // ---- the end of the pair in this CTA
     if (last) {
+      const bool solo = last == kLastSolo;
       const int4 pair = sm.meta[stage][1];
       const int b = pair.x, h = pair.y, cta0 = pair.z, n_cta = pair.w;
 #pragma unroll
@@ -763,37 +812,33 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
         *reinterpret_cast<float2*>(&sm.state[warp][2 * tq][16 * i + 2 * g]) = make_float2(acc[i][0], acc[i][2]);
         *reinterpret_cast<float2*>(&sm.state[warp][2 * tq + 1][16 * i + 2 * g]) = make_float2(acc[i][1], acc[i][3]);
       }
-      if (!ka_meet(sm, meet, a.status)) return;
-      const bool whole = n_cta == 1;
-      float* mine = a.part + ka_slot(blockIdx.x, cta0) * kKaPart;
-      {
-        static_assert(kKaRows * kD / 4 <= kKaCompute, "at most one float4 of the result for each thread");
-        const int row = tid / (kD / 4), ch = 4 * (tid % (kD / 4));
-        if (row < a.r) {
-          float mx = -INFINITY, vx = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < kKaWarps; ++w) {
-            mx = fmaxf(mx, sm.m[w][row]);
-            vx = fmaxf(vx, sm.mv[w][row]);
-          }
-          float den = 0.f;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < kKaWarps; ++w) {
-            den += ka_exp2(sm.m[w][row] - ka_finite(mx)) * sm.l[w][row];
-            const float f = ka_exp2(sm.mv[w][row] - ka_finite(vx));
-            const float4 x = *reinterpret_cast<const float4*>(&sm.state[w][row][ch]);
-            o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
-          }
-          if (whole)
-            ka_store<HALF>(a, b, h, row, ch, ka_result(o, mx, den, vx));
-          else
-            ka_put(mine, row, ch, mx, den, vx, o);
+      if (!(solo ? ka_meet_at(&sm.pair_sync[warp >> 1], meet_pair, a.status) : ka_meet(sm, meet, a.status))) return;
+      // this CTA's part of the pair: the states of all warps, or of the group's two
+      const int w0 = solo ? warp & ~1 : 0, w1 = solo ? w0 + 2 : kKaWarps;
+      for (int at = solo ? tid & 63 : tid; at < a.r * (kD / 4); at += solo ? 64 : kKaCompute) {
+        const int row = at / (kD / 4), ch = 4 * (at % (kD / 4));
+        float mx = -INFINITY, vx = -INFINITY, den = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int w = w0; w < w1; ++w) {
+          mx = fmaxf(mx, sm.m[w][row]);
+          vx = fmaxf(vx, sm.mv[w][row]);
         }
+#pragma unroll 2
+        for (int w = w0; w < w1; ++w) {
+          den += ka_exp2(sm.m[w][row] - ka_finite(mx)) * sm.l[w][row];
+          const float f = ka_exp2(sm.mv[w][row] - ka_finite(vx));
+          const float4 x = *reinterpret_cast<const float4*>(&sm.state[w][row][ch]);
+          o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+        }
+        if (n_cta == 1)
+          ka_store<HALF>(a, b, h, row, ch, ka_result(o, mx, den, vx));
+        else
+          ka_put(a.part + ka_slot(blockIdx.x, cta0) * kKaPart, row, ch, mx, den, vx, o);
       }
-      if (!whole && !ka_join<HALF>(a, sm, b, h, cta0, n_cta, meet)) return;
+      if (n_cta != 1 && !ka_join<HALF>(a, sm, b, h, cta0, n_cta, meet)) return;
       // the next pair's state may be written once everybody has read this one's
-      if (!ka_meet(sm, meet, a.status)) return;
+      if (!(solo ? ka_meet_at(&sm.pair_sync[warp >> 1], meet_pair, a.status) : ka_meet(sm, meet, a.status))) return;
     }
     __syncwarp();
     if (lane == 0) ka_arrive(&sm.empty[stage]);
@@ -816,6 +861,7 @@ __global__ void __launch_bounds__(kKaThreads, 1)
       mbar_init(&sm.empty[i], 2);
     }
     mbar_init(&sm.sync, kKaWarps);
+    for (int i = 0; i < kKaGroups; ++i) mbar_init(&sm.pair_sync[i], 2);
     fence_mbar_init();
     asm volatile("prefetch.tensormap [%0];" ::"l"(&pages) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&tail) : "memory");
