@@ -38,10 +38,10 @@ constexpr int kKaStages = 10;                // unit i uses stage i % stages and
 constexpr int kKaHalf = kBlock / 2;          // tokens of an open block's unit
 constexpr int kKaRows = 8;                   // query heads per kv-head in the MMA columns
 constexpr int kKaMinUnits = 4;               // fewer units than this are not worth a CTA
-constexpr unsigned kKaSolo = 16;             // most units of a pair that one group may take alone (at most 32)
+constexpr unsigned kKaSolo = 20;             // most units of a pair that one group may take alone (at most 32)
 constexpr int kKaStride = kD + 4;            // floats per row of a warp's state in shared memory (bank spread)
 constexpr int kKaPart = 3 * kKaRows + kKaRows * kD;  // floats of a partial: m, l, M, O
-constexpr int kKaJoin = 8;                   // partials in flight when they are joined
+constexpr int kKaJoin = 10;                  // partials in flight when they are joined
 constexpr uint32_t kKaFull = 0xFFFFFFFFu;
 static_assert(kKaStages % kKaGroups == 0, "a stage belongs to one group, which waits for all of its phases in turn");
 
@@ -313,9 +313,10 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
   int32_t row32 = 0;  // entries 0-31 of the table row of sequence row_of
   int row_of = -1;
   while (u < u_end && ok) {
-    if (!aligned && u == seg && s.units <= kKaSolo && u + s.units <= u_end && (s.units <= 2 || u_end - u >= 3 * s.units)) {
-      // ---- short pairs: the next ones of about the same length, up to one for each group, side by side.  Lane k
-      // keeps the k-th; pg[k], lane i: its i-th page.
+    if (!aligned && u == seg && s.units <= kKaSolo && u + s.units <= u_end &&
+        (s.units <= 4 || (h + 3 <= c.heads && u_end - u >= 3 * s.units))) {
+      // ---- short pairs: the next ones of about the same length, up to one for each group, side by side (three at
+      // least, or few units).  Lane k keeps the k-th; pg[k], lane i: its i-th page.
       KaSeq ps = {};
       int pb = 0, ph = 0;
       int32_t pg[kKaGroups];
@@ -323,7 +324,7 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
 #pragma unroll
       for (int k = 0; k < kKaGroups; ++k) {
         pg[k] = 0;
-        if (u < u_end && u + s.units <= u_end && max(most, s.units) <= min(least, s.units) + kKaSolo / 4 && s.units <= kKaSolo) {
+        if (u < u_end && u + s.units <= u_end && s.units <= kKaSolo && 4 * max(most, s.units) <= 5 * min(least, s.units) + 4) {
           if (lane < s.full) pg[k] = c.table[static_cast<int64_t>(b) * c.max_blocks + lane];
           if (lane == k) {
             ps = s;
