@@ -6,6 +6,8 @@
 // rows; nothing ever has to be copied on a write.
 //
 // All of it is bound by latency but the moves of a compaction, which are bound by memory.
+#include <algorithm>
+
 #include "kv8.cuh"
 
 namespace gaac {
@@ -370,6 +372,7 @@ __global__ void __launch_bounds__(kPgThreads) kv8_compact_list_kernel(Kv8Dev c, 
 
 constexpr int kMvThreads = 256;
 constexpr int kMvCtasPerSm = 8;
+constexpr int kMvMost = 152 * 64;
 
 // A CTA copies one (page, kv-head) at a time, 16 KB with four 16-byte loads a thread in flight; where the next one
 // lies is fetched meanwhile.
@@ -393,7 +396,7 @@ __global__ void __launch_bounds__(kMvThreads, kMvCtasPerSm) kv8_compact_move_ker
     uint4* d = reinterpret_cast<uint4*>(c.pages + (to * c.heads + h) * kKv8Pair);
     uint4 x[kKv8Pair / 16 / kMvThreads];
 #pragma unroll
-    for (int i = 0; i < kKv8Pair / 16 / kMvThreads; ++i) x[i] = s[tid + kMvThreads * i];
+    for (int i = 0; i < kKv8Pair / 16 / kMvThreads; ++i) x[i] = __ldcs(s + tid + kMvThreads * i);
     const unsigned next = it + gridDim.x;
     int64_t from2 = 0, to2 = 0;
     if (next < items) {
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(kMvThreads, kMvCtasPerSm) kv8_compact_move_ker
       }
     }
 #pragma unroll
-    for (int i = 0; i < kKv8Pair / 16 / kMvThreads; ++i) d[tid + kMvThreads * i] = x[i];
+    for (int i = 0; i < kKv8Pair / 16 / kMvThreads; ++i) __stcs(d + tid + kMvThreads * i, x[i]);
     it = next;
     from = from2;
     to = to2;
@@ -464,6 +467,9 @@ extern "C" int gaac_kv8_compact(const gaac_kv8* cache, int32_t* moved_to, void* 
     e = kv8_launch(kv8_compact_count_kernel, dim3(chunks), kPgThreads, 0, stream, c);
     if (e == GAAC_OK) e = kv8_launch(kv8_compact_list_kernel<false>, dim3(chunks), kPgThreads, 0, stream, c, moved_to);
   }
-  if (e == GAAC_OK) e = kv8_launch(kv8_compact_move_kernel, dim3(152 * kMvCtasPerSm), kMvThreads, 0, stream, c, moved_to);
+  // At most half the pages move: a CTA for each (page, kv-head) of those, up to kMvMost.
+  const int64_t most = (c.n_pages / 2 + 1) * c.heads;
+  if (e == GAAC_OK)
+    e = kv8_launch(kv8_compact_move_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(most, kMvMost))), kMvThreads, 0, stream, c, moved_to);
   return e;
 }
