@@ -9,11 +9,11 @@
 // the numbers themselves, however its tokens arrive.  NaN stays NaN; an infinity stays one in E5M2 and becomes
 // NaN in E4M3, which has none.
 //
-// Memory bound: 2 bytes read and 1 written per number.  A CTA takes a run of consecutive blocks of one kv-head, K and
-// V together: 512 threads hold a block's 32 KB in registers and have the next block's loads in flight while they
-// quantise it, so the reads never pause and what the run's sequence and pages are is looked up once.  Runs are one
-// block long where there are few (latency), longer where every SM has several.  The first block's CTA also
-// writes the new open block's rows, after it has read the old ones from the same tail.
+// Memory bound: 2 bytes read and 1 written per number.  A CTA takes a run of consecutive blocks of K or of V of one
+// kv-head: 128 threads hold a block's 16 KB in registers and have the next block's loads in flight while they
+// quantise it, so the reads never pause, few warps wait at a block's one barrier, and what the run's sequence and pages
+// are is looked up once.  Runs are one block long where there are few (latency), longer where every SM has several.
+// The first block's CTA also writes the new open block's rows, after it has read the old ones from the same tail.
 #include <algorithm>
 
 #include "kv8.cuh"
@@ -31,9 +31,11 @@ struct Kv8AppendArgs {
   int32_t* status;
 };
 
-constexpr int kApThreads = 512;
-constexpr int kApRows = kBlock * 16 / kApThreads;  // 16-byte vectors of a thread in each of K and V
-constexpr int kApCtasPerSm = 2;
+constexpr int kApThreads = 128;
+constexpr int kApWarps = kApThreads / 32;
+constexpr int kApStep = kApThreads / 16;           // rows that the CTA covers with one 16-byte vector a thread
+constexpr int kApRows = kBlock / kApStep;          // vectors of a thread in a block
+constexpr int kApCtasPerSm = 5;
 
 template <int FMT>
 __device__ __forceinline__ uint32_t to_fp8x2(float lo, float hi) {
@@ -53,134 +55,104 @@ __device__ __forceinline__ uint32_t to_fp8_any(float x) {
   return to_fp8x2<FMT>(x, 0.f) & 0xFFu;
 }
 
-// The scale's exponent for the largest magnitude `bits` (a 16-bit number of the model's type).
+// The scale's exponent for the largest magnitude `bits` (a 16-bit number of the model's type).  A bf16 subnormal's
+// exponent comes out too large by its leading zeros, but any such block takes the smallest scale.
 template <bool HALF, int FMT>
 __device__ __forceinline__ int scale_exponent(uint32_t bits) {
-  const float a = kv8_pair<HALF>(bits).x;
-  if (a == 0.f) return 0;
-  // a * 2^64 is a normal number whatever a is (the smallest bf16 is 2^-133); exact, and below 2^128 for a < 2^64
-  const bool small = a < 0x1p-100f;
-  const uint32_t f = __float_as_uint(small ? a * 0x1p64f : a);
-  const int e = static_cast<int>(f >> 23) - 127 - (small ? 64 : 0);
-  const int top = FMT == GAAC_FP8_E4M3 ? 8 : 15;
-  return max(e - top + ((f & 0x7FFFFFu) > 0x600000u ? 1 : 0), -126);
+  constexpr int kTop = FMT == GAAC_FP8_E4M3 ? 8 : 15;
+  const uint32_t f = __float_as_uint(kv8_pair<HALF>(bits).x);
+  const int e = max(static_cast<int>(f >> 23) - 127 - kTop + ((f & 0x7FFFFFu) > 0x600000u ? 1 : 0), -126);
+  return bits == 0u ? 0 : e;
 }
 
 // A thread's part of a block that fills: channels c8 .. c8 + 7 of kApRows rows, and the block's page.
 struct ApBlock {
-  uint4 w[2][kApRows];
+  uint4 w[kApRows];
   int32_t page;
 };
 
-// A block of new tokens only: k, v at this thread's first row of it.
-__device__ __forceinline__ void ap_load(ApBlock& x, const uint16_t* k, const uint16_t* v, int64_t k_tok, int64_t v_tok) {
-#pragma unroll
-  for (int i = 0; i < kApRows; ++i) {
-    x.w[0][i] = *reinterpret_cast<const uint4*>(k + kApThreads / 16 * i * k_tok);
-    x.w[1][i] = *reinterpret_cast<const uint4*>(v + kApThreads / 16 * i * v_tok);
-  }
-}
-
-// A block that opened before this call: its first `old` tokens are in the tail.
-__device__ __forceinline__ void ap_load_open(ApBlock& x, const uint16_t* tail, int old, const uint16_t* k, const uint16_t* v,
-                                             int64_t k_tok, int64_t v_tok, int t0) {
-#pragma unroll
-  for (int i = 0; i < kApRows; ++i) {
-    const int t = t0 + kApThreads / 16 * i;
-    const bool in_tail = t < old;
-    x.w[0][i] = *reinterpret_cast<const uint4*>(in_tail ? tail + t * kD : k + (t - t0) * k_tok);
-    x.w[1][i] = *reinterpret_cast<const uint4*>(in_tail ? tail + kKv8Tile + t * kD : v + (t - t0) * v_tok);
-  }
-}
-
-// The block's largest magnitudes as 16-bit patterns, whose order is the numbers': K's in the low half of the result,
-// V's in the high one.  FINITE leaves out infinities and NaN, which are otherwise the largest.  One barrier.
+// The block's largest magnitude as a 16-bit pattern, whose order is the numbers'.  FINITE leaves out infinities and
+// NaN, which are otherwise the largest.  One barrier.
 template <bool HALF, bool FINITE>
 __device__ __forceinline__ uint32_t ap_largest(const ApBlock& x, uint32_t* sh) {
   const int tid = threadIdx.x;
-  uint32_t mx = 0;
+  uint32_t m = 0;
 #pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {
-    uint32_t m = 0;
+  for (int i = 0; i < kApRows; ++i) {
+    const uint32_t w[4] = {x.w[i].x, x.w[i].y, x.w[i].z, x.w[i].w};
 #pragma unroll
-    for (int i = 0; i < kApRows; ++i) {
-      const uint32_t w[4] = {x.w[kind][i].x, x.w[kind][i].y, x.w[kind][i].z, x.w[kind][i].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t mag = w[q] & 0x7FFF7FFFu;
-        m = __vmaxu2(m, FINITE ? mag & ~__vcmpgeu2(mag, HALF ? 0x7C007C00u : 0x7F807F80u) : mag);
-      }
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t mag = w[q] & 0x7FFF7FFFu;
+      m = __vmaxu2(m, FINITE ? mag & ~__vcmpgeu2(mag, HALF ? 0x7C007C00u : 0x7F807F80u) : mag);
     }
-    m = max(m & 0xFFFFu, m >> 16);
-    mx |= m << (16 * kind);
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-  if ((tid & 31) == 0) sh[tid >> 5] = mx;
+  m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+  if ((tid & 31) == 0) sh[tid >> 5] = m;
   __syncthreads();
-  mx = sh[tid & (kApThreads / 32 - 1)];
 #pragma unroll
-  for (int d = kApThreads / 64; d > 0; d >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-  return mx;
+  for (int i = 0; i < kApWarps; ++i) m = max(m, sh[i]);
+  return m;
 }
 
 // Four numbers of the model's type times `inv`, as FP8.
 template <bool HALF, int FMT>
 __device__ __forceinline__ uint32_t ap_four(uint32_t w0, uint32_t w1, float inv) {
   const float2 a = kv8_pair<HALF>(w0), b = kv8_pair<HALF>(w1);
-  float r[4];
-  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
-      : "=f"(r[0]), "=f"(r[1]) : "f"(a.x), "f"(a.y), "f"(inv));
-  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
-      : "=f"(r[2]), "=f"(r[3]) : "f"(b.x), "f"(b.y), "f"(inv));
-  return to_fp8x2<FMT>(r[0], r[1]) | to_fp8x2<FMT>(r[2], r[3]) << 16;
+  uint32_t r;
+#define GAAC_AP_FOUR(FP8X2)                                                                                       \
+  asm("{\n .reg .b64 x, y, f;\n .reg .f32 x0, x1, y0, y1;\n .reg .b16 lo, hi;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n" \
+      " mov.b64 f, {%5, %5};\n mul.rn.f32x2 x, x, f;\n mul.rn.f32x2 y, y, f;\n mov.b64 {x0, x1}, x;\n mov.b64 {y0, y1}, y;\n" \
+      " cvt.rn.satfinite." FP8X2 ".f32 lo, x1, x0;\n cvt.rn.satfinite." FP8X2 ".f32 hi, y1, y0;\n mov.b32 %0, {lo, hi};\n}"     \
+      : "=r"(r) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(inv))
+  if (FMT == GAAC_FP8_E4M3)
+    GAAC_AP_FOUR("e4m3x2");
+  else
+    GAAC_AP_FOUR("e5m2x2");
+#undef GAAC_AP_FOUR
+  return r;
 }
 
-// Quantises the block into its page.  sh: two sets of the warps' maxima; a barrier at least, behind which the old
-// rows of the tail have been read.
+// Quantises the block into its page: tile = 2 (page, kv-head) + (K|V), dst = this thread's first number of it.  sh: two
+// sets of the warps' maxima; a barrier at least, behind which the old rows of the tail have been read.
 template <bool HALF, int FMT>
-__device__ __forceinline__ void ap_seal(const ApBlock& x, const Kv8Dev& c, int h, int t0, int c8, uint32_t (*sh)[kApThreads / 32]) {
+__device__ __forceinline__ void ap_seal(const ApBlock& x, uint8_t* dst, float* scale, uint32_t (*sh)[kApWarps]) {
   constexpr uint32_t kInf = HALF ? 0x7C00u : 0x7F80u;
-  const int tid = threadIdx.x;
   uint32_t mx = ap_largest<HALF, false>(x, sh[0]);
-  const bool odd = (mx & 0xFFFFu) >= kInf || (mx >> 16) >= kInf;  // the same for the whole CTA
+  const bool odd = mx >= kInf;  // the same for the whole CTA
   if (odd) mx = ap_largest<HALF, true>(x, sh[1]);
-  const int64_t tile = static_cast<int64_t>(x.page) * c.heads + h;
-  uint8_t* dst = c.pages + tile * kKv8Pair + t0 * kD + c8;
+  const int e = scale_exponent<HALF, FMT>(mx);
+  const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  if (!odd) {
 #pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {
-    const int e = scale_exponent<HALF, FMT>((mx >> (16 * kind)) & 0xFFFFu);
-    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    for (int i = 0; i < kApRows; ++i)
+      *reinterpret_cast<uint2*>(dst + i * kApStep * kD) =
+          make_uint2(ap_four<HALF, FMT>(x.w[i].x, x.w[i].y, inv), ap_four<HALF, FMT>(x.w[i].z, x.w[i].w, inv));
+  } else {
 #pragma unroll
     for (int i = 0; i < kApRows; ++i) {
-      const uint4 w = x.w[kind][i];
-      uint2 o;
-      if (!odd) {
-        o = make_uint2(ap_four<HALF, FMT>(w.x, w.y, inv), ap_four<HALF, FMT>(w.z, w.w, inv));
-      } else {
-        o = make_uint2(0u, 0u);
+      const uint4 w = x.w[i];
+      uint2 o = make_uint2(0u, 0u);
 #pragma unroll 1
-        for (int q = 0; q < 8; ++q) {
-          const float2 f = kv8_pair<HALF>(q < 2 ? w.x : q < 4 ? w.y : q < 6 ? w.z : w.w);
-          const uint32_t y = to_fp8_any<FMT>((q & 1 ? f.y : f.x) * inv) << (8 * (q & 3));
-          if (q < 4) o.x |= y; else o.y |= y;
-        }
+      for (int q = 0; q < 8; ++q) {
+        const float2 f = kv8_pair<HALF>(q < 2 ? w.x : q < 4 ? w.y : q < 6 ? w.z : w.w);
+        const uint32_t y = to_fp8_any<FMT>((q & 1 ? f.y : f.x) * inv) << (8 * (q & 3));
+        if (q < 4) o.x |= y; else o.y |= y;
       }
-      *reinterpret_cast<uint2*>(dst + kind * kKv8Tile + kApThreads / 16 * i * kD) = o;
+      *reinterpret_cast<uint2*>(dst + i * kApStep * kD) = o;
     }
-    if (tid == 0) c.scales[tile * 2 + kind] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
   }
+  if (threadIdx.x == 0) *scale = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
 template <bool HALF, int FMT>
 __global__ void __launch_bounds__(kApThreads, kApCtasPerSm) kv8_append_kernel(const Kv8AppendArgs a) {
-  __shared__ uint32_t sh_max[2][2][kApThreads / 32];  // of a block and the next
+  __shared__ uint32_t sh_max[2][2][kApWarps];  // of a block and the next
   dependent_wait();
   dependent_launch();
   const Kv8Dev& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31;
-  const int h = static_cast<int>(blockIdx.x % c.heads);
-  const int64_t place = blockIdx.x / c.heads;
+  const int hk = static_cast<int>(blockIdx.x % (2 * c.heads)), h = hk >> 1, kind = hk & 1;
+  const int64_t place = blockIdx.x / (2 * c.heads);
   // ---- the sequence and the run of this CTA
   // With R blocks in a run, sequence b owns places [cu[b]/64R + 2b, cu[b+1]/64R + 2b + 2): at least as many as its
   // tokens can touch, wherever its open block ends.  Every warp looks it up for itself.
@@ -226,22 +198,28 @@ __global__ void __launch_bounds__(kApThreads, kApCtasPerSm) kv8_append_kernel(co
   const int blk0 = fits ? len / kBlock : 0, blk1 = fits ? static_cast<int>(now / kBlock) : 0;  // blocks [blk0, blk1) fill
   const int32_t* row = c.table + static_cast<int64_t>(b) * c.max_blocks;
   const int t0 = tid >> 4, c8 = 8 * (tid & 15);
-  uint16_t* tail = c.tail + (static_cast<int64_t>(b) * c.heads + h) * kKv8Pair + c8;
-  const uint16_t* src[2] = {a.k + h * kD + c8, a.v + h * kD + c8};
-  const int64_t step[2] = {a.k_tok, a.v_tok};
+  uint16_t* tail = c.tail + (static_cast<int64_t>(b) * 2 * c.heads + hk) * kKv8Tile + c8;
+  const uint16_t* src = (kind == 0 ? a.k : a.v) + h * kD + c8;
+  const int64_t step = kind == 0 ? a.k_tok : a.v_tok;
   const int blk_begin = blk0 + j, blk_end = min(blk_begin + a.run, blk1);
   // this thread's first row of the run's next block that is loaded
-  const int64_t at0 = first + static_cast<int64_t>(blk_begin) * kBlock + t0 - len;
-  const uint16_t* k = src[0] + at0 * step[0];
-  const uint16_t* v = src[1] + at0 * step[1];
+  const uint16_t* at = src + (first + static_cast<int64_t>(blk_begin) * kBlock + t0 - len) * step;
   auto load = [&](ApBlock& x, int blk) {
-    if (blk * kBlock < len)
-      ap_load_open(x, tail, len - blk * kBlock, k, v, a.k_tok, a.v_tok, t0);
-    else
-      ap_load(x, k, v, a.k_tok, a.v_tok);
+    const int old = len - blk * kBlock;  // a block that opened before this call: its first tokens are in the tail
+    if (old > 0) {
+#pragma unroll
+      for (int i = 0; i < kApRows; ++i)
+        x.w[i] = *reinterpret_cast<const uint4*>(t0 + kApStep * i < old ? tail + (t0 + kApStep * i) * kD : at + kApStep * i * step);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kApRows; ++i) x.w[i] = *reinterpret_cast<const uint4*>(at + kApStep * i * step);
+    }
     x.page = row[blk];
-    k += kBlock * a.k_tok;
-    v += kBlock * a.v_tok;
+    at += kBlock * step;
+  };
+  auto seal = [&](const ApBlock& x, uint32_t (*sh)[kApWarps]) {
+    const int64_t tile = static_cast<int64_t>(x.page) * 2 * c.heads + hk;
+    ap_seal<HALF, FMT>(x, c.pages + tile * kKv8Tile + t0 * kD + c8, c.scales + tile, sh);
   };
   ApBlock x, y;
   if (blk_begin < blk_end) load(x, blk_begin);  // under way while the pages are checked
@@ -256,28 +234,24 @@ __global__ void __launch_bounds__(kApThreads, kApCtasPerSm) kv8_append_kernel(co
   } else if (n > 0) {
     for (int blk = blk_begin; blk < blk_end; blk += 2) {
       if (blk + 1 < blk_end) load(y, blk + 1);
-      ap_seal<HALF, FMT>(x, c, h, t0, c8, sh_max[0]);
+      seal(x, sh_max[0]);
       if (blk + 1 < blk_end) {
         if (blk + 2 < blk_end) load(x, blk + 2);
-        ap_seal<HALF, FMT>(y, c, h, t0, c8, sh_max[1]);
+        seal(y, sh_max[1]);
       }
     }
     // the rows of the new open block
     if (j == 0) {
       const int64_t open = static_cast<int64_t>(blk1) * kBlock;
-#pragma unroll
-      for (int kind = 0; kind < 2; ++kind)
-        for (int t = t0; t < now - open; t += kApThreads / 16) {
-          const int64_t at = open + t - len;
-          if (at >= 0)
-            *reinterpret_cast<uint4*>(tail + kind * kKv8Tile + t * kD) =
-                *reinterpret_cast<const uint4*>(src[kind] + (first + at) * step[kind]);
-        }
+      for (int t = t0; t < now - open; t += kApStep) {
+        const int64_t i = open + t - len;  // among the new tokens
+        if (i >= 0) *reinterpret_cast<uint4*>(tail + t * kD) = *reinterpret_cast<const uint4*>(src + (first + i) * step);
+      }
     }
   }
   // ---- the length advances once every CTA of the sequence has read it
   if (tid == 0) {
-    const unsigned int all = static_cast<unsigned int>(span) * c.heads;
+    const unsigned int all = static_cast<unsigned int>(span) * 2 * c.heads;
     if (kv8_atomic_add_acq_rel(c.work + b, 1u) == all - 1) {
       c.work[b] = 0;
       if (!fault) c.lens[b] = static_cast<int32_t>(now);
@@ -305,14 +279,14 @@ extern "C" int gaac_kv8_append(const gaac_kv8* cache, const void* k, const void*
       (reinterpret_cast<uintptr_t>(cu_tokens) & 3u) || k_tok_stride < width || v_tok_stride < width ||
       (k_tok_stride & 7) || (v_tok_stride & 7) || k_tok_stride > (int64_t{1} << 40) || v_tok_stride > (int64_t{1} << 40))
     return GAAC_EINVAL;
-  // Blocks of a run: one while the blocks leave an SM with fewer than eight, at most sixteen.
-  const int64_t blocks = n_tokens / kBlock * cache->n_kv_heads;
-  const int run = cu_tokens == nullptr ? 1 : static_cast<int>(std::min<int64_t>(16, std::max<int64_t>(1, blocks / (152 * 8))));
+  // Blocks of a run: one while the blocks leave an SM with fewer than sixteen, at most sixteen.
+  const int64_t blocks = n_tokens / kBlock * cache->n_kv_heads * 2;
+  const int run = cu_tokens == nullptr ? 1 : static_cast<int>(std::min<int64_t>(16, std::max<int64_t>(1, blocks / (152 * 16))));
   const int64_t places = cu_tokens == nullptr ? cache->batch : n_tokens / (kBlock * run) + 2 * static_cast<int64_t>(cache->batch);
-  if (places * cache->n_kv_heads > 0x7FFFFFFF) return GAAC_EINVAL;
+  if (places * cache->n_kv_heads > 0x3FFFFFFF) return GAAC_EINVAL;
   const Kv8AppendArgs a{kv8_dev(cache), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_tok_stride,
                         v_tok_stride, cu_tokens, n_tokens, run, d_status};
-  const dim3 grid(static_cast<unsigned>(places * cache->n_kv_heads));
+  const dim3 grid(static_cast<unsigned>(places * 2 * cache->n_kv_heads));
   if (cache->dtype == GAAC_BF16)
     return cache->fmt == GAAC_FP8_E4M3 ? kv8_launch(kv8_append_kernel<false, GAAC_FP8_E4M3>, grid, kApThreads, 0, stream, a)
                                        : kv8_launch(kv8_append_kernel<false, GAAC_FP8_E5M2>, grid, kApThreads, 0, stream, a);
