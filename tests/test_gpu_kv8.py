@@ -189,6 +189,27 @@ def test_append_refused_on_the_device():
     assert torch.equal(c.tail[3, :, 0, :10].transpose(0, 1), k[20:30])
 
 
+def test_append_many_and_long():
+    """More sequences than a warp looks up at once, and runs of many blocks."""
+    lens = [(53 * i) % 200 for i in range(700)]
+    c, k, v = filled(lens, 1)
+    at = torch.cumsum(torch.tensor([0] + lens), 0).tolist()
+    check_blocks(c, {b: torch.stack([k[at[b]:at[b + 1]], v[at[b]:at[b + 1]]]) for b in (0, 1, 31, 32, 33, 255, 256, 699)})
+    c, k, v = filled([30011, 63, 20000], 4, E5, F16)
+    check_blocks(c, {0: torch.stack([k[:30011], v[:30011]]), 1: torch.stack([k[30011:30074], v[30011:30074]]),
+                     2: torch.stack([k[30074:], v[30074:]])})
+    # chunks of many blocks behind open ones
+    n = [9000, 1, 7777]
+    k2, v2 = kv_of(sum(n), 4, F16, 60)
+    d = Kv8Cache(c.n_pages + 300, 3, 4, c.max_blocks + 160, E5, F16)
+    d.append(k, v, cu_of([30011, 63, 20000]))
+    d.append(k2, v2, cu_of(n))
+    assert ok(d) == 0
+    check_blocks(d, {0: torch.stack([torch.cat([k[:30011], k2[:9000]]), torch.cat([v[:30011], v2[:9000]])]),
+                     1: torch.stack([torch.cat([k[30011:30074], k2[9000:9001]]), torch.cat([v[30011:30074], v2[9000:9001]])]),
+                     2: torch.stack([torch.cat([k[30074:], k2[9001:]]), torch.cat([v[30074:], v2[9001:]])])})
+
+
 def test_append_empty_chunk():
     c, _, _ = filled([3, 64], 1)
     e = torch.empty((0, 1, 128), dtype=BF16, device="cuda")
@@ -223,6 +244,23 @@ def test_attention_many_short_sequences():
     q = rand((300, 16, 128), BF16, 5)
     U.check_attention(c, q, SCALE, c.attention(q, SCALE))
     assert ok(c) == 0
+
+
+@pytest.mark.parametrize("lens,heads,group", [
+    ([70000], 1, 1), ([70000], 1, 3), ([40000, 39999], 1, 8),  # shared by most of the GPU: joined in teams
+    ([100000] + [10] * 200, 1, 8), ([5] * 100 + [60001] + [130] * 100, 1, 5),  # the same among short ones
+    ([64 * (i % 25) + 17 * (i % 3) for i in range(90)], 5, 2),  # up to 25 blocks, several heads side by side
+    ([1] * 64, 8, 4), ([0] * 200, 2, 1), ([33] * 160 + [2000], 2, 8), ([1300] * 60, 3, 4), ([129, 0, 1] * 40, 16, 1)])
+def test_attention_cuts(lens, heads, group):
+    """Every way the blocks are cut over the GPU; twice the same bits."""
+    c, _, _ = filled(lens, heads)
+    q = rand((len(lens), heads * group, 128), BF16, 5)
+    a = c.attention(q, SCALE)
+    U.check_attention(c, q, SCALE, a)
+    b = c.attention(q, SCALE)
+    assert torch.equal(a, b) and ok(c) == 0
+    assert all((a[i] == 0).all() for i, n in enumerate(lens) if n == 0)
+    assert (c._ws[:3 * 152 * 4].view(torch.int32) == 0).all()  # counters are back at zero
 
 
 def test_attention_scales_far_apart():

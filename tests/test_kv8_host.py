@@ -71,6 +71,11 @@ def test_attention_refusals(lib):
         assert f(cache(), *args, None, None) == EINVAL, args
 
 
+def test_attention_refuses_more_blocks_than_it_counts(lib):
+    big = cache(batch=60000, n_kv_heads=16, max_blocks=3000, n_pages=64)
+    assert lib.gaac_kv8_decode_attention(big, GOOD, 16, 2048, 0.1, GOOD, 0, GOOD, 1 << 30, None, None) == EINVAL
+
+
 def test_page_call_refusals(lib):
     assert lib.gaac_kv8_reserve(cache(), GOOD + 2, None, None) == EINVAL
     assert lib.gaac_kv8_release(cache(), None, 1, None, None) == EINVAL
