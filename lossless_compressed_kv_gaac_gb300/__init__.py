@@ -521,14 +521,16 @@ def _gpu(*tensors) -> int:
     return index
 
 
-# The current stream's handle, without the stream object that torch.cuda.current_stream() makes (2 us a call).
+# The current stream's handle, without the stream object that torch.cuda.current_stream() makes (2 us a call), and
+# the current device.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(fn: str, index: int, stream, *args):
     """Calls the library with device `index` current and the stream (default: the device's current one) last."""
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         with torch.cuda.device(index):
             return _call(fn, index, stream, *args)
     if stream is None:
@@ -540,12 +542,25 @@ def _call(fn: str, index: int, stream, *args):
         raise GaacError(fn, status)
 
 
-def _rope_strides(t, name):
-    """Batch (0 without one), token and head strides of [tokens, heads, dim] or [batch, tokens, heads, dim]."""
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}: channels must be contiguous")
-    return st[:3] if len(st) == 4 else (0, st[0], st[1])
+def _rope_pair(x, out, dtype, index, name):
+    """gaac_rope_tensor of an input [tokens, heads, dim] or [batch, tokens, heads, dim] and its output (None: in place),
+    and the input's shape."""
+    shape, st = x.shape, x.stride()
+    n = len(shape)
+    if n != 3 and n != 4:
+        raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
+    if x.dtype != dtype or x.get_device() != index or (st[-1] != 1 and shape[-1] > 1):
+        raise ValueError(f"{name} must be of q's type and device, channels contiguous")
+    at = x.data_ptr()
+    if out is None:
+        out_at, so = at, st
+    else:
+        out_at, so = out.data_ptr(), out.stride()
+        if out.shape != shape or out.dtype != dtype or out.get_device() != index or (so[-1] != 1 and shape[-1] > 1):
+            raise ValueError(f"{name}_out must have {name}'s shape, type and device, channels contiguous")
+    if n == 3:
+        return _ROPE_TENSOR.pack(at, out_at, shape[1], 0, st[0], st[1], 0, so[0], so[1]), shape
+    return _ROPE_TENSOR.pack(at, out_at, shape[2], st[0], st[1], st[2], so[0], so[1], so[2]), shape
 
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, turns: torch.Tensor, q_out=None, k_out=None,
@@ -555,49 +570,37 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, turns
     [batch, tokens]; turns: rope_turns(...), one for each pair of the rotated channels (the first
     2 * turns.numel() of a head; the others are copied).  Pairs are (j, j + half) or, interleaved, (2j, 2j + 1).
     q_out, k_out: default in place.  inverse turns the other way: the gradient of the call without it."""
-    dtype, shape = q.dtype, q.shape
+    dtype, index = q.dtype, q.get_device()
     code = _DTYPES.get(dtype)
     if code is None:
         raise ValueError("q must be BF16, FP16 or FP32")
-    if len(shape) == 3:
-        n_seq, (n_tok, heads, dim) = 1, shape
-    elif len(shape) == 4:
-        n_seq, n_tok, heads, dim = shape
-    else:
-        raise ValueError("q must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
-    index = _gpu(q, positions, turns)
-    if q_out is None:
-        q_out = q
-    elif q_out.dtype != dtype or q_out.shape != shape or q_out.get_device() != index:
-        raise ValueError("q_out must have q's type, shape and device")
-    desc = _ROPE_TENSOR.pack(q.data_ptr(), q_out.data_ptr(), heads, *_rope_strides(q, "q"), *_rope_strides(q_out, "q_out"))
+    if index < 0 or positions.get_device() != index or turns.get_device() != index:
+        raise ValueError("tensors must be on one CUDA device")
+    desc, shape = _rope_pair(q, q_out, dtype, index, "q")
     count = 1
     if k is not None:
-        k_shape = k.shape
-        if k.dtype != dtype or len(k_shape) != len(shape) or k_shape[:-2] != shape[:-2] or k_shape[-1] != dim or \
-                k.get_device() != index:
-            raise ValueError("k must have q's type, tokens, width and device")
-        if k_out is None:
-            k_out = k
-        elif k_out.dtype != dtype or k_out.shape != k_shape or k_out.get_device() != index:
-            raise ValueError("k_out must have k's type, shape and device")
-        desc += _ROPE_TENSOR.pack(k.data_ptr(), k_out.data_ptr(), k_shape[-2], *_rope_strides(k, "k"),
-                                  *_rope_strides(k_out, "k_out"))
+        more, k_shape = _rope_pair(k, k_out, dtype, index, "k")
+        if k_shape[:-2] != shape[:-2] or k_shape[-1] != shape[-1]:
+            raise ValueError("k must have q's tokens and width")
+        desc += more
         count = 2
     elif k_out is not None:
         raise ValueError("k_out without k")
-    if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+    turns_shape = turns.shape
+    if turns.dtype != torch.int64 or len(turns_shape) != 1 or not turns.is_contiguous():
         raise ValueError("turns must be a contiguous int64 tensor [pairs]")
-    bits = 32 if positions.dtype == torch.int32 else 64
-    if bits == 64 and positions.dtype != torch.int64:
+    pos_type = positions.dtype
+    if pos_type != torch.int32 and pos_type != torch.int64:
         raise ValueError("positions must be int32 or int64")
+    n_seq, n_tok = (1, shape[0]) if len(shape) == 3 else shape[:2]
     pos_shape, ps = positions.shape, positions.stride()
     if len(pos_shape) == 1 and pos_shape[0] == n_tok:
         ps = (0, ps[0])
-    elif len(pos_shape) != 2 or len(shape) != 4 or pos_shape[0] != n_seq or pos_shape[1] != n_tok:
+    elif len(shape) != 4 or pos_shape != shape[:2]:
         raise ValueError("positions must be [tokens] or [batch, tokens]")
-    _call("gaac_rope", index, stream, desc, count, code, n_seq, n_tok, dim, 2 * turns.shape[0], positions.data_ptr(), bits,
-          *ps, turns.data_ptr(), mscale, (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0))
+    _call("gaac_rope", index, stream, desc, count, code, n_seq, n_tok, shape[-1], 2 * turns_shape[0], positions.data_ptr(),
+          32 if pos_type == torch.int32 else 64, *ps, turns.data_ptr(), mscale,
+          (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0))
 
 
 # ---------------------------------------------------------------- 8-bit paged cache
