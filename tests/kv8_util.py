@@ -68,13 +68,12 @@ def tokens_of(cache, b):
     return torch.cat([x, tail], 1)
 
 
-def attention_ref(cache, q, scale):
+def attention_ref(cache, q, scale, weights=2.0 ** -11):
     """(out, bound) in 64 bits: the attention of q [batch, q_heads, 128], and for every element the error that a
-    computation in 32 bits with 16-bit weights may have before its result is rounded.
+    computation in 32 bits with weights off by `weights` may have before its result is rounded.
 
     Logits: 128 products in fp32 are off by at most 128 * 2^-24 of the sum of their magnitudes, a further 2^-20 of
-    that covers scaling them and splitting off their maxima, and 2^-20 the exponentials.  Weights: rounded to f16
-    (2^-11).  An error d of a logit changes each weight by a factor of about 1 + d, in numerator and denominator."""
+    that covers scaling them and splitting off their maxima, and 2^-19 the exponentials and the sums.  An error d of a logit changes each weight by a factor of about 1 + d, in numerator and denominator."""
     B, hq, _ = q.shape
     g = hq // cache.n_kv_heads
     out = torch.zeros(q.shape, dtype=torch.float64, device=q.device)
@@ -90,12 +89,15 @@ def attention_ref(cache, q, scale):
             p = torch.softmax(s, -1)
             out[b, rows] = p @ v[:, h]
             d = (qb.abs() @ k[:, h].abs().T).amax(-1, keepdim=True) * abs(scale) * (2.0 ** -17 + 2.0 ** -20)
-            bound[b, rows] = (p @ v[:, h].abs()) * (2.0 ** -11 + 2.0 ** -19 + 2.05 * d)
+            bound[b, rows] = (p @ v[:, h].abs()) * (weights + 2.0 ** -19 + 2.05 * d)
     return out, bound
 
 
 def check_attention(cache, q, scale, out):
-    ref, bound = attention_ref(cache, q, scale)
+    """Weights: one f16 (2^-11, a whole step to be generous) for a bf16 result; in two parts for others, each rounded
+    to 11 bits of what is left (2^-22, below 2^-20), or to bf16's 8 (2^-18, below 2^-16) over a bf16 open block."""
+    weights = 2.0 ** -11 if out.dtype == torch.bfloat16 else 2.0 ** -16 if cache.dtype == torch.bfloat16 else 2.0 ** -20
+    ref, bound = attention_ref(cache, q, scale, weights)
     half = torch.finfo(out.dtype).eps / 2
     tol = bound * (1 + half) + half * ref.abs() + torch.finfo(out.dtype).tiny
     err = (out.double() - ref).abs()
