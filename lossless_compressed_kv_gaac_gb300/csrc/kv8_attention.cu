@@ -160,41 +160,27 @@ __device__ __forceinline__ bool ka_wait(uint64_t* bar, uint32_t parity, int32_t*
   return __all_sync(kKaFull, mbar_wait(bar, parity, status));
 }
 
-// The copy warp's ring position; every call by the whole warp.
-struct KaRing {
-  int stage = 0;
-  uint32_t phase = 0;
-  int issued = 0;
+// Where a CTA's work lies.
+struct KaCut {
+  unsigned piece;            // units of a CTA at most
+  bool aligned;
+  int b, h, b32, len32;      // its first pair (b = batch: none); the lengths of sequences b32 .. b32 + 31, one a lane
+  KaSeq s;                   // sequence b
+  unsigned own, skipped;     // places of a pair of sequence b, and those of the first pair before this CTA's
+  unsigned seg, u, u_end;    // in units: the pair's first, this CTA's first and its end
 };
 
-// Waits for the next stage to be free.  false: gave up.
-__device__ __forceinline__ bool ka_acquire(KaSmem& sm, KaRing& r, int32_t* status) {
-  if (r.issued >= kKaStages) {
-    if (!ka_wait(&sm.empty[r.stage], r.phase ^ 1u, status)) return false;
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  }
-  return true;
-}
-__device__ __forceinline__ void ka_next(KaRing& r) {
-  ++r.issued;
-  if (++r.stage == kKaStages) {
-    r.stage = 0;
-    r.phase ^= 1u;
-  }
-}
-
-__device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pages, const CUtensorMap* tail, int copier) {
-  const Kv8Dev& c = a.c;
+// By a whole warp.  The lengths come from L2, so that a call ahead of the dependent-launch wait leaves nothing stale.
+__device__ __forceinline__ KaCut ka_cut(const Kv8Dev& c, int32_t* status) {
   const int lane = threadIdx.x & 31;
-  KaRing ring;
   // ---- the cut: pieces of at most `piece` units (all counts below 2^31: the host has checked)
   unsigned total = 0;
   int len32 = 0;  // lengths of 32 sequences, one a lane
   for (int b0 = 0; b0 < c.batch; b0 += 32) {
     unsigned u = 0;
     if (b0 + lane < c.batch) {
-      const int len = len32 = c.lens[b0 + lane];
-      if (blockIdx.x == 0 && (len < 0 || len > static_cast<int64_t>(c.max_blocks) * kBlock)) report(a.status, GAAC_EINVAL);
+      const int len = len32 = __ldcg(c.lens + b0 + lane);
+      if (status != nullptr && blockIdx.x == 0 && (len < 0 || len > static_cast<int64_t>(c.max_blocks) * kBlock)) report(status, GAAC_EINVAL);
       u = ka_seq(c, len).units;
     }
     total += __reduce_add_sync(kKaFull, u) * c.heads;
@@ -206,7 +192,7 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
   if (static_cast<unsigned>(c.batch) * c.heads <= gridDim.x) {
     unsigned pieces = 0;
     for (int b0 = 0; b0 < c.batch; b0 += 32) {
-      const int len = c.batch <= 32 ? len32 : b0 + lane < c.batch ? c.lens[b0 + lane] : 0;
+      const int len = c.batch <= 32 ? len32 : b0 + lane < c.batch ? __ldcg(c.lens + b0 + lane) : 0;
       pieces += __reduce_add_sync(kKaFull, b0 + lane < c.batch ? (ka_seq(c, len).units + piece - 1) / piece : 0u) * c.heads;
     }
     aligned = pieces <= gridDim.x;
@@ -217,7 +203,7 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
   unsigned base = 0;  // places before sequence b
   int b32 = -1;
   for (int b0 = 0; b0 < c.batch; b0 += 32) {
-    const int len = c.batch <= 32 ? len32 : b0 + lane < c.batch ? c.lens[b0 + lane] : 0;
+    const int len = c.batch <= 32 ? len32 : b0 + lane < c.batch ? __ldcg(c.lens + b0 + lane) : 0;
     unsigned u = 0;
     if (b0 + lane < c.batch) {
       u = ka_seq(c, len).units;
@@ -254,6 +240,57 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
     u = aligned ? skipped * piece : begin;
     u_end = min(u + piece, aligned ? static_cast<unsigned>(s.units) : total);
   }
+  return KaCut{piece, aligned, b, h, b32, len32, s, own, skipped, seg, u, u_end};
+}
+
+// Before the kernel ahead on the stream is done: the pages that this CTA will most likely read first are fetched into
+// L2.  Lengths and table may still change, which wastes a prefetch; every address is checked.
+__device__ __forceinline__ void ka_guess(const KaArgs& a) {
+  const Kv8Dev& c = a.c;
+  const int lane = threadIdx.x & 31;
+  const KaCut cut = ka_cut(c, nullptr);
+  const int l = static_cast<int>(cut.u - cut.seg) + lane;
+  if (cut.b < c.batch && lane < kKaStages && cut.u + lane < cut.u_end && l < cut.s.full) {
+    const int32_t page = __ldcg(c.table + static_cast<int64_t>(cut.b) * c.max_blocks + l);
+    if (page >= 0 && page < c.n_pages)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(c.pages + (static_cast<int64_t>(page) * c.heads + cut.h) * kKv8Pair),
+                   "r"(kKv8Pair) : "memory");
+  }
+}
+
+// The copy warp's ring position; every call by the whole warp.
+struct KaRing {
+  int stage = 0;
+  uint32_t phase = 0;
+  int issued = 0;
+};
+
+// Waits for the next stage to be free.  false: gave up.
+__device__ __forceinline__ bool ka_acquire(KaSmem& sm, KaRing& r, int32_t* status) {
+  if (r.issued >= kKaStages) {
+    if (!ka_wait(&sm.empty[r.stage], r.phase ^ 1u, status)) return false;
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  return true;
+}
+__device__ __forceinline__ void ka_next(KaRing& r) {
+  ++r.issued;
+  if (++r.stage == kKaStages) {
+    r.stage = 0;
+    r.phase ^= 1u;
+  }
+}
+
+__device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pages, const CUtensorMap* tail, int copier) {
+  const Kv8Dev& c = a.c;
+  const int lane = threadIdx.x & 31;
+  KaRing ring;
+  KaCut cut = ka_cut(c, a.status);
+  KaSeq s = cut.s;
+  int b = cut.b, h = cut.h, b32 = cut.b32, len32 = cut.len32;
+  unsigned seg = cut.seg, u = cut.u, u_end = cut.u_end;
+  const unsigned piece = cut.piece, own = cut.own, skipped = cut.skipped;
+  const bool aligned = cut.aligned;
   const uint64_t policy = ka_evict_first();
   const uint32_t q_bytes = static_cast<uint32_t>(a.r) * kD * 2;
   bool ok = true;
@@ -878,6 +915,7 @@ __global__ void __launch_bounds__(kKaThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&tail) : "memory");
   }
   __syncthreads();
+  if (threadIdx.x < 32) ka_guess(a);  // a compute warp: it has nothing to do before the first data
   dependent_wait();
   dependent_launch();
   if (threadIdx.x >= 32 * kKaWarps)
