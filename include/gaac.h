@@ -558,8 +558,10 @@ GAAC_API int gaac_kv8_append(const gaac_kv8* cache, const void* k, const void* v
  * sequence.  q: the cache's dtype, [batch] rows q_seq_stride elements apart (a multiple of
  * 8), each [n_q_heads][128], 16-byte aligned; out: contiguous [batch][n_q_heads][128] of the
  * cache's dtype or GAAC_F32, 16-byte aligned.  workspace: gaac_kv8_attention_workspace()
- * bytes, 16-byte aligned, zero before the first call and left so; not shared by calls that
- * may overlap on the GPU.  A page index outside the pool reports GAAC_EFORMAT and its
+ * bytes, 16-byte aligned, zero before the first call and left so (zero it again after a call
+ * that reported GAAC_ETIMEOUT); not shared by calls that may overlap on the GPU.  batch *
+ * n_kv_heads * (max_blocks + 1) < 2^31.  Weights are rounded to f16 for a BF16 result (2^-12
+ * of each) and carried in two parts for others; sums are fp32.  A page index outside the pool reports GAAC_EFORMAT and its
  * block contributes nothing; a length outside the table reports GAAC_EINVAL and counts as 0.
  */
 GAAC_API size_t gaac_kv8_attention_workspace(void);

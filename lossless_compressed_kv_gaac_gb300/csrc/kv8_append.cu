@@ -13,6 +13,8 @@
 // kv-head: 128 threads hold a block's 16 KB in registers and have the next block's loads in flight while they
 // quantise it, so the reads never pause, few warps wait at a block's one barrier, and what the run's sequence and pages
 // are is looked up once.  Runs are one block long where there are few (latency), longer where every SM has several.
+// 113,000 tokens of 8 heads in chunks of up to 24,000: 105 us, 6.6 TB/s (a block's K and V in CTAs of 512 threads:
+// 120 us; with lane-by-lane conversions and address arithmetic: 150 us).  One token for each of 32 sequences: 2.3 us.
 // The first block's CTA also writes the new open block's rows, after it has read the old ones from the same tail.
 #include <algorithm>
 

@@ -4,17 +4,22 @@
 // with sK, sV the scales of t's block (1 for the open block, which is in the model's type).
 //
 // Memory bound: 256 bytes per token and kv-head are read once, and 4 * (query heads) * 128 operations per token
-// hide under them.  Two CTAs per SM, each of four compute warps and one copy warp:
-//  * Work is cut evenly, whatever the lengths: the (sequence, kv-head) pairs' blocks in one row of units (a page is
-//    one unit, an open block two, an empty sequence one), CTA i of G takes units [i U/G, (i+1) U/G).  A pair that
-//    spans CTAs is joined by the last of them to finish; a CTA has at most two such pairs, its first and its last.
-//  * The copy warp walks the units: one tensor copy (TMA, 128-byte swizzle) brings K and V of a page and head, which
-//    lie together (16 KB), into a ring of stages; the scales ride along as an 8-byte asynchronous copy, the
+// hide under them.  One CTA per SM: five groups of two compute warps, and two copy warps (one alone takes
+// some 950 cycles for each 16 KB, which bounds the kernel at 5.1 TB/s; with two the memory does):
+//  * Work is cut evenly, whatever the lengths: the blocks of all (sequence, kv-head) pairs in one row of units (a page
+//    is one unit, half an open block one, an empty sequence one), every CTA a piece of it of the same size.  Pieces
+//    begin with a pair where there are CTAs for that.  A pair that spans CTAs is joined by the last of them to
+//    finish; a CTA has at most two such pairs, its first and its last.
+//  * The copy warps walk the units: one tensor copy (TMA, 128-byte swizzle) brings K and V of a page and head, which
+//    lie together (16 KB), into a ring of ten stages; the scales ride along as an 8-byte asynchronous copy, the
 //    pair's queries as a bulk copy with its first unit.  Everything a unit's consumers need is in its stage.
-//  * Compute warp w takes tokens [16w, 16w+16) of every block and keeps its own softmax state.  S = K q^T with K as
-//    the 16-row operand (mma.sync m16n8k16, 8 columns = query heads of the kv-head): the decode step has at most
-//    8 rows, so the wide operand is the cache and no tensor-core work is spent on padding tokens; tcgen05's 128-row
-//    tile would be.  O^T = V^T P^T uses the transposed 8-bit V straight from ldmatrix.trans (pairs of channels).
+//  * Units go round the groups.  Short pairs go to one group each, side by side, which saves the CTA-wide meetings
+//    (64 sequences of 10-200 tokens, 8 kv-heads: 18.6 us, 25 without).
+//  * A group's two warps take 32 tokens of a page each and keep their own softmax state until the pair ends.  S = K q^T
+//    with K as the 16-row operand (mma.sync m16n8k16, 8 columns = query heads of the kv-head): the decode step has at
+//    most 8 rows, so the wide operand is the cache and no tensor-core work goes to padding, as it would in
+//    tcgen05's 128-row tile, whose operands would also have to be widened into shared memory first.  O^T = V^T P^T
+//    takes the transposed 8-bit V straight from ldmatrix.trans (pairs of channels).
 //  * FP8 becomes f16 in registers (exact).  The query is scaled by a power of two per row into f16's range (exact
 //    but for parts below 2^-28 of the row's largest), the scale is put back with sK.
 //  * Two running maxima per row: m of the logits, for the softmax's sum l; and M of logit + log2 sV, for the
@@ -22,6 +27,9 @@
 //    weight is 2^15 and those down to 2^-29 of it keep f16's 11 bits.  For f16 and fp32 results what the rounding
 //    leaves follows as a second operand.  m, l, M and O are fp32.
 //  * The open block is multiplied in its own type, the weights always in two parts.
+// Measured (bf16 or fp16 result): 32 sequences of 4,096-32,768 tokens, 8 kv-heads, 1.2 GB: 180 us, 6.7 TB/s; one of
+// 65,536 tokens: 26.4 us, of which 3 us go by before the first data and 4 us from the last to the joined result; one
+// of 777 tokens: 8.5 us.
 #include <cuda.h>
 
 #include <algorithm>
@@ -38,11 +46,16 @@ constexpr int kKaThreads = kKaCompute + 32 * kKaCopyWarps;
 constexpr int kKaStages = 10;                // unit i uses stage i % stages and belongs to group i % groups
 constexpr int kKaHalf = kBlock / 2;          // tokens of an open block's unit
 constexpr int kKaRows = 8;                   // query heads per kv-head in the MMA columns
-constexpr int kKaMinUnits = 4;               // fewer units than this are not worth a CTA
-constexpr unsigned kKaSolo = 20;             // most units of a pair that one group may take alone (at most 32)
+// Fewer units than this are not worth a CTA: 1 x 777 tokens 8.5 us (five: 8.9), 1 x 2,000 9.0 us (five: 9.4), and with
+// two, 4 x 500 tokens 13.7 us (four: 9.0), where the pieces no longer fit pair by pair.
+constexpr int kKaMinUnits = 4;
+// Most units of a pair that one group may take alone (at most 32): 256 x 1,000 tokens 101 us (with sixteen 108),
+// 128 x 10-2,000 tokens 60.7 us (with 32 63.2).
+constexpr unsigned kKaSolo = 20;
 constexpr int kKaStride = kD + 4;            // floats per row of a warp's state in shared memory (bank spread)
 constexpr int kKaPart = 3 * kKaRows + kKaRows * kD;  // floats of a partial: m, l, M, O
-constexpr int kKaJoin = 10;                  // partials in flight when they are joined
+// Partials in flight when they are joined: 1 x 65,536 tokens 27.0 us (with eight 28.5, with twelve 28.1).
+constexpr int kKaJoin = 10;
 constexpr uint32_t kKaFull = 0xFFFFFFFFu;
 static_assert(kKaStages % kKaGroups == 0, "a stage belongs to one group, which waits for all of its phases in turn");
 

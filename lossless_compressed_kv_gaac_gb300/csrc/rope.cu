@@ -9,9 +9,12 @@
 // 0.06 rad at a million), and its top 32 bits, as a signed number, are the angle in [-pi, pi): one float
 // conversion, then sincospi.  The angle is off by at most 2^-33 turns plus p * 2^-65.
 //
-// Memory bound: 2 bytes moved per byte of input.  A thread owns V pairs (16-byte vectors where alignment
-// allows) of one row and walks over heads with them, so the V sines and cosines are computed once for the
-// thread's heads; neighbouring threads take neighbouring vectors, then neighbouring heads.
+// Memory bound: every byte of input is read once and written once.  A thread owns V pairs (16-byte vectors where
+// alignment allows) of one row and walks over up to five heads with them, so V sines and cosines serve all of these;
+// neighbouring threads take neighbouring vectors, then neighbouring heads.  The loads of two heads are under way
+// before the sines are computed.  CTAs of 64 threads, 16 to an SM (64 registers), keep the loads of many rows in
+// flight: 32,768 tokens x 40 heads x 128 in bf16 take 100.3 us, 6.69 TB/s (104.1 us with 128 threads and eight
+// heads, 106.2 us with 256); 32 tokens 2.1 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -102,13 +105,13 @@ __device__ __forceinline__ void rope_pack(RopeVec<T, V>& x, const float* f) {
   }
 }
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 64;
 constexpr int kRopeBatch = 2;  // heads whose loads a thread has in flight
-constexpr int kRopeMost = 8;   // most heads of a thread
+constexpr int kRopeMost = 5;   // most heads of a thread
 
 // Thread (row, walker, unit): heads walker, walker + walkers, ... of one row, V pairs of each.
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 16) rope_kernel(const RopeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using Vec = RopeVec<T, V>;
@@ -122,10 +125,6 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a)
     seq = row / a.n_tok;
     tok = row - seq * a.n_tok;
   }
-  const int64_t pi = seq * a.pos_seq + tok * a.pos_tok;
-  uint64_t p = a.pos64 ? static_cast<uint64_t>(static_cast<const int64_t*>(a.pos)[pi])
-                       : static_cast<uint64_t>(static_cast<int64_t>(static_cast<const int32_t*>(a.pos)[pi]));
-  if (a.inverse) p = 0 - p;
   const char* const xq = a.t[0].x + seq * a.t[0].x_seq + tok * a.t[0].x_tok;
   const char* const xk = a.t[1].x + seq * a.t[1].x_seq + tok * a.t[1].x_tok;
   char* const outq = a.t[0].out + seq * a.t[0].out_seq + tok * a.t[0].out_tok;
@@ -137,8 +136,31 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a)
     const int e1 = turned && !INTER ? e0 + a.rot / 2 : e0 + V;
     const bool two = e1 < a.dim;
     const int64_t o0 = e0 * static_cast<int64_t>(sizeof(T)), o1 = e1 * static_cast<int64_t>(sizeof(T));
+    Vec v[kRopeBatch][2];
+    char* out[kRopeBatch];
+    auto load = [&](int h0) {
+#pragma unroll
+      for (int j = 0; j < kRopeBatch; ++j) {
+        const int h = h0 + j * a.walkers;
+        out[j] = nullptr;
+        if (h < a.heads) {
+          const bool second = h >= a.heads0;
+          if (turned || (second ? a.t[1].copy : a.t[0].copy)) {
+            const char* x = second ? xk + (h - a.heads0) * a.t[1].x_head : xq + h * a.t[0].x_head;
+            out[j] = second ? outk + (h - a.heads0) * a.t[1].out_head : outq + h * a.t[0].out_head;
+            v[j][0] = *reinterpret_cast<const Vec*>(x + o0);
+            if (two) v[j][1] = *reinterpret_cast<const Vec*>(x + o1);
+          }
+        }
+      }
+    };
+    load(walker);  // under way while the sines are computed
     float c[V], s[V];
     if (turned) {
+      const int64_t pi = seq * a.pos_seq + tok * a.pos_tok;
+      uint64_t p = a.pos64 ? static_cast<uint64_t>(static_cast<const int64_t*>(a.pos)[pi])
+                           : static_cast<uint64_t>(static_cast<int64_t>(static_cast<const int32_t*>(a.pos)[pi]));
+      if (a.inverse) p = 0 - p;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const uint64_t turn = p * a.turns[u * V + i] + (1ull << 31);
@@ -154,23 +176,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a)
       }
     }
     // the loads of kRopeBatch heads come before the first store
-    for (int h0 = walker; h0 < a.heads; h0 += kRopeBatch * a.walkers) {
-      Vec v[kRopeBatch][2];
-      char* out[kRopeBatch];
-#pragma unroll
-      for (int j = 0; j < kRopeBatch; ++j) {
-        const int h = h0 + j * a.walkers;
-        out[j] = nullptr;
-        if (h < a.heads) {
-          const bool second = h >= a.heads0;
-          if (turned || (second ? a.t[1].copy : a.t[0].copy)) {
-            const char* x = second ? xk + (h - a.heads0) * a.t[1].x_head : xq + h * a.t[0].x_head;
-            out[j] = second ? outk + (h - a.heads0) * a.t[1].out_head : outq + h * a.t[0].out_head;
-            v[j][0] = *reinterpret_cast<const Vec*>(x + o0);
-            if (two) v[j][1] = *reinterpret_cast<const Vec*>(x + o1);
-          }
-        }
-      }
+    for (int h0 = walker;;) {
 #pragma unroll
       for (int j = 0; j < kRopeBatch; ++j) {
         if (out[j] != nullptr) {
@@ -192,6 +198,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a)
           if (two) *reinterpret_cast<Vec*>(out[j] + o1) = v[j][1];
         }
       }
+      h0 += kRopeBatch * a.walkers;
+      if (h0 >= a.heads) break;
+      load(h0);
     }
   }
 }
