@@ -487,8 +487,8 @@ def rope_frequencies(rot_dim: int, theta: float = 1e4, scaling: str | None = Non
         return w / factor, 1.0
     if scaling != "bands":
         raise ValueError("scaling must be None, 'linear', 'base' or 'bands'")
-    if not original_len or original_len <= 0 or not fast > slow > 0:
-        raise ValueError("band scaling needs original_len > 0 and fast > slow > 0")
+    if not original_len or original_len <= 0 or not fast > slow > 0 or not theta > 1:
+        raise ValueError("band scaling needs original_len > 0, fast > slow > 0 and theta > 1")
 
     def pair_of(turns):  # the (real) index of the pair that turns so often within original_len
         return rot_dim * math.log(original_len / (2 * math.pi * turns)) / (2 * math.log(theta))

@@ -537,6 +537,76 @@ def test_full_and_empty_pools_compact():
     assert ok(c) == 0
 
 
+def test_page_calls_captured_and_on_another_stream():
+    """A scheduler's step in a graph, replayed with other lists and lengths, and the same calls on a side stream."""
+    c, m = Kv8Cache(300, 12, 1, 30), U.Model(300, 12, 30)
+    done, src, dst, cu = ints([0, 1, 2]), ints([5, 5, 7]), ints([0, 1, 2]), ints([0] * 13)
+    k, v = kv_of(2000, 1, BF16, 3)
+    moved = ints([0] * 300)
+    both(c, m, "reserve", [100] * 12)
+    both(c, m, "append", [100] * 12)
+
+    def step(stream=None):
+        c.release(done, stream=stream)
+        c.fork(src, dst, stream=stream)
+        c.append(k, v, cu, stream=stream)
+        G.kv8_compact(c, moved, stream=stream)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    rng = random.Random(1)
+    for i in range(12):
+        rows = rng.sample(range(12), 6)
+        new = [rng.randrange(160) for _ in range(12)]
+        lists = [rows[:3], [rng.choice(rows[3:]) for _ in range(3)], rows[:3]]
+        for t, x in zip((done, src, dst, cu), lists + [cu_of(new)]):
+            t.copy_(x if isinstance(x, torch.Tensor) else ints(x))
+        if i % 3 == 2:
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            step(s)
+            torch.cuda.current_stream().wait_stream(s)
+        else:
+            g.replay()
+        m.release(lists[0])
+        m.fork(lists[1], lists[2])
+        m.reserve(new)
+        m.append(new)
+        assert moved.tolist() == m.compact()
+        m.check(c)
+        # what does not fit is reported and leaves its sequence as it was, which the model follows
+        c.status.zero_()
+
+
+def test_append_rows_past_32_bits():
+    """k and v are columns of a buffer of 2.4e9 elements: rows 60,000 elements apart."""
+    buf = torch.zeros((40000, 60000), dtype=BF16, device="cuda")
+    k, v = kv_of(40000, 1, BF16, 1)
+    buf[:, 128:256], buf[:, 59872:] = k[:, 0], v[:, 0]
+    c = Kv8Cache(640, 2, 1, 640, E4, BF16)
+    c.append(buf[:, None, 128:256], buf[:, None, 59872:], ints([0, 100, 40000]))
+    assert ok(c) == 0
+    check_blocks(c, {0: torch.stack([k[:100], v[:100]]), 1: torch.stack([k[100:], v[100:]])})
+
+
+def test_whole_flow_on_a_side_stream():
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c, _, _ = filled([300, 65, 0], 2)
+        q = rand((3, 8, 128), BF16, 5)
+        c.fork(ints([0]), ints([2]))
+        out = c.attention(q, SCALE)
+        c.release(ints([1]))
+        c.compact()
+        again = c.attention(q, SCALE)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(out[0], again[0]) and torch.equal(out[2], again[2]) and (again[1] == 0).all()
+    U.check_attention(c, q, SCALE, again)
+    assert ok(c) == 0
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("fmt,dtype", [(E4, BF16), (E5, F16)])

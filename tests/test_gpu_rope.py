@@ -187,3 +187,17 @@ def test_captured_and_on_another_stream():
         g.replay()
         check(q, qo, pos, w)
         check(k, ko, pos, w)
+
+
+def test_more_elements_than_32_bits():
+    """A tensor of 2.3e9 elements, in place; rows at its beginning, at 2^31 elements and at its end."""
+    n = 70000
+    x = torch.empty((n, 256, 128), dtype=BF16, device="cuda")
+    rows = [0, 1, 65535, 65536, n - 1]
+    for i in rows:
+        x[i] = rand((256, 128), BF16, i)
+    before = x[rows].clone()
+    pos = torch.arange(n, device="cuda")
+    w, _ = G.rope_frequencies(128)
+    G.rope(x, None, pos, G.rope_turns(w, "cuda"))
+    check(before, x[rows], pos[rows], w)

@@ -124,7 +124,7 @@ def test_python_refuses_host_tensors_and_shapes():
         G.Kv8(z(8, 4, 2, 64, 128, dtype=torch.uint8), z(8, 4, 2), z(2, 4, 2, 64, 128, dtype=torch.bfloat16),
               z(2, 3, dtype=torch.int32), z(8, dtype=torch.int32), z(2, dtype=torch.int32), G.FP8_E4M3)
     for args in ((127,), (0,), (64, -1.0), (64, 1e4, "linear", 0.0), (64, 1e4, "cubic"), (64, 1e4, "bands", 4.0),
-                 (2, 1e4, "base", 2.0)):
+                 (64, 1.0, "bands", 4.0, 4096), (64, 1e4, "bands", 4.0, 4096, 1.0, 2.0), (2, 1e4, "base", 2.0)):
         with pytest.raises(ValueError):
             G.rope_frequencies(*args)
     with pytest.raises(ValueError):
