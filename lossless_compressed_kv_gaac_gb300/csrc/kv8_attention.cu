@@ -5,7 +5,7 @@
 //
 // Memory bound: 256 bytes per token and kv-head are read once, and 4 * (query heads) * 128 operations per token
 // hide under them.  One CTA per SM: five groups of two compute warps, and two copy warps (one alone takes
-// some 950 cycles for each 16 KB, which bounds the kernel at 5.1 TB/s; with two the memory does):
+// some 950 cycles for each 16 KB, which bounds the kernel at 4.9 TB/s; with two the memory does):
 //  * Work is cut evenly, whatever the lengths: the blocks of all (sequence, kv-head) pairs in one row of units (a page
 //    is one unit, half an open block one, an empty sequence one), every CTA a piece of it of the same size.  Pieces
 //    begin with a pair where there are CTAs for that.  A pair that spans CTAs is joined by the last of them to
@@ -27,9 +27,9 @@
 //    weight is 2^15 and those down to 2^-29 of it keep f16's 11 bits.  For f16 and fp32 results what the rounding
 //    leaves follows as a second operand.  m, l, M and O are fp32.
 //  * The open block is multiplied in its own type, the weights always in two parts.
-// Measured (bf16 or fp16 result): 32 sequences of 4,096-32,768 tokens, 8 kv-heads, 1.2 GB: 180 us, 6.7 TB/s; one of
-// 65,536 tokens: 26.4 us, of which 3 us go by before the first data and 4 us from the last to the joined result; one
-// of 777 tokens: 8.5 us.
+// Measured (bf16 or fp16 result): 32 sequences of 4,096-32,768 tokens, 8 kv-heads, 1.2 GB: 177 us, 6.8 TB/s; one of
+// 65,536 tokens: 25.6 us, of which 3 us go by before the first data and 4 us from the last to the joined result; one
+// of 777 tokens: 8.2 us.
 #include <cuda.h>
 
 #include <algorithm>
@@ -271,34 +271,14 @@ __device__ __forceinline__ void ka_guess(const KaArgs& a) {
   }
 }
 
-// The copy warp's ring position; every call by the whole warp.
-struct KaRing {
-  int stage = 0;
-  uint32_t phase = 0;
-  int issued = 0;
-};
-
-// Waits for the next stage to be free.  false: gave up.
-__device__ __forceinline__ bool ka_acquire(KaSmem& sm, KaRing& r, int32_t* status) {
-  if (r.issued >= kKaStages) {
-    if (!ka_wait(&sm.empty[r.stage], r.phase ^ 1u, status)) return false;
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  }
-  return true;
-}
-__device__ __forceinline__ void ka_next(KaRing& r) {
-  ++r.issued;
-  if (++r.stage == kKaStages) {
-    r.stage = 0;
-    r.phase ^= 1u;
-  }
-}
-
+// A copy warp.  The CTA's units, of all its pairs, are numbered; unit j uses stage j % kKaStages, and copy warp w starts
+// the copies of units w, w + kKaCopyWarps, ...: lane 0 does, the others help with what is warp-wide.
 __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pages, const CUtensorMap* tail, int copier) {
+  static_assert(kKaStages % kKaCopyWarps == 0, "a stage belongs to one copy warp");
+  constexpr int kOwn = kKaStages / kKaCopyWarps;
   const Kv8Dev& c = a.c;
   const int lane = threadIdx.x & 31;
-  KaRing ring;
-  KaCut cut = ka_cut(c, a.status);
+  const KaCut cut = ka_cut(c, a.status);
   KaSeq s = cut.s;
   int b = cut.b, h = cut.h, b32 = cut.b32, len32 = cut.len32;
   unsigned seg = cut.seg, u = cut.u, u_end = cut.u_end;
@@ -307,45 +287,61 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
   const uint64_t policy = ka_evict_first();
   const uint32_t q_bytes = static_cast<uint32_t>(a.r) * kD * 2;
   bool ok = true;
-  // One unit of pair (pb, ph) into the ring's next stage; lane 0 starts its copies.  unit: its place in the pair.
-  auto issue = [&](const KaSeq& ps, int pb, int ph, int unit, int32_t page, bool empty, bool first, int last, int cta0, int n_cta) {
-    const bool mine = ring.stage % kKaCopyWarps == copier;
-    if (mine) ok = ka_acquire(sm, ring, a.status);
-    if (mine && lane == 0 && ok) {
-      const int st = ring.stage;
-      uint64_t* full = &sm.full[st];
-      int kind = kUnitNone, n_tok = kBlock;
-      if (empty) {
-      } else if (unit < ps.full) {
-        kind = page >= 0 && page < c.n_pages ? kUnitPage : kUnitNone;
-        if (kind == kUnitNone) report(a.status, GAAC_EFORMAT);
-      } else if (ps.open) {
-        kind = kUnitOpen;
-        n_tok = min(kKaHalf, ps.open - kKaHalf * (unit - ps.full));
-      }
-      const bool with_q = first && !empty;
-      sm.meta[st][0] = make_int4(kind, first ? 1 + with_q : 0, last, n_tok);
-      sm.meta[st][1] = make_int4(pb, ph, cta0, n_cta);
-      const int64_t tile = static_cast<int64_t>(page) * c.heads + ph;
-      if (kind == kUnitPage) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(&sm.scale[st])), "l"(c.scales + 2 * tile) : "memory");
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(full)) : "memory");
-      } else {
-        ka_arrive(full);
-      }
-      mbar_arrive_expect_tx(full, (kind == kUnitNone ? 0 : kKv8Pair) + (with_q ? q_bytes : 0));
-      if (kind == kUnitPage) {
-        ka_tma(sm.stage[st], pages, 0, static_cast<int>(tile * 2 * kBlock), full, policy);
-      } else if (kind == kUnitOpen) {  // K channels 0-63, 64-127, V the same
-        const int y = static_cast<int>((static_cast<int64_t>(pb) * c.heads + ph) * 2 * kBlock) + kKaHalf * (unit - ps.full);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          ka_tma(sm.stage[st] + k * (kKv8Pair / 4), tail, (k & 1) * (kD / 2), y + (k >> 1) * kBlock, full, policy);
-      }
-      if (with_q) bulk_g2s(sm.q[st], a.q + pb * a.q_seq + static_cast<int64_t>(ph) * a.r * kD, q_bytes, full);
+  int count = 0;             // units of all copy warps, modulo kKaCopyWarps (all lanes)
+  int st = copier, used = 0;  // lane 0: the next stage of this warp and how many it has used
+  uint32_t parity = 1u;       // lane 0: of the phase that frees the stage
+  auto acquire = [&]() {
+    if (used >= kOwn) {
+      ok = mbar_wait(&sm.empty[st], parity, a.status);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    ka_next(ring);
+    return ok;
   };
+  auto next_stage = [&]() {
+    ++used;
+    st += kKaCopyWarps;
+    if (st >= kKaStages) {
+      st -= kKaStages;
+      parity ^= 1u;
+    }
+  };
+  // Lane 0: one unit of pair (pb, ph) into the next stage.  unit: its place in the pair.
+  auto issue = [&](const KaSeq& ps, int pb, int ph, int unit, int32_t page, bool empty, bool first, int last, int cta0, int n_cta) {
+    if (!acquire()) return;
+    uint64_t* full = &sm.full[st];
+    int kind = kUnitNone, n_tok = kBlock;
+    if (empty) {
+    } else if (unit < ps.full) {
+      kind = page >= 0 && page < c.n_pages ? kUnitPage : kUnitNone;
+      if (kind == kUnitNone) report(a.status, GAAC_EFORMAT);
+    } else if (ps.open) {
+      kind = kUnitOpen;
+      n_tok = min(kKaHalf, ps.open - kKaHalf * (unit - ps.full));
+    }
+    const bool with_q = first && !empty;
+    sm.meta[st][0] = make_int4(kind, first ? 1 + with_q : 0, last, n_tok);
+    if (last) sm.meta[st][1] = make_int4(pb, ph, cta0, n_cta);
+    const int64_t tile = static_cast<int64_t>(page) * c.heads + ph;
+    if (kind == kUnitPage) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(&sm.scale[st])), "l"(c.scales + 2 * tile) : "memory");
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(full)) : "memory");
+    } else {
+      ka_arrive(full);
+    }
+    mbar_arrive_expect_tx(full, (kind == kUnitNone ? 0 : kKv8Pair) + (with_q ? q_bytes : 0));
+    if (kind == kUnitPage) {
+      ka_tma(sm.stage[st], pages, 0, static_cast<int>(tile * 2 * kBlock), full, policy);
+    } else if (kind == kUnitOpen) {  // K channels 0-63, 64-127, V the same
+      const int y = static_cast<int>((static_cast<int64_t>(pb) * c.heads + ph) * 2 * kBlock) + kKaHalf * (unit - ps.full);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        ka_tma(sm.stage[st] + k * (kKv8Pair / 4), tail, (k & 1) * (kD / 2), y + (k >> 1) * kBlock, full, policy);
+    }
+    if (with_q) bulk_g2s(sm.q[st], a.q + pb * a.q_seq + static_cast<int64_t>(ph) * a.r * kD, q_bytes, full);
+    next_stage();
+  };
+  // The first of the next units that is this warp's, when `count` have been before.
+  auto first_own = [&]() { return (copier - count + kKaCopyWarps) % kKaCopyWarps; };
   auto next_pair = [&]() {  // (b, h), s, seg and u move on
     seg += s.units;
     u = seg;
@@ -361,8 +357,6 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
     }
     s = ka_seq(c, __shfl_sync(kKaFull, len32, b - b32));
   };
-  int32_t row32 = 0;  // entries 0-31 of the table row of sequence row_of
-  int row_of = -1;
   while (u < u_end && ok) {
     if (!aligned && u == seg && s.units <= kKaSolo && u + s.units <= u_end &&
         (s.units <= 4 || (h + 3 <= c.heads && u_end - u >= 3 * s.units))) {
@@ -390,14 +384,17 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
 #pragma unroll 1
       for (unsigned i = 0; i < most && ok; ++i) {
 #pragma unroll 1
-        for (int k = 0; k < kKaGroups; ++k) {
+        for (int k = first_own(); k < kKaGroups; k += kKaCopyWarps) {
           int32_t page = pg[0];
 #pragma unroll
           for (int j = 1; j < kKaGroups; ++j) page = k == j ? pg[j] : page;
+          page = __shfl_sync(kKaFull, page, i);
           const KaSeq of{__shfl_sync(kKaFull, ps.full, k), __shfl_sync(kKaFull, ps.open, k), __shfl_sync(kKaFull, ps.units, k)};
-          issue(of, __shfl_sync(kKaFull, pb, k), __shfl_sync(kKaFull, ph, k), i, __shfl_sync(kKaFull, page, i), i >= of.units,
-                i == 0, i + 1 == of.units ? kLastSolo : 0, 0, 1);
+          const int qb = __shfl_sync(kKaFull, pb, k), qh = __shfl_sync(kKaFull, ph, k);
+          if (lane == 0 && ok) issue(of, qb, qh, i, page, i >= of.units, i == 0, i + 1 == of.units ? kLastSolo : 0, 0, 1);
         }
+        count = (count + kKaGroups) % kKaCopyWarps;
+        ok = __shfl_sync(kKaFull, ok, 0);
       }
       continue;
     }
@@ -408,42 +405,34 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
     const int n_cta = static_cast<int>(aligned ? own : (seg + s.units - 1) / piece - cta0 + 1);
     const int32_t* row = c.table + static_cast<int64_t>(b) * c.max_blocks;
     const int n_pages = max(0, min(n, s.full - l0));
-    // The row's first entries serve every head of the sequence, and those of the next sequence are fetched early.
-    int32_t pg = 0, pg_next = l0 == 0 && row_of == b ? row32 : lane < n_pages ? row[l0 + lane] : 0;
-    if (l0 == 0) {
-      row32 = pg_next;
-      row_of = b;
-    }
-    if (h == c.heads - 1 && b + 1 < c.batch && !aligned && u_end > seg + s.units) {
-      row32 = lane < c.max_blocks ? row[c.max_blocks + lane] : 0;
-      row_of = b + 1;
-    }
+    if (lane == 0) {
+      int i = first_own();
+      int32_t page_next = i < n_pages ? row[l0 + i] : 0;
 #pragma unroll 1
-    for (int i = 0; i < n_all && ok; ++i) {
-      if ((i & 31) == 0) {
-        pg = pg_next;
-        pg_next = i + 32 + lane < n_pages ? row[l0 + i + 32 + lane] : 0;
+      for (; i < n_all && ok; i += kKaCopyWarps) {
+        const int32_t page = page_next;  // one unit ahead
+        page_next = i + kKaCopyWarps < n_pages ? row[l0 + i + kKaCopyWarps] : 0;
+        issue(s, b, h, l0 + i, page, i >= n, i < kKaGroups, i >= n_all - kKaGroups ? kLastAll : 0, cta0, n_cta);
       }
-      const int32_t page = __shfl_sync(kKaFull, pg, i & 31);
-      issue(s, b, h, l0 + i, page, i >= n, i < kKaGroups, i >= n_all - kKaGroups ? kLastAll : 0, cta0, n_cta);
     }
+    count = (count + n_all) % kKaCopyWarps;
+    ok = __shfl_sync(kKaFull, ok, 0);
     next_pair();
   }
   // No copy may be in flight when the CTA ends, not even where a consumer's wait ran out: the last use of every stage
   // is waited for (bounded) before the end is passed on.
-  for (int i = 0; i < min(ring.issued, kKaStages); ++i) {
-    const int j = ring.issued - 1 - i;
-    if (kKaCopyWarps == 1 || j % kKaStages % kKaCopyWarps == copier) mbar_wait(&sm.full[j % kKaStages], (j / kKaStages) & 1, a.status);
-  }
-  for (int i = 0; i < kKaGroups && ok; ++i) {
-    const bool mine = kKaCopyWarps == 1 || ring.stage % kKaCopyWarps == copier;
-    if (mine) ok = ka_acquire(sm, ring, a.status);
-    if (mine && lane == 0 && ok) {
-      sm.meta[ring.stage][0] = make_int4(kUnitEnd, 0, 0, 0);
-      ka_arrive(&sm.full[ring.stage]);
-      ka_arrive(&sm.full[ring.stage]);
+  if (lane == 0) {
+    for (int i = 1; i <= min(used, kOwn); ++i) {
+      const int j = used - i;
+      mbar_wait(&sm.full[copier + kKaCopyWarps * (j % kOwn)], (j / kOwn) & 1, a.status);
     }
-    ka_next(ring);
+    for (int i = first_own(); i < kKaGroups && ok; i += kKaCopyWarps) {
+      if (!acquire()) break;
+      sm.meta[st][0] = make_int4(kUnitEnd, 0, 0, 0);
+      ka_arrive(&sm.full[st]);
+      ka_arrive(&sm.full[st]);
+      next_stage();
+    }
   }
 }
 
