@@ -14,7 +14,7 @@
 //    lie together (16 KB), into a ring of ten stages; the scales ride along as an 8-byte asynchronous copy, the
 //    pair's queries as a bulk copy with its first unit.  Everything a unit's consumers need is in its stage.
 //  * Units go round the groups.  Short pairs go to one group each, side by side, which saves the CTA-wide meetings
-//    (64 sequences of 10-200 tokens, 8 kv-heads: 18.6 us, 25 without).
+//    (64 sequences of 10-200 tokens, 8 kv-heads: 18.0 us, 25 without).
 //  * A group's two warps take 32 tokens of a page each and keep their own softmax state until the pair ends.  S = K q^T
 //    with K as the 16-row operand (mma.sync m16n8k16, 8 columns = query heads of the kv-head): the decode step has at
 //    most 8 rows, so the wide operand is the cache and no tensor-core work goes to padding, as it would in
@@ -27,9 +27,9 @@
 //    weight is 2^15 and those down to 2^-29 of it keep f16's 11 bits.  For f16 and fp32 results what the rounding
 //    leaves follows as a second operand.  m, l, M and O are fp32.
 //  * The open block is multiplied in its own type, the weights always in two parts.
-// Measured (bf16 or fp16 result): 32 sequences of 4,096-32,768 tokens, 8 kv-heads, 1.2 GB: 177 us, 6.8 TB/s; one of
-// 65,536 tokens: 25.6 us, of which 3 us go by before the first data and 4 us from the last to the joined result; one
-// of 777 tokens: 8.2 us.
+// Measured (bf16 or fp16 result): 32 sequences of 4,096-32,768 tokens, 8 kv-heads, 1.2 GB: 176 us, 6.9 TB/s; one of
+// 65,536 tokens: 25.4 us, of which 3 us go by before the first data and 4 us from the last to the joined result; one
+// of 777 tokens: 8.5 us.
 #include <cuda.h>
 
 #include <algorithm>
@@ -49,8 +49,8 @@ constexpr int kKaRows = 8;                   // query heads per kv-head in the M
 // Fewer units than this are not worth a CTA: 1 x 777 tokens 8.5 us (five: 8.9), 1 x 2,000 9.0 us (five: 9.4), and with
 // two, 4 x 500 tokens 13.7 us (four: 9.0), where the pieces no longer fit pair by pair.
 constexpr int kKaMinUnits = 4;
-// Most units of a pair that one group may take alone (at most 32): 256 x 1,000 tokens 101 us (with sixteen 108),
-// 128 x 10-2,000 tokens 60.7 us (with 32 63.2).
+// Most units of a pair that one group may take alone (at most 32).  256 x 1,000 tokens, 17 units a pair: 96 us; left to
+// all groups, with sixteen here, 7% more; 32 makes no difference where it was measured.
 constexpr unsigned kKaSolo = 20;
 constexpr int kKaStride = kD + 4;            // floats per row of a warp's state in shared memory (bank spread)
 constexpr int kKaPart = 3 * kKaRows + kKaRows * kD;  // floats of a partial: m, l, M, O
@@ -69,6 +69,10 @@ struct KaSmem {
   alignas(16) int4 meta[kKaStages][2];  // {kind, first of the pair in its group (2: with queries), last, tokens}, {b, h, first CTA, CTAs}
   alignas(16) float2 scale[kKaStages];
   float m[kKaWarps][kKaRows], l[kKaWarps][kKaRows], mv[kKaWarps][kKaRows];
+  // pairs side by side, for each copy warp: {full blocks, open tokens, b, h}, units, pages
+  alignas(16) int4 side[kKaCopyWarps][kKaGroups];
+  int side_units[kKaCopyWarps][kKaGroups];
+  int32_t side_page[kKaCopyWarps][kKaGroups][kKaSolo];
   uint64_t full[kKaStages], empty[kKaStages], sync, pair_sync[kKaGroups];
   int last;
 };
@@ -357,66 +361,82 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
     }
     s = ka_seq(c, __shfl_sync(kKaFull, len32, b - b32));
   };
+  // Lane 0: this warp's of the next n_all units, of the pairs side by side, or of pair (b, h) from unit l0 on with n
+  // units of which the first n_pages are pages, row their table entries.
+  auto start = [&](int n_all, bool sides, const int32_t* row, int l0, int n, int n_pages, int cta0, int n_cta) {
+    if (lane == 0) {
+      int i = first_own();
+      const int plain_end = sides ? 0 : min(n_pages, n_all - kKaGroups);
+      int32_t page_next = i < n_pages ? row[i] : 0;
+#pragma unroll 1
+      for (; i < n_all && ok; i += kKaCopyWarps) {
+        int32_t page = page_next;  // one unit ahead
+        page_next = i + kKaCopyWarps < n_pages ? row[i + kKaCopyWarps] : 0;
+        if (i >= kKaGroups && i < plain_end && page >= 0 && page < c.n_pages) {  // most units: neither first nor last
+          if (!acquire()) break;
+          uint64_t* full = &sm.full[st];
+          const int64_t tile = static_cast<int64_t>(page) * c.heads + h;
+          sm.meta[st][0] = make_int4(kUnitPage, 0, 0, kBlock);
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(&sm.scale[st])), "l"(c.scales + 2 * tile) : "memory");
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(full)) : "memory");
+          mbar_arrive_expect_tx(full, kKv8Pair);
+          ka_tma(sm.stage[st], pages, 0, static_cast<int>(tile * 2 * kBlock), full, policy);
+          next_stage();
+        } else {
+          KaSeq ps = s;
+          int pb = b, ph = h, unit = l0 + i, last = i >= n_all - kKaGroups ? kLastAll : 0;
+          bool empty = i >= n, first = i < kKaGroups;
+          if (sides) {
+            const int k = i % kKaGroups;
+            unit = i / kKaGroups;
+            const int4 d = sm.side[copier][k];
+            const int units = sm.side_units[copier][k];
+            ps.full = d.x, ps.open = d.y, pb = d.z, ph = d.w;
+            page = sm.side_page[copier][k][min(unit, static_cast<int>(kKaSolo) - 1)];
+            empty = unit >= units;
+            first = unit == 0;
+            last = unit + 1 == units ? kLastSolo : 0;
+          }
+          issue(ps, pb, ph, unit, page, empty, first, last, cta0, n_cta);
+        }
+      }
+    }
+    count = (count + n_all) % kKaCopyWarps;
+    ok = __shfl_sync(kKaFull, ok, 0);
+  };
   while (u < u_end && ok) {
     if (!aligned && u == seg && s.units <= kKaSolo && u + s.units <= u_end &&
         (s.units <= 4 || (h + 3 <= c.heads && u_end - u >= 3 * s.units))) {
       // ---- short pairs: the next ones of about the same length, up to one for each group, side by side (three at
-      // least, or few units).  Lane k keeps the k-th; pg[k], lane i: its i-th page.
-      KaSeq ps = {};
-      int pb = 0, ph = 0;
-      int32_t pg[kKaGroups];
+      // least, or few units)
       unsigned most = 0, least = kKaSolo;
-#pragma unroll
+      __syncwarp();  // lane 0 is done with the last ones
+#pragma unroll 1
       for (int k = 0; k < kKaGroups; ++k) {
-        pg[k] = 0;
-        if (u < u_end && u + s.units <= u_end && s.units <= kKaSolo && 4 * max(most, s.units) <= 5 * min(least, s.units) + 4) {
-          if (lane < s.full) pg[k] = c.table[static_cast<int64_t>(b) * c.max_blocks + lane];
-          if (lane == k) {
-            ps = s;
-            pb = b;
-            ph = h;
-          }
+        const bool take = u < u_end && u + s.units <= u_end && s.units <= kKaSolo &&
+                          4 * max(most, s.units) <= 5 * min(least, s.units) + 4;
+        if (lane == 0) {
+          sm.side[copier][k] = take ? make_int4(s.full, s.open, b, h) : make_int4(0, 0, 0, 0);
+          sm.side_units[copier][k] = take ? static_cast<int>(s.units) : 0;
+        }
+        if (take) {
+          if (lane < s.full) sm.side_page[copier][k][lane] = c.table[static_cast<int64_t>(b) * c.max_blocks + lane];
           most = max(most, s.units);
           least = min(least, s.units);
           next_pair();
         }
       }
-#pragma unroll 1
-      for (unsigned i = 0; i < most && ok; ++i) {
-#pragma unroll 1
-        for (int k = first_own(); k < kKaGroups; k += kKaCopyWarps) {
-          int32_t page = pg[0];
-#pragma unroll
-          for (int j = 1; j < kKaGroups; ++j) page = k == j ? pg[j] : page;
-          page = __shfl_sync(kKaFull, page, i);
-          const KaSeq of{__shfl_sync(kKaFull, ps.full, k), __shfl_sync(kKaFull, ps.open, k), __shfl_sync(kKaFull, ps.units, k)};
-          const int qb = __shfl_sync(kKaFull, pb, k), qh = __shfl_sync(kKaFull, ph, k);
-          if (lane == 0 && ok) issue(of, qb, qh, i, page, i >= of.units, i == 0, i + 1 == of.units ? kLastSolo : 0, 0, 1);
-        }
-        count = (count + kKaGroups) % kKaCopyWarps;
-        ok = __shfl_sync(kKaFull, ok, 0);
-      }
+      __syncwarp();
+      start(kKaGroups * static_cast<int>(most), true, nullptr, 0, 0, 0, 0, 1);
       continue;
     }
     const int l0 = static_cast<int>(u - seg);
     const int n = static_cast<int>(min(u_end, seg + s.units) - u);
-    const int n_all = max(n, kKaGroups);  // every group takes part in every pair, with an empty unit if need be
     const int cta0 = static_cast<int>(aligned ? blockIdx.x - skipped : seg / piece);
     const int n_cta = static_cast<int>(aligned ? own : (seg + s.units - 1) / piece - cta0 + 1);
-    const int32_t* row = c.table + static_cast<int64_t>(b) * c.max_blocks;
-    const int n_pages = max(0, min(n, s.full - l0));
-    if (lane == 0) {
-      int i = first_own();
-      int32_t page_next = i < n_pages ? row[l0 + i] : 0;
-#pragma unroll 1
-      for (; i < n_all && ok; i += kKaCopyWarps) {
-        const int32_t page = page_next;  // one unit ahead
-        page_next = i + kKaCopyWarps < n_pages ? row[l0 + i + kKaCopyWarps] : 0;
-        issue(s, b, h, l0 + i, page, i >= n, i < kKaGroups, i >= n_all - kKaGroups ? kLastAll : 0, cta0, n_cta);
-      }
-    }
-    count = (count + n_all) % kKaCopyWarps;
-    ok = __shfl_sync(kKaFull, ok, 0);
+    const int32_t* row = c.table + static_cast<int64_t>(b) * c.max_blocks + l0;
+    // every group takes part in every pair, with an empty unit if need be
+    start(max(n, kKaGroups), false, row, l0, n, max(0, min(n, s.full - l0)), cta0, n_cta);
     next_pair();
   }
   // No copy may be in flight when the CTA ends, not even where a consumer's wait ran out: the last use of every stage
