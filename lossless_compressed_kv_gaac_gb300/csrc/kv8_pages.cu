@@ -103,29 +103,30 @@ __device__ __forceinline__ bool fill_range(const Kv8Dev& c, const int32_t* cu, i
 }
 
 // For sequences b, b + step, ... (at most 32, one a lane, with blocks [lo, hi) each): visit(k, i, miss) for every 32
-// blocks i .. of the k-th one, miss: this lane's block is there and has no page.  The first table entries of four
+// blocks i .. of the k-th one, miss: this lane's block is there and has no page.  The first table entries of eight
 // sequences are fetched at a time.
 template <typename F>
 __device__ __forceinline__ void for_missing(const Kv8Dev& c, int b, int step, int lo, int hi, F visit) {
   constexpr uint32_t kAll = 0xFFFFFFFFu;
+  constexpr int kAhead = 8;
   const int lane = threadIdx.x & 31;
   uint32_t todo = __ballot_sync(kAll, hi > lo);
   while (todo != 0u) {
-    int k[4], l[4], h[4], entry[4];
+    int k[kAhead], entry[kAhead];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kAhead; ++j) {
       k[j] = todo ? __ffs(todo) - 1 : -1;
       todo &= todo - 1u;
-      l[j] = __shfl_sync(kAll, lo, max(k[j], 0));
-      h[j] = k[j] < 0 ? l[j] : __shfl_sync(kAll, hi, k[j]);
-      entry[j] = l[j] + lane < h[j] ? c.table[static_cast<int64_t>(b + k[j] * step) * c.max_blocks + l[j] + lane] : 0;
+      const int l = __shfl_sync(kAll, lo, max(k[j], 0)), h = __shfl_sync(kAll, hi, max(k[j], 0));
+      entry[j] = k[j] >= 0 && l + lane < h ? c.table[static_cast<int64_t>(b + k[j] * step) * c.max_blocks + l + lane] : 0;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (k[j] < 0) continue;
-      visit(k[j], l[j], entry[j] < 0);
+    for (int j = 0; j < kAhead; ++j) {
+      if (k[j] < 0) break;
+      const int l = __shfl_sync(kAll, lo, k[j]), h = __shfl_sync(kAll, hi, k[j]);
+      visit(k[j], l, entry[j] < 0);
       const int32_t* row = c.table + static_cast<int64_t>(b + k[j] * step) * c.max_blocks;
-      for (int i = l[j] + 32; i < h[j]; i += 32) visit(k[j], i, i + lane < h[j] && row[i + lane] < 0);
+      for (int i = l + 32; i < h; i += 32) visit(k[j], i, i + lane < h && row[i + lane] < 0);
     }
   }
 }
@@ -162,6 +163,9 @@ __global__ void __launch_bounds__(kPgThreads) kv8_reserve_kernel(Kv8Dev c, const
     total += sum;
   }
   if (total == 0) return;
+  // this warp's first sequences, under way while the pages are listed
+  int lo0 = 0, hi0 = 0;
+  if (warp + lane * (kPgThreads / 32) < c.batch) fill_range(c, cu, warp + lane * (kPgThreads / 32), &lo0, &hi0);
   // ---- the lowest free pages, as many as are lacking
   int32_t* list = c.work + w.list_a;
   int found = 0;
@@ -186,12 +190,13 @@ __global__ void __launch_bounds__(kPgThreads) kv8_reserve_kernel(Kv8Dev c, const
   __syncthreads();
   // ---- into the table
   for (int b0 = warp; b0 < c.batch; b0 += 32 * (kPgThreads / 32)) {
-    int lo = 0, hi = 0, rank = 0;
+    int lo = lo0, hi = hi0, rank = 0;
     const int b = b0 + lane * (kPgThreads / 32);
-    if (b < c.batch) {
-      fill_range(c, cu, b, &lo, &hi);
-      rank = need[b];
+    if (b0 != warp) {
+      lo = hi = 0;
+      if (b < c.batch) fill_range(c, cu, b, &lo, &hi);
     }
+    if (b < c.batch) rank = need[b];
     for_missing(c, b0, kPgThreads / 32, lo, hi, [&](int k, int i, bool miss) {
       const uint32_t m = __ballot_sync(0xFFFFFFFFu, miss);
       const int at = __shfl_sync(0xFFFFFFFFu, rank, k) + __popc(m & ((1u << lane) - 1u));
