@@ -569,7 +569,8 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, turns
     dim], BF16, FP16 or FP32, channels contiguous, other strides free; positions: int32 or int64, [tokens] or
     [batch, tokens]; turns: rope_turns(...), one for each pair of the rotated channels (the first
     2 * turns.numel() of a head; the others are copied).  Pairs are (j, j + half) or, interleaved, (2j, 2j + 1).
-    q_out, k_out: default in place.  inverse turns the other way: the gradient of the call without it."""
+    q_out, k_out: default in place.  inverse turns the other way: the gradient of the call without it (autograd does
+    not see either)."""
     dtype, index = q.dtype, q.get_device()
     code = _DTYPES.get(dtype)
     if code is None:

@@ -6,8 +6,8 @@
 // rows; nothing ever has to be copied on a write.
 //
 // All of it is bound by latency but the moves of a compaction, which are bound by memory.  Measured: release of 8 of
-// 32 sequences 1.3 us, fork of as many 4.9 us (one CTA a pair: 8.5 us), reserve without a need 4.1 us (65,536 pages:
-// 4.3 us), with 4,096 pages handed to 256 sequences 10.5 us; moving 2,000 pages of 8 heads (0.54 GB read and written)
+// 32 sequences 1.3 us, fork of as many 4.9 us (one CTA a pair: 8.5 us), reserve without a need 3.5 us (65,536 pages:
+// 4.3 us), with 4,000 pages handed to 256 sequences 9.7 us; moving 2,000 pages of 8 heads (0.54 GB read and written)
 // 77 us, 6.9 TB/s (1,216 CTAs that walk over the moves: 92 us).
 #include <algorithm>
 
