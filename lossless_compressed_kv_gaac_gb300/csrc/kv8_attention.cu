@@ -532,8 +532,23 @@ __device__ __forceinline__ bool ka_fold_all(const KaArgs& a, KaSmem& sm, const f
           o1[k] = __ldcg(reinterpret_cast<const float4*>(p + 3 * kKaRows + row * (kD - 1) + ch));
         }
       }
+      float mn = m, vn = mv;
 #pragma unroll
-      for (int k = 0; k < kKaJoin; ++k) ka_fold(m, l, mv, o, m1[k], l1[k], mv1[k], o1[k]);
+      for (int k = 0; k < kKaJoin; ++k) {
+        mn = fmaxf(mn, m1[k]);
+        vn = fmaxf(vn, mv1[k]);
+      }
+      const float z = ka_finite(mn), zv = ka_finite(vn), f = ka_exp2(mv - zv);
+      l *= ka_exp2(m - z);
+      o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+      for (int k = 0; k < kKaJoin; ++k) {
+        l += l1[k] * ka_exp2(m1[k] - z);
+        const float g = ka_exp2(mv1[k] - zv);
+        o.x += g * o1[k].x, o.y += g * o1[k].y, o.z += g * o1[k].z, o.w += g * o1[k].w;
+      }
+      m = mn;
+      mv = vn;
     }
     if (share > 0) {
       *reinterpret_cast<float4*>(&sm.state[share][row][ch]) = o;
