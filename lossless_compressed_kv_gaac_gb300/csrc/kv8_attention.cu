@@ -27,9 +27,9 @@
 //    weight is 2^15 and those down to 2^-29 of it keep f16's 11 bits.  For f16 and fp32 results what the rounding
 //    leaves follows as a second operand.  m, l, M and O are fp32.
 //  * The open block is multiplied in its own type, the weights always in two parts.
-// Measured (bf16 or fp16 result): 32 sequences of 4,096-32,768 tokens, 8 kv-heads, 1.2 GB: 176 us, 6.9 TB/s; one of
-// 65,536 tokens: 25.4 us, of which 3 us go by before the first data and 4 us from the last to the joined result; one
-// of 777 tokens: 8.5 us.
+// Measured (bf16 or fp16 result): 32 sequences of 4,096-32,768 tokens, 8 kv-heads, 1.2 GB: 174 us, 7.0 TB/s; one of
+// 65,536 tokens: 25.2 us, of which 3 us go by before the first data and 4 us from the last to the joined result; one
+// of 777 tokens: 8.3 us.
 #include <cuda.h>
 
 #include <algorithm>
@@ -46,15 +46,15 @@ constexpr int kKaThreads = kKaCompute + 32 * kKaCopyWarps;
 constexpr int kKaStages = 10;                // unit i uses stage i % stages and belongs to group i % groups
 constexpr int kKaHalf = kBlock / 2;          // tokens of an open block's unit
 constexpr int kKaRows = 8;                   // query heads per kv-head in the MMA columns
-// Fewer units than this are not worth a CTA: 1 x 777 tokens 8.5 us (five: 8.9), 1 x 2,000 9.0 us (five: 9.4), and with
-// two, 4 x 500 tokens 13.7 us (four: 9.0), where the pieces no longer fit pair by pair.
+// Fewer units than this are not worth a CTA: 1 x 777 tokens 8.3 us (five: 8.9), 4 x 500 8.8 us (five: 9.2; two:
+// 13.7, where the pieces no longer fit pair by pair).
 constexpr int kKaMinUnits = 4;
 // Most units of a pair that one group may take alone (at most 32).  256 x 1,000 tokens, 17 units a pair: 96 us; left to
 // all groups, with sixteen here, 7% more; 32 makes no difference where it was measured.
 constexpr unsigned kKaSolo = 20;
 constexpr int kKaStride = kD + 4;            // floats per row of a warp's state in shared memory (bank spread)
 constexpr int kKaPart = 3 * kKaRows + kKaRows * kD;  // floats of a partial: m, l, M, O
-// Partials in flight when they are joined: 1 x 65,536 tokens 27.0 us (with eight 28.5, with twelve 28.1).
+// Partials in flight when they are joined: 1 x 65,536 tokens 25.2 us (with eight 26.6, with twelve 26.0).
 constexpr int kKaJoin = 10;
 constexpr uint32_t kKaFull = 0xFFFFFFFFu;
 static_assert(kKaStages % kKaGroups == 0, "a stage belongs to one group, which waits for all of its phases in turn");
