@@ -516,8 +516,8 @@ GAAC_API int gaac_rope(const gaac_rope_tensor* tensors, int n_tensors, int dtype
  *  work      gaac_kv8_workspace(batch, n_pages) bytes, 16-byte aligned, zero before the first
  *            call; calls on one cache are ordered on the GPU (one stream, or events)
  * batch <= 65535, n_kv_heads <= 1024, 128 * n_kv_heads * n_pages < 2^31 and the same for batch.
- * Only full blocks have pages, and a full block never changes; lengths, tables and counts change
- * through the calls below only.  A new cache has seq_lens and refs 0 and table -1. */
+ * A full block has a page, and so may blocks reserved ahead; a full block never changes.  Lengths,
+ * tables and counts change through the calls below only.  A new cache has seq_lens and refs 0 and table -1. */
 typedef struct {
   uint8_t* pages;
   float* scales;

@@ -263,6 +263,17 @@ def test_attention_cuts(lens, heads, group):
     assert (c._ws[:3 * 152 * 4].view(torch.int32) == 0).all()  # counters are back at zero
 
 
+def test_attention_thousands_of_sequences_and_many_heads():
+    lens = [(29 * i) % 150 for i in range(6000)]
+    c, _, _ = filled(lens, 1)
+    q = rand((6000, 2, 128), BF16, 5)
+    U.check_attention(c, q, SCALE, c.attention(q, SCALE))
+    c, _, _ = filled([70, 0, 2000], 96, E5, F16)
+    q = rand((3, 96 * 3, 128), F16, 5)
+    U.check_attention(c, q, SCALE, c.attention(q, SCALE))
+    assert ok(c) == 0
+
+
 def test_attention_scales_far_apart():
     """V scales 2^-40 .. 2^40 apart between blocks, K scales 2^-6 .. 2^6, and scores that favour either end."""
     c, _, _ = filled([64 * 40 + 7] * 3, 2)
