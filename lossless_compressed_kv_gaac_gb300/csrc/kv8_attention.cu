@@ -27,9 +27,9 @@
 //    weight is 2^15 and those down to 2^-29 of it keep f16's 11 bits.  For f16 and fp32 results what the rounding
 //    leaves follows as a second operand.  m, l, M and O are fp32.
 //  * The open block is multiplied in its own type, the weights always in two parts.
-// Measured (bf16 or fp16 result): 32 sequences of 4,096-32,768 tokens, 8 kv-heads, 1.2 GB: 174 us, 7.0 TB/s; one of
-// 65,536 tokens: 25.2 us, of which 3 us go by before the first data and 4 us from the last to the joined result; one
-// of 777 tokens: 8.3 us.
+// Measured (bf16 or fp16 result): 32 sequences of 4,096-32,768 tokens, 8 kv-heads, 1.2 GB: 175 us, 6.9 TB/s; one of
+// 65,536 tokens: 24.6 us, of which 3 us go by before the first data and 4 us from the last to the joined result; one
+// of 777 tokens: 7.9 us.
 #include <cuda.h>
 
 #include <algorithm>
@@ -54,7 +54,7 @@ constexpr int kKaMinUnits = 4;
 constexpr unsigned kKaSolo = 20;
 constexpr int kKaStride = kD + 4;            // floats per row of a warp's state in shared memory (bank spread)
 constexpr int kKaPart = 3 * kKaRows + kKaRows * kD;  // floats of a partial: m, l, M, O
-// Partials in flight when they are joined: 1 x 65,536 tokens 25.2 us (with eight 26.6, with twelve 26.0).
+// Partials in flight when they are joined: 1 x 65,536 tokens then 25.2 us (with eight 26.6, with twelve 26.0).
 constexpr int kKaJoin = 10;
 constexpr uint32_t kKaFull = 0xFFFFFFFFu;
 static_assert(kKaStages % kKaGroups == 0, "a stage belongs to one group, which waits for all of its phases in turn");
@@ -187,61 +187,102 @@ struct KaCut {
   unsigned seg, u, u_end;    // in units: the pair's first, this CTA's first and its end
 };
 
-// By a whole warp.  The lengths come from L2, so that a call ahead of the dependent-launch wait leaves nothing stale.
+// Places of 1,024 sequences from b0 on: lane j gets the sum over sequences b0 + 32 j .. + 31.  piece: units per place.
+// The lengths come from L2, so that a call ahead of the dependent-launch wait leaves nothing stale; eight loads are in
+// flight.
+__device__ __forceinline__ unsigned ka_sums(const Kv8Dev& c, int b0, unsigned piece, int32_t* status) {
+  constexpr int kAhead = 8;
+  const int lane = threadIdx.x & 31, chunks = min(32, (c.batch - b0 + 31) / 32);
+  unsigned mine = 0;
+#pragma unroll 1
+  for (int j0 = 0; j0 < chunks; j0 += kAhead) {
+    int len[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = b0 + 32 * (j0 + j) + lane;
+      len[j] = j0 + j < chunks && i < c.batch ? __ldcg(c.lens + i) : -1;
+      if (status != nullptr && j0 + j < chunks && i < c.batch &&
+          (len[j] < 0 || len[j] > static_cast<int64_t>(c.max_blocks) * kBlock))
+        report(status, GAAC_EINVAL);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (j0 + j >= chunks) break;
+      const unsigned u = b0 + 32 * (j0 + j) + lane < c.batch ? (ka_seq(c, len[j]).units + piece - 1) / piece : 0u;
+      const unsigned sum = __reduce_add_sync(kKaFull, u);  // 32 sequences of up to 2^24 + 1 units: 30 bits
+      if (lane == j0 + j) mine = sum;
+    }
+  }
+  return mine;
+}
+
+__device__ __forceinline__ unsigned ka_scan(unsigned v, int lane) {  // inclusive
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned x = __shfl_up_sync(kKaFull, v, d);
+    if (lane >= d) v += x;
+  }
+  return v;
+}
+
+// By a whole warp.  FEW: at most 32 sequences, one a lane, whose lengths are read once (by ka_sums one sequence of 777
+// tokens takes 9.2 us, so 7.9).
+template <bool FEW>
 __device__ __forceinline__ KaCut ka_cut(const Kv8Dev& c, int32_t* status) {
   const int lane = threadIdx.x & 31;
+  if (blockIdx.x != 0) status = nullptr;  // one CTA reports lengths that are not valid
   // ---- the cut: pieces of at most `piece` units (all counts below 2^31: the host has checked)
-  unsigned total = 0;
-  int len32 = 0;  // lengths of 32 sequences, one a lane
-  for (int b0 = 0; b0 < c.batch; b0 += 32) {
-    unsigned u = 0;
-    if (b0 + lane < c.batch) {
-      const int len = len32 = __ldcg(c.lens + b0 + lane);
-      if (status != nullptr && blockIdx.x == 0 && (len < 0 || len > static_cast<int64_t>(c.max_blocks) * kBlock)) report(status, GAAC_EINVAL);
-      u = ka_seq(c, len).units;
+  unsigned sums = 0, total = 0;  // FEW: this lane's sequence; else ka_sums
+  int len32 = 0;
+  if (FEW) {
+    if (lane < c.batch) {
+      len32 = __ldcg(c.lens + lane);
+      if (status != nullptr && (len32 < 0 || len32 > static_cast<int64_t>(c.max_blocks) * kBlock)) report(status, GAAC_EINVAL);
+      sums = ka_seq(c, len32).units;
     }
-    total += __reduce_add_sync(kKaFull, u) * c.heads;
+    total = __reduce_add_sync(kKaFull, sums) * c.heads;
+  } else {
+    for (int b0 = 0; b0 < c.batch; b0 += 1024) {
+      sums = ka_sums(c, b0, 1u, status);
+      total += __reduce_add_sync(kKaFull, sums) * c.heads;
+    }
   }
   const unsigned piece = max(static_cast<unsigned>(kKaMinUnits), (total + gridDim.x - 1) / gridDim.x);
   // Pieces begin with their pair where that needs no more CTAs: then none has parts of two pairs to bring to an
   // end.  Otherwise the row of all units is cut without regard to pairs.
   bool aligned = false;
   if (static_cast<unsigned>(c.batch) * c.heads <= gridDim.x) {
-    unsigned pieces = 0;
-    for (int b0 = 0; b0 < c.batch; b0 += 32) {
-      const int len = c.batch <= 32 ? len32 : b0 + lane < c.batch ? __ldcg(c.lens + b0 + lane) : 0;
-      pieces += __reduce_add_sync(kKaFull, b0 + lane < c.batch ? (ka_seq(c, len).units + piece - 1) / piece : 0u) * c.heads;
-    }
-    aligned = pieces <= gridDim.x;
+    const unsigned pieces = FEW ? (sums + piece - 1) / piece : ka_sums(c, 0, piece, nullptr);
+    aligned = __reduce_add_sync(kKaFull, pieces) * c.heads <= gridDim.x;
+    if (aligned) sums = pieces;
   }
   // In places (units, or pieces when aligned): where this CTA begins and ends.
   const unsigned begin = aligned ? blockIdx.x : blockIdx.x * piece;
-  int b = c.batch;
+  int b = c.batch, b32 = 0;
   unsigned base = 0;  // places before sequence b
-  int b32 = -1;
-  for (int b0 = 0; b0 < c.batch; b0 += 32) {
-    const int len = c.batch <= 32 ? len32 : b0 + lane < c.batch ? __ldcg(c.lens + b0 + lane) : 0;
-    unsigned u = 0;
-    if (b0 + lane < c.batch) {
-      u = ka_seq(c, len).units;
-      u = (aligned ? (u + piece - 1) / piece : u) * c.heads;
+  if (!FEW) {         // the 32 sequences that it begins in
+    const unsigned per = aligned ? piece : 1u;
+    for (int b0 = 0; b0 < c.batch; b0 += 1024) {
+      if (c.batch > 1024) sums = ka_sums(c, b0, 1u, nullptr);
+      const unsigned incl = ka_scan(sums, lane);
+      const uint32_t past = __ballot_sync(kKaFull, base + incl * c.heads > begin);
+      const int at = past ? __ffs(past) - 1 : 31;
+      base += __shfl_sync(kKaFull, past ? incl - sums : incl, at) * c.heads;
+      if (past) {
+        b32 = b0 + 32 * at;
+        len32 = b32 + lane < c.batch ? __ldcg(c.lens + b32 + lane) : 0;
+        sums = b32 + lane < c.batch ? (ka_seq(c, len32).units + per - 1) / per : 0u;
+        break;
+      }
+      if (b0 + 1024 >= c.batch) sums = 0u;  // it begins behind all of them
     }
-    unsigned incl = u;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const unsigned v = __shfl_up_sync(kKaFull, incl, d);
-      if (lane >= d) incl += v;
-    }
-    const uint32_t past = __ballot_sync(kKaFull, base + incl > begin);
-    if (past) {
-      const int at = __ffs(past) - 1;
-      base += __shfl_sync(kKaFull, incl - u, at);
-      b = b0 + at;
-      len32 = len;
-      b32 = b0;
-      break;
-    }
-    base += __shfl_sync(kKaFull, incl, 31);
+  }
+  const unsigned incl = ka_scan(sums, lane);
+  const uint32_t past = __ballot_sync(kKaFull, base + incl * c.heads > begin);
+  if (past) {
+    const int at = __ffs(past) - 1;
+    base += __shfl_sync(kKaFull, incl - sums, at) * c.heads;
+    b = b32 + at;
   }
   KaSeq s = {};
   int h = 0;
@@ -265,7 +306,10 @@ __device__ __forceinline__ KaCut ka_cut(const Kv8Dev& c, int32_t* status) {
 __device__ __forceinline__ void ka_guess(const KaArgs& a) {
   const Kv8Dev& c = a.c;
   const int lane = threadIdx.x & 31;
-  const KaCut cut = ka_cut(c, nullptr);
+  // More than 32 sequences: guessing as well takes 256 x 1,000 tokens from 96.6 to 95.2 us and, by the code that it
+  // needs, 1 x 65,536 from 24.6 to 24.9; it is left to calls where the start is a larger part.
+  if (c.batch > 32) return;
+  const KaCut cut = ka_cut<true>(c, nullptr);
   const int l = static_cast<int>(cut.u - cut.seg) + lane;
   if (cut.b < c.batch && lane < kKaStages && cut.u + lane < cut.u_end && l < cut.s.full) {
     const int32_t page = __ldcg(c.table + static_cast<int64_t>(cut.b) * c.max_blocks + l);
@@ -282,7 +326,7 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
   constexpr int kOwn = kKaStages / kKaCopyWarps;
   const Kv8Dev& c = a.c;
   const int lane = threadIdx.x & 31;
-  const KaCut cut = ka_cut(c, a.status);
+  const KaCut cut = c.batch <= 32 ? ka_cut<true>(c, a.status) : ka_cut<false>(c, a.status);
   KaSeq s = cut.s;
   int b = cut.b, h = cut.h, b32 = cut.b32, len32 = cut.len32;
   unsigned seg = cut.seg, u = cut.u, u_end = cut.u_end;

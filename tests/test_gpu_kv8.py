@@ -274,6 +274,23 @@ def test_attention_thousands_of_sequences_and_many_heads():
     assert ok(c) == 0
 
 
+@pytest.mark.parametrize("batch", (31, 32, 33, 64, 65, 150, 255, 257, 1023, 1024, 1025, 2049))
+def test_attention_sequence_counts(batch):
+    """Where lengths are read by 32, by 256 and by 1,024; empty sequences at the ends, one long among them."""
+    lens = [0 if i % 7 == 3 else (37 * i) % 131 for i in range(batch)]
+    lens[0] = lens[-1] = 0
+    lens[batch // 2] = 64 * 23 + 5
+    c, _, _ = filled(lens, 1)
+    q = rand((batch, 2, 128), BF16, batch)
+    U.check_attention(c, q, SCALE, c.attention(q, SCALE))
+    # Only the last has tokens; then none: the results are zeros.
+    c, _, _ = filled([0] * (batch - 1) + [130], 1)
+    U.check_attention(c, q, SCALE, c.attention(q, SCALE))
+    c, _, _ = filled([0] * batch, 1)
+    assert (c.attention(q, SCALE) == 0).all()
+    assert ok(c) == 0
+
+
 def test_attention_scales_far_apart():
     """V scales 2^-40 .. 2^40 apart between blocks, K scales 2^-6 .. 2^6, and scores that favour either end."""
     c, _, _ = filled([64 * 40 + 7] * 3, 2)
