@@ -75,7 +75,11 @@ struct KaSmem {
   int32_t side_page[kKaCopyWarps][kKaGroups][kKaSolo];
   uint64_t full[kKaStages], empty[kKaStages], sync, pair_sync[kKaGroups];
   int last;
+  // Units of each 32 sequences, while the work is cut and there are no states yet.
+  static constexpr int kPlaces = 65536 / 32;
+  __device__ unsigned* places() { return reinterpret_cast<unsigned*>(state); }
 };
+static_assert(sizeof(KaSmem::state) >= KaSmem::kPlaces * sizeof(unsigned), "places in the states' room");
 
 struct KaArgs {
   Kv8Dev c;
@@ -187,33 +191,29 @@ struct KaCut {
   unsigned seg, u, u_end;    // in units: the pair's first, this CTA's first and its end
 };
 
-// Places of 1,024 sequences from b0 on: lane j gets the sum over sequences b0 + 32 j .. + 31.  piece: units per place.
-// The lengths come from L2, so that a call ahead of the dependent-launch wait leaves nothing stale; eight loads are in
-// flight.
-__device__ __forceinline__ unsigned ka_sums(const Kv8Dev& c, int b0, unsigned piece, int32_t* status) {
+// Places of chunks of 32 sequences, piece units per place: put(j, sum) for chunks j0, j0 + step, ...  The lengths come
+// from L2, so that a call ahead of the dependent-launch wait leaves nothing stale; eight loads are in flight.
+template <class Put>
+__device__ __forceinline__ void ka_sums(const Kv8Dev& c, int j0, int step, unsigned piece, int32_t* status, Put put) {
   constexpr int kAhead = 8;
-  const int lane = threadIdx.x & 31, chunks = min(32, (c.batch - b0 + 31) / 32);
-  unsigned mine = 0;
+  const int lane = threadIdx.x & 31, chunks = (c.batch + 31) / 32;
 #pragma unroll 1
-  for (int j0 = 0; j0 < chunks; j0 += kAhead) {
+  for (; j0 < chunks; j0 += kAhead * step) {
     int len[kAhead];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int i = b0 + 32 * (j0 + j) + lane;
-      len[j] = j0 + j < chunks && i < c.batch ? __ldcg(c.lens + i) : -1;
-      if (status != nullptr && j0 + j < chunks && i < c.batch &&
-          (len[j] < 0 || len[j] > static_cast<int64_t>(c.max_blocks) * kBlock))
-        report(status, GAAC_EINVAL);
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t i = 32 * (j0 + static_cast<int64_t>(k) * step) + lane;
+      len[k] = i < c.batch ? __ldcg(c.lens + i) : 0;
+      if (status != nullptr && (len[k] < 0 || len[k] > static_cast<int64_t>(c.max_blocks) * kBlock)) report(status, GAAC_EINVAL);
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (j0 + j >= chunks) break;
-      const unsigned u = b0 + 32 * (j0 + j) + lane < c.batch ? (ka_seq(c, len[j]).units + piece - 1) / piece : 0u;
-      const unsigned sum = __reduce_add_sync(kKaFull, u);  // 32 sequences of up to 2^24 + 1 units: 30 bits
-      if (lane == j0 + j) mine = sum;
+    for (int k = 0; k < kAhead; ++k) {
+      const int j = j0 + k * step;
+      if (j >= chunks) break;
+      const unsigned u = 32 * j + lane < c.batch ? (ka_seq(c, len[k]).units + piece - 1) / piece : 0u;
+      put(j, __reduce_add_sync(kKaFull, u));  // 32 sequences of up to 2^24 + 1 units: 30 bits
     }
   }
-  return mine;
 }
 
 __device__ __forceinline__ unsigned ka_scan(unsigned v, int lane) {  // inclusive
@@ -225,14 +225,16 @@ __device__ __forceinline__ unsigned ka_scan(unsigned v, int lane) {  // inclusiv
   return v;
 }
 
-// By a whole warp.  FEW: at most 32 sequences, one a lane, whose lengths are read once (by ka_sums one sequence of 777
-// tokens takes 9.2 us, so 7.9).
+// By a whole warp.  FEW: at most 32 sequences, one a lane, whose lengths are read once (as many sequences are, one of 777
+// tokens takes 9.2 us, so 7.9).  Else places: the units of each 32 sequences, which all warps have added up (each copy
+// warp for itself: 5,000 sequences of 100 tokens, 1 kv-head, take 160 us, so 105).
 template <bool FEW>
-__device__ __forceinline__ KaCut ka_cut(const Kv8Dev& c, int32_t* status) {
+__device__ __forceinline__ KaCut ka_cut(const Kv8Dev& c, const unsigned* places, int32_t* status) {
   const int lane = threadIdx.x & 31;
   if (blockIdx.x != 0) status = nullptr;  // one CTA reports lengths that are not valid
   // ---- the cut: pieces of at most `piece` units (all counts below 2^31: the host has checked)
-  unsigned sums = 0, total = 0;  // FEW: this lane's sequence; else ka_sums
+  const int chunks = (c.batch + 31) / 32;
+  unsigned sums = 0, total;  // sums, FEW: this lane's sequence's
   int len32 = 0;
   if (FEW) {
     if (lane < c.batch) {
@@ -240,19 +242,22 @@ __device__ __forceinline__ KaCut ka_cut(const Kv8Dev& c, int32_t* status) {
       if (status != nullptr && (len32 < 0 || len32 > static_cast<int64_t>(c.max_blocks) * kBlock)) report(status, GAAC_EINVAL);
       sums = ka_seq(c, len32).units;
     }
-    total = __reduce_add_sync(kKaFull, sums) * c.heads;
+    total = sums;
   } else {
-    for (int b0 = 0; b0 < c.batch; b0 += 1024) {
-      sums = ka_sums(c, b0, 1u, status);
-      total += __reduce_add_sync(kKaFull, sums) * c.heads;
-    }
+    total = 0;
+    for (int j = lane; j < chunks; j += 32) total += places[j];
   }
+  total = __reduce_add_sync(kKaFull, total) * c.heads;
   const unsigned piece = max(static_cast<unsigned>(kKaMinUnits), (total + gridDim.x - 1) / gridDim.x);
   // Pieces begin with their pair where that needs no more CTAs: then none has parts of two pairs to bring to an
   // end.  Otherwise the row of all units is cut without regard to pairs.
   bool aligned = false;
-  if (static_cast<unsigned>(c.batch) * c.heads <= gridDim.x) {
-    const unsigned pieces = FEW ? (sums + piece - 1) / piece : ka_sums(c, 0, piece, nullptr);
+  if (static_cast<unsigned>(c.batch) * c.heads <= min(gridDim.x, 1024u)) {
+    unsigned pieces = (sums + piece - 1) / piece;  // else of a chunk: there are no more of them than lanes
+    if (!FEW)
+      ka_sums(c, 0, 1, piece, nullptr, [&](int j, unsigned sum) {
+        if (lane == j) pieces = sum;
+      });
     aligned = __reduce_add_sync(kKaFull, pieces) * c.heads <= gridDim.x;
     if (aligned) sums = pieces;
   }
@@ -262,19 +267,22 @@ __device__ __forceinline__ KaCut ka_cut(const Kv8Dev& c, int32_t* status) {
   unsigned base = 0;  // places before sequence b
   if (!FEW) {         // the 32 sequences that it begins in
     const unsigned per = aligned ? piece : 1u;
-    for (int b0 = 0; b0 < c.batch; b0 += 1024) {
-      if (c.batch > 1024) sums = ka_sums(c, b0, 1u, nullptr);
-      const unsigned incl = ka_scan(sums, lane);
+    for (int j0 = 0;; j0 += 32) {
+      if (j0 >= chunks) {
+        sums = 0;  // it begins behind all of them
+        break;
+      }
+      const unsigned v = aligned ? sums : j0 + lane < chunks ? places[j0 + lane] : 0u;
+      const unsigned incl = ka_scan(v, lane);
       const uint32_t past = __ballot_sync(kKaFull, base + incl * c.heads > begin);
       const int at = past ? __ffs(past) - 1 : 31;
-      base += __shfl_sync(kKaFull, past ? incl - sums : incl, at) * c.heads;
+      base += __shfl_sync(kKaFull, past ? incl - v : incl, at) * c.heads;
       if (past) {
-        b32 = b0 + 32 * at;
+        b32 = 32 * (j0 + at);
         len32 = b32 + lane < c.batch ? __ldcg(c.lens + b32 + lane) : 0;
         sums = b32 + lane < c.batch ? (ka_seq(c, len32).units + per - 1) / per : 0u;
         break;
       }
-      if (b0 + 1024 >= c.batch) sums = 0u;  // it begins behind all of them
     }
   }
   const unsigned incl = ka_scan(sums, lane);
@@ -309,7 +317,7 @@ __device__ __forceinline__ void ka_guess(const KaArgs& a) {
   // More than 32 sequences: guessing as well takes 256 x 1,000 tokens from 96.6 to 95.2 us and, by the code that it
   // needs, 1 x 65,536 from 24.6 to 24.9; it is left to calls where the start is a larger part.
   if (c.batch > 32) return;
-  const KaCut cut = ka_cut<true>(c, nullptr);
+  const KaCut cut = ka_cut<true>(c, nullptr, nullptr);
   const int l = static_cast<int>(cut.u - cut.seg) + lane;
   if (cut.b < c.batch && lane < kKaStages && cut.u + lane < cut.u_end && l < cut.s.full) {
     const int32_t page = __ldcg(c.table + static_cast<int64_t>(cut.b) * c.max_blocks + l);
@@ -326,7 +334,8 @@ __device__ void ka_copy_warp(const KaArgs& a, KaSmem& sm, const CUtensorMap* pag
   constexpr int kOwn = kKaStages / kKaCopyWarps;
   const Kv8Dev& c = a.c;
   const int lane = threadIdx.x & 31;
-  const KaCut cut = c.batch <= 32 ? ka_cut<true>(c, a.status) : ka_cut<false>(c, a.status);
+  const KaCut cut = c.batch <= 32 ? ka_cut<true>(c, nullptr, a.status) : ka_cut<false>(c, sm.places(), nullptr);
+  if (c.batch > 32) __syncthreads();  // the places are read
   KaSeq s = cut.s;
   int b = cut.b, h = cut.h, b32 = cut.b32, len32 = cut.len32;
   unsigned seg = cut.seg, u = cut.u, u_end = cut.u_end;
@@ -999,10 +1008,19 @@ __global__ void __launch_bounds__(kKaThreads, 1)
   if (threadIdx.x < 32) ka_guess(a);  // a compute warp: it has nothing to do before the first data
   dependent_wait();
   dependent_launch();
-  if (threadIdx.x >= 32 * kKaWarps)
+  if (a.c.batch > 32) {  // all warps add up the units (see ka_cut)
+    unsigned* places = sm.places();
+    ka_sums(a.c, threadIdx.x / 32, kKaThreads / 32, 1u, blockIdx.x == 0 ? a.status : nullptr, [&](int j, unsigned sum) {
+      if (threadIdx.x % 32 == 0) places[j] = sum;
+    });
+    __syncthreads();
+  }
+  if (threadIdx.x >= 32 * kKaWarps) {
     ka_copy_warp(a, sm, &pages, &tail, threadIdx.x / 32 - kKaWarps);
-  else
+  } else {
+    if (a.c.batch > 32) __syncthreads();  // the copy warps have read them
     ka_compute<HALF, FMT, FINE>(a, sm);
+  }
 }
 
 // ------------------------------------------------------------------ host
