@@ -69,6 +69,7 @@ struct KaSmem {
   alignas(16) int4 meta[kKaStages][2];  // {kind, first of the pair in its group (2: with queries), last, tokens}, {b, h, first CTA, CTAs}
   alignas(16) float2 scale[kKaStages];
   float m[kKaWarps][kKaRows], l[kKaWarps][kKaRows], mv[kKaWarps][kKaRows];
+  alignas(16) float solo[2][kKaWarps][3][kKaRows];  // m, l, M of pairs that groups end alone
   // pairs side by side, for each copy warp: {full blocks, open tokens, b, h}, units, pages
   alignas(16) int4 side[kKaCopyWarps][kKaGroups];
   int side_units[kKaCopyWarps][kKaGroups];
@@ -537,6 +538,15 @@ __device__ __forceinline__ void ka_store(const KaArgs& a, int b, int h, int row,
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(ka_pack_bf16(y.x, y.y), ka_pack_bf16(y.z, y.w));
 }
 
+template <bool HALF>
+__device__ __forceinline__ void ka_store2(const KaArgs& a, int b, int h, int row, int ch, float y0, float y1) {
+  const int64_t at = (static_cast<int64_t>(b) * a.c.heads + h) * a.r * kD + row * kD + ch;
+  if (a.out_f32)
+    *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = make_float2(y0, y1);
+  else
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) = HALF ? ka_pack_f16(y0, y1) : ka_pack_bf16(y0, y1);
+}
+
 // O, in units of 2^M, over the sum l, in units of 2^m: halves of the exponent on either side of the division, so
 // that neither leaves fp32 before the result does.
 __device__ __forceinline__ float4 ka_result(float4 o, float m, float l, float mv) {
@@ -709,6 +719,8 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, tq = lane & 3;
   const int warp = tid >> 5, part = warp & 1;  // part: which half of a unit's tokens
   KaSync meet, meet_pair;
+  int turn = 0;
+  bool gave = false;
   int stage = warp >> 1;
   uint32_t phase = 0;
   uint32_t qf[8][2];       // q^T operand: row g, channels 16 j + 4 tq .. + 3 of k-step j
@@ -929,7 +941,6 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
 
     // ---- the end of the pair in this CTA
     if (last) {
-      const bool solo = last == kLastSolo;
       const int4 pair = sm.meta[stage][1];
       const int b = pair.x, h = pair.y, cta0 = pair.z, n_cta = pair.w;
 #pragma unroll
@@ -937,46 +948,98 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
         l[0] += __shfl_xor_sync(kKaFull, l[0], d);
         l[1] += __shfl_xor_sync(kKaFull, l[1], d);
       }
-      if (g == 0) {
+      if (last == kLastSolo) {
+        // The group's two warps exchange halves: this one ends channels 64 part .. + 63, from its registers and the
+        // other's state (5,000 x 100 tokens, 1 kv-head: 87 us; through shared memory as below 105).  Two buffers in
+        // turn, so that one meeting a pair is enough.
+        float(&st)[3][kKaRows] = sm.solo[turn][warp];
+        const float(&st1)[3][kKaRows] = sm.solo[turn][warp ^ 1];
+        float4* give = reinterpret_cast<float4*>(sm.state[warp]) + 128 * turn + lane;
+        const float4* got = reinterpret_cast<const float4*>(sm.state[warp ^ 1]) + 128 * turn + lane;
+        if (g == 0) {
+          *reinterpret_cast<float2*>(&st[0][2 * tq]) = make_float2(m[0], m[1]);
+          *reinterpret_cast<float2*>(&st[1][2 * tq]) = make_float2(l[0], l[1]);
+          *reinterpret_cast<float2*>(&st[2][2 * tq]) = make_float2(mv[0], mv[1]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          give[32 * k] = part ? make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3])
+                              : make_float4(acc[4 + k][0], acc[4 + k][1], acc[4 + k][2], acc[4 + k][3]);
+        if (!ka_meet_at(&sm.pair_sync[warp >> 1], meet_pair, a.status)) return;
+        const float2 m1 = *reinterpret_cast<const float2*>(&st1[0][2 * tq]), l1 = *reinterpret_cast<const float2*>(&st1[1][2 * tq]),
+                     mv1 = *reinterpret_cast<const float2*>(&st1[2][2 * tq]);
+        bool none[2];
+        float f0[2], f1[2], e0[2], e1[2];  // O = f0 o + f1 o1 over the sum: O * e0 * e1, as in ka_result
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          sm.m[warp][2 * tq + i] = m[i];
-          sm.l[warp][2 * tq + i] = l[i];
-          sm.mv[warp][2 * tq + i] = mv[i];
+          const float ma = i ? m1.y : m1.x, la = i ? l1.y : l1.x, va = i ? mv1.y : mv1.x;
+          const float mx = fmaxf(m[i], ma), vx = fmaxf(mv[i], va), z = ka_finite(mx), zv = ka_finite(vx);
+          const float den = ka_exp2(m[i] - z) * l[i] + ka_exp2(ma - z) * la;
+          f0[i] = ka_exp2(mv[i] - zv);
+          f1[i] = ka_exp2(va - zv);
+          e1[i] = ka_exp2(0.5f * (zv - z));
+          e0[i] = e1[i] / den;
+          none[i] = den == 0.f;
         }
-      }
+        turn ^= 1;
+        gave = true;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        *reinterpret_cast<float2*>(&sm.state[warp][2 * tq][16 * i + 2 * g]) = make_float2(acc[i][0], acc[i][2]);
-        *reinterpret_cast<float2*>(&sm.state[warp][2 * tq + 1][16 * i + 2 * g]) = make_float2(acc[i][1], acc[i][3]);
-      }
-      if (!(solo ? ka_meet_at(&sm.pair_sync[warp >> 1], meet_pair, a.status) : ka_meet(sm, meet, a.status))) return;
-      // this CTA's part of the pair: the states of all warps, or of the group's two
-      const int w0 = solo ? warp & ~1 : 0, w1 = solo ? w0 + 2 : kKaWarps;
-      for (int at = solo ? tid & 63 : tid; at < a.r * (kD / 4); at += solo ? 64 : kKaCompute) {
-        const int row = at / (kD / 4), ch = 4 * (at % (kD / 4));
-        float mx = -INFINITY, vx = -INFINITY, den = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-        for (int w = w0; w < w1; ++w) {
-          mx = fmaxf(mx, sm.m[w][row]);
-          vx = fmaxf(vx, sm.mv[w][row]);
+        for (int k = 0; k < 4; ++k) {
+          const float4 x = got[32 * k];
+          float y[4] = {part ? acc[4 + k][0] : acc[k][0], part ? acc[4 + k][1] : acc[k][1],
+                        part ? acc[4 + k][2] : acc[k][2], part ? acc[4 + k][3] : acc[k][3]};
+          y[0] = none[0] ? 0.f : (f0[0] * y[0] + f1[0] * x.x) * e0[0] * e1[0];
+          y[1] = none[1] ? 0.f : (f0[1] * y[1] + f1[1] * x.y) * e0[1] * e1[1];
+          y[2] = none[0] ? 0.f : (f0[0] * y[2] + f1[0] * x.z) * e0[0] * e1[0];
+          y[3] = none[1] ? 0.f : (f0[1] * y[3] + f1[1] * x.w) * e0[1] * e1[1];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (2 * tq + i < a.r) ka_store2<HALF>(a, b, h, 2 * tq + i, 64 * part + 16 * k + 2 * g, y[i], y[2 + i]);
         }
-#pragma unroll 2
-        for (int w = w0; w < w1; ++w) {
-          den += ka_exp2(sm.m[w][row] - ka_finite(mx)) * sm.l[w][row];
-          const float f = ka_exp2(sm.mv[w][row] - ka_finite(vx));
-          const float4 x = *reinterpret_cast<const float4*>(&sm.state[w][row][ch]);
-          o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+      } else {
+        // the other warp of the group may still read what this one gave
+        if (gave && !ka_meet_at(&sm.pair_sync[warp >> 1], meet_pair, a.status)) return;
+        gave = false;
+        if (g == 0) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            sm.m[warp][2 * tq + i] = m[i];
+            sm.l[warp][2 * tq + i] = l[i];
+            sm.mv[warp][2 * tq + i] = mv[i];
+          }
         }
-        if (n_cta == 1)
-          ka_store<HALF>(a, b, h, row, ch, ka_result(o, mx, den, vx));
-        else
-          ka_put(a.part + ka_slot(blockIdx.x, cta0) * kKaPart, row, ch, mx, den, vx, o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          *reinterpret_cast<float2*>(&sm.state[warp][2 * tq][16 * i + 2 * g]) = make_float2(acc[i][0], acc[i][2]);
+          *reinterpret_cast<float2*>(&sm.state[warp][2 * tq + 1][16 * i + 2 * g]) = make_float2(acc[i][1], acc[i][3]);
+        }
+        if (!ka_meet(sm, meet, a.status)) return;
+        // this CTA's part of the pair: the states of all warps
+        for (int at = tid; at < a.r * (kD / 4); at += kKaCompute) {
+          const int row = at / (kD / 4), ch = 4 * (at % (kD / 4));
+          float mx = -INFINITY, vx = -INFINITY, den = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+          for (int w = 0; w < kKaWarps; ++w) {
+            mx = fmaxf(mx, sm.m[w][row]);
+            vx = fmaxf(vx, sm.mv[w][row]);
+          }
+#pragma unroll 2
+          for (int w = 0; w < kKaWarps; ++w) {
+            den += ka_exp2(sm.m[w][row] - ka_finite(mx)) * sm.l[w][row];
+            const float f = ka_exp2(sm.mv[w][row] - ka_finite(vx));
+            const float4 x = *reinterpret_cast<const float4*>(&sm.state[w][row][ch]);
+            o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+          }
+          if (n_cta == 1)
+            ka_store<HALF>(a, b, h, row, ch, ka_result(o, mx, den, vx));
+          else
+            ka_put(a.part + ka_slot(blockIdx.x, cta0) * kKaPart, row, ch, mx, den, vx, o);
+        }
+        if (n_cta != 1 && !ka_join<HALF>(a, sm, b, h, cta0, n_cta, meet)) return;
+        // the next pair's state may be written once everybody has read this one's
+        if (!ka_meet(sm, meet, a.status)) return;
       }
-      if (n_cta != 1 && !ka_join<HALF>(a, sm, b, h, cta0, n_cta, meet)) return;
-      // the next pair's state may be written once everybody has read this one's
-      if (!(solo ? ka_meet_at(&sm.pair_sync[warp >> 1], meet_pair, a.status) : ka_meet(sm, meet, a.status))) return;
     }
     __syncwarp();
     if (lane == 0) ka_arrive(&sm.empty[stage]);
