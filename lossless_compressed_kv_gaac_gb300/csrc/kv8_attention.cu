@@ -49,7 +49,7 @@ constexpr int kKaRows = 8;                   // query heads per kv-head in the M
 // Fewer units than this are not worth a CTA: 1 x 777 tokens 8.3 us (five: 8.9), 4 x 500 8.8 us (five: 9.2; two:
 // 13.7, where the pieces no longer fit pair by pair).
 constexpr int kKaMinUnits = 4;
-// Most units of a pair that one group may take alone (at most 32).  256 x 1,000 tokens, 17 units a pair: 96 us; left to
+// Most units of a pair that one group may take alone (at most 32).  256 x 1,000 tokens, 17 units a pair: 95 us; left to
 // all groups, with sixteen here, 7% more; 32 makes no difference where it was measured.
 constexpr unsigned kKaSolo = 20;
 constexpr int kKaStride = kD + 4;            // floats per row of a warp's state in shared memory (bank spread)
