@@ -351,6 +351,31 @@ def test_attention_nan_and_infinite_tokens():
     assert bad[1, :4, 9].all() and bad.sum() == 4
 
 
+def test_attention_short_pairs_results():
+    """Pairs that one group ends alone, between longer ones: every result type, and what is not finite stays put."""
+    lens = [(53 * i) % 190 if i % 40 else 64 * 30 for i in range(161)]
+    for fmt, dtype, group in ((E4, BF16, 4), (E5, F16, 8), (E4, F16, 1)):
+        c, _, _ = filled(lens, 2, fmt, dtype)
+        q = rand((161, 2 * group, 128), dtype, 6)
+        for out in (dtype, torch.float32):
+            U.check_attention(c, q, SCALE, c.attention(q, SCALE, torch.empty(q.shape, dtype=out, device="cuda")))
+    c, _, _ = filled(lens, 2)
+    q = rand((161, 8, 128), BF16, 6)
+    a = c.attention(q, SCALE)
+    assert torch.equal(a, c.attention(q, SCALE))
+    b1 = next(b for b in range(60, 161) if 64 <= lens[b] < 128 and lens[b] % 64)
+    b2 = next(b for b in range(b1 + 1, 161) if 64 < lens[b] < 190 and lens[b] % 64 > 3)
+    c.pages[int(c.table[b1, 0]), 1, 0, 3, 5] = 0x7F  # a key of head 1
+    c.tail[b2, 0, 1, 2, 9] = math.inf  # V of head 0, channel 9: infinite, or NaN by the weights' second part
+    x = c.attention(q, SCALE)
+    assert torch.isnan(x[b1, 4:]).all()
+    assert not torch.isfinite(x[b2, :4, 9]).any()
+    x[b1, 4:] = a[b1, 4:]
+    x[b2, :4, 9] = a[b2, :4, 9]
+    assert torch.equal(x, a)
+    assert ok(c) == 0
+
+
 def test_attention_bad_table_and_lengths():
     c, _, _ = filled([300, 300, 300], 2)
     q = rand((3, 8, 128), BF16, 5)
