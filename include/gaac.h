@@ -560,9 +560,10 @@ GAAC_API int gaac_kv8_append(const gaac_kv8* cache, const void* k, const void* v
  * cache's dtype or GAAC_F32, 16-byte aligned.  workspace: gaac_kv8_attention_workspace()
  * bytes, 16-byte aligned, zero before the first call and left so (zero it again after a call
  * that reported GAAC_ETIMEOUT); not shared by calls that may overlap on the GPU.  batch *
- * n_kv_heads * (max_blocks + 1) < 2^31.  Weights are rounded to f16 for a BF16 result (2^-12
- * of each) and carried in two parts for others; sums are fp32.  A page index outside the pool reports GAAC_EFORMAT and its
- * block contributes nothing; a length outside the table reports GAAC_EINVAL and counts as 0.
+ * n_kv_heads * (max_blocks + 1) < 2^31.  Weights are carried in two parts, f16 each (2^-22 of a
+ * weight is lost; over a BF16 open block 2^-16); sums are fp32.  A page index outside the pool
+ * reports GAAC_EFORMAT and its block contributes nothing; a length outside the table reports
+ * GAAC_EINVAL and counts as 0.
  */
 GAAC_API size_t gaac_kv8_attention_workspace(void);
 GAAC_API int gaac_kv8_decode_attention(const gaac_kv8* cache, const void* q, int n_q_heads, int64_t q_seq_stride,

@@ -24,12 +24,13 @@
 //    but for parts below 2^-28 of the row's largest), the scale is put back with sK.
 //  * Two running maxima per row: m of the logits, for the softmax's sum l; and M of logit + log2 sV, for the
 //    weights 2^(s + log2 sV - M + 15) that go to the tensor cores as f16: whatever the blocks' scales, the largest
-//    weight is 2^15 and those down to 2^-29 of it keep f16's 11 bits.  For f16 and fp32 results what the rounding
-//    leaves follows as a second operand.  m, l, M and O are fp32.
-//  * The open block is multiplied in its own type, the weights always in two parts.
-// Measured (bf16 or fp16 result): 32 sequences of 4,096-32,768 tokens, 8 kv-heads, 1.2 GB: 175 us, 6.9 TB/s; one of
-// 65,536 tokens: 24.6 us, of which 3 us go by before the first data and 4 us from the last to the joined result; one
-// of 777 tokens: 7.9 us.
+//    weight is 2^15 and those down to 2^-29 of it keep f16's 11 bits.  What the rounding leaves (2^-11 of the weight)
+//    follows as a second operand, for every result type: 2^-11 is an eighth of bf16's own half step, and leaving it to
+//    a bf16 result would save 0.1 us of 8 (1 x 777), 0.3 of 25 (1 x 65,536), 1.4 of 176 (the 1.2 GB below) and at most
+//    3% where hundreds of short sequences leave the groups no pause.  m, l, M and O are fp32.
+//  * The open block is multiplied in its own type, the weights in two parts as well.
+// Measured: 32 sequences of 4,096-32,768 tokens, 8 kv-heads, 1.2 GB: 176 us, 6.9 TB/s; one of 65,536 tokens: 25.0 us,
+// of which 3 us go by before the first data and 4 us from the last to the joined result; one of 777 tokens: 8.0 us.
 #include <cuda.h>
 
 #include <algorithm>
@@ -697,24 +698,21 @@ __device__ __forceinline__ bool ka_join(const KaArgs& a, KaSmem& sm, int b, int 
   return true;
 }
 
-// The P^T operands of 16 tokens from their weights in the logits' places: rounded to f16 or bf16, and with `parts`
-// what that leaves, rounded again.
+// The P^T operands of 16 tokens from their weights in the logits' places: rounded to f16 or bf16, and what that
+// leaves, rounded again (2^-22 of the weight is lost in f16, 2^-16 in bf16).
 template <bool F16>
-__device__ __forceinline__ void ka_weights(const float w[4], bool parts, uint32_t pb[4]) {
+__device__ __forceinline__ void ka_weights(const float w[4], uint32_t pb[4]) {
   const uint32_t h0 = F16 ? ka_pack_f16(w[0], w[1]) : ka_pack_bf16(w[0], w[1]);
   const uint32_t h1 = F16 ? ka_pack_f16(w[2], w[3]) : ka_pack_bf16(w[2], w[3]);
   pb[0] = ka_transpose(h0);
   pb[1] = ka_transpose(h1);
-  if (parts) {
-    const float2 b0 = kv8_pair<F16>(h0), b1 = kv8_pair<F16>(h1);
-    const float r[4] = {w[0] - b0.x, w[1] - b0.y, w[2] - b1.x, w[3] - b1.y};
-    pb[2] = ka_transpose(F16 ? ka_pack_f16(r[0], r[1]) : ka_pack_bf16(r[0], r[1]));
-    pb[3] = ka_transpose(F16 ? ka_pack_f16(r[2], r[3]) : ka_pack_bf16(r[2], r[3]));
-  }
+  const float2 b0 = kv8_pair<F16>(h0), b1 = kv8_pair<F16>(h1);
+  const float r[4] = {w[0] - b0.x, w[1] - b0.y, w[2] - b1.x, w[3] - b1.y};
+  pb[2] = ka_transpose(F16 ? ka_pack_f16(r[0], r[1]) : ka_pack_bf16(r[0], r[1]));
+  pb[3] = ka_transpose(F16 ? ka_pack_f16(r[2], r[3]) : ka_pack_bf16(r[2], r[3]));
 }
 
-// FINE: the result is not bf16, which hides the weights' rounding to f16 (2^-12): they go in in two parts (2^-22).
-template <bool HALF, int FMT, bool FINE>
+template <bool HALF, int FMT>
 __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, tq = lane & 3;
   const int warp = tid >> 5, part = warp & 1;  // part: which half of a unit's tokens
@@ -889,7 +887,7 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
       if (kind == kUnitPage) {
         uint32_t pb[2][4];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) ka_weights<true>(s[t], FINE, pb[t]);
+        for (int t = 0; t < 2; ++t) ka_weights<true>(s[t], pb[t]);
 #pragma unroll
         for (int i = 0; i < 8; i += 2)
 #pragma unroll
@@ -904,14 +902,12 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
             ka_widen<FMT, true>(r[3], a1[2], a1[3]);
             ka_mma_f16(acc[i], a0, pb[t][0], pb[t][1]);
             ka_mma_f16(acc[i + 1], a1, pb[t][0], pb[t][1]);
-            if (FINE) {
-              ka_mma_f16(acc[i], a0, pb[t][2], pb[t][3]);
-              ka_mma_f16(acc[i + 1], a1, pb[t][2], pb[t][3]);
-            }
+            ka_mma_f16(acc[i], a0, pb[t][2], pb[t][3]);
+            ka_mma_f16(acc[i + 1], a1, pb[t][2], pb[t][3]);
           }
       } else {
         uint32_t pb[4];
-        ka_weights<HALF>(s[0], true, pb);
+        ka_weights<HALF>(s[0], pb);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           uint32_t aw[4];
@@ -1051,7 +1047,7 @@ __device__ void ka_compute(const KaArgs& a, KaSmem& sm) {
   }
 }
 
-template <bool HALF, int FMT, bool FINE>
+template <bool HALF, int FMT>
 __global__ void __launch_bounds__(kKaThreads, 1)
     kv8_attention_kernel(const KaArgs a, const __grid_constant__ CUtensorMap pages, const __grid_constant__ CUtensorMap tail) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1082,7 +1078,7 @@ __global__ void __launch_bounds__(kKaThreads, 1)
     ka_copy_warp(a, sm, &pages, &tail, threadIdx.x / 32 - kKaWarps);
   } else {
     if (a.c.batch > 32) __syncthreads();  // the copy warps have read them
-    ka_compute<HALF, FMT, FINE>(a, sm);
+    ka_compute<HALF, FMT>(a, sm);
   }
 }
 
@@ -1128,19 +1124,19 @@ static bool ka_map(CUtensorMap* m, CUtensorMapDataType type, int elem, void* bas
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool HALF, int FMT, bool FINE>
+template <bool HALF, int FMT>
 static int ka_launch(const KaArgs& a, const CUtensorMap& pages, const CUtensorMap& tail, int grid, void* stream) {
   constexpr size_t smem = sizeof(KaSmem) + 1024;  // room to align the stages
   static bool done[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GAAC_ECUDA;
   if (!done[dev]) {
-    if (cudaFuncSetAttribute(kv8_attention_kernel<HALF, FMT, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(kv8_attention_kernel<HALF, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess)
       return GAAC_ECUDA;
     done[dev] = true;
   }
-  return kv8_launch(kv8_attention_kernel<HALF, FMT, FINE>, dim3(grid), kKaThreads, smem, stream, a, pages, tail);
+  return kv8_launch(kv8_attention_kernel<HALF, FMT>, dim3(grid), kKaThreads, smem, stream, a, pages, tail);
 }
 
 }  // namespace gaac
@@ -1187,11 +1183,8 @@ extern "C" int gaac_kv8_decode_attention(const gaac_kv8* cache, const void* q, i
     return GAAC_ECUDA;
   const bool e4 = cache->fmt == GAAC_FP8_E4M3;
   if (cache->dtype == GAAC_F16)
-    return e4 ? ka_launch<true, GAAC_FP8_E4M3, true>(a, pages, tail, grid, stream)
-              : ka_launch<true, GAAC_FP8_E5M2, true>(a, pages, tail, grid, stream);
-  if (a.out_f32)
-    return e4 ? ka_launch<false, GAAC_FP8_E4M3, true>(a, pages, tail, grid, stream)
-              : ka_launch<false, GAAC_FP8_E5M2, true>(a, pages, tail, grid, stream);
-  return e4 ? ka_launch<false, GAAC_FP8_E4M3, false>(a, pages, tail, grid, stream)
-            : ka_launch<false, GAAC_FP8_E5M2, false>(a, pages, tail, grid, stream);
+    return e4 ? ka_launch<true, GAAC_FP8_E4M3>(a, pages, tail, grid, stream)
+              : ka_launch<true, GAAC_FP8_E5M2>(a, pages, tail, grid, stream);
+  return e4 ? ka_launch<false, GAAC_FP8_E4M3>(a, pages, tail, grid, stream)
+            : ka_launch<false, GAAC_FP8_E5M2>(a, pages, tail, grid, stream);
 }

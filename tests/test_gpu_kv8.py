@@ -719,3 +719,19 @@ def test_serving_run(fmt, dtype):
             check_blocks(c, seen)
     assert ok(c) == 0
     check_blocks(c, seen)
+
+
+@pytest.mark.parametrize("fmt,dtype", [(E4, BF16), (E5, BF16), (E4, F16), (E5, F16)])
+@pytest.mark.parametrize("lens", [[777], [5, 0, 64, 130, 20000], [(53 * i) % 190 for i in range(161)]], ids=["one", "mixed", "short"])
+def test_attention_16_bit_result_is_the_rounded_32_bit_one(lens, fmt, dtype):
+    """The result's type changes its last rounding alone, none on the way to it."""
+    c, _, _ = filled(lens, 2, fmt, dtype)
+    q = rand((len(lens), 8, 128), dtype, 5)
+    full = c.attention(q, SCALE, out=torch.empty(q.shape, dtype=F32, device="cuda"))
+    assert torch.equal(c.attention(q, SCALE), full.to(dtype))
+    # weights in two parts over the pages: 2^-22 of each is lost (2^-16 over an open block in bf16), whatever the result
+    ref, bound = U.attention_ref(c, q, SCALE, 2.0 ** -16 if dtype == BF16 else 2.0 ** -20)
+    half = torch.finfo(dtype).eps / 2
+    err = (c.attention(q, SCALE).double() - ref).abs()
+    assert (err <= bound * (1 + half) + half * ref.abs() + torch.finfo(dtype).tiny).all()
+    assert ok(c) == 0
