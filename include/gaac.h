@@ -561,7 +561,10 @@ GAAC_API int gaac_kv8_append(const gaac_kv8* cache, const void* k, const void* v
  * bytes, 16-byte aligned, zero before the first call and left so (zero it again after a call
  * that reported GAAC_ETIMEOUT); not shared by calls that may overlap on the GPU.  batch *
  * n_kv_heads * (max_blocks + 1) < 2^31.  Weights are carried in two parts, f16 each (2^-22 of a
- * weight is lost; over a BF16 open block 2^-16); sums are fp32.  A page index outside the pool
+ * weight is lost; over a BF16 open block 2^-16); sums are fp32.  An infinite V makes its
+ * channel infinite (NaN where both signs meet, or where its weight is 0 in fp32, 2^-141 of the
+ * largest); V of a BF16 open block is otherwise below 2^100 in magnitude, so that its sums stay
+ * in fp32's range, in units of the largest weight's 2^-15.  A page index outside the pool
  * reports GAAC_EFORMAT and its block contributes nothing; a length outside the table reports
  * GAAC_EINVAL and counts as 0.
  */

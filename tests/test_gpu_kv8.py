@@ -735,3 +735,63 @@ def test_attention_16_bit_result_is_the_rounded_32_bit_one(lens, fmt, dtype):
     err = (c.attention(q, SCALE).double() - ref).abs()
     assert (err <= bound * (1 + half) + half * ref.abs() + torch.finfo(dtype).tiny).all()
     assert ok(c) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("lens,b", [([130], 0), ([70000], 0), ([30, 200, 64 * 9 + 50], 2), ([100 + i % 60 for i in range(161)], 60)],
+                         ids=["one", "joined", "few", "short"])
+def test_attention_infinite_values(lens, b, dtype):
+    """V infinite in a channel: its weighted sum is, with the sign, however small the weight; NaN where both signs
+    meet or a value is NaN.  In pages (E5M2) and in the open block; the other channels and rows keep their bits."""
+    c, _, _ = filled(lens, 2, E5, dtype)
+    q = rand((len(lens), 8, 128), dtype, 5)
+    q[b, :4] = q[b, :1]  # the rows of head 0 alike
+    types = (dtype, F32)
+    plain = [c.attention(q, SCALE, out=torch.empty(q.shape, dtype=t, device="cuda")) for t in types]
+    ids, n = c.table[b].tolist(), lens[b]
+    inf8 = torch.tensor([math.inf, -math.inf, math.nan], device="cuda").to(U.FP8[E5]).view(torch.uint8).tolist()
+    c.pages[ids[0], 0, 1, 5, 3] = inf8[0]
+    c.pages[ids[0], 0, 1, 63, 64] = inf8[1]
+    c.pages[ids[0], 0, 1, 2, 77] = inf8[0]
+    c.pages[ids[0], 0, 1, 40, 77] = inf8[1]
+    c.pages[ids[0], 0, 1, 9, 100] = inf8[2]
+    c.tail[b, 0, 1, 1, 9] = math.inf  # the open block's second token
+    c.tail[b, 0, 1, n % 64 - 1, 127] = -math.inf
+    c.tail[b, 0, 1, n % 64:, 50] = math.inf  # behind its last
+    for t, a in zip(types, plain):
+        x = c.attention(q, SCALE, out=torch.empty(q.shape, dtype=t, device="cuda"))
+        for ch, v in ((3, math.inf), (64, -math.inf), (9, math.inf), (127, -math.inf)):
+            assert (x[b, :4, ch] == v).all(), (t, ch, x[b, :4, ch])
+        assert torch.isnan(x[b, :4, 77]).all() and torch.isnan(x[b, :4, 100]).all()
+        for ch in (3, 64, 9, 127, 77, 100):
+            x[b, :4, ch] = a[b, :4, ch]
+        assert torch.equal(x, a)
+    assert ok(c) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("low", [5.0, 25.0, 40.0, 60.0, 100.0])
+def test_attention_infinite_values_of_small_weight(low, dtype):
+    """Token 5's logit is `low` powers of two below the others' (its weight is not 0 in 32 bits), in a page and in the
+    open block; what is finite of such a token counts as before."""
+    c = Kv8Cache(4, 2, 1, 4, E5, dtype)
+    k, v = torch.zeros((2 * 100, 1, 128), dtype=dtype, device="cuda"), rand((2 * 100, 1, 128), dtype, 3)
+    q = torch.zeros((2, 1, 128), dtype=dtype, device="cuda")
+    q[:, :, 0] = 1.0
+    at = (5, 100 + 70)  # sequence 0: in its page; sequence 1: in its open block
+    for i in at:
+        k[i, 0, 0] = -low
+        v[i, 0, 9] = math.inf
+    c.append(k, v, cu_of([100, 100]))
+    scale = math.log(2.0)
+    for t in (dtype, F32):
+        x = c.attention(q, scale, out=torch.empty(q.shape, dtype=t, device="cuda"))
+        assert (x[:, 0, 9] == math.inf).all(), x[:, 0, 9]
+        assert torch.isfinite(x).sum() == x.numel() - 2
+        c.tail[1, 0, 1, 6, 9] = 0.0
+        page = c.pages[int(c.table[0, 0]), 0, 1, 5]
+        page[9] = 0
+        U.check_attention(c, q, scale, c.attention(q, scale, out=torch.empty(q.shape, dtype=t, device="cuda")))
+        c.tail[1, 0, 1, 6, 9] = math.inf
+        page[9] = 0x7C
+    assert ok(c) == 0
