@@ -115,11 +115,25 @@ class LayerCache:
                 "table_bytes": self.table.numel() * 8}
 
 
-def _used_on(t: torch.Tensor, stream):
-    """A tensor made here for a call on another stream than the current one: its memory is not given out again
-    before that stream is past the call."""
+def _stream_object(stream, device) -> torch.cuda.Stream:
+    """The torch stream of a call's `stream` argument, a stream or a raw handle."""
     if isinstance(stream, torch.cuda.Stream):
-        t.record_stream(stream)
+        return stream
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return torch.cuda.ExternalStream(handle, device=device)
+
+
+def _made_for(stream, device, make) -> torch.Tensor:
+    """make()'s tensor for a call on `stream` (None: the current one).  It is made on that stream, so its memory is not
+    what the current stream's pending work still uses, and not given out again before the current stream, where it
+    may be read, is past its use."""
+    if stream is None:
+        return make()
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(_stream_object(stream, device)):
+        t = make()
+    t.record_stream(current)
+    return t
 
 
 class Kv8Cache(Kv8):
@@ -164,8 +178,7 @@ class Kv8Cache(Kv8):
     def attention(self, q: torch.Tensor, scale: float, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """q: [batch, q_heads, 128] -> the same shape and type (or `out`'s: fp32 is allowed)."""
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            _used_on(out, stream)
+            out = _made_for(stream, q.device, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
         kv8_decode_attention(self, q, scale, out, self._ws, self.status, stream)
         return out
 
@@ -180,7 +193,6 @@ class Kv8Cache(Kv8):
 
     def compact(self, stream=None) -> torch.Tensor:
         """int32 [n_pages]: where each page has gone, -1 for free ones."""
-        moved_to = torch.empty_like(self.refs)
-        _used_on(moved_to, stream)
+        moved_to = _made_for(stream, self.device, lambda: torch.empty_like(self.refs))
         kv8_compact(self, moved_to, stream)
         return moved_to

@@ -795,3 +795,43 @@ def test_attention_infinite_values_of_small_weight(low, dtype):
         c.tail[1, 0, 1, 6, 9] = math.inf
         page[9] = 0x7C
     assert ok(c) == 0
+
+
+BUSY = 40_000_000  # cycles that a stream is kept busy: some 20 ms
+
+
+def side_streams():
+    """A stream, as an object and as the raw handle of another."""
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    return ((s, s), (t, t.cuda_stream))
+
+
+@pytest.mark.parametrize("what", ["attention", "compact"])
+def test_results_on_a_side_stream_take_no_memory_in_use(what):
+    """The result of a call with `stream` is not memory that the current stream's pending work still reads, nor is it
+    given out again while the current stream reads it."""
+    c, _, _ = filled([700, 33, 1500], 4)
+    q = rand((3, 16, 128), BF16, 5)
+    run = (lambda s: c.attention(q, SCALE, stream=s)) if what == "attention" else (lambda s: c.compact(stream=s))
+    right = run(None)
+    c.compact()
+    right = run(None)  # of a compact pool, which a further compaction leaves as it is
+    for s, handle in side_streams():
+        torch.cuda.synchronize()
+        used = torch.full_like(right, 7)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(BUSY)
+        seen = used.clone()
+        del used  # its block is free for the current stream, which still has to read it
+        out = run(handle)
+        torch.cuda.synchronize()
+        assert (seen == 7).all()
+        assert torch.equal(out, right)
+        # the other way round: read here, freed, and its memory asked for again there
+        torch.cuda._sleep(BUSY)
+        seen = out.clone()
+        del out
+        with torch.cuda.stream(s):
+            other = torch.full_like(right, 7)
+        torch.cuda.synchronize()
+        assert torch.equal(seen, right) and (other == 7).all()
