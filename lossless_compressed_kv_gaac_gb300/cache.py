@@ -12,6 +12,27 @@ from . import (BLOCK, FP8_E4M3, HEAD_DIM, Kv8, Pools, append, attention_workspac
                kv8_compact, kv8_decode_attention, kv8_fork, kv8_release, kv8_reserve, new_stats, new_table)
 
 
+def _stream_object(stream, device) -> torch.cuda.Stream | None:
+    """The torch stream of a call's `stream` argument: a stream, a raw handle or None, which stays None."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return torch.cuda.ExternalStream(handle, device=device)
+
+
+def _made_for(stream, device, make) -> torch.Tensor:
+    """make()'s tensor for a call on `stream` (None: the current one).  It is made on that stream, so its memory is not
+    what the current stream's pending work still uses, and not given out again before the current stream, where it
+    may be read, is past its use."""
+    if stream is None:
+        return make()
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(_stream_object(stream, device)):
+        t = make()
+    t.record_stream(current)
+    return t
+
+
 class LayerCache:
     """Slot table, pools, window bases and counters of one layer.
 
@@ -56,7 +77,8 @@ class LayerCache:
     def encode(self, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Tensor, stream=None, raw: bool = False):
         """Prefill: k, v BF16 [batch, tokens, kv_heads, 128]; seq_lens int32 [batch].
         raw=True stores every block as BF16 (the uncompressed baseline cache)."""
-        self.seq_lens.copy_(seq_lens)
+        with torch.cuda.stream(_stream_object(stream, self.device)):
+            self.seq_lens.copy_(seq_lens)
         self.all_raw = raw
         encode_blocks(k, v, self.seq_lens, self.max_blocks, self.base3, self.base4, self.table,
                       None if raw else self.slot_ids, self.pools, self.stats, self.status, stream,
@@ -74,10 +96,13 @@ class LayerCache:
 
         return auto_splits(self.batch, self.n_kv_heads, self.max_blocks)
 
-    def workspace(self, n_splits: int = 0) -> torch.Tensor:
+    def workspace(self, n_splits: int = 0, stream=None) -> torch.Tensor:
         need = attention_workspace(self.batch, self.n_kv_heads, self.max_blocks, n_splits)
         if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.zeros(max(need, 16), dtype=torch.uint8, device=self.device)
+            self._ws = _made_for(stream, self.device,
+                                 lambda: torch.zeros(max(need, 16), dtype=torch.uint8, device=self.device))
+        if stream is not None:  # a larger one may take its place
+            self._ws.record_stream(_stream_object(stream, self.device))
         return self._ws
 
     def attention(self, q: torch.Tensor, scale: float, out: torch.Tensor | None = None, n_splits: int = 0,
@@ -85,21 +110,21 @@ class LayerCache:
         """q: BF16 [batch, q_heads, 128] -> fp32 [batch, q_heads, 128].  bf16=True: the uncompressed BF16
         kernel (the cache must have been encoded with raw=True)."""
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+            out = _made_for(stream, q.device, lambda: torch.empty(q.shape, dtype=torch.float32, device=q.device))
         if bf16:
-            decode_attention_bf16(q, self.seq_lens, self.table, self.pools, scale, out, self.workspace(n_splits),
-                                  n_splits, self.status, stream)
+            decode_attention_bf16(q, self.seq_lens, self.table, self.pools, scale, out,
+                                  self.workspace(n_splits, stream), n_splits, self.status, stream)
         else:
             decode_attention(q, self.seq_lens, self.table, self.pools, self.base3, self.base4, scale, out,
-                             self.workspace(n_splits), n_splits, self.status, stream)
+                             self.workspace(n_splits, stream), n_splits, self.status, stream)
         return out
 
     def decompress(self, n_tok: int | None = None, stream=None):
         """BF16 (k, v) [batch, n_tok, kv_heads, 128] rebuilt from the cache (tokens past a sequence: 0)."""
         n_tok = self.max_blocks * BLOCK if n_tok is None else n_tok
         shape = (self.batch, n_tok, self.n_kv_heads, HEAD_DIM)
-        k = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
-        v = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
+        k, v = (_made_for(stream, self.device, lambda: torch.zeros(shape, dtype=torch.bfloat16, device=self.device))
+                for _ in range(2))
         decompress(self.table, self.seq_lens, self.pools, self.base3, self.base4, k, v, self.status, stream)
         return k, v
 
@@ -113,27 +138,6 @@ class LayerCache:
         n_raw = int((mode == 1).sum().item())
         return {"slot_tiles": n_slot, "raw_tiles": n_raw, "slot_bytes": n_slot * 12032, "raw_bytes": n_raw * 16384,
                 "table_bytes": self.table.numel() * 8}
-
-
-def _stream_object(stream, device) -> torch.cuda.Stream:
-    """The torch stream of a call's `stream` argument, a stream or a raw handle."""
-    if isinstance(stream, torch.cuda.Stream):
-        return stream
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    return torch.cuda.ExternalStream(handle, device=device)
-
-
-def _made_for(stream, device, make) -> torch.Tensor:
-    """make()'s tensor for a call on `stream` (None: the current one).  It is made on that stream, so its memory is not
-    what the current stream's pending work still uses, and not given out again before the current stream, where it
-    may be read, is past its use."""
-    if stream is None:
-        return make()
-    current = torch.cuda.current_stream(device)
-    with torch.cuda.stream(_stream_object(stream, device)):
-        t = make()
-    t.record_stream(current)
-    return t
 
 
 class Kv8Cache(Kv8):
