@@ -470,7 +470,9 @@ def rope_frequencies(rot_dim: int, theta: float = 1e4, scaling: str | None = Non
     scaling None: as they are.  "linear": w / factor (positions interpolated).  "base": theta stretched to
     theta * factor^(rot_dim/(rot_dim-2)), which leaves the fastest pair alone and slows the slowest by factor.
     "bands": by how often a pair turns within original_len tokens: `fast` turns and more keep w, `slow` and fewer
-    get w / factor, linear in the pair's index between; mscale = 0.1 ln(factor) + 1."""
+    get w / factor, linear in the pair's index between; mscale = 0.1 ln(factor) + 1.  That is YaRN's scaling (Peng et
+    al., 2023) with the ramp over indices in common use: from that of `fast` turns, rounded down and at least 0, to
+    that of `slow`, rounded up, which may lie behind the last pair."""
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError("rot_dim must be even and positive")
     if not theta > 0 or not factor > 0:
@@ -494,7 +496,7 @@ def rope_frequencies(rot_dim: int, theta: float = 1e4, scaling: str | None = Non
         return rot_dim * math.log(original_len / (2 * math.pi * turns)) / (2 * math.log(theta))
 
     lo = max(0.0, math.floor(pair_of(fast)))
-    hi = min(rot_dim / 2 - 1.0, math.ceil(pair_of(slow)))
+    hi = math.ceil(pair_of(slow))
     keep = 1.0 - ((j - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
     return w * keep + w / factor * (1.0 - keep), (0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0)
 

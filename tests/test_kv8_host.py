@@ -174,3 +174,21 @@ def test_plain_forms_agree_with_hand_values():
     assert U.quantise(x * 0, 1)[1].item() == 1.0
     y = U.rope_ref(torch.tensor([[[1.0, 0.0, 5.0]]]), torch.tensor([1]), torch.tensor([math.pi / 2], dtype=torch.float64))
     assert torch.allclose(y, torch.tensor([[[0.0, 1.0, 5.0]]], dtype=torch.float64), atol=1e-15)
+
+
+@pytest.mark.parametrize("rot,theta,factor,original,fast,slow", [
+    (128, 1e4, 4.0, 131072, 32.0, 1.0), (128, 1e4, 4.0, 262144, 32.0, 1.0), (128, 1e4, 8.0, 65536, 32.0, 1.0),
+    (64, 1e4, 2.0, 1 << 20, 16.0, 2.0), (128, 1e6, 4.0, 32768, 32.0, 1.0), (128, 1e4, 16.0, 4096, 32.0, 1.0)])
+def test_band_frequencies_follow_the_ramp(rot, theta, factor, original, fast, slow):
+    """The share of each pair that is kept, from its definition; above all where every pair turns more than `slow` times
+    within original_len, so that the ramp ends behind the last pair."""
+    w, _ = G.rope_frequencies(rot, theta, "bands", factor, original_len=original, fast=fast, slow=slow)
+    first = rot * math.log(original / (2 * math.pi * fast)) / (2 * math.log(theta))
+    end = rot * math.log(original / (2 * math.pi * slow)) / (2 * math.log(theta))
+    for j in range(rot // 2):
+        plain = theta ** (-2 * j / rot)
+        share = (j - math.floor(first)) / (math.ceil(end) - math.floor(first))
+        kept = 1 - min(1.0, max(0.0, share))
+        assert abs(w[j].item() - (plain * kept + plain / factor * (1 - kept))) <= 1e-12 * plain, j
+        if plain * original / (2 * math.pi) > slow * 1.5 and j < math.ceil(end) - 1:
+            assert w[j].item() > plain / factor * (1 + 1e-9)  # turns more often than slow: not the whole factor
