@@ -577,9 +577,17 @@ GAAC_API int gaac_kv8_decode_attention(const gaac_kv8* cache, const void* q, int
  * Pages for the blocks that the given appends (cu_tokens as gaac_kv8_append; NULL: one token
  * each) will fill: table entries without a page, in order of sequence and block, get the
  * lowest free pages in order.  When they run out the rest stays -1 and GAAC_EPOOL is
- * reported; a sequence that would pass max_blocks gets none and reports GAAC_EINVAL.
+ * reported (what a sequence has got stays with it, for a later append or its release); a
+ * sequence that would pass max_blocks gets none and reports GAAC_EINVAL.  Offsets that decrease
+ * or are negative: GAAC_EINVAL, nothing reserved.
  */
 GAAC_API int gaac_kv8_reserve(const gaac_kv8* cache, const int32_t* cu_tokens, int32_t* d_status, void* stream);
+
+/* gaac_kv8_reserve and gaac_kv8_append of the same tokens.  What either refuses as a whole (bad
+ * arguments, bad cu_tokens, offsets past n_tokens among them) neither reserves nor appends. */
+GAAC_API int gaac_kv8_reserve_append(const gaac_kv8* cache, const void* k, const void* v, int64_t n_tokens,
+                                     int64_t k_tok_stride, int64_t v_tok_stride, const int32_t* cu_tokens,
+                                     int32_t* d_status, void* stream);
 
 /* Empties the listed sequences (int32 seqs[n] on the device): their pages lose a holder, their
  * rows become -1 and their lengths 0.  An index out of range reports GAAC_EINVAL and is

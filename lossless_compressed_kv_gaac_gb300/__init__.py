@@ -126,6 +126,8 @@ def lib() -> ctypes.CDLL:
             L.gaac_kv8_workspace.restype = sz
             L.gaac_kv8_append.argtypes = [P, P, P, i64, i64, i64, P, P, P]
             L.gaac_kv8_append.restype = i32
+            L.gaac_kv8_reserve_append.argtypes = L.gaac_kv8_append.argtypes
+            L.gaac_kv8_reserve_append.restype = i32
             L.gaac_kv8_attention_workspace.argtypes = []
             L.gaac_kv8_attention_workspace.restype = sz
             L.gaac_kv8_decode_attention.argtypes = [P, P, i32, i64, ctypes.c_float, P, i32, P, sz, P, P]
@@ -686,16 +688,17 @@ def _kv8_rows(cache: Kv8, t, heads, name):
 
 
 def kv8_append(cache: Kv8, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor | None = None, status=None,
-               stream=None) -> None:
+               stream=None, reserve: bool = False) -> None:
     """Appends rows cu_tokens[b] .. cu_tokens[b + 1] of k and v ([n, kv_heads, 128] of the cache's type, heads and
     channels contiguous) to sequence b; without cu_tokens (int32 [batch + 1]) one row for each sequence.  The pages
-    of blocks that fill must have been reserved."""
+    of blocks that fill must have been reserved, or are with reserve=True."""
     cu = _kv8_cu(cache, cu_tokens)
     n, k_row = _kv8_rows(cache, k, cache.n_kv_heads, "k")
     n_v, v_row = _kv8_rows(cache, v, cache.n_kv_heads, "v")
     if n_v != n or (cu == 0 and n != cache.batch):
         raise ValueError("k and v must hold the same rows: one for each sequence without cu_tokens")
-    _call("gaac_kv8_append", cache._index, stream, cache._ref, k.data_ptr(), v.data_ptr(), n, k_row, v_row, cu, _ptr(status))
+    _call("gaac_kv8_reserve_append" if reserve else "gaac_kv8_append", cache._index, stream, cache._ref, k.data_ptr(),
+          v.data_ptr(), n, k_row, v_row, cu, _ptr(status))
 
 
 def kv8_attention_workspace() -> int:
@@ -720,7 +723,8 @@ def kv8_decode_attention(cache: Kv8, q: torch.Tensor, scale: float, out: torch.T
 
 
 def kv8_reserve(cache: Kv8, cu_tokens: torch.Tensor | None = None, status=None, stream=None) -> None:
-    """Pages for the blocks that appending these tokens fills: the lowest free ones, in order of sequence and block."""
+    """Pages for the blocks that appending these tokens fills: the lowest free ones, in order of sequence and block.
+    When they run out, sequences keep what they have got."""
     _call("gaac_kv8_reserve", cache._index, stream, cache._ref, _kv8_cu(cache, cu_tokens), _ptr(status))
 
 

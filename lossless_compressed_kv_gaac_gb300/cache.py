@@ -145,8 +145,8 @@ class Kv8Cache(Kv8):
     block of every sequence in the model's type, and counted pages that sequences share.
 
     dtype: BF16 or FP16, the type of k, v, q and the open block.  Faults that only the device sees (no page left, a
-    length past the table) are recorded in `status`, as by the calls of the lossless cache; such a call leaves the
-    sequence as it was.
+    length past the table, offsets out of order) are recorded in `status`, as by the calls of the lossless cache; such
+    a call leaves the sequence's tokens as they were, with the pages that could be reserved for it.
     """
 
     def __init__(self, n_pages: int, batch: int, n_kv_heads: int, max_blocks: int, fmt: int = FP8_E4M3,
@@ -175,9 +175,7 @@ class Kv8Cache(Kv8):
                stream=None):
         """Tokens behind the sequences: rows cu_tokens[b] .. cu_tokens[b + 1] of k, v [n, kv_heads, 128] for sequence
         b, or one row for each.  reserve=False: the pages of blocks that fill have been reserved before."""
-        if reserve:
-            kv8_reserve(self, cu_tokens, self.status, stream)
-        kv8_append(self, k, v, cu_tokens, self.status, stream)
+        kv8_append(self, k, v, cu_tokens, self.status, stream, reserve)
 
     def attention(self, q: torch.Tensor, scale: float, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """q: [batch, q_heads, 128] -> the same shape and type (or `out`'s: fp32 is allowed)."""

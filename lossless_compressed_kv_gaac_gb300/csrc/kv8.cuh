@@ -30,8 +30,9 @@ constexpr int kKv8Tile = kBlock * kD;       // FP8 bytes of one (page, kv-head, 
 constexpr int kKv8Pair = 2 * kKv8Tile;      // K and V of one (page, kv-head), contiguous
 constexpr int kKv8Chunk = 8192;             // pages that one CTA counts (reserve, compact)
 
-// Workspace (int32 words): the append's counters per sequence and the two tickets, which are zero between calls,
-// then scratch that every call writes before it reads.
+// Workspace (int32 words): the append's counters per sequence, two tickets (reserve, compact), the pages that a
+// compaction moves and the reserve's mark of bad offsets; counters, tickets and mark are zero between calls.  Then
+// scratch that every call writes before it reads.
 struct Kv8Work {
   int64_t tickets, need, chunks, list_a, list_b, words;
 };
@@ -62,6 +63,9 @@ inline bool kv8_ok(const gaac_kv8* c) {
   const uintptr_t a4 = reinterpret_cast<uintptr_t>(c->table) | reinterpret_cast<uintptr_t>(c->seq_lens);
   return (a16 & 15u) == 0 && (a4 & 3u) == 0 && (reinterpret_cast<uintptr_t>(c->scales) & 7u) == 0;
 }
+
+// gaac_kv8_reserve for appends of n_tokens rows; the cache has been checked.
+int kv8_reserve_rows(const gaac_kv8* cache, const int32_t* cu_tokens, int64_t n_tokens, int32_t* d_status, void* stream);
 
 inline Kv8Dev kv8_dev(const gaac_kv8* c) {
   return Kv8Dev{c->pages, c->scales, static_cast<uint16_t*>(c->tail), c->table, c->refs, c->seq_lens, c->work,

@@ -270,9 +270,8 @@ extern "C" size_t gaac_kv8_workspace(int batch, int64_t n_pages) {
   return static_cast<size_t>(kv8_work(batch, n_pages).words) * sizeof(int32_t);
 }
 
-extern "C" int gaac_kv8_append(const gaac_kv8* cache, const void* k, const void* v, int64_t n_tokens,
-                               int64_t k_tok_stride, int64_t v_tok_stride, const int32_t* cu_tokens, int32_t* d_status,
-                               void* stream) {
+static int kv8_append(const gaac_kv8* cache, const void* k, const void* v, int64_t n_tokens, int64_t k_tok_stride,
+                      int64_t v_tok_stride, const int32_t* cu_tokens, bool reserve, int32_t* d_status, void* stream) {
   if (!kv8_ok(cache) || n_tokens < 0 || n_tokens > 0x7FFFFFFF || (cu_tokens == nullptr && n_tokens != cache->batch))
     return GAAC_EINVAL;
   if (n_tokens == 0) return GAAC_OK;
@@ -286,6 +285,11 @@ extern "C" int gaac_kv8_append(const gaac_kv8* cache, const void* k, const void*
   const int run = cu_tokens == nullptr ? 1 : static_cast<int>(std::min<int64_t>(16, std::max<int64_t>(1, blocks / (152 * 16))));
   const int64_t places = cu_tokens == nullptr ? cache->batch : n_tokens / (kBlock * run) + 2 * static_cast<int64_t>(cache->batch);
   if (places * cache->n_kv_heads > 0x3FFFFFFF) return GAAC_EINVAL;
+  // every refusal by the arguments comes before the reserve changes anything
+  if (reserve) {
+    const int e = kv8_reserve_rows(cache, cu_tokens, n_tokens, d_status, stream);
+    if (e != GAAC_OK) return e;
+  }
   const Kv8AppendArgs a{kv8_dev(cache), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_tok_stride,
                         v_tok_stride, cu_tokens, n_tokens, run, d_status};
   const dim3 grid(static_cast<unsigned>(places * 2 * cache->n_kv_heads));
@@ -294,4 +298,16 @@ extern "C" int gaac_kv8_append(const gaac_kv8* cache, const void* k, const void*
                                        : kv8_launch(kv8_append_kernel<false, GAAC_FP8_E5M2>, grid, kApThreads, 0, stream, a);
   return cache->fmt == GAAC_FP8_E4M3 ? kv8_launch(kv8_append_kernel<true, GAAC_FP8_E4M3>, grid, kApThreads, 0, stream, a)
                                      : kv8_launch(kv8_append_kernel<true, GAAC_FP8_E5M2>, grid, kApThreads, 0, stream, a);
+}
+
+extern "C" int gaac_kv8_append(const gaac_kv8* cache, const void* k, const void* v, int64_t n_tokens,
+                               int64_t k_tok_stride, int64_t v_tok_stride, const int32_t* cu_tokens, int32_t* d_status,
+                               void* stream) {
+  return kv8_append(cache, k, v, n_tokens, k_tok_stride, v_tok_stride, cu_tokens, false, d_status, stream);
+}
+
+extern "C" int gaac_kv8_reserve_append(const gaac_kv8* cache, const void* k, const void* v, int64_t n_tokens,
+                                       int64_t k_tok_stride, int64_t v_tok_stride, const int32_t* cu_tokens,
+                                       int32_t* d_status, void* stream) {
+  return kv8_append(cache, k, v, n_tokens, k_tok_stride, v_tok_stride, cu_tokens, true, d_status, stream);
 }

@@ -133,8 +133,9 @@ __device__ __forceinline__ void for_missing(const Kv8Dev& c, int b, int step, in
 
 // Entries without a page among the blocks that fill, in order of sequence and block, get the lowest free pages
 // in order.  Every CTA counts the free pages of its chunk and the missing entries of some sequences, a warp each; the
-// last one to finish ranks them, lists the pages and hands them out.
-__global__ void __launch_bounds__(kPgThreads) kv8_reserve_kernel(Kv8Dev c, const int32_t* cu, int32_t* status) {
+// last one to finish ranks them, lists the pages and hands them out, unless some CTA has found offsets that the append
+// of `rows` rows would refuse as a whole.
+__global__ void __launch_bounds__(kPgThreads) kv8_reserve_kernel(Kv8Dev c, const int32_t* cu, int64_t rows, int32_t* status) {
   __shared__ int sh_free;
   dependent_wait();
   dependent_launch();
@@ -145,6 +146,7 @@ __global__ void __launch_bounds__(kPgThreads) kv8_reserve_kernel(Kv8Dev c, const
   for (int b0 = blockIdx.x * (kPgThreads / 32) + warp; b0 < c.batch; b0 += 32 * warps) {
     int lo = 0, hi = 0, mine = 0;
     const int64_t b = b0 + static_cast<int64_t>(lane) * warps;
+    if (b < c.batch && cu != nullptr && (cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > rows)) c.work[w.tickets + 3] = 1;
     if (b < c.batch && !fill_range(c, cu, static_cast<int>(b), &lo, &hi)) report(status, GAAC_EINVAL);
     for_missing(c, b0, warps, lo, hi, [&](int k, int, bool miss) {
       const int n = __popc(__ballot_sync(0xFFFFFFFFu, miss));
@@ -153,6 +155,13 @@ __global__ void __launch_bounds__(kPgThreads) kv8_reserve_kernel(Kv8Dev c, const
     if (b < c.batch) need[b] = mine;
   }
   if (!count_chunk(c, w, true, c.work + w.tickets)) return;
+  if (__syncthreads_or(tid == 0 && __ldcg(c.work + w.tickets + 3) != 0)) {
+    if (tid == 0) {
+      c.work[w.tickets + 3] = 0;
+      report(status, GAAC_EINVAL);
+    }
+    return;
+  }
   // ---- the rank of each sequence's first one
   int total = 0;
   for (int b0 = 0; b0 < c.batch; b0 += kPgThreads) {
@@ -442,9 +451,13 @@ using namespace gaac;
 
 static unsigned chunks_of(const gaac_kv8* c) { return static_cast<unsigned>((c->n_pages + kKv8Chunk - 1) / kKv8Chunk); }
 
+int gaac::kv8_reserve_rows(const gaac_kv8* cache, const int32_t* cu_tokens, int64_t n_tokens, int32_t* d_status, void* stream) {
+  return kv8_launch(kv8_reserve_kernel, dim3(chunks_of(cache)), kPgThreads, 0, stream, kv8_dev(cache), cu_tokens, n_tokens, d_status);
+}
+
 extern "C" int gaac_kv8_reserve(const gaac_kv8* cache, const int32_t* cu_tokens, int32_t* d_status, void* stream) {
   if (!kv8_ok(cache) || (reinterpret_cast<uintptr_t>(cu_tokens) & 3u)) return GAAC_EINVAL;
-  return kv8_launch(kv8_reserve_kernel, dim3(chunks_of(cache)), kPgThreads, 0, stream, kv8_dev(cache), cu_tokens, d_status);
+  return kv8_reserve_rows(cache, cu_tokens, 0x7FFFFFFF, d_status, stream);
 }
 
 extern "C" int gaac_kv8_release(const gaac_kv8* cache, const int32_t* seqs, int n, int32_t* d_status, void* stream) {

@@ -835,3 +835,52 @@ def test_results_on_a_side_stream_take_no_memory_in_use(what):
             other = torch.full_like(right, 7)
         torch.cuda.synchronize()
         assert torch.equal(seen, right) and (other == 7).all()
+
+
+def test_append_with_bad_offsets_reserves_nothing():
+    """Offsets that the append refuses as a whole, or tensors that it refuses, leave the table and the counts alone."""
+    c, _, _ = filled([60, 60, 64, 0], 2, max_blocks=6, spare=12)
+    k, v = kv_of(400, 2, BF16, 9)
+    table, refs, lens = c.table.clone(), c.refs.clone(), c.seq_lens.clone()
+
+    def same():
+        return torch.equal(c.table, table) and torch.equal(c.refs, refs) and torch.equal(c.seq_lens, lens)
+
+    for cu in ([0, 100, 50, 200, 400], [0, 100, 200, 300, 401], [-1, 100, 200, 300, 400], [0, 0, 0, 0, 2 ** 31 - 1],
+               [0, 200, 100, 300, 200], [-2 ** 31, 0, 100, 200, 300]):
+        c.append(k, v, ints(cu))
+        assert ok(c) == G.EINVAL and same(), cu
+        c.status.zero_()
+    for cu in ([0, 100, 50, 200, 400], [-1, 100, 200, 300, 400], [0, 200, 100, 300, 200]):
+        c.reserve(ints(cu))
+        assert ok(c) == G.EINVAL and same(), cu
+        c.status.zero_()
+    for bad in (lambda: c.append(k, v[:300], cu_of([100, 100, 100, 100])), lambda: c.append(k, v.half(), cu_of([100] * 4)),
+                lambda: c.append(k[:3], v[:3])):
+        with pytest.raises(ValueError):
+            bad()
+        assert same()
+    odd = torch.empty(400 * 256 + 1, dtype=BF16, device="cuda")[1:].view(400, 2, 128)
+    with pytest.raises(G.GaacError):
+        c.append(odd, v, cu_of([100] * 4))
+    assert ok(c) == 0 and same()
+    # good offsets still work, with rows before the first and behind the last that belong to nobody
+    c.append(k, v, ints([30, 40, 40, 140, 300]))
+    assert ok(c) == 0 and c.seq_lens.tolist() == [70, 60, 164, 160]
+    assert torch.equal(c.tail[3, :, 0, :32].transpose(0, 1), k[268:300])
+
+
+def test_bad_offsets_among_thousands_of_sequences():
+    """One offset out of order, wherever it stands and whichever CTA finds it; the next call is not affected."""
+    c = Kv8Cache(20000, 5000, 1, 4)
+    k, v = kv_of(5000 * 64, 1, BF16, 1)
+    good = 64 * torch.arange(5001, dtype=torch.int32, device="cuda")
+    for at in (0, 1, 31, 32, 1024, 4999, 5000):
+        cu = good.clone()
+        cu[at] += 100 if at < 5000 else 1
+        c.append(k, v, cu)
+        assert ok(c) == G.EINVAL and (c.table == -1).all() and (c.refs == 0).all() and (c.seq_lens == 0).all()
+        c.status.zero_()
+    c.append(k, v, good)
+    assert ok(c) == 0 and torch.equal(c.table[:, 0], torch.arange(5000, dtype=torch.int32, device="cuda"))
+    assert (c.seq_lens == 64).all() and int(c.refs.sum()) == 5000

@@ -192,3 +192,15 @@ def test_band_frequencies_follow_the_ramp(rot, theta, factor, original, fast, sl
         assert abs(w[j].item() - (plain * kept + plain / factor * (1 - kept))) <= 1e-12 * plain, j
         if plain * original / (2 * math.pi) > slow * 1.5 and j < math.ceil(end) - 1:
             assert w[j].item() > plain / factor * (1 + 1e-9)  # turns more often than slow: not the whole factor
+
+
+def test_reserve_append_refuses_what_append_refuses(lib):
+    f = lib.gaac_kv8_reserve_append
+    for bad in BAD_CACHES:
+        assert f(cache(**bad), GOOD, GOOD, 2, 512, 512, None, None, None) == EINVAL
+    for args in ((None, GOOD, 2, 512, 512, None), (GOOD, None, 2, 512, 512, None), (ODD, GOOD, 2, 512, 512, None),
+                 (GOOD, ODD, 2, 512, 512, None), (GOOD, GOOD, 3, 512, 512, None), (GOOD, GOOD, -1, 512, 512, GOOD),
+                 (GOOD, GOOD, 2, 511, 512, None), (GOOD, GOOD, 2, 512, 504, None), (GOOD, GOOD, 2, 516, 512, None),
+                 (GOOD, GOOD, 1 << 31, 512, 512, GOOD), (GOOD, GOOD, 2, 512, 512, GOOD + 2)):
+        assert f(cache(), *args, None, None) == EINVAL, args
+    assert f(cache(), None, None, 0, 0, 0, GOOD, None, None) == OK  # nothing to append
