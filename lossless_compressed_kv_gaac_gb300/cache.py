@@ -174,7 +174,8 @@ class Kv8Cache(Kv8):
     def append(self, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor | None = None, reserve: bool = True,
                stream=None):
         """Tokens behind the sequences: rows cu_tokens[b] .. cu_tokens[b + 1] of k, v [n, kv_heads, 128] for sequence
-        b, or one row for each.  reserve=False: the pages of blocks that fill have been reserved before."""
+        b, or one row for each, a released one included (cu_tokens passes over it).  reserve=False: the pages of blocks
+        that fill have been reserved before."""
         kv8_append(self, k, v, cu_tokens, self.status, stream, reserve)
 
     def attention(self, q: torch.Tensor, scale: float, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:

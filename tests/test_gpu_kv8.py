@@ -884,3 +884,33 @@ def test_bad_offsets_among_thousands_of_sequences():
     c.append(k, v, good)
     assert ok(c) == 0 and torch.equal(c.table[:, 0], torch.arange(5000, dtype=torch.int32, device="cuda"))
     assert (c.seq_lens == 64).all() and int(c.refs.sum()) == 5000
+
+
+def test_readme_serving_loop():
+    """The 8-bit cache's example as it stands in README.md: ended sequences take no further tokens."""
+    import os
+    import re
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "README.md"), encoding="utf-8") as f:
+        code, = [x for x in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "Kv8Cache" in x]
+    new = [70 + i if i < 30 else 0 for i in range(32)]
+    k, v = kv_of(sum(new), 8, BF16, 1)
+    names = dict(q=rand((sum(new), 16, 128), BF16, 3), k=k, v=v, cu=cu_of(new), scale=SCALE,
+                 positions=torch.cat([torch.arange(n) for n in new]).cuda(), src=ints([0, 5]), dst=ints([30, 31]),
+                 finished=ints([3, 0, 31]))
+    for i in (1, 2):
+        names[f"q{i}"] = rand((32, 16, 128), BF16, 10 + i)
+        names[f"k{i}"], names[f"v{i}"] = kv_of(32, 8, BF16, 20 + 2 * i)
+    exec(compile(code, "README.md", "exec"), names)
+    c = names["cache"]
+    want = [n + 2 for n in new]
+    want[30], want[31] = new[0] + 2, new[5] + 2
+    for b in (3, 0, 31):
+        want[b] = 0
+    assert ok(c) == 0 and c.seq_lens.tolist() == want
+    assert all((c.table[b] == -1).all() for b in (3, 0, 31))
+    c.fork(ints([1]), ints([3]))  # an ended sequence's row takes a new one
+    assert ok(c) == 0 and int(c.seq_lens[3]) == want[1]
+    assert (names["out"][[0, 31]] == 0).all()
+    assert names["k8"].shape == c.pages.shape
