@@ -201,3 +201,42 @@ def test_more_elements_than_32_bits():
     w, _ = G.rope_frequencies(128)
     G.rope(x, None, pos, G.rope_turns(w, "cuda"))
     check(before, x[rows], pos[rows], w)
+
+
+def test_refuses_to_cut_a_graph():
+    """Tensors that autograd follows are refused while it records, since no gradient would come back; inside a Function
+    and without recording the calls run, and inverse is the gradient."""
+    w, m = G.rope_frequencies(64, 1e4, "bands", 4.0, original_len=4096)
+    t = G.rope_turns(w, "cuda")
+    x, g = rand((17, 3, 128), F32, 1), rand((17, 3, 128), F32, 2)
+    pos = torch.arange(1000, 1017, device="cuda")
+    leaf = x.clone().requires_grad_()
+    for bad in (lambda: G.rope(leaf, None, pos, t), lambda: G.rope(leaf * 2, None, pos, t),
+                lambda: G.rope(leaf, None, pos, t, q_out=torch.empty_like(x)),
+                lambda: G.rope(x, leaf, pos, t, k_out=torch.empty_like(x)),
+                lambda: G.rope(x, None, pos, t, q_out=leaf), lambda: G.rope(x, x.clone(), pos, t, k_out=leaf)):
+        with pytest.raises(ValueError, match="autograd"):
+            bad()
+    assert torch.equal(leaf.detach(), x)
+    with torch.no_grad():
+        out = torch.empty_like(x)
+        G.rope(leaf, None, pos, t, q_out=out, mscale=m)
+    check(x, out, pos, w, mscale=m)
+
+    class Rope(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, v):
+            y = torch.empty_like(v)
+            G.rope(v, None, pos, t, q_out=y, mscale=m)
+            return y
+
+        @staticmethod
+        def backward(ctx, gy):
+            gx = torch.empty_like(gy)
+            G.rope(gy.contiguous(), None, pos, t, q_out=gx, mscale=m, inverse=True)
+            return gx
+
+    y = Rope.apply(leaf)
+    y.backward(g)
+    assert torch.equal(y.detach(), out)
+    check(g, leaf.grad, pos, w, mscale=m, inverse=True)

@@ -204,3 +204,11 @@ def test_reserve_append_refuses_what_append_refuses(lib):
                  (GOOD, GOOD, 1 << 31, 512, 512, GOOD), (GOOD, GOOD, 2, 512, 512, GOOD + 2)):
         assert f(cache(), *args, None, None) == EINVAL, args
     assert f(cache(), None, None, 0, 0, 0, GOOD, None, None) == OK  # nothing to append
+
+
+def test_rope_refuses_to_cut_a_graph_before_it_looks_at_devices():
+    q, pos, t = torch.zeros(4, 2, 128, requires_grad=True), torch.zeros(4, dtype=torch.int32), torch.zeros(64, dtype=torch.int64)
+    with pytest.raises(ValueError, match="autograd"):
+        G.rope(q, None, pos, t)
+    with torch.no_grad(), pytest.raises(ValueError, match="device"):
+        G.rope(q, None, pos, t)
