@@ -491,13 +491,14 @@ typedef struct {
 
 /*
  * Rotates the first rot_dim channels of every head of one or two tensors (q and
- * k; they share no elements) by their token's position and copies the others:
+ * k) by their token's position and copies the others:
  *   a' = mscale (a cos - b sin), b' = mscale (b cos + a sin), angle = pos * w_j.
  * turns[j] = w_j / (2 pi) * 2^64 (mod 2^64), j < rot_dim/2: the product with the
  * position is exact modulo one turn, however far the position.  positions:
  * pos_bits-wide (32 or 64) signed integers at seq*pos_seq_stride +
  * tok*pos_tok_stride; any value.  dtype: GAAC_BF16, GAAC_F16 or GAAC_F32,
- * computed in fp32 and rounded once.  2 <= rot_dim <= head_dim <= 4096, even.
+ * computed in fp32 and rounded once.  2 <= rot_dim <= head_dim <= 4096, even.  An
+ * output shares no element with the other tensor (GAAC_EINVAL where it is the first).
  */
 GAAC_API int gaac_rope(const gaac_rope_tensor* tensors, int n_tensors, int dtype, int64_t n_seq, int64_t n_tok,
                        int head_dim, int rot_dim, const void* positions, int pos_bits, int64_t pos_seq_stride,

@@ -573,9 +573,10 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, turns
     dim], BF16, FP16 or FP32, channels contiguous, other strides free; positions: int32 or int64, [tokens] or
     [batch, tokens]; turns: rope_turns(...), one for each pair of the rotated channels (the first
     2 * turns.numel() of a head; the others are copied).  Pairs are (j, j + half) or, interleaved, (2j, 2j + 1).
-    q_out, k_out: default in place.  inverse turns the other way: the gradient of the call without it.  Autograd does
-    not see either, so tensors that require a gradient are refused while it records: call it under torch.no_grad() or
-    from a torch.autograd.Function, with inverse in its backward."""
+    q_out, k_out: default in place; q and k share no elements, nor do their outputs with the other's.  inverse turns
+    the other way: the gradient of the call without it.  Autograd does not see either, so tensors that require a
+    gradient are refused while it records: call it under torch.no_grad() or from a torch.autograd.Function, with
+    inverse in its backward."""
     if (q.requires_grad or (k is not None and k.requires_grad) or (q_out is not None and q_out.requires_grad) or
             (k_out is not None and k_out.requires_grad)) and torch.is_grad_enabled():
         raise ValueError("autograd does not see rope: call it under torch.no_grad() or from an autograd.Function")

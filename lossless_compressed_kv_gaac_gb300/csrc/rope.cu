@@ -306,6 +306,10 @@ extern "C" int gaac_rope(const gaac_rope_tensor* tensors, int n_tensors, int dty
                         t.x_head * size, t.out_seq * size, t.out_tok * size, t.out_head * size, same ? 0 : 1};
     copies = copies || !same;
   }
+  // Two tensors with a first element in common, one of them an output.  Tensors that share others (slices of one
+  // projection's output overlap as ranges and share none) are the caller's to keep apart.
+  if (n_tensors == 2 && (tensors[0].out == tensors[1].out || tensors[0].out == tensors[1].x || tensors[1].out == tensors[0].x))
+    return GAAC_EINVAL;
   a.heads0 = tensors[0].n_heads;
   a.heads = static_cast<int>(heads);
   a.n_seq = static_cast<unsigned>(n_seq);

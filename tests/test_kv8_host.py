@@ -212,3 +212,20 @@ def test_rope_refuses_to_cut_a_graph_before_it_looks_at_devices():
         G.rope(q, None, pos, t)
     with torch.no_grad(), pytest.raises(ValueError, match="device"):
         G.rope(q, None, pos, t)
+
+
+def test_rope_refuses_q_and_k_that_share_their_first_element(lib):
+    """The second tensor's output is the first's, or one's output is the other's input: some element would be turned
+    twice, or read after it has been."""
+    other, third, fourth = GOOD + (1 << 20), GOOD + (2 << 20), GOOD + (3 << 20)
+    t = (G.gaac_rope_tensor * 2)()
+
+    def call(x0, o0, x1, o1):
+        for e, x, o in ((t[0], x0, o0), (t[1], x1, o1)):
+            e.x, e.out, e.n_heads, e.x_seq, e.x_tok, e.x_head = x, o, 2, 0, 256, 128
+            e.out_seq, e.out_tok, e.out_head = 0, 256, 128
+        return lib.gaac_rope(t, 2, 0, 1, 4, 128, 128, GOOD, 32, 0, 1, GOOD, 1.0, 0, None)
+
+    for args in ((GOOD, GOOD, GOOD, GOOD), (GOOD, other, third, other), (GOOD, other, other, third),
+                 (GOOD, third, other, GOOD), (GOOD, GOOD, other, GOOD)):
+        assert call(*args) == EINVAL, args
