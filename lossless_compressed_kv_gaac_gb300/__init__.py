@@ -692,6 +692,14 @@ def _kv8_rows(cache: Kv8, t, heads, name):
     return shape[0], (st[0] if shape[0] > 1 else shape[1] * HEAD_DIM)
 
 
+def _kv8_status(cache: Kv8, status):
+    if status is None:
+        return 0
+    if status.get_device() != cache._index or status.dtype != torch.int32 or status.numel() < 1:
+        raise ValueError("status must be an int32 tensor on the cache's device")
+    return status.data_ptr()
+
+
 def kv8_append(cache: Kv8, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor | None = None, status=None,
                stream=None, reserve: bool = False) -> None:
     """Appends rows cu_tokens[b] .. cu_tokens[b + 1] of k and v ([n, kv_heads, 128] of the cache's type, heads and
@@ -703,7 +711,7 @@ def kv8_append(cache: Kv8, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Te
     if n_v != n or (cu == 0 and n != cache.batch):
         raise ValueError("k and v must hold the same rows: one for each sequence without cu_tokens")
     _call("gaac_kv8_reserve_append" if reserve else "gaac_kv8_append", cache._index, stream, cache._ref, k.data_ptr(),
-          v.data_ptr(), n, k_row, v_row, cu, _ptr(status))
+          v.data_ptr(), n, k_row, v_row, cu, _kv8_status(cache, status))
 
 
 def kv8_attention_workspace() -> int:
@@ -724,19 +732,19 @@ def kv8_decode_attention(cache: Kv8, q: torch.Tensor, scale: float, out: torch.T
     if workspace.get_device() != cache._index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous on the cache's device")
     _call("gaac_kv8_decode_attention", cache._index, stream, cache._ref, q.data_ptr(), q.shape[1], row, scale,
-          out.data_ptr(), code, workspace.data_ptr(), workspace.nbytes, _ptr(status))
+          out.data_ptr(), code, workspace.data_ptr(), workspace.nbytes, _kv8_status(cache, status))
 
 
 def kv8_reserve(cache: Kv8, cu_tokens: torch.Tensor | None = None, status=None, stream=None) -> None:
     """Pages for the blocks that appending these tokens fills: the lowest free ones, in order of sequence and block.
     When they run out, sequences keep what they have got."""
-    _call("gaac_kv8_reserve", cache._index, stream, cache._ref, _kv8_cu(cache, cu_tokens), _ptr(status))
+    _call("gaac_kv8_reserve", cache._index, stream, cache._ref, _kv8_cu(cache, cu_tokens), _kv8_status(cache, status))
 
 
 def kv8_release(cache: Kv8, seqs: torch.Tensor, status=None, stream=None) -> None:
     """Empties the listed sequences (int32); pages that no other sequence holds become free."""
     n = _index_list(seqs, "seqs", cache)
-    _call("gaac_kv8_release", cache._index, stream, cache._ref, seqs.data_ptr(), n, _ptr(status))
+    _call("gaac_kv8_release", cache._index, stream, cache._ref, seqs.data_ptr(), n, _kv8_status(cache, status))
 
 
 def kv8_fork(cache: Kv8, src: torch.Tensor, dst: torch.Tensor, status=None, stream=None) -> None:
@@ -744,7 +752,7 @@ def kv8_fork(cache: Kv8, src: torch.Tensor, dst: torch.Tensor, status=None, stre
     n = _index_list(src, "src", cache)
     if _index_list(dst, "dst", cache) != n:
         raise ValueError("src and dst must have the same length")
-    _call("gaac_kv8_fork", cache._index, stream, cache._ref, src.data_ptr(), dst.data_ptr(), n, _ptr(status))
+    _call("gaac_kv8_fork", cache._index, stream, cache._ref, src.data_ptr(), dst.data_ptr(), n, _kv8_status(cache, status))
 
 
 def kv8_compact(cache: Kv8, moved_to: torch.Tensor, stream=None) -> None:

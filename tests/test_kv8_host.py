@@ -229,3 +229,13 @@ def test_rope_refuses_q_and_k_that_share_their_first_element(lib):
     for args in ((GOOD, GOOD, GOOD, GOOD), (GOOD, other, third, other), (GOOD, other, other, third),
                  (GOOD, third, other, GOOD), (GOOD, GOOD, other, GOOD)):
         assert call(*args) == EINVAL, args
+
+
+@pytest.mark.parametrize("index,status", [(0, torch.zeros(1, dtype=torch.int32)), (-1, torch.zeros(1)),
+                                          (-1, torch.zeros(0, dtype=torch.int32))], ids=["host", "type", "empty"])
+def test_a_status_that_the_kernels_cannot_write_is_refused(index, status):
+    class Fake:  # a cache on device `index` (-1: the host's tensors pass for its own) that never reaches the library
+        _index, _ref, batch, n_pages = index, None, 2, 8
+
+    with pytest.raises(ValueError, match="status"):
+        G.kv8_reserve(Fake(), None, status)
