@@ -30,9 +30,8 @@ constexpr int kKv8Tile = kBlock * kD;       // FP8 bytes of one (page, kv-head, 
 constexpr int kKv8Pair = 2 * kKv8Tile;      // K and V of one (page, kv-head), contiguous
 constexpr int kKv8Chunk = 8192;             // pages that one CTA counts (reserve, compact)
 
-// Workspace (int32 words): the append's counters per sequence, two tickets (reserve, compact), the pages that a
-// compaction moves and the reserve's mark of bad offsets; counters, tickets and mark are zero between calls.  Then
-// scratch that every call writes before it reads.
+// Workspace (int32 words): the append's counters per sequence and the two tickets, which are zero between calls,
+// then scratch that every call writes before it reads.
 struct Kv8Work {
   int64_t tickets, need, chunks, list_a, list_b, words;
 };

@@ -6,8 +6,8 @@
 // rows; nothing ever has to be copied on a write.
 //
 // All of it is bound by latency but the moves of a compaction, which are bound by memory.  Measured: release of 8 of
-// 32 sequences 1.3 us, fork of as many 4.9 us (one CTA a pair: 8.5 us), reserve without a need 3.5 us (65,536 pages:
-// 4.3 us), with 4,000 pages handed to 256 sequences 9.7 us; moving 2,000 pages of 8 heads (0.54 GB read and written)
+// 32 sequences 1.3 us, fork of as many 4.9 us (one CTA a pair: 8.5 us), reserve without a need 3.8 us (65,536 pages:
+// 3.6 us), with 4,096 pages handed to 256 empty sequences 11.6 us; moving 2,000 pages of 8 heads (0.54 GB read and written)
 // 77 us, 6.9 TB/s (1,216 CTAs that walk over the moves: 92 us).
 #include <algorithm>
 
@@ -73,29 +73,35 @@ __device__ __forceinline__ uint32_t held_mask(const int32_t* refs, int64_t p0, i
   return held;
 }
 
-// This CTA's chunk: counts its free (or held) pages, and says whether it is the last CTA to do so.  What the CTA's
-// threads have written before is visible to the last one.
-__device__ __forceinline__ bool count_chunk(const Kv8Dev& c, const Kv8Work& w, bool free_ones, int32_t* ticket) {
+// This CTA's chunk: counts its free (or held) pages, and says whether it is the last CTA to do so (kLast), and whether a
+// thread of any CTA came with `bad` (kLastBad).  What the CTA's threads have written before is visible to the last one.
+enum { kNotLast, kLast, kLastBad };
+__device__ __forceinline__ int count_chunk(const Kv8Dev& c, const Kv8Work& w, bool free_ones, int32_t* ticket, bool bad = false) {
+  constexpr int kBad = 1 << 16;  // beside a chunk's count in a sum over threads, and beside the count of CTAs in the ticket
+  static_assert(kKv8Chunk < kBad, "a chunk's count below the mark");
   __shared__ int last;
   uint32_t ex;
   const uint32_t held = held_mask(c.refs, static_cast<int64_t>(blockIdx.x) * kKv8Chunk + threadIdx.x * kPgPer, c.n_pages, &ex);
   int total;
-  block_exclusive(__popc(free_ones ? ex & ~held : held), &total);
+  block_exclusive(__popc(free_ones ? ex & ~held : held) + (bad ? kBad : 0), &total);
   if (threadIdx.x == 0) {
-    c.work[w.chunks + blockIdx.x] = total;
-    last = kv8_atomic_add_acq_rel(ticket, 1u) == gridDim.x - 1;
-    if (last) *ticket = 0;
+    c.work[w.chunks + blockIdx.x] = total % kBad;
+    const unsigned add = total >= kBad ? kBad + 1u : 1u, sum = kv8_atomic_add_acq_rel(ticket, add) + add;
+    last = sum % kBad != gridDim.x ? kNotLast : sum >= kBad ? kLastBad : kLast;  // at most 2^11 CTAs
+    if (last != kNotLast) *ticket = 0;
   }
   __syncthreads();
   return last;
 }
 
-// Blocks of sequence b that the next tokens fill: [lo, hi).  false: the lengths are not valid.
-__device__ __forceinline__ bool fill_range(const Kv8Dev& c, const int32_t* cu, int b, int* lo, int* hi) {
+// Blocks of sequence b that the next tokens fill: [lo, hi).  false: the lengths are not valid.  bad: nor are the offsets
+// of `rows` rows, with which the append refuses the whole call.
+__device__ __forceinline__ bool fill_range(const Kv8Dev& c, const int32_t* cu, int b, int* lo, int* hi, int64_t rows, bool* bad) {
   const int len = c.lens[b];
-  const int64_t n = cu == nullptr ? 1 : static_cast<int64_t>(cu[b + 1]) - cu[b];
+  const int64_t from = cu == nullptr ? 0 : cu[b], to = cu == nullptr ? 1 : cu[b + 1], n = to - from;
   const int64_t now = len + n;
   *lo = *hi = 0;
+  *bad = from < 0 || n < 0 || to > rows;
   if (len < 0 || n < 0 || now > static_cast<int64_t>(c.max_blocks) * kBlock) return false;
   *lo = len / kBlock;
   *hi = static_cast<int>(now / kBlock);
@@ -143,23 +149,22 @@ __global__ void __launch_bounds__(kPgThreads) kv8_reserve_kernel(Kv8Dev c, const
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int32_t* need = c.work + w.need;
   const int warps = gridDim.x * (kPgThreads / 32);
+  bool bad = false;
   for (int b0 = blockIdx.x * (kPgThreads / 32) + warp; b0 < c.batch; b0 += 32 * warps) {
     int lo = 0, hi = 0, mine = 0;
     const int64_t b = b0 + static_cast<int64_t>(lane) * warps;
-    if (b < c.batch && cu != nullptr && (cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > rows)) c.work[w.tickets + 3] = 1;
-    if (b < c.batch && !fill_range(c, cu, static_cast<int>(b), &lo, &hi)) report(status, GAAC_EINVAL);
+    bool odd = false;
+    if (b < c.batch && !fill_range(c, cu, static_cast<int>(b), &lo, &hi, rows, &odd)) report(status, GAAC_EINVAL);
+    bad = bad || odd;
     for_missing(c, b0, warps, lo, hi, [&](int k, int, bool miss) {
       const int n = __popc(__ballot_sync(0xFFFFFFFFu, miss));
       if (lane == k) mine += n;
     });
     if (b < c.batch) need[b] = mine;
   }
-  if (!count_chunk(c, w, true, c.work + w.tickets)) return;
-  if (__syncthreads_or(tid == 0 && __ldcg(c.work + w.tickets + 3) != 0)) {
-    if (tid == 0) {
-      c.work[w.tickets + 3] = 0;
-      report(status, GAAC_EINVAL);
-    }
+  const int last = count_chunk(c, w, true, c.work + w.tickets, bad);
+  if (last != kLast) {
+    if (last == kLastBad && tid == 0) report(status, GAAC_EINVAL);
     return;
   }
   // ---- the rank of each sequence's first one
@@ -174,7 +179,7 @@ __global__ void __launch_bounds__(kPgThreads) kv8_reserve_kernel(Kv8Dev c, const
   if (total == 0) return;
   // this warp's first sequences, under way while the pages are listed
   int lo0 = 0, hi0 = 0;
-  if (warp + lane * (kPgThreads / 32) < c.batch) fill_range(c, cu, warp + lane * (kPgThreads / 32), &lo0, &hi0);
+  if (warp + lane * (kPgThreads / 32) < c.batch) fill_range(c, cu, warp + lane * (kPgThreads / 32), &lo0, &hi0, rows, &bad);
   // ---- the lowest free pages, as many as are lacking
   int32_t* list = c.work + w.list_a;
   int found = 0;
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(kPgThreads) kv8_reserve_kernel(Kv8Dev c, const
     const int b = b0 + lane * (kPgThreads / 32);
     if (b0 != warp) {
       lo = hi = 0;
-      if (b < c.batch) fill_range(c, cu, b, &lo, &hi);
+      if (b < c.batch) fill_range(c, cu, b, &lo, &hi, rows, &bad);
     }
     if (b < c.batch) rank = need[b];
     for_missing(c, b0, kPgThreads / 32, lo, hi, [&](int k, int i, bool miss) {
@@ -314,7 +319,7 @@ __global__ void __launch_bounds__(kPgThreads) kv8_compact_count_kernel(Kv8Dev c)
   dependent_wait();
   dependent_launch();
   const Kv8Work w = kv8_work(c.batch, c.n_pages);
-  if (!count_chunk(c, w, false, c.work + w.tickets + 1)) return;
+  if (count_chunk(c, w, false, c.work + w.tickets + 1) == kNotLast) return;
   int run = 0;
   for (unsigned c0 = 0; c0 < gridDim.x; c0 += kPgThreads) {
     const unsigned ch = c0 + threadIdx.x;
