@@ -659,6 +659,7 @@ class Kv8:
         self._c = gaac_kv8(*(t.data_ptr() for t in self._tensors), n_pages, batch, heads, max_blocks, fmt,
                            _DTYPES[tail.dtype])
         self._ref = ctypes.byref(self._c)
+        self._own_status = (None, 0)  # a status tensor made with the cache, and its address
 
     pages = property(lambda s: s._tensors[0])
     scales = property(lambda s: s._tensors[1])
@@ -693,6 +694,9 @@ def _kv8_rows(cache: Kv8, t, heads, name):
 
 
 def _kv8_status(cache: Kv8, status):
+    own, at = cache._own_status
+    if status is own:
+        return at
     if status is None:
         return 0
     if status.get_device() != cache._index or status.dtype != torch.int32 or status.numel() < 1:

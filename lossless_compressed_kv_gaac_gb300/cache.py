@@ -168,6 +168,7 @@ class Kv8Cache(Kv8):
     def _over(self, *args):
         Kv8.__init__(self, *args)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._own_status = (self.status, self.status.data_ptr())
         with torch.cuda.device(self.device):
             self._ws = torch.zeros(kv8_attention_workspace(), dtype=torch.uint8, device=self.device)
 

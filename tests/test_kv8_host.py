@@ -235,7 +235,7 @@ def test_rope_refuses_q_and_k_that_share_their_first_element(lib):
                                           (-1, torch.zeros(0, dtype=torch.int32))], ids=["host", "type", "empty"])
 def test_a_status_that_the_kernels_cannot_write_is_refused(index, status):
     class Fake:  # a cache on device `index` (-1: the host's tensors pass for its own) that never reaches the library
-        _index, _ref, batch, n_pages = index, None, 2, 8
+        _index, _ref, batch, n_pages, _own_status = index, None, 2, 8, (None, 0)
 
     with pytest.raises(ValueError, match="status"):
         G.kv8_reserve(Fake(), None, status)
