@@ -515,7 +515,8 @@ GAAC_API int gaac_rope(const gaac_rope_tensor* tensors, int n_tensors, int dtype
  *  refs      int32 [n_pages]: sequences that hold a page; 0 = free.  16-byte aligned
  *  seq_lens  int32 [batch]
  *  work      gaac_kv8_workspace(batch, n_pages) bytes, 16-byte aligned, zero before the first
- *            call; calls on one cache are ordered on the GPU (one stream, or events)
+ *            call; calls on one cache are ordered on the GPU (one stream, or events), but that
+ *            attentions with a workspace each may overlap one another
  * batch <= 65535, n_kv_heads <= 1024, 128 * n_kv_heads * n_pages < 2^31 and the same for batch.
  * A full block has a page, and so may blocks reserved ahead; a full block never changes.  Lengths,
  * tables and counts change through the calls below only.  A new cache has seq_lens and refs 0 and table -1. */

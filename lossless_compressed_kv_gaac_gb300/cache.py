@@ -144,6 +144,10 @@ class Kv8Cache(Kv8):
     """One layer's 8-bit paged KV cache: FP8 pages of 64 tokens with a scale for each (page, kv-head, K|V), the open
     block of every sequence in the model's type, and counted pages that sequences share.
 
+    Calls on one cache share its workspaces, attention too: they are ordered on the GPU (one stream, or events), and
+    after whatever made the cache.  Attentions that run beside one another take kv8_decode_attention with a workspace
+    each.
+
     dtype: BF16 or FP16, the type of k, v, q and the open block.  Faults that only the device sees (no page left, a
     length past the table, offsets out of order) are recorded in `status`, as by the calls of the lossless cache; such
     a call leaves the sequence's tokens as they were, with the pages that could be reserved for it.

@@ -7,7 +7,9 @@
 // Angles: w_j comes as a fraction of a turn in 64-bit fixed point, F_j = w_j / (2 pi) * 2^64.  The product
 // p * F_j modulo 2^64 is the exact fraction of the turn whatever the position (32-bit floats would be off by
 // 0.06 rad at a million), and its top 32 bits, as a signed number, are the angle in [-pi, pi): one float
-// conversion, then sincospi.  The angle is off by at most 2^-33 turns plus p * 2^-65.
+// conversion, then sincospi.  The angle is off by at most 2^-26 turns for the conversion, 2^-33 for the bits left
+// out, and p times the table's own error: 2^-65 where F_j is the nearest, 2^-52 of w_j / (2 pi) where it comes from
+// 64-bit floats (2^-34 turns at a million for the fastest pair).
 //
 // Memory bound: every byte of input is read once and written once.  A thread owns V pairs (16-byte vectors where
 // alignment allows) of one row and walks over up to five heads with them, so V sines and cosines serve all of these;
@@ -325,8 +327,8 @@ extern "C" int gaac_rope(const gaac_rope_tensor* tensors, int n_tensors, int dty
   a.inverse = (flags & GAAC_ROPE_INVERSE) != 0;
   a.rot_units = rot_dim / 2 / v;
   a.units = a.rot_units + (copies ? ((head_dim - rot_dim) / v + 1) / 2 : 0);
-  // Heads per thread: as many as leave every SM its threads, so that sines are shared where there is work for all,
-  // and single heads where latency counts.
+  // Heads per thread: as many as leave twice the threads that 152 SMs hold at a time (16 CTAs of 64 each), so that
+  // sines are shared where there is work for all, and single heads where latency counts.
   const int64_t want = int64_t{152} * 2048, per_row = rows * a.units;
   const int64_t walkers = std::max<int64_t>((heads + kRopeMost - 1) / kRopeMost, (want + per_row - 1) / per_row);
   a.walkers = static_cast<int>(std::min<int64_t>(heads, walkers));

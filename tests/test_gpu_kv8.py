@@ -914,3 +914,20 @@ def test_readme_serving_loop():
     assert ok(c) == 0 and int(c.seq_lens[3]) == want[1]
     assert (names["out"][[0, 31]] == 0).all()
     assert names["k8"].shape == c.pages.shape
+
+
+def test_two_attentions_at_once():
+    """Two streams, a workspace each, one cache: the results of one after the other."""
+    c, _, _ = filled([30000, 33, 1500, 0, 700], 4)
+    q = [rand((5, 16, 128), BF16, s) for s in (5, 6)]
+    right = [c.attention(x, SCALE) for x in q]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in q], [torch.empty_like(x) for x in q]
+    ws = [torch.zeros(G.kv8_attention_workspace(), dtype=torch.uint8, device="cuda") for _ in q]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for i in (0, 1):
+            G.kv8_decode_attention(c, q[i], SCALE, outs[i], ws[i], c.status, streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, right)) and ok(c) == 0
+    assert all((w[:3 * 4 * torch.cuda.get_device_properties(0).multi_processor_count] == 0).all() for w in ws)
