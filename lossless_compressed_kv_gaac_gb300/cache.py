@@ -17,6 +17,8 @@ def _stream_object(stream, device) -> torch.cuda.Stream | None:
     if stream is None or isinstance(stream, torch.cuda.Stream):
         return stream
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle in (0, 1, 2):  # the default stream, or a thread's, which keeps its order with that
+        return torch.cuda.default_stream(device)
     return torch.cuda.ExternalStream(handle, device=device)
 
 

@@ -3,7 +3,7 @@ happens on that call's stream."""
 import pytest
 import torch
 
-from lossless_compressed_kv_gaac_gb300.cache import LayerCache
+from lossless_compressed_kv_gaac_gb300.cache import LayerCache, _stream_object as stream_object
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +97,27 @@ def test_first_attention_on_a_side_stream_has_a_zeroed_workspace():
         out = c.attention(q, 0.1, stream=handle)
         torch.cuda.synchronize()
         assert int(c.status.item()) == 0 and torch.equal(out, right)
+
+
+@pytest.mark.parametrize("handle", [0, 1, 2])
+def test_raw_handle_of_the_default_stream(handle):
+    """0 and 1 (the legacy default stream's names) are that stream, for what a call makes too; 2 is the thread's default
+    stream, which waits for that one and makes it wait."""
+    k, v, q, lens = inputs()
+    c = cache(k, v, lens)
+    right = c.attention(q, 0.1)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(BUSY)
+        k2, v2 = c.decompress(k.shape[1], stream=handle)
+        out = c.attention(q, 0.1, stream=handle)
+    done = torch.cuda.default_stream().record_event()
+    done.synchronize()
+    assert not s.query()  # nothing of it waited for the current stream
+    used = torch.full_like(k2, 7)  # the default stream's memory, of which the results' is a part
+    n = int(lens)
+    torch.cuda.synchronize()
+    assert torch.equal(k2[:, :n], k[:, :n]) and torch.equal(v2[:, :n], v[:, :n]) and torch.equal(out, right)
+    assert used.eq(7).all() and int(c.status.item()) == 0
+    assert stream_object(handle, c.device).cuda_stream == 0 and stream_object(None, c.device) is None
