@@ -23,40 +23,40 @@ DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 def listed():
     return [
         # a decode step's queries and keys: launch latency
-        {"name": "norm+rope decode 32, 32q/8kv", "op": "norm", "tokens": 32, "hq": 32, "hk": 8, "dim": 128, "rot": 128,
+        {"name": "norm+rope decode 32 32q/8kv", "op": "norm", "tokens": 32, "hq": 32, "hk": 8, "dim": 128, "rot": 128,
          "dtype": "bf16", "interleaved": False, "far": 131072},
         # prefill of a long prompt
-        {"name": "norm+rope prefill 32768, 32q/8kv", "op": "norm", "tokens": 32768, "hq": 32, "hk": 8, "dim": 128,
+        {"name": "norm+rope prefill 32768 32q/8kv", "op": "norm", "tokens": 32768, "hq": 32, "hk": 8, "dim": 128,
          "rot": 128, "dtype": "bf16", "interleaved": False, "far": 32768},
         # a training step's gradient: an odd number of tokens, half of the head turned, interleaved pairs
-        {"name": "norm+rope gradient 4999, 16q/8kv, half", "op": "norm_grad", "tokens": 4999, "hq": 16, "hk": 8,
+        {"name": "norm+rope gradient 4999 16q/8kv half", "op": "norm_grad", "tokens": 4999, "hq": 16, "hk": 8,
          "dim": 128, "rot": 64, "dtype": "fp16", "interleaved": True, "far": 1000000},
         # the same of a larger batch
-        {"name": "norm+rope gradient 16384, 32q/8kv", "op": "norm_grad", "tokens": 16384, "hq": 32, "hk": 8,
+        {"name": "norm+rope gradient 16384 32q/8kv", "op": "norm_grad", "tokens": 16384, "hq": 32, "hk": 8,
          "dim": 128, "rot": 128, "dtype": "bf16", "interleaved": False, "far": 32768},
         # one short chat: few tiles, latency
-        {"name": "prompt 1 x 777, 16q/8kv", "op": "prompt", "batch": 1, "lo": 777, "hi": 777, "hq": 16, "hkv": 8,
+        {"name": "prompt 1 x 777 16q/8kv", "op": "prompt", "batch": 1, "lo": 777, "hi": 777, "hq": 16, "hkv": 8,
          "dtype": "bf16"},
         # a batch of short and middling prompts admitted together
-        {"name": "prompt 32 x 1-2048, 16q/8kv", "op": "prompt", "batch": 32, "lo": 1, "hi": 2048, "hq": 16, "hkv": 8,
+        {"name": "prompt 32 x 1-2048 16q/8kv", "op": "prompt", "batch": 32, "lo": 1, "hi": 2048, "hq": 16, "hkv": 8,
          "dtype": "fp16"},
         # few longer ones of very different lengths, an odd number of heads to a kv-head
-        {"name": "prompt 8 x 300-5000, 20q/4kv", "op": "prompt", "batch": 8, "lo": 300, "hi": 5000, "hq": 20,
+        {"name": "prompt 8 x 300-5000 20q/4kv", "op": "prompt", "batch": 8, "lo": 300, "hi": 5000, "hq": 20,
          "hkv": 4, "dtype": "bf16"},
         # one long document
-        {"name": "prompt 1 x 16384, 32q/8kv", "op": "prompt", "batch": 1, "lo": 16384, "hi": 16384, "hq": 32,
+        {"name": "prompt 1 x 16384 32q/8kv", "op": "prompt", "batch": 1, "lo": 16384, "hi": 16384, "hq": 32,
          "hkv": 8, "dtype": "bf16"},
         # one search of four beams over a small vocabulary: latency
-        {"name": "select 1 x 4, 32000", "op": "select", "batch": 1, "beams": 4, "n_out": 4, "vocab": 32000,
+        {"name": "select 1 x 4 32000", "op": "select", "batch": 1, "beams": 4, "n_out": 4, "vocab": 32000,
          "dtype": "fp32", "ended": 0.0},
         # a batch of searches over a large, odd one, some beams ended, twice the beams wanted
-        {"name": "select 32 x 8, 128511", "op": "select", "batch": 32, "beams": 8, "n_out": 16, "vocab": 128511,
+        {"name": "select 32 x 8 128511", "op": "select", "batch": 32, "beams": 8, "n_out": 16, "vocab": 128511,
          "dtype": "bf16", "ended": 0.1},
         # four searches of four beams behind a short prompt
-        {"name": "reorder 4 x 4, up to 1000 tokens", "op": "reorder", "batch": 4, "beams": 4, "tokens": 1000,
+        {"name": "reorder 4 x 4 up to 1000 tokens", "op": "reorder", "batch": 4, "beams": 4, "tokens": 1000,
          "max_blocks": 64, "hkv": 8, "dtype": "bf16"},
         # a batch of searches behind long ones
-        {"name": "reorder 32 x 8, up to 30000 tokens", "op": "reorder", "batch": 32, "beams": 8, "tokens": 30000,
+        {"name": "reorder 32 x 8 up to 30000 tokens", "op": "reorder", "batch": 32, "beams": 8, "tokens": 30000,
          "max_blocks": 512, "hkv": 8, "dtype": "bf16"},
     ]
 
