@@ -69,6 +69,7 @@ extern "C" {
 #define GAAC_ESC_CAPACITY 496
 #define GAAC_RAW_TILE_BYTES 16384
 #define GAAC_MAX_GQA 8 /* query heads per kv-head supported by decode attention */
+#define GAAC_MAX_BEAMS 32 /* beams of a search */
 
 /* Status codes (return values and *d_status). */
 enum {
@@ -504,6 +505,47 @@ GAAC_API int gaac_rope(const gaac_rope_tensor* tensors, int n_tensors, int dtype
                        int head_dim, int rot_dim, const void* positions, int pos_bits, int64_t pos_seq_stride,
                        int64_t pos_tok_stride, const uint64_t* turns, float mscale, unsigned flags, void* stream);
 
+/* One tensor of gaac_qk_norm_rope: elements as in gaac_rope_tensor, and the norm's weights [head_dim] of
+ * weight_dtype (NULL: ones), shared by all heads.  Gradient only (else not read): dz, the gradient of the
+ * result, and dweight, fp32 [head_dim], which receives the weights' gradient (NULL: not wanted). */
+typedef struct {
+  const void* x;
+  const void* dz;
+  void* out;
+  const void* weight;
+  float* dweight;
+  int32_t n_heads;
+  int64_t x_seq, x_tok, x_head;
+  int64_t dz_seq, dz_tok, dz_head;
+  int64_t out_seq, out_tok, out_head;
+} gaac_norm_tensor;
+
+/*
+ * Norms of every head of one or two tensors (q and k), then gaac_rope, in one pass:
+ *   y = x / sqrt(mean(x^2) + eps) * weight,  the first rot_dim channels of y turned by the position.
+ * weight_dtype: dtype or GAAC_F32.  eps >= 0.  2 <= rot_dim <= head_dim <= 256, both even.  Everything else as
+ * gaac_rope (flags: GAAC_ROPE_INTERLEAVED).  Computed in fp32 and rounded once; the mean of x^2 has to be in
+ * fp32's range.  A head of zeros stays zeros with eps > 0 and becomes NaN with eps = 0.
+ */
+GAAC_API int gaac_qk_norm_rope(const gaac_norm_tensor* tensors, int n_tensors, int dtype, int weight_dtype, int64_t n_seq,
+                               int64_t n_tok, int head_dim, int rot_dim, const void* positions, int pos_bits,
+                               int64_t pos_seq_stride, int64_t pos_tok_stride, const uint64_t* turns, float mscale, float eps,
+                               unsigned flags, void* stream);
+
+/*
+ * The gradient of gaac_qk_norm_rope with the same x, weights, positions, turns, mscale and eps: out receives that
+ * of x (out may be dz or x itself with the same strides), dweight that of the weights, summed over all tokens and
+ * heads in fp32 in an order that the sizes alone decide.  No tokens: dweight is zero.  workspace:
+ * gaac_qk_norm_rope_workspace(head_dim) bytes, 16-byte aligned, of any contents; not shared by calls that may
+ * overlap on the GPU.  The two tensors have a dweight of their own.
+ */
+GAAC_API size_t gaac_qk_norm_rope_workspace(int head_dim);
+GAAC_API int gaac_qk_norm_rope_gradient(const gaac_norm_tensor* tensors, int n_tensors, int dtype, int weight_dtype,
+                                        int64_t n_seq, int64_t n_tok, int head_dim, int rot_dim, const void* positions,
+                                        int pos_bits, int64_t pos_seq_stride, int64_t pos_tok_stride, const uint64_t* turns,
+                                        float mscale, float eps, unsigned flags, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
 /* One layer's 8-bit paged cache, in caller-owned device memory.
  *  pages     [n_pages][n_kv_heads][2 (K, V)][64][128] FP8 numbers (fmt: GAAC_FP8_E4M3 or
  *            GAAC_FP8_E5M2), 16-byte aligned; a value is its FP8 number times its scale
@@ -603,10 +645,35 @@ GAAC_API int gaac_kv8_release(const gaac_kv8* cache, const int32_t* seqs, int n,
 GAAC_API int gaac_kv8_fork(const gaac_kv8* cache, const int32_t* src, const int32_t* dst, int n, int32_t* d_status,
                            void* stream);
 
+/* The sequences of a beam search follow its choice: for groups of `beams` sequences (at most GAAC_MAX_BEAMS; batch is a
+ * multiple), sequence g*beams + i becomes what g*beams + parents[g*beams + i] was, all at once (int32 [batch] on the
+ * device; a parent may have several, or no, sequences).  Full blocks are shared, the open block's rows copied; a sequence
+ * that changes gives its old row's pages up, reserved ones among them.  A parent outside [0, beams): GAAC_EINVAL, a parent
+ * whose length is not valid: GAAC_EFORMAT, and the sequence stays as it was; a page index outside the pool in a full block
+ * is taken over uncounted and reports GAAC_EFORMAT. */
+GAAC_API int gaac_kv8_reorder(const gaac_kv8* cache, const int32_t* parents, int beams, int32_t* d_status, void* stream);
+
 /* Moves the held pages to the front of the pool: with n held, the lowest free page below n takes
  * the contents of the highest held one at n or above, and so on.  The table follows.
  * moved_to: int32 [n_pages] on the device, each page's new place, -1 for a free one. */
 GAAC_API int gaac_kv8_compact(const gaac_kv8* cache, int32_t* moved_to, void* stream);
+
+/*
+ * A beam search's selection: for each of batch searches of `beams` beams, the n_out largest of
+ *   scores[b][i] + x[b][i][t] - ln sum_u exp x[b][i][u]
+ * over beams i and tokens t < vocab, in descending order, equal ones in that of i * vocab + t.  logits: dtype
+ * GAAC_BF16, GAAC_F16 or GAAC_F32, row b*beams + i at row_stride elements times that; scores fp32 [batch][beams].
+ * ended: uint8 [batch][beams] or NULL; a beam that has ended has one candidate, end_token, at its score.  Out, each
+ * [batch][n_out]: fp32 out_scores, int32 parents (the beam i) and int32 tokens.  What is left counts as -infinity: the
+ * other tokens of an ended beam, logits of -infinity, and all of a beam whose score or sum is not finite (its logits are
+ * all -infinity, or one is NaN or infinity).  1 <= beams <= GAAC_MAX_BEAMS, 1 <= n_out <= 64 and beams*vocab,
+ * 1 <= vocab <= 2^20.  Sums are fp32 over 8,192 logits, 64 bits over these.  workspace: gaac_beam_workspace() bytes (0 for
+ * arguments that are not valid), 16-byte aligned, of any contents; not shared by calls that may overlap on the GPU.
+ */
+GAAC_API size_t gaac_beam_workspace(int batch, int beams, int vocab, int n_out);
+GAAC_API int gaac_beam_select(const void* logits, int dtype, int64_t row_stride, const float* scores, const uint8_t* ended,
+                              int end_token, int batch, int beams, int vocab, int n_out, float* out_scores, int32_t* parents,
+                              int32_t* tokens, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -122,6 +122,13 @@ def lib() -> ctypes.CDLL:
             L.gaac_rope.argtypes = [P, i32, i32, i64, i64, i32, i32, P, i32, i64, i64, P, ctypes.c_float,
                                     ctypes.c_uint, P]
             L.gaac_rope.restype = i32
+            L.gaac_qk_norm_rope_workspace.argtypes = [i32]
+            L.gaac_qk_norm_rope_workspace.restype = sz
+            L.gaac_qk_norm_rope.argtypes = [P, i32, i32, i32, i64, i64, i32, i32, P, i32, i64, i64, P, ctypes.c_float,
+                                            ctypes.c_float, ctypes.c_uint, P]
+            L.gaac_qk_norm_rope.restype = i32
+            L.gaac_qk_norm_rope_gradient.argtypes = L.gaac_qk_norm_rope.argtypes[:-1] + [P, sz, P]
+            L.gaac_qk_norm_rope_gradient.restype = i32
             L.gaac_kv8_workspace.argtypes = [i32, i64]
             L.gaac_kv8_workspace.restype = sz
             L.gaac_kv8_append.argtypes = [P, P, P, i64, i64, i64, P, P, P]
@@ -138,6 +145,12 @@ def lib() -> ctypes.CDLL:
             L.gaac_kv8_release.restype = i32
             L.gaac_kv8_fork.argtypes = [P, P, P, i32, P, P]
             L.gaac_kv8_fork.restype = i32
+            L.gaac_kv8_reorder.argtypes = [P, P, i32, P, P]
+            L.gaac_kv8_reorder.restype = i32
+            L.gaac_beam_workspace.argtypes = [i32, i32, i32, i32]
+            L.gaac_beam_workspace.restype = sz
+            L.gaac_beam_select.argtypes = [P, i32, i64, P, P, i32, i32, i32, i32, i32, P, P, P, P, sz, P]
+            L.gaac_beam_select.restype = i32
             L.gaac_kv8_compact.argtypes = [P, P, P]
             L.gaac_kv8_compact.restype = i32
             _lib = L
@@ -613,6 +626,122 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, turns
           (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0))
 
 
+class gaac_norm_tensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("dz", ctypes.c_void_p), ("out", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p), ("n_heads", ctypes.c_int32),
+                ("x_seq", ctypes.c_int64), ("x_tok", ctypes.c_int64), ("x_head", ctypes.c_int64),
+                ("dz_seq", ctypes.c_int64), ("dz_tok", ctypes.c_int64), ("dz_head", ctypes.c_int64),
+                ("out_seq", ctypes.c_int64), ("out_tok", ctypes.c_int64), ("out_head", ctypes.c_int64)]
+
+
+_NORM_TENSOR = struct.Struct("@5Pi9q")  # gaac_norm_tensor packed in one go
+assert _NORM_TENSOR.size == ctypes.sizeof(gaac_norm_tensor)
+
+
+def _head_strides(t, shape, dtype, index, name):
+    """(seq, token, head) strides of t, which must have this shape, type and device, channels contiguous."""
+    st = t.stride()
+    if t.shape != shape or t.dtype != dtype or t.get_device() != index or (st[-1] != 1 and shape[-1] > 1):
+        raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim] of q's type and device, "
+                         "channels contiguous")
+    return (0, st[0], st[1]) if len(shape) == 3 else st[:3]
+
+
+def _norm_pair(x, dz, out, weight, dweight, dtype, index, name):
+    """gaac_norm_tensor of an input, its result's gradient (or None), the output (None: in place of dz, else of x) and the
+    weights, and the weights' type (None without them)."""
+    shape = x.shape
+    if len(shape) not in (3, 4):
+        raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
+    xs = _head_strides(x, shape, dtype, index, name)
+    zs, z_at = (0, 0, 0), 0
+    if dz is not None:
+        zs, z_at = _head_strides(dz, shape, dtype, index, "d" + name), dz.data_ptr()
+    if out is None:
+        out_at, so = (x.data_ptr(), xs) if dz is None else (z_at, zs)
+    else:
+        out_at, so = out.data_ptr(), _head_strides(out, shape, dtype, index, f"{name}'s output")
+    at = [0, 0]
+    for i, (w, types) in enumerate(((weight, (dtype, torch.float32)), (dweight, (torch.float32,)))):
+        if w is not None:
+            if w.shape != shape[-1:] or w.dtype not in types or w.get_device() != index or not w.is_contiguous():
+                raise ValueError(f"{name}'s weights must be contiguous [dim] on its device, of its type or fp32, their "
+                                 "gradient fp32")
+            at[i] = w.data_ptr()
+    return _NORM_TENSOR.pack(x.data_ptr(), z_at, out_at, at[0], at[1], shape[-2], *xs, *zs, *so), \
+        None if weight is None else weight.dtype
+
+
+def _norm_rope(fn, q, k, dq, dk, q_out, k_out, q_weight, k_weight, dq_weight, dk_weight, positions, turns, interleaved,
+               mscale, eps, stream, *more):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in
+                                       (q, k, dq, dk, q_out, k_out, q_weight, k_weight, dq_weight, dk_weight)):
+        raise ValueError("autograd does not see qk_norm_rope: call it under torch.no_grad() or from an autograd.Function")
+    dtype, index, shape = q.dtype, q.get_device(), q.shape
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError("q must be BF16, FP16 or FP32")
+    if index < 0 or positions.get_device() != index or turns.get_device() != index:
+        raise ValueError("tensors must be on one CUDA device")
+    desc, w_type = _norm_pair(q, dq, q_out, q_weight, dq_weight, dtype, index, "q")
+    count = 1
+    if k is not None:
+        if k.dim() != len(shape) or k.shape[:-2] != shape[:-2] or k.shape[-1] != shape[-1]:
+            raise ValueError("k must have q's tokens and width")
+        second, k_type = _norm_pair(k, dk, k_out, k_weight, dk_weight, dtype, index, "k")
+        if w_type is not None and k_type is not None and w_type != k_type:
+            raise ValueError("the weights of q and k must be of one type")
+        desc, count, w_type = desc + second, 2, w_type or k_type
+    elif dk is not None or k_out is not None or k_weight is not None or dk_weight is not None:
+        raise ValueError("k's gradient, output or weights without k")
+    if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+        raise ValueError("turns must be a contiguous int64 tensor [pairs]")
+    pos_type = positions.dtype
+    if pos_type != torch.int32 and pos_type != torch.int64:
+        raise ValueError("positions must be int32 or int64")
+    n_seq, n_tok = (1, shape[0]) if len(shape) == 3 else shape[:2]
+    pos_shape, ps = positions.shape, positions.stride()
+    if len(pos_shape) == 1 and pos_shape[0] == n_tok:
+        ps = (0, ps[0])
+    elif len(shape) != 4 or pos_shape != shape[:2]:
+        raise ValueError("positions must be [tokens] or [batch, tokens]")
+    _call(fn, index, stream, desc, count, code, code if w_type is None else _DTYPES[w_type], n_seq, n_tok, shape[-1],
+          2 * turns.shape[0], positions.data_ptr(), 32 if pos_type == torch.int32 else 64, *ps, turns.data_ptr(), mscale,
+          eps, ROPE_INTERLEAVED if interleaved else 0, *more)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor | None, k_weight: torch.Tensor | None,
+                 positions: torch.Tensor, turns: torch.Tensor, eps: float = 1e-6, q_out=None, k_out=None,
+                 interleaved: bool = False, mscale: float = 1.0, stream=None) -> None:
+    """Norms of every head of q and, if given, k, x / sqrt(mean(x^2) + eps) * weight, and their rotary positions, in
+    one pass.  q_weight, k_weight: [dim] of q's type or fp32, None for ones; dim is at most 256.  Everything else as
+    in rope: in place by default, and not seen by autograd (qk_norm_rope_gradient is its backward)."""
+    _norm_rope("gaac_qk_norm_rope", q, k, None, None, q_out, k_out, q_weight, k_weight, None, None, positions, turns,
+               interleaved, mscale, eps, stream)
+
+
+def qk_norm_rope_workspace(dim: int) -> int:
+    """Bytes of qk_norm_rope_gradient's workspace, of any contents."""
+    return lib().gaac_qk_norm_rope_workspace(dim)
+
+
+def qk_norm_rope_gradient(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Tensor, k: torch.Tensor | None,
+                          q_weight: torch.Tensor | None, k_weight: torch.Tensor | None, positions: torch.Tensor,
+                          turns: torch.Tensor, dq_weight: torch.Tensor | None, dk_weight: torch.Tensor | None,
+                          workspace: torch.Tensor, eps: float = 1e-6, dq_out=None, dk_out=None, interleaved: bool = False,
+                          mscale: float = 1.0, stream=None) -> None:
+    """The backward pass of qk_norm_rope: dq, dk are the gradients of its results, q and k what it was given (not
+    its results).  dq_out, dk_out receive the gradients of q and k (default: in place of dq and dk), dq_weight and
+    dk_weight, fp32 [dim] or None, those of the weights.  workspace: qk_norm_rope_workspace(dim) bytes, not shared by
+    calls that may overlap on the GPU."""
+    if (dk is None) != (k is None) or dq is None:
+        raise ValueError("q and k each go with their gradient")
+    if workspace.get_device() != q.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on q's device")
+    _norm_rope("gaac_qk_norm_rope_gradient", q, k, dq, dk, dq_out, dk_out, q_weight, k_weight, dq_weight, dk_weight,
+               positions, turns, interleaved, mscale, eps, stream, workspace.data_ptr(), workspace.nbytes)
+
+
 # ---------------------------------------------------------------- 8-bit paged cache
 class gaac_kv8(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("tail", ctypes.c_void_p),
@@ -759,9 +888,62 @@ def kv8_fork(cache: Kv8, src: torch.Tensor, dst: torch.Tensor, status=None, stre
     _call("gaac_kv8_fork", cache._index, stream, cache._ref, src.data_ptr(), dst.data_ptr(), n, _kv8_status(cache, status))
 
 
+def kv8_reorder(cache: Kv8, parents: torch.Tensor, status=None, stream=None) -> None:
+    """parents: int32 [groups, beams], groups * beams sequences: sequence g * beams + i becomes what
+    g * beams + parents[g, i] was, all at once.  Full blocks are shared, open blocks copied, reserved pages of the
+    sequences that change given back."""
+    if parents.dtype != torch.int32 or parents.dim() != 2 or not parents.is_contiguous() or \
+            parents.get_device() != cache._index or parents.numel() != cache.batch:
+        raise ValueError("parents must be a contiguous int32 tensor [groups, beams] of the cache's sequences and device")
+    _call("gaac_kv8_reorder", cache._index, stream, cache._ref, parents.data_ptr(), parents.shape[1], _kv8_status(cache, status))
+
+
 def kv8_compact(cache: Kv8, moved_to: torch.Tensor, stream=None) -> None:
     """Moves the held pages to the front of the pool; moved_to (int32 [n_pages]) gets each page's new place, -1 for
     free ones."""
     if _index_list(moved_to, "moved_to", cache) != cache.n_pages:
         raise ValueError("moved_to must hold n_pages values")
     _call("gaac_kv8_compact", cache._index, stream, cache._ref, moved_to.data_ptr())
+
+
+# ---------------------------------------------------------------- beam search
+def beam_workspace(batch: int, beams: int, vocab: int, n_out: int) -> int:
+    """Bytes of beam_select's workspace, of any contents; 0 for sizes that it does not take."""
+    return lib().gaac_beam_workspace(batch, beams, vocab, n_out)
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, out_scores: torch.Tensor, parents: torch.Tensor,
+                tokens: torch.Tensor, workspace: torch.Tensor, ended: torch.Tensor | None = None, end_token: int = 0,
+                stream=None) -> None:
+    """The n_out largest of scores[b, i] + log_softmax(logits[b * beams + i])[t] over beams i and tokens t, for each
+    search b, in descending order, equal ones by i, then t.  logits: [batch * beams, vocab], BF16, FP16 or FP32, tokens
+    contiguous (rows may be strided); scores: fp32 [batch, beams].  out_scores (fp32), parents (the beam i) and tokens
+    (int32): [batch, n_out].  ended: bool or uint8 [batch, beams]; such a beam has one candidate, end_token, at its score.
+    A beam whose score or sum of exponentials is not finite has none; where there are too few, the lowest of the others
+    follow at -infinity.  workspace: beam_workspace(...) bytes, not shared by calls that may overlap on the GPU."""
+    index = logits.get_device()
+    code = _DTYPES.get(logits.dtype)
+    if torch.is_grad_enabled() and (logits.requires_grad or scores.requires_grad):
+        raise ValueError("autograd does not see beam_select: call it under torch.no_grad()")
+    if code is None or logits.dim() != 2 or index < 0 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be BF16, FP16 or FP32 [batch * beams, vocab] on a CUDA device, tokens contiguous")
+    if scores.dim() != 2 or scores.dtype != torch.float32 or not scores.is_contiguous() or scores.get_device() != index or \
+            scores.numel() != logits.shape[0]:
+        raise ValueError("scores must be contiguous fp32 [batch, beams] on the logits' device")
+    batch, beams = scores.shape
+    shape = out_scores.shape
+    if len(shape) != 2 or shape[0] != batch or parents.shape != shape or tokens.shape != shape:
+        raise ValueError("out_scores, parents and tokens must be [batch, n_out]")
+    for t, dtype, name in ((out_scores, torch.float32, "out_scores"), (parents, torch.int32, "parents"),
+                           (tokens, torch.int32, "tokens")):
+        if t.dtype != dtype or t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous on the logits' device, of {dtype}")
+    if ended is not None and (ended.dtype not in (torch.bool, torch.uint8) or ended.shape != scores.shape or
+                              not ended.is_contiguous() or ended.get_device() != index):
+        raise ValueError("ended must be contiguous bool or uint8 [batch, beams] on the logits' device")
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the logits' device")
+    _call("gaac_beam_select", index, stream, logits.data_ptr(), code, max(logits.stride(0), logits.shape[1]) if
+          logits.shape[0] <= 1 else logits.stride(0), scores.data_ptr(), 0 if ended is None else ended.data_ptr(), end_token,
+          batch, beams, logits.shape[1], shape[1], out_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(),
+          workspace.data_ptr(), workspace.nbytes)

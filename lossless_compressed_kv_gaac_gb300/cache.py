@@ -7,9 +7,10 @@ from __future__ import annotations
 
 import torch
 
-from . import (BLOCK, FP8_E4M3, HEAD_DIM, Kv8, Pools, append, attention_workspace, calibrate, decode_attention,
-               decode_attention_bf16, decompress, encode_blocks, entry_fields, kv8_append, kv8_attention_workspace,
-               kv8_compact, kv8_decode_attention, kv8_fork, kv8_release, kv8_reserve, new_stats, new_table)
+from . import (BLOCK, FP8_E4M3, HEAD_DIM, Kv8, Pools, append, attention_workspace, beam_select, beam_workspace, calibrate,
+               decode_attention, decode_attention_bf16, decompress, encode_blocks, entry_fields, kv8_append,
+               kv8_attention_workspace, kv8_compact, kv8_decode_attention, kv8_fork, kv8_release, kv8_reorder,
+               kv8_reserve, new_stats, new_table)
 
 
 def _stream_object(stream, device) -> torch.cuda.Stream | None:
@@ -201,8 +202,40 @@ class Kv8Cache(Kv8):
     def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None):
         kv8_fork(self, src, dst, self.status, stream)
 
+    def reorder(self, parents: torch.Tensor, stream=None):
+        """The beams of each search follow its choice: sequence g * beams + i becomes what g * beams + parents[g, i] was
+        (int32 [groups, beams], as Beams.select gives them)."""
+        kv8_reorder(self, parents, self.status, stream)
+
     def compact(self, stream=None) -> torch.Tensor:
         """int32 [n_pages]: where each page has gone, -1 for free ones."""
         moved_to = _made_for(stream, self.device, lambda: torch.empty_like(self.refs))
         kv8_compact(self, moved_to, stream)
         return moved_to
+
+
+class Beams:
+    """The choice of `batch` beam searches of `beams` beams over a vocabulary, with its workspace: beam i of search b is
+    row b * beams + i of the logits, and sequence b * beams + i of a cache.
+
+    n_out: candidates that are chosen (default: beams).  end_token: what ended beams go on with.  Calls on one object
+    share its workspace: they are ordered on the GPU, and after whatever made it."""
+
+    def __init__(self, batch: int, beams: int, vocab: int, n_out: int | None = None, end_token: int = 0, device="cuda"):
+        self.batch, self.beams, self.vocab, self.end_token = batch, beams, vocab, end_token
+        self.n_out = beams if n_out is None else n_out
+        need = beam_workspace(batch, beams, vocab, self.n_out)
+        if need == 0:
+            raise ValueError("batch >= 1, 1 <= beams <= 32, 1 <= n_out <= 64 and 1 <= vocab <= 2^20 are wanted")
+        self.device = torch.device(device)
+        self._ws = torch.empty(need, dtype=torch.uint8, device=device)
+
+    def select(self, logits: torch.Tensor, scores: torch.Tensor, ended: torch.Tensor | None = None, stream=None):
+        """logits [batch * beams, vocab], scores fp32 [batch, beams], ended bool or uint8 [batch, beams] -> (scores fp32,
+        parents int32, tokens int32), each [batch, n_out], as beam_select says."""
+        if tuple(logits.shape) != (self.batch * self.beams, self.vocab) or tuple(scores.shape) != (self.batch, self.beams):
+            raise ValueError("logits must be [batch * beams, vocab] and scores [batch, beams]")
+        out = [_made_for(stream, self._ws.device, lambda t=t: torch.empty((self.batch, self.n_out), dtype=t, device=self._ws.device))
+               for t in (torch.float32, torch.int32, torch.int32)]
+        beam_select(logits, scores, *out, self._ws, ended, self.end_token, stream)
+        return tuple(out)

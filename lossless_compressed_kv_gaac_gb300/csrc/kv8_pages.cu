@@ -1,4 +1,4 @@
-// Pages of the 8-bit cache: reserve, release, fork, compact.
+// Pages of the 8-bit cache: reserve, release, fork, reorder, compact.
 //
 // refs[p] counts the sequences that hold page p; a page with none is free.  There is no free list to keep: the
 // lowest free pages are found by counting refs, so every result is a function of the tables alone (no order of
@@ -307,6 +307,81 @@ __global__ void __launch_bounds__(kFkThreads) kv8_fork_kernel(Kv8Dev c, const in
   if (tid == 0 && part == 0) c.lens[d] = len;
 }
 
+// ------------------------------------------------------------------ reorder
+// Sequence g * beams + i becomes what g * beams + parents[g][i] was.  A thread takes one place (a column of the table,
+// 16 bytes of an open row) of all the beams of a group: it has read every beam's old value before it writes the first
+// new one, so the exchange needs no second copy of anything.  BEAMS: the beams at most.
+
+constexpr int kRoThreads = 128;
+
+template <int BEAMS>
+__global__ void __launch_bounds__(kRoThreads) kv8_reorder_kernel(Kv8Dev c, const int32_t* parents, int beams, unsigned parts,
+                                                                 int32_t* status) {
+  __shared__ int parent[BEAMS], len[BEAMS];  // len: what a sequence becomes; -1 where it stays as it is
+  dependent_wait();
+  dependent_launch();
+  const int tid = threadIdx.x;
+  const int64_t group = blockIdx.x / parts, first = group * beams;
+  const unsigned part = blockIdx.x % parts;
+  if (tid < beams) {
+    const int p = parents[first + tid];
+    const bool in = p >= 0 && p < beams;
+    const int n = in ? c.lens[first + p] : 0;
+    const bool fits = n >= 0 && n <= static_cast<int64_t>(c.max_blocks) * kBlock;
+    if (part == 0 && (!in || !fits)) report(status, in ? GAAC_EFORMAT : GAAC_EINVAL);
+    parent[tid] = in ? p : tid;
+    len[tid] = in && fits && p != tid ? n : -1;
+  }
+  __syncthreads();
+  int most = 0;  // open rows
+  for (int i = 0; i < beams; ++i) most = max(most, len[i] % kBlock);
+  const unsigned at = part * kRoThreads + tid, step = parts * kRoThreads;
+  // ---- tables and counts: a sequence gives up its old row and holds its parent's full blocks
+  for (int64_t col = at; col < c.max_blocks; col += step) {
+    int32_t was[BEAMS], now[BEAMS];
+#pragma unroll
+    for (int i = 0; i < BEAMS; ++i)
+      if (i < beams) was[i] = c.table[(first + i) * c.max_blocks + col];
+#pragma unroll
+    for (int i = 0; i < BEAMS; ++i)
+      if (i < beams) now[i] = len[i] < 0 ? was[i] : col < len[i] / kBlock ? c.table[(first + parent[i]) * c.max_blocks + col] : -1;
+#pragma unroll
+    for (int i = 0; i < BEAMS; ++i)
+      if (i < beams && len[i] >= 0) {
+        const bool held = now[i] >= 0 && now[i] < c.n_pages;
+        if (!held && col < len[i] / kBlock) report(status, GAAC_EFORMAT);
+        if (now[i] != was[i]) {
+          if (was[i] >= 0 && was[i] < c.n_pages) atomicSub(c.refs + was[i], 1);
+          if (held) atomicAdd(c.refs + now[i], 1);
+          c.table[(first + i) * c.max_blocks + col] = now[i];
+        }
+      }
+  }
+  // ---- open rows of every (kv-head, K|V): 16 vectors of 16 bytes each
+  constexpr int kRow = kD / 8;
+  uint4* const tail = reinterpret_cast<uint4*>(c.tail);
+  const int64_t seq = static_cast<int64_t>(c.heads) * 2 * kBlock * kRow;
+  const unsigned per = most * kRow, all = per * 2 * c.heads;
+  for (unsigned k = at; k < all; k += step) {
+    const unsigned in = k % per;
+    uint4* const t = tail + first * seq + k / per * (kBlock * kRow) + in;
+    const int row = in / kRow;
+    uint4 x[BEAMS];
+#pragma unroll
+    for (int i = 0; i < BEAMS; ++i)
+      if (i < beams && row < len[i] % kBlock) x[i] = t[parent[i] * seq];
+#pragma unroll
+    for (int i = 0; i < BEAMS; ++i)
+      if (i < beams && row < len[i] % kBlock) t[i * seq] = x[i];
+  }
+  // ---- the lengths change once every CTA of the group has read them
+  if (tid == 0 && kv8_atomic_add_acq_rel(c.work + first, 1u) == parts - 1) {
+    c.work[first] = 0;
+    for (int i = 0; i < beams; ++i)
+      if (len[i] >= 0) c.lens[first + i] = len[i];
+  }
+}
+
 // ------------------------------------------------------------------ compact
 // With n held pages, the held pages at n and above move into the holes below n: the lowest hole takes the highest
 // page, and so on.  Source and target never overlap.
@@ -480,6 +555,24 @@ extern "C" int gaac_kv8_fork(const gaac_kv8* cache, const int32_t* src, const in
     return GAAC_EINVAL;
   return kv8_launch_cluster(kv8_fork_kernel, dim3(kFkCtas * n), kFkThreads, 0, kFkCtas, stream, kv8_dev(cache), src, dst, n,
                             d_status);
+}
+
+extern "C" int gaac_kv8_reorder(const gaac_kv8* cache, const int32_t* parents, int beams, int32_t* d_status, void* stream) {
+  if (!kv8_ok(cache) || parents == nullptr || (reinterpret_cast<uintptr_t>(parents) & 3u) || beams < 1 || beams > GAAC_MAX_BEAMS ||
+      cache->batch % beams != 0)
+    return GAAC_EINVAL;
+  if (beams == 1) return GAAC_OK;  // nothing has another parent
+  // CTAs of a group: as many as its open rows and table columns fill, up to eight for each SM in all.
+  const int groups = cache->batch / beams;
+  const int64_t places = std::max<int64_t>(cache->max_blocks, int64_t{2} * cache->n_kv_heads * (kBlock - 1) * (kD / 8));
+  const unsigned parts = static_cast<unsigned>(
+      std::min<int64_t>((places + kRoThreads - 1) / kRoThreads, std::max<int64_t>(1, (152 * 8 + groups - 1) / groups)));
+  const dim3 grid(parts * groups);
+  const Kv8Dev c = kv8_dev(cache);
+  if (beams <= 4) return kv8_launch(kv8_reorder_kernel<4>, grid, kRoThreads, 0, stream, c, parents, beams, parts, d_status);
+  if (beams <= 8) return kv8_launch(kv8_reorder_kernel<8>, grid, kRoThreads, 0, stream, c, parents, beams, parts, d_status);
+  if (beams <= 16) return kv8_launch(kv8_reorder_kernel<16>, grid, kRoThreads, 0, stream, c, parents, beams, parts, d_status);
+  return kv8_launch(kv8_reorder_kernel<32>, grid, kRoThreads, 0, stream, c, parents, beams, parts, d_status);
 }
 
 extern "C" int gaac_kv8_compact(const gaac_kv8* cache, int32_t* moved_to, void* stream) {

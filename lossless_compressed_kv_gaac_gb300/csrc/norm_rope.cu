@@ -1,0 +1,510 @@
+// Norms of queries and keys for each head with the rotation by their positions in the same pass, and the gradient.
+//
+// A head x of n channels, weights w:
+//   r = 1 / sqrt(mean x^2 + eps),  y = x r w,  the first rot_dim channels of y turned as in rope.cu.
+// Backward, with dz the gradient of the result:
+//   g = dz turned back,  h = g w,  dx = r (h - x r mean(h x r)),  dw = sum over tokens and heads of g x r.
+//
+// Memory bound: the forward pass reads and writes every element once, the backward pass reads x and dz and writes dx;
+// r is computed again rather than kept, since x has to be read for dx anyway.  A group of 2 to 32 lanes owns the heads of
+// a row that it walks over; a lane has two vectors of V elements of each (a unit: V pairs of the rotated part, or of the
+// channels behind it), so that the mean takes a few shuffles and V sines serve all heads of the walk.  V is 16 bytes
+// where widths and alignment allow, else one element with four units a lane.
+// Sums are fp32.  dw: every lane adds up its channels over its rows, a CTA its lanes in order, a second launch the
+// CTAs in order, so the result is the same each time.
+#include <algorithm>
+#include <cmath>
+
+#include "kv8.cuh"
+#include "rope.cuh"
+
+namespace gaac {
+
+constexpr int kNrThreads = 64;
+constexpr int kNrBatch = 2;        // heads whose loads a lane has in flight
+constexpr int kNrMost = 5;         // most heads of a lane's walk
+constexpr int kNrMaxDim = 256;
+constexpr int kNgThreads = 128;    // gradient
+constexpr int kNgCtasPerSm = 3;
+constexpr int kNgMostCtas = 152 * kNgCtasPerSm;
+
+struct NormTensor {
+  const char* x;
+  const char* dz;  // gradient only
+  char* out;
+  const void* w;   // nullptr: ones
+  float* dw;       // gradient only; may be nullptr
+  int64_t x_seq, x_tok, x_head, dz_seq, dz_tok, dz_head, out_seq, out_tok, out_head;  // bytes
+};
+
+struct NormArgs {
+  NormTensor t[2];
+  int heads0, heads;  // heads of the first tensor; of both
+  unsigned n_seq, n_tok;
+  int rot, dim, w_f32;
+  const void* pos;
+  int pos64;
+  int64_t pos_seq, pos_tok;
+  const uint64_t* turns;
+  float mscale, eps;
+  int rot_units, units, lanes;  // of a head; lanes of a group
+  int walkers;                  // groups that share the heads of a row
+  unsigned row_walkers;         // rows * walkers
+  float* part;                  // gradient: [CTA][2][dim]
+};
+
+// A lane's units of a head: element offsets of the two vectors of unit k, and whether they exist.
+template <int V, int UPL, bool INTER>
+struct NormUnits {
+  int e0[UPL], e1[UPL];
+  bool turned[UPL], one[UPL], two[UPL];
+  __device__ __forceinline__ NormUnits(const NormArgs& a, int lane) {
+#pragma unroll
+    for (int k = 0; k < UPL; ++k) {
+      const int u = lane + k * a.lanes;
+      turned[k] = u < a.rot_units;
+      e0[k] = turned[k] ? (INTER ? 2 * u * V : u * V) : a.rot + 2 * (u - a.rot_units) * V;
+      e1[k] = turned[k] && !INTER ? e0[k] + a.rot / 2 : e0[k] + V;
+      one[k] = u < a.units;
+      two[k] = one[k] && e1[k] < a.dim;
+    }
+  }
+};
+
+template <typename T, int V, int UPL, bool INTER>
+struct NormLane {
+  using Vec = RopeVec<T, V>;
+  using Units = NormUnits<V, UPL, INTER>;
+
+  static __device__ __forceinline__ void load(Vec (&v)[UPL][2], const char* x, const Units& n) {
+#pragma unroll
+    for (int k = 0; k < UPL; ++k) {
+      v[k][0] = v[k][1] = Vec{};
+      if (n.one[k]) v[k][0] = *reinterpret_cast<const Vec*>(x + n.e0[k] * static_cast<int64_t>(sizeof(T)));
+      if (n.two[k]) v[k][1] = *reinterpret_cast<const Vec*>(x + n.e1[k] * static_cast<int64_t>(sizeof(T)));
+    }
+  }
+  static __device__ __forceinline__ void store(char* out, const Units& n, int k, const float* f) {
+    Vec y;
+    if (n.one[k]) {
+      rope_pack<T, V>(y, f);
+      *reinterpret_cast<Vec*>(out + n.e0[k] * static_cast<int64_t>(sizeof(T))) = y;
+    }
+    if (n.two[k]) {
+      rope_pack<T, V>(y, f + V);
+      *reinterpret_cast<Vec*>(out + n.e1[k] * static_cast<int64_t>(sizeof(T))) = y;
+    }
+  }
+  static __device__ __forceinline__ void weights(float (&w)[UPL][2 * V], const NormArgs& a, const void* p, const Units& n) {
+#pragma unroll
+    for (int k = 0; k < UPL; ++k)
+#pragma unroll
+      for (int i = 0; i < 2 * V; ++i) {
+        const int e = i < V ? n.e0[k] + i : n.e1[k] + i - V;
+        w[k][i] = 1.f;
+        if (p != nullptr && (i < V ? n.one[k] : n.two[k])) {
+          if (a.w_f32)
+            w[k][i] = static_cast<const float*>(p)[e];
+          else if constexpr (sizeof(T) == 2)
+            w[k][i] = RopePair<T>::get(static_cast<const T*>(p)[e]);
+        }
+      }
+  }
+  static __device__ __forceinline__ void sines(float (&s)[UPL][V], float (&c)[UPL][V], const NormArgs& a, const Units& n, int lane,
+                                               int64_t pos_at) {
+    const uint64_t p = rope_position(a.pos, a.pos64, pos_at);
+#pragma unroll
+    for (int k = 0; k < UPL; ++k)
+      if (n.turned[k]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) rope_sincos<T>(p * a.turns[(lane + k * a.lanes) * V + i], a.mscale, s[k][i], c[k][i]);
+      }
+  }
+};
+
+// The sum of x over the group's lanes.
+__device__ __forceinline__ float group_sum(float x, int lanes, uint32_t mask) {
+  for (int d = lanes >> 1; d > 0; d >>= 1) x += __shfl_xor_sync(mask, x, d);
+  return x;
+}
+__device__ __forceinline__ uint32_t group_mask(int lanes) {
+  const uint32_t low = lanes == 32 ? 0xFFFFFFFFu : (1u << lanes) - 1u;
+  return low << (threadIdx.x & 31 & ~(lanes - 1));
+}
+
+// Group (row, walker): heads walker, walker + walkers, ... of one row.
+template <typename T, int V, int UPL, bool INTER>
+__global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NormArgs a) {
+  dependent_wait();
+  dependent_launch();
+  using L = NormLane<T, V, UPL, INTER>;
+  const int lane = threadIdx.x & (a.lanes - 1);
+  const uint32_t mask = group_mask(a.lanes);
+  const unsigned rw = blockIdx.x * (kNrThreads / a.lanes) + threadIdx.x / a.lanes;
+  if (rw >= a.row_walkers) return;
+  const unsigned row = rw / a.walkers;
+  const int walker = static_cast<int>(rw - row * a.walkers);
+  unsigned seq = 0, tok = row;
+  if (a.n_seq > 1) {
+    seq = row / a.n_tok;
+    tok = row - seq * a.n_tok;
+  }
+  const NormUnits<V, UPL, INTER> n(a, lane);
+  const char* const xq = a.t[0].x + seq * a.t[0].x_seq + tok * a.t[0].x_tok;
+  const char* const xk = a.t[1].x + seq * a.t[1].x_seq + tok * a.t[1].x_tok;
+  char* const outq = a.t[0].out + seq * a.t[0].out_seq + tok * a.t[0].out_tok;
+  char* const outk = a.t[1].out + seq * a.t[1].out_seq + tok * a.t[1].out_tok;
+  RopeVec<T, V> v[kNrBatch][UPL][2];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int j = 0; j < kNrBatch; ++j) {
+      const int h = h0 + j * a.walkers;
+      if (h < a.heads) L::load(v[j], h >= a.heads0 ? xk + (h - a.heads0) * a.t[1].x_head : xq + h * a.t[0].x_head, n);
+    }
+  };
+  load(walker);
+  float s[UPL][V], c[UPL][V], w[UPL][2 * V];
+  L::sines(s, c, a, n, lane, seq * a.pos_seq + tok * a.pos_tok);
+  int of = -1;  // the tensor whose weights w holds
+  const float mean = 1.f / a.dim;
+  for (int h0 = walker;;) {
+#pragma unroll
+    for (int j = 0; j < kNrBatch; ++j) {
+      const int h = h0 + j * a.walkers;
+      if (h >= a.heads) break;
+      const int second = h >= a.heads0;
+      if (second != of) {
+        L::weights(w, a, a.t[second].w, n);
+        of = second;
+      }
+      char* out = second ? outk + (h - a.heads0) * a.t[1].out_head : outq + h * a.t[0].out_head;
+      float e[UPL][2 * V], sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < UPL; ++k) {
+        rope_unpack<T, V>(v[j][k][0], e[k]);
+        rope_unpack<T, V>(v[j][k][1], e[k] + V);
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) sum += e[k][i] * e[k][i];
+      }
+      const float r = rsqrtf(group_sum(sum, a.lanes, mask) * mean + a.eps);
+#pragma unroll
+      for (int k = 0; k < UPL; ++k) {
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) e[k][i] *= r * w[k][i];
+        if (n.turned[k]) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : V + i;
+            const float x0 = e[k][ia], x1 = e[k][ib];
+            e[k][ia] = x0 * c[k][i] - x1 * s[k][i];
+            e[k][ib] = x1 * c[k][i] + x0 * s[k][i];
+          }
+        }
+        L::store(out, n, k, e[k]);
+      }
+    }
+    h0 += kNrBatch * a.walkers;
+    if (h0 >= a.heads) break;
+    load(h0);
+  }
+}
+
+// One tensor's heads first, first + step, ... below n_heads of a row: writes dx, adds to dw.
+template <typename T, int V, int UPL, bool INTER>
+__device__ __forceinline__ void norm_gradient_heads(const NormArgs& a, const NormTensor& t, unsigned seq, unsigned tok, int first,
+                                                    int n_heads, const NormUnits<V, UPL, INTER>& n, uint32_t mask,
+                                                    const float (&s)[UPL][V], const float (&c)[UPL][V],
+                                                    const float (&w)[UPL][2 * V], float (&dw)[UPL][2 * V]) {
+  using L = NormLane<T, V, UPL, INTER>;
+  const char* const x = t.x + seq * t.x_seq + tok * t.x_tok;
+  const char* const dz = t.dz + seq * t.dz_seq + tok * t.dz_tok;
+  char* const out = t.out + seq * t.out_seq + tok * t.out_tok;
+  const float mean = 1.f / a.dim;
+#pragma unroll 1
+  for (int h0 = first; h0 < n_heads; h0 += kNrBatch * a.walkers) {
+    RopeVec<T, V> vx[kNrBatch][UPL][2], vg[kNrBatch][UPL][2];
+#pragma unroll
+    for (int j = 0; j < kNrBatch; ++j) {
+      const int h = h0 + j * a.walkers;
+      if (h < n_heads) {
+        L::load(vx[j], x + h * t.x_head, n);
+        L::load(vg[j], dz + h * t.dz_head, n);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kNrBatch; ++j) {
+      const int h = h0 + j * a.walkers;
+      if (h >= n_heads) break;
+      float e[UPL][2 * V], g[UPL][2 * V], xx = 0.f, hx = 0.f;
+#pragma unroll
+      for (int k = 0; k < UPL; ++k) {
+        rope_unpack<T, V>(vx[j][k][0], e[k]);
+        rope_unpack<T, V>(vx[j][k][1], e[k] + V);
+        rope_unpack<T, V>(vg[j][k][0], g[k]);
+        rope_unpack<T, V>(vg[j][k][1], g[k] + V);
+        if (n.turned[k]) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : V + i;
+            const float g0 = g[k][ia], g1 = g[k][ib];
+            g[k][ia] = g0 * c[k][i] + g1 * s[k][i];
+            g[k][ib] = g1 * c[k][i] - g0 * s[k][i];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) {
+          xx += e[k][i] * e[k][i];
+          hx += g[k][i] * w[k][i] * e[k][i];
+        }
+      }
+      xx = group_sum(xx, a.lanes, mask);
+      hx = group_sum(hx, a.lanes, mask);
+      const float r = rsqrtf(xx * mean + a.eps), m = hx * mean * r;  // m: the mean of h x r
+#pragma unroll
+      for (int k = 0; k < UPL; ++k) {
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) {
+          const float y = e[k][i] * r;
+          dw[k][i] += g[k][i] * y;
+          e[k][i] = r * (g[k][i] * w[k][i] - y * m);
+        }
+        L::store(out + h * t.out_head, n, k, e[k]);
+      }
+    }
+  }
+}
+
+// Groups take (row, walker) in turn over the whole grid.
+template <typename T, int V, int UPL, bool INTER>
+__global__ void __launch_bounds__(kNgThreads, kNgCtasPerSm) qk_norm_rope_gradient_kernel(const NormArgs a) {
+  __shared__ float sums[kNgThreads * UPL * 2 * V];  // [group][dim], one tensor at a time
+  dependent_wait();
+  dependent_launch();
+  using L = NormLane<T, V, UPL, INTER>;
+  const int lane = threadIdx.x & (a.lanes - 1), groups = kNgThreads / a.lanes, group = threadIdx.x / a.lanes;
+  const uint32_t mask = group_mask(a.lanes);
+  const NormUnits<V, UPL, INTER> n(a, lane);
+  float w[2][UPL][2 * V], dw[2][UPL][2 * V];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    L::weights(w[t], a, a.t[t].w, n);
+#pragma unroll
+    for (int k = 0; k < UPL; ++k)
+#pragma unroll
+      for (int i = 0; i < 2 * V; ++i) dw[t][k][i] = 0.f;
+  }
+#pragma unroll 1
+  for (int64_t rw = static_cast<int64_t>(blockIdx.x) * groups + group; rw < a.row_walkers; rw += static_cast<int64_t>(gridDim.x) * groups) {
+    const unsigned row = static_cast<unsigned>(rw) / a.walkers;
+    const int walker = static_cast<int>(static_cast<unsigned>(rw) - row * a.walkers);
+    unsigned seq = 0, tok = row;
+    if (a.n_seq > 1) {
+      seq = row / a.n_tok;
+      tok = row - seq * a.n_tok;
+    }
+    float s[UPL][V], c[UPL][V];
+    L::sines(s, c, a, n, lane, seq * a.pos_seq + tok * a.pos_tok);
+    norm_gradient_heads<T, V, UPL, INTER>(a, a.t[0], seq, tok, walker, a.heads0, n, mask, s, c, w[0], dw[0]);
+    // the walk goes on where the first tensor's heads end
+    const int left = (walker - a.heads0) % a.walkers, first = left < 0 ? left + a.walkers : left;
+    norm_gradient_heads<T, V, UPL, INTER>(a, a.t[1], seq, tok, first, a.heads - a.heads0, n, mask, s, c, w[1], dw[1]);
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    __syncthreads();  // the other tensor's sums are read
+#pragma unroll
+    for (int k = 0; k < UPL; ++k)
+#pragma unroll
+      for (int i = 0; i < 2 * V; ++i)
+        if (i < V ? n.one[k] : n.two[k]) sums[group * a.dim + (i < V ? n.e0[k] + i : n.e1[k] + i - V)] = dw[t][k][i];
+    __syncthreads();
+    for (int ch = threadIdx.x; ch < a.dim; ch += kNgThreads) {
+      float sum = 0.f;
+      for (int i = 0; i < groups; ++i) sum += sums[i * a.dim + ch];
+      a.part[(static_cast<int64_t>(blockIdx.x) * 2 + t) * a.dim + ch] = sum;
+    }
+  }
+}
+
+// dw of 32 channels: 32 threads each, in 32 runs of CTAs that are joined in order.
+__global__ void __launch_bounds__(1024) norm_weights_kernel(const float* part, int ctas, int dim, float* dw0, float* dw1) {
+  __shared__ float sums[32][33];
+  dependent_wait();
+  dependent_launch();
+  const int ch = threadIdx.x & 31, run = threadIdx.x >> 5;
+  const int at = blockIdx.x * 32 + ch;  // of [2][dim]
+  const int per = (ctas + 31) / 32;
+  float sum = 0.f;
+  if (at < 2 * dim) {
+#pragma unroll 8
+    for (int i = run * per; i < min(ctas, (run + 1) * per); ++i) sum += __ldcg(part + static_cast<int64_t>(i) * 2 * dim + at);
+  }
+  sums[run][ch] = sum;
+  __syncthreads();
+  if (run == 0 && at < 2 * dim) {
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum += sums[i][ch];
+    float* dw = at < dim ? dw0 : dw1;
+    if (dw != nullptr) dw[at < dim ? at : at - dim] = sum;
+  }
+}
+
+template <typename T, int V, int UPL>
+static int norm_launch(const NormArgs& a, bool inter, int grid, void* stream) {
+  if (grid > 0)
+    return inter ? kv8_launch(qk_norm_rope_gradient_kernel<T, V, UPL, true>, dim3(grid), kNgThreads, 0, stream, a)
+                 : kv8_launch(qk_norm_rope_gradient_kernel<T, V, UPL, false>, dim3(grid), kNgThreads, 0, stream, a);
+  const unsigned per = kNrThreads / a.lanes;
+  const dim3 all((a.row_walkers + per - 1) / per);
+  return inter ? kv8_launch(qk_norm_rope_kernel<T, V, UPL, true>, all, kNrThreads, 0, stream, a)
+               : kv8_launch(qk_norm_rope_kernel<T, V, UPL, false>, all, kNrThreads, 0, stream, a);
+}
+
+struct Span {  // the elements of one tensor, in bytes
+  uintptr_t begin, end;
+};
+
+// The arguments of either call.  grid: 0 for the forward pass, else where the gradient's CTAs go.
+static int norm_rope(const gaac_norm_tensor* tensors, int n_tensors, int dtype, int weight_dtype, int64_t n_seq, int64_t n_tok,
+                     int head_dim, int rot_dim, const void* positions, int pos_bits, int64_t pos_seq_stride,
+                     int64_t pos_tok_stride, const uint64_t* turns, float mscale, float eps, unsigned flags, bool gradient,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  if (tensors == nullptr || n_tensors < 1 || n_tensors > 2 || (dtype != GAAC_BF16 && dtype != GAAC_F16 && dtype != GAAC_F32) ||
+      (weight_dtype != dtype && weight_dtype != GAAC_F32) || (pos_bits != 32 && pos_bits != 64) ||
+      (flags & ~static_cast<unsigned>(GAAC_ROPE_INTERLEAVED)) || !std::isfinite(mscale) || !std::isfinite(eps) || eps < 0.f)
+    return GAAC_EINVAL;
+  if (n_seq < 0 || n_tok < 0 || n_seq > 0x7FFFFFFF || n_tok > 0x7FFFFFFF || head_dim < 2 || head_dim > kNrMaxDim || (head_dim & 1) ||
+      rot_dim < 2 || rot_dim > head_dim || (rot_dim & 1))
+    return GAAC_EINVAL;
+  const int64_t rows = n_seq * n_tok;
+  if (rows > 0x7FFFFFFF) return GAAC_EINVAL;
+  int64_t heads = 0;
+  for (int i = 0; i < n_tensors; ++i) {
+    const gaac_norm_tensor& t = tensors[i];
+    if (t.n_heads < 1 || t.n_heads > 65536 || (reinterpret_cast<uintptr_t>(t.weight) & (weight_dtype == GAAC_F32 ? 3u : 1u)) ||
+        (gradient && (reinterpret_cast<uintptr_t>(t.dweight) & 3u)))
+      return GAAC_EINVAL;
+    heads += t.n_heads;
+  }
+  if (gradient && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 15u) ||
+                   workspace_bytes < gaac_qk_norm_rope_workspace(head_dim)))
+    return GAAC_EINVAL;
+  if (gradient && n_tensors == 2 && tensors[0].dweight != nullptr && tensors[0].dweight == tensors[1].dweight) return GAAC_EINVAL;
+  if (rows == 0 && !gradient) return GAAC_OK;
+  if (rows > 0 && (positions == nullptr || turns == nullptr || pos_seq_stride < 0 || pos_tok_stride < 0 ||
+                   (reinterpret_cast<uintptr_t>(positions) & (pos_bits / 8 - 1)) || (reinterpret_cast<uintptr_t>(turns) & 7u)))
+    return GAAC_EINVAL;
+  const int size = dtype == GAAC_F32 ? 4 : 2, full = 16 / size;
+  bool wide = (rot_dim / 2) % full == 0 && (head_dim - rot_dim) % full == 0;
+  NormArgs a = {};
+  for (int i = 0; i < n_tensors && rows > 0; ++i) {
+    const gaac_norm_tensor& t = tensors[i];
+    if (t.x == nullptr || t.out == nullptr || (gradient && t.dz == nullptr)) return GAAC_EINVAL;
+    const int64_t most = int64_t{1} << 56;
+    const int64_t strides[9] = {t.x_seq, t.x_tok, t.x_head, t.out_seq, t.out_tok, t.out_head, t.dz_seq, t.dz_tok, t.dz_head};
+    const int64_t counts[3] = {n_seq, n_tok, t.n_heads};
+    int64_t all = 0;
+    for (int k = 0; k < (gradient ? 9 : 6); ++k) {
+      if (strides[k] < 0 || strides[k] > most / counts[k % 3]) return GAAC_EINVAL;
+      if (counts[k % 3] > 1) all |= strides[k];
+    }
+    int64_t count[3] = {n_seq, n_tok, t.n_heads}, so[3] = {t.out_seq, t.out_tok, t.out_head};
+    if (!distinct(head_dim, count, so)) return GAAC_EINVAL;
+    auto span = [&](const void* p, const int64_t* s) {
+      const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+      return Span{b, b + ((n_seq - 1) * s[0] + (n_tok - 1) * s[1] + (t.n_heads - 1) * s[2] + head_dim) * size};
+    };
+    const Span x = span(t.x, strides), o = span(t.out, strides + 3), z = gradient ? span(t.dz, strides + 6) : x;
+    const uintptr_t addresses = x.begin | o.begin | z.begin;
+    if (addresses & (size - 1)) return GAAC_EINVAL;
+    // In place means the same elements, of x or of dz; any other overlap would read what has been written.
+    auto clash = [&](const Span& in, const int64_t* s) {
+      bool same = in.begin == o.begin;
+      for (int k = 0; k < 3; ++k) same = same && (counts[k] == 1 || s[k] == strides[3 + k]);
+      return !same && in.begin < o.end && o.begin < in.end;
+    };
+    if (clash(x, strides) || (gradient && clash(z, strides + 6))) return GAAC_EINVAL;
+    wide = wide && all % full == 0 && (addresses & 15u) == 0;
+    a.t[i] = NormTensor{static_cast<const char*>(t.x), static_cast<const char*>(t.dz), static_cast<char*>(t.out), t.weight, t.dweight,
+                        t.x_seq * size, t.x_tok * size, t.x_head * size, t.dz_seq * size, t.dz_tok * size, t.dz_head * size,
+                        t.out_seq * size, t.out_tok * size, t.out_head * size};
+  }
+  if (rows == 0)
+    for (int i = 0; i < n_tensors; ++i) a.t[i].dw = tensors[i].dweight;
+  // Two tensors with a first element in common, one of them an output (the caller keeps other overlaps apart).
+  if (n_tensors == 2 && rows > 0) {
+    const void* o[2] = {tensors[0].out, tensors[1].out};
+    for (int i = 0; i < 2; ++i)
+      if (o[i] == o[1 - i] || o[i] == tensors[1 - i].x || (gradient && o[i] == tensors[1 - i].dz)) return GAAC_EINVAL;
+  }
+  const int v = wide ? full : 1;
+  a.heads0 = tensors[0].n_heads;
+  a.heads = static_cast<int>(heads);
+  a.n_seq = static_cast<unsigned>(n_seq);
+  a.n_tok = static_cast<unsigned>(n_tok);
+  a.rot = rot_dim;
+  a.dim = head_dim;
+  a.w_f32 = weight_dtype == GAAC_F32;
+  a.pos = positions;
+  a.pos64 = pos_bits == 64;
+  a.pos_seq = pos_seq_stride;
+  a.pos_tok = pos_tok_stride;
+  a.turns = turns;
+  a.mscale = mscale;
+  a.eps = eps;
+  a.rot_units = rot_dim / 2 / v;
+  a.units = a.rot_units + ((head_dim - rot_dim) / v + 1) / 2;
+  a.lanes = 2;
+  while (a.lanes < 32 && a.lanes < a.units) a.lanes *= 2;
+  // Heads of a walk: as rope's, as many as leave twice the lanes that 152 SMs hold at a time, so that sines are shared
+  // where there is work for all, and single heads where latency counts.
+  const int64_t want = int64_t{152} * 2048, per_row = std::max<int64_t>(rows, 1) * a.lanes;
+  const int64_t walkers = std::max<int64_t>(gradient ? 1 : (heads + kNrMost - 1) / kNrMost, (want + per_row - 1) / per_row);
+  a.walkers = static_cast<int>(std::min<int64_t>(heads, walkers));
+  if (rows * a.walkers > 0x7FFFFFFF) return GAAC_EINVAL;
+  a.row_walkers = static_cast<unsigned>(rows * a.walkers);
+  a.part = static_cast<float*>(workspace);
+  int grid = 0;
+  if (gradient) {
+    const int64_t per = kNgThreads / a.lanes;
+    grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kNgMostCtas, (a.row_walkers + per - 1) / per)));
+  }
+  const bool inter = (flags & GAAC_ROPE_INTERLEAVED) != 0;
+  int e;
+  if (dtype == GAAC_BF16)
+    e = wide ? norm_launch<__nv_bfloat16, 8, 1>(a, inter, grid, stream) : norm_launch<__nv_bfloat16, 1, 4>(a, inter, grid, stream);
+  else if (dtype == GAAC_F16)
+    e = wide ? norm_launch<__half, 8, 1>(a, inter, grid, stream) : norm_launch<__half, 1, 4>(a, inter, grid, stream);
+  else
+    e = wide ? norm_launch<float, 4, 1>(a, inter, grid, stream) : norm_launch<float, 1, 4>(a, inter, grid, stream);
+  if (e != GAAC_OK || !gradient) return e;
+  return kv8_launch(norm_weights_kernel, dim3((2 * head_dim + 31) / 32), 1024, 0, stream, static_cast<const float*>(a.part), grid, head_dim,
+                    a.t[0].dw, a.t[1].dw);
+}
+
+}  // namespace gaac
+
+using namespace gaac;
+
+extern "C" size_t gaac_qk_norm_rope_workspace(int head_dim) {
+  if (head_dim < 2 || head_dim > kNrMaxDim) return 0;
+  return (static_cast<size_t>(kNgMostCtas) * 2 * head_dim * sizeof(float) + 15) & ~static_cast<size_t>(15);
+}
+
+extern "C" int gaac_qk_norm_rope(const gaac_norm_tensor* tensors, int n_tensors, int dtype, int weight_dtype, int64_t n_seq,
+                                 int64_t n_tok, int head_dim, int rot_dim, const void* positions, int pos_bits,
+                                 int64_t pos_seq_stride, int64_t pos_tok_stride, const uint64_t* turns, float mscale, float eps,
+                                 unsigned flags, void* stream) {
+  return norm_rope(tensors, n_tensors, dtype, weight_dtype, n_seq, n_tok, head_dim, rot_dim, positions, pos_bits, pos_seq_stride,
+                   pos_tok_stride, turns, mscale, eps, flags, false, nullptr, 0, stream);
+}
+
+extern "C" int gaac_qk_norm_rope_gradient(const gaac_norm_tensor* tensors, int n_tensors, int dtype, int weight_dtype,
+                                          int64_t n_seq, int64_t n_tok, int head_dim, int rot_dim, const void* positions,
+                                          int pos_bits, int64_t pos_seq_stride, int64_t pos_tok_stride, const uint64_t* turns,
+                                          float mscale, float eps, unsigned flags, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
+  return norm_rope(tensors, n_tensors, dtype, weight_dtype, n_seq, n_tok, head_dim, rot_dim, positions, pos_bits, pos_seq_stride,
+                   pos_tok_stride, turns, mscale, eps, flags, true, workspace, workspace_bytes, stream);
+}
