@@ -546,6 +546,36 @@ GAAC_API int gaac_qk_norm_rope_gradient(const gaac_norm_tensor* tensors, int n_t
                                         float mscale, float eps, unsigned flags, void* workspace, size_t workspace_bytes,
                                         void* stream);
 
+/* Tensors of gaac_prompt_attention: element (row, head, c) of q at q + row*q_tok + head*q_head + c and so on, 16-byte
+ * aligned, strides in elements, multiples of 8, at least 128 (a dimension of size 1 has any).  out's elements are
+ * distinct and no input's.  lse: fp32 [n_tokens][n_q_heads] or NULL. */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;
+  int64_t q_tok, q_head;
+  int64_t k_tok, k_head;
+  int64_t v_tok, v_head;
+  int64_t out_tok, out_head;
+} gaac_prompt;
+
+/*
+ * Causal attention within packed sequences: rows [cu_tokens[b], cu_tokens[b+1]) of q [n_tokens][n_q_heads][128] and k, v
+ * [n_tokens][n_kv_heads][128] are the tokens of sequence b (int32 [batch+1] on the device, not decreasing, within
+ * [0, n_tokens]; else GAAC_EINVAL and nothing is computed):
+ *   out[i][hq] = sum_{j <= i} softmax_j(scale * q[i][hq] . k[j][hk]) v[j][hk],  hk = hq / (n_q_heads / n_kv_heads),
+ * which is an integer <= GAAC_MAX_GQA; lse[i][hq] = ln sum_{j <= i} exp(scale * q[i][hq] . k[j][hk]).  dtype, of all four:
+ * GAAC_BF16 or GAAC_F16.  scale: any finite number.  Rows of no sequence are not written.  n_tokens < 2^31 - 2^16, batch
+ * <= 65535.  Logits and sums are fp32; weights are rounded to dtype (f16: those below 2^-17 of the row's largest lose
+ * bits, below 2^-25 they may be 0).  What tokens behind i and other sequences hold has no influence on row i, nor whether it
+ * is finite.  An infinite V makes its channel infinite (NaN where both signs meet, or where its weight is rounded to
+ * 0).  A row whose logits are all -infinity is 0, its lse -infinity.
+ */
+GAAC_API int gaac_prompt_attention(const gaac_prompt* tensors, int dtype, int64_t n_tokens, int n_q_heads, int n_kv_heads,
+                                   const int32_t* cu_tokens, int batch, float scale, int32_t* d_status, void* stream);
+
 /* One layer's 8-bit paged cache, in caller-owned device memory.
  *  pages     [n_pages][n_kv_heads][2 (K, V)][64][128] FP8 numbers (fmt: GAAC_FP8_E4M3 or
  *            GAAC_FP8_E5M2), 16-byte aligned; a value is its FP8 number times its scale

@@ -122,6 +122,8 @@ def lib() -> ctypes.CDLL:
             L.gaac_rope.argtypes = [P, i32, i32, i64, i64, i32, i32, P, i32, i64, i64, P, ctypes.c_float,
                                     ctypes.c_uint, P]
             L.gaac_rope.restype = i32
+            L.gaac_prompt_attention.argtypes = [P, i32, i64, i32, i32, P, i32, ctypes.c_float, P, P]
+            L.gaac_prompt_attention.restype = i32
             L.gaac_qk_norm_rope_workspace.argtypes = [i32]
             L.gaac_qk_norm_rope_workspace.restype = sz
             L.gaac_qk_norm_rope.argtypes = [P, i32, i32, i32, i64, i64, i32, i32, P, i32, i64, i64, P, ctypes.c_float,
@@ -462,6 +464,29 @@ def decode_attention_hd256(q, seq_lens, table, pools: Pools, base3, base4, scale
         workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream)))
 
 
+def _stream_object(stream, device) -> torch.cuda.Stream | None:
+    """The torch stream of a call's `stream` argument: a stream, a raw handle or None, which stays None."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle in (0, 1, 2):  # the default stream, or a thread's, which keeps its order with that
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(handle, device=device)
+
+
+def _made_for(stream, device, make) -> torch.Tensor:
+    """make()'s tensor for a call on `stream` (None: the current one).  It is made on that stream, so its memory is not
+    what the current stream's pending work still uses, and not given out again before the current stream, where it
+    may be read, is past its use."""
+    if stream is None:
+        return make()
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(_stream_object(stream, device)):
+        t = make()
+    t.record_stream(current)
+    return t
+
+
 # ---------------------------------------------------------------- rotary positions
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # GAAC_BF16, GAAC_F16, GAAC_F32
 ROPE_INTERLEAVED, ROPE_INVERSE = 1, 2
@@ -740,6 +765,53 @@ def qk_norm_rope_gradient(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Te
         raise ValueError("workspace must be contiguous on q's device")
     _norm_rope("gaac_qk_norm_rope_gradient", q, k, dq, dk, dq_out, dk_out, q_weight, k_weight, dq_weight, dk_weight,
                positions, turns, interleaved, mscale, eps, stream, workspace.data_ptr(), workspace.nbytes)
+
+
+# ---------------------------------------------------------------- attention of prompts
+class gaac_prompt(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "out", "lse")] + \
+        [(n, ctypes.c_int64) for n in ("q_tok", "q_head", "k_tok", "k_head", "v_tok", "v_head", "out_tok", "out_head")]
+
+
+_PROMPT = struct.Struct("@5P8q")  # gaac_prompt packed in one go
+assert _PROMPT.size == ctypes.sizeof(gaac_prompt)
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, scale: float,
+                     out: torch.Tensor | None = None, lse: torch.Tensor | None = None, status=None,
+                     stream=None) -> torch.Tensor:
+    """Causal attention of whole prompts, packed: rows cu_tokens[b] .. cu_tokens[b + 1] (int32 [batch + 1]) are the tokens
+    of sequence b, and a token attends to itself and those before it in its sequence.  q: [n, q_heads, 128]; k, v:
+    [n, kv_heads, 128], at most 8 query heads to a kv-head; BF16 or FP16, channels contiguous, other strides free
+    (multiples of 8 elements, 16-byte aligned: slices of one projection will do).  out: of q's shape and type (made,
+    contiguous, if not given; rows of no sequence are not written); lse: fp32 [n, q_heads], contiguous, receives the
+    logarithm of each row's sum of exponentials.  Offsets that are not valid are reported in status (int32)."""
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        raise ValueError("autograd does not see prompt_attention: call it under torch.no_grad()")
+    dtype, index = q.dtype, q.get_device()
+    if dtype not in (torch.bfloat16, torch.float16) or index < 0:
+        raise ValueError("q must be BF16 or FP16 on a CUDA device")
+    n, hq = q.shape[:2] if q.dim() == 3 else (-1, -1)
+    hkv = k.shape[1] if k.dim() == 3 else -1
+    if out is None:
+        out = _made_for(stream, q.device, lambda: torch.empty(q.shape, dtype=dtype, device=q.device))
+    for t, shape, name in ((q, (n, hq, HEAD_DIM), "q"), (k, (n, hkv, HEAD_DIM), "k"), (v, (n, hkv, HEAD_DIM), "v"),
+                           (out, (n, hq, HEAD_DIM), "out")):
+        if t.shape != shape or t.dtype != dtype or t.get_device() != index or t.stride(2) != 1:
+            raise ValueError(f"{name} must be [tokens, heads, {HEAD_DIM}] of q's type and device, channels contiguous")
+    if cu_tokens.dtype != torch.int32 or cu_tokens.dim() != 1 or cu_tokens.shape[0] < 1 or not cu_tokens.is_contiguous() or \
+            cu_tokens.get_device() != index:
+        raise ValueError("cu_tokens must be a contiguous int32 tensor [batch + 1] on q's device")
+    if lse is not None and (lse.shape != (n, hq) or lse.dtype != torch.float32 or not lse.is_contiguous() or
+                            lse.get_device() != index):
+        raise ValueError("lse must be contiguous fp32 [tokens, q_heads] on q's device")
+    if status is not None and (status.get_device() != index or status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status must be an int32 tensor on q's device")
+    desc = _PROMPT.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse) or 0, *q.stride()[:2],
+                        *k.stride()[:2], *v.stride()[:2], *out.stride()[:2])
+    _call("gaac_prompt_attention", index, stream, desc, _DTYPES[dtype], n, hq, hkv, cu_tokens.data_ptr(),
+          cu_tokens.shape[0] - 1, scale, _ptr(status))
+    return out
 
 
 # ---------------------------------------------------------------- 8-bit paged cache

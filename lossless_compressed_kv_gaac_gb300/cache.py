@@ -7,33 +7,11 @@ from __future__ import annotations
 
 import torch
 
-from . import (BLOCK, FP8_E4M3, HEAD_DIM, Kv8, Pools, append, attention_workspace, beam_select, beam_workspace, calibrate,
+from . import (BLOCK, FP8_E4M3, HEAD_DIM, Kv8, Pools, _made_for, _stream_object, append, attention_workspace,
+               beam_select, beam_workspace, calibrate,
                decode_attention, decode_attention_bf16, decompress, encode_blocks, entry_fields, kv8_append,
                kv8_attention_workspace, kv8_compact, kv8_decode_attention, kv8_fork, kv8_release, kv8_reorder,
                kv8_reserve, new_stats, new_table)
-
-
-def _stream_object(stream, device) -> torch.cuda.Stream | None:
-    """The torch stream of a call's `stream` argument: a stream, a raw handle or None, which stays None."""
-    if stream is None or isinstance(stream, torch.cuda.Stream):
-        return stream
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if handle in (0, 1, 2):  # the default stream, or a thread's, which keeps its order with that
-        return torch.cuda.default_stream(device)
-    return torch.cuda.ExternalStream(handle, device=device)
-
-
-def _made_for(stream, device, make) -> torch.Tensor:
-    """make()'s tensor for a call on `stream` (None: the current one).  It is made on that stream, so its memory is not
-    what the current stream's pending work still uses, and not given out again before the current stream, where it
-    may be read, is past its use."""
-    if stream is None:
-        return make()
-    current = torch.cuda.current_stream(device)
-    with torch.cuda.stream(_stream_object(stream, device)):
-        t = make()
-    t.record_stream(current)
-    return t
 
 
 class LayerCache:

@@ -31,11 +31,10 @@
 //  * The open block is multiplied in its own type, the weights in two parts as well.
 // Measured: 32 sequences of 4,096-32,768 tokens, 8 kv-heads, 1.2 GB: 176 us, 6.9 TB/s; one of 65,536 tokens: 25.0 us,
 // of which 3 us go by before the first data and 4 us from the last to the joined result; one of 777 tokens: 8.0 us.
-#include <cuda.h>
-
 #include <algorithm>
 
 #include "kv8.cuh"
+#include "tma.cuh"
 
 namespace gaac {
 
@@ -1131,28 +1130,12 @@ static int ka_sms() {
 // Counters: one for each pair (at its first CTA) and two for the teams that begin at a CTA.
 static size_t ka_counter_bytes(int grid) { return (static_cast<size_t>(3 * grid) * 4 + 15) & ~static_cast<size_t>(15); }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiled ka_encode() {
-  static EncodeTiled fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiled>(p);
-  }();
-  return fn;
-}
-
 // A map of [rows][128 bytes-wide column blocks]: boxes of box_x elements by box_y rows, 128-byte swizzle.
 static bool ka_map(CUtensorMap* m, CUtensorMapDataType type, int elem, void* base, int64_t rows, unsigned box_x, unsigned box_y) {
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(rows)};
   const cuuint64_t stride[1] = {static_cast<cuuint64_t>(kD * elem)};
   const cuuint32_t box[2] = {box_x, box_y}, one[2] = {1, 1};
-  return ka_encode()(m, type, 2, base, dims, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return tma_encode()(m, type, 2, base, dims, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1194,7 +1177,7 @@ extern "C" int gaac_kv8_decode_attention(const gaac_kv8* cache, const void* q, i
   if (static_cast<int64_t>(cache->batch) * cache->n_kv_heads > 0x7FFFFFFF / (static_cast<int64_t>(cache->max_blocks) + 1))
     return GAAC_EINVAL;
   const int sms = ka_sms();
-  if (sms <= 0 || ka_encode() == nullptr) return GAAC_ECUDA;
+  if (sms <= 0 || tma_encode() == nullptr) return GAAC_ECUDA;
   if (workspace_bytes < gaac_kv8_attention_workspace()) return GAAC_EINVAL;
   const int grid = sms;
   KaArgs a;

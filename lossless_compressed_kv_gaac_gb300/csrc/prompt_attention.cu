@@ -1,0 +1,572 @@
+// Attention of whole prompts: causal, grouped heads, packed sequences of different lengths.
+//
+//   out_i = sum_{j <= i} softmax_j(scale q_i . k_j) v_j   within a sequence, query head hq reading kv-head hq / G.
+//
+// Tensor bound where prompts are long: 4 * 128 operations for each pair (i, j <= i) and query head.  A CTA takes 2 x
+// floor(128 / G) consecutive tokens of one sequence with all G query heads of one kv-head, as two tiles of up to 128
+// rows (row r of a tile: token r / G, head r % G), so that a tile's rows share their keys, its diagonal is short
+// and few tokens still fill a tile.  Warps:
+//  * one issues the copies (TMA): both tiles' queries, then K and V of 128 tokens in turn into a ring of five slots;
+//  * one thread issues tcgen05.mma: S = Q K^T (128 x 128, both operands in shared memory), O += P V (P in TMEM, V's
+//    rows as they lie, token-major).  While one tile's S is in its softmax, the tensor cores work for the other.
+//  * four warps for each tile: a thread owns a row.  S comes from TMEM into its registers; P goes back, rounded to the
+//    inputs' type, over the S it came from.  All of TMEM's 512 columns are used: S and O of both tiles.
+// Softmax: weights are 2^(c s - c m), c = |scale| log2 e, with a reference m that follows the running maximum only where
+// that has grown by more than 2^8: then O and the sum are scaled.  Until then weights are at most 2^8, which costs
+// nothing in either type (rounding is relative; f16 goes to 2^16, and loses weights below 2^-25, of the reference
+// or of 2^-8 of the maximum).  Sums are fp32 over the unrounded weights; a weight's rounding, 2^-9 in bf16 and 2^-12 in
+// f16, is that of the result's type.
+// Where a mask leaves keys out, V has to be finite there, or 0 * V would be NaN: two warps look such blocks of V over
+// before they are multiplied and put zeros in the place of what is not finite.  What of that rows may see is added
+// to them at the end, from memory.
+#include <algorithm>
+#include <cmath>
+
+#include "kv8.cuh"
+#include "tma.cuh"
+
+namespace gaac {
+
+constexpr int kPaRows = 128;                  // rows of a tile
+constexpr int kPaKeys = 128;                  // keys of a block
+constexpr int kPaTile = 128 * kD * 2;         // bytes of a tile of Q, K or V
+constexpr int kPaHalf = kPaTile / 2;          // 64 channels of it: rows of 128 bytes, swizzled
+constexpr int kPaSlots = 5;
+constexpr int kPaSoftmax = 256;
+constexpr int kPaThreads = kPaSoftmax + 128;   // + the multiplier, the copier and two that look V over
+constexpr int kPaCleaners = 64;
+constexpr int kPaLook = 3;                    // blocks of a unit that have masked keys, at most
+constexpr uint32_t kPaFull = 0xFFFFFFFFu;
+constexpr uint32_t kPaColS = 0, kPaColO = 256;  // TMEM columns: S of tile t at 128 t, P over it, O at 256 + 128 t
+
+struct PaArgs {
+  const int32_t* cu;
+  int batch, hkv, g, per;      // per: tokens of a tile
+  unsigned places;
+  int64_t n_tokens;
+  float c;                     // |scale| log2 e
+  int negate;                  // scale < 0: the logits' sign turns
+  const char* v;
+  int64_t v_tok, v_head;       // bytes
+  char* out;
+  int64_t out_tok, out_head;   // bytes
+  float* lse;                  // [n_tokens][hkv * g], or nullptr
+  int32_t* status;
+};
+
+struct PaSmem {
+  alignas(1024) uint8_t q[2][kPaTile];
+  alignas(1024) uint8_t kv[kPaSlots][kPaTile];
+  uint64_t q_full[2], kv_full[kPaSlots], kv_empty[kPaSlots], s_full[2], p_full[2], o_full[2], due[kPaLook], clean[kPaLook], done;
+  uint32_t tmem;
+  int odd;  // a V that some row may see is not finite in a block with masked keys
+};
+
+// ------------------------------------------------------------------ tcgen05
+
+__device__ __forceinline__ void t5_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a),
+      "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void t5_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a),
+      "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+// `bar` is arrived at once all that this thread has issued so far is done.
+__device__ __forceinline__ void t5_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void t5_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void t5_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void t5_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define GAAC_R8(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]), "+r"(x[i + 4]), "+r"(x[i + 5]), "+r"(x[i + 6]), "+r"(x[i + 7])
+#define GAAC_W8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
+#define GAAC_I8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+
+// 32 columns of this warp's 32 lanes, one lane a thread.  The registers hold them after t5_wait_ld.
+__device__ __forceinline__ void t5_ld32(uint32_t* x, uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+      "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : GAAC_W8(x, 0), GAAC_W8(x, 8), GAAC_W8(x, 16), GAAC_W8(x, 24)
+      : "r"(at)
+      : "memory");
+}
+// Nothing may use the registers before the wait: it passes them through.
+__device__ __forceinline__ void t5_wait_ld(uint32_t* x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : GAAC_R8(x, 0), GAAC_R8(x, 8), GAAC_R8(x, 16), GAAC_R8(x, 24)::"memory");
+}
+__device__ __forceinline__ void t5_st32(uint32_t at, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      GAAC_I8(x, 0), GAAC_I8(x, 8), GAAC_I8(x, 16), GAAC_I8(x, 24)
+      : "memory");
+}
+__device__ __forceinline__ void t5_st16(uint32_t at, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      GAAC_I8(x, 0), GAAC_I8(x, 8)
+      : "memory");
+}
+
+// Shared-memory operand, 128-byte swizzle.  Rows of 64 channels, channels along the contraction (Q, K): groups of eight
+// rows 1,024 bytes apart.  Contraction over the rows (V): the same, and the next 64 channels kPaHalf further.
+__device__ __forceinline__ uint64_t pa_desc(uint32_t addr, uint32_t leading) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(leading >> 4) << 16 | static_cast<uint64_t>(1024 >> 4) << 32 |
+         1ull << 46 | 2ull << 61;
+}
+// 128 x 128 with fp32 sums; v: B is V, whose rows run along the contraction.
+__device__ __forceinline__ uint32_t pa_idesc(bool bf16, bool v) {
+  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (v ? 1u << 16 : 0u) | (128u >> 3) << 17 | (128u >> 4) << 24;
+}
+
+__device__ __forceinline__ void pa_tma(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ float pa_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <bool HALF>
+__device__ __forceinline__ uint32_t pa_pack(float lo, float hi) {
+  uint32_t r;
+  if (HALF)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ------------------------------------------------------------------ units
+
+// What a CTA works on: tokens t0 .. t0 + 2 per - 1 of a sequence that begins at row `first` and has len tokens.
+struct PaUnit {
+  int first, len, t0, h;
+  int blocks[2];  // of keys, for each tile; 0: no tokens
+  int look;       // the first block with keys that some row does not see; less than kPaLook from the last
+};
+
+// With T = 2 per tokens a unit, sequence b owns places [cu[b] / T + b, cu[b + 1] / T + b + 1): as many as it can need.
+// By a whole warp.  false: nothing to do here.
+__device__ __forceinline__ bool pa_unit(const PaArgs& a, PaUnit& u) {
+  const int lane = threadIdx.x & 31;
+  const unsigned head = blockIdx.x / a.places;
+  const int64_t place = a.places - 1 - (blockIdx.x - head * a.places);  // long rows of keys first
+  const int64_t unit = 2 * a.per;
+  int count = 0, bad = 0;
+#pragma unroll 4
+  for (int i0 = 0; i0 < a.batch; i0 += 32) {
+    const int i = i0 + lane;
+    bool below = false;
+    if (i < a.batch) {
+      const int64_t lo = a.cu[i], hi = a.cu[i + 1];
+      if (lo < 0 || hi < lo || hi > a.n_tokens) bad = 1;
+      below = hi / unit + i + 1 <= place;
+    }
+    count += __popc(__ballot_sync(kPaFull, below));
+  }
+  if (__any_sync(kPaFull, bad)) {
+    if (blockIdx.x == 0 && lane == 0) report(a.status, GAAC_EINVAL);
+    return false;
+  }
+  if (count >= a.batch) return false;
+  const int64_t lo = a.cu[count], hi = a.cu[count + 1], p0 = lo / unit + count;
+  const int64_t t0 = (place - p0) * unit;
+  if (place < p0 || t0 >= hi - lo) return false;
+  u.first = static_cast<int>(lo);
+  u.len = static_cast<int>(hi - lo);
+  u.t0 = static_cast<int>(t0);
+  u.h = static_cast<int>(head);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int from = u.t0 + t * a.per;
+    u.blocks[t] = from < u.len ? (min(u.len, from + a.per) + kPaKeys - 1) / kPaKeys : 0;
+  }
+  u.look = u.t0 / kPaKeys;
+  return true;
+}
+
+// The copy that brings K (kind 0) or V of block i is number 2 i + kind.
+__device__ __forceinline__ int pa_slot(int n) { return n % kPaSlots; }
+__device__ __forceinline__ uint32_t pa_phase(int n) { return (n / kPaSlots) & 1; }
+
+__device__ __forceinline__ void pa_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+__device__ void pa_load(const PaArgs& a, PaSmem& sm, const PaUnit& u, const CUtensorMap* mq, const CUtensorMap* mk, const CUtensorMap* mv) {
+  const int blocks = max(u.blocks[0], u.blocks[1]);
+  const uint32_t q_bytes = static_cast<uint32_t>(a.g) * a.per * kD * 2;
+  auto q = [&](int t) {
+    if (u.blocks[t] == 0) return;
+    mbar_arrive_expect_tx(&sm.q_full[t], q_bytes);
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+      pa_tma(sm.q[t] + half * kPaHalf, mq, half * (kD / 2), u.h * a.g, u.first + u.t0 + t * a.per, &sm.q_full[t]);
+  };
+  q(0);
+  int n = 0;
+  bool ok = true;
+  for (; n < 2 * blocks && ok; ++n) {
+    const int slot = pa_slot(n);
+    if (n >= kPaSlots) ok = mbar_wait(&sm.kv_empty[slot], pa_phase(n) ^ 1u, a.status);
+    if (!ok) break;
+    mbar_arrive_expect_tx(&sm.kv_full[slot], kPaTile);
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+      pa_tma(sm.kv[slot] + half * kPaHalf, n & 1 ? mv : mk, half * (kD / 2), u.h, u.first + (n >> 1) * kPaKeys, &sm.kv_full[slot]);
+    if (n == 0) q(1);
+    // the slot's barrier is now in the phase of this copy, whoever waits for it without having seen those before
+    if ((n & 1) && (n >> 1) >= u.look) pa_arrive(&sm.due[(n >> 1) - u.look]);
+  }
+  // no copy may be in flight when the CTA ends, not even where a wait ran out
+  for (int i = max(0, n - kPaSlots); i < n; ++i) mbar_wait(&sm.kv_full[pa_slot(i)], pa_phase(i), a.status);
+  for (int t = 0; t < 2; ++t)
+    if (u.blocks[t]) mbar_wait(&sm.q_full[t], 0, a.status);
+}
+
+template <bool HALF>
+__device__ void pa_mma(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_t tmem) {
+  const uint32_t id_qk = pa_idesc(!HALF, false), id_pv = pa_idesc(!HALF, true);
+  const int blocks = max(u.blocks[0], u.blocks[1]);
+  bool ok = true;
+  auto qk = [&](int t, int i) {
+    const uint32_t q = smem_addr(sm.q[t]), k = smem_addr(sm.kv[pa_slot(2 * i)]);
+#pragma unroll
+    for (int j = 0; j < kD / 16; ++j) {
+      const uint32_t at = (j / 4) * kPaHalf + (j % 4) * 32;
+      t5_mma_ss(tmem + kPaColS + 128 * t, pa_desc(q + at, 16), pa_desc(k + at, 16), id_qk, j > 0);
+    }
+    t5_commit(&sm.s_full[t]);
+  };
+  auto pv = [&](int t, int i) {
+    const uint32_t v = smem_addr(sm.kv[pa_slot(2 * i + 1)]);
+#pragma unroll
+    for (int j = 0; j < kPaKeys / 16; ++j)
+      t5_mma_ts(tmem + kPaColO + 128 * t, tmem + kPaColS + 128 * t + 8 * j, pa_desc(v + j * 2048, kPaHalf), id_pv, i > 0 || j > 0);
+    t5_commit(&sm.o_full[t]);
+  };
+  auto arrived = [&](int n) { return mbar_wait(&sm.kv_full[pa_slot(n)], pa_phase(n), a.status); };
+  ok = arrived(0);
+  for (int t = 0; t < 2 && ok; ++t)
+    if (u.blocks[t]) {
+      ok = mbar_wait(&sm.q_full[t], 0, a.status);
+      if (ok) qk(t, 0);
+    }
+  // a slot is handed back where there is a copy that waits for it
+  if (ok && kPaSlots < 2 * blocks) t5_commit(&sm.kv_empty[0]);
+  for (int i = 0; i < blocks && ok; ++i) {
+    ok = arrived(2 * i + 1);
+    if (ok && i + 1 < blocks) ok = arrived(2 * i + 2);
+    if (ok && i >= u.look) ok = mbar_wait(&sm.clean[i - u.look], 0, a.status);
+    for (int t = 0; t < 2 && ok; ++t) {
+      if (i >= u.blocks[t]) continue;
+      ok = mbar_wait(&sm.p_full[t], i & 1, a.status);
+      if (!ok) break;
+      t5_after();
+      pv(t, i);
+      if (i + 1 < u.blocks[t]) qk(t, i + 1);
+    }
+    for (int n = 2 * i + 1; n <= 2 * i + 2 && ok; ++n)
+      if (n + kPaSlots < 2 * blocks) t5_commit(&sm.kv_empty[pa_slot(n)]);
+  }
+  // nothing may be under way when TMEM is given back
+  t5_commit(&sm.done);
+  mbar_wait(&sm.done, 0, a.status);
+}
+
+// Two warps: infinities and NaN become 0 in the blocks of V with masked keys.
+template <bool HALF>
+__device__ void pa_look(const PaArgs& a, PaSmem& sm, const PaUnit& u) {
+  constexpr uint32_t kCarry = HALF ? 0x04000400u : 0x00800080u;  // takes an exponent of ones into the sign's place
+  const int tid = threadIdx.x % kPaCleaners, blocks = max(u.blocks[0], u.blocks[1]);
+  for (int i = u.look; i < blocks; ++i) {
+    const int n = 2 * i + 1;
+    if (!__all_sync(kPaFull, mbar_wait(&sm.due[i - u.look], 0, a.status) && mbar_wait(&sm.kv_full[pa_slot(n)], pa_phase(n), a.status)))
+      return;
+    uint4* const v = reinterpret_cast<uint4*>(sm.kv[pa_slot(n)]) + tid;
+#pragma unroll 8
+    for (int k = 0; k < kPaTile / 16; k += kPaCleaners) {
+      const uint4 w = v[k];
+      const uint32_t any = ((w.x & 0x7FFF7FFFu) + kCarry) | ((w.y & 0x7FFF7FFFu) + kCarry) | ((w.z & 0x7FFF7FFFu) + kCarry) |
+                           ((w.w & 0x7FFF7FFFu) + kCarry);
+      if (any & 0x80008000u) {
+        auto fix = [](uint32_t x) {
+          const uint32_t y = ((x & 0x7FFF7FFFu) + kCarry) & 0x80008000u;  // the sign's place of what is not finite
+          return x & ~((y >> 15) * 0xFFFFu);
+        };
+        v[k] = make_uint4(fix(w.x), fix(w.y), fix(w.z), fix(w.w));
+        if (i * kPaKeys + (k + tid) % (kPaHalf / 16) / 8 < u.len) sm.odd = 1;  // eight vectors of a token in each half
+      }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) pa_arrive(&sm.clean[i - u.look]);
+  }
+}
+
+template <bool HALF>
+__device__ void pa_softmax(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_t tmem, int t) {
+  const int row = threadIdx.x % kPaRows, blocks = u.blocks[t];
+  const int from = u.t0 + t * a.per, in_tile = row / a.g, token = from + in_tile;
+  const bool real = in_tile < a.per && token < u.len;
+  const uint32_t lane_at = tmem + (static_cast<uint32_t>(row & ~31) << 16);  // this warp's lanes
+  const uint32_t at_s = lane_at + kPaColS + 128 * t, at_o = lane_at + kPaColO + 128 * t;
+  float m = -INFINITY, l = 0.f;  // the reference, times c; the sum
+  bool ok = true;
+  for (int i = 0; i < blocks && ok; ++i) {
+    ok = __all_sync(kPaFull, mbar_wait(&sm.s_full[t], i & 1, a.status));
+    if (!ok) break;
+    t5_after();
+    uint32_t s[128];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t5_ld32(s + 32 * k, at_s + 32 * k);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t5_wait_ld(s + 32 * k);
+    if (a.negate) {
+#pragma unroll
+      for (int k = 0; k < 128; ++k) s[k] ^= 0x80000000u;
+    }
+    const bool masked = i * kPaKeys + kPaKeys - 1 > from;  // for some row
+    if (masked) {
+      const int last = token - i * kPaKeys;  // the last key that this row sees
+#pragma unroll
+      for (int k = 0; k < 128; ++k)
+        if (k > last) s[k] = 0xFF800000u;
+    }
+    float x[4] = {__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]), __uint_as_float(s[3])};
+#pragma unroll
+    for (int k = 4; k < 128; ++k) x[k % 4] = fmaxf(x[k % 4], __uint_as_float(s[k]));
+    const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * a.c;
+    // ---- a new reference where the old one is too far below
+    const bool up = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
+    if (__any_sync(kPaFull, up)) {
+      const float to = up ? top : m, f = up ? pa_exp2(m - to) : 1.f;
+      l *= f;
+      m = to;
+      if (i > 0) {
+        ok = __all_sync(kPaFull, mbar_wait(&sm.o_full[t], (i - 1) & 1, a.status));
+        if (!ok) break;
+        t5_after();
+#pragma unroll 1
+        for (int k = 0; k < 128; k += 32) {
+          uint32_t o[32];
+          t5_ld32(o, at_o + k);
+          t5_wait_ld(o);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+          t5_st32(at_o + k, o);
+        }
+      }
+    }
+    const float base = m == -INFINITY ? 0.f : m;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t p[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float p0 = pa_exp2(fmaf(__uint_as_float(s[32 * k + 2 * j]), a.c, -base));
+        const float p1 = pa_exp2(fmaf(__uint_as_float(s[32 * k + 2 * j + 1]), a.c, -base));
+        sum[2 * (j & 1)] += p0;
+        sum[2 * (j & 1) + 1] += p1;
+        p[j] = pa_pack<HALF>(p0, p1);
+      }
+      t5_st16(at_s + 16 * k, p);
+    }
+    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    t5_wait_st();
+    t5_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) pa_arrive(&sm.p_full[t]);
+  }
+  if (blocks == 0 || !ok) return;
+  if (!__all_sync(kPaFull, mbar_wait(&sm.o_full[t], (blocks - 1) & 1, a.status))) return;
+  t5_after();
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t token_at = static_cast<int64_t>(u.first) + token;
+  const int head = u.h * a.g + row % a.g;
+  char* const out = a.out + token_at * a.out_tok + head * a.out_head;
+#pragma unroll 1
+  for (int k = 0; k < 128; k += 32) {
+    uint32_t o[32];
+    t5_ld32(o, at_o + k);
+    t5_wait_ld(o);
+    if (!real) continue;
+    float y[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) y[j] = l == 0.f ? 0.f : __uint_as_float(o[j]) * inv;
+    if (*reinterpret_cast<volatile int*>(&sm.odd)) {  // V that is not finite, of the blocks that were looked over
+      for (int key = u.look * kPaKeys; key <= token; ++key) {
+        const uint16_t* v = reinterpret_cast<const uint16_t*>(a.v + (static_cast<int64_t>(u.first) + key) * a.v_tok + u.h * a.v_head) + k;
+#pragma unroll 1
+        for (int j = 0; j < 32; ++j) {
+          const float w = kv8_pair<HALF>(v[j]).x;
+          if (!isfinite(w)) {
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              if (q == j) y[q] += w;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint4*>(out + (k + 8 * j) * 2) =
+          make_uint4(pa_pack<HALF>(y[8 * j], y[8 * j + 1]), pa_pack<HALF>(y[8 * j + 2], y[8 * j + 3]),
+                     pa_pack<HALF>(y[8 * j + 4], y[8 * j + 5]), pa_pack<HALF>(y[8 * j + 6], y[8 * j + 7]));
+  }
+  if (real && a.lse != nullptr) a.lse[token_at * (static_cast<int64_t>(a.hkv) * a.g) + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147181f;
+}
+
+template <bool HALF>
+__global__ void __launch_bounds__(kPaThreads, 1)
+    prompt_attention_kernel(const PaArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                            const __grid_constant__ CUtensorMap mv) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  PaSmem& sm = *reinterpret_cast<PaSmem*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+  const int warp = threadIdx.x / 32;
+  dependent_wait();
+  dependent_launch();
+  PaUnit u;
+  if (!pa_unit(a, u)) return;  // the same for all warps
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sm.q_full[t], 1);
+      mbar_init(&sm.s_full[t], 1);
+      mbar_init(&sm.p_full[t], 4);
+      mbar_init(&sm.o_full[t], 1);
+    }
+    sm.odd = 0;
+    mbar_init(&sm.done, 1);
+    for (int i = 0; i < kPaLook; ++i) {
+      mbar_init(&sm.due[i], 1);
+      mbar_init(&sm.clean[i], kPaCleaners / 32);
+    }
+    for (int i = 0; i < kPaSlots; ++i) {
+      mbar_init(&sm.kv_full[i], 1);
+      mbar_init(&sm.kv_empty[i], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  t5_before();
+  __syncthreads();
+  t5_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sm.tmem);
+  if (warp >= 10) {
+    pa_look<HALF>(a, sm, u);
+  } else if (warp == 9) {
+    if ((threadIdx.x & 31) == 0) pa_load(a, sm, u, &mq, &mk, &mv);
+  } else if (warp == 8) {
+    if ((threadIdx.x & 31) == 0) pa_mma<HALF>(a, sm, u, tmem);
+  } else {
+    pa_softmax<HALF>(a, sm, u, tmem, warp / 4);
+  }
+  __syncwarp();
+  t5_before();
+  __syncthreads();
+  if (warp == 8) {
+    t5_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+// [tokens][heads][128] of a 16-bit type: boxes of 64 channels, `heads_box` heads and `tokens_box` tokens.
+static bool pa_map(CUtensorMap* m, const void* base, int64_t tokens, int64_t heads, int64_t tok, int64_t head, unsigned heads_box,
+                   unsigned tokens_box) {
+  const cuuint64_t dims[3] = {kD, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? head * 2 : kD * 2), static_cast<cuuint64_t>(tokens > 1 ? tok * 2 : kD * 2)};
+  const cuuint32_t box[3] = {kD / 2, heads_box, tokens_box}, one[3] = {1, 1, 1};
+  return tma_encode()(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool HALF>
+static int pa_launch(const PaArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, unsigned grid, void* stream) {
+  constexpr size_t smem = sizeof(PaSmem) + 1024;  // room to align the tiles
+  static bool done[64] = {false};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GAAC_ECUDA;
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(prompt_attention_kernel<HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+      return GAAC_ECUDA;
+    done[dev] = true;
+  }
+  return kv8_launch(prompt_attention_kernel<HALF>, dim3(grid), kPaThreads, smem, stream, a, q, k, v);
+}
+
+}  // namespace gaac
+
+using namespace gaac;
+
+extern "C" int gaac_prompt_attention(const gaac_prompt* p, int dtype, int64_t n_tokens, int n_q_heads, int n_kv_heads,
+                                     const int32_t* cu_tokens, int batch, float scale, int32_t* d_status, void* stream) {
+  if (p == nullptr || (dtype != GAAC_BF16 && dtype != GAAC_F16) || n_tokens < 0 || n_tokens > 0x7FFFFFFF - 65536 || batch < 0 ||
+      batch > 65535 || !std::isfinite(scale) || n_kv_heads < 1 || n_kv_heads > 1024 || n_q_heads < 1 || n_q_heads % n_kv_heads != 0 ||
+      n_q_heads / n_kv_heads > GAAC_MAX_GQA)
+    return GAAC_EINVAL;
+  if (n_tokens == 0 || batch == 0) return GAAC_OK;
+  const uintptr_t all = reinterpret_cast<uintptr_t>(p->q) | reinterpret_cast<uintptr_t>(p->k) | reinterpret_cast<uintptr_t>(p->v) |
+                        reinterpret_cast<uintptr_t>(p->out);
+  if (p->q == nullptr || p->k == nullptr || p->v == nullptr || p->out == nullptr || cu_tokens == nullptr || (all & 15u) ||
+      ((reinterpret_cast<uintptr_t>(cu_tokens) | reinterpret_cast<uintptr_t>(p->lse)) & 3u))
+    return GAAC_EINVAL;
+  const int64_t heads[4] = {n_q_heads, n_kv_heads, n_kv_heads, n_q_heads};
+  const int64_t tok[4] = {p->q_tok, p->k_tok, p->v_tok, p->out_tok}, head[4] = {p->q_head, p->k_head, p->v_head, p->out_head};
+  const void* base[4] = {p->q, p->k, p->v, p->out};
+  for (int i = 0; i < 4; ++i) {
+    const int64_t st = n_tokens > 1 ? tok[i] : kD, sh = heads[i] > 1 ? head[i] : kD;
+    if (st < kD || sh < kD || ((st | sh) & 7) || st > (int64_t{1} << 38) || sh > (int64_t{1} << 38)) return GAAC_EINVAL;
+  }
+  // Heads of one token and tokens of one head of the result are apart, and the result is not an input.
+  if (n_tokens > 1 && n_q_heads > 1 && tok[3] < static_cast<int64_t>(n_q_heads - 1) * head[3] + kD && head[3] < (n_tokens - 1) * tok[3] + kD)
+    return GAAC_EINVAL;
+  for (int i = 0; i < 3; ++i)
+    if (base[i] == base[3]) return GAAC_EINVAL;
+  if (tma_encode() == nullptr) return GAAC_ECUDA;
+  PaArgs a;
+  a.cu = cu_tokens;
+  a.batch = batch;
+  a.hkv = n_kv_heads;
+  a.g = n_q_heads / n_kv_heads;
+  a.per = kPaRows / a.g;
+  const int64_t places = n_tokens / (2 * a.per) + batch;
+  if (places * n_kv_heads > 0x7FFFFFFF) return GAAC_EINVAL;
+  a.places = static_cast<unsigned>(places);
+  a.n_tokens = n_tokens;
+  // Not 0, which would make NaN of the masked logits: with the smallest number above it no finite logit moves a weight.
+  a.c = scale == 0.f ? 0x1p-149f : static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634);
+  a.negate = scale < 0.f;
+  a.v = static_cast<const char*>(p->v);
+  a.v_tok = p->v_tok * 2;
+  a.v_head = p->v_head * 2;
+  a.out = static_cast<char*>(p->out);
+  a.out_tok = p->out_tok * 2;
+  a.out_head = p->out_head * 2;
+  a.lse = p->lse;
+  a.status = d_status;
+  CUtensorMap q, k, v;
+  if (!pa_map(&q, p->q, n_tokens, n_q_heads, p->q_tok, p->q_head, a.g, a.per) ||
+      !pa_map(&k, p->k, n_tokens, n_kv_heads, p->k_tok, p->k_head, 1, kPaKeys) ||
+      !pa_map(&v, p->v, n_tokens, n_kv_heads, p->v_tok, p->v_head, 1, kPaKeys))
+    return GAAC_ECUDA;
+  const unsigned grid = static_cast<unsigned>(places * n_kv_heads);
+  return dtype == GAAC_F16 ? pa_launch<true>(a, q, k, v, grid, stream) : pa_launch<false>(a, q, k, v, grid, stream);
+}

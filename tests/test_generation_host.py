@@ -112,3 +112,37 @@ def test_python_refusals():
 
 def test_struct_matches_the_header():
     assert ctypes.sizeof(G.gaac_norm_tensor) == 5 * 8 + 8 + 9 * 8
+
+
+def prompt_call(lib, **kw):  # noqa: F811
+    d = dict(q=GOOD, k=MORE, v=2 * MORE, out=3 * MORE, lse=None, q_tok=1024, q_head=128, k_tok=256, k_head=128, v_tok=256, v_head=128,
+             out_tok=1024, out_head=128)
+    a = dict(dtype=0, n=100, hq=8, hkv=2, cu=GOOD, batch=3, scale=0.1)
+    d.update({k: v for k, v in kw.items() if k in d})
+    a.update({k: v for k, v in kw.items() if k in a})
+    p = G.gaac_prompt(*(d[n] for n, _ in G.gaac_prompt._fields_))
+    return lib.gaac_prompt_attention(ctypes.byref(p), *a.values(), None, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=2), dict(dtype=-1), dict(n=-1), dict(n=2 ** 31 - 100), dict(hq=0), dict(hq=7), dict(hq=18), dict(hkv=0), dict(hq=1025, hkv=1025),
+    dict(cu=None), dict(cu=GOOD + 2), dict(batch=-1), dict(batch=65536), dict(scale=math.nan), dict(scale=math.inf), dict(q=None), dict(k=None),
+    dict(v=None), dict(out=None), dict(q=GOOD + 8), dict(k=ODD), dict(v=ODD), dict(out=ODD), dict(lse=GOOD + 2), dict(q_tok=127), dict(k_tok=0),
+    dict(v_head=64), dict(q_tok=1028), dict(k_head=132), dict(out_tok=1 << 39), dict(out=GOOD), dict(out=MORE), dict(out_tok=512),
+    dict(out_head=1024, out_tok=1024)], ids=str)
+def test_prompt_refusals(lib, bad):  # noqa: F811
+    assert prompt_call(lib, **bad) == EINVAL
+
+
+def test_prompt_nothing_to_do(lib):  # noqa: F811
+    assert lib.gaac_prompt_attention(None, 0, 4, 2, 1, GOOD, 1, 0.1, None, None) == EINVAL
+    assert prompt_call(lib, n=0) == OK and prompt_call(lib, batch=0) == OK
+
+
+def test_prompt_refuses_on_the_host():
+    z = torch.zeros
+    cu = z(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        G.prompt_attention(z(4, 2, 128).bfloat16(), z(4, 1, 128).bfloat16(), z(4, 1, 128).bfloat16(), cu, 0.1)
+    with pytest.raises(ValueError, match="autograd"):
+        G.prompt_attention(z(4, 2, 128, requires_grad=True), z(4, 1, 128), z(4, 1, 128), cu, 0.1)
