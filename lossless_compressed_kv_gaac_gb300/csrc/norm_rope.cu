@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "f32x2.cuh"
 #include "kv8.cuh"
 #include "rope.cuh"
 
@@ -22,7 +23,8 @@ namespace gaac {
 
 constexpr int kNrThreads = 64;
 constexpr int kNrBatch = 2;        // heads whose loads a lane has in flight
-constexpr int kNrMost = 5;         // most heads of a lane's walk
+constexpr int kNrMost = 5;         // most heads of a walk
+constexpr int kNrCtasPerSm = 12;
 constexpr int kNrMaxDim = 256;
 constexpr int kNgThreads = 128;    // gradient
 constexpr int kNgCtasPerSm = 3;
@@ -48,9 +50,11 @@ struct NormArgs {
   const uint64_t* turns;
   float mscale, eps;
   int rot_units, units, lanes;  // of a head; lanes of a group
-  int walkers;                  // groups that share the heads of a row
+  int walk, walkers;            // heads of a walk; groups that share the heads of a row (gradient: of the first tensor)
+  int walkers1;                 // gradient: of the second
   unsigned row_walkers;         // rows * walkers
-  float* part;                  // gradient: [CTA][2][dim]
+  unsigned ctas0;               // gradient: CTAs of the first tensor
+  float* part;                  // gradient: [CTA][dim]
 };
 
 // A lane's units of a head: element offsets of the two vectors of unit k, and whether they exist.
@@ -71,10 +75,20 @@ struct NormUnits {
   }
 };
 
+// A lane's channels of a head as UPL * V pairs (a, b), two of them to a packed number.  Pairs that are not turned have
+// sine 0 and cosine 1, so that all are treated alike.
 template <typename T, int V, int UPL, bool INTER>
 struct NormLane {
   using Vec = RopeVec<T, V>;
   using Units = NormUnits<V, UPL, INTER>;
+  static constexpr int kPairs = UPL * V / 2;  // packed
+
+  // The element of packed number q, half i, of the as (b = 0) or bs (1): unit, and place in its two vectors.
+  static __device__ __forceinline__ constexpr int unit(int q) { return 2 * q / V; }
+  static __device__ __forceinline__ constexpr int place(int q, int i, int b) {
+    const int p = (2 * q + i) % V;
+    return INTER ? 2 * p + b : p + b * V;
+  }
 
   static __device__ __forceinline__ void load(Vec (&v)[UPL][2], const char* x, const Units& n) {
 #pragma unroll
@@ -84,41 +98,92 @@ struct NormLane {
       if (n.two[k]) v[k][1] = *reinterpret_cast<const Vec*>(x + n.e1[k] * static_cast<int64_t>(sizeof(T)));
     }
   }
-  static __device__ __forceinline__ void store(char* out, const Units& n, int k, const float* f) {
-    Vec y;
-    if (n.one[k]) {
-      rope_pack<T, V>(y, f);
-      *reinterpret_cast<Vec*>(out + n.e0[k] * static_cast<int64_t>(sizeof(T))) = y;
+  static __device__ __forceinline__ void unpack(const Vec (&v)[UPL][2], uint64_t (&a)[kPairs], uint64_t (&b)[kPairs]) {
+    float f[UPL][2 * V];
+#pragma unroll
+    for (int k = 0; k < UPL; ++k) {
+      rope_unpack<T, V>(v[k][0], f[k]);
+      rope_unpack<T, V>(v[k][1], f[k] + V);
     }
-    if (n.two[k]) {
-      rope_pack<T, V>(y, f + V);
-      *reinterpret_cast<Vec*>(out + n.e1[k] * static_cast<int64_t>(sizeof(T))) = y;
+#pragma unroll
+    for (int q = 0; q < kPairs; ++q) {
+      constexpr int kStep = V == 1 ? 1 : 0;  // V == 1: the halves are of two units
+      a[q] = f2_make(f[unit(q)][place(q, 0, 0)], f[unit(q) + kStep][place(q, 1, 0)]);
+      b[q] = f2_make(f[unit(q)][place(q, 0, 1)], f[unit(q) + kStep][place(q, 1, 1)]);
     }
   }
-  static __device__ __forceinline__ void weights(float (&w)[UPL][2 * V], const NormArgs& a, const void* p, const Units& n) {
+  static __device__ __forceinline__ void store(char* out, const Units& n, const uint64_t (&a)[kPairs], const uint64_t (&b)[kPairs]) {
+    float f[UPL][2 * V];
 #pragma unroll
-    for (int k = 0; k < UPL; ++k)
+    for (int q = 0; q < kPairs; ++q) {
+      constexpr int kStep = V == 1 ? 1 : 0;
+      const float2 x = f2_get(a[q]), y = f2_get(b[q]);
+      f[unit(q)][place(q, 0, 0)] = x.x, f[unit(q) + kStep][place(q, 1, 0)] = x.y;
+      f[unit(q)][place(q, 0, 1)] = y.x, f[unit(q) + kStep][place(q, 1, 1)] = y.y;
+    }
 #pragma unroll
-      for (int i = 0; i < 2 * V; ++i) {
-        const int e = i < V ? n.e0[k] + i : n.e1[k] + i - V;
-        w[k][i] = 1.f;
-        if (p != nullptr && (i < V ? n.one[k] : n.two[k])) {
-          if (a.w_f32)
-            w[k][i] = static_cast<const float*>(p)[e];
-          else if constexpr (sizeof(T) == 2)
-            w[k][i] = RopePair<T>::get(static_cast<const T*>(p)[e]);
+    for (int k = 0; k < UPL; ++k) {
+      Vec y;
+      if (n.one[k]) {
+        rope_pack<T, V>(y, f[k]);
+        *reinterpret_cast<Vec*>(out + n.e0[k] * static_cast<int64_t>(sizeof(T))) = y;
+      }
+      if (n.two[k]) {
+        rope_pack<T, V>(y, f[k] + V);
+        *reinterpret_cast<Vec*>(out + n.e1[k] * static_cast<int64_t>(sizeof(T))) = y;
+      }
+    }
+  }
+  // f(a or b (0, 1), q, half, channel) for every channel of the lane.
+  template <typename F>
+  static __device__ __forceinline__ void each(const Units& n, F f) {
+#pragma unroll
+    for (int q = 0; q < kPairs; ++q)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = unit(q) + (V == 1 ? i : 0);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int at = place(q, i, b);
+          if (at < V ? n.one[k] : n.two[k]) f(b, q, i, at < V ? n.e0[k] + at : n.e1[k] + at - V);
         }
       }
   }
-  static __device__ __forceinline__ void sines(float (&s)[UPL][V], float (&c)[UPL][V], const NormArgs& a, const Units& n, int lane,
-                                               int64_t pos_at) {
+  static __device__ __forceinline__ void weights(uint64_t (&wa)[kPairs], uint64_t (&wb)[kPairs], const NormArgs& a, const void* p,
+                                                 const Units& n) {
+    float w[2][kPairs][2];
+#pragma unroll
+    for (int q = 0; q < kPairs; ++q) w[0][q][0] = w[0][q][1] = w[1][q][0] = w[1][q][1] = 1.f;
+    if (p != nullptr && (a.w_f32 || sizeof(T) == 4)) {
+      each(n, [&](int b, int q, int i, int ch) { w[b][q][i] = static_cast<const float*>(p)[ch]; });
+    } else if (p != nullptr) {
+      if constexpr (sizeof(T) == 2) {
+        Vec v[UPL][2];
+        if ((reinterpret_cast<uintptr_t>(p) & (V * 2 - 1)) == 0) {
+          load(v, static_cast<const char*>(p), n);
+          unpack(v, wa, wb);
+          return;
+        }
+        each(n, [&](int b, int q, int i, int ch) { w[b][q][i] = RopePair<T>::get(static_cast<const T*>(p)[ch]); });
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kPairs; ++q) wa[q] = f2_make(w[0][q][0], w[0][q][1]), wb[q] = f2_make(w[1][q][0], w[1][q][1]);
+  }
+  static __device__ __forceinline__ void sines(uint64_t (&s)[kPairs], uint64_t (&c)[kPairs], const NormArgs& a, const Units& n,
+                                               int lane, int64_t pos_at) {
     const uint64_t p = rope_position(a.pos, a.pos64, pos_at);
 #pragma unroll
-    for (int k = 0; k < UPL; ++k)
-      if (n.turned[k]) {
+    for (int q = 0; q < kPairs; ++q) {
+      float x[2] = {0.f, 0.f}, y[2] = {1.f, 1.f};
 #pragma unroll
-        for (int i = 0; i < V; ++i) rope_sincos<T>(p * a.turns[(lane + k * a.lanes) * V + i], a.mscale, s[k][i], c[k][i]);
+      for (int i = 0; i < 2; ++i) {
+        const int k = unit(q) + (V == 1 ? i : 0);
+        if (n.turned[k]) rope_sincos<T>(p * a.turns[(lane + k * a.lanes) * V + (2 * q + i) % V], a.mscale, x[i], y[i]);
       }
+      s[q] = f2_make(x[0], x[1]);
+      c[q] = f2_make(y[0], y[1]);
+    }
   }
 };
 
@@ -132,18 +197,19 @@ __device__ __forceinline__ uint32_t group_mask(int lanes) {
   return low << (threadIdx.x & 31 & ~(lanes - 1));
 }
 
-// Group (row, walker): heads walker, walker + walkers, ... of one row.
+// Group (row, walker): `walk` heads of one row, from walker * walk on.
 template <typename T, int V, int UPL, bool INTER>
-__global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kNrThreads, kNrCtasPerSm) qk_norm_rope_kernel(const NormArgs a) {
   dependent_wait();
   dependent_launch();
   using L = NormLane<T, V, UPL, INTER>;
+  constexpr int kP = L::kPairs;
   const int lane = threadIdx.x & (a.lanes - 1);
   const uint32_t mask = group_mask(a.lanes);
   const unsigned rw = blockIdx.x * (kNrThreads / a.lanes) + threadIdx.x / a.lanes;
   if (rw >= a.row_walkers) return;
   const unsigned row = rw / a.walkers;
-  const int walker = static_cast<int>(rw - row * a.walkers);
+  const int first = static_cast<int>(rw - row * a.walkers) * a.walk, end = min(first + a.walk, a.heads);
   unsigned seq = 0, tok = row;
   if (a.n_seq > 1) {
     seq = row / a.n_tok;
@@ -158,195 +224,169 @@ __global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NormArgs
   auto load = [&](int h0) {
 #pragma unroll
     for (int j = 0; j < kNrBatch; ++j) {
-      const int h = h0 + j * a.walkers;
-      if (h < a.heads) L::load(v[j], h >= a.heads0 ? xk + (h - a.heads0) * a.t[1].x_head : xq + h * a.t[0].x_head, n);
+      const int h = h0 + j;
+      if (h < end) L::load(v[j], h >= a.heads0 ? xk + (h - a.heads0) * a.t[1].x_head : xq + h * a.t[0].x_head, n);
     }
   };
-  load(walker);
-  float s[UPL][V], c[UPL][V], w[UPL][2 * V];
+  load(first);
+  uint64_t s[kP], c[kP];
   L::sines(s, c, a, n, lane, seq * a.pos_seq + tok * a.pos_tok);
-  int of = -1;  // the tensor whose weights w holds
+  // a' = r (a ca + b sb),  b' = r (b cb + a sa): the weights are part of the sines
+  uint64_t ca[kP], cb[kP], sa[kP], sb[kP];
+  int of = -1;  // the tensor whose weights they hold
   const float mean = 1.f / a.dim;
-  for (int h0 = walker;;) {
+#pragma unroll 1
+  for (int h0 = first;;) {
 #pragma unroll
     for (int j = 0; j < kNrBatch; ++j) {
-      const int h = h0 + j * a.walkers;
-      if (h >= a.heads) break;
+      const int h = h0 + j;
+      if (h >= end) break;
       const int second = h >= a.heads0;
       if (second != of) {
-        L::weights(w, a, a.t[second].w, n);
+        L::weights(ca, cb, a, a.t[second].w, n);
+#pragma unroll
+        for (int q = 0; q < kP; ++q) {
+          sa[q] = f2_mul(s[q], ca[q]);
+          sb[q] = f2_mul(f2_mul(s[q], f2_all(-1.f)), cb[q]);
+          ca[q] = f2_mul(c[q], ca[q]);
+          cb[q] = f2_mul(c[q], cb[q]);
+        }
         of = second;
       }
-      char* out = second ? outk + (h - a.heads0) * a.t[1].out_head : outq + h * a.t[0].out_head;
-      float e[UPL][2 * V], sum = 0.f;
+      uint64_t x[kP], y[kP], sum = 0;
+      L::unpack(v[j], x, y);
 #pragma unroll
-      for (int k = 0; k < UPL; ++k) {
-        rope_unpack<T, V>(v[j][k][0], e[k]);
-        rope_unpack<T, V>(v[j][k][1], e[k] + V);
+      for (int q = 0; q < kP; ++q) sum = f2_fma(y[q], y[q], f2_fma(x[q], x[q], sum));
+      const uint64_t r = f2_all(rsqrtf(group_sum(f2_sum(sum), a.lanes, mask) * mean + a.eps));
 #pragma unroll
-        for (int i = 0; i < 2 * V; ++i) sum += e[k][i] * e[k][i];
+      for (int q = 0; q < kP; ++q) {
+        const uint64_t t = x[q];
+        x[q] = f2_mul(r, f2_fma(t, ca[q], f2_mul(y[q], sb[q])));
+        y[q] = f2_mul(r, f2_fma(y[q], cb[q], f2_mul(t, sa[q])));
       }
-      const float r = rsqrtf(group_sum(sum, a.lanes, mask) * mean + a.eps);
-#pragma unroll
-      for (int k = 0; k < UPL; ++k) {
-#pragma unroll
-        for (int i = 0; i < 2 * V; ++i) e[k][i] *= r * w[k][i];
-        if (n.turned[k]) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : V + i;
-            const float x0 = e[k][ia], x1 = e[k][ib];
-            e[k][ia] = x0 * c[k][i] - x1 * s[k][i];
-            e[k][ib] = x1 * c[k][i] + x0 * s[k][i];
-          }
-        }
-        L::store(out, n, k, e[k]);
-      }
+      L::store(second ? outk + (h - a.heads0) * a.t[1].out_head : outq + h * a.t[0].out_head, n, x, y);
     }
-    h0 += kNrBatch * a.walkers;
-    if (h0 >= a.heads) break;
+    h0 += kNrBatch;
+    if (h0 >= end) break;
     load(h0);
   }
 }
 
-// One tensor's heads first, first + step, ... below n_heads of a row: writes dx, adds to dw.
-template <typename T, int V, int UPL, bool INTER>
-__device__ __forceinline__ void norm_gradient_heads(const NormArgs& a, const NormTensor& t, unsigned seq, unsigned tok, int first,
-                                                    int n_heads, const NormUnits<V, UPL, INTER>& n, uint32_t mask,
-                                                    const float (&s)[UPL][V], const float (&c)[UPL][V],
-                                                    const float (&w)[UPL][2 * V], float (&dw)[UPL][2 * V]) {
-  using L = NormLane<T, V, UPL, INTER>;
-  const char* const x = t.x + seq * t.x_seq + tok * t.x_tok;
-  const char* const dz = t.dz + seq * t.dz_seq + tok * t.dz_tok;
-  char* const out = t.out + seq * t.out_seq + tok * t.out_tok;
-  const float mean = 1.f / a.dim;
-#pragma unroll 1
-  for (int h0 = first; h0 < n_heads; h0 += kNrBatch * a.walkers) {
-    RopeVec<T, V> vx[kNrBatch][UPL][2], vg[kNrBatch][UPL][2];
-#pragma unroll
-    for (int j = 0; j < kNrBatch; ++j) {
-      const int h = h0 + j * a.walkers;
-      if (h < n_heads) {
-        L::load(vx[j], x + h * t.x_head, n);
-        L::load(vg[j], dz + h * t.dz_head, n);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kNrBatch; ++j) {
-      const int h = h0 + j * a.walkers;
-      if (h >= n_heads) break;
-      float e[UPL][2 * V], g[UPL][2 * V], xx = 0.f, hx = 0.f;
-#pragma unroll
-      for (int k = 0; k < UPL; ++k) {
-        rope_unpack<T, V>(vx[j][k][0], e[k]);
-        rope_unpack<T, V>(vx[j][k][1], e[k] + V);
-        rope_unpack<T, V>(vg[j][k][0], g[k]);
-        rope_unpack<T, V>(vg[j][k][1], g[k] + V);
-        if (n.turned[k]) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : V + i;
-            const float g0 = g[k][ia], g1 = g[k][ib];
-            g[k][ia] = g0 * c[k][i] + g1 * s[k][i];
-            g[k][ib] = g1 * c[k][i] - g0 * s[k][i];
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 2 * V; ++i) {
-          xx += e[k][i] * e[k][i];
-          hx += g[k][i] * w[k][i] * e[k][i];
-        }
-      }
-      xx = group_sum(xx, a.lanes, mask);
-      hx = group_sum(hx, a.lanes, mask);
-      const float r = rsqrtf(xx * mean + a.eps), m = hx * mean * r;  // m: the mean of h x r
-#pragma unroll
-      for (int k = 0; k < UPL; ++k) {
-#pragma unroll
-        for (int i = 0; i < 2 * V; ++i) {
-          const float y = e[k][i] * r;
-          dw[k][i] += g[k][i] * y;
-          e[k][i] = r * (g[k][i] * w[k][i] - y * m);
-        }
-        L::store(out + h * t.out_head, n, k, e[k]);
-      }
-    }
-  }
-}
-
-// Groups take (row, walker) in turn over the whole grid.
+// CTAs below ctas0 take the first tensor, the others the second; their groups take (row, walker) in turn.
 template <typename T, int V, int UPL, bool INTER>
 __global__ void __launch_bounds__(kNgThreads, kNgCtasPerSm) qk_norm_rope_gradient_kernel(const NormArgs a) {
-  __shared__ float sums[kNgThreads * UPL * 2 * V];  // [group][dim], one tensor at a time
+  __shared__ float sums[kNgThreads * UPL * 2 * V];  // [group][dim]
   dependent_wait();
   dependent_launch();
   using L = NormLane<T, V, UPL, INTER>;
+  constexpr int kP = L::kPairs;
   const int lane = threadIdx.x & (a.lanes - 1), groups = kNgThreads / a.lanes, group = threadIdx.x / a.lanes;
   const uint32_t mask = group_mask(a.lanes);
+  const bool second = blockIdx.x >= a.ctas0;
+  const NormTensor& t = a.t[second];
+  const int n_heads = second ? a.heads - a.heads0 : a.heads0, walkers = second ? a.walkers1 : a.walkers;
+  const int64_t cta = second ? blockIdx.x - a.ctas0 : blockIdx.x, ctas = second ? gridDim.x - a.ctas0 : a.ctas0;
+  const unsigned rows = a.n_seq * a.n_tok;
   const NormUnits<V, UPL, INTER> n(a, lane);
-  float w[2][UPL][2 * V], dw[2][UPL][2 * V];
+  const float mean = 1.f / a.dim;
+  uint64_t wa[kP], wb[kP], da[kP], db[kP];
+  L::weights(wa, wb, a, t.w, n);
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    L::weights(w[t], a, a.t[t].w, n);
-#pragma unroll
-    for (int k = 0; k < UPL; ++k)
-#pragma unroll
-      for (int i = 0; i < 2 * V; ++i) dw[t][k][i] = 0.f;
-  }
+  for (int q = 0; q < kP; ++q) da[q] = db[q] = 0;
 #pragma unroll 1
-  for (int64_t rw = static_cast<int64_t>(blockIdx.x) * groups + group; rw < a.row_walkers; rw += static_cast<int64_t>(gridDim.x) * groups) {
-    const unsigned row = static_cast<unsigned>(rw) / a.walkers;
-    const int walker = static_cast<int>(static_cast<unsigned>(rw) - row * a.walkers);
+  for (int64_t rw = cta * groups + group; rw < static_cast<int64_t>(rows) * walkers; rw += ctas * groups) {
+    const unsigned row = static_cast<unsigned>(rw) / walkers;
+    const int first = (static_cast<unsigned>(rw) - row * walkers) * a.walk, end = min(first + a.walk, n_heads);
     unsigned seq = 0, tok = row;
     if (a.n_seq > 1) {
       seq = row / a.n_tok;
       tok = row - seq * a.n_tok;
     }
-    float s[UPL][V], c[UPL][V];
+    const char* const x = t.x + seq * t.x_seq + tok * t.x_tok;
+    const char* const dz = t.dz + seq * t.dz_seq + tok * t.dz_tok;
+    char* const out = t.out + seq * t.out_seq + tok * t.out_tok;
+    RopeVec<T, V> vx[2][UPL][2], vz[2][UPL][2];
+    L::load(vx[0], x + first * t.x_head, n);
+    L::load(vz[0], dz + first * t.dz_head, n);
+    uint64_t s[kP], c[kP];
     L::sines(s, c, a, n, lane, seq * a.pos_seq + tok * a.pos_tok);
-    norm_gradient_heads<T, V, UPL, INTER>(a, a.t[0], seq, tok, walker, a.heads0, n, mask, s, c, w[0], dw[0]);
-    // the walk goes on where the first tensor's heads end
-    const int left = (walker - a.heads0) % a.walkers, first = left < 0 ? left + a.walkers : left;
-    norm_gradient_heads<T, V, UPL, INTER>(a, a.t[1], seq, tok, first, a.heads - a.heads0, n, mask, s, c, w[1], dw[1]);
-  }
+    auto one = [&](const RopeVec<T, V> (&v)[UPL][2], const RopeVec<T, V> (&z)[UPL][2], int h) {
+      uint64_t xa[kP], xb[kP], ga[kP], gb[kP], ta[kP], tb[kP], xx = 0, hx = 0;
+      L::unpack(v, xa, xb);
+      L::unpack(z, ga, gb);
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    __syncthreads();  // the other tensor's sums are read
+      for (int q = 0; q < kP; ++q) {
+        const uint64_t g0 = ga[q], minus = f2_mul(s[q], f2_all(-1.f));
+        ga[q] = f2_fma(g0, c[q], f2_mul(gb[q], s[q]));
+        gb[q] = f2_fma(gb[q], c[q], f2_mul(g0, minus));
+        ta[q] = f2_mul(ga[q], xa[q]);
+        tb[q] = f2_mul(gb[q], xb[q]);
+        xx = f2_fma(xb[q], xb[q], f2_fma(xa[q], xa[q], xx));
+        hx = f2_fma(tb[q], wb[q], f2_fma(ta[q], wa[q], hx));
+      }
+      const float r = rsqrtf(group_sum(f2_sum(xx), a.lanes, mask) * mean + a.eps);
+      const float m = group_sum(f2_sum(hx), a.lanes, mask) * mean * r;  // the mean of h x r
+      const uint64_t r2 = f2_all(r), k2 = f2_all(-r * r * m);
 #pragma unroll
-    for (int k = 0; k < UPL; ++k)
-#pragma unroll
-      for (int i = 0; i < 2 * V; ++i)
-        if (i < V ? n.one[k] : n.two[k]) sums[group * a.dim + (i < V ? n.e0[k] + i : n.e1[k] + i - V)] = dw[t][k][i];
-    __syncthreads();
-    for (int ch = threadIdx.x; ch < a.dim; ch += kNgThreads) {
-      float sum = 0.f;
-      for (int i = 0; i < groups; ++i) sum += sums[i * a.dim + ch];
-      a.part[(static_cast<int64_t>(blockIdx.x) * 2 + t) * a.dim + ch] = sum;
+      for (int q = 0; q < kP; ++q) {
+        da[q] = f2_fma(ta[q], r2, da[q]);
+        db[q] = f2_fma(tb[q], r2, db[q]);
+        xa[q] = f2_fma(f2_mul(ga[q], wa[q]), r2, f2_mul(xa[q], k2));
+        xb[q] = f2_fma(f2_mul(gb[q], wb[q]), r2, f2_mul(xb[q], k2));
+      }
+      L::store(out + h * t.out_head, n, xa, xb);
+    };
+    // the next head's loads are under way while one is worked on
+#pragma unroll 1
+    for (int h = first; h < end; h += 2) {
+      if (h + 1 < end) {
+        L::load(vx[1], x + (h + 1) * t.x_head, n);
+        L::load(vz[1], dz + (h + 1) * t.dz_head, n);
+      }
+      one(vx[0], vz[0], h);
+      if (h + 1 < end) {
+        if (h + 2 < end) {
+          L::load(vx[0], x + (h + 2) * t.x_head, n);
+          L::load(vz[0], dz + (h + 2) * t.dz_head, n);
+        }
+        one(vx[1], vz[1], h + 1);
+      }
     }
+  }
+  L::each(n, [&](int b, int q, int i, int ch) {
+    const float2 d = f2_get(b ? db[q] : da[q]);
+    sums[group * a.dim + ch] = i ? d.y : d.x;
+  });
+  __syncthreads();
+  for (int ch = threadIdx.x; ch < a.dim; ch += kNgThreads) {
+    float sum = 0.f;
+    for (int i = 0; i < groups; ++i) sum += sums[i * a.dim + ch];
+    a.part[static_cast<int64_t>(blockIdx.x) * a.dim + ch] = sum;
   }
 }
 
-// dw of 32 channels: 32 threads each, in 32 runs of CTAs that are joined in order.
-__global__ void __launch_bounds__(1024) norm_weights_kernel(const float* part, int ctas, int dim, float* dw0, float* dw1) {
+// dw of 32 channels of one tensor: 32 threads each, in 32 runs of its CTAs that are joined in order.
+__global__ void __launch_bounds__(1024) norm_weights_kernel(const float* part, int ctas0, int ctas, int dim, float* dw0, float* dw1) {
   __shared__ float sums[32][33];
   dependent_wait();
   dependent_launch();
-  const int ch = threadIdx.x & 31, run = threadIdx.x >> 5;
-  const int at = blockIdx.x * 32 + ch;  // of [2][dim]
-  const int per = (ctas + 31) / 32;
+  const int ch = threadIdx.x & 31, run = threadIdx.x >> 5, at = blockIdx.x * 32 + ch;
+  const int begin = blockIdx.y == 0 ? 0 : ctas0, end = blockIdx.y == 0 ? ctas0 : ctas;
+  float* const dw = blockIdx.y == 0 ? dw0 : dw1;
+  if (dw == nullptr) return;
+  const int per = (end - begin + 31) / 32;
   float sum = 0.f;
-  if (at < 2 * dim) {
-#pragma unroll 8
-    for (int i = run * per; i < min(ctas, (run + 1) * per); ++i) sum += __ldcg(part + static_cast<int64_t>(i) * 2 * dim + at);
+  if (at < dim) {
+#pragma unroll 16
+    for (int i = begin + run * per; i < min(end, begin + (run + 1) * per); ++i) sum += __ldcg(part + static_cast<int64_t>(i) * dim + at);
   }
   sums[run][ch] = sum;
   __syncthreads();
-  if (run == 0 && at < 2 * dim) {
+  if (run == 0 && at < dim) {
     sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) sum += sums[i][ch];
-    float* dw = at < dim ? dw0 : dw1;
-    if (dw != nullptr) dw[at < dim ? at : at - dim] = sum;
+    dw[at] = sum;
   }
 }
 
@@ -457,18 +497,25 @@ static int norm_rope(const gaac_norm_tensor* tensors, int n_tensors, int dtype, 
   a.units = a.rot_units + ((head_dim - rot_dim) / v + 1) / 2;
   a.lanes = 2;
   while (a.lanes < 32 && a.lanes < a.units) a.lanes *= 2;
-  // Heads of a walk: as rope's, as many as leave twice the lanes that 152 SMs hold at a time, so that sines are shared
-  // where there is work for all, and single heads where latency counts.
-  const int64_t want = int64_t{152} * 2048, per_row = std::max<int64_t>(rows, 1) * a.lanes;
-  const int64_t walkers = std::max<int64_t>(gradient ? 1 : (heads + kNrMost - 1) / kNrMost, (want + per_row - 1) / per_row);
-  a.walkers = static_cast<int>(std::min<int64_t>(heads, walkers));
-  if (rows * a.walkers > 0x7FFFFFFF) return GAAC_EINVAL;
+  // Heads of a walk: as many as leave twice the lanes that 152 SMs hold at a time, so that sines are shared where there
+  // is work for all, and single heads where latency counts.
+  const int64_t want = int64_t{152} * (gradient ? 768 : 2048), lanes = std::max<int64_t>(rows, 1) * heads * a.lanes;
+  a.walk = static_cast<int>(std::min<int64_t>(gradient ? heads : kNrMost, std::max<int64_t>(1, lanes / want)));
+  const int first = gradient ? a.heads0 : a.heads;
+  a.walkers = (first + a.walk - 1) / a.walk;
+  a.walkers1 = (a.heads - a.heads0 + a.walk - 1) / a.walk;
+  if (rows * std::max(a.walkers, a.walkers1) > 0x7FFFFFFF) return GAAC_EINVAL;
   a.row_walkers = static_cast<unsigned>(rows * a.walkers);
   a.part = static_cast<float*>(workspace);
   int grid = 0;
-  if (gradient) {
+  if (gradient) {  // CTAs of either tensor in the ratio of their heads
     const int64_t per = kNgThreads / a.lanes;
-    grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kNgMostCtas, (a.row_walkers + per - 1) / per)));
+    auto ctas = [&](int n, int walkers) {
+      const int64_t share = std::max<int64_t>(1, (kNgMostCtas - 1) * static_cast<int64_t>(n) / heads);
+      return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(share, (rows * walkers + per - 1) / per)));
+    };
+    a.ctas0 = ctas(a.heads0, a.walkers);
+    grid = a.ctas0 + (n_tensors == 2 ? ctas(a.heads - a.heads0, a.walkers1) : 0);
   }
   const bool inter = (flags & GAAC_ROPE_INTERLEAVED) != 0;
   int e;
@@ -479,8 +526,9 @@ static int norm_rope(const gaac_norm_tensor* tensors, int n_tensors, int dtype, 
   else
     e = wide ? norm_launch<float, 4, 1>(a, inter, grid, stream) : norm_launch<float, 1, 4>(a, inter, grid, stream);
   if (e != GAAC_OK || !gradient) return e;
-  return kv8_launch(norm_weights_kernel, dim3((2 * head_dim + 31) / 32), 1024, 0, stream, static_cast<const float*>(a.part), grid, head_dim,
-                    a.t[0].dw, a.t[1].dw);
+  if (a.t[0].dw == nullptr && a.t[1].dw == nullptr) return GAAC_OK;
+  return kv8_launch(norm_weights_kernel, dim3((head_dim + 31) / 32, n_tensors), 1024, 0, stream, static_cast<const float*>(a.part),
+                    static_cast<int>(a.ctas0), grid, head_dim, a.t[0].dw, a.t[1].dw);
 }
 
 }  // namespace gaac
@@ -489,7 +537,7 @@ using namespace gaac;
 
 extern "C" size_t gaac_qk_norm_rope_workspace(int head_dim) {
   if (head_dim < 2 || head_dim > kNrMaxDim) return 0;
-  return (static_cast<size_t>(kNgMostCtas) * 2 * head_dim * sizeof(float) + 15) & ~static_cast<size_t>(15);
+  return (static_cast<size_t>(kNgMostCtas + 1) * head_dim * sizeof(float) + 15) & ~static_cast<size_t>(15);
 }
 
 extern "C" int gaac_qk_norm_rope(const gaac_norm_tensor* tensors, int n_tensors, int dtype, int weight_dtype, int64_t n_seq,

@@ -7,7 +7,7 @@
 // rows (row r of a tile: token r / G, head r % G), so that a tile's rows share their keys, its diagonal is short
 // and few tokens still fill a tile.  Warps:
 //  * one issues the copies (TMA): both tiles' queries, then K and V of 128 tokens in turn into a ring of five slots;
-//  * one thread issues tcgen05.mma: S = Q K^T (128 x 128, both operands in shared memory), O += P V (P in TMEM, V's
+//  * one multiplies (tcgen05.mma): S = Q K^T (128 x 128, both operands in shared memory), O += P V (P in TMEM, V's
 //    rows as they lie, token-major).  While one tile's S is in its softmax, the tensor cores work for the other.
 //  * four warps for each tile: a thread owns a row.  S comes from TMEM into its registers; P goes back, rounded to the
 //    inputs' type, over the S it came from.  All of TMEM's 512 columns are used: S and O of both tiles.
@@ -16,12 +16,13 @@
 // nothing in either type (rounding is relative; f16 goes to 2^16, and loses weights below 2^-25, of the reference
 // or of 2^-8 of the maximum).  Sums are fp32 over the unrounded weights; a weight's rounding, 2^-9 in bf16 and 2^-12 in
 // f16, is that of the result's type.
-// Where a mask leaves keys out, V has to be finite there, or 0 * V would be NaN: two warps look such blocks of V over
-// before they are multiplied and put zeros in the place of what is not finite.  What of that rows may see is added
+// Where a mask leaves keys out, V has to be finite there, or 0 * V would be NaN: one warp looks such a block of V over
+// before it is multiplied and puts zeros in the place of what is not finite.  What of that rows may see is added
 // to them at the end, from memory.
 #include <algorithm>
 #include <cmath>
 
+#include "f32x2.cuh"
 #include "kv8.cuh"
 #include "tma.cuh"
 
@@ -33,8 +34,9 @@ constexpr int kPaTile = 128 * kD * 2;         // bytes of a tile of Q, K or V
 constexpr int kPaHalf = kPaTile / 2;          // 64 channels of it: rows of 128 bytes, swizzled
 constexpr int kPaSlots = 5;
 constexpr int kPaSoftmax = 256;
-constexpr int kPaThreads = kPaSoftmax + 128;   // + the multiplier, the copier and two that look V over
-constexpr int kPaCleaners = 64;
+constexpr int kPaThreads = kPaSoftmax + 128;   // + two multipliers, the copier and one that looks V over
+constexpr int kPaCleaners = 32;
+constexpr int kPaEarly = 64;                  // keys of a block whose weights are multiplied ahead of the others
 constexpr int kPaLook = 3;                    // blocks of a unit that have masked keys, at most
 constexpr uint32_t kPaFull = 0xFFFFFFFFu;
 constexpr uint32_t kPaColS = 0, kPaColO = 256;  // TMEM columns: S of tile t at 128 t, P over it, O at 256 + 128 t
@@ -57,7 +59,7 @@ struct PaArgs {
 struct PaSmem {
   alignas(1024) uint8_t q[2][kPaTile];
   alignas(1024) uint8_t kv[kPaSlots][kPaTile];
-  uint64_t q_full[2], kv_full[kPaSlots], kv_empty[kPaSlots], s_full[2], p_full[2], o_full[2], due[kPaLook], clean[kPaLook], done;
+  uint64_t q_full[2], kv_full[kPaSlots], kv_empty[kPaSlots], s_full[2], p_early[2], p_full[2], o_full[2], due[kPaLook], clean[kPaLook], done[2];
   uint32_t tmem;
   int odd;  // a V that some row may see is not finite in a block with masked keys
 };
@@ -84,22 +86,29 @@ __device__ __forceinline__ void t5_before() { asm volatile("tcgen05.fence::befor
 __device__ __forceinline__ void t5_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void t5_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-#define GAAC_R8(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]), "+r"(x[i + 4]), "+r"(x[i + 5]), "+r"(x[i + 6]), "+r"(x[i + 7])
 #define GAAC_W8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
+#define GAAC_W32(x, i) GAAC_W8(x, i), GAAC_W8(x, i + 8), GAAC_W8(x, i + 16), GAAC_W8(x, i + 24)
 #define GAAC_I8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
 
-// 32 columns of this warp's 32 lanes, one lane a thread.  The registers hold them after t5_wait_ld.
+// Columns of this warp's 32 lanes, one lane a thread: the wait is part of the load, so nothing uses a register before it.
 __device__ __forceinline__ void t5_ld32(uint32_t* x, uint32_t at) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
-      "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
       : GAAC_W8(x, 0), GAAC_W8(x, 8), GAAC_W8(x, 16), GAAC_W8(x, 24)
       : "r"(at)
       : "memory");
 }
-// Nothing may use the registers before the wait: it passes them through.
-__device__ __forceinline__ void t5_wait_ld(uint32_t* x) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : GAAC_R8(x, 0), GAAC_R8(x, 8), GAAC_R8(x, 16), GAAC_R8(x, 24)::"memory");
+__device__ __forceinline__ void t5_ld128(uint32_t* x, uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : GAAC_W32(x, 0), GAAC_W32(x, 32), GAAC_W32(x, 64), GAAC_W32(x, 96)
+      : "r"(at), "r"(at + 32), "r"(at + 64), "r"(at + 96)
+      : "memory");
 }
 __device__ __forceinline__ void t5_st32(uint32_t at, const uint32_t* x) {
   asm volatile(
@@ -133,6 +142,11 @@ __device__ __forceinline__ void pa_tma(void* dst, const CUtensorMap* map, int x,
       : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float pa_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -236,57 +250,83 @@ __device__ void pa_load(const PaArgs& a, PaSmem& sm, const PaUnit& u, const CUte
     if (u.blocks[t]) mbar_wait(&sm.q_full[t], 0, a.status);
 }
 
+// One lane of a converged warp, always the same one.
+__device__ __forceinline__ bool pa_elect() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0u;
+}
+
+// Tile t's multiplier.  All of the warp walks along and one lane issues, so that addresses and descriptors are known to be
+// the same for the warp: with a branch that one lane alone takes, an instruction took some 75 cycles to issue, and its
+// thread, not the tensor cores, was what the kernel waited for.  One warp for both tiles spends as long in its waits
+// and commits as the tensor cores need for the products; with one for each, either's fall under the other's products.
 template <bool HALF>
-__device__ void pa_mma(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_t tmem) {
+__device__ void pa_mma(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_t tmem, int t) {
   const uint32_t id_qk = pa_idesc(!HALF, false), id_pv = pa_idesc(!HALF, true);
-  const int blocks = max(u.blocks[0], u.blocks[1]);
-  bool ok = true;
-  auto qk = [&](int t, int i) {
-    const uint32_t q = smem_addr(sm.q[t]), k = smem_addr(sm.kv[pa_slot(2 * i)]);
+  const int blocks = u.blocks[t], all = max(u.blocks[0], u.blocks[1]);
+  const uint32_t col_s = tmem + kPaColS + 128 * t, col_o = tmem + kPaColO + 128 * t;
+  const uint64_t q0 = pa_desc(smem_addr(sm.q[t]), 16), k0 = pa_desc(smem_addr(sm.kv[0]), 16), v0 = pa_desc(smem_addr(sm.kv[0]), kPaHalf);
+  auto qk = [&](int slot) {
+    const uint64_t k = k0 + slot * (kPaTile / 16);
 #pragma unroll
     for (int j = 0; j < kD / 16; ++j) {
-      const uint32_t at = (j / 4) * kPaHalf + (j % 4) * 32;
-      t5_mma_ss(tmem + kPaColS + 128 * t, pa_desc(q + at, 16), pa_desc(k + at, 16), id_qk, j > 0);
+      const uint32_t at = ((j / 4) * kPaHalf + (j % 4) * 32) / 16;
+      t5_mma_ss(col_s, q0 + at, k + at, id_qk, j > 0);
     }
     t5_commit(&sm.s_full[t]);
   };
-  auto pv = [&](int t, int i) {
-    const uint32_t v = smem_addr(sm.kv[pa_slot(2 * i + 1)]);
+  auto pv = [&](int slot, uint32_t add, int j0, int j1) {
+    const uint64_t v = v0 + slot * (kPaTile / 16);
 #pragma unroll
-    for (int j = 0; j < kPaKeys / 16; ++j)
-      t5_mma_ts(tmem + kPaColO + 128 * t, tmem + kPaColS + 128 * t + 8 * j, pa_desc(v + j * 2048, kPaHalf), id_pv, i > 0 || j > 0);
-    t5_commit(&sm.o_full[t]);
+    for (int j = j0; j < j1; ++j) t5_mma_ts(col_o, col_s + 8 * j, v + j * (2048 / 16), id_pv, j > 0 ? 1u : add);
   };
-  auto arrived = [&](int n) { return mbar_wait(&sm.kv_full[pa_slot(n)], pa_phase(n), a.status); };
-  ok = arrived(0);
-  for (int t = 0; t < 2 && ok; ++t)
-    if (u.blocks[t]) {
-      ok = mbar_wait(&sm.q_full[t], 0, a.status);
-      if (ok) qk(t, 0);
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kPaFull, mbar_wait(bar, parity, a.status)); };
+  // A slot is handed back by the multipliers of both tiles (of the one that has tokens), where there is a copy that waits for
+  // it.  The first tile has one block less than the second at most, which no copy waits for.
+  bool ok = true;
+  if (blocks > 0) {
+    ok = wait(&sm.q_full[t], 0) && wait(&sm.kv_full[0], 0);
+    if (ok && pa_elect()) {
+      qk(0);
+      if (kPaSlots < 2 * all) t5_commit(&sm.kv_empty[0]);
     }
-  // a slot is handed back where there is a copy that waits for it
-  if (ok && kPaSlots < 2 * blocks) t5_commit(&sm.kv_empty[0]);
+    __syncwarp();
+  }
+  int slot = 1;  // of V of block i
+  uint32_t phase = 0;
   for (int i = 0; i < blocks && ok; ++i) {
-    ok = arrived(2 * i + 1);
-    if (ok && i + 1 < blocks) ok = arrived(2 * i + 2);
-    if (ok && i >= u.look) ok = mbar_wait(&sm.clean[i - u.look], 0, a.status);
-    for (int t = 0; t < 2 && ok; ++t) {
-      if (i >= u.blocks[t]) continue;
-      ok = mbar_wait(&sm.p_full[t], i & 1, a.status);
-      if (!ok) break;
-      t5_after();
-      pv(t, i);
-      if (i + 1 < u.blocks[t]) qk(t, i + 1);
+    const int v_slot = slot;
+    ok = wait(&sm.kv_full[v_slot], phase) && (i < u.look || wait(&sm.clean[i - u.look], 0)) && wait(&sm.p_early[t], i & 1);
+    if (!ok) break;
+    t5_after();
+    if (pa_elect()) pv(v_slot, i > 0, 0, kPaEarly / 16);
+    __syncwarp();
+    if (++slot == kPaSlots) slot = 0, phase ^= 1u;
+    const int k_slot = slot;
+    const uint32_t k_phase = phase;
+    if (++slot == kPaSlots) slot = 0, phase ^= 1u;
+    ok = (i + 1 >= blocks || wait(&sm.kv_full[k_slot], k_phase)) && wait(&sm.p_full[t], i & 1);
+    if (!ok) break;
+    t5_after();
+    if (pa_elect()) {
+      pv(v_slot, 1u, kPaEarly / 16, kPaKeys / 16);
+      t5_commit(&sm.o_full[t]);
+      if (2 * i + 1 + kPaSlots < 2 * all) t5_commit(&sm.kv_empty[v_slot]);
+      if (i + 1 < blocks) {
+        qk(k_slot);
+        if (2 * i + 2 + kPaSlots < 2 * all) t5_commit(&sm.kv_empty[k_slot]);
+      }
     }
-    for (int n = 2 * i + 1; n <= 2 * i + 2 && ok; ++n)
-      if (n + kPaSlots < 2 * blocks) t5_commit(&sm.kv_empty[pa_slot(n)]);
+    __syncwarp();
   }
   // nothing may be under way when TMEM is given back
-  t5_commit(&sm.done);
-  mbar_wait(&sm.done, 0, a.status);
+  if (pa_elect()) t5_commit(&sm.done[t]);
+  __syncwarp();
+  wait(&sm.done[t], 0);
 }
 
-// Two warps: infinities and NaN become 0 in the blocks of V with masked keys.
+// One warp: infinities and NaN become 0 in the blocks of V with masked keys.
 template <bool HALF>
 __device__ void pa_look(const PaArgs& a, PaSmem& sm, const PaUnit& u) {
   constexpr uint32_t kCarry = HALF ? 0x04000400u : 0x00800080u;  // takes an exponent of ones into the sign's place
@@ -330,10 +370,7 @@ __device__ void pa_softmax(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_
     if (!ok) break;
     t5_after();
     uint32_t s[128];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) t5_ld32(s + 32 * k, at_s + 32 * k);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) t5_wait_ld(s + 32 * k);
+    t5_ld128(s, at_s);
     if (a.negate) {
 #pragma unroll
       for (int k = 0; k < 128; ++k) s[k] ^= 0x80000000u;
@@ -345,10 +382,16 @@ __device__ void pa_softmax(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_
       for (int k = 0; k < 128; ++k)
         if (k > last) s[k] = 0xFF800000u;
     }
-    float x[4] = {__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]), __uint_as_float(s[3])};
+    float x[8];
 #pragma unroll
-    for (int k = 4; k < 128; ++k) x[k % 4] = fmaxf(x[k % 4], __uint_as_float(s[k]));
-    const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * a.c;
+    for (int j = 0; j < 8; ++j) x[j] = max3(__uint_as_float(s[j]), __uint_as_float(s[8 + j]), __uint_as_float(s[16 + j]));
+#pragma unroll
+    for (int k = 24; k < 120; k += 16)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = max3(x[j], __uint_as_float(s[k + j]), __uint_as_float(s[k + 8 + j]));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = fmaxf(x[j], __uint_as_float(s[120 + j]));
+    const float top = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7])) * a.c;
     // ---- a new reference where the old one is too far below
     const bool up = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
     if (__any_sync(kPaFull, up)) {
@@ -363,7 +406,6 @@ __device__ void pa_softmax(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_
         for (int k = 0; k < 128; k += 32) {
           uint32_t o[32];
           t5_ld32(o, at_o + k);
-          t5_wait_ld(o);
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
           t5_st32(at_o + k, o);
@@ -371,21 +413,28 @@ __device__ void pa_softmax(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_
       }
     }
     const float base = m == -INFINITY ? 0.f : m;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint64_t c2 = f2_make(a.c, a.c), base2 = f2_make(-base, -base);
+    uint64_t sum[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       uint32_t p[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const float p0 = pa_exp2(fmaf(__uint_as_float(s[32 * k + 2 * j]), a.c, -base));
-        const float p1 = pa_exp2(fmaf(__uint_as_float(s[32 * k + 2 * j + 1]), a.c, -base));
-        sum[2 * (j & 1)] += p0;
-        sum[2 * (j & 1) + 1] += p1;
+        const float2 e = f2_get(f2_fma(f2_make(__uint_as_float(s[32 * k + 2 * j]), __uint_as_float(s[32 * k + 2 * j + 1])), c2, base2));
+        const float p0 = pa_exp2(e.x), p1 = pa_exp2(e.y);
+        sum[j & 1] = f2_add(sum[j & 1], f2_make(p0, p1));
         p[j] = pa_pack<HALF>(p0, p1);
+      }
+      if (k == kPaEarly / 32) {  // the weights of the first keys are where the tensor cores read them
+        t5_wait_st();
+        t5_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) pa_arrive(&sm.p_early[t]);
       }
       t5_st16(at_s + 16 * k, p);
     }
-    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    const float2 sums = f2_get(f2_add(sum[0], sum[1]));
+    l += sums.x + sums.y;
     t5_wait_st();
     t5_before();
     __syncwarp();
@@ -402,7 +451,6 @@ __device__ void pa_softmax(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_
   for (int k = 0; k < 128; k += 32) {
     uint32_t o[32];
     t5_ld32(o, at_o + k);
-    t5_wait_ld(o);
     if (!real) continue;
     float y[32];
 #pragma unroll
@@ -445,18 +493,19 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sm.q_full[t], 1);
       mbar_init(&sm.s_full[t], 1);
+      mbar_init(&sm.p_early[t], 4);
       mbar_init(&sm.p_full[t], 4);
       mbar_init(&sm.o_full[t], 1);
+      mbar_init(&sm.done[t], 1);
     }
     sm.odd = 0;
-    mbar_init(&sm.done, 1);
     for (int i = 0; i < kPaLook; ++i) {
       mbar_init(&sm.due[i], 1);
       mbar_init(&sm.clean[i], kPaCleaners / 32);
     }
     for (int i = 0; i < kPaSlots; ++i) {
       mbar_init(&sm.kv_full[i], 1);
-      mbar_init(&sm.kv_empty[i], 1);
+      mbar_init(&sm.kv_empty[i], u.blocks[1] > 0 ? 2 : 1);
     }
     fence_mbar_init();
   }
@@ -468,14 +517,20 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   __syncthreads();
   t5_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sm.tmem);
-  if (warp >= 10) {
-    pa_look<HALF>(a, sm, u);
-  } else if (warp == 9) {
-    if ((threadIdx.x & 31) == 0) pa_load(a, sm, u, &mq, &mk, &mv);
-  } else if (warp == 8) {
-    if ((threadIdx.x & 31) == 0) pa_mma<HALF>(a, sm, u, tmem);
-  } else {
+  // Registers go from the four warps that need few to the softmax, whose rows fill 128 of them: 256 * 208 + 128 * 88 is what
+  // 384 threads are launched with.
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     pa_softmax<HALF>(a, sm, u, tmem, warp / 4);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp < 10) {
+      pa_mma<HALF>(a, sm, u, __shfl_sync(kPaFull, tmem, 0), warp - 8);
+    } else if (warp == 10) {
+      if ((threadIdx.x & 31) == 0) pa_load(a, sm, u, &mq, &mk, &mv);
+    } else {
+      pa_look<HALF>(a, sm, u);
+    }
   }
   __syncwarp();
   t5_before();
