@@ -250,6 +250,19 @@ __device__ void pa_load(const PaArgs& a, PaSmem& sm, const PaUnit& u, const CUte
     if (u.blocks[t]) mbar_wait(&sm.q_full[t], 0, a.status);
 }
 
+// A bounded wait that the whole warp takes alike.  The first polls come back at once: a phase that is nearly over is met
+// without the time that a sleeping warp needs to wake.
+__device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+    if (__all_sync(kPaFull, ok)) return true;
+  }
+  return __all_sync(kPaFull, mbar_wait(bar, parity, status));
+}
+
 // One lane of a converged warp, always the same one.
 __device__ __forceinline__ bool pa_elect() {
   uint32_t r;
@@ -281,7 +294,7 @@ __device__ void pa_mma(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_t tm
 #pragma unroll
     for (int j = j0; j < j1; ++j) t5_mma_ts(col_o, col_s + 8 * j, v + j * (2048 / 16), id_pv, j > 0 ? 1u : add);
   };
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kPaFull, mbar_wait(bar, parity, a.status)); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return pa_wait(bar, parity, a.status); };
   // A slot is handed back by the multipliers of both tiles (of the one that has tokens), where there is a copy that waits for
   // it.  The first tile has one block less than the second at most, which no copy waits for.
   bool ok = true;
@@ -297,16 +310,17 @@ __device__ void pa_mma(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_t tm
   uint32_t phase = 0;
   for (int i = 0; i < blocks && ok; ++i) {
     const int v_slot = slot;
-    ok = wait(&sm.kv_full[v_slot], phase) && (i < u.look || wait(&sm.clean[i - u.look], 0)) && wait(&sm.p_early[t], i & 1);
+    ok = wait(&sm.kv_full[v_slot], phase);
+    if (++slot == kPaSlots) slot = 0, phase ^= 1u;
+    const int k_slot = slot;
+    ok = ok && (i + 1 >= blocks || wait(&sm.kv_full[k_slot], phase)) && (i < u.look || wait(&sm.clean[i - u.look], 0)) &&
+         wait(&sm.p_early[t], i & 1);
+    if (++slot == kPaSlots) slot = 0, phase ^= 1u;
     if (!ok) break;
     t5_after();
     if (pa_elect()) pv(v_slot, i > 0, 0, kPaEarly / 16);
     __syncwarp();
-    if (++slot == kPaSlots) slot = 0, phase ^= 1u;
-    const int k_slot = slot;
-    const uint32_t k_phase = phase;
-    if (++slot == kPaSlots) slot = 0, phase ^= 1u;
-    ok = (i + 1 >= blocks || wait(&sm.kv_full[k_slot], k_phase)) && wait(&sm.p_full[t], i & 1);
+    ok = wait(&sm.p_full[t], i & 1);
     if (!ok) break;
     t5_after();
     if (pa_elect()) {
@@ -366,7 +380,7 @@ __device__ void pa_softmax(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_
   float m = -INFINITY, l = 0.f;  // the reference, times c; the sum
   bool ok = true;
   for (int i = 0; i < blocks && ok; ++i) {
-    ok = __all_sync(kPaFull, mbar_wait(&sm.s_full[t], i & 1, a.status));
+    ok = pa_wait(&sm.s_full[t], i & 1, a.status);
     if (!ok) break;
     t5_after();
     uint32_t s[128];
@@ -392,14 +406,37 @@ __device__ void pa_softmax(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = fmaxf(x[j], __uint_as_float(s[120 + j]));
     const float top = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7])) * a.c;
-    // ---- a new reference where the old one is too far below
-    const bool up = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
-    if (__any_sync(kPaFull, up)) {
+    // Nothing below but the check needs this block's maximum, so it is found while the exponentials are taken with the
+    // reference as it is; where that turns out to be too far below, they are taken again.
+    if (i == 0) m = top;
+    const uint64_t c2 = f2_make(a.c, a.c);
+    uint64_t sum[2];
+    float base;
+    auto weights = [&](int k, uint32_t (&p)[16]) {
+      const uint64_t base2 = f2_make(-base, -base);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float2 e = f2_get(f2_fma(f2_make(__uint_as_float(s[32 * k + 2 * j]), __uint_as_float(s[32 * k + 2 * j + 1])), c2, base2));
+        const float p0 = pa_exp2(e.x), p1 = pa_exp2(e.y);
+        sum[j & 1] = f2_add(sum[j & 1], f2_make(p0, p1));
+        p[j] = pa_pack<HALF>(p0, p1);
+      }
+    };
+    uint32_t p[16];
+    while (true) {
+      base = m == -INFINITY ? 0.f : m;
+      sum[0] = sum[1] = 0;
+      weights(0, p);
+      t5_st16(at_s, p);
+      weights(1, p);
+      t5_st16(at_s + 16, p);
+      const bool up = top > m + 8.f;
+      if (!__any_sync(kPaFull, up)) break;
       const float to = up ? top : m, f = up ? pa_exp2(m - to) : 1.f;
       l *= f;
       m = to;
       if (i > 0) {
-        ok = __all_sync(kPaFull, mbar_wait(&sm.o_full[t], (i - 1) & 1, a.status));
+        ok = pa_wait(&sm.o_full[t], (i - 1) & 1, a.status);
         if (!ok) break;
         t5_after();
 #pragma unroll 1
@@ -412,27 +449,16 @@ __device__ void pa_softmax(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_
         }
       }
     }
-    const float base = m == -INFINITY ? 0.f : m;
-    const uint64_t c2 = f2_make(a.c, a.c), base2 = f2_make(-base, -base);
-    uint64_t sum[2] = {0, 0};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t p[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float2 e = f2_get(f2_fma(f2_make(__uint_as_float(s[32 * k + 2 * j]), __uint_as_float(s[32 * k + 2 * j + 1])), c2, base2));
-        const float p0 = pa_exp2(e.x), p1 = pa_exp2(e.y);
-        sum[j & 1] = f2_add(sum[j & 1], f2_make(p0, p1));
-        p[j] = pa_pack<HALF>(p0, p1);
-      }
-      if (k == kPaEarly / 32) {  // the weights of the first keys are where the tensor cores read them
-        t5_wait_st();
-        t5_before();
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) pa_arrive(&sm.p_early[t]);
-      }
-      t5_st16(at_s + 16 * k, p);
-    }
+    if (!ok) break;
+    weights(2, p);
+    // the weights of the first keys are where the tensor cores read them
+    t5_wait_st();
+    t5_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) pa_arrive(&sm.p_early[t]);
+    t5_st16(at_s + 32, p);
+    weights(3, p);
+    t5_st16(at_s + 48, p);
     const float2 sums = f2_get(f2_add(sum[0], sum[1]));
     l += sums.x + sums.y;
     t5_wait_st();
@@ -441,7 +467,7 @@ __device__ void pa_softmax(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_
     if ((threadIdx.x & 31) == 0) pa_arrive(&sm.p_full[t]);
   }
   if (blocks == 0 || !ok) return;
-  if (!__all_sync(kPaFull, mbar_wait(&sm.o_full[t], (blocks - 1) & 1, a.status))) return;
+  if (!pa_wait(&sm.o_full[t], (blocks - 1) & 1, a.status)) return;
   t5_after();
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t token_at = static_cast<int64_t>(u.first) + token;
