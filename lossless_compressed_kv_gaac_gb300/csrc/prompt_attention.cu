@@ -16,8 +16,8 @@
 // nothing in either type (rounding is relative; f16 goes to 2^16, and loses weights below 2^-25, of the reference
 // or of 2^-8 of the maximum).  Sums are fp32 over the unrounded weights; a weight's rounding, 2^-9 in bf16 and 2^-12 in
 // f16, is that of the result's type.
-// Where a mask leaves keys out, V has to be finite there, or 0 * V would be NaN: one warp looks such a block of V over
-// before it is multiplied and puts zeros in the place of what is not finite.  What of that rows may see is added
+// Where a mask leaves keys out, V has to be finite there, or 0 * V would be NaN: four warps look such a block of V over
+// before it is multiplied and put zeros in the place of what is not finite.  What of that rows may see is added
 // to them at the end, from memory.
 #include <algorithm>
 #include <cmath>
@@ -34,8 +34,8 @@ constexpr int kPaTile = 128 * kD * 2;         // bytes of a tile of Q, K or V
 constexpr int kPaHalf = kPaTile / 2;          // 64 channels of it: rows of 128 bytes, swizzled
 constexpr int kPaSlots = 5;
 constexpr int kPaSoftmax = 256;
-constexpr int kPaThreads = kPaSoftmax + 128;   // + two multipliers, the copier and one that looks V over
-constexpr int kPaCleaners = 32;
+constexpr int kPaCleaners = 128;
+constexpr int kPaThreads = kPaSoftmax + 128 + kPaCleaners;   // 128: two multipliers, the copier, one warp idle
 constexpr int kPaEarly = 64;                  // keys of a block whose weights are multiplied ahead of the others
 constexpr int kPaLook = 3;                    // blocks of a unit that have masked keys, at most
 constexpr uint32_t kPaFull = 0xFFFFFFFFu;
@@ -340,7 +340,7 @@ __device__ void pa_mma(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_t tm
   wait(&sm.done[t], 0);
 }
 
-// One warp: infinities and NaN become 0 in the blocks of V with masked keys.
+// Four warps (one takes 8,500 cycles for a block, longer than a short prompt's whole softmax): infinities and NaN become 0 in the blocks of V with masked keys.
 template <bool HALF>
 __device__ void pa_look(const PaArgs& a, PaSmem& sm, const PaUnit& u) {
   constexpr uint32_t kCarry = HALF ? 0x04000400u : 0x00800080u;  // takes an exponent of ones into the sign's place
@@ -350,7 +350,7 @@ __device__ void pa_look(const PaArgs& a, PaSmem& sm, const PaUnit& u) {
     if (!__all_sync(kPaFull, mbar_wait(&sm.due[i - u.look], 0, a.status) && mbar_wait(&sm.kv_full[pa_slot(n)], pa_phase(n), a.status)))
       return;
     uint4* const v = reinterpret_cast<uint4*>(sm.kv[pa_slot(n)]) + tid;
-#pragma unroll 8
+#pragma unroll 4
     for (int k = 0; k < kPaTile / 16; k += kPaCleaners) {
       const uint4 w = v[k];
       const uint32_t any = ((w.x & 0x7FFF7FFFu) + kCarry) | ((w.y & 0x7FFF7FFFu) + kCarry) | ((w.z & 0x7FFF7FFFu) + kCarry) |
@@ -511,6 +511,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   PaSmem& sm = *reinterpret_cast<PaSmem*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
   const int warp = threadIdx.x / 32;
+  if (threadIdx.x == 32 * 10) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mq) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mk) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mv) : "memory");
+  }
   dependent_wait();
   dependent_launch();
   PaUnit u;
@@ -543,20 +548,21 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   __syncthreads();
   t5_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sm.tmem);
-  // Registers go from the four warps that need few to the softmax, whose rows fill 128 of them: 256 * 208 + 128 * 88 is what
-  // 384 threads are launched with.
+  // Registers go from the eight warps that need few to the softmax, whose rows fill 128 of them: 256 * 208 + 128 * (56 + 40) is
+  // what 512 threads are launched with.
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     pa_softmax<HALF>(a, sm, u, tmem, warp / 4);
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp < 10) {
       pa_mma<HALF>(a, sm, u, __shfl_sync(kPaFull, tmem, 0), warp - 8);
     } else if (warp == 10) {
       if ((threadIdx.x & 31) == 0) pa_load(a, sm, u, &mq, &mk, &mv);
-    } else {
-      pa_look<HALF>(a, sm, u);
     }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    pa_look<HALF>(a, sm, u);
   }
   __syncwarp();
   t5_before();
