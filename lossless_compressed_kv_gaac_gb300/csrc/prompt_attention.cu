@@ -44,7 +44,9 @@ constexpr uint32_t kPaColS = 0, kPaColO = 256;  // TMEM columns: S of tile t at 
 struct PaArgs {
   const int32_t* cu;
   int batch, hkv, g, per;      // per: tokens of a tile
+  int g_inverse;               // row / g is row * g_inverse >> 16
   unsigned places;
+  int heads_apart;             // one kv-head after the other
   int64_t n_tokens;
   float c;                     // |scale| log2 e
   int negate;                  // scale < 0: the logits' sign turns
@@ -171,37 +173,77 @@ struct PaUnit {
   int look;       // the first block with keys that some row does not see; less than kPaLook from the last
 };
 
-// With T = 2 per tokens a unit, sequence b owns places [cu[b] / T + b, cu[b + 1] / T + b + 1): as many as it can need.
-// By a whole warp.  false: nothing to do here.
+// Units of 2 per tokens, numbered (x) by a rule that puts those with many keys first, so that the last CTAs to run are short
+// ones.  By a whole warp.  false: nothing to do here.
+//  * Up to 32 sequences, one a lane: the units that are number `level` of their sequence, for all sequences, from the highest
+//    level down.  There are C(l) = sum_b max(0, units_b - l) of level l and above.
+//  * More: from the last sequence back, and from the last unit of each.  Sequence b owns places [cu[b] / T + b, cu[b + 1] / T +
+//    b + 1), T = 2 per: as many as it can need, some are empty.
 __device__ __forceinline__ bool pa_unit(const PaArgs& a, PaUnit& u) {
   const int lane = threadIdx.x & 31;
-  const unsigned head = blockIdx.x / a.places;
-  const int64_t place = a.places - 1 - (blockIdx.x - head * a.places);  // long rows of keys first
   const int64_t unit = 2 * a.per;
-  int count = 0, bad = 0;
-#pragma unroll 4
-  for (int i0 = 0; i0 < a.batch; i0 += 32) {
-    const int i = i0 + lane;
-    bool below = false;
-    if (i < a.batch) {
-      const int64_t lo = a.cu[i], hi = a.cu[i + 1];
-      if (lo < 0 || hi < lo || hi > a.n_tokens) bad = 1;
-      below = hi / unit + i + 1 <= place;
+  int64_t lo, hi, t0;
+  if (a.batch <= 32) {
+    const int64_t from = lane < a.batch ? a.cu[lane] : 0, to = lane < a.batch ? a.cu[lane + 1] : 0;
+    if (__any_sync(kPaFull, from < 0 || to < from || to > a.n_tokens)) {
+      if (blockIdx.x == 0 && lane == 0) report(a.status, GAAC_EINVAL);
+      return false;
     }
-    count += __popc(__ballot_sync(kPaFull, below));
+    const int units = static_cast<int>((to - from + unit - 1) / unit);
+    const int total = __reduce_add_sync(kPaFull, units), top = __reduce_max_sync(kPaFull, units);
+    int x = static_cast<int>(blockIdx.x);
+    if (a.heads_apart) {
+      u.h = total > 0 ? x / total : a.hkv;
+      x -= u.h * total;
+    } else {
+      u.h = x % a.hkv;
+      x /= a.hkv;
+    }
+    if (u.h >= a.hkv || x >= total) return false;
+    int low = 0, high = top;  // C(low) > x >= C(high)
+    while (high - low > 1) {
+      const int mid = (low + high) / 2;
+      if (static_cast<int>(__reduce_add_sync(kPaFull, max(0, units - mid))) > x)
+        low = mid;
+      else
+        high = mid;
+    }
+    x -= static_cast<int>(__reduce_add_sync(kPaFull, max(0, units - high)));
+    uint32_t have = __ballot_sync(kPaFull, units > low);
+    for (; x > 0; --x) have &= have - 1u;
+    const int b = __ffs(have) - 1;
+    lo = __shfl_sync(kPaFull, from, b);
+    hi = __shfl_sync(kPaFull, to, b);
+    t0 = low * unit;
+  } else {
+    u.h = static_cast<int>(blockIdx.x / a.places);
+    const int64_t place = a.places - 1 - (blockIdx.x - u.h * a.places);
+    int count = 0, bad = 0;
+#pragma unroll 4
+    for (int i0 = 0; i0 < a.batch; i0 += 32) {
+      const int i = i0 + lane;
+      bool below = false;
+      if (i < a.batch) {
+        const int64_t from = a.cu[i], to = a.cu[i + 1];
+        if (from < 0 || to < from || to > a.n_tokens) bad = 1;
+        below = to / unit + i + 1 <= place;
+      }
+      count += __popc(__ballot_sync(kPaFull, below));
+    }
+    if (__any_sync(kPaFull, bad)) {
+      if (blockIdx.x == 0 && lane == 0) report(a.status, GAAC_EINVAL);
+      return false;
+    }
+    if (count >= a.batch) return false;
+    lo = a.cu[count];
+    hi = a.cu[count + 1];
+    const int64_t p0 = lo / unit + count;
+    t0 = (place - p0) * unit;
+    if (place < p0 || t0 >= hi - lo) return false;
   }
-  if (__any_sync(kPaFull, bad)) {
-    if (blockIdx.x == 0 && lane == 0) report(a.status, GAAC_EINVAL);
-    return false;
-  }
-  if (count >= a.batch) return false;
-  const int64_t lo = a.cu[count], hi = a.cu[count + 1], p0 = lo / unit + count;
-  const int64_t t0 = (place - p0) * unit;
-  if (place < p0 || t0 >= hi - lo) return false;
   u.first = static_cast<int>(lo);
   u.len = static_cast<int>(hi - lo);
   u.t0 = static_cast<int>(t0);
-  u.h = static_cast<int>(head);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int from = u.t0 + t * a.per;
@@ -472,16 +514,19 @@ __device__ void pa_softmax(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t token_at = static_cast<int64_t>(u.first) + token;
   const int head = u.h * a.g + row % a.g;
-  char* const out = a.out + token_at * a.out_tok + head * a.out_head;
+  // A thread has a row; stores of neighbouring channels by neighbouring threads need a turn through shared memory (stored by
+  // rows, the two tiles of a unit take 4,000 cycles).  The queries have been multiplied: a warp's rows take their place, 16-byte
+  // pieces swizzled by the row.
+  uint8_t* const stage = sm.q[t] + (row & ~31) * (2 * kD);
+  const int lane = row & 31;
 #pragma unroll 1
   for (int k = 0; k < 128; k += 32) {
     uint32_t o[32];
     t5_ld32(o, at_o + k);
-    if (!real) continue;
     float y[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) y[j] = l == 0.f ? 0.f : __uint_as_float(o[j]) * inv;
-    if (*reinterpret_cast<volatile int*>(&sm.odd)) {  // V that is not finite, of the blocks that were looked over
+    if (real && *reinterpret_cast<volatile int*>(&sm.odd)) {  // V that is not finite, of the blocks that were looked over
       for (int key = u.look * kPaKeys; key <= token; ++key) {
         const uint16_t* v = reinterpret_cast<const uint16_t*>(a.v + (static_cast<int64_t>(u.first) + key) * a.v_tok + u.h * a.v_head) + k;
 #pragma unroll 1
@@ -497,9 +542,18 @@ __device__ void pa_softmax(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<uint4*>(out + (k + 8 * j) * 2) =
+      *reinterpret_cast<uint4*>(stage + lane * (2 * kD) + (((k / 8 + j) ^ (lane & 7)) << 4)) =
           make_uint4(pa_pack<HALF>(y[8 * j], y[8 * j + 1]), pa_pack<HALF>(y[8 * j + 2], y[8 * j + 3]),
                      pa_pack<HALF>(y[8 * j + 4], y[8 * j + 5]), pa_pack<HALF>(y[8 * j + 6], y[8 * j + 7]));
+  }
+  __syncwarp();
+  const int piece = lane & 15;
+#pragma unroll 8
+  for (int k = 0; k < 16; ++k) {
+    const int r = 2 * k + (lane >> 4), of = (row & ~31) + r, tok = of * a.g_inverse >> 16;
+    if (tok < a.per && from + tok < u.len)
+      *reinterpret_cast<uint4*>(a.out + (static_cast<int64_t>(u.first) + from + tok) * a.out_tok + (u.h * a.g + of - tok * a.g) * a.out_head + piece * 16) =
+          *reinterpret_cast<const uint4*>(stage + r * (2 * kD) + ((piece ^ (r & 7)) << 4));
   }
   if (real && a.lse != nullptr) a.lse[token_at * (static_cast<int64_t>(a.hkv) * a.g) + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147181f;
 }
@@ -634,9 +688,12 @@ extern "C" int gaac_prompt_attention(const gaac_prompt* p, int dtype, int64_t n_
   a.hkv = n_kv_heads;
   a.g = n_q_heads / n_kv_heads;
   a.per = kPaRows / a.g;
+  a.g_inverse = 65536 / a.g + 1;
   const int64_t places = n_tokens / (2 * a.per) + batch;
   if (places * n_kv_heads > 0x7FFFFFFF) return GAAC_EINVAL;
   a.places = static_cast<unsigned>(places);
+  // Where K and V are too much for L2 together, the CTAs that run at a time share one kv-head's.
+  a.heads_apart = n_tokens * n_kv_heads * (2 * kD * 2) > (int64_t{64} << 20);
   a.n_tokens = n_tokens;
   // Not 0, which would make NaN of the masked logits: with the smallest number above it no finite logit moves a weight.
   a.c = scale == 0.f ? 0x1p-149f : static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634);
