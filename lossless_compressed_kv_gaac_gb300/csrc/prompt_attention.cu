@@ -548,12 +548,24 @@ __device__ void pa_softmax(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_
   }
   __syncwarp();
   const int piece = lane & 15;
-#pragma unroll 8
-  for (int k = 0; k < 16; ++k) {
-    const int r = 2 * k + (lane >> 4), of = (row & ~31) + r, tok = of * a.g_inverse >> 16;
-    if (tok < a.per && from + tok < u.len)
-      *reinterpret_cast<uint4*>(a.out + (static_cast<int64_t>(u.first) + from + tok) * a.out_tok + (u.h * a.g + of - tok * a.g) * a.out_head + piece * 16) =
-          *reinterpret_cast<const uint4*>(stage + r * (2 * kD) + ((piece ^ (r & 7)) << 4));
+  char* const out = a.out + (static_cast<int64_t>(u.first) + from) * a.out_tok + u.h * a.g * a.out_head + piece * 16;
+  const int left = min(a.per, u.len - from);
+#pragma unroll
+  for (int k0 = 0; k0 < 16; k0 += 8) {  // eight loads, then eight stores: one after the other, a step takes 225 cycles
+    uint4 y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = 2 * (k0 + k) + (lane >> 4);
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(y[k].x), "=r"(y[k].y), "=r"(y[k].z), "=r"(y[k].w) : "r"(smem_addr(stage) + r * (2 * kD) + ((piece ^ (r & 7)) << 4)));
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int of = (row & ~31) + 2 * (k0 + k) + (lane >> 4), tok = of * a.g_inverse >> 16;
+      if (tok < left)
+        asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(out + tok * a.out_tok + (of - tok * a.g) * a.out_head), "r"(y[k].x),
+                     "r"(y[k].y), "r"(y[k].z), "r"(y[k].w) : "memory");
+    }
   }
   if (real && a.lse != nullptr) a.lse[token_at * (static_cast<int64_t>(a.hkv) * a.g) + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147181f;
 }
