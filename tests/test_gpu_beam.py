@@ -123,6 +123,34 @@ def test_select_masked_and_not_finite():
 
 
 @pytest.mark.parametrize("dtype", DT)
+def test_select_runs(dtype):
+    """Rows long enough for several runs of a CTA, with many beams: what comes late is far above or below what came early,
+    masked starts, sorted rows, rows of few values."""
+    g = gen(11)
+    dt, V, rows = DT[dtype], 70001, 256
+    x = torch.randn((rows, V), generator=g, device="cuda")
+    x[0, :40000] = -INF
+    x[1, 20000:] = -INF
+    x[2, :33000] -= 900
+    x[3, 33000:] -= 900
+    x[4] = torch.arange(V, device="cuda") / 1000
+    x[5] = -torch.arange(V, device="cuda") / 1000
+    x[6] = torch.randint(0, 3, (V,), generator=g, device="cuda").float()
+    x[7] = 5
+    x[8, 8192:] = 7
+    x[9, :] = -INF
+    x[9, 69999] = -700
+    x[10, 50000] = 300
+    x[11] = (torch.arange(V, device="cuda") // 300) / 8
+    scores = -torch.rand((rows // 8, 8), generator=g, device="cuda")
+    for n_out in (8, 16, 64):
+        check(x.to(dt), scores, n_out)
+    each = torch.zeros((rows, 1), device="cuda")  # every row alone
+    flat, at = check(x.to(dt), each, 33)
+    assert torch.equal(flat, at)
+
+
+@pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("offset", [0, 1, 3])
 def test_select_strided_rows(dtype, offset):
     """Rows of a wider tensor, at every alignment; what lies beside them is not looked at."""
