@@ -13,9 +13,10 @@
 //  2. A CTA for each search adds up the sums in 64 bits, a fixed order, and merges the sorted lists: the largest of
 //     their heads is taken n_out times, by one warp.
 // Order: logits as unsigned numbers of the same order, the lower token first where they are equal; in the merge the
-// candidate in 64 bits, so that logits that differ stay apart, then the lower i * vocab + t.
+// candidate to 48 bits, so that logits that differ stay apart, then the lower i * vocab + t.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "f32x2.cuh"
 #include "kv8.cuh"
@@ -26,12 +27,13 @@ constexpr int kBmThreads = 256;
 constexpr int kBmPer = 32;                        // logits of a thread
 constexpr int kBmTile = kBmThreads * kBmPer;
 constexpr int kBmMostTiles = 4;                   // runs of a CTA
+constexpr int kBmCtasPerSm = 2;
 constexpr int kBmRoom = 512;                      // logits that are ranked by counting
 constexpr int kBmMostOut = 64;
 constexpr int kBmMostBeams = 32;
 constexpr int kBmMostVocab = 1 << 20;
 constexpr int kBmMerge = 128;                     // threads of a merge
-constexpr int kBmStage = 96 * 1024;               // bytes of lists that a merge holds in shared memory
+constexpr int kBmStage = 96 * 1024;               // bytes of candidates that a merge holds in shared memory
 constexpr uint32_t kBmAll = 0xFFFFFFFFu;
 constexpr uint32_t kBmLowest = 0x007FFFFFu;       // -infinity in the order of bm_order
 
@@ -54,12 +56,22 @@ __device__ __forceinline__ uint32_t bm_order(float x) {
   return x != x ? kBmLowest : (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float bm_value(uint32_t u) { return __uint_as_float((u & 0x80000000u) ? u & 0x7FFFFFFFu : ~u); }
-__device__ __forceinline__ uint64_t bm_order64(double x) {
-  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
-  return (b >> 63) ? ~b : b | (1ull << 63);
+// The exact sum of two numbers as the nearest one and what that leaves (Knuth).
+__device__ __forceinline__ float2 bm_two_sum(float x, float y) {
+  const float s = __fadd_rn(x, y), b = __fsub_rn(s, x);
+  return make_float2(s, __fadd_rn(__fsub_rn(x, __fsub_rn(s, b)), __fsub_rn(y, b)));
 }
-__device__ __forceinline__ double bm_value64(uint64_t u) {
-  return __longlong_as_double(static_cast<long long>((u >> 63) ? u & ~(1ull << 63) : ~u));
+// A beam's candidates: (x - peak) + hi + lo, the largest logit first so that its size takes nothing from the others.
+struct BmShift {
+  float peak, hi, lo;
+};
+// A candidate as a place in an order: its value to 48 bits, as the nearest fp32 number and what that leaves (64-bit arithmetic takes 16
+// cycles an instruction and more on this GPU).
+__device__ __forceinline__ uint64_t bm_candidate(float x, const BmShift& a) {
+  const float2 d = bm_two_sum(x, -a.peak), c = bm_two_sum(d.x, a.hi);
+  const float e = __fadd_rn(__fadd_rn(c.y, d.y), a.lo), r = __fadd_rn(c.x, e);
+  if (!(fabsf(r) < INFINITY)) return static_cast<uint64_t>(bm_order(r)) << 32;
+  return static_cast<uint64_t>(bm_order(r)) << 32 | bm_order(__fsub_rn(e, __fsub_rn(r, c.x)));
 }
 
 __device__ __forceinline__ float bm_exp2(float x) {
@@ -74,94 +86,105 @@ __device__ __forceinline__ float bm_max3(float x, float y, float z) {
   return r;
 }
 
-template <typename T>
-struct BmVec;
-template <>
-struct BmVec<float> {
-  static constexpr int kN = 4;
-  static __device__ __forceinline__ void get(uint4 w, float* f) {
-    f[0] = __uint_as_float(w.x), f[1] = __uint_as_float(w.y), f[2] = __uint_as_float(w.z), f[3] = __uint_as_float(w.w);
-  }
-  static __device__ __forceinline__ uint32_t bits(const char* p) { return *reinterpret_cast<const uint32_t*>(p); }
-};
-template <bool HALF>
-struct BmVec16 {
-  static constexpr int kN = 8;
-  static __device__ __forceinline__ void get(uint4 w, float* f) {
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 p = kv8_pair<HALF>(x[i]);
-      f[2 * i] = p.x, f[2 * i + 1] = p.y;
-    }
-  }
-  static __device__ __forceinline__ uint32_t bits(const char* p) { return *reinterpret_cast<const uint16_t*>(p); }
-};
-template <>
-struct BmVec<__half> : BmVec16<true> {};
-template <>
-struct BmVec<__nv_bfloat16> : BmVec16<false> {};
+// A thread's part of a run: kBmPer logits in loads of E each, kBmThreads * E apart.  E is 16 bytes' worth where all rows of the
+// call lie so, 2 for 16-bit logits on 4-byte boundaries, else 1: what decides is the same for all rows, so that equal rows have equal
+// sums whatever their places in memory.  (Vectors on 16-byte boundaries of every row, put together from two lanes' where a row
+// begins between them, took 230 instructions a run, single loads take 32.)
+template <typename T, int E>
+struct BmRun {
+  static constexpr bool kPacked = sizeof(T) == 2 && E >= 2;        // two logits to a word
+  static constexpr int kWords = kPacked ? kBmPer / 2 : kBmPer, kLoads = kBmPer / E;
+  uint32_t w[kWords];
 
-// A thread's tokens are the same whatever the row's alignment, so that equal rows have equal sums.  Loads lie on
-// 16-byte boundaries, the row's first logit being number `skip` of vector 0; where that is not 0, tokens are put together
-// from a vector and the next lane's (the last lane loads one more).
-template <typename T>
-struct BmRow {
-  using Vec = BmVec<T>;
-  static constexpr int kN = Vec::kN, kVecs = kBmPer / kN;
-  const char* row;
-  int skip, vocab;
-
-  __device__ __forceinline__ uint4 one(int v) const {
-    const int t = v * kN - skip;
-    const char* p = row + static_cast<int64_t>(t) * static_cast<int64_t>(sizeof(T));
-    if (t >= 0 && t + kN <= vocab) return __ldcs(reinterpret_cast<const uint4*>(p));
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (t + i >= 0 && t + i < vocab) w[i * sizeof(T) / 4] |= Vec::bits(p + i * sizeof(T)) << (i * sizeof(T) % 4 * 8);
-    return make_uint4(w[0], w[1], w[2], w[3]);
+  static __device__ __forceinline__ int token(int tile, int i) { return tile * kBmTile + (i / E * kBmThreads + static_cast<int>(threadIdx.x)) * E + i % E; }
+  static __device__ __forceinline__ uint32_t one(const char* p) {
+    if (sizeof(T) == 4) return __ldcs(reinterpret_cast<const uint32_t*>(p));
+    return __ldcs(reinterpret_cast<const uint16_t*>(p));
   }
-  // Vectors of run `tile`: one of kVecs at kBmThreads apart.
-  __device__ __forceinline__ void load(int tile, uint4 (&w)[kVecs], uint4 (&more)[kVecs]) const {
-    const int v0 = tile * (kBmTile / kN) + threadIdx.x;
+  static __device__ __forceinline__ float widen(uint32_t bits) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(bits);
+    if constexpr (std::is_same<T, __half>::value) return kv8_pair<true>(bits).x;
+    return __uint_as_float(bits << 16);
+  }
+  // Tokens of run `tile`; those behind the vocabulary are -infinity.
+  __device__ __forceinline__ void load(const char* row, int tile, int vocab) {
+    const char* const p = row + (static_cast<int64_t>(tile) * kBmTile + threadIdx.x * E) * static_cast<int64_t>(sizeof(T));
+    const uint32_t low = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00u : 0xFF80u;
+    const bool whole = (tile + 1) * kBmTile <= vocab;
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) w[j] = one(v0 + j * kBmThreads);
-    if (skip != 0 && threadIdx.x % 32 == 31) {
+    for (int j = 0; j < kLoads; ++j) {
+      const char* const q = p + j * kBmThreads * E * static_cast<int>(sizeof(T));
+      const int left = vocab - token(tile, j * E);  // of this load's tokens
+      if constexpr (E * sizeof(T) == 16) {
+        uint4 v = make_uint4(low, low, low, low);
+        if (sizeof(T) == 2) v = make_uint4(low * 0x10001u, low * 0x10001u, low * 0x10001u, low * 0x10001u);
+        uint32_t* const to = w + j * 4;
+        if (whole || left >= E) v = __ldcs(reinterpret_cast<const uint4*>(q));
+        to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+        if (!whole && left > 0 && left < E) {
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) more[j] = one(v0 + j * kBmThreads + 1);
+          for (int i = 0; i < E; ++i)
+            if (i < left) {
+              const uint32_t x = one(q + i * sizeof(T));
+              if (sizeof(T) == 4)
+                to[i % 4] = x;
+              else
+                to[i / 2] = i % 2 ? (to[i / 2] & 0xFFFFu) | x << 16 : (to[i / 2] & 0xFFFF0000u) | x;
+            }
+        }
+      } else if constexpr (E == 2) {
+        w[j] = low * 0x10001u;
+        if (whole || left >= 2)
+          w[j] = __ldcs(reinterpret_cast<const uint32_t*>(q));
+        else if (left == 1)
+          w[j] = low << 16 | one(q);
+      } else {
+        w[j] = whole || left > 0 ? one(q) : low;
+      }
     }
   }
-  // Words of vector j with the row's alignment taken out.
-  __device__ __forceinline__ void align(uint4& w, const uint4& more) const {
-    const int lane = threadIdx.x & 31, bytes = skip * static_cast<int>(sizeof(T));
-    uint32_t n[8] = {w.x, w.y, w.z, w.w, 0u, 0u, 0u, 0u};
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (kPacked) return i % 2 ? (std::is_same<T, __half>::value ? kv8_pair<true>(w[i / 2]).y : __uint_as_float(w[i / 2] & 0xFFFF0000u)) : widen(w[i / 2] & 0xFFFFu);
+    return widen(w[i]);
+  }
+  // The largest of logits 8 g .. 8 g + 7.
+  __device__ __forceinline__ float top(int g) const {
+    if constexpr (kPacked) {
+      uint32_t x = w[4 * g];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      n[4 + i] = __shfl_down_sync(kBmAll, n[i], 1);
-      if (lane == 31) n[4 + i] = i == 0 ? more.x : i == 1 ? more.y : i == 2 ? more.z : more.w;
+      for (int i = 1; i < 4; ++i) {
+        if (std::is_same<T, __half>::value)
+          asm("max.f16x2 %0, %0, %1;" : "+r"(x) : "r"(w[4 * g + i]));
+        else
+          asm("max.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(w[4 * g + i]));
+      }
+      const float2 f = kv8_pair<std::is_same<T, __half>::value>(x);
+      return fmaxf(f.x, f.y);
     }
-    if (bytes & 8) {
+    float m = fmaxf(get(8 * g), get(8 * g + 1));
 #pragma unroll
-      for (int i = 0; i < 6; ++i) n[i] = n[i + 2];
-    }
-    if (bytes & 4) {
-#pragma unroll
-      for (int i = 0; i < 5; ++i) n[i] = n[i + 1];
-    }
-    if (sizeof(T) == 2 && (bytes & 2)) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) n[i] = __funnelshift_r(n[i], n[i + 1], 16);
-    }
-    w = make_uint4(n[0], n[1], n[2], n[3]);
+    for (int i = 2; i < 8; i += 2) m = bm_max3(m, get(8 * g + i), get(8 * g + i + 1));
+    return m;
   }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kBmThreads, 2) beam_chunk_kernel(const BeamArgs a) {
-  using Row = BmRow<T>;
-  using Vec = BmVec<T>;
-  constexpr int kN = Vec::kN, kVecs = Row::kVecs, kWarps = kBmThreads / 32;
+// The k-th largest (k >= 1) of the lanes' numbers: a bitonic sort, largest first.
+__device__ __forceinline__ uint32_t bm_kth(uint32_t x, int k) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+    for (int d = size / 2; d > 0; d /= 2) {
+      const uint32_t y = __shfl_xor_sync(kBmAll, x, d);
+      x = ((lane & d) == 0) == ((lane & size) == 0) ? max(x, y) : min(x, y);
+    }
+  return __shfl_sync(kBmAll, x, k - 1);
+}
+
+template <typename T, int E>
+__global__ void __launch_bounds__(kBmThreads, kBmCtasPerSm) beam_chunk_kernel(const BeamArgs a) {
+  using Run = BmRun<T, E>;
+  constexpr int kWarps = kBmThreads / 32;
   __shared__ uint32_t rep[2 * kBmMostBeams];
   __shared__ float warp_sum[kWarps], warp_base[kWarps];
   __shared__ int count[kBmMostTiles];  // logits that reach the bound, of each run
@@ -174,44 +197,25 @@ __global__ void __launch_bounds__(kBmThreads, 2) beam_chunk_kernel(const BeamArg
   const int chunk = static_cast<int>(blockIdx.x % a.chunks);
   if (a.ended != nullptr && a.ended[beam]) return;  // its candidate needs no logits
   const char* const begin = a.logits + beam * a.row;
-  const Row row{begin, static_cast<int>((reinterpret_cast<uintptr_t>(begin) & 15u) / sizeof(T)), a.vocab};
   uint64_t* const list = a.lists + (beam * a.chunks + chunk) * a.n_out;
   const int first = chunk * a.tiles, end = min(first + a.tiles, (a.vocab + kBmTile - 1) / kBmTile);
   if (tid < kBmMostTiles) count[tid] = 0;
   float base = -INFINITY, sum = 0.f;  // this thread's sum of exp(x - base)
   float floor = 0.f;            // the bound as a number
   uint64_t least = 0;           // of a key that is still looked at
-  uint4 w[kVecs], more[kVecs];
-  row.load(first, w, more);
+  Run next;
+  next.load(begin, first, a.vocab);
   int taken = 0;  // keys in `found`, the same for all threads
 #pragma unroll 1
   for (int tile = first; tile < end; ++tile) {
-    uint4 now[kVecs];
+    const Run now = next;
+    if (tile + 1 < end) next.load(begin, tile + 1, a.vocab);
+    float m[4], top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      if (row.skip != 0) row.align(w[j], more[j]);
-      now[j] = w[j];
+    for (int g = 0; g < 4; ++g) {
+      m[g] = now.top(g);
+      top = fmaxf(top, m[g]);
     }
-    if (tile + 1 < end) row.load(tile + 1, w, more);
-    float x[kBmPer], m[kVecs];
-    const int t0 = tile * kBmTile + tid * kN;  // token of element i: t0 + i / kN * kBmThreads * kN + i % kN
-    const bool whole = (tile + 1) * kBmTile <= a.vocab;
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      Vec::get(now[j], x + j * kN);
-      if (!whole) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-          if (t0 + j * kBmThreads * kN + i >= a.vocab) x[j * kN + i] = -INFINITY;
-      }
-      m[j] = x[j * kN];
-#pragma unroll
-      for (int i = 1; i + 1 < kN; i += 2) m[j] = bm_max3(m[j], x[j * kN + i], x[j * kN + i + 1]);
-      m[j] = fmaxf(m[j], x[j * kN + kN - 1]);
-    }
-    float top = m[0];
-#pragma unroll
-    for (int j = 1; j < kVecs; ++j) top = fmaxf(top, m[j]);
     if (tile == first) {
       // ---- maxima of groups of threads; the n_out-th largest of them, by every warp
       uint32_t g = bm_order(top);
@@ -221,14 +225,13 @@ __global__ void __launch_bounds__(kBmThreads, 2) beam_chunk_kernel(const BeamArg
       if (reps == 32) g = max(g, __shfl_xor_sync(kBmAll, g, 4));
       if (lane % (kBmThreads / reps) == 0) rep[tid / (kBmThreads / reps)] = g;
       __syncthreads();
-      uint32_t r0 = rep[lane], r1 = reps == 64 ? rep[32 + lane] : 0u, bound = 0, peak = 0;
-      for (int left = a.n_out;;) {
-        bound = __reduce_max_sync(kBmAll, max(r0, r1));
-        if (peak == 0) peak = bound;
-        left -= __popc(__ballot_sync(kBmAll, r0 == bound)) + (reps == 64 ? __popc(__ballot_sync(kBmAll, r1 == bound)) : 0);
-        if (left <= 0) break;
-        if (r0 == bound) r0 = 0;
-        if (r1 == bound) r1 = 0;
+      const uint32_t r0 = rep[lane], r1 = reps == 64 ? rep[32 + lane] : 0u;
+      const uint32_t peak = __reduce_max_sync(kBmAll, max(r0, r1));
+      uint32_t bound;
+      if (reps == 32) {
+        bound = bm_kth(r0, a.n_out);
+      } else {  // as many of either half: the smaller of the two is reached by all of these
+        bound = min(bm_kth(r0, (a.n_out + 1) / 2), bm_kth(r1, (a.n_out + 1) / 2));
       }
       least = static_cast<uint64_t>(bound) << 32;
       floor = bm_value(bound);
@@ -243,26 +246,29 @@ __global__ void __launch_bounds__(kBmThreads, 2) beam_chunk_kernel(const BeamArg
     uint64_t part[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < kBmPer; i += 2) {
-      const float2 e = f2_get(f2_mul(f2_add(f2_make(x[i], x[i + 1]), minus), scale));
+      const float2 e = f2_get(f2_mul(f2_add(f2_make(now.get(i), now.get(i + 1)), minus), scale));
       part[i / 2 & 1] = f2_add(part[i / 2 & 1], f2_make(bm_exp2(e.x), bm_exp2(e.y)));
     }
     sum += f2_sum(f2_add(part[0], part[1]));
     // ---- logits that reach the bound
-    auto key = [&](int i) {
-      return static_cast<uint64_t>(bm_order(x[i])) << 32 | static_cast<uint32_t>(~(t0 + i / kN * kBmThreads * kN + i % kN));
-    };
-    auto real = [&](int i) { return t0 + i / kN * kBmThreads * kN + i % kN < a.vocab; };
+    auto key = [&](float x, int t) { return static_cast<uint64_t>(bm_order(x)) << 32 | static_cast<uint32_t>(~t); };
     if (top >= floor) {
+      uint32_t hit = 0;  // which do, a bit for each
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j)
-        if (m[j] >= floor) {
+      for (int g = 0; g < 4; ++g)
+        if (m[g] >= floor) {
 #pragma unroll
-          for (int i = j * kN; i < (j + 1) * kN; ++i)
-            if (x[i] >= floor && real(i) && key(i) >= least) {
-              const int at = taken + atomicAdd(&count[tile - first], 1);
-              if (at < kBmRoom) found[at] = key(i);
-            }
+          for (int i = 8 * g; i < 8 * g + 8; ++i) hit |= now.get(i) >= floor ? 1u << i : 0u;
         }
+      while (hit != 0u) {  // few: their logits are read again
+        const int e = __ffs(hit) - 1, t = Run::token(tile, e);
+        hit &= hit - 1u;
+        if (t >= a.vocab) continue;
+        const uint64_t k = key(Run::widen(Run::one(begin + t * static_cast<int64_t>(sizeof(T)))), t);
+        if (k < least) continue;
+        const int at = taken + atomicAdd(&count[tile - first], 1);
+        if (at < kBmRoom) found[at] = k;
+      }
     }
     __syncthreads();
     int n = taken + count[tile - first];
@@ -273,8 +279,9 @@ __global__ void __launch_bounds__(kBmThreads, 2) beam_chunk_kernel(const BeamArg
         uint64_t b = 0;
 #pragma unroll
         for (int i = 0; i < kBmPer; ++i) {
-          const uint64_t k = key(i);
-          if (real(i) && k < below && k > b) b = k;
+          const int t = Run::token(tile, i);
+          const uint64_t k = key(now.get(i), t);
+          if (t < a.vocab && k < below && k > b) b = k;
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) b = max(b, static_cast<uint64_t>(__shfl_xor_sync(kBmAll, static_cast<unsigned long long>(b), d)));
@@ -291,7 +298,7 @@ __global__ void __launch_bounds__(kBmThreads, 2) beam_chunk_kernel(const BeamArg
     }
     taken = n;
     // ---- with more runs to come: the n_out largest so far alone, and a bound that their ties behind them do not reach
-    if (tile + 1 < end && n > kBmRoom - kBmMostOut) {
+    if (tile + 1 < end && n > a.n_out && (tile == first || n > kBmRoom - kBmMostOut)) {
       uint64_t k[kBmRoom / kBmThreads];
       int rank[kBmRoom / kBmThreads];
 #pragma unroll
@@ -360,7 +367,7 @@ __device__ __forceinline__ BmHead bm_warp_best(BmHead h) {
 __global__ void __launch_bounds__(kBmMerge) beam_merge_kernel(const BeamArgs a, int staged) {
   constexpr int kWarps = kBmMerge / 32;
   extern __shared__ uint64_t stage[];
-  __shared__ double log_sum[kBmMostBeams], score[kBmMostBeams];
+  __shared__ BmShift shift[kBmMostBeams];
   __shared__ int kind[kBmMostBeams];                             // of a beam
   __shared__ uint8_t taken[kBmMostBeams * (kBmMostVocab / kBmTile)];  // of each list
   enum { kAlive, kEnded, kDead };
@@ -370,16 +377,15 @@ __global__ void __launch_bounds__(kBmMerge) beam_merge_kernel(const BeamArgs a, 
   const int64_t first = static_cast<int64_t>(blockIdx.x) * a.beams;
   const uint64_t* lists = a.lists + first * a.chunks * a.n_out;
   const int n_lists = a.beams * a.chunks;
-  if (staged)
-    for (int i = tid; i < n_lists * a.n_out; i += kBmMerge) stage[i] = __ldcg(lists + i);
   for (int l = tid; l < n_lists; l += kBmMerge) taken[l] = 0;
   for (int i = warp; i < a.beams; i += kWarps) {
     const bool end = a.ended != nullptr && a.ended[first + i];
     const float s = a.scores[first + i];
-    double log_total = 0.0;
+    double log_total = 0.0;  // of the sum relative to the peak
+    float m = 0.f;
     if (!end) {
       const float2* p = a.sums + (first + i) * a.chunks;
-      float m = -INFINITY;
+      m = -INFINITY;
       for (int j = lane; j < a.chunks; j += 32) m = fmaxf(m, __ldcg(&p[j].x));
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kBmAll, m, d));
@@ -398,67 +404,98 @@ __global__ void __launch_bounds__(kBmMerge) beam_merge_kernel(const BeamArgs a, 
       } else {
         log_total = t == 0.f ? -INFINITY : NAN;
       }
-      log_total += m;
     }
     if (lane == 0) {
-      log_sum[i] = log_total;
-      score[i] = s;
+      const double d = s - log_total;
+      shift[i] = BmShift{m, static_cast<float>(d), static_cast<float>(d - static_cast<float>(d))};
       // without a finite score and, unless it has ended, a finite sum, every candidate counts as -infinity
-      kind[i] = !isfinite(s) || (!end && !isfinite(log_total)) ? kDead : end ? kEnded : kAlive;
+      kind[i] = !isfinite(s) || (!end && !(isfinite(log_total) && isfinite(m))) ? kDead : end ? kEnded : kAlive;
     }
   }
   __syncthreads();
-  if (warp != 0) return;
-  if (staged) lists = stage;
-  // The next candidate of list l, which is of beam i.  Candidates at -infinity come in the order of their tokens; a beam that is
-  // dead has no others, one that has ended the end token before them: their lists are made up in the first chunk's place.
-  auto head = [&](int l, int i) {
-    const int k = taken[l];
+  // Candidate k of list l, which is of beam i.  Those at -infinity come in the order of their tokens; a beam that is dead has no
+  // others, one that has ended the end token before them: their lists are made up in the first chunk's place.
+  auto candidate = [&](int l, int i, int k) {
     BmHead h{0, ~0u};
     if (kind[i] != kAlive) {
       int t = k;
       if (kind[i] == kEnded) t = k == 0 ? a.end_token : k - 1 < a.end_token ? k - 1 : k;
-      if (l == i * a.chunks && k < a.n_out && t < a.vocab) {
-        h.c = bm_order64(kind[i] == kEnded && k == 0 ? score[i] : -INFINITY);
+      if (l == i * a.chunks && t < a.vocab) {
+        h.c = kind[i] == kEnded && k == 0 ? bm_candidate(0.f, shift[i]) : static_cast<uint64_t>(kBmLowest) << 32;
         h.at = static_cast<uint32_t>(i) * a.vocab + t;
       }
-    } else if (k < a.n_out) {
-      const uint64_t e = staged ? stage[l * a.n_out + k] : __ldcg(lists + static_cast<int64_t>(l) * a.n_out + k);
+    } else {
+      const uint64_t e = __ldcg(lists + static_cast<int64_t>(l) * a.n_out + k);
       if (e != 0) {
-        h.c = bm_order64(score[i] + (static_cast<double>(bm_value(static_cast<uint32_t>(e >> 32))) - log_sum[i]));
+        h.c = bm_candidate(bm_value(static_cast<uint32_t>(e >> 32)), shift[i]);
         h.at = static_cast<uint32_t>(i) * a.vocab + ~static_cast<uint32_t>(e);
       }
     }
     return h;
   };
+  // All of them at once where there is room, else one by one as they are wanted.
+  const int all = n_lists * a.n_out;
+  uint32_t* const stage_at = reinterpret_cast<uint32_t*>(stage + all);
+  if (staged) {
+#pragma unroll 4
+    for (int j = tid; j < all; j += kBmMerge) {
+      const int l = j / a.n_out;
+      const BmHead h = candidate(l, l / a.chunks, j - l * a.n_out);
+      stage[j] = h.c;
+      stage_at[j] = h.at;
+    }
+    __syncthreads();
+  }
+  if (warp != 0) return;
   BmHead mine{0, ~0u};
   int of = -1;  // the list that it is from
   auto look = [&]() {  // the best head of lists lane, lane + 32, ...
     mine = BmHead{0, ~0u};
     for (int l = lane; l < n_lists; l += 32) {
-      const BmHead h = head(l, l / a.chunks);
+      const int k = taken[l];
+      if (k == a.n_out) continue;
+      const BmHead h = staged ? BmHead{stage[l * a.n_out + k], stage_at[l * a.n_out + k]} : candidate(l, l / a.chunks, k);
       if (bm_before(h, mine)) {
         mine = h;
         of = l;
       }
     }
   };
-  look();
   uint64_t got_c[2] = {0, 0};  // choices lane and lane + 32
   uint32_t got_at[2] = {0, 0};
-  for (int r = 0; r < a.n_out; ++r) {
-    const BmHead b = bm_warp_best(mine);
+  auto keep = [&](int r, const BmHead& b) {
     if (lane == r) got_c[0] = b.c, got_at[0] = b.at;
     if (lane + 32 == r) got_c[1] = b.c, got_at[1] = b.at;
-    if (of >= 0 && mine.at == b.at) {  // places are distinct
-      ++taken[of];
-      look();
+  };
+  if (staged && n_lists <= 32) {  // a list to a lane, its next candidate in registers
+    const int from = lane * a.n_out, end = lane < n_lists ? from + a.n_out : from;
+    int at = from;
+    mine = at < end ? BmHead{stage[at], stage_at[at]} : BmHead{0, ~0u};
+    BmHead after = at + 1 < end ? BmHead{stage[at + 1], stage_at[at + 1]} : BmHead{0, ~0u};
+    for (int r = 0; r < a.n_out; ++r) {
+      const BmHead b = bm_warp_best(mine);
+      keep(r, b);
+      if (mine.at == b.at) {  // places are distinct
+        mine = after;
+        ++at;
+        after = at + 1 < end ? BmHead{stage[at + 1], stage_at[at + 1]} : BmHead{0, ~0u};
+      }
     }
-    __syncwarp();
+  } else {
+    look();
+    for (int r = 0; r < a.n_out; ++r) {
+      const BmHead b = bm_warp_best(mine);
+      keep(r, b);
+      if (of >= 0 && mine.at == b.at) {
+        ++taken[of];
+        look();
+      }
+      __syncwarp();
+    }
   }
   for (int r = lane, k = 0; r < a.n_out; r += 32, ++k) {
     const int64_t at = static_cast<int64_t>(blockIdx.x) * a.n_out + r;
-    a.out_scores[at] = static_cast<float>(bm_value64(k ? got_c[1] : got_c[0]));
+    a.out_scores[at] = bm_value(static_cast<uint32_t>((k ? got_c[1] : got_c[0]) >> 32));
     const uint32_t place = k ? got_at[1] : got_at[0];
     a.parents[at] = static_cast<int32_t>(place / a.vocab);
     a.tokens[at] = static_cast<int32_t>(place % a.vocab);
@@ -520,11 +557,16 @@ extern "C" int gaac_beam_select(const void* logits, int dtype, int64_t row_strid
   a.parents = parents;
   a.tokens = tokens;
   const dim3 grid(static_cast<unsigned>(ctas));
-  const int e = dtype == GAAC_F32   ? kv8_launch(beam_chunk_kernel<float>, grid, kBmThreads, 0, stream, a)
-                : dtype == GAAC_F16 ? kv8_launch(beam_chunk_kernel<__half>, grid, kBmThreads, 0, stream, a)
-                                    : kv8_launch(beam_chunk_kernel<__nv_bfloat16>, grid, kBmThreads, 0, stream, a);
+  // What all rows begin on, in bytes.
+  const uintptr_t lie = reinterpret_cast<uintptr_t>(logits) | (rows > 1 ? static_cast<uintptr_t>(a.row) : 0u);
+  auto launch = [&](auto* wide, auto* pairs, auto* single) {
+    return kv8_launch((lie & 15u) == 0 ? wide : (lie & 3u) == 0 ? pairs : single, grid, kBmThreads, 0, stream, a);
+  };
+  const int e = dtype == GAAC_F32   ? launch(beam_chunk_kernel<float, 4>, beam_chunk_kernel<float, 1>, beam_chunk_kernel<float, 1>)
+                : dtype == GAAC_F16 ? launch(beam_chunk_kernel<__half, 8>, beam_chunk_kernel<__half, 2>, beam_chunk_kernel<__half, 1>)
+                                    : launch(beam_chunk_kernel<__nv_bfloat16, 8>, beam_chunk_kernel<__nv_bfloat16, 2>, beam_chunk_kernel<__nv_bfloat16, 1>);
   if (e != GAAC_OK) return e;
-  const size_t bytes = static_cast<size_t>(beams) * chunks * n_out * sizeof(uint64_t);
+  const size_t bytes = static_cast<size_t>(beams) * chunks * n_out * (sizeof(uint64_t) + sizeof(uint32_t));
   const bool staged = bytes <= kBmStage;
   static bool done[64] = {false};
   int dev = 0;

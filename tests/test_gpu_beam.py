@@ -23,9 +23,10 @@ def candidates(logits, scores, ended, end_token):
     """All candidates [batch, beams, vocab] in 64 bits; NaN counts as -infinity."""
     batch, beams = scores.shape
     x = logits.double().view(batch, beams, -1)
-    lse = torch.logsumexp(x, -1)
-    dead = ~(scores.isfinite() & lse.isfinite())
-    c = scores.double()[..., None] + (x - lse[..., None])
+    top = x.amax(-1, keepdim=True)
+    total = torch.exp(x - top).sum(-1)
+    dead = ~(scores.isfinite() & total.isfinite() & top[..., 0].isfinite())
+    c = scores.double()[..., None] + ((x - top) - torch.log(total)[..., None])  # a large maximum takes nothing from the sum
     if ended is not None:
         only = torch.full_like(c, -INF)
         only[..., end_token] = scores.double()
