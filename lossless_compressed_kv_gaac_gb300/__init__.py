@@ -697,6 +697,31 @@ def _norm_pair(x, dz, out, weight, dweight, dtype, index, name):
         None if weight is None else weight.dtype
 
 
+def _norm_input(x, out, weight, dtype, index, name):
+    """_norm_pair of the forward pass: gaac_norm_tensor, the input's shape and the weights' type (None without them)."""
+    shape, st = x.shape, x.stride()
+    n = len(shape)
+    if (n != 3 and n != 4) or x.dtype != dtype or x.get_device() != index or (st[-1] != 1 and shape[-1] > 1):
+        raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim] of q's type and device, "
+                         "channels contiguous")
+    at = x.data_ptr()
+    if out is None:
+        out_at, so = at, st
+    else:
+        out_at, so = out.data_ptr(), out.stride()
+        if out.shape != shape or out.dtype != dtype or out.get_device() != index or (so[-1] != 1 and shape[-1] > 1):
+            raise ValueError(f"{name}_out must have {name}'s shape, type and device, channels contiguous")
+    w_at, w_type = 0, None
+    if weight is not None:
+        w_at, w_type, ws = weight.data_ptr(), weight.dtype, weight.shape
+        if len(ws) != 1 or ws[0] != shape[-1] or (w_type != dtype and w_type != torch.float32) or \
+                weight.get_device() != index or not weight.is_contiguous():
+            raise ValueError(f"{name}'s weights must be contiguous [dim] on its device, of its type or fp32")
+    if n == 3:
+        return _NORM_TENSOR.pack(at, 0, out_at, w_at, 0, shape[1], 0, st[0], st[1], 0, 0, 0, 0, so[0], so[1]), shape, w_type
+    return _NORM_TENSOR.pack(at, 0, out_at, w_at, 0, shape[2], st[0], st[1], st[2], 0, 0, 0, so[0], so[1], so[2]), shape, w_type
+
+
 def _norm_rope(fn, q, k, dq, dk, q_out, k_out, q_weight, k_weight, dq_weight, dk_weight, positions, turns, interleaved,
                mscale, eps, stream, *more):
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in
@@ -741,8 +766,45 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor
     """Norms of every head of q and, if given, k, x / sqrt(mean(x^2) + eps) * weight, and their rotary positions, in
     one pass.  q_weight, k_weight: [dim] of q's type or fp32, None for ones; dim is at most 256.  Everything else as
     in rope: in place by default, and not seen by autograd (qk_norm_rope_gradient is its backward)."""
-    _norm_rope("gaac_qk_norm_rope", q, k, None, None, q_out, k_out, q_weight, k_weight, None, None, positions, turns,
-               interleaved, mscale, eps, stream)
+    if (q.requires_grad or (k is not None and k.requires_grad) or (q_weight is not None and q_weight.requires_grad) or
+            (k_weight is not None and k_weight.requires_grad) or (q_out is not None and q_out.requires_grad) or
+            (k_out is not None and k_out.requires_grad)) and torch.is_grad_enabled():
+        raise ValueError("autograd does not see qk_norm_rope: call it under torch.no_grad() or from an autograd.Function")
+    dtype, index = q.dtype, q.get_device()
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError("q must be BF16, FP16 or FP32")
+    if index < 0 or positions.get_device() != index or turns.get_device() != index:
+        raise ValueError("tensors must be on one CUDA device")
+    desc, shape, w_type = _norm_input(q, q_out, q_weight, dtype, index, "q")
+    count = 1
+    if k is not None:
+        more, k_shape, k_type = _norm_input(k, k_out, k_weight, dtype, index, "k")
+        if k_shape[:-2] != shape[:-2] or k_shape[-1] != shape[-1]:
+            raise ValueError("k must have q's tokens and width")
+        if w_type is None:
+            w_type = k_type
+        elif k_type is not None and k_type != w_type:
+            raise ValueError("the weights of q and k must be of one type")
+        desc += more
+        count = 2
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k's output or weights without k")
+    turns_shape = turns.shape
+    if turns.dtype != torch.int64 or len(turns_shape) != 1 or not turns.is_contiguous():
+        raise ValueError("turns must be a contiguous int64 tensor [pairs]")
+    pos_type = positions.dtype
+    if pos_type != torch.int32 and pos_type != torch.int64:
+        raise ValueError("positions must be int32 or int64")
+    n_seq, n_tok = (1, shape[0]) if len(shape) == 3 else shape[:2]
+    pos_shape, ps = positions.shape, positions.stride()
+    if len(pos_shape) == 1 and pos_shape[0] == n_tok:
+        ps = (0, ps[0])
+    elif len(shape) != 4 or pos_shape != shape[:2]:
+        raise ValueError("positions must be [tokens] or [batch, tokens]")
+    _call("gaac_qk_norm_rope", index, stream, desc, count, code, code if w_type is None else _DTYPES[w_type], n_seq, n_tok,
+          shape[-1], 2 * turns_shape[0], positions.data_ptr(), 32 if pos_type == torch.int32 else 64, *ps, turns.data_ptr(),
+          mscale, eps, ROPE_INTERLEAVED if interleaved else 0)
 
 
 def qk_norm_rope_workspace(dim: int) -> int:

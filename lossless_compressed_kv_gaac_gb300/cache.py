@@ -7,8 +7,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (BLOCK, FP8_E4M3, HEAD_DIM, Kv8, Pools, _made_for, _stream_object, append, attention_workspace,
-               beam_select, beam_workspace, calibrate,
+from . import (BLOCK, _DTYPES, FP8_E4M3, HEAD_DIM, Kv8, Pools, _call, _made_for, _stream_object, append,
+               attention_workspace, beam_workspace, calibrate,
                decode_attention, decode_attention_bf16, decompress, encode_blocks, entry_fields, kv8_append,
                kv8_attention_workspace, kv8_compact, kv8_decode_attention, kv8_fork, kv8_release, kv8_reorder,
                kv8_reserve, new_stats, new_table)
@@ -205,15 +205,37 @@ class Beams:
         need = beam_workspace(batch, beams, vocab, self.n_out)
         if need == 0:
             raise ValueError("batch >= 1, 1 <= beams <= 32, 1 <= n_out <= 64 and 1 <= vocab <= 2^20 are wanted")
-        self.device = torch.device(device)
         self._ws = torch.empty(need, dtype=torch.uint8, device=device)
+        self.device, self._index = self._ws.device, self._ws.get_device()
+        self._rows, self._scores, self._out = (batch * beams, vocab), (batch, beams), (batch, self.n_out)
 
     def select(self, logits: torch.Tensor, scores: torch.Tensor, ended: torch.Tensor | None = None, stream=None):
         """logits [batch * beams, vocab], scores fp32 [batch, beams], ended bool or uint8 [batch, beams] -> (scores fp32,
         parents int32, tokens int32), each [batch, n_out], as beam_select says."""
-        if tuple(logits.shape) != (self.batch * self.beams, self.vocab) or tuple(scores.shape) != (self.batch, self.beams):
-            raise ValueError("logits must be [batch * beams, vocab] and scores [batch, beams]")
-        out = [_made_for(stream, self._ws.device, lambda t=t: torch.empty((self.batch, self.n_out), dtype=t, device=self._ws.device))
-               for t in (torch.float32, torch.int32, torch.int32)]
-        beam_select(logits, scores, *out, self._ws, ended, self.end_token, stream)
-        return tuple(out)
+        code, index = _DTYPES.get(logits.dtype), self._index
+        if code is None or logits.shape != self._rows or logits.get_device() != index or \
+                (logits.stride(1) != 1 and self.vocab > 1):
+            raise ValueError("logits must be BF16, FP16 or FP32 [batch * beams, vocab] on the workspace's device, tokens contiguous")
+        if scores.shape != self._scores or scores.dtype != torch.float32 or scores.get_device() != index or \
+                not scores.is_contiguous():
+            raise ValueError("scores must be contiguous fp32 [batch, beams] on the logits' device")
+        if (logits.requires_grad or scores.requires_grad) and torch.is_grad_enabled():
+            raise ValueError("autograd does not see select: call it under torch.no_grad()")
+        if ended is not None and (ended.dtype not in (torch.bool, torch.uint8) or ended.shape != self._scores or
+                                  ended.get_device() != index or not ended.is_contiguous()):
+            raise ValueError("ended must be contiguous bool or uint8 [batch, beams] on the logits' device")
+
+        def make(dtype):
+            return torch.empty(self._out, dtype=dtype, device=self.device)
+
+        if stream is None:
+            best, parents, tokens = make(torch.float32), make(torch.int32), make(torch.int32)
+        else:
+            best, parents, tokens = (_made_for(stream, self.device, lambda t=t: make(t))
+                                     for t in (torch.float32, torch.int32, torch.int32))
+        # what beam_select would do, whose checks of the results and the workspace are met here
+        _call("gaac_beam_select", index, stream, logits.data_ptr(), code,
+              logits.stride(0) if self._rows[0] > 1 else self.vocab, scores.data_ptr(), 0 if ended is None else ended.data_ptr(),
+              self.end_token, self.batch, self.beams, self.vocab, self.n_out, best.data_ptr(), parents.data_ptr(),
+              tokens.data_ptr(), self._ws.data_ptr(), self._ws.nbytes)
+        return best, parents, tokens

@@ -315,8 +315,8 @@ __global__ void __launch_bounds__(kFkThreads) kv8_fork_kernel(Kv8Dev c, const in
 constexpr int kRoThreads = 128;
 
 template <int BEAMS>
-__global__ void __launch_bounds__(kRoThreads) kv8_reorder_kernel(Kv8Dev c, const int32_t* parents, int beams, unsigned parts,
-                                                                 int32_t* status) {
+__global__ void __launch_bounds__(kRoThreads) kv8_reorder_kernel(Kv8Dev c, const int32_t* parents, int beams, unsigned table_parts,
+                                                                 unsigned parts, int32_t* status) {
   __shared__ int parent[BEAMS], len[BEAMS];  // len: what a sequence becomes; -1 where it stays as it is
   dependent_wait();
   dependent_launch();
@@ -335,9 +335,8 @@ __global__ void __launch_bounds__(kRoThreads) kv8_reorder_kernel(Kv8Dev c, const
   __syncthreads();
   int most = 0;  // open rows
   for (int i = 0; i < beams; ++i) most = max(most, len[i] % kBlock);
-  const unsigned at = part * kRoThreads + tid, step = parts * kRoThreads;
-  // ---- tables and counts: a sequence gives up its old row and holds its parent's full blocks
-  for (int64_t col = at; col < c.max_blocks; col += step) {
+  // ---- tables and counts, by the first CTAs: a sequence gives up its old row and holds its parent's full blocks
+  for (int64_t col = part * kRoThreads + tid; part < table_parts && col < c.max_blocks; col += table_parts * kRoThreads) {
     int32_t was[BEAMS], now[BEAMS];
 #pragma unroll
     for (int i = 0; i < BEAMS; ++i)
@@ -357,12 +356,12 @@ __global__ void __launch_bounds__(kRoThreads) kv8_reorder_kernel(Kv8Dev c, const
         }
       }
   }
-  // ---- open rows of every (kv-head, K|V): 16 vectors of 16 bytes each
+  // ---- open rows of every (kv-head, K|V), by the others: 16 vectors of 16 bytes each
   constexpr int kRow = kD / 8;
   uint4* const tail = reinterpret_cast<uint4*>(c.tail);
   const int64_t seq = static_cast<int64_t>(c.heads) * 2 * kBlock * kRow;
   const unsigned per = most * kRow, all = per * 2 * c.heads;
-  for (unsigned k = at; k < all; k += step) {
+  for (unsigned k = (part - table_parts) * kRoThreads + tid; part >= table_parts && k < all; k += (parts - table_parts) * kRoThreads) {
     const unsigned in = k % per;
     uint4* const t = tail + first * seq + k / per * (kBlock * kRow) + in;
     const int row = in / kRow;
@@ -562,17 +561,17 @@ extern "C" int gaac_kv8_reorder(const gaac_kv8* cache, const int32_t* parents, i
       cache->batch % beams != 0)
     return GAAC_EINVAL;
   if (beams == 1) return GAAC_OK;  // nothing has another parent
-  // CTAs of a group: as many as its open rows and table columns fill, up to eight for each SM in all.
+  // CTAs of a group: those that its table columns fill and those that its open rows may, up to four of either kind for each SM
   const int groups = cache->batch / beams;
-  const int64_t places = std::max<int64_t>(cache->max_blocks, int64_t{2} * cache->n_kv_heads * (kBlock - 1) * (kD / 8));
-  const unsigned parts = static_cast<unsigned>(
-      std::min<int64_t>((places + kRoThreads - 1) / kRoThreads, std::max<int64_t>(1, (152 * 8 + groups - 1) / groups)));
+  const int64_t most = std::max<int64_t>(1, (152 * 4 + groups - 1) / groups);
+  auto ctas = [&](int64_t places) { return static_cast<unsigned>(std::min(most, (places + kRoThreads - 1) / kRoThreads)); };
+  const unsigned table_parts = ctas(cache->max_blocks), parts = table_parts + ctas(int64_t{2} * cache->n_kv_heads * (kBlock - 1) * (kD / 8));
   const dim3 grid(parts * groups);
   const Kv8Dev c = kv8_dev(cache);
-  if (beams <= 4) return kv8_launch(kv8_reorder_kernel<4>, grid, kRoThreads, 0, stream, c, parents, beams, parts, d_status);
-  if (beams <= 8) return kv8_launch(kv8_reorder_kernel<8>, grid, kRoThreads, 0, stream, c, parents, beams, parts, d_status);
-  if (beams <= 16) return kv8_launch(kv8_reorder_kernel<16>, grid, kRoThreads, 0, stream, c, parents, beams, parts, d_status);
-  return kv8_launch(kv8_reorder_kernel<32>, grid, kRoThreads, 0, stream, c, parents, beams, parts, d_status);
+  if (beams <= 4) return kv8_launch(kv8_reorder_kernel<4>, grid, kRoThreads, 0, stream, c, parents, beams, table_parts, parts, d_status);
+  if (beams <= 8) return kv8_launch(kv8_reorder_kernel<8>, grid, kRoThreads, 0, stream, c, parents, beams, table_parts, parts, d_status);
+  if (beams <= 16) return kv8_launch(kv8_reorder_kernel<16>, grid, kRoThreads, 0, stream, c, parents, beams, table_parts, parts, d_status);
+  return kv8_launch(kv8_reorder_kernel<32>, grid, kRoThreads, 0, stream, c, parents, beams, table_parts, parts, d_status);
 }
 
 extern "C" int gaac_kv8_compact(const gaac_kv8* cache, int32_t* moved_to, void* stream) {

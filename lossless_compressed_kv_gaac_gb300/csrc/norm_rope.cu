@@ -22,9 +22,9 @@
 namespace gaac {
 
 constexpr int kNrThreads = 64;
-constexpr int kNrBatch = 2;        // heads whose loads a lane has in flight
-constexpr int kNrMost = 5;         // most heads of a walk
-constexpr int kNrCtasPerSm = 12;
+constexpr int kNrBatch = 4;        // heads whose loads a lane has in flight
+constexpr int kNrMost = 20;         // most heads of a walk
+constexpr int kNrCtasPerSm = 8;
 constexpr int kNrMaxDim = 256;
 constexpr int kNgThreads = 128;    // gradient
 constexpr int kNgCtasPerSm = 3;
@@ -221,14 +221,11 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtasPerSm) qk_norm_rope_kernel(
   char* const outq = a.t[0].out + seq * a.t[0].out_seq + tok * a.t[0].out_tok;
   char* const outk = a.t[1].out + seq * a.t[1].out_seq + tok * a.t[1].out_tok;
   RopeVec<T, V> v[kNrBatch][UPL][2];
-  auto load = [&](int h0) {
-#pragma unroll
-    for (int j = 0; j < kNrBatch; ++j) {
-      const int h = h0 + j;
-      if (h < end) L::load(v[j], h >= a.heads0 ? xk + (h - a.heads0) * a.t[1].x_head : xq + h * a.t[0].x_head, n);
-    }
+  auto load = [&](RopeVec<T, V> (&to)[UPL][2], int h) {
+    if (h < end) L::load(to, h >= a.heads0 ? xk + (h - a.heads0) * a.t[1].x_head : xq + h * a.t[0].x_head, n);
   };
-  load(first);
+#pragma unroll
+  for (int j = 0; j < kNrBatch; ++j) load(v[j], first + j);
   uint64_t s[kP], c[kP];
   L::sines(s, c, a, n, lane, seq * a.pos_seq + tok * a.pos_tok);
   // a' = r (a ca + b sb),  b' = r (b cb + a sa): the weights are part of the sines
@@ -236,7 +233,7 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtasPerSm) qk_norm_rope_kernel(
   int of = -1;  // the tensor whose weights they hold
   const float mean = 1.f / a.dim;
 #pragma unroll 1
-  for (int h0 = first;;) {
+  for (int h0 = first; h0 < end; h0 += kNrBatch) {
 #pragma unroll
     for (int j = 0; j < kNrBatch; ++j) {
       const int h = h0 + j;
@@ -255,6 +252,7 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtasPerSm) qk_norm_rope_kernel(
       }
       uint64_t x[kP], y[kP], sum = 0;
       L::unpack(v[j], x, y);
+      load(v[j], h + kNrBatch);
 #pragma unroll
       for (int q = 0; q < kP; ++q) sum = f2_fma(y[q], y[q], f2_fma(x[q], x[q], sum));
       const uint64_t r = f2_all(rsqrtf(group_sum(f2_sum(sum), a.lanes, mask) * mean + a.eps));
@@ -266,9 +264,6 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtasPerSm) qk_norm_rope_kernel(
       }
       L::store(second ? outk + (h - a.heads0) * a.t[1].out_head : outq + h * a.t[0].out_head, n, x, y);
     }
-    h0 += kNrBatch;
-    if (h0 >= end) break;
-    load(h0);
   }
 }
 
