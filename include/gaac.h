@@ -680,7 +680,7 @@ GAAC_API int gaac_kv8_fork(const gaac_kv8* cache, const int32_t* src, const int3
  * device; a parent may have several, or no, sequences).  Full blocks are shared, the open block's rows copied; a sequence
  * that changes gives its old row's pages up, reserved ones among them.  A parent outside [0, beams): GAAC_EINVAL, a parent
  * whose length is not valid: GAAC_EFORMAT, and the sequence stays as it was; a page index outside the pool in a full block
- * is taken over uncounted and reports GAAC_EFORMAT. */
+ * is taken over uncounted and reports GAAC_EFORMAT.  With one beam nothing is done. */
 GAAC_API int gaac_kv8_reorder(const gaac_kv8* cache, const int32_t* parents, int beams, int32_t* d_status, void* stream);
 
 /* Moves the held pages to the front of the pool: with n held, the lowest free page below n takes

@@ -2,16 +2,20 @@
 //
 //   c(i, t) = score_i + x_it - ln sum_u exp x_iu,   the n_out largest over (i, t), ties to the lowest i * vocab + t.
 //
-// Memory bound: the logits are read once.  Two launches:
+// The logits are read once.  Two launches:
 //  1. A CTA takes up to kBmMostTiles runs of kBmTile consecutive logits of one beam, 32 a thread and run, the next run's loads
 //     under way while one is worked on.  They give its part of the sum and its n_out largest logits: within a beam the order
 //     of the logits is that of the candidates, so no candidate beyond these can be among the chosen.  The n_out-th largest
-//     of the maxima of 32 (64 for n_out > 32) groups of threads of the first run is a bound that at least n_out logits
-//     reach; those of all runs that do (some tens of each run) are put side by side in shared memory and ranked by counting.
-//     A run that has more of them than there is room for (logits that are all alike, or sorted) is searched for its largest
-//     one at a time instead.
-//  2. A CTA for each search adds up the sums in 64 bits, a fixed order, and merges the sorted lists: the largest of
+//     of the maxima of 32 groups of threads of the first run (for n_out > 32 of 64, half of them from either half) is a bound that at
+//     least n_out logits reach.  Those of all runs that do, some tens, are put side by side in shared memory and ranked by
+//     counting, after the first run too, which leaves the others the n_out-th largest itself for a bound.  A run that has more
+//     of them than there is room for (logits that are all alike, or sorted) is searched for its largest one at a time.
+//  2. A CTA for each search adds up the sums in 64 bits, in a fixed order, and merges the sorted lists: the largest of
 //     their heads is taken n_out times, by one warp.
+// Bound by its instructions where there is much to read: 32 searches of 8 beams, 128,511 bf16 logits at odd addresses, n_out 16,
+// 66 MB: 53 us, of which 35 the first launch (550 instructions for 32 logits of a warp's lanes: 110 the sum, 100 loads and widening,
+// 150 the candidates) and 12 the merge.  What it was: every CTA one run, 104 us; odd rows put together from aligned vectors
+// of neighbouring lanes, 72 us; the bound by taking the largest maximum n_out times in place of a sort, 5 us more.
 // Order: logits as unsigned numbers of the same order, the lower token first where they are equal; in the merge the
 // candidate to 48 bits, so that logits that differ stay apart, then the lower i * vocab + t.
 #include <algorithm>
@@ -27,7 +31,7 @@ constexpr int kBmThreads = 256;
 constexpr int kBmPer = 32;                        // logits of a thread
 constexpr int kBmTile = kBmThreads * kBmPer;
 constexpr int kBmMostTiles = 4;                   // runs of a CTA
-constexpr int kBmCtasPerSm = 2;
+constexpr int kBmCtasPerSm = 2;                   // three spill: 87 us in place of 35
 constexpr int kBmRoom = 512;                      // logits that are ranked by counting
 constexpr int kBmMostOut = 64;
 constexpr int kBmMostBeams = 32;

@@ -10,6 +10,14 @@
 // a row that it walks over; a lane has two vectors of V elements of each (a unit: V pairs of the rotated part, or of the
 // channels behind it), so that the mean takes a few shuffles and V sines serve all heads of the walk.  V is 16 bytes
 // where widths and alignment allow, else one element with four units a lane.
+// Arithmetic is packed, two numbers an instruction; the forward pass multiplies the weights into the sines once for a row and
+// tensor.  Each head's registers are loaded again, with the head four further on, as soon as they are unpacked.
+// Forward, 32,768 tokens x 40 heads x 128, bf16: 120 us, 5.6 TB/s (82% of a copy).  One head at a time without packing: 148 us;
+// walks of five heads 154-179 us by CTAs an SM, of ten 129-157, of twenty 120 (8 CTAs, four heads in flight) to 163 (spills).  32
+// tokens: 4.4 us.
+// Backward, 16,384 tokens x 40 heads x 128, bf16: 116 us, 4.3 TB/s (64%); its 168 registers leave three CTAs of 128 to an SM
+// (four spill: 175 us; two with every load of two heads ahead: 185 us).  With both tensors' weights and sums in one CTA and
+// without packing 184 us.  4,999 tokens x 24 heads, fp16, half turned, interleaved: 34.8 us.
 // Sums are fp32.  dw: every lane adds up its channels over its rows, a CTA its lanes in order, a second launch the
 // CTAs in order, so the result is the same each time.
 #include <algorithm>

@@ -7,18 +7,25 @@
 // rows (row r of a tile: token r / G, head r % G), so that a tile's rows share their keys, its diagonal is short
 // and few tokens still fill a tile.  Warps:
 //  * one issues the copies (TMA): both tiles' queries, then K and V of 128 tokens in turn into a ring of five slots;
-//  * one multiplies (tcgen05.mma): S = Q K^T (128 x 128, both operands in shared memory), O += P V (P in TMEM, V's
+//  * one for each tile multiplies (tcgen05.mma): S = Q K^T (128 x 128, both operands in shared memory), O += P V (P in TMEM, V's
 //    rows as they lie, token-major).  While one tile's S is in its softmax, the tensor cores work for the other.
 //  * four warps for each tile: a thread owns a row.  S comes from TMEM into its registers; P goes back, rounded to the
 //    inputs' type, over the S it came from.  All of TMEM's 512 columns are used: S and O of both tiles.
+//  * four look over V (below).
 // Softmax: weights are 2^(c s - c m), c = |scale| log2 e, with a reference m that follows the running maximum only where
 // that has grown by more than 2^8: then O and the sum are scaled.  Until then weights are at most 2^8, which costs
-// nothing in either type (rounding is relative; f16 goes to 2^16, and loses weights below 2^-25, of the reference
-// or of 2^-8 of the maximum).  Sums are fp32 over the unrounded weights; a weight's rounding, 2^-9 in bf16 and 2^-12 in
-// f16, is that of the result's type.
+// nothing in either type (rounding is relative; f16 goes to 2^16, and loses those below 2^-25 of the reference, which is
+// at most the row's maximum).  Sums are fp32 over the unrounded weights; a weight's rounding, 2^-8 at most in bf16 and
+// 2^-11 in f16, is that of the result's type.
 // Where a mask leaves keys out, V has to be finite there, or 0 * V would be NaN: four warps look such a block of V over
 // before it is multiplied and put zeros in the place of what is not finite.  What of that rows may see is added
 // to them at the end, from memory.
+// 1 x 16,384 tokens, 32 / 8 heads, bf16: 1.39-1.42 ms, 1.55-1.58 PFLOP/s, 80% of the measured burst rate of a library product.  A block of
+// keys takes both tiles some 3,000 cycles, of which the tensor cores work 2,048: a tile's chain is its softmax (1,200-1,300 cycles: the
+// exponentials are a third of it), P V and Q K^T (768 behind the last weight) and the ways between warps (some 500).  What
+// brought it there from 1.82 ms: a multiplying warp for each tile and converged issue (1.69), packed arithmetic and three-way
+// maxima, weights multiplied in two parts, and the maximum off the chain with waits that poll (1.43).  Short prompts pay 7,000 cycles
+// a unit for its start and end (32 x 1-2,048 tokens, 16 / 8 heads, f16: 240 us, 0.8 PFLOP/s; 1 x 777: 17.5 us).
 #include <algorithm>
 #include <cmath>
 
