@@ -663,112 +663,50 @@ _NORM_TENSOR = struct.Struct("@5Pi9q")  # gaac_norm_tensor packed in one go
 assert _NORM_TENSOR.size == ctypes.sizeof(gaac_norm_tensor)
 
 
-def _head_strides(t, shape, dtype, index, name):
-    """(seq, token, head) strides of t, which must have this shape, type and device, channels contiguous."""
-    st = t.stride()
-    if t.shape != shape or t.dtype != dtype or t.get_device() != index or (st[-1] != 1 and shape[-1] > 1):
-        raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim] of q's type and device, "
-                         "channels contiguous")
-    return (0, st[0], st[1]) if len(shape) == 3 else st[:3]
-
-
-def _norm_pair(x, dz, out, weight, dweight, dtype, index, name):
-    """gaac_norm_tensor of an input, its result's gradient (or None), the output (None: in place of dz, else of x) and the
-    weights, and the weights' type (None without them)."""
-    shape = x.shape
-    if len(shape) not in (3, 4):
-        raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
-    xs = _head_strides(x, shape, dtype, index, name)
-    zs, z_at = (0, 0, 0), 0
-    if dz is not None:
-        zs, z_at = _head_strides(dz, shape, dtype, index, "d" + name), dz.data_ptr()
-    if out is None:
-        out_at, so = (x.data_ptr(), xs) if dz is None else (z_at, zs)
-    else:
-        out_at, so = out.data_ptr(), _head_strides(out, shape, dtype, index, f"{name}'s output")
-    at = [0, 0]
-    for i, (w, types) in enumerate(((weight, (dtype, torch.float32)), (dweight, (torch.float32,)))):
-        if w is not None:
-            if w.shape != shape[-1:] or w.dtype not in types or w.get_device() != index or not w.is_contiguous():
-                raise ValueError(f"{name}'s weights must be contiguous [dim] on its device, of its type or fp32, their "
-                                 "gradient fp32")
-            at[i] = w.data_ptr()
-    return _NORM_TENSOR.pack(x.data_ptr(), z_at, out_at, at[0], at[1], shape[-2], *xs, *zs, *so), \
-        None if weight is None else weight.dtype
-
-
-def _norm_input(x, out, weight, dtype, index, name):
-    """_norm_pair of the forward pass: gaac_norm_tensor, the input's shape and the weights' type (None without them)."""
+def _norm_input(x, dz, out, weight, dweight, dtype, index, name):
+    """gaac_norm_tensor of an input, its result's gradient (None in the forward pass), the output (None: in place of dz,
+    else of x) and the weights; the input's shape and the weights' type (None without them)."""
     shape, st = x.shape, x.stride()
     n = len(shape)
     if (n != 3 and n != 4) or x.dtype != dtype or x.get_device() != index or (st[-1] != 1 and shape[-1] > 1):
         raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim] of q's type and device, "
                          "channels contiguous")
-    at = x.data_ptr()
-    if out is None:
-        out_at, so = at, st
-    else:
+    at = out_at = x.data_ptr()
+    so, z_at, zs = st, 0, (0, 0, 0)
+    if dz is not None:
+        z_at, zs = dz.data_ptr(), dz.stride()
+        if dz.shape != shape or dz.dtype != dtype or dz.get_device() != index or (zs[-1] != 1 and shape[-1] > 1):
+            raise ValueError(f"d{name} must have {name}'s shape, type and device, channels contiguous")
+        out_at, so = z_at, zs
+    if out is not None:
         out_at, so = out.data_ptr(), out.stride()
         if out.shape != shape or out.dtype != dtype or out.get_device() != index or (so[-1] != 1 and shape[-1] > 1):
-            raise ValueError(f"{name}_out must have {name}'s shape, type and device, channels contiguous")
-    w_at, w_type = 0, None
+            raise ValueError(f"{name}'s output must have its shape, type and device, channels contiguous")
+    w_at, w_type, d_at = 0, None, 0
     if weight is not None:
         w_at, w_type, ws = weight.data_ptr(), weight.dtype, weight.shape
         if len(ws) != 1 or ws[0] != shape[-1] or (w_type != dtype and w_type != torch.float32) or \
                 weight.get_device() != index or not weight.is_contiguous():
             raise ValueError(f"{name}'s weights must be contiguous [dim] on its device, of its type or fp32")
+    if dweight is not None:
+        d_at, ws = dweight.data_ptr(), dweight.shape
+        if len(ws) != 1 or ws[0] != shape[-1] or dweight.dtype != torch.float32 or dweight.get_device() != index or \
+                not dweight.is_contiguous():
+            raise ValueError(f"the gradient of {name}'s weights must be contiguous fp32 [dim] on its device")
     if n == 3:
-        return _NORM_TENSOR.pack(at, 0, out_at, w_at, 0, shape[1], 0, st[0], st[1], 0, 0, 0, 0, so[0], so[1]), shape, w_type
-    return _NORM_TENSOR.pack(at, 0, out_at, w_at, 0, shape[2], st[0], st[1], st[2], 0, 0, 0, so[0], so[1], so[2]), shape, w_type
+        return _NORM_TENSOR.pack(at, z_at, out_at, w_at, d_at, shape[1], 0, st[0], st[1], 0, zs[0], zs[1], 0, so[0],
+                                 so[1]), shape, w_type
+    return _NORM_TENSOR.pack(at, z_at, out_at, w_at, d_at, shape[2], st[0], st[1], st[2], zs[0], zs[1], zs[2], so[0], so[1],
+                             so[2]), shape, w_type
 
 
 def _norm_rope(fn, q, k, dq, dk, q_out, k_out, q_weight, k_weight, dq_weight, dk_weight, positions, turns, interleaved,
                mscale, eps, stream, *more):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in
-                                       (q, k, dq, dk, q_out, k_out, q_weight, k_weight, dq_weight, dk_weight)):
-        raise ValueError("autograd does not see qk_norm_rope: call it under torch.no_grad() or from an autograd.Function")
-    dtype, index, shape = q.dtype, q.get_device(), q.shape
-    code = _DTYPES.get(dtype)
-    if code is None:
-        raise ValueError("q must be BF16, FP16 or FP32")
-    if index < 0 or positions.get_device() != index or turns.get_device() != index:
-        raise ValueError("tensors must be on one CUDA device")
-    desc, w_type = _norm_pair(q, dq, q_out, q_weight, dq_weight, dtype, index, "q")
-    count = 1
-    if k is not None:
-        if k.dim() != len(shape) or k.shape[:-2] != shape[:-2] or k.shape[-1] != shape[-1]:
-            raise ValueError("k must have q's tokens and width")
-        second, k_type = _norm_pair(k, dk, k_out, k_weight, dk_weight, dtype, index, "k")
-        if w_type is not None and k_type is not None and w_type != k_type:
-            raise ValueError("the weights of q and k must be of one type")
-        desc, count, w_type = desc + second, 2, w_type or k_type
-    elif dk is not None or k_out is not None or k_weight is not None or dk_weight is not None:
-        raise ValueError("k's gradient, output or weights without k")
-    if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
-        raise ValueError("turns must be a contiguous int64 tensor [pairs]")
-    pos_type = positions.dtype
-    if pos_type != torch.int32 and pos_type != torch.int64:
-        raise ValueError("positions must be int32 or int64")
-    n_seq, n_tok = (1, shape[0]) if len(shape) == 3 else shape[:2]
-    pos_shape, ps = positions.shape, positions.stride()
-    if len(pos_shape) == 1 and pos_shape[0] == n_tok:
-        ps = (0, ps[0])
-    elif len(shape) != 4 or pos_shape != shape[:2]:
-        raise ValueError("positions must be [tokens] or [batch, tokens]")
-    _call(fn, index, stream, desc, count, code, code if w_type is None else _DTYPES[w_type], n_seq, n_tok, shape[-1],
-          2 * turns.shape[0], positions.data_ptr(), 32 if pos_type == torch.int32 else 64, *ps, turns.data_ptr(), mscale,
-          eps, ROPE_INTERLEAVED if interleaved else 0, *more)
-
-
-def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor | None, k_weight: torch.Tensor | None,
-                 positions: torch.Tensor, turns: torch.Tensor, eps: float = 1e-6, q_out=None, k_out=None,
-                 interleaved: bool = False, mscale: float = 1.0, stream=None) -> None:
-    """Norms of every head of q and, if given, k, x / sqrt(mean(x^2) + eps) * weight, and their rotary positions, in
-    one pass.  q_weight, k_weight: [dim] of q's type or fp32, None for ones; dim is at most 256.  Everything else as
-    in rope: in place by default, and not seen by autograd (qk_norm_rope_gradient is its backward)."""
     if (q.requires_grad or (k is not None and k.requires_grad) or (q_weight is not None and q_weight.requires_grad) or
             (k_weight is not None and k_weight.requires_grad) or (q_out is not None and q_out.requires_grad) or
-            (k_out is not None and k_out.requires_grad)) and torch.is_grad_enabled():
+            (k_out is not None and k_out.requires_grad) or (dq is not None and dq.requires_grad) or
+            (dk is not None and dk.requires_grad) or (dq_weight is not None and dq_weight.requires_grad) or
+            (dk_weight is not None and dk_weight.requires_grad)) and torch.is_grad_enabled():
         raise ValueError("autograd does not see qk_norm_rope: call it under torch.no_grad() or from an autograd.Function")
     dtype, index = q.dtype, q.get_device()
     code = _DTYPES.get(dtype)
@@ -776,19 +714,19 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor
         raise ValueError("q must be BF16, FP16 or FP32")
     if index < 0 or positions.get_device() != index or turns.get_device() != index:
         raise ValueError("tensors must be on one CUDA device")
-    desc, shape, w_type = _norm_input(q, q_out, q_weight, dtype, index, "q")
+    desc, shape, w_type = _norm_input(q, dq, q_out, q_weight, dq_weight, dtype, index, "q")
     count = 1
     if k is not None:
-        more, k_shape, k_type = _norm_input(k, k_out, k_weight, dtype, index, "k")
+        second, k_shape, k_type = _norm_input(k, dk, k_out, k_weight, dk_weight, dtype, index, "k")
         if k_shape[:-2] != shape[:-2] or k_shape[-1] != shape[-1]:
             raise ValueError("k must have q's tokens and width")
         if w_type is None:
             w_type = k_type
         elif k_type is not None and k_type != w_type:
             raise ValueError("the weights of q and k must be of one type")
-        desc += more
+        desc += second
         count = 2
-    elif k_out is not None or k_weight is not None:
+    elif k_out is not None or k_weight is not None or dk_weight is not None:
         raise ValueError("k's output or weights without k")
     turns_shape = turns.shape
     if turns.dtype != torch.int64 or len(turns_shape) != 1 or not turns.is_contiguous():
@@ -802,9 +740,19 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor
         ps = (0, ps[0])
     elif len(shape) != 4 or pos_shape != shape[:2]:
         raise ValueError("positions must be [tokens] or [batch, tokens]")
-    _call("gaac_qk_norm_rope", index, stream, desc, count, code, code if w_type is None else _DTYPES[w_type], n_seq, n_tok,
-          shape[-1], 2 * turns_shape[0], positions.data_ptr(), 32 if pos_type == torch.int32 else 64, *ps, turns.data_ptr(),
-          mscale, eps, ROPE_INTERLEAVED if interleaved else 0)
+    _call(fn, index, stream, desc, count, code, code if w_type is None else _DTYPES[w_type], n_seq, n_tok, shape[-1],
+          2 * turns_shape[0], positions.data_ptr(), 32 if pos_type == torch.int32 else 64, *ps, turns.data_ptr(), mscale,
+          eps, ROPE_INTERLEAVED if interleaved else 0, *more)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor | None, k_weight: torch.Tensor | None,
+                 positions: torch.Tensor, turns: torch.Tensor, eps: float = 1e-6, q_out=None, k_out=None,
+                 interleaved: bool = False, mscale: float = 1.0, stream=None) -> None:
+    """Norms of every head of q and, if given, k, x / sqrt(mean(x^2) + eps) * weight, and their rotary positions, in
+    one pass.  q_weight, k_weight: [dim] of q's type or fp32, None for ones; dim is at most 256.  Everything else as
+    in rope: in place by default, and not seen by autograd (qk_norm_rope_gradient is its backward)."""
+    _norm_rope("gaac_qk_norm_rope", q, k, None, None, q_out, k_out, q_weight, k_weight, None, None, positions, turns,
+               interleaved, mscale, eps, stream)
 
 
 def qk_norm_rope_workspace(dim: int) -> int:
@@ -1042,7 +990,8 @@ def kv8_compact(cache: Kv8, moved_to: torch.Tensor, stream=None) -> None:
 
 # ---------------------------------------------------------------- beam search
 def beam_workspace(batch: int, beams: int, vocab: int, n_out: int) -> int:
-    """Bytes of beam_select's workspace, of any contents; 0 for sizes that it does not take."""
+    """Bytes of beam_select's workspace, which is zero before the first call and serves calls of these sizes; 0 for sizes
+    that it does not take."""
     return lib().gaac_beam_workspace(batch, beams, vocab, n_out)
 
 
@@ -1054,7 +1003,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, out_scores: torch.Te
     contiguous (rows may be strided); scores: fp32 [batch, beams].  out_scores (fp32), parents (the beam i) and tokens
     (int32): [batch, n_out].  ended: bool or uint8 [batch, beams]; such a beam has one candidate, end_token, at its score.
     A beam whose score or sum of exponentials is not finite has none; where there are too few, the lowest of the others
-    follow at -infinity.  workspace: beam_workspace(...) bytes, not shared by calls that may overlap on the GPU."""
+    follow at -infinity.  workspace: beam_workspace(...) bytes, zero before the first call, for calls of the same sizes that do
+    not overlap on the GPU."""
     index = logits.get_device()
     code = _DTYPES.get(logits.dtype)
     if torch.is_grad_enabled() and (logits.requires_grad or scores.requires_grad):

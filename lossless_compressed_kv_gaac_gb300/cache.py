@@ -205,7 +205,7 @@ class Beams:
         need = beam_workspace(batch, beams, vocab, self.n_out)
         if need == 0:
             raise ValueError("batch >= 1, 1 <= beams <= 32, 1 <= n_out <= 64 and 1 <= vocab <= 2^20 are wanted")
-        self._ws = torch.empty(need, dtype=torch.uint8, device=device)
+        self._ws = torch.zeros(need, dtype=torch.uint8, device=device)
         self.device, self._index = self._ws.device, self._ws.get_device()
         self._rows, self._scores, self._out = (batch * beams, vocab), (batch, beams), (batch, self.n_out)
 

@@ -36,8 +36,7 @@ constexpr int kBmRoom = 512;                      // logits that are ranked by c
 constexpr int kBmMostOut = 64;
 constexpr int kBmMostBeams = 32;
 constexpr int kBmMostVocab = 1 << 20;
-constexpr int kBmMerge = 128;                     // threads of a merge
-constexpr int kBmStage = 96 * 1024;               // bytes of candidates that a merge holds in shared memory
+constexpr int kBmStage = 36 * 1024;               // bytes of candidates that a merge holds in shared memory
 constexpr uint32_t kBmAll = 0xFFFFFFFFu;
 constexpr uint32_t kBmLowest = 0x007FFFFFu;       // -infinity in the order of bm_order
 
@@ -48,6 +47,8 @@ struct BeamArgs {
   const uint8_t* ended;       // nullptr: none
   int end_token, beams, vocab, n_out, chunks, tiles;  // chunks of a beam, of so many runs each
   float2* sums;               // [beam][chunk]: maximum, sum of exp(x - maximum)
+  int32_t* tickets;           // [search]: CTAs that are done, 0 between calls
+  int staged;                 // a merge's candidates fit in shared memory
   uint64_t* lists;            // [beam][chunk][n_out]: order of the logit << 32 | ~token, descending; 0 behind the last
   float* out_scores;
   int32_t* parents;
@@ -88,6 +89,160 @@ __device__ __forceinline__ float bm_max3(float x, float y, float z) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
+}
+
+// The head of a list as a candidate: its place in the order (0: none), and i * vocab + t.
+struct BmHead {
+  uint64_t c;
+  uint32_t at;
+};
+__device__ __forceinline__ bool bm_before(const BmHead& x, const BmHead& y) { return x.c > y.c || (x.c == y.c && x.at < y.at); }
+
+// The largest of a warp's heads, in every lane.
+__device__ __forceinline__ BmHead bm_warp_best(BmHead h) {
+  const uint32_t hi = static_cast<uint32_t>(h.c >> 32), lo = static_cast<uint32_t>(h.c);
+  const uint32_t mh = __reduce_max_sync(kBmAll, hi);
+  const uint32_t ml = __reduce_max_sync(kBmAll, hi == mh ? lo : 0u);
+  const uint32_t at = __reduce_min_sync(kBmAll, hi == mh && lo == ml ? h.at : ~0u);
+  return BmHead{static_cast<uint64_t>(mh) << 32 | ml, at};
+}
+
+// The choice of one search, by the CTA that was the last to read its logits.
+__device__ __noinline__ void beam_merge(const BeamArgs& a, int64_t search) {
+  constexpr int kWarps = kBmThreads / 32;
+  const bool staged = a.staged;
+  extern __shared__ uint64_t stage[];
+  __shared__ BmShift shift[kBmMostBeams];
+  __shared__ int kind[kBmMostBeams];                             // of a beam
+  __shared__ uint8_t taken[kBmMostBeams * (kBmMostVocab / kBmTile)];  // of each list
+  enum { kAlive, kEnded, kDead };
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t first = search * a.beams;
+  const uint64_t* lists = a.lists + first * a.chunks * a.n_out;
+  const int n_lists = a.beams * a.chunks;
+  for (int l = tid; l < n_lists; l += kBmThreads) taken[l] = 0;
+  for (int i = warp; i < a.beams; i += kWarps) {
+    const bool end = a.ended != nullptr && a.ended[first + i];
+    const float s = a.scores[first + i];
+    double log_total = 0.0;  // of the sum relative to the peak
+    float m = 0.f;
+    if (!end) {
+      const float2* p = a.sums + (first + i) * a.chunks;
+      m = -INFINITY;
+      for (int j = lane; j < a.chunks; j += 32) m = fmaxf(m, __ldcg(&p[j].x));
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kBmAll, m, d));
+      double total = 0.0;
+      for (int j = lane; j < a.chunks; j += 32) {
+        const float2 v = __ldcg(p + j);
+        total += static_cast<double>(v.y) * static_cast<double>(expf(v.x - m));
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(kBmAll, total, d);
+      // ln(total) from its exponent in 64 bits and the fp32 logarithm of its mantissa in [0.75, 1.5), which is off by 2^-25
+      const float t = static_cast<float>(total);
+      if (t > 0.f && t < INFINITY) {
+        const int e = static_cast<int>((__float_as_uint(t) - 0x3F400000u)) >> 23;
+        log_total = e * 0.693147180559945309 + static_cast<double>(logf(__uint_as_float(__float_as_uint(t) - (static_cast<uint32_t>(e) << 23))));
+      } else {
+        log_total = t == 0.f ? -INFINITY : NAN;
+      }
+    }
+    if (lane == 0) {
+      const double d = s - log_total;
+      shift[i] = BmShift{m, static_cast<float>(d), static_cast<float>(d - static_cast<float>(d))};
+      // without a finite score and, unless it has ended, a finite sum, every candidate counts as -infinity
+      kind[i] = !isfinite(s) || (!end && !(isfinite(log_total) && isfinite(m))) ? kDead : end ? kEnded : kAlive;
+    }
+  }
+  __syncthreads();
+  // Candidate k of list l, which is of beam i.  Those at -infinity come in the order of their tokens; a beam that is dead has no
+  // others, one that has ended the end token before them: their lists are made up in the first chunk's place.
+  auto candidate = [&](int l, int i, int k) {
+    BmHead h{0, ~0u};
+    if (kind[i] != kAlive) {
+      int t = k;
+      if (kind[i] == kEnded) t = k == 0 ? a.end_token : k - 1 < a.end_token ? k - 1 : k;
+      if (l == i * a.chunks && t < a.vocab) {
+        h.c = kind[i] == kEnded && k == 0 ? bm_candidate(0.f, shift[i]) : static_cast<uint64_t>(kBmLowest) << 32;
+        h.at = static_cast<uint32_t>(i) * a.vocab + t;
+      }
+    } else {
+      const uint64_t e = __ldcg(lists + static_cast<int64_t>(l) * a.n_out + k);
+      if (e != 0) {
+        h.c = bm_candidate(bm_value(static_cast<uint32_t>(e >> 32)), shift[i]);
+        h.at = static_cast<uint32_t>(i) * a.vocab + ~static_cast<uint32_t>(e);
+      }
+    }
+    return h;
+  };
+  // All of them at once where there is room, else one by one as they are wanted.
+  const int all = n_lists * a.n_out;
+  uint32_t* const stage_at = reinterpret_cast<uint32_t*>(stage + all);
+  if (staged) {
+#pragma unroll 4
+    for (int j = tid; j < all; j += kBmThreads) {
+      const int l = j / a.n_out;
+      const BmHead h = candidate(l, l / a.chunks, j - l * a.n_out);
+      stage[j] = h.c;
+      stage_at[j] = h.at;
+    }
+    __syncthreads();
+  }
+  if (warp != 0) return;
+  BmHead mine{0, ~0u};
+  int of = -1;  // the list that it is from
+  auto look = [&]() {  // the best head of lists lane, lane + 32, ...
+    mine = BmHead{0, ~0u};
+    for (int l = lane; l < n_lists; l += 32) {
+      const int k = taken[l];
+      if (k == a.n_out) continue;
+      const BmHead h = staged ? BmHead{stage[l * a.n_out + k], stage_at[l * a.n_out + k]} : candidate(l, l / a.chunks, k);
+      if (bm_before(h, mine)) {
+        mine = h;
+        of = l;
+      }
+    }
+  };
+  uint64_t got_c[2] = {0, 0};  // choices lane and lane + 32
+  uint32_t got_at[2] = {0, 0};
+  auto keep = [&](int r, const BmHead& b) {
+    if (lane == r) got_c[0] = b.c, got_at[0] = b.at;
+    if (lane + 32 == r) got_c[1] = b.c, got_at[1] = b.at;
+  };
+  if (staged && n_lists <= 32) {  // a list to a lane, its next candidate in registers
+    const int from = lane * a.n_out, end = lane < n_lists ? from + a.n_out : from;
+    int at = from;
+    mine = at < end ? BmHead{stage[at], stage_at[at]} : BmHead{0, ~0u};
+    BmHead after = at + 1 < end ? BmHead{stage[at + 1], stage_at[at + 1]} : BmHead{0, ~0u};
+    for (int r = 0; r < a.n_out; ++r) {
+      const BmHead b = bm_warp_best(mine);
+      keep(r, b);
+      if (mine.at == b.at) {  // places are distinct
+        mine = after;
+        ++at;
+        after = at + 1 < end ? BmHead{stage[at + 1], stage_at[at + 1]} : BmHead{0, ~0u};
+      }
+    }
+  } else {
+    look();
+    for (int r = 0; r < a.n_out; ++r) {
+      const BmHead b = bm_warp_best(mine);
+      keep(r, b);
+      if (of >= 0 && mine.at == b.at) {
+        ++taken[of];
+        look();
+      }
+      __syncwarp();
+    }
+  }
+  for (int r = lane, k = 0; r < a.n_out; r += 32, ++k) {
+    const int64_t at = search * a.n_out + r;
+    a.out_scores[at] = bm_value(static_cast<uint32_t>((k ? got_c[1] : got_c[0]) >> 32));
+    const uint32_t place = k ? got_at[1] : got_at[0];
+    a.parents[at] = static_cast<int32_t>(place / a.vocab);
+    a.tokens[at] = static_cast<int32_t>(place % a.vocab);
+  }
 }
 
 // A thread's part of a run: kBmPer logits in loads of E each, kBmThreads * E apart.  E is 16 bytes' worth where all rows of the
@@ -194,12 +349,26 @@ __global__ void __launch_bounds__(kBmThreads, kBmCtasPerSm) beam_chunk_kernel(co
   __shared__ int count[kBmMostTiles];  // logits that reach the bound, of each run
   __shared__ uint64_t found[kBmRoom];
   __shared__ uint64_t best[2][kWarps];
+  __shared__ int last;
   dependent_wait();
   dependent_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t beam = blockIdx.x / a.chunks;
   const int chunk = static_cast<int>(blockIdx.x % a.chunks);
-  if (a.ended != nullptr && a.ended[beam]) return;  // its candidate needs no logits
+  const int64_t search = beam / a.beams;
+  // One more CTA of the search is done; the last one makes the choice.  Everybody's stores come before thread 0's release by the
+  // barrier, and what the others released before what follows.
+  auto done = [&]() {
+    __syncthreads();
+    if (tid == 0) {
+      const unsigned all = static_cast<unsigned>(a.beams) * a.chunks;
+      last = kv8_atomic_add_acq_rel(a.tickets + search, 1u) == all - 1;
+      if (last) a.tickets[search] = 0;
+    }
+    __syncthreads();
+    if (last) beam_merge(a, search);
+  };
+  if (a.ended != nullptr && a.ended[beam]) return done();  // its candidate needs no logits
   const char* const begin = a.logits + beam * a.row;
   uint64_t* const list = a.lists + (beam * a.chunks + chunk) * a.n_out;
   const int first = chunk * a.tiles, end = min(first + a.tiles, (a.vocab + kBmTile - 1) / kBmTile);
@@ -350,160 +519,7 @@ __global__ void __launch_bounds__(kBmThreads, kBmCtasPerSm) beam_chunk_kernel(co
     for (int i = 0; i < kWarps; ++i) sum += warp_base[i] == high ? warp_sum[i] : warp_sum[i] * bm_exp2((warp_base[i] - high) * 1.44269504f);
     a.sums[beam * a.chunks + chunk] = make_float2(high, sum);
   }
-}
-
-// The head of a list as a candidate: its place in the order (0: none), and i * vocab + t.
-struct BmHead {
-  uint64_t c;
-  uint32_t at;
-};
-__device__ __forceinline__ bool bm_before(const BmHead& x, const BmHead& y) { return x.c > y.c || (x.c == y.c && x.at < y.at); }
-
-// The largest of a warp's heads, in every lane.
-__device__ __forceinline__ BmHead bm_warp_best(BmHead h) {
-  const uint32_t hi = static_cast<uint32_t>(h.c >> 32), lo = static_cast<uint32_t>(h.c);
-  const uint32_t mh = __reduce_max_sync(kBmAll, hi);
-  const uint32_t ml = __reduce_max_sync(kBmAll, hi == mh ? lo : 0u);
-  const uint32_t at = __reduce_min_sync(kBmAll, hi == mh && lo == ml ? h.at : ~0u);
-  return BmHead{static_cast<uint64_t>(mh) << 32 | ml, at};
-}
-
-__global__ void __launch_bounds__(kBmMerge) beam_merge_kernel(const BeamArgs a, int staged) {
-  constexpr int kWarps = kBmMerge / 32;
-  extern __shared__ uint64_t stage[];
-  __shared__ BmShift shift[kBmMostBeams];
-  __shared__ int kind[kBmMostBeams];                             // of a beam
-  __shared__ uint8_t taken[kBmMostBeams * (kBmMostVocab / kBmTile)];  // of each list
-  enum { kAlive, kEnded, kDead };
-  dependent_wait();
-  dependent_launch();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * a.beams;
-  const uint64_t* lists = a.lists + first * a.chunks * a.n_out;
-  const int n_lists = a.beams * a.chunks;
-  for (int l = tid; l < n_lists; l += kBmMerge) taken[l] = 0;
-  for (int i = warp; i < a.beams; i += kWarps) {
-    const bool end = a.ended != nullptr && a.ended[first + i];
-    const float s = a.scores[first + i];
-    double log_total = 0.0;  // of the sum relative to the peak
-    float m = 0.f;
-    if (!end) {
-      const float2* p = a.sums + (first + i) * a.chunks;
-      m = -INFINITY;
-      for (int j = lane; j < a.chunks; j += 32) m = fmaxf(m, __ldcg(&p[j].x));
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kBmAll, m, d));
-      double total = 0.0;
-      for (int j = lane; j < a.chunks; j += 32) {
-        const float2 v = __ldcg(p + j);
-        total += static_cast<double>(v.y) * static_cast<double>(expf(v.x - m));
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(kBmAll, total, d);
-      // ln(total) from its exponent in 64 bits and the fp32 logarithm of its mantissa in [0.75, 1.5), which is off by 2^-25
-      const float t = static_cast<float>(total);
-      if (t > 0.f && t < INFINITY) {
-        const int e = static_cast<int>((__float_as_uint(t) - 0x3F400000u)) >> 23;
-        log_total = e * 0.693147180559945309 + static_cast<double>(logf(__uint_as_float(__float_as_uint(t) - (static_cast<uint32_t>(e) << 23))));
-      } else {
-        log_total = t == 0.f ? -INFINITY : NAN;
-      }
-    }
-    if (lane == 0) {
-      const double d = s - log_total;
-      shift[i] = BmShift{m, static_cast<float>(d), static_cast<float>(d - static_cast<float>(d))};
-      // without a finite score and, unless it has ended, a finite sum, every candidate counts as -infinity
-      kind[i] = !isfinite(s) || (!end && !(isfinite(log_total) && isfinite(m))) ? kDead : end ? kEnded : kAlive;
-    }
-  }
-  __syncthreads();
-  // Candidate k of list l, which is of beam i.  Those at -infinity come in the order of their tokens; a beam that is dead has no
-  // others, one that has ended the end token before them: their lists are made up in the first chunk's place.
-  auto candidate = [&](int l, int i, int k) {
-    BmHead h{0, ~0u};
-    if (kind[i] != kAlive) {
-      int t = k;
-      if (kind[i] == kEnded) t = k == 0 ? a.end_token : k - 1 < a.end_token ? k - 1 : k;
-      if (l == i * a.chunks && t < a.vocab) {
-        h.c = kind[i] == kEnded && k == 0 ? bm_candidate(0.f, shift[i]) : static_cast<uint64_t>(kBmLowest) << 32;
-        h.at = static_cast<uint32_t>(i) * a.vocab + t;
-      }
-    } else {
-      const uint64_t e = __ldcg(lists + static_cast<int64_t>(l) * a.n_out + k);
-      if (e != 0) {
-        h.c = bm_candidate(bm_value(static_cast<uint32_t>(e >> 32)), shift[i]);
-        h.at = static_cast<uint32_t>(i) * a.vocab + ~static_cast<uint32_t>(e);
-      }
-    }
-    return h;
-  };
-  // All of them at once where there is room, else one by one as they are wanted.
-  const int all = n_lists * a.n_out;
-  uint32_t* const stage_at = reinterpret_cast<uint32_t*>(stage + all);
-  if (staged) {
-#pragma unroll 4
-    for (int j = tid; j < all; j += kBmMerge) {
-      const int l = j / a.n_out;
-      const BmHead h = candidate(l, l / a.chunks, j - l * a.n_out);
-      stage[j] = h.c;
-      stage_at[j] = h.at;
-    }
-    __syncthreads();
-  }
-  if (warp != 0) return;
-  BmHead mine{0, ~0u};
-  int of = -1;  // the list that it is from
-  auto look = [&]() {  // the best head of lists lane, lane + 32, ...
-    mine = BmHead{0, ~0u};
-    for (int l = lane; l < n_lists; l += 32) {
-      const int k = taken[l];
-      if (k == a.n_out) continue;
-      const BmHead h = staged ? BmHead{stage[l * a.n_out + k], stage_at[l * a.n_out + k]} : candidate(l, l / a.chunks, k);
-      if (bm_before(h, mine)) {
-        mine = h;
-        of = l;
-      }
-    }
-  };
-  uint64_t got_c[2] = {0, 0};  // choices lane and lane + 32
-  uint32_t got_at[2] = {0, 0};
-  auto keep = [&](int r, const BmHead& b) {
-    if (lane == r) got_c[0] = b.c, got_at[0] = b.at;
-    if (lane + 32 == r) got_c[1] = b.c, got_at[1] = b.at;
-  };
-  if (staged && n_lists <= 32) {  // a list to a lane, its next candidate in registers
-    const int from = lane * a.n_out, end = lane < n_lists ? from + a.n_out : from;
-    int at = from;
-    mine = at < end ? BmHead{stage[at], stage_at[at]} : BmHead{0, ~0u};
-    BmHead after = at + 1 < end ? BmHead{stage[at + 1], stage_at[at + 1]} : BmHead{0, ~0u};
-    for (int r = 0; r < a.n_out; ++r) {
-      const BmHead b = bm_warp_best(mine);
-      keep(r, b);
-      if (mine.at == b.at) {  // places are distinct
-        mine = after;
-        ++at;
-        after = at + 1 < end ? BmHead{stage[at + 1], stage_at[at + 1]} : BmHead{0, ~0u};
-      }
-    }
-  } else {
-    look();
-    for (int r = 0; r < a.n_out; ++r) {
-      const BmHead b = bm_warp_best(mine);
-      keep(r, b);
-      if (of >= 0 && mine.at == b.at) {
-        ++taken[of];
-        look();
-      }
-      __syncwarp();
-    }
-  }
-  for (int r = lane, k = 0; r < a.n_out; r += 32, ++k) {
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * a.n_out + r;
-    a.out_scores[at] = bm_value(static_cast<uint32_t>((k ? got_c[1] : got_c[0]) >> 32));
-    const uint32_t place = k ? got_at[1] : got_at[0];
-    a.parents[at] = static_cast<int32_t>(place / a.vocab);
-    a.tokens[at] = static_cast<int32_t>(place % a.vocab);
-  }
+  done();
 }
 
 // Runs of a CTA: as many as leave every SM three CTAs.
@@ -523,7 +539,8 @@ using namespace gaac;
 extern "C" size_t gaac_beam_workspace(int batch, int beams, int vocab, int n_out) {
   if (batch < 1 || beams < 1 || beams > kBmMostBeams || vocab < 1 || vocab > kBmMostVocab || n_out < 1 || n_out > kBmMostOut) return 0;
   const size_t lists = static_cast<size_t>(batch) * beams * beam_chunks(static_cast<int64_t>(batch) * beams, vocab);
-  return (lists * (sizeof(float2) + n_out * sizeof(uint64_t)) + 15) & ~static_cast<size_t>(15);
+  const size_t tickets = (static_cast<size_t>(batch) + 3) / 4 * 4 * sizeof(int32_t);
+  return (tickets + lists * (sizeof(float2) + n_out * sizeof(uint64_t)) + 15) & ~static_cast<size_t>(15);
 }
 
 extern "C" int gaac_beam_select(const void* logits, int dtype, int64_t row_stride, const float* scores, const uint8_t* ended,
@@ -555,7 +572,8 @@ extern "C" int gaac_beam_select(const void* logits, int dtype, int64_t row_strid
   a.n_out = n_out;
   a.chunks = chunks;
   a.tiles = beam_tiles(rows, vocab);
-  a.lists = static_cast<uint64_t*>(workspace);
+  a.tickets = static_cast<int32_t*>(workspace);
+  a.lists = reinterpret_cast<uint64_t*>(a.tickets + (batch + 3) / 4 * 4);
   a.sums = reinterpret_cast<float2*>(a.lists + ctas * n_out);
   a.out_scores = out_scores;
   a.parents = parents;
@@ -563,21 +581,12 @@ extern "C" int gaac_beam_select(const void* logits, int dtype, int64_t row_strid
   const dim3 grid(static_cast<unsigned>(ctas));
   // What all rows begin on, in bytes.
   const uintptr_t lie = reinterpret_cast<uintptr_t>(logits) | (rows > 1 ? static_cast<uintptr_t>(a.row) : 0u);
-  auto launch = [&](auto* wide, auto* pairs, auto* single) {
-    return kv8_launch((lie & 15u) == 0 ? wide : (lie & 3u) == 0 ? pairs : single, grid, kBmThreads, 0, stream, a);
-  };
-  const int e = dtype == GAAC_F32   ? launch(beam_chunk_kernel<float, 4>, beam_chunk_kernel<float, 1>, beam_chunk_kernel<float, 1>)
-                : dtype == GAAC_F16 ? launch(beam_chunk_kernel<__half, 8>, beam_chunk_kernel<__half, 2>, beam_chunk_kernel<__half, 1>)
-                                    : launch(beam_chunk_kernel<__nv_bfloat16, 8>, beam_chunk_kernel<__nv_bfloat16, 2>, beam_chunk_kernel<__nv_bfloat16, 1>);
-  if (e != GAAC_OK) return e;
   const size_t bytes = static_cast<size_t>(beams) * chunks * n_out * (sizeof(uint64_t) + sizeof(uint32_t));
-  const bool staged = bytes <= kBmStage;
-  static bool done[64] = {false};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GAAC_ECUDA;
-  if (!done[dev]) {
-    if (cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBmStage) != cudaSuccess) return GAAC_ECUDA;
-    done[dev] = true;
-  }
-  return kv8_launch(beam_merge_kernel, dim3(batch), kBmMerge, staged ? bytes : 0, stream, a, staged ? 1 : 0);
+  a.staged = bytes <= kBmStage;
+  auto launch = [&](auto* wide, auto* pairs, auto* single) {
+    return kv8_launch((lie & 15u) == 0 ? wide : (lie & 3u) == 0 ? pairs : single, grid, kBmThreads, a.staged ? bytes : 0, stream, a);
+  };
+  return dtype == GAAC_F32   ? launch(beam_chunk_kernel<float, 4>, beam_chunk_kernel<float, 1>, beam_chunk_kernel<float, 1>)
+         : dtype == GAAC_F16 ? launch(beam_chunk_kernel<__half, 8>, beam_chunk_kernel<__half, 2>, beam_chunk_kernel<__half, 1>)
+                             : launch(beam_chunk_kernel<__nv_bfloat16, 8>, beam_chunk_kernel<__nv_bfloat16, 2>, beam_chunk_kernel<__nv_bfloat16, 1>);
 }

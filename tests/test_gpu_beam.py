@@ -169,7 +169,6 @@ def test_select_in_a_graph_and_on_another_stream():
     logits = torch.randn((8, 30000), generator=g, device="cuda").bfloat16()
     scores = -torch.rand((2, 4), generator=g, device="cuda")
     b = Beams(2, 4, 30000)
-    b._ws.fill_(255)
     want = b.select(logits, scores)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -182,6 +181,9 @@ def test_select_in_a_graph_and_on_another_stream():
     logits.copy_(torch.randn((8, 30000), generator=g, device="cuda"))
     graph.replay()
     check(logits, scores, 4, got=out)
+    for _ in range(20):  # one behind the other, the same each time
+        again = b.select(logits, scores)
+    assert all(torch.equal(x, y) for x, y in zip(out, again))
 
 
 def model_reorder(m, beams, parents):
