@@ -207,7 +207,8 @@ class Beams:
             raise ValueError("batch >= 1, 1 <= beams <= 32, 1 <= n_out <= 64 and 1 <= vocab <= 2^20 are wanted")
         self._ws = torch.zeros(need, dtype=torch.uint8, device=device)
         self.device, self._index = self._ws.device, self._ws.get_device()
-        self._rows, self._scores, self._out = (batch * beams, vocab), (batch, beams), (batch, self.n_out)
+        self._rows, self._scores = (batch * beams, vocab), (batch, beams)
+        self._like = tuple(torch.empty((batch, self.n_out), dtype=t, device=device) for t in (torch.float32, torch.int32))
 
     def select(self, logits: torch.Tensor, scores: torch.Tensor, ended: torch.Tensor | None = None, stream=None):
         """logits [batch * beams, vocab], scores fp32 [batch, beams], ended bool or uint8 [batch, beams] -> (scores fp32,
@@ -225,14 +226,12 @@ class Beams:
                                   ended.get_device() != index or not ended.is_contiguous()):
             raise ValueError("ended must be contiguous bool or uint8 [batch, beams] on the logits' device")
 
-        def make(dtype):
-            return torch.empty(self._out, dtype=dtype, device=self.device)
-
+        like, like_whole = self._like  # empty_like takes half of empty's microseconds
         if stream is None:
-            best, parents, tokens = make(torch.float32), make(torch.int32), make(torch.int32)
+            best, parents, tokens = torch.empty_like(like), torch.empty_like(like_whole), torch.empty_like(like_whole)
         else:
-            best, parents, tokens = (_made_for(stream, self.device, lambda t=t: make(t))
-                                     for t in (torch.float32, torch.int32, torch.int32))
+            best, parents, tokens = (_made_for(stream, self.device, lambda t=t: torch.empty_like(t))
+                                     for t in (like, like_whole, like_whole))
         # what beam_select would do, whose checks of the results and the workspace are met here
         _call("gaac_beam_select", index, stream, logits.data_ptr(), code,
               logits.stride(0) if self._rows[0] > 1 else self.vocab, scores.data_ptr(), 0 if ended is None else ended.data_ptr(),
