@@ -2,7 +2,7 @@
 //
 //   c(i, t) = score_i + x_it - ln sum_u exp x_iu,   the n_out largest over (i, t), ties to the lowest i * vocab + t.
 //
-// The logits are read once.  Two launches:
+// The logits are read once, in one launch:
 //  1. A CTA takes up to kBmMostTiles runs of kBmTile consecutive logits of one beam, 32 a thread and run, the next run's loads
 //     under way while one is worked on.  They give its part of the sum and its n_out largest logits: within a beam the order
 //     of the logits is that of the candidates, so no candidate beyond these can be among the chosen.  The n_out-th largest
@@ -10,12 +10,13 @@
 //     least n_out logits reach.  Those of all runs that do, some tens, are put side by side in shared memory and ranked by
 //     counting, after the first run too, which leaves the others the n_out-th largest itself for a bound.  A run that has more
 //     of them than there is room for (logits that are all alike, or sorted) is searched for its largest one at a time.
-//  2. A CTA for each search adds up the sums in 64 bits, in a fixed order, and merges the sorted lists: the largest of
-//     their heads is taken n_out times, by one warp.
-// Bound by its instructions where there is much to read: 32 searches of 8 beams, 128,511 bf16 logits at odd addresses, n_out 16,
-// 66 MB: 53 us, of which 35 the first launch (550 instructions for 32 logits of a warp's lanes: 110 the sum, 100 loads and widening,
-// 150 the candidates) and 12 the merge.  What it was: every CTA one run, 104 us; odd rows put together from aligned vectors
-// of neighbouring lanes, 72 us; the bound by taking the largest maximum n_out times in place of a sort, 5 us more.
+//  2. The last CTA of a search adds up the sums in 64 bits, in a fixed order, and merges the sorted lists: the largest of
+//     their heads is taken n_out times, by one warp.  The other searches are read meanwhile.
+// Bound by its instructions and barriers where there is much to read: 32 searches of 8 beams, 128,511 bf16 logits at odd addresses,
+// n_out 16, 66 MB: 38.5 us (530 instructions for 32 logits of a warp's lanes, of which the sum takes 110, loads and widening 100, the
+// candidates 150).  What it was: every CTA one run and the choice a launch of its own, 104 us; odd rows put together from
+// aligned vectors of neighbouring lanes, 72 us; the bound by taking the largest maximum n_out times in place of a sort, 5 us
+// more; the choice in a second launch, 8 us more.  One search of 4 beams, 32,000 fp32 logits: 7.7 us.
 // Order: logits as unsigned numbers of the same order, the lower token first where they are equal; in the merge the
 // candidate to 48 bits, so that logits that differ stay apart, then the lower i * vocab + t.
 #include <algorithm>
@@ -30,7 +31,7 @@ namespace gaac {
 constexpr int kBmThreads = 256;
 constexpr int kBmPer = 32;                        // logits of a thread
 constexpr int kBmTile = kBmThreads * kBmPer;
-constexpr int kBmMostTiles = 4;                   // runs of a CTA
+constexpr int kBmMostTiles = 8;                   // runs of a CTA
 constexpr int kBmCtasPerSm = 2;                   // three spill: 87 us in place of 35
 constexpr int kBmRoom = 512;                      // logits that are ranked by counting
 constexpr int kBmMostOut = 64;
@@ -392,10 +393,8 @@ __global__ void __launch_bounds__(kBmThreads, kBmCtasPerSm) beam_chunk_kernel(co
     if (tile == first) {
       // ---- maxima of groups of threads; the n_out-th largest of them, by every warp
       uint32_t g = bm_order(top);
-      g = max(g, __shfl_xor_sync(kBmAll, g, 1));
-      g = max(g, __shfl_xor_sync(kBmAll, g, 2));
-      const int reps = a.n_out > 32 ? 64 : 32;  // groups of 4 or of 8 threads
-      if (reps == 32) g = max(g, __shfl_xor_sync(kBmAll, g, 4));
+      const int reps = a.n_out > 32 ? 64 : 32;
+      for (int d = 1; d < kBmThreads / reps; d *= 2) g = max(g, __shfl_xor_sync(kBmAll, g, d));
       if (lane % (kBmThreads / reps) == 0) rep[tid / (kBmThreads / reps)] = g;
       __syncthreads();
       const uint32_t r0 = rep[lane], r1 = reps == 64 ? rep[32 + lane] : 0u;
@@ -522,10 +521,13 @@ __global__ void __launch_bounds__(kBmThreads, kBmCtasPerSm) beam_chunk_kernel(co
   done();
 }
 
-// Runs of a CTA: as many as leave every SM three CTAs.
+// Runs of a CTA: as many as leave every SM three CTAs, up to kBmMostTiles, the same for all CTAs of a beam as nearly as it goes (32
+// searches of 8 beams, 16 runs a beam: 38.5 us with eight runs, 42.4 with four).
 static int beam_tiles(int64_t rows, int vocab) {
   const int64_t tiles = (vocab + kBmTile - 1) / kBmTile;
-  return static_cast<int>(std::min<int64_t>(std::min<int64_t>(kBmMostTiles, tiles), std::max<int64_t>(1, rows * tiles / (152 * 3))));
+  const int64_t least = (tiles + kBmMostTiles - 1) / kBmMostTiles;
+  const int64_t chunks = std::max(least, std::min<int64_t>(tiles, (152 * 3 + rows - 1) / rows));
+  return static_cast<int>((tiles + chunks - 1) / chunks);
 }
 static int beam_chunks(int64_t rows, int vocab) {
   const int per = kBmTile * beam_tiles(rows, vocab);
