@@ -534,7 +534,7 @@ GAAC_API int gaac_qk_norm_rope(const gaac_norm_tensor* tensors, int n_tensors, i
 
 /*
  * The gradient of gaac_qk_norm_rope with the same x, weights, positions, turns, mscale and eps: out receives that
- * of x (out may be dz or x itself with the same strides), dweight that of the weights, summed over all tokens and
+ * of x (out may be dz or x itself with the same strides, else their ranges must not overlap), dweight that of the weights, summed over all tokens and
  * heads in fp32 in an order that the sizes alone decide.  No tokens: dweight is zero.  workspace:
  * gaac_qk_norm_rope_workspace(head_dim) bytes, 16-byte aligned, of any contents; not shared by calls that may
  * overlap on the GPU.  The two tensors have a dweight of their own.
@@ -568,8 +568,8 @@ typedef struct {
  *   out[i][hq] = sum_{j <= i} softmax_j(scale * q[i][hq] . k[j][hk]) v[j][hk],  hk = hq / (n_q_heads / n_kv_heads),
  * which is an integer <= GAAC_MAX_GQA; lse[i][hq] = ln sum_{j <= i} exp(scale * q[i][hq] . k[j][hk]).  dtype, of all four:
  * GAAC_BF16 or GAAC_F16.  scale: any finite number.  Rows of no sequence are not written.  n_tokens < 2^31 - 2^16, batch
- * <= 65535.  Logits and sums are fp32; weights are rounded to dtype (f16: those below 2^-17 of the row's largest lose
- * bits, below 2^-25 they may be 0).  What tokens behind i and other sequences hold has no influence on row i, nor whether it
+ * <= 65535.  Logits and sums are fp32; weights are rounded to dtype (f16: those below 2^-14 of the row's largest may
+ * lose bits, below 2^-25 they may be 0).  What tokens behind i and other sequences hold has no influence on row i, nor whether it
  * is finite.  An infinite V makes its channel infinite (NaN where both signs meet, or where its weight is rounded to
  * 0).  A row whose logits are all -infinity is 0, its lse -infinity.
  */

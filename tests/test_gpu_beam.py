@@ -164,6 +164,13 @@ def test_select_strided_rows(dtype, offset):
     check(x, -torch.rand((2, 3), generator=g, device="cuda"), 6)
 
 
+def test_select_rows_past_32_bits():
+    g = gen(12)
+    x = torch.zeros((3, 1 << 30), dtype=torch.float16, device="cuda")[:, :9000]
+    x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+    check(x, torch.zeros((1, 3), device="cuda"), 5)
+
+
 def test_select_in_a_graph_and_on_another_stream():
     g = gen(9)
     logits = torch.randn((8, 30000), generator=g, device="cuda").bfloat16()

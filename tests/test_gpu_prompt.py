@@ -246,6 +246,18 @@ def test_graph_stream_and_the_same_each_time():
     assert torch.equal(got, check(q, k, v, lens))
 
 
+def test_offsets_past_32_bits():
+    """Tokens a megabyte and more apart: q, k, v and out lie over 4 GB."""
+    g = gen(14)
+    wide = torch.zeros((2300, 1 << 20), dtype=BF16, device="cuda")
+    parts = [wide[:, i * 4096:i * 4096 + h * 128].view(2300, h, 128) for i, h in enumerate((4, 2, 2, 4))]
+    q, k, v, out = parts
+    for x in (q, k, v):
+        x.copy_(normal(g, *x.shape))
+    got = check(q, k, v, [2300], out=out)
+    assert got.data_ptr() == out.data_ptr() and int(wide[:, 4 * 4096:].abs().max()) == 0
+
+
 def test_prompt_to_search():
     """Norms and rotation, prompt attention, append, fork, then steps of a search: the cache's attention of the last prompt
     token is the prompt attention's last row but for the cache's 8 bits, and every table stays consistent."""

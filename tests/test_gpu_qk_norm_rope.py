@@ -182,6 +182,22 @@ def test_weights_and_strides():
     check_gradient(gr, pair_sums(z.double(), 128, False), t0, None, out, dw, 128, 36)
 
 
+def test_offsets_past_32_bits():
+    g = gen(9)
+    # two buffers: an output that lies between the elements of another tensor is refused, as one that overlaps it
+    x, z = (torch.zeros((2200, 1 << 20), dtype=torch.bfloat16, device="cuda")[:, :256].view(2200, 2, 128) for _ in range(2))
+    x.copy_(normal(g, 2200, 2, 128))
+    z.copy_(normal(g, 2200, 2, 128))
+    x0, z0, pos, freq = x.clone(), z.clone(), torch.arange(2200, device="cuda"), G.rope_frequencies(128)[0]
+    turns = G.rope_turns(freq, "cuda")
+    ws, dw = torch.empty(G.qk_norm_rope_workspace(128), dtype=torch.uint8, device="cuda"), torch.empty(128, device="cuda")
+    G.qk_norm_rope_gradient(z, None, x, None, None, None, pos, turns, dw, None, ws)
+    check_gradient(U.rope_ref(z0, pos, freq, inverse=True), pair_sums(z0.double(), 128, False), x0, None, z, dw, 128, 4400)
+    G.qk_norm_rope(x, None, None, None, pos, turns)
+    want, y = ref(x0, None, pos, freq, EPS)
+    close(x, want, pair_sums(y, 128, False), relative(128))
+
+
 def test_special_heads():
     """Zeros stay zeros; NaN and infinities stay in their head; no tokens: weight gradients of zero."""
     g = gen(2)
