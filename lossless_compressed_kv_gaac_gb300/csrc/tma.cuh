@@ -1,4 +1,4 @@
-// Tensor maps: the driver's encoder, looked up at run time (the library links no driver library).
+// Tensor maps: the CUDA driver's encoder, looked up at run time (the library links no part of that driver).
 #pragma once
 
 #include <cuda.h>
