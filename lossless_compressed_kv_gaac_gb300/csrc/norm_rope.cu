@@ -8,20 +8,25 @@
 // Memory bound: the forward pass reads and writes every element once, the backward pass reads x and dz and writes dx;
 // r is computed again rather than kept, since x has to be read for dx anyway.  A group of 2 to 32 lanes owns the heads of
 // a row that it walks over; a lane has two vectors of V elements of each (a unit: V pairs of the rotated part, or of the
-// channels behind it), so that the mean takes a few shuffles and V sines serve all heads of the walk.  V is 16 bytes
-// where widths and alignment allow, else one element with four units a lane.
+// channels behind it), so that the mean takes a few shuffles and V sines serve all heads of the walk.  Vectors of
+// neighbouring lanes are neighbours, so that an instruction takes whole sectors (with a lane's two side by side, the
+// gradient of interleaved pairs 34.1 us for 27.4).  V is 16 bytes where widths and alignment allow, else one element with four
+// units a lane.
 // Arithmetic is packed, two numbers an instruction; the forward pass multiplies the weights into the sines once for a row and
 // tensor.  Each head's registers are loaded again, with the head four further on, as soon as they are unpacked.
-// Forward, 32,768 tokens x 40 heads x 128, bf16: 120 us, 5.6 TB/s (82% of a copy).  One head at a time without packing: 148 us;
+// Forward, 32,768 tokens x 40 heads x 128, bf16: 119 us, 5.6 TB/s (83% of a copy).  One head at a time without packing: 148 us;
 // walks of five heads 154-179 us by CTAs an SM, of ten 129-157, of twenty 120 (8 CTAs, four heads in flight) to 163 (spills).  32
-// tokens: 4.4 us.
-// Backward, 16,384 tokens x 40 heads x 128, bf16: 116 us, 4.3 TB/s (64%); its 168 registers leave three CTAs of 128 to an SM
-// (four spill: 175 us; two with every load of two heads ahead: 185 us).  With both tensors' weights and sums in one CTA and
-// without packing 184 us.  4,999 tokens x 24 heads, fp16, half turned, interleaved: 34.8 us.
+// tokens: 3.0 us.
+// The backward pass has no registers for loads in flight (two heads' in them leave three CTAs to an SM and take 116 us), so
+// its next three heads, across walks, come by asynchronous copies into shared memory, and 128 registers leave four CTAs.
+// 16,384 tokens x 40 heads x 128, bf16: 94 us, 5.3 TB/s (79%); two heads ahead the same, walks of 4 heads 99 us, of 16 the
+// same, a row's heads in one walk that begins with empty hands 97.  With both tensors' weights and sums in one CTA and without
+// packing 184 us.  4,999 tokens x 24 heads, fp16, half turned, interleaved: 27.4 us; 512 tokens x 24: 9.5 us.
 // Sums are fp32.  dw: every lane adds up its channels over its rows, a CTA its lanes in order, a second launch the
 // CTAs in order, so the result is the same each time.
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "f32x2.cuh"
 #include "kv8.cuh"
@@ -35,7 +40,9 @@ constexpr int kNrMost = 20;         // most heads of a walk
 constexpr int kNrCtasPerSm = 8;
 constexpr int kNrMaxDim = 256;
 constexpr int kNgThreads = 128;    // gradient
-constexpr int kNgCtasPerSm = 3;
+constexpr int kNgMost = 8;         // most heads of a walk
+constexpr int kNgAhead = 3;        // heads whose copies a lane has under way, where they are vectors
+constexpr int kNgCtasPerSm = 4;
 constexpr int kNgMostCtas = 152 * kNgCtasPerSm;
 
 struct NormTensor {
@@ -59,7 +66,7 @@ struct NormArgs {
   float mscale, eps;
   int rot_units, units, lanes;  // of a head; lanes of a group
   int walk, walkers;            // heads of a walk; groups that share the heads of a row (gradient: of the first tensor)
-  int walkers1;                 // gradient: of the second
+  int walk1, walkers1;          // gradient: of the second
   unsigned row_walkers;         // rows * walkers
   unsigned ctas0;               // gradient: CTAs of the first tensor
   float* part;                  // gradient: [CTA][dim]
@@ -75,8 +82,13 @@ struct NormUnits {
     for (int k = 0; k < UPL; ++k) {
       const int u = lane + k * a.lanes;
       turned[k] = u < a.rot_units;
-      e0[k] = turned[k] ? (INTER ? 2 * u * V : u * V) : a.rot + 2 * (u - a.rot_units) * V;
-      e1[k] = turned[k] && !INTER ? e0[k] + a.rot / 2 : e0[k] + V;
+      if (V > 1 || !INTER) {  // neighbouring lanes have neighbouring vectors
+        e0[k] = turned[k] ? u * V : a.rot + (u - a.rot_units) * V;
+        e1[k] = e0[k] + (turned[k] ? a.rot_units : a.units - a.rot_units) * V;
+      } else {
+        e0[k] = turned[k] ? 2 * u : a.rot + 2 * (u - a.rot_units);
+        e1[k] = e0[k] + 1;
+      }
       one[k] = u < a.units;
       two[k] = one[k] && e1[k] < a.dim;
     }
@@ -187,7 +199,9 @@ struct NormLane {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int k = unit(q) + (V == 1 ? i : 0);
-        if (n.turned[k]) rope_sincos<T>(p * a.turns[(lane + k * a.lanes) * V + (2 * q + i) % V], a.mscale, x[i], y[i]);
+        const int at = (2 * q + i) % V;  // interleaved pairs stay within a vector
+        const int pair = !INTER || V == 1 ? (lane + k * a.lanes) * V + at : at < V / 2 ? n.e0[k] / 2 + at : n.e1[k] / 2 + at - V / 2;
+        if (n.turned[k]) rope_sincos<T>(p * a.turns[pair], a.mscale, x[i], y[i]);
       }
       s[q] = f2_make(x[0], x[1]);
       c[q] = f2_make(y[0], y[1]);
@@ -275,10 +289,91 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtasPerSm) qk_norm_rope_kernel(
   }
 }
 
+// The heads of x and dz that a lane works on next, kAhead of them, the oldest first.  Single elements wait in registers.
+template <typename T, int V, int UPL, bool INTER, bool kVectors = V * sizeof(T) == 16>
+struct NormAhead {
+  using Vec = RopeVec<T, V>;
+  using L = NormLane<T, V, UPL, INTER>;
+  static constexpr int kAhead = 1, kBytes = 16;
+  const typename L::Units& n;
+  Vec x[UPL][2], dz[UPL][2];
+  __device__ __forceinline__ NormAhead(const typename L::Units& n, char*) : n(n) {}
+  __device__ __forceinline__ void fetch(const char* from, const char* dz_from, bool there) {
+    if (!there) return;
+    L::load(x, from, n);
+    L::load(dz, dz_from, n);
+  }
+  __device__ __forceinline__ void take(uint64_t (&xa)[L::kPairs], uint64_t (&xb)[L::kPairs], uint64_t (&za)[L::kPairs],
+                                       uint64_t (&zb)[L::kPairs]) {
+    L::unpack(x, xa, xb);
+    L::unpack(dz, za, zb);
+  }
+};
+
+// Vectors wait in shared memory, at places that one lane alone fills, by asynchronous copies, and reads.
+template <typename T, int V, int UPL, bool INTER>
+struct NormAhead<T, V, UPL, INTER, true> {
+  using Vec = RopeVec<T, V>;
+  using L = NormLane<T, V, UPL, INTER>;
+  static constexpr int kAhead = kNgAhead, kStages = kAhead + 1, kStep = kNgThreads * 16, kStage = 4 * UPL * kStep;
+  static constexpr int kBytes = kStages * kStage;
+  const typename L::Units& n;
+  const uint32_t base;
+  uint32_t put = 0, get = 0;
+  __device__ __forceinline__ NormAhead(const typename L::Units& n, char* ring)
+      : n(n), base(static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16) {}
+  // Each call is a group of copies, an empty one where there is nothing.
+  __device__ __forceinline__ void fetch(const char* x, const char* dz, bool there) {
+    if (there) {
+#pragma unroll
+      for (int k = 0; k < UPL; ++k) {
+        const uint32_t to = base + put + k * 4 * kStep;
+        copy(to, x, n.e0[k], n.one[k]);
+        copy(to + kStep, x, n.e1[k], n.two[k]);
+        copy(to + 2 * kStep, dz, n.e0[k], n.one[k]);
+        copy(to + 3 * kStep, dz, n.e1[k], n.two[k]);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    put = put + kStage == kBytes ? 0 : put + kStage;
+  }
+  __device__ __forceinline__ void take(uint64_t (&xa)[L::kPairs], uint64_t (&xb)[L::kPairs], uint64_t (&za)[L::kPairs],
+                                       uint64_t (&zb)[L::kPairs]) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    Vec x[UPL][2], dz[UPL][2];
+#pragma unroll
+    for (int k = 0; k < UPL; ++k) {
+      const uint32_t at = base + get + k * 4 * kStep;
+      read(x[k][0], at);
+      read(x[k][1], at + kStep);
+      read(dz[k][0], at + 2 * kStep);
+      read(dz[k][1], at + 3 * kStep);
+    }
+    L::unpack(x, xa, xb);
+    L::unpack(dz, za, zb);
+    get = get + kStage == kBytes ? 0 : get + kStage;
+  }
+  // 16 bytes, zeros where there is nothing.
+  static __device__ __forceinline__ void copy(uint32_t to, const char* from, int element, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                 "l"(from + (there ? element : 0) * static_cast<int64_t>(sizeof(T))), "r"(there ? 16 : 0)
+                 : "memory");
+  }
+  static __device__ __forceinline__ void read(Vec& v, uint32_t at) {
+    uint4 w;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
+    memcpy(&v, &w, 16);
+  }
+};
+
 // CTAs below ctas0 take the first tensor, the others the second; their groups take (row, walker) in turn.
 template <typename T, int V, int UPL, bool INTER>
 __global__ void __launch_bounds__(kNgThreads, kNgCtasPerSm) qk_norm_rope_gradient_kernel(const NormArgs a) {
-  __shared__ float sums[kNgThreads * UPL * 2 * V];  // [group][dim]
+  using Ahead = NormAhead<T, V, UPL, INTER>;
+  constexpr int kAhead = Ahead::kAhead;
+  constexpr int kSums = kNgThreads * UPL * 2 * V * static_cast<int>(sizeof(float));
+  __shared__ __align__(16) char ring[Ahead::kBytes > kSums ? Ahead::kBytes : kSums];
+  float* const sums = reinterpret_cast<float*>(ring);  // [group][dim], when the heads are through
   dependent_wait();
   dependent_launch();
   using L = NormLane<T, V, UPL, INTER>;
@@ -287,8 +382,9 @@ __global__ void __launch_bounds__(kNgThreads, kNgCtasPerSm) qk_norm_rope_gradien
   const uint32_t mask = group_mask(a.lanes);
   const bool second = blockIdx.x >= a.ctas0;
   const NormTensor& t = a.t[second];
-  const int n_heads = second ? a.heads - a.heads0 : a.heads0, walkers = second ? a.walkers1 : a.walkers;
-  const int64_t cta = second ? blockIdx.x - a.ctas0 : blockIdx.x, ctas = second ? gridDim.x - a.ctas0 : a.ctas0;
+  const int n_heads = second ? a.heads - a.heads0 : a.heads0, walk = second ? a.walk1 : a.walk;
+  const unsigned walkers = second ? a.walkers1 : a.walkers;
+  const unsigned cta = second ? blockIdx.x - a.ctas0 : blockIdx.x, ctas = second ? gridDim.x - a.ctas0 : a.ctas0;
   const unsigned rows = a.n_seq * a.n_tok;
   const NormUnits<V, UPL, INTER> n(a, lane);
   const float mean = 1.f / a.dim;
@@ -296,27 +392,53 @@ __global__ void __launch_bounds__(kNgThreads, kNgCtasPerSm) qk_norm_rope_gradien
   L::weights(wa, wb, a, t.w, n);
 #pragma unroll
   for (int q = 0; q < kP; ++q) da[q] = db[q] = 0;
-#pragma unroll 1
-  for (int64_t rw = cta * groups + group; rw < static_cast<int64_t>(rows) * walkers; rw += ctas * groups) {
-    const unsigned row = static_cast<unsigned>(rw) / walkers;
-    const int first = (static_cast<unsigned>(rw) - row * walkers) * a.walk, end = min(first + a.walk, n_heads);
-    unsigned seq = 0, tok = row;
+  Ahead in(n, ring);
+  const unsigned walks = rows * walkers, step = ctas * groups;
+  auto place = [&](unsigned rw, unsigned& seq, unsigned& tok, int& first) {  // -> heads of walk rw
+    const unsigned row = rw / walkers;
+    first = (rw - row * walkers) * walk;
+    seq = 0, tok = row;
     if (a.n_seq > 1) {
       seq = row / a.n_tok;
       tok = row - seq * a.n_tok;
     }
-    const char* const x = t.x + seq * t.x_seq + tok * t.x_tok;
-    const char* const dz = t.dz + seq * t.dz_seq + tok * t.dz_tok;
-    char* const out = t.out + seq * t.out_seq + tok * t.out_tok;
-    RopeVec<T, V> vx[2][UPL][2], vz[2][UPL][2];
-    L::load(vx[0], x + first * t.x_head, n);
-    L::load(vz[0], dz + first * t.dz_head, n);
+    return min(walk, n_heads - first);
+  };
+  // What is fetched next: `left` more heads of walk `ahead`, at x and dz.
+  unsigned ahead = cta * groups + group - step;
+  int left = 0;
+  const char *x = nullptr, *dz = nullptr;
+  auto fetch = [&] {
+    if (left == 0) {
+      ahead += step;
+      if (ahead < walks) {
+        unsigned seq, tok;
+        int first;
+        left = place(ahead, seq, tok, first);
+        x = t.x + seq * t.x_seq + tok * t.x_tok + first * t.x_head;
+        dz = t.dz + seq * t.dz_seq + tok * t.dz_tok + first * t.dz_head;
+      } else {
+        ahead -= step;
+      }
+    }
+    in.fetch(x, dz, left > 0);
+    if (left > 0) --left, x += t.x_head, dz += t.dz_head;
+  };
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) fetch();
+#pragma unroll 1
+  for (unsigned rw = cta * groups + group; rw < walks; rw += step) {
+    unsigned seq, tok;
+    int first;
+    const int n_walk = place(rw, seq, tok, first);
+    char* out = t.out + seq * t.out_seq + tok * t.out_tok + first * t.out_head;
     uint64_t s[kP], c[kP];
     L::sines(s, c, a, n, lane, seq * a.pos_seq + tok * a.pos_tok);
-    auto one = [&](const RopeVec<T, V> (&v)[UPL][2], const RopeVec<T, V> (&z)[UPL][2], int h) {
+#pragma unroll 1
+    for (int h = 0; h < n_walk; ++h, out += t.out_head) {
       uint64_t xa[kP], xb[kP], ga[kP], gb[kP], ta[kP], tb[kP], xx = 0, hx = 0;
-      L::unpack(v, xa, xb);
-      L::unpack(z, ga, gb);
+      in.take(xa, xb, ga, gb);
+      fetch();
 #pragma unroll
       for (int q = 0; q < kP; ++q) {
         const uint64_t g0 = ga[q], minus = f2_mul(s[q], f2_all(-1.f));
@@ -337,25 +459,10 @@ __global__ void __launch_bounds__(kNgThreads, kNgCtasPerSm) qk_norm_rope_gradien
         xa[q] = f2_fma(f2_mul(ga[q], wa[q]), r2, f2_mul(xa[q], k2));
         xb[q] = f2_fma(f2_mul(gb[q], wb[q]), r2, f2_mul(xb[q], k2));
       }
-      L::store(out + h * t.out_head, n, xa, xb);
-    };
-    // the next head's loads are under way while one is worked on
-#pragma unroll 1
-    for (int h = first; h < end; h += 2) {
-      if (h + 1 < end) {
-        L::load(vx[1], x + (h + 1) * t.x_head, n);
-        L::load(vz[1], dz + (h + 1) * t.dz_head, n);
-      }
-      one(vx[0], vz[0], h);
-      if (h + 1 < end) {
-        if (h + 2 < end) {
-          L::load(vx[0], x + (h + 2) * t.x_head, n);
-          L::load(vz[0], dz + (h + 2) * t.dz_head, n);
-        }
-        one(vx[1], vz[1], h + 1);
-      }
+      L::store(out, n, xa, xb);
     }
   }
+  __syncthreads();  // no head waits any more
   L::each(n, [&](int b, int q, int i, int ch) {
     const float2 d = f2_get(b ? db[q] : da[q]);
     sums[group * a.dim + ch] = i ? d.y : d.x;
@@ -500,14 +607,24 @@ static int norm_rope(const gaac_norm_tensor* tensors, int n_tensors, int dtype, 
   a.units = a.rot_units + ((head_dim - rot_dim) / v + 1) / 2;
   a.lanes = 2;
   while (a.lanes < 32 && a.lanes < a.units) a.lanes *= 2;
-  // Heads of a walk: as many as leave twice the lanes that 152 SMs hold at a time, so that sines are shared where there
-  // is work for all, and single heads where latency counts.
-  const int64_t want = int64_t{152} * (gradient ? 768 : 2048), lanes = std::max<int64_t>(rows, 1) * heads * a.lanes;
-  a.walk = static_cast<int>(std::min<int64_t>(gradient ? heads : kNrMost, std::max<int64_t>(1, lanes / want)));
-  const int first = gradient ? a.heads0 : a.heads;
-  a.walkers = (first + a.walk - 1) / a.walk;
-  a.walkers1 = (a.heads - a.heads0 + a.walk - 1) / a.walk;
-  if (rows * std::max(a.walkers, a.walkers1) > 0x7FFFFFFF) return GAAC_EINVAL;
+  // Heads of a walk: as many as leave twice the lanes that 152 SMs hold at a time (gradient: one walk for each group that
+  // they hold), so that sines are shared where there is work for all, and single heads where latency counts.
+  const int64_t want = int64_t{152} * (gradient ? kNgThreads * kNgCtasPerSm : 2048), lanes = std::max<int64_t>(rows, 1) * heads * a.lanes;
+  const int64_t fair = std::max<int64_t>(1, gradient ? (lanes + want - 1) / want : lanes / want);
+  const int64_t walkers_most = 0x7FFFFFFF / std::max<int64_t>(rows, 1);  // walks are counted in 31 bits
+  if (gradient) {  // walks of like lengths
+    auto of = [&](int n, int* walk) {
+      const int most = static_cast<int>(std::max(std::min<int64_t>(fair, kNgMost), (n + walkers_most - 1) / walkers_most));
+      const int walkers = (n + most - 1) / most;
+      *walk = walkers > 0 ? (n + walkers - 1) / walkers : 1;
+      return walkers;
+    };
+    a.walkers = of(a.heads0, &a.walk);
+    a.walkers1 = of(a.heads - a.heads0, &a.walk1);
+  } else {
+    a.walk = static_cast<int>(std::max(std::min<int64_t>(kNrMost, fair), (heads + walkers_most - 1) / walkers_most));
+    a.walkers = (a.heads + a.walk - 1) / a.walk;
+  }
   a.row_walkers = static_cast<unsigned>(rows * a.walkers);
   a.part = static_cast<float*>(workspace);
   int grid = 0;

@@ -60,7 +60,8 @@ CASES = [  # tokens, hq, hk, dim, rot, dtype, interleaved
     (5, 3, 1, 64, 64, "fp32", False), (33, 4, 2, 256, 128, "bf16", True), (9, 5, 5, 256, 256, "fp32", False),
     (7, 2, 3, 96, 32, "fp16", False), (6, 2, 1, 20, 6, "bf16", False), (3, 1, 2, 2, 2, "fp32", True),
     (11, 7, 1, 250, 250, "bf16", False), (4, 40, 8, 128, 2, "fp32", True), (2500, 8, 2, 64, 32, "bf16", False),
-    (13, 2, 2, 24, 16, "fp16", False), (1, 6, 2, 34, 18, "fp16", True)]
+    (13, 2, 2, 24, 16, "fp16", False), (1, 6, 2, 34, 18, "fp16", True), (6000, 21, 5, 136, 112, "bf16", True),
+    (6000, 21, 5, 136, 112, "fp16", False), (9000, 9, 1, 76, 32, "fp32", True), (40, 3, 7, 100, 92, "fp32", False)]
 
 
 @pytest.mark.parametrize("n,hq,hk,dim,rot,dtype,inter", CASES)
