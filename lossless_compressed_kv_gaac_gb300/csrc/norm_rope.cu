@@ -10,7 +10,7 @@
 // a row that it walks over; a lane has two vectors of V elements of each (a unit: V pairs of the rotated part, or of the
 // channels behind it), so that the mean takes a few shuffles and V sines serve all heads of the walk.  Vectors of
 // neighbouring lanes are neighbours, so that an instruction takes whole sectors (with a lane's two side by side, the
-// gradient of interleaved pairs 34.1 us for 27.4).  V is 16 bytes where widths and alignment allow, else one element with four
+// gradient of interleaved pairs took 34.1 us for 27.4).  V is 16 bytes where widths and alignment allow, else one element with four
 // units a lane.
 // Arithmetic is packed, two numbers an instruction; the forward pass multiplies the weights into the sines once for a row and
 // tensor.  Each head's registers are loaded again, with the head four further on, as soon as they are unpacked.
@@ -19,9 +19,9 @@
 // tokens: 3.0 us.
 // The backward pass has no registers for loads in flight (two heads' in them leave three CTAs to an SM and take 116 us), so
 // its next three heads, across walks, come by asynchronous copies into shared memory, and 128 registers leave four CTAs.
-// 16,384 tokens x 40 heads x 128, bf16: 94 us, 5.3 TB/s (79%); two heads ahead the same, walks of 4 heads 99 us, of 16 the
-// same, a row's heads in one walk that begins with empty hands 97.  With both tensors' weights and sums in one CTA and without
-// packing 184 us.  4,999 tokens x 24 heads, fp16, half turned, interleaved: 27.4 us; 512 tokens x 24: 9.5 us.
+// 16,384 tokens x 40 heads x 128, bf16: 85 us, 5.9 TB/s (88% of a copy).  Shuffles of the two means one after the other: 94 us,
+// and of that form two heads ahead the same, walks of 4 heads 99, of 16 the same, a row's heads in one walk that begins with
+// empty hands 97.  4,999 tokens x 24 heads, fp16, half turned, interleaved: 25.0 us; 512 tokens x 24: 9.1 us.
 // Sums are fp32.  dw: every lane adds up its channels over its rows, a CTA its lanes in order, a second launch the
 // CTAs in order, so the result is the same each time.
 #include <algorithm>
@@ -213,6 +213,14 @@ struct NormLane {
 __device__ __forceinline__ float group_sum(float x, int lanes, uint32_t mask) {
   for (int d = lanes >> 1; d > 0; d >>= 1) x += __shfl_xor_sync(mask, x, d);
   return x;
+}
+// Of two numbers at a time, whose shuffles overlap.
+__device__ __forceinline__ float2 group_sums(float x, float y, int lanes, uint32_t mask) {
+  for (int d = lanes >> 1; d > 0; d >>= 1) {
+    const float a = __shfl_xor_sync(mask, x, d), b = __shfl_xor_sync(mask, y, d);
+    x += a, y += b;
+  }
+  return {x, y};
 }
 __device__ __forceinline__ uint32_t group_mask(int lanes) {
   const uint32_t low = lanes == 32 ? 0xFFFFFFFFu : (1u << lanes) - 1u;
@@ -449,8 +457,9 @@ __global__ void __launch_bounds__(kNgThreads, kNgCtasPerSm) qk_norm_rope_gradien
         xx = f2_fma(xb[q], xb[q], f2_fma(xa[q], xa[q], xx));
         hx = f2_fma(tb[q], wb[q], f2_fma(ta[q], wa[q], hx));
       }
-      const float r = rsqrtf(group_sum(f2_sum(xx), a.lanes, mask) * mean + a.eps);
-      const float m = group_sum(f2_sum(hx), a.lanes, mask) * mean * r;  // the mean of h x r
+      const float2 sum = group_sums(f2_sum(xx), f2_sum(hx), a.lanes, mask);
+      const float r = rsqrtf(sum.x * mean + a.eps);
+      const float m = sum.y * mean * r;  // the mean of h x r
       const uint64_t r2 = f2_all(r), k2 = f2_all(-r * r * m);
 #pragma unroll
       for (int q = 0; q < kP; ++q) {
