@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(kFkThreads) kv8_fork_kernel(Kv8Dev c, const in
 // Sequence g * beams + i becomes what g * beams + parents[g][i] was.  A thread takes one place (a column of the table,
 // 16 bytes of an open row) of all the beams of a group: it has read every beam's old value before it writes the first
 // new one, so the exchange needs no second copy of anything.  BEAMS: the beams at most.  32 searches of 8 beams, rows of 512
-// pages, open blocks of 8 heads half full, 59 MB moved: 11.0 us in a graph, 5.4 TB/s (13.4-14.6 us one by one); eight or sixteen CTAs an SM in place of four 15.5 and 17.1
-// us, table and open rows by the same CTAs 15.4-16.7.  4 searches of 4: 3.9 us.
+// pages, open blocks of 8 heads half full, 59 MB moved: 11.0 us in a graph, 5.4 TB/s (13.4-14.6 us one by one; then eight
+// or sixteen CTAs an SM in place of four 15.5 and 17.1 us, table and open rows by the same CTAs 15.4-16.7).  4 searches of 4: 3.9 us.
 
 constexpr int kRoThreads = 128;
 
