@@ -697,9 +697,9 @@ GAAC_API int gaac_kv8_compact(const gaac_kv8* cache, int32_t* moved_to, void* st
  * [batch][n_out]: fp32 out_scores, int32 parents (the beam i) and int32 tokens.  What is left counts as -infinity: the
  * other tokens of an ended beam, logits of -infinity, and all of a beam whose score or sum is not finite (its logits are
  * all -infinity, or one is NaN or infinity).  1 <= beams <= GAAC_MAX_BEAMS, 1 <= n_out <= 64 and beams*vocab,
- * 1 <= vocab <= 2^20.  Sums are fp32 over 8,192 logits, 64 bits over these.  workspace: gaac_beam_workspace() bytes (0 for
- * arguments that are not valid), 16-byte aligned, zero before the first call and for calls of one batch, beams, vocab and n_out;
- * not shared by calls that may overlap on the GPU.
+ * 1 <= vocab <= 2^20.  Sums are fp32 over up to 65,536 logits, relative to the largest of them, and 64 bits over these.
+ * workspace: gaac_beam_workspace() bytes (0 for arguments that are not valid), 16-byte aligned, zero before the first call and
+ * for calls of one batch, beams, vocab and n_out; not shared by calls that may overlap on the GPU.
  */
 GAAC_API size_t gaac_beam_workspace(int batch, int beams, int vocab, int n_out);
 GAAC_API int gaac_beam_select(const void* logits, int dtype, int64_t row_stride, const float* scores, const uint8_t* ended,

@@ -410,7 +410,9 @@ __global__ void __launch_bounds__(kBmThreads, kBmCtasPerSm) beam_chunk_kernel(co
       base = bm_value(peak);
     }
     // ---- the sum.  The difference first: a product with log2(e) would be off by the last bit of a large logit.
-    if (top > base + 60.f) {  // rare: what comes is far above the runs before, or the first that is finite
+    // The base is this thread's largest logit so far: an exponent's error grows with the distance from it (with a base that
+    // rose by steps of 60 only, a peak in a later run took 3e-6 of the sum), and what is far below has no weight.
+    if (top > base) {  // rare behind the first run, whose peak all threads begin with
       sum *= bm_exp2((base - top) * 1.44269504f);
       base = top;
     }
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(kBmThreads, kBmCtasPerSm) beam_chunk_kernel(co
     if (rank < a.n_out) list[rank] = k;
   }
   if (tid >= taken && tid < a.n_out) list[tid] = 0;
-  // Threads' bases differ where one has met far larger logits: all go to the largest.
+  // Threads' bases differ where one has met larger logits than the first run's: all go to the largest.
   float high = base;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) high = fmaxf(high, __shfl_xor_sync(kBmAll, high, d));

@@ -320,3 +320,24 @@ def test_search_loop_in_a_graph():
     held = torch.bincount(a["c"].table[a["c"].table >= 0].long(), minlength=256)
     assert torch.equal(held, a["c"].refs.long())
     assert a["c"].seq_lens.tolist() == [220] * n
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("V", [70000, 70001])
+def test_select_peak_in_a_later_run(V, dtype):
+    """The largest logit 3 to 59 above the first run's, in a later run of the same CTA, with a step on the way in half of the
+    rows; nothing else has weight.  The sum is off by 2^-22 for its exponentials (twice that of the small terms, 5% of it),
+    three roundings of 2^-24 and the logarithm's 2^-25, together below 2^-21, the result by 2^-24 of itself."""
+    rows = 256
+    x = torch.full((rows, V), -300.0, device="cuda")
+    gap = torch.linspace(3, 59, rows, device="cuda")
+    x[:, 5] = -2.7
+    x[:, 3 * 8192 + 77] = gap - 2.7
+    x[::2, 8192 + 9] = gap[::2] / 2 - 5
+    x = x.to(DT[dtype])
+    scores = torch.zeros((rows, 1), device="cuda")
+    out, _, tokens = Beams(rows, 1, V, 2).select(x, scores)
+    best, at = candidates(x, scores, None, 0).view(rows, V).topk(2)
+    assert torch.equal(tokens.long(), at)
+    err = (out.double() - best).abs()
+    assert (err <= 2.0 ** -21 + best.abs() * 2.0 ** -24).all(), err.max().item()
