@@ -525,7 +525,8 @@ typedef struct {
  *   y = x / sqrt(mean(x^2) + eps) * weight,  the first rot_dim channels of y turned by the position.
  * weight_dtype: dtype or GAAC_F32.  eps >= 0.  2 <= rot_dim <= head_dim <= 256, both even.  Everything else as
  * gaac_rope (flags: GAAC_ROPE_INTERLEAVED).  Computed in fp32 and rounded once; the mean of x^2 has to be in
- * fp32's range.  A head of zeros stays zeros with eps > 0 and becomes NaN with eps = 0.
+ * fp32's range.  A head of zeros stays zeros with eps > 0 and becomes NaN with eps = 0.  An infinite channel becomes NaN, and
+ * so does the one that it is turned with; the others of its head become 0.
  */
 GAAC_API int gaac_qk_norm_rope(const gaac_norm_tensor* tensors, int n_tensors, int dtype, int weight_dtype, int64_t n_seq,
                                int64_t n_tok, int head_dim, int rot_dim, const void* positions, int pos_bits,

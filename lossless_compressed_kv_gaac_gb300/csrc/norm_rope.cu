@@ -21,7 +21,7 @@
 // its next three heads, across walks, come by asynchronous copies into shared memory, and 128 registers leave four CTAs.
 // 16,384 tokens x 40 heads x 128, bf16: 85 us, 5.9 TB/s (88% of a copy).  Shuffles of the two means one after the other: 94 us,
 // and of that form two heads ahead the same, walks of 4 heads 99, of 16 the same, a row's heads in one walk that begins with
-// empty hands 97.  4,999 tokens x 24 heads, fp16, half turned, interleaved: 25.0 us; 512 tokens x 24: 9.1 us.
+// empty hands 97.  4,999 tokens x 24 heads, fp16, half turned, interleaved: 25.7 us; 512 tokens x 24: 9.3 us.
 // Sums are fp32.  dw: every lane adds up its channels over its rows, a CTA its lanes in order, a second launch the
 // CTAs in order, so the result is the same each time.
 #include <algorithm>
@@ -96,8 +96,9 @@ struct NormUnits {
 };
 
 // A lane's channels of a head as UPL * V pairs (a, b), two of them to a packed number.  Pairs that are not turned have
-// sine 0 and cosine 1, so that all are treated alike.
-template <typename T, int V, int UPL, bool INTER>
+// sine 0 and cosine 1, and take nothing of each other (of_partner).  PART: there are such pairs; where the whole head is
+// turned the selects for that would take 2% (121.4 us for 119.1, gradient 86.9 for 85.2).
+template <typename T, int V, int UPL, bool INTER, bool PART>
 struct NormLane {
   using Vec = RopeVec<T, V>;
   using Units = NormUnits<V, UPL, INTER>;
@@ -153,6 +154,13 @@ struct NormLane {
         *reinterpret_cast<Vec*>(out + n.e1[k] * static_cast<int64_t>(sizeof(T))) = y;
       }
     }
+  }
+  // What a turned channel takes of its partner; 0 where it is not turned, since an infinity times the sine 0 is NaN.
+  static __device__ __forceinline__ uint64_t of_partner(uint64_t x, const Units& n, int q) {
+    if constexpr (!PART) return x;
+    if constexpr (V > 1) return n.turned[unit(q)] ? x : 0;
+    const float2 f = f2_get(x);
+    return f2_make(n.turned[unit(q)] ? f.x : 0.f, n.turned[unit(q) + 1] ? f.y : 0.f);
   }
   // f(a or b (0, 1), q, half, channel) for every channel of the lane.
   template <typename F>
@@ -228,11 +236,11 @@ __device__ __forceinline__ uint32_t group_mask(int lanes) {
 }
 
 // Group (row, walker): `walk` heads of one row, from walker * walk on.
-template <typename T, int V, int UPL, bool INTER>
+template <typename T, int V, int UPL, bool INTER, bool PART>
 __global__ void __launch_bounds__(kNrThreads, kNrCtasPerSm) qk_norm_rope_kernel(const NormArgs a) {
   dependent_wait();
   dependent_launch();
-  using L = NormLane<T, V, UPL, INTER>;
+  using L = NormLane<T, V, UPL, INTER, PART>;
   constexpr int kP = L::kPairs;
   const int lane = threadIdx.x & (a.lanes - 1);
   const uint32_t mask = group_mask(a.lanes);
@@ -289,8 +297,8 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtasPerSm) qk_norm_rope_kernel(
 #pragma unroll
       for (int q = 0; q < kP; ++q) {
         const uint64_t t = x[q];
-        x[q] = f2_mul(r, f2_fma(t, ca[q], f2_mul(y[q], sb[q])));
-        y[q] = f2_mul(r, f2_fma(y[q], cb[q], f2_mul(t, sa[q])));
+        x[q] = f2_mul(r, f2_fma(t, ca[q], L::of_partner(f2_mul(y[q], sb[q]), n, q)));
+        y[q] = f2_mul(r, f2_fma(y[q], cb[q], L::of_partner(f2_mul(t, sa[q]), n, q)));
       }
       L::store(second ? outk + (h - a.heads0) * a.t[1].out_head : outq + h * a.t[0].out_head, n, x, y);
     }
@@ -298,10 +306,10 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtasPerSm) qk_norm_rope_kernel(
 }
 
 // The heads of x and dz that a lane works on next, kAhead of them, the oldest first.  Single elements wait in registers.
-template <typename T, int V, int UPL, bool INTER, bool kVectors = V * sizeof(T) == 16>
+template <typename T, int V, int UPL, bool INTER, bool PART, bool kVectors = V * sizeof(T) == 16>
 struct NormAhead {
   using Vec = RopeVec<T, V>;
-  using L = NormLane<T, V, UPL, INTER>;
+  using L = NormLane<T, V, UPL, INTER, PART>;
   static constexpr int kAhead = 1, kBytes = 16;
   const typename L::Units& n;
   Vec x[UPL][2], dz[UPL][2];
@@ -319,10 +327,10 @@ struct NormAhead {
 };
 
 // Vectors wait in shared memory, at places that one lane alone fills, by asynchronous copies, and reads.
-template <typename T, int V, int UPL, bool INTER>
-struct NormAhead<T, V, UPL, INTER, true> {
+template <typename T, int V, int UPL, bool INTER, bool PART>
+struct NormAhead<T, V, UPL, INTER, PART, true> {
   using Vec = RopeVec<T, V>;
-  using L = NormLane<T, V, UPL, INTER>;
+  using L = NormLane<T, V, UPL, INTER, PART>;
   static constexpr int kAhead = kNgAhead, kStages = kAhead + 1, kStep = kNgThreads * 16, kStage = 4 * UPL * kStep;
   static constexpr int kBytes = kStages * kStage;
   const typename L::Units& n;
@@ -375,16 +383,16 @@ struct NormAhead<T, V, UPL, INTER, true> {
 };
 
 // CTAs below ctas0 take the first tensor, the others the second; their groups take (row, walker) in turn.
-template <typename T, int V, int UPL, bool INTER>
+template <typename T, int V, int UPL, bool INTER, bool PART>
 __global__ void __launch_bounds__(kNgThreads, kNgCtasPerSm) qk_norm_rope_gradient_kernel(const NormArgs a) {
-  using Ahead = NormAhead<T, V, UPL, INTER>;
+  using Ahead = NormAhead<T, V, UPL, INTER, PART>;
   constexpr int kAhead = Ahead::kAhead;
   constexpr int kSums = kNgThreads * UPL * 2 * V * static_cast<int>(sizeof(float));
   __shared__ __align__(16) char ring[Ahead::kBytes > kSums ? Ahead::kBytes : kSums];
   float* const sums = reinterpret_cast<float*>(ring);  // [group][dim], when the heads are through
   dependent_wait();
   dependent_launch();
-  using L = NormLane<T, V, UPL, INTER>;
+  using L = NormLane<T, V, UPL, INTER, PART>;
   constexpr int kP = L::kPairs;
   const int lane = threadIdx.x & (a.lanes - 1), groups = kNgThreads / a.lanes, group = threadIdx.x / a.lanes;
   const uint32_t mask = group_mask(a.lanes);
@@ -450,8 +458,8 @@ __global__ void __launch_bounds__(kNgThreads, kNgCtasPerSm) qk_norm_rope_gradien
 #pragma unroll
       for (int q = 0; q < kP; ++q) {
         const uint64_t g0 = ga[q], minus = f2_mul(s[q], f2_all(-1.f));
-        ga[q] = f2_fma(g0, c[q], f2_mul(gb[q], s[q]));
-        gb[q] = f2_fma(gb[q], c[q], f2_mul(g0, minus));
+        ga[q] = f2_fma(g0, c[q], L::of_partner(f2_mul(gb[q], s[q]), n, q));
+        gb[q] = f2_fma(gb[q], c[q], L::of_partner(f2_mul(g0, minus), n, q));
         ta[q] = f2_mul(ga[q], xa[q]);
         tb[q] = f2_mul(gb[q], xb[q]);
         xx = f2_fma(xb[q], xb[q], f2_fma(xa[q], xa[q], xx));
@@ -509,15 +517,18 @@ __global__ void __launch_bounds__(1024) norm_weights_kernel(const float* part, i
   }
 }
 
-template <typename T, int V, int UPL>
-static int norm_launch(const NormArgs& a, bool inter, int grid, void* stream) {
-  if (grid > 0)
-    return inter ? kv8_launch(qk_norm_rope_gradient_kernel<T, V, UPL, true>, dim3(grid), kNgThreads, 0, stream, a)
-                 : kv8_launch(qk_norm_rope_gradient_kernel<T, V, UPL, false>, dim3(grid), kNgThreads, 0, stream, a);
+template <typename T, int V, int UPL, bool INTER, bool PART>
+static int norm_launch(const NormArgs& a, int grid, void* stream) {
+  if (grid > 0) return kv8_launch(qk_norm_rope_gradient_kernel<T, V, UPL, INTER, PART>, dim3(grid), kNgThreads, 0, stream, a);
   const unsigned per = kNrThreads / a.lanes;
-  const dim3 all((a.row_walkers + per - 1) / per);
-  return inter ? kv8_launch(qk_norm_rope_kernel<T, V, UPL, true>, all, kNrThreads, 0, stream, a)
-               : kv8_launch(qk_norm_rope_kernel<T, V, UPL, false>, all, kNrThreads, 0, stream, a);
+  return kv8_launch(qk_norm_rope_kernel<T, V, UPL, INTER, PART>, dim3((a.row_walkers + per - 1) / per), kNrThreads, 0, stream, a);
+}
+template <typename T>
+static int norm_launch(const NormArgs& a, bool wide, bool inter, int grid, void* stream) {
+  constexpr int V = 16 / sizeof(T);
+  if (!wide) return inter ? norm_launch<T, 1, 4, true, true>(a, grid, stream) : norm_launch<T, 1, 4, false, true>(a, grid, stream);
+  if (a.rot < a.dim) return inter ? norm_launch<T, V, 1, true, true>(a, grid, stream) : norm_launch<T, V, 1, false, true>(a, grid, stream);
+  return inter ? norm_launch<T, V, 1, true, false>(a, grid, stream) : norm_launch<T, V, 1, false, false>(a, grid, stream);
 }
 
 struct Span {  // the elements of one tensor, in bytes
@@ -647,13 +658,9 @@ static int norm_rope(const gaac_norm_tensor* tensors, int n_tensors, int dtype, 
     grid = a.ctas0 + (n_tensors == 2 ? ctas(a.heads - a.heads0, a.walkers1) : 0);
   }
   const bool inter = (flags & GAAC_ROPE_INTERLEAVED) != 0;
-  int e;
-  if (dtype == GAAC_BF16)
-    e = wide ? norm_launch<__nv_bfloat16, 8, 1>(a, inter, grid, stream) : norm_launch<__nv_bfloat16, 1, 4>(a, inter, grid, stream);
-  else if (dtype == GAAC_F16)
-    e = wide ? norm_launch<__half, 8, 1>(a, inter, grid, stream) : norm_launch<__half, 1, 4>(a, inter, grid, stream);
-  else
-    e = wide ? norm_launch<float, 4, 1>(a, inter, grid, stream) : norm_launch<float, 1, 4>(a, inter, grid, stream);
+  const int e = dtype == GAAC_BF16  ? norm_launch<__nv_bfloat16>(a, wide, inter, grid, stream)
+                : dtype == GAAC_F16 ? norm_launch<__half>(a, wide, inter, grid, stream)
+                                    : norm_launch<float>(a, wide, inter, grid, stream);
   if (e != GAAC_OK || !gradient) return e;
   if (a.t[0].dw == nullptr && a.t[1].dw == nullptr) return GAAC_OK;
   return kv8_launch(norm_weights_kernel, dim3((head_dim + 31) / 32, n_tensors), 1024, 0, stream, static_cast<const float*>(a.part),

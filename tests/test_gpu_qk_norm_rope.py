@@ -254,3 +254,60 @@ def test_graph_and_other_stream():
     torch.cuda.synchronize()
     replayed = [t.clone() for t in out]
     assert all(torch.equal(a, b) for a, b in zip(both(), replayed))
+
+
+UNTURNED = [(128, 64, "bf16", False), (128, 64, "fp16", True), (256, 128, "fp32", False), (64, 32, "fp32", True),
+            (34, 18, "fp16", True), (20, 6, "bf16", False), (76, 32, "fp32", True), (128, 2, "bf16", True)]
+
+
+@pytest.mark.parametrize("dim,rot,dtype,inter", UNTURNED)
+def test_infinity_in_a_channel_that_is_not_turned(dim, rot, dtype, inter):
+    """Token t has one in channel rot + t: that becomes NaN (infinity over infinity), the others of its head 0."""
+    g, dt = gen(dim), DT[dtype]
+    n = dim - rot
+    x = normal(g, n, 2, dim, dtype=dt)
+    t = torch.arange(n, device="cuda")
+    x[t, 1, rot + t] = torch.inf
+    w = normal(g, dim, dtype=dt) + 3
+    freq = G.rope_frequencies(rot, 1e4)[0]
+    y = torch.empty_like(x)
+    G.qk_norm_rope(x, None, w, None, t, G.rope_turns(freq, "cuda"), q_out=y, interleaved=inter)
+    want, size = ref(x, w, t, freq, EPS, inter)
+    close(y[:, 0], want[:, 0], pair_sums(size, rot, inter)[:, 0], relative(dim))
+    assert torch.equal(y[:, 1].isnan(), want[:, 1].isnan()) and (torch.nan_to_num(y[:, 1], nan=0) == 0).all()
+
+
+@pytest.mark.parametrize("dim,rot,dtype,inter", UNTURNED)
+def test_gradient_with_infinities_in_channels_that_are_not_turned(dim, rot, dtype, inter):
+    """One in a head's dz reaches the head's dx and its own channel of dw, one in x likewise: other heads' dx and other channels
+    of dw are what they are without it (an infinite x leaves 0 of its head's part)."""
+    g, dt = gen(dim + 1), DT[dtype]
+    n, heads = 5, 3
+    x, dz = normal(g, n, heads, dim, dtype=dt), normal(g, n, heads, dim, dtype=dt)
+    w = normal(g, dim, dtype=dt) + 3
+    pos, turns = torch.arange(n, device="cuda"), G.rope_turns(G.rope_frequencies(rot, 1e4)[0], "cuda")
+    ws = torch.empty(G.qk_norm_rope_workspace(dim), dtype=torch.uint8, device="cuda")
+
+    def gradient(dz, x):
+        dx, dw = torch.empty_like(x), torch.empty(dim, device="cuda")
+        G.qk_norm_rope_gradient(dz, None, x, None, w, None, pos, turns, dw, None, ws, dq_out=dx, interleaved=inter)
+        return dx, dw
+
+    others = torch.ones(n, heads, dtype=torch.bool, device="cuda")
+    others[2, 1] = False
+    dx0, dw0 = gradient(dz, x)
+    silent = dz.clone()
+    silent[2, 1] = 0
+    dx1, dw1 = gradient(silent, x)
+    for ch in range(rot, dim):
+        rest = torch.arange(dim, device="cuda") != ch
+        bad = dz.clone()
+        bad[2, 1, ch] = -torch.inf
+        dx, dw = gradient(bad, x)
+        assert torch.equal(dx[others], dx0[others]) and not dx[2, 1].isfinite().any()
+        assert torch.equal(dw[rest], dw0[rest]) and dw[ch].isinf()
+        bad = x.clone()
+        bad[2, 1, ch] = torch.inf
+        dx, dw = gradient(dz, bad)
+        assert torch.equal(dx[others], dx1[others])
+        assert torch.equal(dw[rest], dw1[rest]) and dw[ch].isnan()
