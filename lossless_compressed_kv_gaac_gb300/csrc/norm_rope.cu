@@ -19,9 +19,10 @@
 // tokens: 3.0 us.
 // The backward pass has no registers for loads in flight (two heads' in them leave three CTAs to an SM and take 116 us), so
 // its next three heads, across walks, come by asynchronous copies into shared memory, and 128 registers leave four CTAs.
-// 16,384 tokens x 40 heads x 128, bf16: 85 us, 5.9 TB/s (88% of a copy).  Shuffles of the two means one after the other: 94 us,
-// and of that form two heads ahead the same, walks of 4 heads 99, of 16 the same, a row's heads in one walk that begins with
-// empty hands 97.  4,999 tokens x 24 heads, fp16, half turned, interleaved: 25.7 us; 512 tokens x 24: 9.3 us.
+// 16,384 tokens x 40 heads x 128, bf16: 88 us, 5.7 TB/s (84% of a copy), of which 3 us are sines as fine as an fp32 dw wants them;
+// walks of 16 heads 89, of 32 93.  With coarser sines, 85 us: shuffles of the two means one after the other 94, and of that form
+// two heads ahead the same, walks of 4 heads 99, a row's heads in one walk that begins with empty hands 97.  4,999 tokens x 24
+// heads, fp16, half turned, interleaved: 27 us; 512 tokens x 24: 9.6 us.
 // Sums are fp32.  dw: every lane adds up its channels over its rows, a CTA its lanes in order, a second launch the
 // CTAs in order, so the result is the same each time.
 #include <algorithm>
@@ -198,6 +199,8 @@ struct NormLane {
 #pragma unroll
     for (int q = 0; q < kPairs; ++q) wa[q] = f2_make(w[0][q][0], w[0][q][1]), wb[q] = f2_make(w[1][q][0], w[1][q][1]);
   }
+  // As accurate as results of type S want them.
+  template <typename S>
   static __device__ __forceinline__ void sines(uint64_t (&s)[kPairs], uint64_t (&c)[kPairs], const NormArgs& a, const Units& n,
                                                int lane, int64_t pos_at) {
     const uint64_t p = rope_position(a.pos, a.pos64, pos_at);
@@ -209,7 +212,7 @@ struct NormLane {
         const int k = unit(q) + (V == 1 ? i : 0);
         const int at = (2 * q + i) % V;  // interleaved pairs stay within a vector
         const int pair = !INTER || V == 1 ? (lane + k * a.lanes) * V + at : at < V / 2 ? n.e0[k] / 2 + at : n.e1[k] / 2 + at - V / 2;
-        if (n.turned[k]) rope_sincos<T>(p * a.turns[pair], a.mscale, x[i], y[i]);
+        if (n.turned[k]) rope_sincos<S>(p * a.turns[pair], a.mscale, x[i], y[i]);
       }
       s[q] = f2_make(x[0], x[1]);
       c[q] = f2_make(y[0], y[1]);
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtasPerSm) qk_norm_rope_kernel(
 #pragma unroll
   for (int j = 0; j < kNrBatch; ++j) load(v[j], first + j);
   uint64_t s[kP], c[kP];
-  L::sines(s, c, a, n, lane, seq * a.pos_seq + tok * a.pos_tok);
+  L::template sines<T>(s, c, a, n, lane, seq * a.pos_seq + tok * a.pos_tok);
   // a' = r (a ca + b sb),  b' = r (b cb + a sa): the weights are part of the sines
   uint64_t ca[kP], cb[kP], sa[kP], sb[kP];
   int of = -1;  // the tensor whose weights they hold
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(kNgThreads, kNgCtasPerSm) qk_norm_rope_gradien
     const int n_walk = place(rw, seq, tok, first);
     char* out = t.out + seq * t.out_seq + tok * t.out_tok + first * t.out_head;
     uint64_t s[kP], c[kP];
-    L::sines(s, c, a, n, lane, seq * a.pos_seq + tok * a.pos_tok);
+    L::template sines<float>(s, c, a, n, lane, seq * a.pos_seq + tok * a.pos_tok);  // dw is fp32
 #pragma unroll 1
     for (int h = 0; h < n_walk; ++h, out += t.out_head) {
       uint64_t xa[kP], xb[kP], ga[kP], gb[kP], ta[kP], tb[kP], xx = 0, hx = 0;

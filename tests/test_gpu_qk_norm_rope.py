@@ -311,3 +311,23 @@ def test_gradient_with_infinities_in_channels_that_are_not_turned(dim, rot, dtyp
         dx, dw = gradient(dz, bad)
         assert torch.equal(dx[others], dx1[others])
         assert torch.equal(dw[rest], dw1[rest]) and dw[ch].isnan()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim", [256, 250])
+def test_weight_gradient_is_fp32_for_16_bit_inputs(dim, dtype):
+    """x = 1 and eps = 0, dz is 1 in the first of each pair and 0 in the second: dw is the angles' cosines and -sines.  An angle
+    is off by 2^-25 of half a turn, its functions by 2^-24: 2^-22.6 together; the root by 2^-22 (two units in the last
+    place) and the two products by 2^-24 each, of the value."""
+    dt, pairs = DT[dtype], dim // 2
+    x, dz = torch.ones((1, 1, dim), dtype=dt, device="cuda"), torch.zeros((1, 1, dim), dtype=dt, device="cuda")
+    dz[..., :pairs] = 1
+    freq = G.rope_frequencies(dim, 1e4)[0]
+    turns = G.rope_turns(freq, "cuda")
+    ws, dx, dw = torch.empty(G.qk_norm_rope_workspace(dim), dtype=torch.uint8, device="cuda"), torch.empty_like(x), torch.empty(dim, device="cuda")
+    for pos in torch.randint(0, 100000, (100,), generator=torch.Generator().manual_seed(dim)).tolist():
+        p = torch.tensor([pos], device="cuda")
+        G.qk_norm_rope_gradient(dz, None, x, None, None, None, p, turns, dw, None, ws, eps=0.0, dq_out=dx)
+        want = U.rope_ref(dz, p, freq, inverse=True)[0, 0]
+        err = (dw.double() - want).abs()
+        assert (err <= 2.0 ** -22.6 + 1.5 * 2.0 ** -22 * want.abs()).all(), err.max().item()
