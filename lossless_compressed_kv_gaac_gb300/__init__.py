@@ -796,7 +796,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_token
     (multiples of 8 elements, 16-byte aligned: slices of one projection will do).  out: of q's shape and type (made,
     contiguous, if not given; rows of no sequence are not written); lse: fp32 [n, q_heads], contiguous, receives the
     logarithm of each row's sum of exponentials.  Offsets that are not valid are reported in status (int32)."""
-    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or
+                                    (out is not None and out.requires_grad) or (lse is not None and lse.requires_grad)):
         raise ValueError("autograd does not see prompt_attention: call it under torch.no_grad()")
     dtype, index = q.dtype, q.get_device()
     if dtype not in (torch.bfloat16, torch.float16) or index < 0:
@@ -1007,7 +1008,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, out_scores: torch.Te
     not overlap on the GPU."""
     index = logits.get_device()
     code = _DTYPES.get(logits.dtype)
-    if torch.is_grad_enabled() and (logits.requires_grad or scores.requires_grad):
+    if torch.is_grad_enabled() and (logits.requires_grad or scores.requires_grad or out_scores.requires_grad):
         raise ValueError("autograd does not see beam_select: call it under torch.no_grad()")
     if code is None or logits.dim() != 2 or index < 0 or (logits.stride(1) != 1 and logits.shape[1] > 1):
         raise ValueError("logits must be BF16, FP16 or FP32 [batch * beams, vocab] on a CUDA device, tokens contiguous")

@@ -146,3 +146,16 @@ def test_prompt_refuses_on_the_host():
         G.prompt_attention(z(4, 2, 128).bfloat16(), z(4, 1, 128).bfloat16(), z(4, 1, 128).bfloat16(), cu, 0.1)
     with pytest.raises(ValueError, match="autograd"):
         G.prompt_attention(z(4, 2, 128, requires_grad=True), z(4, 1, 128), z(4, 1, 128), cu, 0.1)
+
+
+def test_outputs_that_autograd_follows_are_refused():
+    z = torch.zeros
+    q, k, cu = z(4, 2, 128, dtype=torch.bfloat16), z(4, 1, 128, dtype=torch.bfloat16), z(2, dtype=torch.int32)
+    for kw in (dict(out=q.clone().requires_grad_()), dict(lse=z(4, 2, requires_grad=True))):
+        with pytest.raises(ValueError, match="autograd"):
+            G.prompt_attention(q, k, k, cu, 0.1, **kw)
+        with pytest.raises(ValueError, match="CUDA"), torch.no_grad():
+            G.prompt_attention(q, k, k, cu, 0.1, **kw)
+    i = dict(dtype=torch.int32)
+    with pytest.raises(ValueError, match="autograd"):
+        G.beam_select(z(4, 10), z(2, 2), z(2, 2, requires_grad=True), z(2, 2, **i), z(2, 2, **i), z(4))
