@@ -549,7 +549,9 @@ GAAC_API int gaac_qk_norm_rope_gradient(const gaac_norm_tensor* tensors, int n_t
 
 /* Tensors of gaac_prompt_attention: element (row, head, c) of q at q + row*q_tok + head*q_head + c and so on, 16-byte
  * aligned, strides in elements, multiples of 8, at least 128 (a dimension of size 1 has any).  out's elements are
- * distinct and no input's.  lse: fp32 [n_tokens][n_q_heads] or NULL. */
+ * distinct and no input's (GAAC_EINVAL where out and an input lie in one range, unless one stride of the tokens keeps
+ * their heads apart or the strides have a common divisor that does).  lse: fp32 [n_tokens][n_q_heads], in no range of the
+ * others, or NULL. */
 typedef struct {
   const void* q;
   const void* k;

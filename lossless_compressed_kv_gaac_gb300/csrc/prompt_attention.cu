@@ -28,6 +28,7 @@
 // a unit for its start and end (32 x 1-2,048 tokens, 16 / 8 heads, f16: 240 us, 0.8 PFLOP/s; 1 x 777: 17.5 us).
 #include <algorithm>
 #include <cmath>
+#include <numeric>
 
 #include "f32x2.cuh"
 #include "kv8.cuh"
@@ -658,6 +659,28 @@ static bool pa_map(CUtensorMap* m, const void* base, int64_t tokens, int64_t hea
                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// What a tensor's elements lie between and how they repeat: [tokens][heads][128], strides in elements.
+struct PaSpan {
+  int64_t at, tok, head, heads, end;  // the addresses in bytes
+  PaSpan(const void* base, int64_t n, int64_t heads, int64_t tok, int64_t head)
+      : at(static_cast<int64_t>(reinterpret_cast<uintptr_t>(base))), tok(n > 1 ? tok : 0), head(heads > 1 ? head : 0), heads(heads),
+        end(at + ((n - 1) * this->tok + (heads - 1) * this->head + kD) * 2) {}
+  int64_t row() const { return (heads - 1) * head + kD; }
+};
+// No element in common, shown in one of three ways: the ranges are apart; tokens lie alike and a token's heads are apart, as the slices
+// of one projection; or all strides are multiples of a period in which the heads' channels have places of their own.
+static bool pa_apart(const PaSpan& x, const PaSpan& y) {
+  if (x.end <= y.at || y.end <= x.at) return true;
+  const int64_t d = (y.at - x.at) / 2;
+  auto within = [d](int64_t period, int64_t first, int64_t second) {
+    if (period == 0) return false;
+    const int64_t r = ((d % period) + period) % period;
+    return r >= first && r + second <= period;
+  };
+  return (x.tok == y.tok && within(x.tok, x.row(), y.row())) ||
+         within(std::gcd(std::gcd(x.tok, y.tok), std::gcd(x.head, y.head)), kD, kD);
+}
+
 template <bool HALF>
 static int pa_launch(const PaArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, unsigned grid, void* stream) {
   constexpr size_t smem = sizeof(PaSmem) + 1024;  // room to align the tiles
@@ -693,13 +716,19 @@ extern "C" int gaac_prompt_attention(const gaac_prompt* p, int dtype, int64_t n_
   const void* base[4] = {p->q, p->k, p->v, p->out};
   for (int i = 0; i < 4; ++i) {
     const int64_t st = n_tokens > 1 ? tok[i] : kD, sh = heads[i] > 1 ? head[i] : kD;
-    if (st < kD || sh < kD || ((st | sh) & 7) || st > (int64_t{1} << 38) || sh > (int64_t{1} << 38)) return GAAC_EINVAL;
+    if (st < kD || sh < kD || ((st | sh) & 7) || st > std::min(int64_t{1} << 38, (int64_t{1} << 56) / n_tokens) ||
+        sh > (int64_t{1} << 38))
+      return GAAC_EINVAL;
   }
-  // Heads of one token and tokens of one head of the result are apart, and the result is not an input.
+  // Heads of one token and tokens of one head of the result are apart, and no input has a part of the results.
   if (n_tokens > 1 && n_q_heads > 1 && tok[3] < static_cast<int64_t>(n_q_heads - 1) * head[3] + kD && head[3] < (n_tokens - 1) * tok[3] + kD)
     return GAAC_EINVAL;
-  for (int i = 0; i < 3; ++i)
-    if (base[i] == base[3]) return GAAC_EINVAL;
+  const PaSpan out(p->out, n_tokens, n_q_heads, p->out_tok, p->out_head);
+  const int64_t lse = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p->lse)), lse_end = lse + n_tokens * n_q_heads * 4;
+  for (int i = 0; i < 4; ++i) {
+    const PaSpan t(base[i], n_tokens, heads[i], tok[i], head[i]);
+    if ((i < 3 && !pa_apart(t, out)) || (lse != 0 && lse < t.end && t.at < lse_end)) return GAAC_EINVAL;
+  }
   if (tma_encode() == nullptr) return GAAC_ECUDA;
   PaArgs a;
   a.cu = cu_tokens;

@@ -159,3 +159,17 @@ def test_outputs_that_autograd_follows_are_refused():
     i = dict(dtype=torch.int32)
     with pytest.raises(ValueError, match="autograd"):
         G.beam_select(z(4, 10), z(2, 2), z(2, 2, requires_grad=True), z(2, 2, **i), z(2, 2, **i), z(4))
+
+
+SIZE = 2 * 100 * 1024  # bytes of prompt_call's q and out
+APART = dict(q_tok=2048, out_tok=2048)  # rows with room for another tensor's heads
+
+
+@pytest.mark.parametrize("bad", [
+    dict(out=GOOD + 16), dict(out=GOOD + 256), dict(out=GOOD + 2048), dict(out=GOOD + SIZE - 16), dict(q=3 * MORE + 256), dict(out=MORE + 256),
+    dict(out=2 * MORE + 100 * 512 - 16), dict(**APART, out=GOOD + 2048 - 16), dict(**APART, out=GOOD + 2048 + 16),
+    dict(q_tok=2048, out=GOOD + 2048), dict(q_head=256, q_tok=2048, out_head=256, out_tok=2048, out=GOOD + 512),
+    dict(q_head=256, q_tok=2048, out_head=256, out_tok=2048, out=GOOD + 128), dict(n=1, out=GOOD + 256), dict(n=1, out=GOOD + 2048 - 16),
+    dict(lse=GOOD), dict(lse=GOOD - 4), dict(lse=MORE + 512), dict(lse=3 * MORE + SIZE - 4), dict(lse=3 * MORE - 100 * 8 * 4 + 4)], ids=str)
+def test_prompt_refuses_results_that_overlap(lib, bad):  # noqa: F811
+    assert prompt_call(lib, **bad) == EINVAL

@@ -302,3 +302,26 @@ def test_prompt_to_search():
     c.release(torch.arange(6, dtype=torch.int32, device="cuda"))
     assert int(c.refs.abs().max()) == 0
     assert not math.isnan(o.float().sum().item())
+
+
+def test_results_between_the_inputs_elements():
+    """out as a slice of the projection that q, k and v are slices of, heads in turn with the queries' or tokens with the keys';
+    what lies beside it is left alone, and an out that takes a channel of an input is refused."""
+    g, n = gen(17), 150
+    x = normal(g, n, 12, 128)
+    rest = x[:, :8].clone()
+    check(x[:, :4], x[:, 4:6], x[:, 6:8], [100, 50], out=x[:, 8:])
+    assert torch.equal(x[:, :8], rest)
+    for args in ((x[:, :4], x[:, 4:6], x[:, 6:8], x[:, 2:6]), (x[:, :4], x[:, 4:6], x[:, 6:8], x[:, 7:11])):
+        with pytest.raises(G.GaacError):
+            G.prompt_attention(*args[:3], offsets([n]), 0.1, out=args[3])
+    x = normal(g, n, 3, 4, 128)
+    rest = x[:, :, :3].clone()
+    check(*(x[:, :, i] for i in range(3)), [n], out=x[:, :, 3])
+    assert torch.equal(x[:, :, :3], rest)
+    x = normal(g, 2, n, 4, 128).transpose(0, 1)
+    rest = x[:, :, :3].clone()
+    check(*(x[:, :, i] for i in range(3)), [n], out=x[:, :, 3])
+    assert torch.equal(x[:, :, :3], rest)
+    x = normal(g, 1, 8, 128)
+    check(x[:, :2], x[:, 2:3], x[:, 3:4], [1], out=x[:, 4:6])
