@@ -570,7 +570,7 @@ typedef struct {
  * [0, n_tokens]; else GAAC_EINVAL and nothing is computed):
  *   out[i][hq] = sum_{j <= i} softmax_j(scale * q[i][hq] . k[j][hk]) v[j][hk],  hk = hq / (n_q_heads / n_kv_heads),
  * which is an integer <= GAAC_MAX_GQA; lse[i][hq] = ln sum_{j <= i} exp(scale * q[i][hq] . k[j][hk]).  dtype, of all four:
- * GAAC_BF16 or GAAC_F16.  scale: any finite number.  Rows of no sequence are not written.  n_tokens < 2^31 - 2^16, batch
+ * GAAC_BF16 or GAAC_F16.  scale: times log2 e it is finite in fp32.  Rows of no sequence are not written.  n_tokens < 2^31 - 2^16, batch
  * <= 65535.  Logits and sums are fp32; weights are rounded to dtype (f16: those below 2^-14 of the row's largest may
  * lose bits, below 2^-25 they may be 0).  What tokens behind i and other sequences hold has no influence on row i, nor whether it
  * is finite.  An infinite V makes its channel infinite (NaN where both signs meet, or where its weight is rounded to

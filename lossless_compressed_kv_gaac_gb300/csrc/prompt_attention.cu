@@ -27,6 +27,7 @@
 // maxima, weights multiplied in two parts, and the maximum off the chain with waits that poll (1.43).  Short prompts pay 7,000 cycles
 // a unit for its start and end (32 x 1-2,048 tokens, 16 / 8 heads, f16: 240 us, 0.8 PFLOP/s; 1 x 777: 17.5 us).
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <numeric>
 
@@ -701,8 +702,9 @@ using namespace gaac;
 
 extern "C" int gaac_prompt_attention(const gaac_prompt* p, int dtype, int64_t n_tokens, int n_q_heads, int n_kv_heads,
                                      const int32_t* cu_tokens, int batch, float scale, int32_t* d_status, void* stream) {
+  const double c = std::fabs(static_cast<double>(scale)) * 1.4426950408889634;
   if (p == nullptr || (dtype != GAAC_BF16 && dtype != GAAC_F16) || n_tokens < 0 || n_tokens > 0x7FFFFFFF - 65536 || batch < 0 ||
-      batch > 65535 || !std::isfinite(scale) || n_kv_heads < 1 || n_kv_heads > 1024 || n_q_heads < 1 || n_q_heads % n_kv_heads != 0 ||
+      batch > 65535 || !(c <= FLT_MAX) || n_kv_heads < 1 || n_kv_heads > 1024 || n_q_heads < 1 || n_q_heads % n_kv_heads != 0 ||
       n_q_heads / n_kv_heads > GAAC_MAX_GQA)
     return GAAC_EINVAL;
   if (n_tokens == 0 || batch == 0) return GAAC_OK;
@@ -744,7 +746,7 @@ extern "C" int gaac_prompt_attention(const gaac_prompt* p, int dtype, int64_t n_
   a.heads_apart = n_tokens * n_kv_heads * (2 * kD * 2) > (int64_t{64} << 20);
   a.n_tokens = n_tokens;
   // Not 0, which would make NaN of the masked logits: with the smallest number above it no finite logit moves a weight.
-  a.c = scale == 0.f ? 0x1p-149f : static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634);
+  a.c = scale == 0.f ? 0x1p-149f : static_cast<float>(c);
   a.negate = scale < 0.f;
   a.v = static_cast<const char*>(p->v);
   a.v_tok = p->v_tok * 2;

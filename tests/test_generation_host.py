@@ -173,3 +173,9 @@ APART = dict(q_tok=2048, out_tok=2048)  # rows with room for another tensor's he
     dict(lse=GOOD), dict(lse=GOOD - 4), dict(lse=MORE + 512), dict(lse=3 * MORE + SIZE - 4), dict(lse=3 * MORE - 100 * 8 * 4 + 4)], ids=str)
 def test_prompt_refuses_results_that_overlap(lib, bad):  # noqa: F811
     assert prompt_call(lib, **bad) == EINVAL
+
+
+@pytest.mark.parametrize("scale", [3e38, -3e38, 2.36e38])
+def test_prompt_refuses_scales_that_overflow(lib, scale):  # noqa: F811
+    """scale * log2 e has to be a number of fp32."""
+    assert prompt_call(lib, scale=scale) == EINVAL
