@@ -46,6 +46,8 @@ constexpr int kPaSoftmax = 256;
 constexpr int kPaCleaners = 128;
 constexpr int kPaThreads = kPaSoftmax + 128 + kPaCleaners;   // 128: two multipliers, the copier, one warp idle
 constexpr int kPaEarly = 64;                  // keys of a block whose weights are multiplied ahead of the others
+constexpr int64_t kPaApartBytes = int64_t{64} << 20;  // of K and V, and units for each SM, from which kv-heads are taken one
+constexpr int kPaApartUnits = 11;                     // after the other
 constexpr int kPaLook = 3;                    // blocks of a unit that have masked keys, at most
 constexpr uint32_t kPaFull = 0xFFFFFFFFu;
 constexpr uint32_t kPaColS = 0, kPaColO = 256;  // TMEM columns: S of tile t at 128 t, P over it, O at 256 + 128 t
@@ -742,8 +744,12 @@ extern "C" int gaac_prompt_attention(const gaac_prompt* p, int dtype, int64_t n_
   const int64_t places = n_tokens / (2 * a.per) + batch;
   if (places * n_kv_heads > 0x7FFFFFFF) return GAAC_EINVAL;
   a.places = static_cast<unsigned>(places);
-  // Where K and V are too much for L2 together, the CTAs that run at a time share one kv-head's.
-  a.heads_apart = n_tokens * n_kv_heads * (2 * kD * 2) > (int64_t{64} << 20);
+  // The CTAs that run at a time share one kv-head's keys where K and V are more than half of L2 and there are units enough to
+  // level out what every head ends with.  One head after the other against all in turn, in % of the time: 4 x 16,384 tokens,
+  // 32 / 8 heads, -11 to -16; 32 of 1-4,096, 16 / 8, -6 to -9; 32 of 1-2,048, 16 / 8, -1 to -6; 8 of 1-12,000, 16 / 8, -8 to +6 by
+  // their lengths; 1 x 16,384, 32 / 8 (64 MB), within 1.  Less data: 1 x 8,192, 32 / 8, +5 to +9.  Fewer units (of an SM): 8 of
+  // 1-5,000, 16 / 8 (7-9), +8 to +12; 8 of 600-10,000, 8 / 8 (7-10), +3 to +10; 1 x 24,576, 16 / 16 (10), +1 to +3.
+  a.heads_apart = n_tokens * n_kv_heads * (2 * kD * 2) > kPaApartBytes && places * n_kv_heads >= int64_t{152} * kPaApartUnits;
   a.n_tokens = n_tokens;
   // Not 0, which would make NaN of the masked logits: with the smallest number above it no finite logit moves a weight.
   a.c = scale == 0.f ? 0x1p-149f : static_cast<float>(c);

@@ -325,3 +325,13 @@ def test_results_between_the_inputs_elements():
     assert torch.equal(x[:, :, :3], rest)
     x = normal(g, 1, 8, 128)
     check(x[:, :2], x[:, 2:3], x[:, 3:4], [1], out=x[:, 4:6])
+
+
+@pytest.mark.parametrize("hq,hkv,longest", [(16, 8, 1100), (8, 8, 1300), (2, 1, 8400)])
+def test_more_keys_than_a_cache_holds(hq, hkv, longest):
+    """Up to 32 sequences, some empty, with so many keys in all that the CTAs take one kv-head after the other."""
+    lens = torch.randint(longest // 2, longest + 1, (32,), generator=torch.Generator().manual_seed(hq)).tolist()
+    lens[3] = lens[17] = lens[31] = 0
+    lens[5], lens[30] = 1, longest
+    assert sum(lens) * hkv > 1.3 * 131072
+    check(*qkv(gen(16), sum(lens), hq, hkv, FP16 if hq == 8 else BF16), lens)
