@@ -335,3 +335,19 @@ def test_more_keys_than_a_cache_holds(hq, hkv, longest):
     lens[5], lens[30] = 1, longest
     assert sum(lens) * hkv > 1.3 * 131072
     check(*qkv(gen(16), sum(lens), hq, hkv, FP16 if hq == 8 else BF16), lens)
+
+
+@pytest.mark.parametrize("batch", [33, 100])
+def test_bad_offsets_of_many_sequences_are_reported(batch):
+    """More sequences than a warp has lanes, a bad offset among the first 32 or behind them."""
+    q, k, v = qkv(gen(15), 400, 2, 1)
+    good = torch.arange(batch + 1, dtype=torch.int32) * 4
+    for at in (1, 20, batch - 1, batch):
+        for bad in (-1, int(good[at - 1]) - 1, 401):
+            cu = good.clone()
+            cu[at] = bad
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            out, lse = torch.full((400, 2, 128), 3.0, dtype=BF16, device="cuda"), torch.full((400, 2), 3.0, device="cuda")
+            G.prompt_attention(q, k, v, cu.cuda(), 0.1, out=out, lse=lse, status=status)
+            assert int(status.item()) == G.EINVAL and (out == 3).all() and (lse == 3).all(), (at, bad)
+    check(q, k, v, [4] * batch)
