@@ -341,3 +341,25 @@ def test_select_peak_in_a_later_run(V, dtype):
     assert torch.equal(tokens.long(), at)
     err = (out.double() - best).abs()
     assert (err <= 2.0 ** -21 + best.abs() * 2.0 ** -24).all(), err.max().item()
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("V", [70000, 70002])
+def test_select_runs_of_aligned_rows(V, dtype):
+    """Several runs of a CTA with rows on 16-byte and on 4-byte boundaries, which are loaded as vectors and as pairs."""
+    g = gen(V)
+    rows = 256
+    x = torch.randn((rows, V), generator=g, device="cuda")
+    x[0, :40000] = -INF
+    x[1, 20000:] = -INF
+    x[2, :33000] -= 900
+    x[3] = torch.arange(V, device="cuda") / 1000
+    x[4] = -torch.arange(V, device="cuda") / 1000
+    x[5] = torch.randint(0, 3, (V,), generator=g, device="cuda").float()
+    x[6] = 5
+    x[7, V - 3:] = torch.tensor([9.0, 8.0, 9.0], device="cuda")  # in the last vector
+    scores = -torch.rand((rows // 8, 8), generator=g, device="cuda")
+    for n_out in (8, 40):
+        check(x.to(DT[dtype]), scores, n_out)
+    flat, at = check(x.to(DT[dtype]), torch.zeros((rows, 1), device="cuda"), 33)
+    assert torch.equal(flat, at)
