@@ -327,9 +327,10 @@ def test_results_between_the_inputs_elements():
     check(x[:, :2], x[:, 2:3], x[:, 3:4], [1], out=x[:, 4:6])
 
 
-@pytest.mark.parametrize("hq,hkv,longest", [(16, 8, 1100), (8, 8, 1300), (2, 1, 8400)])
+@pytest.mark.parametrize("hq,hkv,longest", [(16, 8, 1100), (16, 4, 2400), (8, 8, 1300), (2, 1, 8400)])
 def test_more_keys_than_a_cache_holds(hq, hkv, longest):
-    """Up to 32 sequences, some empty, with so many keys in all that the CTAs take one kv-head after the other."""
+    """Up to 32 sequences, some empty, with so many keys in all that the CTAs take one kv-head after the other, where there
+    are 1,672 units of 256 / (hq / hkv) tokens or more too (the first two)."""
     lens = torch.randint(longest // 2, longest + 1, (32,), generator=torch.Generator().manual_seed(hq)).tolist()
     lens[3] = lens[17] = lens[31] = 0
     lens[5], lens[30] = 1, longest
