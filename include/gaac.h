@@ -573,7 +573,7 @@ typedef struct {
  * GAAC_BF16 or GAAC_F16.  scale: times log2 e it is finite in fp32.  Rows of no sequence are not written.  n_tokens < 2^31 - 2^16, batch
  * <= 65535.  Logits and sums are fp32; weights are rounded to dtype (f16: those below 2^-14 of the row's largest may
  * lose bits, below 2^-25 they may be 0).  What tokens behind i and other sequences hold has no influence on row i, nor whether it
- * is finite.  An infinite V makes its channel infinite (NaN where both signs meet, or where its weight is rounded to
+ * is finite.  An infinite V makes its channel infinite (NaN where both signs meet; one of the two where its weight is rounded to
  * 0).  A row whose logits are all -infinity is 0, its lse -infinity.
  */
 GAAC_API int gaac_prompt_attention(const gaac_prompt* tensors, int dtype, int64_t n_tokens, int n_q_heads, int n_kv_heads,

@@ -630,9 +630,9 @@ static int norm_rope(const gaac_norm_tensor* tensors, int n_tensors, int dtype, 
   a.units = a.rot_units + ((head_dim - rot_dim) / v + 1) / 2;
   a.lanes = 2;
   while (a.lanes < 32 && a.lanes < a.units) a.lanes *= 2;
-  // Heads of a walk: as many as leave twice the lanes that 152 SMs hold at a time (gradient: one walk for each group that
+  // Heads of a walk: as many as leave four times the lanes that 152 SMs hold at a time (gradient: one walk for each group that
   // they hold), so that sines are shared where there is work for all, and single heads where latency counts.
-  const int64_t want = int64_t{152} * (gradient ? kNgThreads * kNgCtasPerSm : 2048), lanes = std::max<int64_t>(rows, 1) * heads * a.lanes;
+  const int64_t want = int64_t{152} * (gradient ? kNgThreads * kNgCtasPerSm : 4 * kNrThreads * kNrCtasPerSm), lanes = std::max<int64_t>(rows, 1) * heads * a.lanes;
   const int64_t fair = std::max<int64_t>(1, gradient ? (lanes + want - 1) / want : lanes / want);
   const int64_t walkers_most = 0x7FFFFFFF / std::max<int64_t>(rows, 1);  // walks are counted in 31 bits
   if (gradient) {  // walks of like lengths

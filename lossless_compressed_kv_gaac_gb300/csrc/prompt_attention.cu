@@ -537,7 +537,7 @@ __device__ void pa_softmax(const PaArgs& a, PaSmem& sm, const PaUnit& u, uint32_
     float y[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) y[j] = l == 0.f ? 0.f : __uint_as_float(o[j]) * inv;
-    if (real && *reinterpret_cast<volatile int*>(&sm.odd)) {  // V that is not finite, of the blocks that were looked over
+    if (real && l != 0.f && *reinterpret_cast<volatile int*>(&sm.odd)) {  // V that is not finite, of the blocks that were looked over
       for (int key = u.look * kPaKeys; key <= token; ++key) {
         const uint16_t* v = reinterpret_cast<const uint16_t*>(a.v + (static_cast<int64_t>(u.first) + key) * a.v_tok + u.h * a.v_head) + k;
 #pragma unroll 1

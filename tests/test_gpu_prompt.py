@@ -352,3 +352,17 @@ def test_bad_offsets_of_many_sequences_are_reported(batch):
             G.prompt_attention(q, k, v, cu.cuda(), 0.1, out=out, lse=lse, status=status)
             assert int(status.item()) == G.EINVAL and (out == 3).all() and (lse == 3).all(), (at, bad)
     check(q, k, v, [4] * batch)
+
+
+@pytest.mark.parametrize("n", [100, 300])
+def test_infinite_values_of_rows_without_weights(n):
+    """A row whose logits are all -infinity is 0, whatever V is; a row behind them that has a weight sees an infinite V."""
+    q, k, v = (x.clone() for x in qkv(gen(18), n, 2, 1))
+    q.abs_()
+    k[:n - 20] = -INF
+    v[3, 0, 5] = v[n - 40, 0, 9] = INF
+    out = G.prompt_attention(q, k, v, offsets([n]), 0.1)
+    assert (out[:n - 20] == 0).all()
+    ordinary = torch.ones(128, dtype=torch.bool, device="cuda")
+    ordinary[[5, 9]] = False
+    assert out[n - 20:, :, ordinary].isfinite().all() and not out[n - 20:, :, ~ordinary].isfinite().any()
