@@ -796,7 +796,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_token
     (multiples of 8 elements, 16-byte aligned: slices of one projection will do).  out: of q's shape and type (made,
     contiguous, if not given; rows of no sequence are not written), with no element of an input's (another slice of the
     projection will do); lse: fp32 [n, q_heads], contiguous, memory of its own, receives the
-    logarithm of each row's sum of exponentials.  Offsets that are not valid are reported in status (int32)."""
+    logarithm of each row's sum of exponentials.  Offsets that are not valid leave out as it was, and like everything that
+    only the device sees they are reported in status (int32), if it is given."""
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or
                                     (out is not None and out.requires_grad) or (lse is not None and lse.requires_grad)):
         raise ValueError("autograd does not see prompt_attention: call it under torch.no_grad()")

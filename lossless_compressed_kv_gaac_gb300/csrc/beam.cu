@@ -13,8 +13,8 @@
 //  2. The last CTA of a search adds up the sums in 64 bits, in a fixed order, and merges the sorted lists: the largest of
 //     their heads is taken n_out times, by one warp.  The other searches are read meanwhile.
 // Bound by its instructions and barriers where there is much to read: 32 searches of 8 beams, 128,511 bf16 logits at odd addresses,
-// n_out 16, 66 MB: 38.5 us (530 instructions for 32 logits of a warp's lanes, of which the sum takes 110, loads and widening 100, the
-// candidates 150).  What it was: every CTA one run and the choice a launch of its own, 104 us; odd rows put together from
+// n_out 16, 66 MB: 38.5 us (490 instructions for 32 logits of a warp's lanes, of which the sum takes 110, loads and widening 100, the
+// candidates 150).  Rows that rise all along, which every run searches, 515 us; five tokens left by a mask 575, one in a hundred 39.  What it was: every CTA one run and the choice a launch of its own, 104 us; odd rows put together from
 // aligned vectors of neighbouring lanes, 72 us; the bound by taking the largest maximum n_out times in place of a sort, 5 us
 // more; the choice in a second launch, 8 us more.  One search of 4 beams, 32,000 fp32 logits: 7.7 us.
 // Order: logits as unsigned numbers of the same order, the lower token first where they are equal; in the merge the
@@ -523,8 +523,9 @@ __global__ void __launch_bounds__(kBmThreads, kBmCtasPerSm) beam_chunk_kernel(co
   done();
 }
 
-// Runs of a CTA: as many as leave every SM three CTAs, up to kBmMostTiles, the same for all CTAs of a beam as nearly as it goes (32
-// searches of 8 beams, 16 runs a beam: 38.5 us with eight runs, 42.4 with four).
+// Runs of a CTA: as many as leave every SM three CTAs, of which two run at a time, up to kBmMostTiles, the same for all CTAs of a
+// beam as nearly as it goes (32 searches of 8 beams, 16 runs a beam: 38.5 us with eight runs, 42.4 with four).  Two CTAs in place of
+// three: 64 rows of 50,257 bf16 logits 10.6 us for 13.1, but 128 of 128,256 23.3 for 21.1; four: 41.5 for 38.7 with 256 of 128,511.
 static int beam_tiles(int64_t rows, int vocab) {
   const int64_t tiles = (vocab + kBmTile - 1) / kBmTile;
   const int64_t least = (tiles + kBmMostTiles - 1) / kBmMostTiles;
