@@ -14,7 +14,8 @@
 //     their heads is taken n_out times, by one warp.  The other searches are read meanwhile.
 // Bound by its instructions and barriers where there is much to read: 32 searches of 8 beams, 128,511 bf16 logits at odd addresses,
 // n_out 16, 66 MB: 38.5 us (490 instructions for 32 logits of a warp's lanes, of which the sum takes 110, loads and widening 100, the
-// candidates 150).  Rows that rise all along, which every run searches, 515 us; five tokens left by a mask 575, one in a hundred 39.  What it was: every CTA one run and the choice a launch of its own, 104 us; odd rows put together from
+// candidates 150).  Rows that rise all along, which every run searches, 515 us; five tokens left by a mask 575, one in a hundred 39.
+// What it was: every CTA one run and the choice a launch of its own, 104 us; odd rows put together from
 // aligned vectors of neighbouring lanes, 72 us; the bound by taking the largest maximum n_out times in place of a sort, 5 us
 // more; the choice in a second launch, 8 us more.  One search of 4 beams, 32,000 fp32 logits: 7.7 us.
 // Order: logits as unsigned numbers of the same order, the lower token first where they are equal; in the merge the
